@@ -32,6 +32,16 @@ LA_FM_IDENTITY, LA_FM_ELU1, LA_FM_FAVOR = 0, 1, 2
 LA_BF16, LA_F32 = 0, 1
 LA_PATH_AUTO, LA_PATH_SIMT, LA_PATH_TC = 0, 1, 2
 
+LA_GATE_VALUE, LA_GATE_LOG, LA_GATE_SIGMOID = 0, 1, 2
+LA_RECURRENCE_CHUNK = 128
+LA_ROTARY_HALF, LA_ROTARY_INTERLEAVED = 0, 1
+LA_ROTARY_PLAIN, LA_ROTARY_LINEAR, LA_ROTARY_PARTS = 0, 1, 2
+LA_ACT_NONE, LA_ACT_SILU = 0, 1
+
+GATE_KINDS = {"value": LA_GATE_VALUE, "log": LA_GATE_LOG, "sigmoid": LA_GATE_SIGMOID}
+ROTARY_LAYOUTS = {"half": LA_ROTARY_HALF, "interleaved": LA_ROTARY_INTERLEAVED}
+ROTARY_SCALINGS = {"none": LA_ROTARY_PLAIN, "linear": LA_ROTARY_LINEAR, "parts": LA_ROTARY_PARTS}
+ACTIVATIONS = {"none": LA_ACT_NONE, "silu": LA_ACT_SILU}
 FEATURE_MAPS = {"identity": LA_FM_IDENTITY, "elu1": LA_FM_ELU1, "favor": LA_FM_FAVOR}
 
 # every function the header declares (checked by the tests against include/la_chunked.h)
@@ -42,7 +52,9 @@ EXPORTS = ("la_chunked_fwd", "la_chunked_fwd_path", "la_chunked_fwd_host",
            "la_decay_fwd", "la_decay_decode_step", "la_decay_workspace_bytes", "la_decay_plan",
            "la_chunked_bwd", "la_chunked_bwd_workspace_bytes", "la_chunked_bwd_ll",
            "la_chunked_bwd_ll_workspace_bytes", "la_chunked_state",
-           "la_state_combine", "la_chunked_fwd_init", "la_version")
+           "la_state_combine", "la_chunked_fwd_init", "la_recurrence_fwd", "la_recurrence_bwd",
+           "la_recurrence_step", "la_rotary_table", "la_rotary", "la_group_norm_fwd",
+           "la_group_norm_bwd", "la_group_norm_bwd_workspace_bytes", "la_version")
 
 
 class la_feature_map(ctypes.Structure):
@@ -58,6 +70,10 @@ class la_plan_info(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class la_strides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("l", ctypes.c_longlong)]
 
 
 class LAError(RuntimeError):
@@ -138,6 +154,23 @@ def lib() -> ctypes.CDLL:
             L.la_chunked_fwd_init.argtypes = [p, p, p, p, i, i, i, i, i, i, fmp, i, f, p, p, i, p, sz,
                                               p, i]
             L.la_chunked_fwd_init.restype = i
+            stp, d8 = ctypes.POINTER(la_strides), ctypes.c_double
+            L.la_recurrence_fwd.argtypes = [p] * 7 + [i] * 4 + [stp] * 3 + [i] * 4 + [p]
+            L.la_recurrence_fwd.restype = i
+            L.la_recurrence_bwd.argtypes = [p] * 9 + [i] * 4 + [stp] * 5 + [i] * 4 + [p]
+            L.la_recurrence_bwd.restype = i
+            L.la_recurrence_step.argtypes = [p] * 4 + [i] * 7 + [p]
+            L.la_recurrence_step.restype = i
+            L.la_rotary_table.argtypes = [i, d8, i, d8, d8, d8, d8, ctypes.POINTER(ctypes.c_ulonglong)]
+            L.la_rotary_table.restype = i
+            L.la_rotary.argtypes = [p] * 6 + [ll] + [i] * 6 + [stp] * 4 + [i, i, f, i, p]
+            L.la_rotary.restype = i
+            L.la_group_norm_fwd.argtypes = [p] * 5 + [i] * 4 + [stp] * 3 + [i, i, f, i, p]
+            L.la_group_norm_fwd.restype = i
+            L.la_group_norm_bwd.argtypes = [p] * 9 + [i] * 4 + [stp] * 5 + [i, i, f, i, p, sz, p]
+            L.la_group_norm_bwd.restype = i
+            L.la_group_norm_bwd_workspace_bytes.argtypes = [i] * 4
+            L.la_group_norm_bwd_workspace_bytes.restype = sz
             L.la_version.argtypes = []
             L.la_version.restype = ctypes.c_char_p
             _lib = L
@@ -304,6 +337,59 @@ def la_chunked_fwd_init(q, k, v, out, B, H, L, dk, dv, C, feature_map, normalize
     return lib().la_chunked_fwd_init(q, k, v, out, B, H, L, dk, dv, C, _fm(feature_map), normalize,
                                      gamma, state0, zstate0, dtype, workspace, workspace_bytes,
                                      stream, path)
+
+
+def la_recurrence_fwd(x, gate, h0, lengths, out, h_last, chunk_states, B, H, L, d, x_strides,
+                      gate_strides, out_strides, gate_kind, complement, dtype, gate_dtype,
+                      stream) -> int:
+    return lib().la_recurrence_fwd(x, gate, h0, lengths, out, h_last, chunk_states, B, H, L, d,
+                                   x_strides, gate_strides, out_strides, gate_kind, complement,
+                                   dtype, gate_dtype, stream)
+
+
+def la_recurrence_bwd(x, gate, chunk_states, lengths, dout, dh_last, dx, dgate, dh0, B, H, L, d,
+                      x_strides, gate_strides, dout_strides, dx_strides, dgate_strides, gate_kind,
+                      complement, dtype, gate_dtype, stream) -> int:
+    return lib().la_recurrence_bwd(x, gate, chunk_states, lengths, dout, dh_last, dx, dgate, dh0,
+                                   B, H, L, d, x_strides, gate_strides, dout_strides, dx_strides,
+                                   dgate_strides, gate_kind, complement, dtype, gate_dtype, stream)
+
+
+def la_recurrence_step(x, gate, state, out, B, H, d, gate_kind, complement, dtype, gate_dtype,
+                       stream) -> int:
+    return lib().la_recurrence_step(x, gate, state, out, B, H, d, gate_kind, complement, dtype,
+                                    gate_dtype, stream)
+
+
+def la_rotary_table(rot, base, scaling, factor, original_length, fast, slow, turns) -> int:
+    return lib().la_rotary_table(rot, base, scaling, factor, original_length, fast, slow, turns)
+
+
+def la_rotary(q, k, q_out, k_out, turns, positions, offset, B, H, Hk, L, d, rot, q_strides,
+              k_strides, q_out_strides, k_out_strides, layout, inverse, amplitude, dtype,
+              stream) -> int:
+    return lib().la_rotary(q, k, q_out, k_out, turns, positions, offset, B, H, Hk, L, d, rot,
+                           q_strides, k_strides, q_out_strides, k_out_strides, layout, inverse,
+                           amplitude, dtype, stream)
+
+
+def la_group_norm_fwd(x, weight, bias, gate, out, B, H, L, d, x_strides, gate_strides, out_strides,
+                      center, activation, eps, dtype, stream) -> int:
+    return lib().la_group_norm_fwd(x, weight, bias, gate, out, B, H, L, d, x_strides, gate_strides,
+                                   out_strides, center, activation, eps, dtype, stream)
+
+
+def la_group_norm_bwd(x, weight, bias, gate, dout, dx, dgate, dweight, dbias, B, H, L, d, x_strides,
+                      gate_strides, dout_strides, dx_strides, dgate_strides, center, activation, eps,
+                      dtype, workspace, workspace_bytes, stream) -> int:
+    return lib().la_group_norm_bwd(x, weight, bias, gate, dout, dx, dgate, dweight, dbias, B, H, L,
+                                   d, x_strides, gate_strides, dout_strides, dx_strides,
+                                   dgate_strides, center, activation, eps, dtype, workspace,
+                                   workspace_bytes, stream)
+
+
+def la_group_norm_bwd_workspace_bytes(B, H, L, d) -> int:
+    return lib().la_group_norm_bwd_workspace_bytes(B, H, L, d)
 
 
 def la_version() -> str:
@@ -593,3 +679,224 @@ def chunked_fwd(q, k, v, C=64, feature_map="identity", omega=None, normalize=Fal
     if rc != LA_OK:
         raise LAError(rc, "la_chunked_fwd")
     return out
+
+
+# ---- around the attention: recurrence, rotary positions, group norm ---------------------
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _view(t, B, H, L, d, name, dtype, device):
+    """Strides argument of a [B, H, L, d] tensor (None when contiguous)."""
+    if tuple(t.shape) != (B, H, L, d):
+        raise ValueError(f"{name} must be {(B, H, L, d)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return None
+    sb, sh, sl, sd = t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the channels (last axis) must be adjacent")
+    return ctypes.byref(la_strides(sb, sh, sl))
+
+
+def _view_last(t, B, H, L, d, name, dtype, device):
+    """Strides argument of a [B, L, H*d] tensor, channels last (None when contiguous)."""
+    if tuple(t.shape) != (B, L, H * d):
+        raise ValueError(f"{name} must be {(B, L, H * d)}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return None
+    sb, sl, sd = t.stride()
+    if sd != 1 and H * d > 1:
+        raise ValueError(f"{name}: the channels (last axis) must be adjacent")
+    return ctypes.byref(la_strides(sb, d, sl))
+
+
+def _dense(t, shape, name, dtype, device):
+    """Pointer of a contiguous tensor of that shape and type (None stays None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {shape} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _launch(what, fn, device, stream, *args):
+    """Calls fn(*args, stream) on the tensors' device; raises LAError on a bad status."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"{what}: CUDA tensors are needed, got {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index is None or device.index == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc != LA_OK:
+        raise LAError(rc, what)
+
+
+def recurrence_fwd(x, gate, h0=None, gate_kind="sigmoid", complement=False, lengths=None,
+                   save_chunks=False, out=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + w_t x_t (la_recurrence_fwd) of CUDA tensors
+    x, gate [B,H,L,d] (bf16 or fp32 each, strided views allowed).  gate_kind: "value", "log" or
+    "sigmoid"; complement: w = 1 - a instead of 1.  h0 [B,H,d] fp32: the state before row 0.
+    lengths [B] int32: rows behind a sequence's end are 0 and keep the state.  Returns (out,
+    h_last [B,H,d] fp32), with save_chunks also the chunk states that recurrence_bwd reads."""
+    import torch
+    B, H, L, d = x.shape
+    dev, f32 = x.device, torch.float32
+    if out is None:
+        out = torch.empty((B, H, L, d), dtype=x.dtype, device=dev)
+    last = torch.empty((B, H, d), dtype=f32, device=dev)
+    chunks = None
+    if save_chunks:
+        chunks = torch.empty((B, H, -(-L // LA_RECURRENCE_CHUNK), d), dtype=f32, device=dev)
+    _launch("la_recurrence_fwd", lib().la_recurrence_fwd, dev, stream, x.data_ptr(), gate.data_ptr(),
+            _dense(h0, (B, H, d), "h0", f32, dev), _dense(lengths, (B,), "lengths", torch.int32, dev),
+            out.data_ptr(), last.data_ptr(), _ptr(chunks), B, H, L, d,
+            _view(x, B, H, L, d, "x", x.dtype, dev), _view(gate, B, H, L, d, "gate", gate.dtype, dev),
+            _view(out, B, H, L, d, "out", x.dtype, dev), GATE_KINDS[gate_kind], int(complement),
+            _dtype_code(x), _dtype_code(gate))
+    return (out, last, chunks) if save_chunks else (out, last)
+
+
+def recurrence_bwd(x, gate, chunk_states, dout, dh_last=None, gate_kind="sigmoid",
+                   complement=False, lengths=None, dx=None, dgate=None, stream=None):
+    """(dx, dgate, dh0) of recurrence_fwd(..., save_chunks=True) for dout [B,H,L,d] and dh_last
+    [B,H,d] fp32 (None: zero); dh0 [B,H,d] fp32 is the gradient of h0."""
+    import torch
+    B, H, L, d = x.shape
+    dev, f32 = x.device, torch.float32
+    if dx is None:
+        dx = torch.empty((B, H, L, d), dtype=x.dtype, device=dev)
+    if dgate is None:
+        dgate = torch.empty((B, H, L, d), dtype=gate.dtype, device=dev)
+    dh0 = torch.empty((B, H, d), dtype=f32, device=dev)
+    nc = -(-L // LA_RECURRENCE_CHUNK)
+    _launch("la_recurrence_bwd", lib().la_recurrence_bwd, dev, stream, x.data_ptr(), gate.data_ptr(),
+            _dense(chunk_states, (B, H, nc, d), "chunk_states", f32, dev),
+            _dense(lengths, (B,), "lengths", torch.int32, dev), dout.data_ptr(),
+            _dense(dh_last, (B, H, d), "dh_last", f32, dev), dx.data_ptr(), dgate.data_ptr(),
+            dh0.data_ptr(), B, H, L, d, _view(x, B, H, L, d, "x", x.dtype, dev),
+            _view(gate, B, H, L, d, "gate", gate.dtype, dev),
+            _view(dout, B, H, L, d, "dout", x.dtype, dev), _view(dx, B, H, L, d, "dx", x.dtype, dev),
+            _view(dgate, B, H, L, d, "dgate", gate.dtype, dev), GATE_KINDS[gate_kind],
+            int(complement), _dtype_code(x), _dtype_code(gate))
+    return dx, dgate, dh0
+
+
+def recurrence_step(x, gate, state, gate_kind="sigmoid", complement=False, out=None, stream=None):
+    """One decoding step of the recurrence: x, gate [B,H,d] (this token), state [B,H,d] fp32
+    updated in place.  Returns out [B,H,d]."""
+    import torch
+    B, H, d = x.shape
+    dev = x.device
+    if out is None:
+        out = torch.empty((B, H, d), dtype=x.dtype, device=dev)
+    _launch("la_recurrence_step", lib().la_recurrence_step, dev, stream,
+            _dense(x, (B, H, d), "x", x.dtype, dev), _dense(gate, (B, H, d), "gate", gate.dtype, dev),
+            _dense(state, (B, H, d), "state", torch.float32, dev),
+            _dense(out, (B, H, d), "out", x.dtype, dev), B, H, d, GATE_KINDS[gate_kind],
+            int(complement), _dtype_code(x), _dtype_code(gate))
+    return out
+
+
+class RotaryTable:
+    """Frequencies of rotary(): turns (int64 CUDA tensor [rot/2], a turn per position in units
+    of 2^-64), rot channels, amplitude of the rotated pairs."""
+
+    def __init__(self, turns, rot, amplitude=1.0):
+        self.turns, self.rot, self.amplitude = turns, rot, amplitude
+
+
+def rotary_table(rot, base=10000.0, scaling="none", factor=1.0, original_length=0.0, fast=32.0,
+                 slow=1.0, amplitude=1.0, device="cuda"):
+    """The table rotary() reads, made once (la_rotary_table).  scaling: "none", "linear" (every
+    frequency / factor) or "parts" (only those of few turns over original_length)."""
+    import torch
+    host = (ctypes.c_ulonglong * (rot // 2))()
+    rc = la_rotary_table(rot, float(base), ROTARY_SCALINGS[scaling], float(factor),
+                         float(original_length), float(fast), float(slow), host)
+    if rc != LA_OK:
+        raise LAError(rc, "la_rotary_table")
+    signed = [v - (1 << 64) if v >> 63 else v for v in host]
+    return RotaryTable(torch.tensor(signed, dtype=torch.int64, device=device), rot, float(amplitude))
+
+
+def rotary(q, k, table, positions=None, offset=0, layout="half", inverse=False, q_out=None,
+           k_out=None, stream=None):
+    """q [B,H,L,d] and k [B,Hk,L,d] (k may be None) turned by their positions (la_rotary):
+    positions [B,L] int32, or offset + t.  Strided views are allowed on both sides, and q_out=q,
+    k_out=k for in place.  inverse turns back, which is also the gradient.  Returns (q_out,
+    k_out)."""
+    import torch
+    B, H, L, d = q.shape
+    dev, dt = q.device, q.dtype
+    if q_out is None:
+        q_out = torch.empty((B, H, L, d), dtype=dt, device=dev)
+    Hk, ks, kos = 0, None, None
+    if k is not None:
+        Hk = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((B, Hk, L, d), dtype=dt, device=dev)
+        ks = _view(k, B, Hk, L, d, "k", dt, dev)
+        kos = _view(k_out, B, Hk, L, d, "k_out", dt, dev)
+    _launch("la_rotary", lib().la_rotary, dev, stream, q.data_ptr(), _ptr(k), q_out.data_ptr(),
+            _ptr(k_out), _dense(table.turns, (table.rot // 2,), "table", torch.int64, dev),
+            _dense(positions, (B, L), "positions", torch.int32, dev), int(offset), B, H, Hk, L, d,
+            table.rot, _view(q, B, H, L, d, "q", dt, dev), ks,
+            _view(q_out, B, H, L, d, "q_out", dt, dev), kos, ROTARY_LAYOUTS[layout], int(inverse),
+            table.amplitude, _dtype_code(q))
+    return q_out, k_out
+
+
+def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="silu", center=True,
+                   out=None, stream=None):
+    """Group norm of x [B,H,L,d] over each head's channels (la_group_norm_fwd), channels last on
+    the way out: y = xh weight + bias, out [B,L,H*d] = y act(gate) with gate [B,L,H*d], else
+    act(y).  weight, bias: fp32, H*d values, or None; center=False leaves the mean in."""
+    import torch
+    B, H, L, d = x.shape
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    if out is None:
+        out = torch.empty((B, L, H * d), dtype=dt, device=dev)
+    _launch("la_group_norm_fwd", lib().la_group_norm_fwd, dev, stream, x.data_ptr(),
+            _dense(weight, (H * d,), "weight", f32, dev), _dense(bias, (H * d,), "bias", f32, dev),
+            _ptr(gate), out.data_ptr(), B, H, L, d, _view(x, B, H, L, d, "x", dt, dev),
+            None if gate is None else _view_last(gate, B, H, L, d, "gate", dt, dev),
+            _view_last(out, B, H, L, d, "out", dt, dev), int(center), ACTIVATIONS[activation],
+            float(eps), _dtype_code(x))
+    return out
+
+
+def group_norm_bwd(x, dout, weight=None, bias=None, gate=None, eps=1e-5, activation="silu",
+                   center=True, dx=None, dgate=None, workspace=None, stream=None):
+    """(dx, dgate, dweight, dbias) of group_norm_fwd for dout [B,L,H*d]; None where the forward
+    had None."""
+    import torch
+    B, H, L, d = x.shape
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    if dx is None:
+        dx = torch.empty((B, H, L, d), dtype=dt, device=dev)
+    if gate is not None and dgate is None:
+        dgate = torch.empty((B, L, H * d), dtype=dt, device=dev)
+    dw = torch.empty(H * d, dtype=f32, device=dev) if weight is not None else None
+    db = torch.empty(H * d, dtype=f32, device=dev) if bias is not None else None
+    need = la_group_norm_bwd_workspace_bytes(B, H, L, d) if dw is not None or db is not None else 0
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch("la_group_norm_bwd", lib().la_group_norm_bwd, dev, stream, x.data_ptr(),
+            _dense(weight, (H * d,), "weight", f32, dev), _dense(bias, (H * d,), "bias", f32, dev),
+            _ptr(gate), dout.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), B, H, L, d,
+            _view(x, B, H, L, d, "x", dt, dev),
+            None if gate is None else _view_last(gate, B, H, L, d, "gate", dt, dev),
+            _view_last(dout, B, H, L, d, "dout", dt, dev), _view(dx, B, H, L, d, "dx", dt, dev),
+            None if gate is None else _view_last(dgate, B, H, L, d, "dgate", dt, dev), int(center),
+            ACTIVATIONS[activation], float(eps), _dtype_code(x), workspace.data_ptr() if need else None,
+            need)
+    return dx, dgate, dw, db

@@ -1,0 +1,89 @@
+// layer.cuh -- strided [B, H, L, d] views and their checks, shared by the operators that
+// stand around the attention (recurrence, rotary positions, group norm).
+#pragma once
+
+#include <limits.h>
+
+#include "common.cuh"
+
+namespace la {
+
+// Element (b, h, t, i) at b * b_ + h * h_ + t * l_ + i.
+struct View {
+    long long b, h, l;
+};
+
+__host__ __device__ inline long long row_of(const View &v, int b, int h, int t)
+{
+    return b * v.b + h * v.h + t * v.l;
+}
+
+// Contiguous [B, H, L, d] (head_major) or [B, L, H, d] where no strides are given.
+inline View make_view(const la_strides *s, int H, int L, int d, bool head_major = true)
+{
+    if (s) return View{s->b, s->h, s->l};
+    if (head_major) return View{(long long)H * L * d, (long long)L * d, d};
+    return View{(long long)H * L * d, d, (long long)H * d};
+}
+
+// Sizes every one of these operators takes: positive, below 2^31 heads in all and 2^20 channels
+// (grid limits), and element counts that 64-bit offsets hold with room to spare.
+inline bool sizes_ok(int B, int H, int L, int d)
+{
+    if (B <= 0 || H <= 0 || L <= 0 || d <= 0 || d > (1 << 20)) return false;
+    return (double)B * H * L * d < 4.6e18 && (double)B * H < (double)INT_MAX;
+}
+
+inline size_t dtype_size(int dtype) { return dtype == LA_F32 ? 4 : 2; }
+
+inline bool dtype_ok(int dtype) { return dtype == LA_BF16 || dtype == LA_F32; }
+
+inline bool aligned(const void *p, size_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+
+// Strides of an input: not negative, offsets inside 2^60 elements.
+inline bool input_view_ok(const View &v, int B, int H, int L)
+{
+    const long long s[3] = {v.b, v.h, v.l};
+    const int n[3] = {B, H, L};
+    __int128 top = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (s[i] < 0) return false;
+        top += (__int128)s[i] * (n[i] - 1);
+    }
+    return top < ((__int128)1 << 60);
+}
+
+// Strides of an output: also no two elements in one place.  Sorted by stride, each axis must
+// step over everything the axes below it span.
+inline bool output_view_ok(const View &v, int B, int H, int L, int d)
+{
+    if (!input_view_ok(v, B, H, L)) return false;
+    long long s[3] = {v.b, v.h, v.l};
+    int n[3] = {B, H, L};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (s[j] < s[i]) {
+                const long long ts = s[i];
+                s[i] = s[j];
+                s[j] = ts;
+                const int tn = n[i];
+                n[i] = n[j];
+                n[j] = tn;
+            }
+    __int128 span = d;  // elements the axes so far span
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) continue;
+        if (s[i] < span) return false;
+        span += (__int128)s[i] * (n[i] - 1);
+    }
+    return true;
+}
+
+// All rows of the view start on `bytes`-byte boundaries.
+inline bool rows_aligned(const void *p, const View &v, int B, int H, int L, size_t elem, size_t bytes)
+{
+    auto ok = [&](long long s, int n) { return n == 1 || (s * (long long)elem) % (long long)bytes == 0; };
+    return aligned(p, bytes) && ok(v.b, B) && ok(v.h, H) && ok(v.l, L);
+}
+
+}  // namespace la

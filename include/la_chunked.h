@@ -56,7 +56,7 @@ enum la_status {
     LA_ERR_DEVICE = -7,      /* device: an index or shape check failed inside a kernel    */
     LA_ERR_SCRATCH_LIMIT = -8, /* la_chunked_fwd_noalloc: the problem needs more scratch than
                                   its fixed buffer holds (8 MiB)                          */
-    LA_ERR_ARG = -9            /* an argument value is out of range (la_decay_*: gamma)    */
+    LA_ERR_ARG = -9            /* an argument value is out of range (gamma, eps, strides)  */
 };
 
 /* ---- feature maps phi -------------------------------------------------------------- */
@@ -430,6 +430,174 @@ int la_chunked_fwd_init(const void *q, const void *k, const void *v, void *out, 
                         int dk, int dv, int C, const la_feature_map *feature_map, int normalize,
                         float gamma, const float *state0, const float *zstate0, int dtype,
                         void *workspace, size_t workspace_bytes, void *stream, int path);
+
+/* ---- what stands around the attention: rotary positions, a gated recurrence, group norm ----
+ *
+ * None of the three is on the pages' hot path; they are what a layer built from it needs next
+ * to it: the rotation of q and k that goes with the Retention decay, a recurrence whose decay
+ * is data instead of one constant, and the per-head normalisation with a gate that replaces
+ * the attention normaliser.  Layouts are [B, H, L, d] with adjacent channels; the strides of
+ * the other three axes may be given, so that they work on views of a fused projection.
+ * Every call runs on the current device; tensors must live there. */
+
+/* Strides in elements: element (b, h, t, i) is at b*strides.b + h*strides.h + t*strides.l + i.
+ * A NULL pointer means contiguous [B, H, L, d].  Strides of inputs must not be negative (0
+ * broadcasts); those of outputs must keep all elements apart (LA_ERR_ARG otherwise). */
+typedef struct la_strides {
+    long long b, h, l;
+} la_strides;
+
+/* How the recurrence's gate a_t follows from the gate input g_t. */
+enum la_gate_kind {
+    LA_GATE_VALUE = 0,  /* a = g                                                          */
+    LA_GATE_LOG = 1,    /* a = exp(g); g = -inf is a = 0                                  */
+    LA_GATE_SIGMOID = 2 /* a = 1 / (1 + exp(-g))                                          */
+};
+
+/* Rows per stored state of la_recurrence_fwd. */
+#define LA_RECURRENCE_CHUNK 128
+
+/*
+ * la_recurrence_fwd -- gated linear recurrence, one scalar state per channel:
+ *     h_t = a_t h_{t-1} + w_t x_t,   out_t = h_t,   w = 1, or 1 - a with `complement`,
+ * the elementwise counterpart of the decayed state S_t = gamma S_{t-1} + phi(k_t) v_t^T with
+ * a decay per token and channel.  A gate of 0 forgets everything before its row (the first
+ * row of a packed document).  States, gates and sums are fp32; out is rounded once.
+ *   x, out        [B, H, L, d], dtype `dtype`
+ *   gate          [B, H, L, d], dtype `gate_dtype`; gates are meant to be in [0, 1] (others
+ *                 are computed as the formula says, products of up to L of them in fp32)
+ *   h0            device fp32 [B, H, d], the state before row 0, or NULL for zero
+ *   lengths       NULL, or device int [B]: sequence b ends after lengths[b] rows (clamped to
+ *                 0..L).  Rows behind are not read; out is 0 there and the state stays.
+ *   h_last        device fp32 [B, H, d], the state after the last row, or NULL; may be h0
+ *   chunk_states  device fp32 [B, H, ceil(L / LA_RECURRENCE_CHUNK), d] or NULL: the states
+ *                 before rows 0, 128, 256, ..., which la_recurrence_bwd reads
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED (dtype, gate kind), LA_ERR_ARG
+ * (strides) or LA_ERR_CUDA.  Asynchronous on `stream`, no workspace; the sums' order depends
+ * on the sizes alone, so equal calls give equal bits.
+ */
+int la_recurrence_fwd(const void *x, const void *gate, const float *h0, const int *lengths,
+                      void *out, float *h_last, float *chunk_states, int B, int H, int L, int d,
+                      const la_strides *x_strides, const la_strides *gate_strides,
+                      const la_strides *out_strides, int gate_kind, int complement, int dtype,
+                      int gate_dtype, void *stream);
+
+/*
+ * la_recurrence_bwd -- its gradients.  With e_t = dout_t + a_{t+1} e_{t+1} (dh_last behind the
+ * last row):
+ *     dx_t = w_t e_t,  dgate_t = e_t (h_{t-1} - [complement] x_t) da/dg,  dh0 = a_0 e_0.
+ * h_{t-1} is recomputed in fp32 from x, gate and the forward's chunk_states; the forward's
+ * rounded output is not an input.
+ *   dout          [B, H, L, d], dtype `dtype`
+ *   dh_last       device fp32 [B, H, d], the gradient of h_last, or NULL for zero
+ *   dx, dgate     [B, H, L, d], dtype `dtype` and `gate_dtype`; fully overwritten, 0 behind a
+ *                 sequence's end
+ *   dh0           device fp32 [B, H, d] or NULL; may be dh_last
+ * Other arguments and errors as la_recurrence_fwd.
+ */
+int la_recurrence_bwd(const void *x, const void *gate, const float *chunk_states,
+                      const int *lengths, const void *dout, const float *dh_last, void *dx,
+                      void *dgate, float *dh0, int B, int H, int L, int d,
+                      const la_strides *x_strides, const la_strides *gate_strides,
+                      const la_strides *dout_strides, const la_strides *dx_strides,
+                      const la_strides *dgate_strides, int gate_kind, int complement, int dtype,
+                      int gate_dtype, void *stream);
+
+/* One decoding step: state = a state + w x, out = state, for contiguous [B, H, d] x, gate, out
+ * and fp32 state (updated in place, as la_decode_step's).  Stepping t = 0..L-1 reproduces
+ * la_recurrence_fwd's rows. */
+int la_recurrence_step(const void *x, const void *gate, float *state, void *out, int B, int H,
+                       int d, int gate_kind, int complement, int dtype, int gate_dtype,
+                       void *stream);
+
+/* ---- rotary positions ---- */
+enum la_rotary_layout {
+    LA_ROTARY_HALF = 0,       /* channel j is turned with channel j + rot/2               */
+    LA_ROTARY_INTERLEAVED = 1 /* channel 2j is turned with channel 2j + 1                 */
+};
+
+/* How the frequencies are scaled for contexts `factor` times the original length. */
+enum la_rotary_scaling {
+    LA_ROTARY_PLAIN = 0,  /* theta_j = base^(-2j/rot)                                       */
+    LA_ROTARY_LINEAR = 1, /* theta_j / factor                                               */
+    LA_ROTARY_PARTS = 2   /* by turns r over the original length: theta_j where r >= fast,
+                             theta_j / factor where r <= slow, mixed linearly in r between  */
+};
+
+/*
+ * la_rotary_table -- host only: fills turns[0..rot/2) with the frequencies as fractions of a
+ * full turn per position, in units of 2^-64.  A position times that, modulo 2^64, is its
+ * angle without any loss however far the position is.  The caller copies the table to the
+ * device and keeps it.  fast, slow, original_length are read for LA_ROTARY_PARTS only (0 < slow
+ * < fast).  LA_ERR_SHAPE for rot <= 0 or odd, LA_ERR_ARG for base <= 0, factor < 1 or values
+ * that are not finite.
+ */
+int la_rotary_table(int rot, double base, int scaling, double factor, double original_length,
+                    double fast, double slow, unsigned long long *turns);
+
+/*
+ * la_rotary -- turns the first `rot` channels of q and k by their positions: a pair (u, v) at
+ * position p becomes amplitude (u cos - v sin, u sin + v cos) of the angle p theta_j; channels
+ * from rot on are copied.  The gradient of a rotation is the rotation back: `inverse` turns
+ * by -p theta_j (amplitude stays a factor).
+ *   q, q_out      [B, H, L, d], k, k_out [B, Hk, L, d], dtype `dtype`; k and k_out may both be
+ *                 NULL.  q_out may be q with the same strides (in place), k_out likewise;
+ *                 other overlaps are not allowed.
+ *   turns         device copy of la_rotary_table's array, rot/2 entries (rot = 0: may be NULL)
+ *   positions     device int [B, L], or NULL: row t of every sequence is at offset + t
+ *   rot           even, 0 <= rot <= d
+ * Angles are exact to 2^-33 of a turn, sines and cosines fp32; each output is rounded once.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED, LA_ERR_ARG or LA_ERR_CUDA.
+ */
+int la_rotary(const void *q, const void *k, void *q_out, void *k_out,
+              const unsigned long long *turns, const int *positions, long long offset, int B,
+              int H, int Hk, int L, int d, int rot, const la_strides *q_strides,
+              const la_strides *k_strides, const la_strides *q_out_strides,
+              const la_strides *k_out_strides, int layout, int inverse, float amplitude,
+              int dtype, void *stream);
+
+/* ---- group norm with an activation, channels last ---- */
+enum la_activation {
+    LA_ACT_NONE = 0, /* act(y) = y                                                        */
+    LA_ACT_SILU = 1  /* act(y) = y / (1 + exp(-y))                                        */
+};
+
+/*
+ * la_group_norm_fwd -- the channels of each token normalised in H groups of d, as they leave
+ * the attention, with the gate that follows it:
+ *     xh = (x - mean) / sqrt(var + eps)  over the d channels of (b, h, t)
+ *          (center = 0: x / sqrt(mean(x^2) + eps)),
+ *     y = xh weight + bias,   out = y act(gate) with a gate, act(y) without.
+ *   x             [B, H, L, d] (the attention's output layout), dtype `dtype`
+ *   weight, bias  device fp32 [H, d] or NULL (1 and 0)
+ *   gate, out     dtype `dtype`; their NULL strides mean contiguous [B, L, H, d], channels
+ *                 last (gate itself may be NULL)
+ *   eps           > 0 and finite, else LA_ERR_ARG
+ * Statistics are fp32 over values held in fp32, the variance from centred values.
+ */
+int la_group_norm_fwd(const void *x, const float *weight, const float *bias, const void *gate,
+                      void *out, int B, int H, int L, int d, const la_strides *x_strides,
+                      const la_strides *gate_strides, const la_strides *out_strides, int center,
+                      int activation, float eps, int dtype, void *stream);
+
+/*
+ * la_group_norm_bwd -- its gradients from dout (as out, NULL strides: [B, L, H, d]): dx (as x),
+ * dgate (as gate; NULL if and only if gate is), dweight and dbias (device fp32 [H, d], each
+ * may be NULL).  Statistics are recomputed from x.  dweight and dbias are summed in a fixed
+ * order through the workspace of la_group_norm_bwd_workspace_bytes(...) bytes (0 when neither
+ * is asked for).
+ */
+int la_group_norm_bwd(const void *x, const float *weight, const float *bias, const void *gate,
+                      const void *dout, void *dx, void *dgate, float *dweight, float *dbias,
+                      int B, int H, int L, int d, const la_strides *x_strides,
+                      const la_strides *gate_strides, const la_strides *dout_strides,
+                      const la_strides *dx_strides, const la_strides *dgate_strides, int center,
+                      int activation, float eps, int dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Workspace bytes la_group_norm_bwd needs for these sizes when weight gradients are asked for
+ * (0 on invalid arguments). */
+size_t la_group_norm_bwd_workspace_bytes(int B, int H, int L, int d);
 
 /* Library version string, e.g. "0.1.0". */
 const char *la_version(void);
