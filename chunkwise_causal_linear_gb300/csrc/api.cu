@@ -69,7 +69,7 @@ static int *err_ptr()
     return ptrs[dev];
 }
 
-static int device_sms()
+int device_sms()
 {
     static int sms[64] = {0};
     int dev = 0;

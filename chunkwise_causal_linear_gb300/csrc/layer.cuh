@@ -8,6 +8,8 @@
 
 namespace la {
 
+int device_sms();  // SMs of the current device, 0 on an error (api.cu)
+
 // Element (b, h, t, i) at b * b_ + h * h_ + t * l_ + i.
 struct View {
     long long b, h, l;
@@ -31,6 +33,7 @@ inline View make_view(const la_strides *s, int H, int L, int d, bool head_major 
 inline bool sizes_ok(int B, int H, int L, int d)
 {
     if (B <= 0 || H <= 0 || L <= 0 || d <= 0 || d > (1 << 20)) return false;
+    if (L > INT_MAX - (1 << 16)) return false;  // row numbers of a last, partial tile stay ints
     return (double)B * H * L * d < 4.6e18 && (double)B * H < (double)INT_MAX;
 }
 
