@@ -33,7 +33,7 @@ LA_BF16, LA_F32 = 0, 1
 LA_PATH_AUTO, LA_PATH_SIMT, LA_PATH_TC = 0, 1, 2
 
 LA_GATE_VALUE, LA_GATE_LOG, LA_GATE_SIGMOID = 0, 1, 2
-LA_RECURRENCE_CHUNK = 128
+LA_RECURRENCE_CHUNK = 64
 LA_ROTARY_HALF, LA_ROTARY_INTERLEAVED = 0, 1
 LA_ROTARY_PLAIN, LA_ROTARY_LINEAR, LA_ROTARY_PARTS = 0, 1, 2
 LA_ACT_NONE, LA_ACT_SILU = 0, 1

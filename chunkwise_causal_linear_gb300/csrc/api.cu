@@ -56,7 +56,7 @@ int ilog2(int x)
 // ---- device error word (one per device) -------------------------------------------
 __device__ int g_la_err = 0;
 
-static int *err_ptr()
+int *err_ptr()
 {
     static int *ptrs[64] = {nullptr};
     int dev = 0;

@@ -9,6 +9,7 @@
 namespace la {
 
 int device_sms();  // SMs of the current device, 0 on an error (api.cu)
+int *err_ptr();    // its device error word, NULL on an error
 
 // Element (b, h, t, i) at b * b_ + h * h_ + t * l_ + i.
 struct View {

@@ -7,31 +7,37 @@
 // c_t = a_t e_t, e_t = dout_t + c_{t+1}: c -> P c + E with the same P.
 //
 // The rows of one head's block of 32 V channels go through one cluster of S blocks (S = 1: one
-// block).  A step of the cluster covers S tiles of 128 rows, one per block; a tile is 8 warps
-// of 16 rows, a lane holds V channels of them in registers.  Per step: fold the 16 rows, put
-// (P, H) into shared memory, one block barrier, fold the 8 warps; with S > 1 every block then
-// writes its tile's (P, H) into the others' shared memory and one cluster barrier later every
-// block knows the state before its tile and after the step.  Every input is read once and every
-// output written once; nothing goes through global memory between the blocks, no flag is
-// waited for, and the order of the sums depends on the sizes alone.
+// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R rows (16
+// forward, 8 backward, which holds three values a row and channel), a lane holds V channels of
+// them in registers, V = 2 as pairs for the packed fp32 instructions.  Per step: fold the R rows,
+// put (P, H) into shared memory, one block barrier, run the carried state over the 8 warps.  With
+// S > 1 every block sends its tile's (P, H) into the others' shared memory (st.async, which
+// counts on an mbarrier there), and folds its next tile before it waits for what the others sent
+// for this one; the release of a cluster barrier in that place waited for the output rows still
+// on their way (a quarter of the time).  Every input is read once and every output written
+// once; nothing goes through global memory between the blocks, and the order of the sums
+// depends on the sizes alone.
 //
-// The kernel is bound by memory (12 bytes and ~40 instructions an fp32 element), so the inputs
-// of the next steps are on the way while one is folded: each warp copies its own rows into its
-// own ring in shared memory (cp.async, no barrier).
+// The inputs of the next steps are on the way while one is folded: each warp copies its own rows
+// into its own ring in shared memory (cp.async, no barrier).
 #include <algorithm>
+#include <type_traits>
 
 #include "layer.cuh"
+#include "tc_ptx.cuh"
 
 namespace la {
 
+using namespace ptx;
+
 namespace {
 
-constexpr int RC = LA_RECURRENCE_CHUNK;
-constexpr int REC_W = 8;             // warps of a tile
-constexpr int REC_R = RC / REC_W;    // rows of a warp
+constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the forward leaves
+constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
-constexpr int REC_STAGES = 3;        // ring: one step in work, two on the way
-constexpr int REC_MAX_SPLIT = 8;     // portable cluster size
+constexpr int REC_MAX_SPLIT = 8;         // blocks of a portable cluster
+constexpr int FWD_R = 16, BWD_R = 8;     // rows of a warp
+static_assert(BWD_R * REC_W == RC && RC % FWD_R == 0, "backward tiles and forward warps start at chunks");
 
 struct RecArgs {
     const void *x, *g, *dout;
@@ -44,36 +50,147 @@ struct RecArgs {
     int ncb;            // channel blocks of a head
     int split;          // blocks of a cluster
     int grx, grg, gro;  // bytes per copy of x, gate, dout: 16, 4 or 2 (their alignment)
+    int *err;           // device error word
 };
 
-// a, w and da/dg from the gate input.  1 - a comes from its own formula where a is close to 1.
-// expf is good to 1 ulp and the approximate reciprocal of [1, 2] too, so a and 1 - a are off by
-// at most 6 units of 2^-24.
-template <int KIND, bool COMP>
-__device__ __forceinline__ void gate_of(float g, float &a, float &w, float &slope)
+constexpr uint64_t REC_TIMEOUT_NS = 2000000000ull;  // limit of a wait for another block
+
+
+// 2^x and 1/x by the special function unit: relative error 2^-22 and 2^-23, results below the
+// normal range flushed to 0.
+__device__ __forceinline__ float ex2(float x)
 {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// V channels of a lane; pairs use the packed fp32 instructions.
+template <int V> struct Ch {
+    float v[V];
+};
+template <int V> __device__ __forceinline__ Ch<V> all(float x)
+{
+    Ch<V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = x;
+    return r;
+}
+__device__ __forceinline__ Ch<1> fma(Ch<1> a, Ch<1> b, Ch<1> c) { return {{fmaf(a.v[0], b.v[0], c.v[0])}}; }
+__device__ __forceinline__ Ch<1> mul(Ch<1> a, Ch<1> b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ Ch<1> add(Ch<1> a, Ch<1> b) { return {{a.v[0] + b.v[0]}}; }
+__device__ __forceinline__ Ch<2> fma(Ch<2> a, Ch<2> b, Ch<2> c)
+{
+    Ch<2> r;
+    asm("{ .reg .b64 x, y, z, w;\n"
+        "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.v[0]), "=f"(r.v[1])
+        : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]), "f"(c.v[0]), "f"(c.v[1]));
+    return r;
+}
+__device__ __forceinline__ Ch<2> mul(Ch<2> a, Ch<2> b)
+{
+    Ch<2> r;
+    asm("{ .reg .b64 x, y, w;\n"
+        "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+        "mul.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.v[0]), "=f"(r.v[1]) : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+    return r;
+}
+__device__ __forceinline__ Ch<2> add(Ch<2> a, Ch<2> b)
+{
+    Ch<2> r;
+    asm("{ .reg .b64 x, y, w;\n"
+        "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+        "add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.v[0]), "=f"(r.v[1]) : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+    return r;
+}
+
+// a and 1 - a from the gate input, 1 - a (computed where WANT_C) from its own formula where a is
+// close to 1.  With u = 2^-24 both are off by at most (9 + 1.3 |g|) u relatively: the argument
+// g log2(e) is rounded (1.3 |g| u), 2^x 4 u, the sum 1 u, the reciprocal 2 u, a product or
+// difference 1 u.  Accurate versions of the exponential and the quotient cost 20 more
+// instructions an element and made the bf16 kernel 1.6 times slower than with plain gates.
+template <int KIND, bool WANT_C, int V>
+__device__ __forceinline__ void gate_of(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
+{
+    constexpr float LOG2E = 1.44269504f;
     if (KIND == LA_GATE_VALUE) {
         a = g;
-        w = COMP ? 1.f - g : 1.f;
-        slope = 1.f;
+        if (WANT_C) c = fma(g, all<V>(-1.f), all<V>(1.f));
     } else if (KIND == LA_GATE_LOG) {
-        a = expf(g);
-        w = COMP ? -expm1f(g) : 1.f;
-        slope = a;
+        const Ch<V> t = mul(g, all<V>(LOG2E));
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.v[v] = ex2(t.v[v]);
+        if (WANT_C) {
+            // -expm1(g): below log 2 from s = expm1(g / 2) by its series, expm1(g) = s (s + 2)
+            // (the first term left out is 2e-8 of the sum)
+            const Ch<V> y = mul(g, all<V>(0.5f));
+            Ch<V> p = fma(y, all<V>(1.f / 5040), all<V>(1.f / 720));
+            p = fma(y, p, all<V>(1.f / 120));
+            p = fma(y, p, all<V>(1.f / 24));
+            p = fma(y, p, all<V>(1.f / 6));
+            p = fma(y, p, all<V>(0.5f));
+            p = fma(y, p, all<V>(1.f));
+            const Ch<V> s = mul(y, p), n = mul(s, all<V>(-1.f));
+            const Ch<V> e = mul(n, add(s, all<V>(2.f))), f = fma(a, all<V>(-1.f), all<V>(1.f));
+#pragma unroll
+            for (int v = 0; v < V; ++v) c.v[v] = fabsf(g.v[v]) < 0.693f ? e.v[v] : f.v[v];
+        }
     } else {
-        // sigmoid(g) and sigmoid(-g) from e^-|g|, which never overflows
-        const float e = expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e), s = e * r;
-        a = g >= 0.f ? r : s;
-        const float c = g >= 0.f ? s : r;
-        w = COMP ? c : 1.f;
-        slope = a * c;
+        // a = 1 / (1 + e), 1 - a = e a; where e is so large that a is 0, 1 - a is 1
+        Ch<V> e = mul(g, all<V>(-LOG2E));
+#pragma unroll
+        for (int v = 0; v < V; ++v) e.v[v] = ex2(e.v[v]);
+        const Ch<V> d = add(e, all<V>(1.f));
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.v[v] = rcp(d.v[v]);
+        if (WANT_C) {
+            c = mul(e, a);
+#pragma unroll
+            for (int v = 0; v < V; ++v) c.v[v] = a.v[v] == 0.f ? 1.f : c.v[v];
+        }
     }
 }
 
 // The state times a gate (or a product of gates), a gate of 0 forgetting infinities and NaN as
 // well.
-__device__ __forceinline__ float forget(float a, float h) { return a == 0.f ? 0.f : a * h; }
-__device__ __forceinline__ float step(float a, float h, float b) { return a == 0.f ? b : fmaf(a, h, b); }
+template <int V> __device__ __forceinline__ Ch<V> forget(const Ch<V> &a, const Ch<V> &h)
+{
+    Ch<V> r = mul(a, h);
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.v[v] = a.v[v] == 0.f ? 0.f : r.v[v];
+    return r;
+}
+template <int V> __device__ __forceinline__ Ch<V> step(const Ch<V> &a, const Ch<V> &h, const Ch<V> &b)
+{
+    Ch<V> r = fma(a, h, b);
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.v[v] = a.v[v] == 0.f ? b.v[v] : r.v[v];
+    return r;
+}
+// One row.  EXACT = false leaves out the forgetting of infinities and NaN, which then stay to the
+// last row: whoever finds that one finite has the same value as with EXACT.
+template <bool EXACT, int V> __device__ __forceinline__ Ch<V> row(const Ch<V> &a, const Ch<V> &h, const Ch<V> &b)
+{
+    if constexpr (EXACT) return step(a, h, b);
+    else return fma(a, h, b);
+}
+template <int V> __device__ __forceinline__ bool finite(const Ch<V> &h)
+{
+    bool ok = true;
+#pragma unroll
+    for (int v = 0; v < V; ++v) ok = ok && fabsf(h.v[v]) <= 3.402823466e38f;
+    return ok;
+}
 
 __device__ __forceinline__ int rows_of(const RecArgs &a, int b)
 {
@@ -93,427 +210,584 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 // Rows [0, nrow) and channels [0, nch) of a warp's rows into its ring slot, CW channels a row, in
 // copies of `gran` bytes: N copies make a row, a warp makes 32 / N rows at once.
-template <typename T, int CW, int BYTES>
+template <typename T, int R, int CW, int BYTES, int ROW = CW>
 __device__ __forceinline__ void copy_by(T *slot, const T *src, long long stride, int nrow, int nch, int lane)
 {
-    constexpr int E = BYTES / sizeof(T), N = CW / E, RP = 32 / N;
-    static_assert(32 % N == 0 && REC_R % RP == 0, "whole rows per warp instruction");
-    const int r0 = lane / N, c = lane % N * E;
-    if (c >= nch) return;
-    const T *p = src + r0 * stride + c;
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot) + lane * BYTES;
-    constexpr int M = REC_R / RP, BATCH = M < 8 ? M : 8;
-    for (int j0 = 0; j0 < M; j0 += BATCH) {
+    constexpr int E = BYTES / sizeof(T), N = CW / E;
+    if constexpr (N > 32) {  // a row takes two instructions: by halves
+        copy_by<T, R, CW / 2, BYTES, ROW>(slot, src, stride, nrow, nch, lane);
+        copy_by<T, R, CW / 2, BYTES, ROW>(slot + CW / 2, src + CW / 2, stride, nrow, nch - CW / 2, lane);
+    } else {
+        constexpr int RP = 32 / N, M = R / RP;
+        static_assert(32 % N == 0 && R % RP == 0, "whole rows per warp instruction");
+        const int r0 = lane / N, c = lane % N * E;
+        if (c >= nch) return;
+        const T *p = src + r0 * stride + c;
+        T *q = slot + r0 * ROW + c;
         if constexpr (BYTES == 2) {
-            T v[BATCH];
+            constexpr int BATCH = 4;  // loads on the way at once
+#pragma unroll 1
+            for (int i = 0; i < M; i += BATCH) {
+                T v[BATCH];
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j, p += RP * stride)
-                if (r0 + (j0 + j) * RP < nrow) v[j] = *p;
+                for (int j = 0; j < BATCH; ++j, p += RP * stride)
+                    if (r0 + (i + j) * RP < nrow) v[j] = *p;
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) slot[lane + 32 * (j0 + j)] = v[j];
+                for (int j = 0; j < BATCH; ++j, q += RP * ROW) *q = v[j];
+            }
         } else {
+            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(q);
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j, p += RP * stride)
-                if (r0 + (j0 + j) * RP < nrow) cp_async<BYTES>(dst + 32 * BYTES * (j0 + j), p);
+            for (int j = 0; j < M; ++j, p += RP * stride)
+                if (r0 + j * RP < nrow) cp_async<BYTES>(dst + (uint32_t)sizeof(T) * j * RP * ROW, p);
         }
     }
 }
-template <typename T, int CW>
+template <typename T, int R, int CW>
 __device__ __forceinline__ void copy_rows(T *slot, const T *src, long long stride, int nrow, int nch, int gran,
                                           int lane)
 {
     if (nrow <= 0) return;
-    if (gran == 16) copy_by<T, CW, 16>(slot, src, stride, nrow, nch, lane);
-    else if (gran == 4) copy_by<T, CW, 4>(slot, src, stride, nrow, nch, lane);
-    else if constexpr (sizeof(T) == 2 && CW == 32) copy_by<T, CW, 2>(slot, src, stride, nrow, nch, lane);
+    if (gran == 16) copy_by<T, R, CW, 16>(slot, src, stride, nrow, nch, lane);
+    else if (gran == 4) copy_by<T, R, CW, 4>(slot, src, stride, nrow, nch, lane);
+    else if constexpr (sizeof(T) == 2 && CW == 32) copy_by<T, R, CW, 2>(slot, src, stride, nrow, nch, lane);
 }
 
-// ---- V neighbouring channels ----------------------------------------------------------------
-template <int V> __device__ __forceinline__ void get(const float *p, float (&v)[V])
+// ---- V neighbouring channels (pairs are aligned and inside the channels together) -------------
+template <int V> __device__ __forceinline__ Ch<V> get(const float *p)
 {
     if constexpr (V == 2) {
         const float2 t = *(const float2 *)p;
-        v[0] = t.x;
-        v[1] = t.y;
+        return {{t.x, t.y}};
     } else {
-        v[0] = *p;
+        return {{*p}};
     }
 }
-template <int V> __device__ __forceinline__ void get(const __nv_bfloat16 *p, float (&v)[V])
+template <int V> __device__ __forceinline__ Ch<V> get(const __nv_bfloat16 *p)
 {
     if constexpr (V == 2) {
-        const float2 t = __bfloat1622float2(*(const __nv_bfloat162 *)p);
-        v[0] = t.x;
-        v[1] = t.y;
+        const uint32_t t = *(const uint32_t *)p;
+        return {{__uint_as_float(t << 16), __uint_as_float(t & 0xffff0000u)}};
     } else {
-        v[0] = __bfloat162float(*p);
+        return {{__bfloat162float(*p)}};
     }
 }
-// V = 2 is launched only where pairs are aligned and inside the channels together
-template <int V> __device__ __forceinline__ void put(float *p, const float (&v)[V])
+template <int V> __device__ __forceinline__ void put(float *p, const Ch<V> &x)
 {
-    if constexpr (V == 2) *(float2 *)p = make_float2(v[0], v[1]);
-    else *p = v[0];
+    if constexpr (V == 2) *(float2 *)p = make_float2(x.v[0], x.v[1]);
+    else *p = x.v[0];
 }
-template <int V> __device__ __forceinline__ void put(__nv_bfloat16 *p, const float (&v)[V])
+template <int V> __device__ __forceinline__ void put(__nv_bfloat16 *p, const Ch<V> &x)
 {
-    if constexpr (V == 2) *(__nv_bfloat162 *)p = __floats2bfloat162_rn(v[0], v[1]);
-    else *p = __float2bfloat16_rn(v[0]);
+    if constexpr (V == 2) *(__nv_bfloat162 *)p = __floats2bfloat162_rn(x.v[0], x.v[1]);
+    else *p = __float2bfloat16_rn(x.v[0]);
 }
+// (P, H) of V channels, next to each other in shared memory
+template <int V> struct __align__(8 * V) Fold {
+    Ch<V> p, h;
+};
 
 // ---- between the blocks of a cluster -----------------------------------------------------------
-__device__ __forceinline__ void cluster_put(uint32_t addr, int rank, float p, float h)
+// Sends a fold to `slot` in block `rank` of the cluster, counted there on `bar`.
+template <int V>
+__device__ __forceinline__ void send(const Fold<V> *slot, const uint64_t *bar, int rank, const Fold<V> &f)
 {
-    uint32_t far;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(far), "f"(p), "f"(h) : "memory");
+    uint32_t to, sig;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(slot)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(sig) : "r"(smem_u32(bar)), "r"(rank));
+    if constexpr (V == 2)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                     "f"(f.p.v[0]), "f"(f.p.v[1]), "f"(f.h.v[0]), "f"(f.h.v[1]), "r"(sig) : "memory");
+    else
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                     "f"(f.p.v[0]), "f"(f.h.v[0]), "r"(sig) : "memory");
 }
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; "
+                 "selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(200000u) : "memory");
+    return ok != 0;
+}
 
-// The folds of a step: warps of the tile (agg, two buffers), tiles of the cluster (peer, two).
-// Two buffers and one barrier a step are enough: a buffer is written again two steps later,
-// after a barrier that every reader of it has reached.
-template <int CW>
-struct RecFolds {
-    float2 agg[2][REC_W][CW];
-    float2 peer[2][REC_MAX_SPLIT][CW];
+// What the blocks of a cluster send one another: three buffers, each with its mbarrier.  Step k
+// uses buffer k % 3: a block sends for step k + 3 after it has what every block sent for step
+// k + 2, and a block sends that after the block barrier of its step k + 2, which its warps reach
+// when they have read step k.
+constexpr int REC_BUFS = 3;
+template <int V> struct Peers {
+    Fold<V> *slot;  // [REC_BUFS][split][32]
+    uint64_t *bar;  // [REC_BUFS]
+    int split, rank, *err;
+    bool dead;  // a wait ran out: no more waiting
+
+    __device__ void init(void *mem, int split_, int rank_, int *err_)
+    {
+        bar = (uint64_t *)mem;
+        slot = (Fold<V> *)((char *)mem + 16 * REC_BUFS);
+        split = split_;
+        rank = rank_;
+        err = err_;
+        dead = false;
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < REC_BUFS; ++i) mbar_init(&bar[i], 1);
+            mbar_init_fence();
+        }
+        cluster_barrier();  // every block is there, with its barriers, before anyone sends
+    }
+    __device__ __forceinline__ void publish(int k, int warp, int lane, const Fold<V> &f)
+    {
+        const int buf = k % REC_BUFS;
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<V>)));
+        if (warp < split) send<V>(slot + (buf * split + rank) * 32 + lane, &bar[buf], warp, f);
+    }
+    // The carry over the tiles of step k, `carry = P carry + H`: returns the carry before this
+    // block's tile and leaves the one after the step.
+    __device__ __forceinline__ Ch<V> over(int k, int lane, Ch<V> &carry)
+    {
+        const int buf = k % REC_BUFS;
+        const uint32_t parity = (k / REC_BUFS) & 1;
+        if (!dead && !arrived(&bar[buf], parity)) {
+            const uint64_t t0 = globaltimer();
+            while (!arrived(&bar[buf], parity))
+                if (globaltimer() - t0 > REC_TIMEOUT_NS) {
+                    record_error(err, LA_ERR_TIMEOUT);
+                    dead = true;
+                    break;
+                }
+        }
+        const Fold<V> *f = slot + buf * split * 32 + lane;
+        const Ch<V> start = carry;
+        Ch<V> mine = carry;
+        for (int r = 0; r < split; ++r, f += 32) {
+            if (r == rank) mine = carry;
+            carry = fma(f->p, carry, f->h);
+        }
+        if (!finite(carry)) {
+            f = slot + buf * split * 32 + lane;
+            carry = start;
+            for (int r = 0; r < split; ++r, f += 32) {
+                if (r == rank) mine = carry;
+                carry = step(f->p, carry, f->h);
+            }
+        }
+        return mine;
+    }
+    static constexpr size_t bytes(int split) { return 16 * REC_BUFS + sizeof(Fold<V>) * REC_BUFS * split * 32; }
 };
 
-// The carry through the tiles of a step in order `carry = P carry + H`: returns the carry before
-// this block's tile and leaves the one after the step.  tot: this tile's fold.
-template <int V, int CW>
-__device__ __forceinline__ void across_tiles(RecFolds<CW> &f, int buf, int split, int rank, int warp, int lane,
-                                             const float (&P)[V], const float (&H)[V], float (&carry)[V],
-                                             float (&mine)[V])
-{
-    if (split == 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            mine[v] = carry[v];
-            carry[v] = step(P[v], carry[v], H[v]);
-        }
-        return;
-    }
-    if (warp < split) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            cluster_put((uint32_t)__cvta_generic_to_shared(&f.peer[buf][rank][lane * V + v]), warp, P[v], H[v]);
-    }
-    cluster_barrier();
-    for (int r = 0; r < split; ++r) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (r == rank) mine[v] = carry[v];
-            const float2 q = f.peer[buf][r][lane * V + v];
-            carry[v] = step(q.x, carry[v], q.y);
-        }
-    }
-}
+// Shared memory: the folds of a step for the warps of the tile, in three buffers as well (a warp
+// may be a step ahead of another that still reads), the rings, and what the blocks of the
+// cluster send.
+template <typename T, typename G, int V, bool BWD> struct RecSmem {
+    static constexpr int R = BWD ? BWD_R : FWD_R;
+    static constexpr size_t AGG = sizeof(Fold<V>) * REC_BUFS * REC_W * 32;
+    static constexpr size_t AHEAD = BWD ? AGG / 2 : 0;  // backward: H beside (P, E)
+    static constexpr size_t SLOT = (size_t)R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
+    static constexpr size_t STAGE = REC_W * SLOT;
+    // three stages where two blocks share an SM with them (227 KB, 1 KB taken a block), else two
+    static constexpr int STAGES = AGG + AHEAD + 3 * STAGE <= 112 * 1024 ? 3 : 2;
+    static constexpr size_t PEERS = AGG + AHEAD + STAGES * STAGE;
+    static size_t bytes(int split) { return PEERS + (split > 1 ? Peers<V>::bytes(split) : 0); }
+};
 
-template <typename T, typename G, int V>
-__host__ __device__ constexpr size_t rec_slot_bytes(bool bwd) { return (size_t)REC_R * 32 * V * (sizeof(T) * (bwd ? 2 : 1) + sizeof(G)); }
-template <typename T, typename G, int V>
-constexpr size_t rec_smem(bool bwd)
-{
-    return sizeof(RecFolds<32 * V>) * (bwd ? 2 : 1) + REC_STAGES * REC_W * rec_slot_bytes<T, G, V>(bwd);
-}
+// threadIdx.x / 32 as a value that the compiler knows to be the same in the whole warp
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
 
 // ---- forward ---------------------------------------------------------------------------------
-template <typename T, typename G, int KIND, bool COMP, int V>
+template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
 __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a)
 {
-    constexpr int CW = 32 * V;
+    using Sm = RecSmem<T, G, V, false>;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = FWD_R, TILE = R * REC_W;
     extern __shared__ __align__(16) unsigned char smem[];
-    RecFolds<CW> &folds = *(RecFolds<CW> *)smem;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = a.split, rank = blockIdx.x % split, blk = blockIdx.x / split;
+    Fold<V> *const agg = (Fold<V> *)smem;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0, blk = blockIdx.x / split;
     const int bh = blk / a.ncb, c0 = blk % a.ncb * CW, b = bh / a.H, hd = bh % a.H;
     const int c = c0 + lane * V;
     const bool on = c < a.d;
     const T *x = (const T *)a.x + row_of(a.vx, b, hd, 0) + c0;
     const G *g = (const G *)a.g + row_of(a.vg, b, hd, 0) + c0;
-    T *out = (T *)a.out + row_of(a.vo, b, hd, 0) + c;
-    const int n = rows_of(a, b), nt = (a.L + RC - 1) / RC, steps = (nt + split - 1) / split;
-    unsigned char *ring = smem + sizeof(RecFolds<CW>) + warp * rec_slot_bytes<T, G, V>(false);
-    auto slot = [&](int k) { return ring + (k % REC_STAGES) * (REC_W * rec_slot_bytes<T, G, V>(false)); };
-    auto first_row = [&](int k) { return (k * split + rank) * RC + warp * REC_R; };
+    T *out = (T *)a.out + row_of(a.vo, b, hd, 0) + c0;
+    const int n = rows_of(a, b), nc = (a.L + RC - 1) / RC;
+    const int nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
+    unsigned char *const ring = smem + Sm::AGG + warp * Sm::SLOT;
+    auto first_row = [&](int k) { return (k * split + rank) * TILE + warp * R; };
+    int in = 0, at = 0;  // ring slots of the next copy and the next step
     auto load = [&](int k) {
         if (k < steps) {
-            const int t0 = first_row(k), rows = min(n - t0, REC_R);
-            T *sx = (T *)slot(k);
-            copy_rows<T, CW>(sx, x + t0 * a.vx.l, a.vx.l, rows, a.d - c0, a.grx, lane);
-            copy_rows<G, CW>((G *)(sx + REC_R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane);
+            const int t0 = first_row(k), rows = min(n - t0, R);
+            T *sx = (T *)(ring + in * Sm::STAGE);
+            copy_rows<T, R, CW>(sx, x + t0 * a.vx.l, a.vx.l, rows, a.d - c0, a.grx, lane);
+            copy_rows<G, R, CW>((G *)(sx + R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane);
         }
         cp_commit();
+        in = in + 1 == ST ? 0 : in + 1;
     };
-    float carry[V];
+    Ch<V> carry = all<V>(0.f);
+    if (a.h0 && on)
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = a.h0 && on ? a.h0[(size_t)bh * a.d + c + v] : 0.f;
-#pragma unroll
-    for (int k = 0; k < REC_STAGES - 1; ++k) load(k);
-    if (split > 1) cluster_barrier();  // every block of the cluster is there before it is written to
-    for (int k = 0; k < steps; ++k) {
-        cp_wait<REC_STAGES - 2>();
+        for (int v = 0; v < V; ++v) carry.v[v] = a.h0[(size_t)bh * a.d + c + v];
+
+    struct Step {
+        Ch<V> a[R], b[R];  // gates and what joins the state
+    };
+    // the rows of step k; their fold goes to the warps of the tile
+    auto fold = [&](int k, Step &s) {
+        cp_wait<ST - 2>();
         __syncwarp();
-        const T *sx = (const T *)slot(k);
-        const G *sg = (const G *)(sx + REC_R * CW);
-        const int t0 = first_row(k), rows = min(n - t0, REC_R);
-        float ga[REC_R][V], bx[REC_R][V], P[V], H[V];
+        const T *sx = (const T *)(ring + at * Sm::STAGE) + lane * V;
+        const G *sg = (const G *)(ring + at * Sm::STAGE + sizeof(T) * R * CW) + lane * V;
+        at = at + 1 == ST ? 0 : at + 1;
+        const int rows = min(n - first_row(k), R);
 #pragma unroll
-        for (int i = 0; i < REC_R; ++i) {
-            float xv[V], gv[V];
-            get<V>(sx + i * CW + lane * V, xv);
-            get<V>(sg + i * CW + lane * V, gv);
+        for (int i = 0; i < R; ++i) {
+            const Ch<V> xv = get<V>(sx + i * CW);
+            Ch<V> w;
+            gate_of<KIND, COMP, V>(get<V>(sg + i * CW), s.a[i], w);
+            s.b[i] = COMP ? mul(w, xv) : xv;
+        }
+        if constexpr (ST == 2) __syncwarp();
+        load(k + ST - 1);  // into the slot that the whole warp has read
+        if (rows < R) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float w, sl;
-                gate_of<KIND, COMP>(gv[v], ga[i][v], w, sl);
-                bx[i][v] = COMP ? w * xv[v] : xv[v];
+            for (int i = 0; i < R; ++i)
+                if (i >= rows) {
+                    s.a[i] = all<V>(1.f);
+                    s.b[i] = all<V>(0.f);
+                }
+        }
+        Fold<V> f;
+        auto run = [&](auto exact) {
+            f.p = s.a[0];
+            f.h = s.b[0];
+#pragma unroll
+            for (int i = 1; i < R; ++i) {
+                f.h = row<decltype(exact)::value>(s.a[i], f.h, s.b[i]);
+                f.p = mul(f.p, s.a[i]);
             }
-        }
-        load(k + REC_STAGES - 1);  // into the slot of step k - 1, which the whole warp has read
-        if (rows < REC_R) {
-#pragma unroll
-            for (int i = 0; i < REC_R; ++i)
-                if (i >= rows)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        ga[i][v] = 1.f;
-                        bx[i][v] = 0.f;
-                    }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            P[v] = ga[0][v];
-            H[v] = bx[0][v];
-#pragma unroll
-            for (int i = 1; i < REC_R; ++i) {
-                H[v] = step(ga[i][v], H[v], bx[i][v]);
-                P[v] *= ga[i][v];
-            }
-        }
-        const int buf = k & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) folds.agg[buf][warp][lane * V + v] = make_float2(P[v], H[v]);
+        };
+        run(std::false_type());
+        if (!finite(f.h)) run(std::true_type());
+        agg[(k % REC_BUFS * REC_W + warp) * 32 + lane] = f;
         __syncthreads();
-        // the rows of the warps before this one, and of the tile
-        float Pw[V], Hw[V];
+    };
+    // the fold of the tile, for the other blocks
+    auto whole_tile = [&](int k) {
+        const Fold<V> *f = agg + k % REC_BUFS * REC_W * 32 + lane;
+        Fold<V> t = f[0];
+        auto run = [&](auto exact) {
+            t = f[0];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            P[v] = 1.f;
-            H[v] = 0.f;
+            for (int w = 1; w < REC_W; ++w) {
+                const Fold<V> q = f[w * 32];
+                t.h = row<decltype(exact)::value>(q.p, t.h, q.h);
+                t.p = mul(q.p, t.p);
+            }
+        };
+        run(std::false_type());
+        if (!finite(t.h)) run(std::true_type());
+        return t;
+    };
+    // h from the state before the tile to that before this warp; returns the one after the tile
+    auto over_warps = [&](int k, Ch<V> &h) {
+        const Fold<V> *f = agg + k % REC_BUFS * REC_W * 32 + lane;
+        const Ch<V> start = h;
+        Ch<V> e = h;
+        auto run = [&](auto exact) {
+            e = start;
 #pragma unroll
             for (int w = 0; w < REC_W; ++w) {
-                if (w == warp) {
-                    Pw[v] = P[v];
-                    Hw[v] = H[v];
-                }
-                const float2 q = folds.agg[buf][w][lane * V + v];
-                H[v] = step(q.x, H[v], q.y);
-                P[v] *= q.x;
+                if (w == warp) h = e;
+                const Fold<V> q = f[w * 32];
+                e = row<decltype(exact)::value>(q.p, e, q.h);
             }
-        }
-        float h[V];
-        across_tiles<V, CW>(folds, buf, split, rank, warp, lane, P, H, carry, h);
-        const int tile = k * split + rank;
-        if (a.chunks && warp == 0 && on && tile < nt)
+        };
+        run(std::false_type());
+        if (!finite(e)) run(std::true_type());
+        return e;
+    };
+    // the rows of step k from the state before them
+    auto finish = [&](int k, const Step &s, const Ch<V> &start) {
+        const int t0 = first_row(k), rows = min(n - t0, R);
+        if (a.chunks && t0 % RC == 0 && t0 < a.L && on)
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.chunks[((size_t)bh * nt + tile) * a.d + c + v] = h[v];
+            for (int v = 0; v < V; ++v) a.chunks[((size_t)bh * nc + t0 / RC) * a.d + c + v] = start.v[v];
+        T *const o = out + t0 * a.vo.l;
+        Ch<V> h;
+        auto run = [&](auto exact, auto whole) {
+            h = start;
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = step(Pw[v], h[v], Hw[v]);
-        T *o = out + t0 * a.vo.l;
-        if (rows == REC_R) {
-#pragma unroll
-            for (int i = 0; i < REC_R; ++i) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) h[v] = step(ga[i][v], h[v], bx[i][v]);
-                if (on) put<V>(o + i * a.vo.l, h);
+            for (int i = 0; i < R; ++i) {
+                h = row<decltype(exact)::value>(s.a[i], h, s.b[i]);
+                if (on && (decltype(whole)::value || t0 + i < a.L))
+                    put<V>(o + i * a.vo.l + lane * V, decltype(whole)::value || i < rows ? h : all<V>(0.f));
             }
+        };
+        if (rows == R) {
+            run(std::false_type(), std::true_type());
+            if (!finite(h)) run(std::true_type(), std::true_type());
         } else {
-#pragma unroll
-            for (int i = 0; i < REC_R; ++i) {
-                float z[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    h[v] = step(ga[i][v], h[v], bx[i][v]);
-                    z[v] = i < rows ? h[v] : 0.f;
-                }
-                if (on && t0 + i < a.L) put<V>(o + i * a.vo.l, z);
-            }
+            run(std::true_type(), std::false_type());
         }
+    };
+
+#pragma unroll
+    for (int k = 0; k < ST - 1; ++k) load(k);
+    if constexpr (!SPLIT) {
+        Step s;
+        for (int k = 0; k < steps; ++k) {
+            fold(k, s);
+            Ch<V> h = carry;
+            carry = over_warps(k, h);
+            finish(k, s, h);
+        }
+    } else {
+        // The next step is folded before what the others sent for this one is waited for.
+        Peers<V> peers;
+        peers.init(smem + Sm::PEERS, split, rank, a.err);
+        Step s0, s1;
+        fold(0, s0);
+        peers.publish(0, warp, lane, whole_tile(0));
+        auto turn = [&](int k, const Step &now, Step &next) {
+            if (k + 1 < steps) fold(k + 1, next);
+            Ch<V> h = peers.over(k, lane, carry);
+            if (k + 1 < steps) peers.publish(k + 1, warp, lane, whole_tile(k + 1));
+            over_warps(k, h);
+            finish(k, now, h);
+        };
+        for (int k = 0; k < steps; k += 2) {
+            turn(k, s0, s1);
+            if (k + 1 < steps) turn(k + 1, s1, s0);
+        }
+        cluster_barrier();  // nothing is sent to a block that has ended
     }
     if (a.h_last && rank == 0 && warp == 0 && on)
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.h_last[(size_t)bh * a.d + c + v] = carry[v];
+        for (int v = 0; v < V; ++v) a.h_last[(size_t)bh * a.d + c + v] = carry.v[v];
 }
 
 // ---- backward ----------------------------------------------------------------------------------
 // The tiles from the last to the first.  h before each row is run forward again from the state
 // that the forward left for the tile.
-template <typename T, typename G, int KIND, bool COMP, int V>
+template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
 __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a)
 {
-    constexpr int CW = 32 * V;
+    using Sm = RecSmem<T, G, V, true>;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = BWD_R, TILE = RC;
+    constexpr bool WANT_C = COMP || KIND == LA_GATE_SIGMOID;
     extern __shared__ __align__(16) unsigned char smem[];
-    RecFolds<CW> &back = *(RecFolds<CW> *)smem;                          // (P, E)
-    RecFolds<CW> &ahead = *(RecFolds<CW> *)(smem + sizeof(RecFolds<CW>));  // (P, H); agg alone
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = a.split, rank = blockIdx.x % split, blk = blockIdx.x / split;
+    Fold<V> *const agg = (Fold<V> *)smem;            // (P, E) of the warps
+    Ch<V> *const ahead = (Ch<V> *)(smem + Sm::AGG);  // their H
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0, blk = blockIdx.x / split;
     const int bh = blk / a.ncb, c0 = blk % a.ncb * CW, b = bh / a.H, hd = bh % a.H;
     const int c = c0 + lane * V;
     const bool on = c < a.d;
     const T *x = (const T *)a.x + row_of(a.vx, b, hd, 0) + c0;
     const G *g = (const G *)a.g + row_of(a.vg, b, hd, 0) + c0;
     const T *dout = (const T *)a.dout + row_of(a.vo, b, hd, 0) + c0;
-    T *dx = (T *)a.dx + row_of(a.vdx, b, hd, 0) + c;
-    G *dg = (G *)a.dg + row_of(a.vdg, b, hd, 0) + c;
-    const int n = rows_of(a, b), nt = (a.L + RC - 1) / RC, steps = (nt + split - 1) / split;
-    unsigned char *ring = smem + 2 * sizeof(RecFolds<CW>) + warp * rec_slot_bytes<T, G, V>(true);
-    auto slot = [&](int k) { return ring + (k % REC_STAGES) * (REC_W * rec_slot_bytes<T, G, V>(true)); };
+    T *dx = (T *)a.dx + row_of(a.vdx, b, hd, 0) + c0;
+    G *dg = (G *)a.dg + row_of(a.vdg, b, hd, 0) + c0;
+    const int n = rows_of(a, b), nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
+    unsigned char *const ring = smem + Sm::AGG + Sm::AHEAD + warp * Sm::SLOT;
     // a step's tiles run backwards; before the first tile there are none (negative rows)
-    auto first_row = [&](int k) { return (nt - 1 - (k * split + rank)) * RC + warp * REC_R; };
+    auto first_row = [&](int k) { return (nt - 1 - (k * split + rank)) * TILE + warp * R; };
+    int in = 0, at = 0;
     auto load = [&](int k) {
         if (k < steps && first_row(k) >= 0) {
-            const int t0 = first_row(k), rows = min(n - t0, REC_R);
-            T *sx = (T *)slot(k), *sd = sx + REC_R * CW;
-            copy_rows<T, CW>(sx, x + t0 * a.vx.l, a.vx.l, rows, a.d - c0, a.grx, lane);
-            copy_rows<T, CW>(sd, dout + t0 * a.vo.l, a.vo.l, rows, a.d - c0, a.gro, lane);
-            copy_rows<G, CW>((G *)(sd + REC_R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane);
+            const int t0 = first_row(k), rows = min(n - t0, R);
+            T *sx = (T *)(ring + in * Sm::STAGE), *sd = sx + R * CW;
+            copy_rows<T, R, CW>(sx, x + t0 * a.vx.l, a.vx.l, rows, a.d - c0, a.grx, lane);
+            copy_rows<T, R, CW>(sd, dout + t0 * a.vo.l, a.vo.l, rows, a.d - c0, a.gro, lane);
+            copy_rows<G, R, CW>((G *)(sd + R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane);
         }
         cp_commit();
+        in = in + 1 == ST ? 0 : in + 1;
     };
-    float carry[V];
+    Ch<V> carry = all<V>(0.f);  // a_{t+1} e_{t+1}
+    if (a.dh_last && on)
 #pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = a.dh_last && on ? a.dh_last[(size_t)bh * a.d + c + v] : 0.f;
+        for (int v = 0; v < V; ++v) carry.v[v] = a.dh_last[(size_t)bh * a.d + c + v];
 #pragma unroll
-    for (int k = 0; k < REC_STAGES - 1; ++k) load(k);
-    if (split > 1) cluster_barrier();
+    for (int k = 0; k < ST - 1; ++k) load(k);
+    Peers<V> peers;
+    if constexpr (SPLIT) peers.init(smem + Sm::PEERS, split, rank, a.err);
     for (int k = 0; k < steps; ++k) {
-        cp_wait<REC_STAGES - 2>();
-        __syncwarp();
-        load(k + REC_STAGES - 1);  // into the slot of step k - 1, which the whole warp has read
-        const T *sx = (const T *)slot(k), *sd = sx + REC_R * CW;
-        const G *sg = (const G *)(sd + REC_R * CW);
         const int tile = nt - 1 - (k * split + rank), t0 = first_row(k);
-        const int rows = tile < 0 ? 0 : min(n - t0, REC_R);
-        float h[V];  // the state before the tile
+        const int rows = tile < 0 ? 0 : min(n - t0, R);
+        Ch<V> h = all<V>(0.f);  // the state before the tile
+        if (on && tile >= 0)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            h[v] = on && tile >= 0 ? a.chunks_in[((size_t)bh * nt + tile) * a.d + c + v] : 0.f;
-        float ga[REC_R][V], hb[REC_R][V], P[V], H[V], E[V];  // hb: w x, then the state before the row
+            for (int v = 0; v < V; ++v) h.v[v] = a.chunks_in[((size_t)bh * nt + tile) * a.d + c + v];
+        cp_wait<ST - 2>();
+        __syncwarp();
+        if constexpr (ST > 2) load(k + ST - 1);  // into the slot of step k - 1, which the whole warp has read
+        const T *sx = (const T *)(ring + at * Sm::STAGE) + lane * V, *sd = sx + R * CW;
+        const G *sg = (const G *)(ring + at * Sm::STAGE + 2 * sizeof(T) * R * CW) + lane * V;
+        at = at + 1 == ST ? 0 : at + 1;
+        // hb: w x, then the state before the row; cc: 1 - a
+        Ch<V> ga[R], hb[R], cc[R];
 #pragma unroll
-        for (int i = 0; i < REC_R; ++i) {
-            float xv[V], gv[V];
-            get<V>(sx + i * CW + lane * V, xv);
-            get<V>(sg + i * CW + lane * V, gv);
+        for (int i = 0; i < R; ++i) {
+            const Ch<V> xv = get<V>(sx + i * CW);
+            gate_of<KIND, WANT_C, V>(get<V>(sg + i * CW), ga[i], cc[i]);
+            hb[i] = COMP ? mul(cc[i], xv) : xv;
+        }
+        if (rows < R) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float w, sl;
-                gate_of<KIND, COMP>(gv[v], ga[i][v], w, sl);
-                hb[i][v] = COMP ? w * xv[v] : xv[v];
+            for (int i = 0; i < R; ++i)
                 if (i >= rows) {
-                    ga[i][v] = 1.f;
-                    hb[i][v] = 0.f;
+                    ga[i] = all<V>(1.f);
+                    hb[i] = all<V>(0.f);
                 }
-            }
         }
+        Ch<V> P, H, E;
+        auto fold = [&](auto exact, auto whole) {
+            P = all<V>(1.f);
+            H = E = all<V>(0.f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            P[v] = 1.f;
-            H[v] = 0.f;
-            E[v] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < REC_R; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                H[v] = step(ga[i][v], H[v], hb[i][v]);
-                P[v] *= ga[i][v];
+            for (int i = 0; i < R; ++i) {
+                H = row<decltype(exact)::value>(ga[i], H, hb[i]);
+                P = mul(P, ga[i]);
             }
 #pragma unroll
-        for (int i = REC_R - 1; i >= 0; --i) {
-            float dv[V];
-            get<V>(sd + i * CW + lane * V, dv);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (i < rows) E[v] = forget(ga[i][v], E[v] + dv[v]);
+            for (int i = R - 1; i >= 0; --i)
+                if (decltype(whole)::value || i < rows) {
+                    const Ch<V> e = add(E, get<V>(sd + i * CW));
+                    E = decltype(exact)::value ? forget(ga[i], e) : mul(ga[i], e);
+                }
+        };
+        if (rows == R) {
+            fold(std::false_type(), std::true_type());
+            if (!finite(H) || !finite(E)) fold(std::true_type(), std::true_type());
+        } else {
+            fold(std::true_type(), std::false_type());
         }
-        const int buf = k & 1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            back.agg[buf][warp][lane * V + v] = make_float2(P[v], E[v]);
-            ahead.agg[buf][warp][lane * V + v] = make_float2(P[v], H[v]);
-        }
+        const int buf = k % REC_BUFS;
+        Fold<V> *const here = agg + buf * REC_W * 32 + lane;
+        Ch<V> *const front = ahead + buf * REC_W * 32 + lane;
+        here[warp * 32] = Fold<V>{P, E};
+        front[warp * 32] = H;
         __syncthreads();
-        float Pw[V], Ew[V];
+        Ch<V> e = carry;
+        if constexpr (SPLIT) {
+            Fold<V> t;
+            auto run = [&](auto exact) {
+                t = here[(REC_W - 1) * 32];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-#pragma unroll
-            for (int w = 0; w < REC_W; ++w)
-                if (w < warp) {
-                    const float2 q = ahead.agg[buf][w][lane * V + v];
-                    h[v] = step(q.x, h[v], q.y);
+                for (int w = REC_W - 2; w >= 0; --w) {
+                    const Fold<V> q = here[w * 32];
+                    t.h = row<decltype(exact)::value>(q.p, t.h, q.h);
+                    t.p = mul(q.p, t.p);
                 }
-            P[v] = 1.f;
-            E[v] = 0.f;
+            };
+            run(std::false_type());
+            if (!finite(t.h)) run(std::true_type());
+            peers.publish(k, warp, lane, t);
+        }
+        // h over the warps before this one, e over those behind it
+        {
+            const Ch<V> start = h;
+            auto run = [&](auto exact) {
+                h = start;
+                for (int w = 0; w < warp; ++w) h = row<decltype(exact)::value>(here[w * 32].p, h, front[w * 32]);
+            };
+            run(std::false_type());
+            if (!finite(h)) run(std::true_type());
+        }
+        if constexpr (SPLIT) e = peers.over(k, lane, carry);
+        {
+            const Ch<V> start = e;
+            Ch<V> f = e;
+            auto run = [&](auto exact) {
+                f = start;
 #pragma unroll
-            for (int w = REC_W - 1; w >= 0; --w) {
-                if (w == warp) {
-                    Pw[v] = P[v];
-                    Ew[v] = E[v];
+                for (int w = REC_W - 1; w >= 0; --w) {
+                    if (w == warp) e = f;
+                    const Fold<V> q = here[w * 32];
+                    f = row<decltype(exact)::value>(q.p, f, q.h);
                 }
-                const float2 q = back.agg[buf][w][lane * V + v];
-                E[v] = step(q.x, E[v], q.y);
-                P[v] *= q.x;
+            };
+            run(std::false_type());
+            if (!finite(f)) run(std::true_type());
+            if constexpr (!SPLIT) carry = f;
+        }
+        // run forward; on a result that is not finite once more, exactly, from w x
+        const Ch<V> hs = h;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const Ch<V> bx = hb[i];
+            hb[i] = h;
+            h = fma(ga[i], h, bx);
+        }
+        const bool tame = finite(h);
+        if (!tame) {
+            h = hs;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                hb[i] = h;
+                if (i < rows) {
+                    const Ch<V> xv = get<V>(sx + i * CW);
+                    h = step(ga[i], h, COMP ? mul(cc[i], xv) : xv);
+                }
             }
         }
-        float e[V];
-        across_tiles<V, CW>(back, buf, split, rank, warp, lane, P, E, carry, e);
+        T *const ox = dx + t0 * a.vdx.l;
+        G *const og = dg + t0 * a.vdg.l;
+        // With EXACT = false e and h are finite, so a slope of 0 makes the product 0 by itself.
+        auto finish = [&](auto exact, auto whole, Ch<V> &e) {
+            constexpr bool EX = decltype(exact)::value, ALL = decltype(whole)::value;
 #pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = step(Pw[v], e[v], Ew[v]);
-#pragma unroll
-        for (int i = 0; i < REC_R; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float bx = hb[i][v];
-                hb[i][v] = h[v];
-                h[v] = step(ga[i][v], h[v], bx);
-            }
-        if (tile >= 0) {
-            T *ox = dx + t0 * a.vdx.l;
-            G *og = dg + t0 * a.vdg.l;
-#pragma unroll
-            for (int i = REC_R - 1; i >= 0; --i) {
-                float xv[V], gv[V], dv[V], rx[V], rg[V];
-                get<V>(sx + i * CW + lane * V, xv);
-                get<V>(sg + i * CW + lane * V, gv);
-                get<V>(sd + i * CW + lane * V, dv);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float ai, w, sl;
-                    gate_of<KIND, COMP>(gv[v], ai, w, sl);
-                    rx[v] = rg[v] = 0.f;
-                    if (i < rows) {
-                        e[v] += dv[v];  // e_t
-                        rx[v] = COMP ? w * e[v] : e[v];
-                        rg[v] = forget(sl, e[v] * (COMP ? hb[i][v] - xv[v] : hb[i][v]));
-                        e[v] = forget(ga[i][v], e[v]);
+            for (int i = R - 1; i >= 0; --i) {
+                Ch<V> rx = all<V>(0.f), rg = rx;
+                if (ALL || i < rows) {
+                    e = add(e, get<V>(sd + i * CW));  // e_t
+                    rx = COMP ? mul(cc[i], e) : e;
+                    Ch<V> f = hb[i];
+                    if (COMP) f = fma(get<V>(sx + i * CW), all<V>(-1.f), f);
+                    if (KIND == LA_GATE_VALUE) {
+                        rg = mul(e, f);
+                        e = EX ? forget(ga[i], e) : mul(ga[i], e);
+                    } else {
+                        const Ch<V> ae = EX ? forget(ga[i], e) : mul(ga[i], e);
+                        const Ch<V> se = KIND == LA_GATE_LOG ? ae : EX ? forget(cc[i], ae) : mul(cc[i], ae);
+                        rg = EX ? forget(se, f) : mul(se, f);
+                        e = ae;
                     }
                 }
-                if (on && t0 + i < a.L) {
-                    put<V>(ox + i * a.vdx.l, rx);
-                    put<V>(og + i * a.vdg.l, rg);
+                if (on && (ALL || t0 + i < a.L)) {
+                    put<V>(ox + i * a.vdx.l + lane * V, rx);
+                    put<V>(og + i * a.vdg.l + lane * V, rg);
                 }
             }
+        };
+        if (rows == R) {
+            const Ch<V> e0 = e;
+            finish(std::false_type(), std::true_type(), e);
+            if (!tame || !finite(e)) {
+                e = e0;
+                finish(std::true_type(), std::true_type(), e);
+            }
+        } else if (tile >= 0) {
+            finish(std::true_type(), std::false_type(), e);
+        }
+        if constexpr (ST == 2) {
+            __syncwarp();
+            load(k + 1);
         }
     }
+    if constexpr (SPLIT) cluster_barrier();  // nothing is sent to a block that has ended
     if (a.dh0 && rank == 0 && warp == 0 && on)
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.dh0[(size_t)bh * a.d + c + v] = carry[v];
+        for (int v = 0; v < V; ++v) a.dh0[(size_t)bh * a.d + c + v] = carry.v[v];
 }
 
 constexpr int STEP_THREADS = 128;
@@ -524,20 +798,22 @@ __global__ void __launch_bounds__(STEP_THREADS) rec_step_kernel(const T *x, cons
 {
     const long long i = (long long)blockIdx.x * STEP_THREADS + threadIdx.x;
     if (i >= n) return;
-    float ga, w, sl;
-    gate_of<KIND, COMP>(to_f32(g[i]), ga, w, sl);
-    const float h = step(ga, state[i], COMP ? w * to_f32(x[i]) : to_f32(x[i]));
-    state[i] = h;
-    out[i] = from_f32<T>(h);
+    Ch<1> ga, c;
+    gate_of<KIND, COMP, 1>({{to_f32(g[i])}}, ga, c);
+    const Ch<1> xv{{to_f32(x[i])}}, h = step(ga, {{state[i]}}, COMP ? mul(c, xv) : xv);
+    state[i] = h.v[0];
+    out[i] = from_f32<T>(h.v[0]);
 }
 
 // ---- host side ---------------------------------------------------------------------------------
-// Blocks of a cluster: as many as the sequence has tiles for and one wave of the GPU (two blocks
-// an SM) holds.
-int choose_split(long long blocks, int L, int sms)
+// Blocks of a cluster: a power of two (those of other sizes do not pack into the GPU: 9 made 32
+// clusters two waves), as many as the sequence has tiles for and one wave of two blocks an SM
+// holds.
+int choose_split(long long blocks, long long tiles, int sms)
 {
-    const long long tiles = ((long long)L + RC - 1) / RC, fit = 2ll * sms / blocks;
-    return (int)std::max(1ll, std::min(std::min(tiles, fit), (long long)REC_MAX_SPLIT));
+    int split = 1;
+    while (split < REC_MAX_SPLIT && 2 * split * blocks <= 2ll * sms && split < tiles) split *= 2;
+    return split;
 }
 
 int granule(const void *p, const View &v, const RecArgs &a, size_t elem)
@@ -588,28 +864,38 @@ int dispatch(int dtype, int gate_dtype, int kind, int comp, F f)
                                 : by_kind(__nv_bfloat16(), __nv_bfloat16());
 }
 
-// Two channels a lane where both inputs are bf16 and pairs are whole and aligned: a row of a block
-// is then 128 bytes, as it is with one channel a lane in fp32.
+// Two channels a lane where pairs are whole and aligned and the blocks of 64 channels alone give
+// every SM one; else one channel a lane, for twice the blocks, and clusters over the rows.
 template <bool BWD>
 struct LaunchRec {
+    static constexpr int TILE = REC_W * (BWD ? BWD_R : FWD_R);
     RecArgs &a;
     int sms;
     cudaStream_t s;
-    template <typename T, typename G, int KIND, bool COMP, int V> int go() const
+    template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT> int go() const
     {
-        a.ncb = (a.d + 32 * V - 1) / (32 * V);
-        a.split = choose_split((long long)a.B * a.H * a.ncb, a.L, sms);
-        if constexpr (BWD) return launch_rec(rec_bwd_kernel<T, G, KIND, COMP, V>, a, rec_smem<T, G, V>(true), s);
-        else return launch_rec(rec_fwd_kernel<T, G, KIND, COMP, V>, a, rec_smem<T, G, V>(false), s);
+        const size_t smem = RecSmem<T, G, V, BWD>::bytes(a.split);
+        if constexpr (BWD) return launch_rec(rec_bwd_kernel<T, G, KIND, COMP, V, SPLIT>, a, smem, s);
+        else return launch_rec(rec_fwd_kernel<T, G, KIND, COMP, V, SPLIT>, a, smem, s);
+    }
+    template <typename T> bool pairs(const void *p, const View &v) const
+    {
+        return !p || rows_aligned(p, v, a.B, a.H, a.L, sizeof(T), 2 * sizeof(T));
     }
     template <typename T, typename G, int KIND, bool COMP> int operator()() const
     {
-        if constexpr (sizeof(T) == 2 && sizeof(G) == 2 && !BWD) {
-            auto pairs = [&](const void *p, const View &v) { return rows_aligned(p, v, a.B, a.H, a.L, 2, 4); };
-            if (a.d % 2 == 0 && a.d > 32 && pairs(a.x, a.vx) && pairs(a.g, a.vg) && pairs(a.out, a.vo))
-                return go<T, G, KIND, COMP, 2>();
+        const long long heads = (long long)a.B * a.H;
+        a.split = 1;
+        // forward, pairs of fp32 inputs would take twice the shared memory and leave one block an SM
+        if constexpr (BWD || sizeof(T) + sizeof(G) == 4) {
+            a.ncb = (a.d + 63) / 64;
+            if (a.d % 2 == 0 && a.d > 32 && heads * a.ncb >= sms && pairs<T>(a.x, a.vx) && pairs<G>(a.g, a.vg) &&
+                pairs<T>(a.out, a.vo) && pairs<T>(a.dout, a.vo) && pairs<T>(a.dx, a.vdx) && pairs<G>(a.dg, a.vdg))
+                return go<T, G, KIND, COMP, 2, false>();
         }
-        return go<T, G, KIND, COMP, 1>();
+        a.ncb = (a.d + 31) / 32;
+        a.split = choose_split(heads * a.ncb, (a.L + TILE - 1) / TILE, sms);
+        return a.split > 1 ? go<T, G, KIND, COMP, 1, true>() : go<T, G, KIND, COMP, 1, false>();
     }
 };
 
@@ -667,7 +953,8 @@ int la_recurrence_fwd(const void *x, const void *gate, const float *h0, const in
     a.grx = granule(x, a.vx, a, e);
     a.grg = granule(gate, a.vg, a, dtype_size(gate_dtype));
     const int sms = device_sms();
-    if (sms <= 0) return LA_ERR_CUDA;
+    a.err = err_ptr();
+    if (sms <= 0 || !a.err) return LA_ERR_CUDA;
     return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<false>{a, sms, (cudaStream_t)stream});
 }
 
@@ -703,7 +990,8 @@ int la_recurrence_bwd(const void *x, const void *gate, const float *chunk_states
     a.grg = granule(gate, a.vg, a, eg);
     a.gro = granule(dout, a.vo, a, e);
     const int sms = device_sms();
-    if (sms <= 0) return LA_ERR_CUDA;
+    a.err = err_ptr();
+    if (sms <= 0 || !a.err) return LA_ERR_CUDA;
     return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<true>{a, sms, (cudaStream_t)stream});
 }
 

@@ -455,7 +455,7 @@ enum la_gate_kind {
 };
 
 /* Rows per stored state of la_recurrence_fwd. */
-#define LA_RECURRENCE_CHUNK 128
+#define LA_RECURRENCE_CHUNK 64
 
 /*
  * la_recurrence_fwd -- gated linear recurrence, one scalar state per channel:
@@ -471,7 +471,7 @@ enum la_gate_kind {
  *                 0..L).  Rows behind are not read; out is 0 there and the state stays.
  *   h_last        device fp32 [B, H, d], the state after the last row, or NULL; may be h0
  *   chunk_states  device fp32 [B, H, ceil(L / LA_RECURRENCE_CHUNK), d] or NULL: the states
- *                 before rows 0, 128, 256, ..., which la_recurrence_bwd reads
+ *                 before rows 0, 64, 128, ..., which la_recurrence_bwd reads
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED (dtype, gate kind), LA_ERR_ARG
  * (strides) or LA_ERR_CUDA.  Asynchronous on `stream`, no workspace; the sums' order depends
  * on the sizes alone, so equal calls give equal bits.

@@ -58,43 +58,45 @@ def recurrence_grads(x, g, dout, dlast, kind, complement, h0=None, lengths=None)
 
 
 # ---- bounds of the recurrence ----------------------------------------------------------
-# A gate evaluated in fp32 is off by at most 6 u (exponential 2 u, sum 2 u, quotient 1 u, product
-# 1 u); a row multiplies by it and adds, 2 u more: every row a term passes multiplies it by
-# (1 + 8 u) at most, and the same where rows are combined in groups (a product of gates has as
-# many factors, a combination one product and one sum).  A term enters with w x: 6 u + 2 u, and
-# a group's combination adds 4 u.  So the error of h_t is at most
-#     u sum_s (8 (t - s) + 12) |w_s x_s| prod a  =  u (8 N_t + 12 M_t),
-#     M_t = a M_{t-1} + |w x|,   N_t = a (N_{t-1} + M_{t-1}).
+# A gate a, and 1 - a, evaluated in fp32 is off by at most K = (9 + 1.3 |g|) u relatively: the
+# argument g log2(e) of a power of two is rounded twice (1.3 |g| u), the power is good to 4 u, a
+# sum 1 u, a reciprocal 2 u, a product or difference 2 u (value gates: 1 u).  A row multiplies by
+# its gate and adds, 2 u more, and where rows are combined in groups a product of gates has as
+# many factors and a combination one product and one sum: every row that a term passes
+# multiplies it by (1 + K + 2 u) at most.  A term enters with w x: K + 2 u, and the groups'
+# combinations add 4 u.  So the error of h_t is at most  sum_s (sum_{s<r<=t} (K_r + 2 u) +
+# K_s + 6 u) |w_s x_s| prod a  =  N_t,  with
+#     N_t = a (N_{t-1} + (K_t + 2 u) M_{t-1}) + (K_t + 6 u) |w x|,   M_t = a M_{t-1} + |w x|.
 # Products of gates below the normal range are flushed or rounded absolutely: TINY a row.
-def _spread(a, terms, start, lengths):
-    """M and N after each row for |a|, |terms| [B, H, L, d], start [B, H, d]."""
-    B, H, L, d = terms.shape
-    M, N = np.abs(start).copy(), np.zeros((B, H, d))
-    Ms, Ns = np.zeros_like(terms), np.zeros_like(terms)
-    for t in range(L):
-        for b in range(B):
-            if lengths is None or t < lengths[b]:
-                N[b] = a[b, :, t] * (N[b] + M[b])
-                M[b] = a[b, :, t] * M[b] + terms[b, :, t]
-        Ms[:, :, t], Ns[:, :, t] = M, N
-    return Ms, Ns
+def gate_error(kind, g):
+    if kind == "value":
+        return np.full(g.shape, U)
+    return U * (9 + 1.3 * np.minimum(np.abs(g.astype(np.float64)), 200.0))
 
 
 def recurrence_bounds(x, g, kind, complement, h0=None, lengths=None):
     """Error bound of h after each row, in fp32 (no rounding to the stored type)."""
     a, w, _ = gates(kind, g, complement)
-    start = np.zeros(x.shape[:2] + x.shape[3:]) if h0 is None else h0.astype(np.float64)
-    M, N = _spread(np.abs(a), np.abs(w * x), start, lengths)
-    L = x.shape[2]
-    return U * (8 * N + 12 * M) + TINY * np.arange(1, L + 1)[:, None]
+    K, terms = gate_error(kind, g), np.abs(w * x)
+    a = np.abs(a)
+    B, H, L, d = x.shape
+    M = np.zeros((B, H, d)) if h0 is None else np.abs(h0.astype(np.float64))
+    N, out = np.zeros((B, H, d)), np.zeros_like(terms)
+    for t in range(L):
+        for b in range(B):
+            if lengths is None or t < lengths[b]:
+                N[b] = a[b, :, t] * (N[b] + (K[b, :, t] + 2 * U) * M[b]) + (K[b, :, t] + 6 * U) * terms[b, :, t]
+                M[b] = a[b, :, t] * M[b] + terms[b, :, t]
+        out[:, :, t] = N
+    return out + TINY * np.arange(1, L + 1)[:, None]
 
 
 def recurrence_grad_bounds(x, g, dout, dlast, kind, complement, h0=None, lengths=None):
     """(bound of dx, of dg, of dh0) in fp32.  e runs the same recurrence backwards, so it has the
-    same bound; dx = w e adds 6 u + 1 u; dg = e slope (before - x) adds the bounds of its factors,
-    7 u of the slope and 3 u of the operations."""
+    same bound; dx = w e adds K + 1 u; dg = e slope (before - x) adds the bounds of its factors,
+    2 K + 1 u of the slope and 3 u of the operations."""
     a, w, slope = gates(kind, g, complement)
-    a = np.abs(a)
+    K, a = gate_error(kind, g), np.abs(a)
     B, H, L, d = x.shape
     _, _, before = recurrence(x, g, kind, complement, h0, lengths)
     hb = np.zeros_like(before)
@@ -108,15 +110,16 @@ def recurrence_grad_bounds(x, g, dout, dlast, kind, complement, h0=None, lengths
         for b in range(B):
             if lengths is None or t < lengths[b]:
                 M[b] = M[b] + terms[b, :, t]
-                eb[b, :, t] = U * (8 * N[b] + 12 * M[b])
-                N[b] = a[b, :, t] * (N[b] + M[b])
+                N[b] = N[b] + 6 * U * terms[b, :, t]
+                eb[b, :, t] = N[b]
+                N[b] = a[b, :, t] * (N[b] + (K[b, :, t] + 2 * U) * M[b])
                 M[b] = a[b, :, t] * M[b]
     eb += TINY * L
     factor = before - x if complement else before
-    dxb = np.abs(w) * eb + 8 * U * np.abs(e * w)
+    dxb = np.abs(w) * eb + (K + 2 * U) * np.abs(e * w)
     dgb = np.abs(slope) * (eb * np.abs(factor) + (np.abs(e) + eb) * (hb + U * np.abs(factor)))
-    dgb += 11 * U * np.abs(e * slope * factor)
-    return dxb, dgb, U * (8 * N + 12 * M) + 8 * U * np.abs(dh0) + TINY * L
+    dgb += (2 * K + 4 * U) * np.abs(e * slope * factor)
+    return dxb, dgb, N + 2 * U * np.abs(dh0) + TINY * L
 
 
 def stored(bound, ref, dtype):

@@ -71,9 +71,10 @@ def gate_values(rng, kind, shape, resets=True):
     return g
 
 
-# (B, H, L, d): one row, seams of the 128-row chunks, odd sizes, several column blocks
+# (B, H, L, d): one row, seams of the chunks, odd sizes, several column blocks
 REC_SHAPES = [(1, 1, 1, 1), (2, 3, 5, 7), (1, 2, 127, 64), (2, 1, 128, 32), (1, 1, 129, 40), (1, 2, 300, 130),
-              (3, 2, 1000, 48), (1, 1, 2500, 64), (2, 2, 513, 256), (1, 3, 260, 33)]
+              (3, 2, 1000, 48), (1, 1, 2500, 64), (2, 2, 513, 256), (1, 3, 260, 33),
+              (1, 1, 63, 64), (1, 1, 64, 66), (1, 2, 65, 64), (40, 4, 70, 64), (90, 1, 129, 128)]
 TYPES = [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")]
 
 
@@ -107,8 +108,9 @@ def run_recurrence(la, shape, kind, complement, dtype, gate_dtype, order=None, l
     on = np.ones((B, 1, L, 1)) if clip is None else (np.arange(L) < np.array(clip)[:, None])[:, None, :, None]
     check("out", out, want, bound * on, dtype)
     check("last", last, wlast, bound[:, :, -1])
-    cb = np.concatenate([np.zeros((B, H, 1, d)), bound[:, :, 127:-1:128]], 2)[:, :, :-(-L // 128)]
-    check("chunks", chunks, before[:, :, ::128], cb)
+    n_c = la.LA_RECURRENCE_CHUNK
+    cb = np.concatenate([np.zeros((B, H, 1, d)), bound[:, :, n_c - 1:-1:n_c]], 2)[:, :, :-(-L // n_c)]
+    check("chunks", chunks, before[:, :, ::n_c], cb)
     wx, wg, w0, _ = ref.recurrence_grads(hx, hg, hd, hl, kind, complement, hh, clip)
     bx, bg, b0 = ref.recurrence_grad_bounds(hx, hg, hd, hl, kind, complement, hh, clip)
     check("dx", dx, wx, bx * on, dtype)
@@ -170,7 +172,7 @@ def test_recurrence_step(la, kind, dtype, shape):
 
 
 @pytest.mark.parametrize("kind,zero", [("value", 0.0), ("log", -np.inf), ("sigmoid", -np.inf)])
-@pytest.mark.parametrize("row", [1, 15, 16, 127, 128, 200])
+@pytest.mark.parametrize("row", [1, 7, 8, 15, 16, 63, 64, 127, 128, 200])
 def test_recurrence_gate_zero_forgets_everything(la, kind, zero, row):
     """A gate of 0 starts anew, whatever stood before it: infinities, NaN."""
     rng = np.random.default_rng(7)
