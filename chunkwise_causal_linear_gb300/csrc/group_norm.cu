@@ -1,180 +1,482 @@
 // group_norm.cu -- group norm over one head's channels of one token, with weight, bias and an
 // activation or a gate, and its gradients (sm_103a).
 //
-// One warp per group.  The weight gradients sum over all tokens: a second kernel walks the
-// rows per channel with the statistics the first one left in the workspace.
+// Bound by memory: x and gate read once, out written once.  A group is held in the registers of
+// TPG threads (8 to 32 lanes of a warp, or the block for d above 1024), so mean, centred
+// variance and the output come from one read.  A block stays with one head and walks over its
+// tokens: weight and bias stay in registers, and so do the sums of their gradients, which leave
+// the block once.  The blocks' sums are joined by a second, small kernel in a fixed order.
 #include <math.h>
 
+#include <algorithm>
+
 #include "layer.cuh"
+#include "tc_common.cuh"
 
 namespace la {
 
 namespace {
 
 constexpr int GN_THREADS = 256;
+constexpr int GN_MAX_D = 8192;
 
 struct GnArgs {
     const void *x, *gate, *dout;
     void *out, *dx, *dgate;
     const float *w, *b;
-    float *dw, *db, *stats;  // stats: mean and rstd per (b, t, h)
+    float *dw, *db, *part;  // part: [nb][2][H d], the blocks' sums for dw and db
     View vx, vg, vo, vdx, vdg;
     int B, H, L, d, center, act;
-    float eps;
+    float eps, inv_d;
+    int nb;  // blocks of a head
 };
 
-__device__ __forceinline__ float warp_sum(float v)
+// ---- VEC neighbouring channels ----------------------------------------------------------------
+template <int VEC> __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&f)[VEC])
+{
+    if constexpr (VEC == 8) {
+        const uint4 t = *(const uint4 *)p;
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = tcc::bf_lo(w[i]);
+            f[2 * i + 1] = tcc::bf_hi(w[i]);
+        }
+    } else if constexpr (VEC == 2) {
+        const uint32_t t = *(const uint32_t *)p;
+        f[0] = tcc::bf_lo(t);
+        f[1] = tcc::bf_hi(t);
+    } else {
+        f[0] = __bfloat162float(*p);
+    }
+}
+template <int VEC> __device__ __forceinline__ void load(const float *p, float (&f)[VEC])
+{
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const float4 t = ((const float4 *)p)[i];
+            f[4 * i] = t.x;
+            f[4 * i + 1] = t.y;
+            f[4 * i + 2] = t.z;
+            f[4 * i + 3] = t.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = p[i];
+    }
+}
+__device__ __forceinline__ uint32_t bf_pair(float a, float b)
+{
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&t;
+}
+template <int VEC> __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[VEC])
+{
+    if constexpr (VEC == 8)
+        *(uint4 *)p = make_uint4(bf_pair(f[0], f[1]), bf_pair(f[2], f[3]), bf_pair(f[4], f[5]), bf_pair(f[6], f[7]));
+    else if constexpr (VEC == 2)
+        *(uint32_t *)p = bf_pair(f[0], f[1]);
+    else
+        *p = __float2bfloat16_rn(f[0]);
+}
+template <int VEC> __device__ __forceinline__ void store(float *p, const float (&f)[VEC])
+{
+    if constexpr (VEC == 4) *(float4 *)p = make_float4(f[0], f[1], f[2], f[3]);
+    else *p = f[0];
+}
+
+// ---- sums over the threads of a group, the same in every one of them ---------------------------
+template <int TPG, int N> __device__ __forceinline__ void group_sum(float (&v)[N], float *sm)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = (TPG > 32 ? 32 : TPG) / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if constexpr (TPG > 32) {
+        constexpr int W = TPG / 32;
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();  // the sums before these have been read
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) sm[warp * N + i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += sm[w * N + i];
+    }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
-
-// act(z) and act'(z)
-__device__ __forceinline__ float act_of(int act, float z, float &slope)
+// 1 / (1 + e^-z), off by at most (7 + 2.5 |z|) 2^-24 relatively; 0 where e^-z leaves the range.
+__device__ __forceinline__ float sigmoid(float z)
 {
-    if (act == LA_ACT_NONE) {
-        slope = 1.f;
-        return z;
-    }
-    const float s = sigmoid(z);
-    slope = s * (1.f + z * (1.f - s));
-    return z * s;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
 }
 
-template <typename T>
-__device__ void group_stats(const GnArgs &a, const T *x, int lane, float &mean, float &rstd)
-{
-    mean = 0.f;
-    if (a.center) {
-        float s = 0.f;
-        for (int c = lane; c < a.d; c += 32) s += to_f32(x[c]);
-        mean = warp_sum(s) / a.d;
+// The tokens of a block's group of threads, r = first, first + step, ..., and where a tensor's rows
+// of them are.
+struct Walk {
+    int b, t, sb, st, L;
+    bool wrap;
+    __device__ Walk(long long first, long long step, int L_) : L(L_), wrap(false)
+    {
+        b = (int)(first / L);
+        t = (int)(first % L);
+        sb = (int)(step / L);
+        st = (int)(step % L);
     }
-    float v = 0.f;
-    for (int c = lane; c < a.d; c += 32) {
-        const float e = to_f32(x[c]) - mean;
-        v = fmaf(e, e, v);
+    __device__ __forceinline__ void next()
+    {
+        b += sb;
+        t += st;
+        wrap = t >= L;
+        if (wrap) {
+            t -= L;
+            ++b;
+        }
     }
-    rstd = rsqrtf(warp_sum(v) / a.d + a.eps);
-}
-
-// group i of B * L * H, heads fastest
-struct Place {
-    int b, h, t;
 };
-__device__ __forceinline__ Place place_of(const GnArgs &a, long long i)
-{
-    return Place{(int)(i / a.H / a.L), (int)(i % a.H), (int)(i / a.H % a.L)};
-}
+template <typename T> struct Rows {
+    T *p;
+    long long by, back;  // a step, and what a step into the next sequence adds to it
+    __device__ Rows(const void *base, const View &v, int h, const Walk &w)
+        : p((T *)base + row_of(v, w.b, h, w.t)), by(w.sb * v.b + w.st * v.l), back(v.b - w.L * v.l)
+    {
+    }
+    __device__ __forceinline__ void next(const Walk &w) { p += w.wrap ? by + back : by; }
+};
 
-template <typename T>
-__global__ void __launch_bounds__(GN_THREADS) gn_fwd_kernel(const GnArgs a)
+template <int VEC, int NV> struct Group {
+    float v[NV][VEC];
+};
+template <typename T, int VEC, int TPG, int NV>
+__device__ __forceinline__ void read(Group<VEC, NV> &g, const T *p, int lane, int d)
 {
-    const long long i = ((long long)blockIdx.x * GN_THREADS + threadIdx.x) / 32;
-    const int lane = threadIdx.x & 31;
-    if (i >= (long long)a.B * a.L * a.H) return;
-    const Place p = place_of(a, i);
-    const T *x = (const T *)a.x + row_of(a.vx, p.b, p.h, p.t);
-    const T *g = a.gate ? (const T *)a.gate + row_of(a.vg, p.b, p.h, p.t) : nullptr;
-    T *out = (T *)a.out + row_of(a.vo, p.b, p.h, p.t);
-    float mean, rstd, sl;
-    group_stats(a, x, lane, mean, rstd);
-    for (int c = lane; c < a.d; c += 32) {
-        const int wc = p.h * a.d + c;
-        const float y = (to_f32(x[c]) - mean) * rstd * (a.w ? a.w[wc] : 1.f) + (a.b ? a.b[wc] : 0.f);
-        out[c] = from_f32<T>(g ? y * act_of(a.act, to_f32(g[c]), sl) : act_of(a.act, y, sl));
-    }
-}
-
-// dy of one channel (and dgate)
-template <typename T>
-__device__ __forceinline__ float grad_y(const GnArgs &a, float xh, float w, float b, const T *g, float dout, int c,
-                                        float &dgate)
-{
-    const float y = xh * w + b;
-    float sl;
-    if (g) {
-        const float act = act_of(a.act, to_f32(g[c]), sl);
-        dgate = dout * y * sl;
-        return dout * act;
-    }
-    act_of(a.act, y, sl);
-    dgate = 0.f;
-    return dout * sl;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(GN_THREADS) gn_bwd_kernel(const GnArgs a)
-{
-    const long long i = ((long long)blockIdx.x * GN_THREADS + threadIdx.x) / 32;
-    const int lane = threadIdx.x & 31;
-    if (i >= (long long)a.B * a.L * a.H) return;
-    const Place p = place_of(a, i);
-    const T *x = (const T *)a.x + row_of(a.vx, p.b, p.h, p.t);
-    const T *g = a.gate ? (const T *)a.gate + row_of(a.vg, p.b, p.h, p.t) : nullptr;
-    const T *dout = (const T *)a.dout + row_of(a.vo, p.b, p.h, p.t);
-    T *dx = (T *)a.dx + row_of(a.vdx, p.b, p.h, p.t);
-    T *dg = a.gate ? (T *)a.dgate + row_of(a.vdg, p.b, p.h, p.t) : nullptr;
-    float mean, rstd, dgv;
-    group_stats(a, x, lane, mean, rstd);
-    float s1 = 0.f, s2 = 0.f;
-    for (int c = lane; c < a.d; c += 32) {
-        const int wc = p.h * a.d + c;
-        const float xh = (to_f32(x[c]) - mean) * rstd, w = a.w ? a.w[wc] : 1.f;
-        const float e = grad_y(a, xh, w, a.b ? a.b[wc] : 0.f, g, to_f32(dout[c]), c, dgv) * w;
-        s1 += e;
-        s2 = fmaf(e, xh, s2);
-    }
-    s1 = a.center ? warp_sum(s1) / a.d : 0.f;
-    s2 = warp_sum(s2) / a.d;
-    for (int c = lane; c < a.d; c += 32) {
-        const int wc = p.h * a.d + c;
-        const float xh = (to_f32(x[c]) - mean) * rstd, w = a.w ? a.w[wc] : 1.f;
-        const float e = grad_y(a, xh, w, a.b ? a.b[wc] : 0.f, g, to_f32(dout[c]), c, dgv) * w;
-        dx[c] = from_f32<T>(rstd * (e - s1 - xh * s2));
-        if (dg) dg[c] = from_f32<T>(dgv);
-    }
-    if (a.stats && lane == 0) {
-        a.stats[2 * i] = mean;
-        a.stats[2 * i + 1] = rstd;
-    }
-}
-
-// one block per 32 channels of a head: 8 warps walk the tokens
-template <typename T>
-__global__ void __launch_bounds__(GN_THREADS) gn_weight_kernel(const GnArgs a)
-{
-    __shared__ float sw[8][32], sb[8][32];
-    const int h = blockIdx.x, c = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x / 32;
-    const bool on = c < a.d;
-    const int wc = h * a.d + c;
-    const float w = on && a.w ? a.w[wc] : 1.f, bias = on && a.b ? a.b[wc] : 0.f;
-    float aw = 0.f, ab = 0.f, dgv;
-    if (on)
-        for (long long r = warp; r < (long long)a.B * a.L; r += 8) {
-            const int b = (int)(r / a.L), t = (int)(r % a.L);
-            const T *x = (const T *)a.x + row_of(a.vx, b, h, t);
-            const T *g = a.gate ? (const T *)a.gate + row_of(a.vg, b, h, t) : nullptr;
-            const T *dout = (const T *)a.dout + row_of(a.vo, b, h, t);
-            const float xh = (to_f32(x[c]) - a.stats[2 * (r * a.H + h)]) * a.stats[2 * (r * a.H + h) + 1];
-            const float dy = grad_y(a, xh, w, bias, g, to_f32(dout[c]), c, dgv);
-            aw = fmaf(dy, xh, aw);
-            ab += dy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPG + lane) * VEC;
+        if (c < d) {
+            load<VEC>(p + c, g.v[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g.v[i][e] = 0.f;
         }
-    sw[warp][threadIdx.x & 31] = aw;
-    sb[warp][threadIdx.x & 31] = ab;
+    }
+}
+template <typename T, int VEC, int TPG, int NV>
+__device__ __forceinline__ void write(const Group<VEC, NV> &g, T *p, int lane, int d)
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPG + lane) * VEC;
+        if (c < d) store<VEC>(p + c, g.v[i]);
+    }
+}
+
+// x -> xh in place; returns rstd.  Channels past d count as nothing.
+template <int VEC, int TPG, int NV>
+__device__ __forceinline__ float normalise(Group<VEC, NV> &x, const GnArgs &a, int lane, float *sm)
+{
+    if (a.center) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s[0] += x.v[i][e];
+        group_sum<TPG>(s, sm);
+        const float mean = s[0] * a.inv_d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * TPG + lane) * VEC < a.d)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x.v[i][e] -= mean;
+    }
+    float q[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) q[0] = fmaf(x.v[i][e], x.v[i][e], q[0]);
+    group_sum<TPG>(q, sm);
+    const float rstd = rsqrtf(fmaf(q[0], a.inv_d, a.eps));
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x.v[i][e] *= rstd;
+    return rstd;
+}
+
+// Weight and bias of the block's head: in registers where they are few, else read again.
+template <int VEC, int TPG, int NV> struct Affine {
+    static constexpr bool KEEP = NV * VEC <= 8;
+    Group<VEC, KEEP ? NV : 1> w_, b_;
+    const float *w, *b;
+    int lane, d;
+    __device__ Affine(const GnArgs &a, int h, int lane_) : lane(lane_), d(a.d)
+    {
+        w = a.w ? a.w + (size_t)h * d : nullptr;
+        b = a.b ? a.b + (size_t)h * d : nullptr;
+        if constexpr (KEEP)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) get(i, w_.v[i], b_.v[i]);
+    }
+    __device__ __forceinline__ void get(int i, float (&wv)[VEC], float (&bv)[VEC]) const
+    {
+        const int c = (i * TPG + lane) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            wv[e] = w && c + e < d ? w[c + e] : 1.f;
+            bv[e] = b && c + e < d ? b[c + e] : 0.f;
+        }
+    }
+    __device__ __forceinline__ void at(int i, float (&wv)[VEC], float (&bv)[VEC]) const
+    {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                wv[e] = w_.v[i][e];
+                bv[e] = b_.v[i][e];
+            }
+        } else {
+            get(i, wv, bv);
+        }
+    }
+};
+
+// Blocks an SM by the values a thread holds, so that enough loads are on their way.
+template <int VEC, int NV> __host__ __device__ constexpr int blocks_per_sm(bool bwd)
+{
+    return NV * VEC <= 8 ? (bwd ? 2 : 4) : NV * VEC <= 16 ? 2 : 1;
+}
+
+// What is asked for, known to the compiler: GATE and SILU.
+template <typename T, int VEC, int TPG, int NV, bool GATE, bool SILU>
+__global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(false)) gn_fwd_kernel(const GnArgs a)
+{
+    constexpr int GPB = GN_THREADS / TPG;
+    __shared__ float sm[GN_THREADS / 32];
+    const int lane = threadIdx.x % TPG, group = threadIdx.x / TPG;
+    const int h = blockIdx.x % a.H, part = blockIdx.x / a.H;
+    const long long rows = (long long)a.B * a.L, first = (long long)part * GPB, step = (long long)a.nb * GPB;
+    const Affine<VEC, TPG, NV> aff(a, h, lane);
+    Walk at(first + group, step, a.L);
+    Rows<const T> px(a.x, a.vx, h, at), pz(a.gate, a.vg, h, at);
+    Rows<T> po(a.out, a.vo, h, at);
+    // every group of a warp (of the block, where the block is one) takes part in every turn's sums
+    const int turns = (int)((rows - first + step - 1) / step);
+    for (int k = 0; k < turns; ++k) {
+        Group<VEC, NV> x = {}, z = {};
+        const bool on = at.b < a.B;
+        if (on) {
+            read<T, VEC, TPG, NV>(x, px.p, lane, a.d);
+            if (GATE) read<T, VEC, TPG, NV>(z, pz.p, lane, a.d);
+        }
+        normalise<VEC, TPG, NV>(x, a, lane, sm);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[VEC], b[VEC];
+            aff.at(i, w, b);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float y = fmaf(x.v[i][e], w[e], b[e]), g = GATE ? z.v[i][e] : y;
+                const float f = SILU ? g * sigmoid(g) : g;
+                x.v[i][e] = GATE ? y * f : f;
+            }
+        }
+        if (on) write<T, VEC, TPG, NV>(x, po.p, lane, a.d);
+        at.next();
+        px.next(at);
+        if (GATE) pz.next(at);
+        po.next(at);
+    }
+}
+
+template <typename T, int VEC, int TPG, int NV, bool GATE, bool SILU>
+__global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(true)) gn_bwd_kernel(const GnArgs a)
+{
+    constexpr int GPB = GN_THREADS / TPG;
+    __shared__ float sm[2 * GN_THREADS / 32];
+    const int lane = threadIdx.x % TPG, group = threadIdx.x / TPG;
+    const int h = blockIdx.x % a.H, part = blockIdx.x / a.H;
+    const long long rows = (long long)a.B * a.L, first = (long long)part * GPB, step = (long long)a.nb * GPB;
+    const Affine<VEC, TPG, NV> aff(a, h, lane);
+    Group<VEC, NV> dw = {}, db = {};
+    Walk at(first + group, step, a.L);
+    Rows<const T> px(a.x, a.vx, h, at), pz(a.gate, a.vg, h, at), pd(a.dout, a.vo, h, at);
+    Rows<T> pdx(a.dx, a.vdx, h, at), pdz(a.dgate, a.vdg, h, at);
+    const int turns = (int)((rows - first + step - 1) / step);
+    for (int k = 0; k < turns; ++k) {
+        Group<VEC, NV> x = {}, z = {}, o = {};
+        const bool on = at.b < a.B;
+        if (on) {
+            read<T, VEC, TPG, NV>(x, px.p, lane, a.d);
+            read<T, VEC, TPG, NV>(o, pd.p, lane, a.d);
+            if (GATE) read<T, VEC, TPG, NV>(z, pz.p, lane, a.d);
+        }
+        const float rstd = normalise<VEC, TPG, NV>(x, a, lane, sm);
+        float s[2] = {0.f, 0.f};  // sums of dy w and of dy w xh
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[VEC], b[VEC];
+            aff.at(i, w, b);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float xh = x.v[i][e], y = fmaf(xh, w[e], b[e]), g = GATE ? z.v[i][e] : y;
+                float f = g, slope = 1.f;
+                if (SILU) {
+                    const float sg = sigmoid(g);
+                    f = g * sg;
+                    slope = fmaf(f, 1.f - sg, sg);  // sg (1 + g (1 - sg))
+                }
+                float dy = o.v[i][e];
+                if (GATE) {
+                    z.v[i][e] = dy * y * slope;  // dgate
+                    dy *= f;
+                } else {
+                    dy *= slope;
+                }
+                dw.v[i][e] = fmaf(dy, xh, dw.v[i][e]);
+                db.v[i][e] += dy;
+                dy *= w[e];
+                o.v[i][e] = dy;
+                s[0] += dy;
+                s[1] = fmaf(dy, xh, s[1]);
+            }
+        }
+        group_sum<TPG>(s, sm);
+        const float m1 = a.center ? s[0] * a.inv_d : 0.f, m2 = s[1] * a.inv_d;
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x.v[i][e] = rstd * (o.v[i][e] - m1 - x.v[i][e] * m2);
+            write<T, VEC, TPG, NV>(x, pdx.p, lane, a.d);
+            if (GATE) write<T, VEC, TPG, NV>(z, pdz.p, lane, a.d);
+        }
+        at.next();
+        px.next(at);
+        pd.next(at);
+        if (GATE) pz.next(at);
+        pdx.next(at);
+        if (GATE) pdz.next(at);
+    }
+    if (!a.part) return;
+    // the groups of the block joined, one after the other
+    extern __shared__ float sums[];  // [2][GPB][d]
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPG + lane) * VEC;
+        if (c < a.d)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                sums[group * a.d + c + e] = dw.v[i][e];
+                sums[(GPB + group) * a.d + c + e] = db.v[i][e];
+            }
+    }
     __syncthreads();
-    if (warp == 0 && on) {
-        for (int i = 1; i < 8; ++i) {
-            aw += sw[i][threadIdx.x];
-            ab += sb[i][threadIdx.x];
-        }
-        if (a.dw) a.dw[wc] = aw;
-        if (a.db) a.db[wc] = ab;
+    float *out = a.part + (size_t)part * 2 * a.H * a.d + (size_t)h * a.d;
+    for (int c = threadIdx.x; c < 2 * a.d; c += GN_THREADS) {
+        const int which = c >= a.d, cc = which ? c - a.d : c;
+        const float *p = sums + (size_t)which * GPB * a.d + cc;
+        float v = 0.f;
+        for (int g = 0; g < GPB; ++g) v += p[g * a.d];
+        out[(size_t)which * a.H * a.d + cc] = v;
     }
+}
+
+// dweight, dbias: the blocks' sums of 32 channels joined by 8 warps
+__global__ void __launch_bounds__(GN_THREADS) gn_join_kernel(const GnArgs a)
+{
+    __shared__ float sm[2][8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long n = (long long)a.H * a.d, c = (long long)blockIdx.x * 32 + lane;
+    tcc::pdl_wait();  // the blocks' sums are there
+    float w = 0.f, b = 0.f;
+    if (c < n)
+        for (int p = warp; p < a.nb; p += 8) {
+            w += a.part[(size_t)p * 2 * n + c];
+            b += a.part[(size_t)p * 2 * n + n + c];
+        }
+    sm[0][warp][lane] = w;
+    sm[1][warp][lane] = b;
+    __syncthreads();
+    if (warp < 2 && c < n) {
+        float v = 0.f;
+        for (int i = 0; i < 8; ++i) v += sm[warp][i][lane];
+        float *out = warp ? a.db : a.dw;
+        if (out) out[c] = v;
+    }
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+// Blocks of a head: about 8 (4 for the gradients) an SM in all, none without a token.
+int blocks_of_head(int B, int H, int L, int d, int sms, bool bwd)
+{
+    const long long rows = (long long)B * L, gpb = d > 1024 ? 1 : d > 256 ? 8 : 16;
+    const long long want = std::max(1ll, (long long)sms * (bwd ? 4 : 8) / H);
+    return (int)std::max(1ll, std::min(want, (rows + gpb - 1) / gpb));
+}
+
+template <typename T, int VEC, int TPG, int NV, bool BWD> int launch_gn(const GnArgs &a, cudaStream_t s)
+{
+    const long long blocks = (long long)a.nb * a.H;
+    if (blocks > INT_MAX) return LA_ERR_SHAPE;
+    const size_t smem = BWD && a.part ? sizeof(float) * 2 * (GN_THREADS / TPG) * a.d : 0;
+    auto go = [&](auto kern) {
+        if (smem > 48 * 1024 &&
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return (int)LA_ERR_CUDA;
+        kern<<<(unsigned)blocks, GN_THREADS, smem, s>>>(a);
+        return cudaPeekAtLastError() == cudaSuccess ? (int)LA_OK : (int)LA_ERR_CUDA;
+    };
+    const bool silu = a.act == LA_ACT_SILU;
+    if constexpr (BWD)
+        return a.gate ? silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, true, true>) : go(gn_bwd_kernel<T, VEC, TPG, NV, true, false>)
+                      : silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, false, true>) : go(gn_bwd_kernel<T, VEC, TPG, NV, false, false>);
+    else
+        return a.gate ? silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, true, true>) : go(gn_fwd_kernel<T, VEC, TPG, NV, true, false>)
+                      : silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, false, true>) : go(gn_fwd_kernel<T, VEC, TPG, NV, false, false>);
+}
+
+// Threads and vectors of a group by its number of vectors: the fewest registers that hold it, a
+// block once a warp would need more than 32 values a lane.
+template <typename T, int VEC, bool BWD> int by_size(const GnArgs &a, cudaStream_t s)
+{
+    const int nv = (a.d + VEC - 1) / VEC;
+    if constexpr (VEC >= 4) {
+        if (nv <= 8) return launch_gn<T, VEC, 8, 1, BWD>(a, s);
+        if (nv <= 16) return launch_gn<T, VEC, 16, 1, BWD>(a, s);
+    }
+    if (nv <= 32) return launch_gn<T, VEC, 32, 1, BWD>(a, s);
+    if (nv <= 64) return launch_gn<T, VEC, 32, 2, BWD>(a, s);
+    if (nv <= 128) return launch_gn<T, VEC, 32, 4, BWD>(a, s);
+    if constexpr (VEC <= 4)
+        if (nv <= 256) return launch_gn<T, VEC, 32, 8, BWD>(a, s);
+    if constexpr (VEC == 8) {
+        if (nv <= 256) return launch_gn<T, VEC, 256, 1, BWD>(a, s);
+        return launch_gn<T, VEC, 256, 4, BWD>(a, s);
+    } else {
+        if (nv <= 256 * 4 / VEC) return launch_gn<T, VEC, 256, (4 / VEC > 1 ? 4 / VEC : 1), BWD>(a, s);
+        return launch_gn<T, VEC, 256, 32 / VEC, BWD>(a, s);
+    }
+}
+
+template <bool BWD> int by_type(const GnArgs &a, int dtype, cudaStream_t s)
+{
+    const size_t e = dtype_size(dtype);
+    auto fits = [&](int vec) {
+        auto ok = [&](const void *p, const View &v) { return !p || rows_aligned(p, v, a.B, a.H, a.L, e, vec * e); };
+        return a.d % vec == 0 && ok(a.x, a.vx) && ok(a.gate, a.vg) && ok(a.out, a.vo) && ok(a.dout, a.vo) &&
+               ok(a.dx, a.vdx) && ok(a.dgate, a.vdg);
+    };
+    if (dtype == LA_F32) return fits(4) ? by_size<float, 4, BWD>(a, s) : by_size<float, 1, BWD>(a, s);
+    if (fits(8)) return by_size<__nv_bfloat16, 8, BWD>(a, s);
+    return fits(2) ? by_size<__nv_bfloat16, 2, BWD>(a, s) : by_size<__nv_bfloat16, 1, BWD>(a, s);
 }
 
 int check_act(int activation, float eps, int dtype)
@@ -199,6 +501,7 @@ int la_group_norm_fwd(const void *x, const float *weight, const float *bias, con
 {
     if (!x || !out) return LA_ERR_NULL;
     if (!sizes_ok(B, H, L, d)) return LA_ERR_SHAPE;
+    if (d > GN_MAX_D) return LA_ERR_UNSUPPORTED;
     const int rc = check_act(activation, eps, dtype);
     if (rc != LA_OK) return rc;
     GnArgs a = {};
@@ -213,19 +516,18 @@ int la_group_norm_fwd(const void *x, const float *weight, const float *bias, con
     const size_t e = dtype_size(dtype);
     if (!aligned(x, e) || !aligned(gate, e) || !aligned(out, e) || !aligned(weight, 4) || !aligned(bias, 4))
         return LA_ERR_ARG;
-    const long long blocks = ((long long)B * L * H + GN_THREADS / 32 - 1) / (GN_THREADS / 32);
-    if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    if (dtype == LA_BF16)
-        gn_fwd_kernel<__nv_bfloat16><<<(unsigned)blocks, GN_THREADS, 0, (cudaStream_t)stream>>>(a);
-    else
-        gn_fwd_kernel<float><<<(unsigned)blocks, GN_THREADS, 0, (cudaStream_t)stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    const int sms = device_sms();
+    if (sms <= 0) return LA_ERR_CUDA;
+    a.inv_d = 1.f / (float)d;
+    a.nb = blocks_of_head(B, H, L, d, sms, false);
+    return by_type<false>(a, dtype, (cudaStream_t)stream);
 }
 
 size_t la_group_norm_bwd_workspace_bytes(int B, int H, int L, int d)
 {
-    if (!sizes_ok(B, H, L, d)) return 0;
-    return (size_t)B * H * L * 2 * sizeof(float);
+    if (!sizes_ok(B, H, L, d) || d > GN_MAX_D) return 0;
+    const int sms = device_sms();
+    return sizeof(float) * 2 * (size_t)blocks_of_head(B, H, L, d, sms > 0 ? sms : 152, true) * H * d;
 }
 
 int la_group_norm_bwd(const void *x, const float *weight, const float *bias, const void *gate,
@@ -238,6 +540,7 @@ int la_group_norm_bwd(const void *x, const float *weight, const float *bias, con
 {
     if (!x || !dout || !dx || (gate == nullptr) != (dgate == nullptr)) return LA_ERR_NULL;
     if (!sizes_ok(B, H, L, d)) return LA_ERR_SHAPE;
+    if (d > GN_MAX_D) return LA_ERR_UNSUPPORTED;
     const int rc = check_act(activation, eps, dtype);
     if (rc != LA_OK) return rc;
     GnArgs a = {};
@@ -260,25 +563,18 @@ int la_group_norm_bwd(const void *x, const float *weight, const float *bias, con
     if (dweight || dbias) {
         if (!workspace || workspace_bytes < la_group_norm_bwd_workspace_bytes(B, H, L, d)) return LA_ERR_WORKSPACE;
         if (!aligned(workspace, 4)) return LA_ERR_ARG;
-        a.stats = (float *)workspace;
+        a.part = (float *)workspace;
     }
-    const long long blocks = ((long long)B * L * H + GN_THREADS / 32 - 1) / (GN_THREADS / 32);
-    if (blocks > INT_MAX) return LA_ERR_SHAPE;
+    const int sms = device_sms();
+    if (sms <= 0) return LA_ERR_CUDA;
+    a.inv_d = 1.f / (float)d;
+    a.nb = blocks_of_head(B, H, L, d, sms, true);
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == LA_BF16)
-        gn_bwd_kernel<__nv_bfloat16><<<(unsigned)blocks, GN_THREADS, 0, s>>>(a);
-    else
-        gn_bwd_kernel<float><<<(unsigned)blocks, GN_THREADS, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
-    if (a.stats) {
-        const dim3 grid((unsigned)H, (unsigned)((d + 31) / 32));
-        if (dtype == LA_BF16)
-            gn_weight_kernel<__nv_bfloat16><<<grid, GN_THREADS, 0, s>>>(a);
-        else
-            gn_weight_kernel<float><<<grid, GN_THREADS, 0, s>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return LA_ERR_CUDA;
-    }
-    return LA_OK;
+    const int rc2 = by_type<true>(a, dtype, s);
+    if (rc2 != LA_OK || !a.part) return rc2;
+    const long long join = ((long long)H * d + 31) / 32;
+    if (join > INT_MAX) return LA_ERR_SHAPE;
+    return tcc::launch_dependent(gn_join_kernel, (int)join, GN_THREADS, 0, s, a) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 }  // extern "C"

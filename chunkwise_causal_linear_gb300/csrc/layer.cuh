@@ -29,13 +29,13 @@ inline View make_view(const la_strides *s, int H, int L, int d, bool head_major 
     return View{(long long)H * L * d, d, (long long)H * d};
 }
 
-// Sizes every one of these operators takes: positive, below 2^31 heads in all and 2^20 channels
+// Sizes every one of these operators takes: positive, below 2^30 heads in all and 2^20 channels
 // (grid limits), and element counts that 64-bit offsets hold with room to spare.
 inline bool sizes_ok(int B, int H, int L, int d)
 {
     if (B <= 0 || H <= 0 || L <= 0 || d <= 0 || d > (1 << 20)) return false;
     if (L > INT_MAX - (1 << 16)) return false;  // row numbers of a last, partial tile stay ints
-    return (double)B * H * L * d < 4.6e18 && (double)B * H < (double)INT_MAX;
+    return (double)B * H * L * d < 4.6e18 && (double)B * H < (double)(INT_MAX / 2);
 }
 
 inline size_t dtype_size(int dtype) { return dtype == LA_F32 ? 4 : 2; }

@@ -4,7 +4,13 @@
 // A frequency is kept as a 64-bit fraction of a full turn per position, so the angle of
 // position p is p * turns modulo 2^64: one integer product, exact however far p is.  An fp32
 // product p * theta would be off by a radian at p ~ 2^24.
+//
+// Bound by memory: every element is read and written once.  A thread holds the sines and cosines
+// of VEC pairs (16-byte vectors) of one token and goes over up to 8 heads with them; the first
+// heads' loads are on the way while the sines (~45 instructions a pair) are computed.
 #include <math.h>
+
+#include <algorithm>
 
 #include "layer.cuh"
 
@@ -13,6 +19,8 @@ namespace la {
 namespace {
 
 constexpr int ROT_THREADS = 256;
+constexpr int ROT_AT_ONCE = 2;  // heads whose loads are on the way together
+constexpr int ROT_HEADS = 8;    // heads of a thread at most
 
 struct RotArgs {
     const void *q, *k;
@@ -24,6 +32,7 @@ struct RotArgs {
     int B, H, Hk, L, d, rot;
     int layout, inverse;
     float amp;
+    int heads, qgroups;  // heads of a thread, groups of them in q
 };
 
 // Sine and cosine of 2 pi f / 2^64.  The nearest quarter turn is taken off in integers; what is
@@ -40,37 +49,128 @@ __device__ __forceinline__ void turn_sincos(unsigned long long f, float &s, floa
     if ((q + 1) & 2) c = -c;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(ROT_THREADS) rotary_kernel(const RotArgs a)
+// VEC neighbouring elements as they are stored
+template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Vec {
+    T v[VEC];
+};
+
+// Unit u of a token: VEC pairs of the rotated channels, or two vectors of the copied ones.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
 {
-    const int units = a.rot / 2 + (a.d - a.rot);
-    const long long n = (long long)a.B * a.L * units;
-    const long long i = (long long)blockIdx.x * ROT_THREADS + threadIdx.x;
+    using V = Vec<T, VEC>;
+    const int pair_units = a.rot / (2 * VEC), units = pair_units + (a.d - a.rot + 2 * VEC - 1) / (2 * VEC);
+    const unsigned long long n = (unsigned long long)a.B * a.L * units;
+    const unsigned long long i = (unsigned long long)blockIdx.x * ROT_THREADS + threadIdx.x;
     if (i >= n) return;
-    const int u = (int)(i % units), t = (int)(i / units % a.L), b = (int)(i / units / a.L);
-    float s = 0.f, c = 0.f;
-    const bool pair = u < a.rot / 2;
-    if (pair) {
-        const long long p = a.pos ? (long long)a.pos[(size_t)b * a.L + t] : a.offset + t;
-        turn_sincos((unsigned long long)p * a.turns[u], s, c);
-        s *= a.inverse ? -a.amp : a.amp;
-        c *= a.amp;
+    int u, t, b;
+    if (n >> 32) {
+        u = (int)(i % units);
+        t = (int)(i / units % a.L);
+        b = (int)(i / units / a.L);
+    } else {
+        const unsigned row = (unsigned)i / (unsigned)units;
+        u = (int)((unsigned)i - row * units);
+        b = (int)(row / (unsigned)a.L);
+        t = (int)(row - (unsigned)b * a.L);
     }
-    const int c0 = pair ? (a.layout == LA_ROTARY_HALF ? u : 2 * u) : a.rot / 2 + u;
-    const int c1 = a.layout == LA_ROTARY_HALF ? u + a.rot / 2 : 2 * u + 1;
-    for (int h = 0; h < a.H + a.Hk; ++h) {
-        const bool isq = h < a.H;
-        const int hd = isq ? h : h - a.H;
-        const T *in = isq ? (const T *)a.q + row_of(a.vq, b, hd, t) : (const T *)a.k + row_of(a.vk, b, hd, t);
-        T *out = isq ? (T *)a.qo + row_of(a.vqo, b, hd, t) : (T *)a.ko + row_of(a.vko, b, hd, t);
-        if (pair) {
-            const float x = to_f32(in[c0]), y = to_f32(in[c1]);
-            out[c0] = from_f32<T>(x * c - y * s);
-            out[c1] = from_f32<T>(x * s + y * c);
-        } else {
-            out[c0] = in[c0];
+    const bool isq = (int)blockIdx.y < a.qgroups, pair = u < pair_units;
+    const int h0 = (isq ? blockIdx.y : blockIdx.y - a.qgroups) * a.heads, h1 = min(h0 + a.heads, isq ? a.H : a.Hk);
+    const View &vi = isq ? a.vq : a.vk, &vo = isq ? a.vqo : a.vko;
+    const T *in = (const T *)(isq ? a.q : a.k) + row_of(vi, b, h0, t);
+    T *out = (T *)(isq ? a.qo : a.ko) + row_of(vo, b, h0, t);
+    const bool half = a.layout == LA_ROTARY_HALF;
+    int c0, c1;  // the unit's two vectors
+    bool two = true;
+    if (pair) {
+        c0 = half ? u * VEC : 2 * u * VEC;
+        c1 = half ? c0 + a.rot / 2 : c0 + VEC;
+    } else {
+        c0 = a.rot + 2 * (u - pair_units) * VEC;
+        c1 = c0 + VEC;
+        two = c1 < a.d;
+        if (!two) c1 = c0;
+    }
+    V x[ROT_AT_ONCE], y[ROT_AT_ONCE];
+    auto fetch = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < ROT_AT_ONCE; ++j)
+            if (h + j < h1) {
+                x[j] = *(const V *)(in + j * vi.h + c0);
+                y[j] = *(const V *)(in + j * vi.h + c1);
+            }
+        in += ROT_AT_ONCE * vi.h;
+    };
+    fetch(h0);
+    float s[VEC], c[VEC];
+    if (pair) {
+        const unsigned long long p = (unsigned long long)(a.pos ? (long long)a.pos[(size_t)b * a.L + t] : a.offset + t);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            turn_sincos(p * a.turns[u * VEC + e], s[e], c[e]);
+            s[e] *= a.inverse ? -a.amp : a.amp;
+            c[e] *= a.amp;
         }
     }
+    for (int h = h0; h < h1; h += ROT_AT_ONCE) {
+        if (h != h0) fetch(h);
+#pragma unroll
+        for (int j = 0; j < ROT_AT_ONCE; ++j)
+            if (h + j < h1) {
+                if (pair && half) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        const float p = to_f32(x[j].v[e]), q = to_f32(y[j].v[e]);
+                        x[j].v[e] = from_f32<T>(p * c[e] - q * s[e]);
+                        y[j].v[e] = from_f32<T>(p * s[e] + q * c[e]);
+                    }
+                } else if (pair) {
+                    // elements 2e, 2e + 1 of x then y
+                    auto turn = [&](T &m, T &n, int e) {
+                        const float p = to_f32(m), q = to_f32(n);
+                        m = from_f32<T>(p * c[e] - q * s[e]);
+                        n = from_f32<T>(p * s[e] + q * c[e]);
+                    };
+                    if constexpr (VEC == 1) {
+                        turn(x[j].v[0], y[j].v[0], 0);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VEC / 2; ++e) {
+                            turn(x[j].v[2 * e], x[j].v[2 * e + 1], e);
+                            turn(y[j].v[2 * e], y[j].v[2 * e + 1], VEC / 2 + e);
+                        }
+                    }
+                }
+                *(V *)(out + j * vo.h + c0) = x[j];
+                if (two) *(V *)(out + j * vo.h + c1) = y[j];
+            }
+        out += ROT_AT_ONCE * vo.h;
+    }
+}
+
+template <typename T, int VEC> int launch_rotary(RotArgs &a, int sms, cudaStream_t s)
+{
+    const int units = a.rot / (2 * VEC) + (a.d - a.rot + 2 * VEC - 1) / (2 * VEC);
+    const long long blocks = ((long long)a.B * a.L * units + ROT_THREADS - 1) / ROT_THREADS;
+    if (blocks > INT_MAX) return LA_ERR_SHAPE;
+    // heads of a thread: as many as still leave every SM eight blocks
+    a.heads = ROT_HEADS;
+    auto groups = [&](int n) { return (n + a.heads - 1) / a.heads; };
+    while (a.heads > 1 && blocks * (groups(a.H) + groups(a.Hk)) < 8ll * sms) a.heads /= 2;
+    while ((long long)groups(a.H) + groups(a.Hk) > 65535) a.heads *= 2;  // limit of the grid
+    a.qgroups = groups(a.H);
+    const int ny = a.qgroups + groups(a.Hk);
+    rotary_kernel<T, VEC><<<dim3((unsigned)blocks, (unsigned)ny), ROT_THREADS, 0, s>>>(a);
+    return cudaPeekAtLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+}
+
+template <typename T, int VEC> bool whole_vectors(const RotArgs &a)
+{
+    auto ok = [&](const void *p, const View &v, int H) {
+        return !p || rows_aligned(p, v, a.B, H, a.L, sizeof(T), sizeof(T) * VEC);
+    };
+    return a.rot % (2 * VEC) == 0 && a.d % VEC == 0 && ok(a.q, a.vq, a.H) && ok(a.qo, a.vqo, a.H) &&
+           ok(a.k, a.vk, a.Hk) && ok(a.ko, a.vko, a.Hk);
 }
 
 }  // namespace
@@ -145,13 +245,14 @@ int la_rotary(const void *q, const void *k, void *q_out, void *k_out,
     if (!aligned(q, e) || !aligned(k, e) || !aligned(q_out, e) || !aligned(k_out, e) || !aligned(turns, 8) ||
         !aligned(positions, 4))
         return LA_ERR_ARG;
-    const long long n = (long long)B * L * (rot / 2 + (d - rot)), blocks = (n + ROT_THREADS - 1) / ROT_THREADS;
-    if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    if (dtype == LA_BF16)
-        rotary_kernel<__nv_bfloat16><<<(unsigned)blocks, ROT_THREADS, 0, (cudaStream_t)stream>>>(a);
-    else
-        rotary_kernel<float><<<(unsigned)blocks, ROT_THREADS, 0, (cudaStream_t)stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    const int sms = device_sms();
+    if (sms <= 0) return LA_ERR_CUDA;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (dtype == LA_F32)
+        return whole_vectors<float, 4>(a) ? launch_rotary<float, 4>(a, sms, s) : launch_rotary<float, 1>(a, sms, s);
+    if (whole_vectors<__nv_bfloat16, 8>(a)) return launch_rotary<__nv_bfloat16, 8>(a, sms, s);
+    return whole_vectors<__nv_bfloat16, 4>(a) ? launch_rotary<__nv_bfloat16, 4>(a, sms, s)
+                                              : launch_rotary<__nv_bfloat16, 1>(a, sms, s);
 }
 
 }  // extern "C"

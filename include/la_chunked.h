@@ -573,6 +573,7 @@ enum la_activation {
  *   gate, out     dtype `dtype`; their NULL strides mean contiguous [B, L, H, d], channels
  *                 last (gate itself may be NULL)
  *   eps           > 0 and finite, else LA_ERR_ARG
+ *   d             at most 8192, else LA_ERR_UNSUPPORTED
  * Statistics are fp32 over values held in fp32, the variance from centred values.
  */
 int la_group_norm_fwd(const void *x, const float *weight, const float *bias, const void *gate,

@@ -174,8 +174,11 @@ def group_norm(x, w, b, gate, eps, act, center, dout=None):
 
     With c = (d + 8) u the relative bound of a sum of d values: the mean is off by c mean|x|,
     a centred value by that and 1 u, which rstd scales: dxh = rstd (c mean|x| + 2 u |xc|); rstd
-    by half the variance's relative error, 2 max|dxc| / std + c + 8 u.  The activation is off by
-    8 u |z| plus its slope (at most 1.1) times the error of z."""
+    by half the variance's relative error, mean(dxc |xc|) / var + c + 8 u.  With k = (8 + 2.5 |z|)
+    u the sigmoid s is off by at most k s (its argument is scaled and rounded, 2.4 |z| u, the
+    power 4 u, the sum 1 u, the quotient 2 u), so z s by k |z s| + 1 u and the slope s + z s (1 - s)
+    by k (s + 2 |z s|) + 4 u (s + |z s|); the error of z comes in by slopes of at most 1.1 and
+    0.5."""
     x = np.swapaxes(x.astype(np.float64), 1, 2)
     d = x.shape[-1]
     c = (d + 8) * U
@@ -195,8 +198,9 @@ def group_norm(x, w, b, gate, eps, act, center, dout=None):
     if act == "silu":
         sg = _sigmoid(z)
         f, slope = z * sg, sg * (1 + z * (1 - sg))
-        f_b = 1.1 * z_b + 8 * U * np.abs(f)
-        slope_b = 0.5 * z_b + 8 * U * (1 + np.abs(z)) * sg
+        k = U * (8 + 2.5 * np.minimum(np.abs(z), 200.0))
+        f_b = 1.1 * z_b + (k + U) * np.abs(f)
+        slope_b = 0.5 * z_b + k * (sg + 2 * np.abs(f)) + 4 * U * (sg + np.abs(f))
     else:
         f, slope, f_b, slope_b = z, np.ones_like(z), z_b, np.zeros_like(z)
     out = f if gate is None else y * f
