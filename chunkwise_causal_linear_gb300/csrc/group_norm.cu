@@ -3,12 +3,13 @@
 //
 // Bound by memory: x and gate read once, out written once.  A group is held in the registers of
 // TPG threads (8 to 32 lanes of a warp, or the block for d above 1024), so mean, centred
-// variance and the output come from one read.  A block stays with one head and walks over its
+// variance and the output come from one read, which is on its way some rows ahead.  A block stays with one head and walks over its
 // tokens: weight and bias stay in registers, and so do the sums of their gradients, which leave
 // the block once.  The blocks' sums are joined by a second, small kernel in a fixed order.
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "layer.cuh"
 #include "tc_common.cuh"
@@ -156,20 +157,6 @@ template <int VEC, int NV> struct Group {
     float v[NV][VEC];
 };
 template <typename T, int VEC, int TPG, int NV>
-__device__ __forceinline__ void read(Group<VEC, NV> &g, const T *p, int lane, int d)
-{
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPG + lane) * VEC;
-        if (c < d) {
-            load<VEC>(p + c, g.v[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) g.v[i][e] = 0.f;
-        }
-    }
-}
-template <typename T, int VEC, int TPG, int NV>
 __device__ __forceinline__ void write(const Group<VEC, NV> &g, T *p, int lane, int d)
 {
 #pragma unroll
@@ -178,6 +165,123 @@ __device__ __forceinline__ void write(const Group<VEC, NV> &g, T *p, int lane, i
         if (c < d) store<VEC>(p + c, g.v[i]);
     }
 }
+
+// ---- the rows on their way ------------------------------------------------------------------------
+// Each thread copies its own vectors of the next rows into its own places in shared memory, so
+// nothing is synchronised and no register waits for memory.  Single bf16 values, which cp.async
+// does not copy, are loaded when they are needed.
+template <typename T, int VEC, int TPG, int NV, int ARRAYS, int BLOCKS> struct Ring {
+    static constexpr int BYTES = VEC * (int)sizeof(T);  // of a vector
+    static constexpr bool USED = BYTES >= 4;
+    static constexpr int STAGE = ARRAYS * NV * BYTES * GN_THREADS;
+    static constexpr int FIT = (160 * 1024) / (BLOCKS * STAGE);
+    static constexpr int ST = !USED ? 1 : FIT > 6 ? 6 : FIT < 2 ? 2 : FIT;
+    static constexpr int SMEM = USED ? ST * STAGE : 0;
+    unsigned char *sm;
+    int in = 0, at = 0;
+
+    __device__ Ring(unsigned char *mem) : sm(mem + threadIdx.x * BYTES) {}
+    __device__ __forceinline__ void copy(int array, const T *p, int lane, int d) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPG + lane) * VEC;
+            const uint32_t to =
+                (uint32_t)__cvta_generic_to_shared(sm + in * STAGE + (array * NV + i) * BYTES * GN_THREADS);
+            if (c < d) {
+                if constexpr (BYTES == 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + c) : "memory");
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(p + c) : "memory");
+            }
+        }
+    }
+    __device__ __forceinline__ void commit()
+    {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in = in + 1 == ST ? 0 : in + 1;
+    }
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2 < 0 ? 0 : ST - 2) : "memory"); }
+    __device__ __forceinline__ void take(int array, Group<VEC, NV> &g, int lane, int d, bool on) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const T *p = (const T *)(sm + at * STAGE + (array * NV + i) * BYTES * GN_THREADS);
+            if (on && (i * TPG + lane) * VEC < d) {
+                load<VEC>(p, g.v[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) g.v[i][e] = 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ void done() { at = at + 1 == ST ? 0 : at + 1; }
+};
+template <typename T, int VEC, int TPG, int NV>
+__device__ __forceinline__ void read(Group<VEC, NV> &g, const T *p, int lane, int d, bool on)
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPG + lane) * VEC;
+        if (on && c < d) {
+            load<VEC>(p + c, g.v[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) g.v[i][e] = 0.f;
+        }
+    }
+}
+
+// The inputs of a block's rows, one after the other.
+template <typename T, int VEC, int TPG, int NV, int ARRAYS, int BLOCKS> struct Source {
+    using R = Ring<T, VEC, TPG, NV, ARRAYS, BLOCKS>;
+    R ring;
+    Walk at;
+    Rows<const T> p0, p1, p2;
+    int lane, d, B;
+
+    __device__ Source(unsigned char *mem, const Walk &w, const Rows<const T> &a0, const Rows<const T> &a1,
+                      const Rows<const T> &a2, int lane_, const GnArgs &a)
+        : ring(mem), at(w), p0(a0), p1(a1), p2(a2), lane(lane_), d(a.d), B(a.B)
+    {
+        if constexpr (R::USED)
+#pragma unroll
+            for (int i = 0; i < R::ST - 1; ++i) fetch();
+    }
+    __device__ __forceinline__ void step()
+    {
+        at.next();
+        p0.next(at);
+        if (ARRAYS > 1) p1.next(at);
+        if (ARRAYS > 2) p2.next(at);
+    }
+    __device__ __forceinline__ void fetch()
+    {
+        if (at.b < B) {
+            ring.copy(0, p0.p, lane, d);
+            if (ARRAYS > 1) ring.copy(1, p1.p, lane, d);
+            if (ARRAYS > 2) ring.copy(2, p2.p, lane, d);
+        }
+        ring.commit();
+        step();
+    }
+    // the next row of each input, zeros where there is none
+    __device__ __forceinline__ void next(Group<VEC, NV> *g, bool on)
+    {
+        if constexpr (R::USED) {
+            ring.wait();
+#pragma unroll
+            for (int i = 0; i < ARRAYS; ++i) ring.take(i, g[i], lane, d, on);
+            ring.done();
+            fetch();
+        } else {
+            read<T, VEC, TPG, NV>(g[0], p0.p, lane, d, on);
+            if (ARRAYS > 1) read<T, VEC, TPG, NV>(g[1], p1.p, lane, d, on);
+            if (ARRAYS > 2) read<T, VEC, TPG, NV>(g[2], p2.p, lane, d, on);
+            step();
+        }
+    }
+};
 
 // x -> xh in place; returns rstd.  Channels past d count as nothing.
 template <int VEC, int TPG, int NV>
@@ -248,34 +352,35 @@ template <int VEC, int TPG, int NV> struct Affine {
     }
 };
 
-// Blocks an SM by the values a thread holds, so that enough loads are on their way.
+// Blocks an SM by the values a thread holds.
 template <int VEC, int NV> __host__ __device__ constexpr int blocks_per_sm(bool bwd)
 {
-    return NV * VEC <= 8 ? (bwd ? 2 : 4) : NV * VEC <= 16 ? 2 : 1;
+    return NV * VEC <= 8 ? (bwd ? 2 : 3) : NV * VEC <= 16 ? 2 : 1;
 }
+template <typename T, int VEC, int TPG, int NV, bool GATE, bool BWD>
+using SourceOf = Source<T, VEC, TPG, NV, (BWD ? 2 : 1) + GATE, blocks_per_sm<VEC, NV>(BWD)>;
 
 // What is asked for, known to the compiler: GATE and SILU.
 template <typename T, int VEC, int TPG, int NV, bool GATE, bool SILU>
 __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(false)) gn_fwd_kernel(const GnArgs a)
 {
     constexpr int GPB = GN_THREADS / TPG;
+    extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float sm[GN_THREADS / 32];
     const int lane = threadIdx.x % TPG, group = threadIdx.x / TPG;
     const int h = blockIdx.x % a.H, part = blockIdx.x / a.H;
     const long long rows = (long long)a.B * a.L, first = (long long)part * GPB, step = (long long)a.nb * GPB;
-    const Affine<VEC, TPG, NV> aff(a, h, lane);
     Walk at(first + group, step, a.L);
-    Rows<const T> px(a.x, a.vx, h, at), pz(a.gate, a.vg, h, at);
+    const Rows<const T> px(a.x, a.vx, h, at), pz(a.gate, a.vg, h, at);
     Rows<T> po(a.out, a.vo, h, at);
+    SourceOf<T, VEC, TPG, NV, GATE, false> src(dyn, at, px, pz, pz, lane, a);
+    const Affine<VEC, TPG, NV> aff(a, h, lane);
     // every group of a warp (of the block, where the block is one) takes part in every turn's sums
     const int turns = (int)((rows - first + step - 1) / step);
     for (int k = 0; k < turns; ++k) {
-        Group<VEC, NV> x = {}, z = {};
+        Group<VEC, NV> in[1 + GATE], &x = in[0], &z = in[GATE];
         const bool on = at.b < a.B;
-        if (on) {
-            read<T, VEC, TPG, NV>(x, px.p, lane, a.d);
-            if (GATE) read<T, VEC, TPG, NV>(z, pz.p, lane, a.d);
-        }
+        src.next(in, on);
         normalise<VEC, TPG, NV>(x, a, lane, sm);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -290,8 +395,6 @@ __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(false)) gn_
         }
         if (on) write<T, VEC, TPG, NV>(x, po.p, lane, a.d);
         at.next();
-        px.next(at);
-        if (GATE) pz.next(at);
         po.next(at);
     }
 }
@@ -300,24 +403,22 @@ template <typename T, int VEC, int TPG, int NV, bool GATE, bool SILU>
 __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(true)) gn_bwd_kernel(const GnArgs a)
 {
     constexpr int GPB = GN_THREADS / TPG;
+    extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float sm[2 * GN_THREADS / 32];
     const int lane = threadIdx.x % TPG, group = threadIdx.x / TPG;
     const int h = blockIdx.x % a.H, part = blockIdx.x / a.H;
     const long long rows = (long long)a.B * a.L, first = (long long)part * GPB, step = (long long)a.nb * GPB;
+    Walk at(first + group, step, a.L);
+    const Rows<const T> px(a.x, a.vx, h, at), pz(a.gate, a.vg, h, at), pd(a.dout, a.vo, h, at);
+    Rows<T> pdx(a.dx, a.vdx, h, at), pdz(a.dgate, a.vdg, h, at);
+    SourceOf<T, VEC, TPG, NV, GATE, true> src(dyn, at, px, pd, pz, lane, a);
     const Affine<VEC, TPG, NV> aff(a, h, lane);
     Group<VEC, NV> dw = {}, db = {};
-    Walk at(first + group, step, a.L);
-    Rows<const T> px(a.x, a.vx, h, at), pz(a.gate, a.vg, h, at), pd(a.dout, a.vo, h, at);
-    Rows<T> pdx(a.dx, a.vdx, h, at), pdz(a.dgate, a.vdg, h, at);
     const int turns = (int)((rows - first + step - 1) / step);
     for (int k = 0; k < turns; ++k) {
-        Group<VEC, NV> x = {}, z = {}, o = {};
+        Group<VEC, NV> in[2 + GATE], &x = in[0], &o = in[1], &z = in[1 + GATE];
         const bool on = at.b < a.B;
-        if (on) {
-            read<T, VEC, TPG, NV>(x, px.p, lane, a.d);
-            read<T, VEC, TPG, NV>(o, pd.p, lane, a.d);
-            if (GATE) read<T, VEC, TPG, NV>(z, pz.p, lane, a.d);
-        }
+        src.next(in, on);
         const float rstd = normalise<VEC, TPG, NV>(x, a, lane, sm);
         float s[2] = {0.f, 0.f};  // sums of dy w and of dy w xh
 #pragma unroll
@@ -359,15 +460,14 @@ __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(true)) gn_b
             if (GATE) write<T, VEC, TPG, NV>(z, pdz.p, lane, a.d);
         }
         at.next();
-        px.next(at);
-        pd.next(at);
-        if (GATE) pz.next(at);
         pdx.next(at);
         if (GATE) pdz.next(at);
     }
     if (!a.part) return;
-    // the groups of the block joined, one after the other
-    extern __shared__ float sums[];  // [2][GPB][d]
+    // the groups of the block joined, one after the other; the ring's memory is free now
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float *const sums = (float *)dyn;  // [2][GPB][d]
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * TPG + lane) * VEC;
@@ -426,21 +526,24 @@ template <typename T, int VEC, int TPG, int NV, bool BWD> int launch_gn(const Gn
 {
     const long long blocks = (long long)a.nb * a.H;
     if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    const size_t smem = BWD && a.part ? sizeof(float) * 2 * (GN_THREADS / TPG) * a.d : 0;
-    auto go = [&](auto kern) {
-        if (smem > 48 * 1024 &&
+    auto go = [&](auto kern, auto gate) {
+        size_t smem = SourceOf<T, VEC, TPG, NV, decltype(gate)::value, BWD>::R::SMEM;
+        if (BWD && a.part) smem = std::max(smem, sizeof(float) * 2 * (GN_THREADS / TPG) * a.d);
+        if (smem > 47 * 1024 &&
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return (int)LA_ERR_CUDA;
         kern<<<(unsigned)blocks, GN_THREADS, smem, s>>>(a);
         return cudaPeekAtLastError() == cudaSuccess ? (int)LA_OK : (int)LA_ERR_CUDA;
     };
     const bool silu = a.act == LA_ACT_SILU;
+    const std::true_type yes;
+    const std::false_type no;
     if constexpr (BWD)
-        return a.gate ? silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, true, true>) : go(gn_bwd_kernel<T, VEC, TPG, NV, true, false>)
-                      : silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, false, true>) : go(gn_bwd_kernel<T, VEC, TPG, NV, false, false>);
+        return a.gate ? silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, true, true>, yes) : go(gn_bwd_kernel<T, VEC, TPG, NV, true, false>, yes)
+                      : silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, false, true>, no) : go(gn_bwd_kernel<T, VEC, TPG, NV, false, false>, no);
     else
-        return a.gate ? silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, true, true>) : go(gn_fwd_kernel<T, VEC, TPG, NV, true, false>)
-                      : silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, false, true>) : go(gn_fwd_kernel<T, VEC, TPG, NV, false, false>);
+        return a.gate ? silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, true, true>, yes) : go(gn_fwd_kernel<T, VEC, TPG, NV, true, false>, yes)
+                      : silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, false, true>, no) : go(gn_fwd_kernel<T, VEC, TPG, NV, false, false>, no);
 }
 
 // Threads and vectors of a group by its number of vectors: the fewest registers that hold it, a
