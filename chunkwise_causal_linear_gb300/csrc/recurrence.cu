@@ -243,14 +243,30 @@ __device__ __forceinline__ void copy_by(T *slot, const T *src, long long stride,
         }
     }
 }
+// The rare cases out of the way of the common one, which fits the instruction cache.
+template <typename T, int R, int CW>
+__device__ __noinline__ void copy_odd(T *slot, const T *src, long long stride, int nrow, int nch, int gran, int lane)
+{
+    if (gran == 16) copy_by<T, R, CW, 16>(slot, src, stride, nrow, nch, lane);
+    else if (gran == 4) copy_by<T, R, CW, 4>(slot, src, stride, nrow, nch, lane);
+    else if constexpr (sizeof(T) == 2 && CW == 32) copy_by<T, R, CW, 2>(slot, src, stride, nrow, nch, lane);
+}
 template <typename T, int R, int CW>
 __device__ __forceinline__ void copy_rows(T *slot, const T *src, long long stride, int nrow, int nch, int gran,
                                           int lane)
 {
-    if (nrow <= 0) return;
-    if (gran == 16) copy_by<T, R, CW, 16>(slot, src, stride, nrow, nch, lane);
-    else if (gran == 4) copy_by<T, R, CW, 4>(slot, src, stride, nrow, nch, lane);
-    else if constexpr (sizeof(T) == 2 && CW == 32) copy_by<T, R, CW, 2>(slot, src, stride, nrow, nch, lane);
+    if (nrow < R || gran != 16) {
+        if (nrow > 0) copy_odd<T, R, CW>(slot, src, stride, nrow, nch, gran, lane);
+        return;
+    }
+    constexpr int E = 16 / sizeof(T), N = CW / E, RP = 32 / N;  // elements a copy, copies a row, rows at once
+    const int r0 = lane / N, c = lane % N * E;
+    const T *p = src + r0 * stride + c;
+    const uint32_t dst = smem_u32(slot + r0 * CW + c);
+    if (c < nch)
+#pragma unroll
+        for (int j = 0; j < R / RP; ++j, p += RP * stride)
+            cp_async<16>(dst + (uint32_t)sizeof(T) * j * RP * CW, p);
 }
 
 // ---- V neighbouring channels (pairs are aligned and inside the channels together) -------------
@@ -286,6 +302,58 @@ template <int V> __device__ __forceinline__ void put(__nv_bfloat16 *p, const Ch<
 template <int V> struct __align__(8 * V) Fold {
     Ch<V> p, h;
 };
+
+// ---- rows one after the other -----------------------------------------------------------------
+// For the last, partial rows of a sequence and where something is not finite: from the copies in
+// shared memory, in a loop that stays small.
+template <typename T, typename G, int KIND, bool COMP, int V>
+__device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
+{
+    Fold<V> f{all<V>(1.f), all<V>(0.f)};
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
+        const Ch<V> x = get<V>(sx + i * 32 * V);
+        Ch<V> a, c;
+        gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        f.h = step(a, f.h, COMP ? mul(c, x) : x);
+        f.p = mul(f.p, a);
+    }
+    return f;
+}
+// out: this lane's channels of the first row; `present` rows of it exist
+template <typename T, typename G, int KIND, bool COMP, int V>
+__device__ __noinline__ void finish_rows(const T *sx, const G *sg, int rows, int present, Ch<V> h, T *out,
+                                         long long stride)
+{
+#pragma unroll 1
+    for (int i = 0; i < present; ++i, out += stride) {
+        if (i < rows) {
+            const Ch<V> x = get<V>(sx + i * 32 * V);
+            Ch<V> a, c;
+            gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+            h = step(a, h, COMP ? mul(c, x) : x);
+        }
+        put<V>(out, i < rows ? h : all<V>(0.f));
+    }
+}
+// The folds f[0], f[stride], ... of n runs applied to h.
+template <int V> __device__ __noinline__ Ch<V> apply_exact(const Fold<V> *f, int stride, int n, Ch<V> h)
+{
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) h = step(f[i * stride].p, h, f[i * stride].h);
+    return h;
+}
+// n runs in a row as one.
+template <int V> __device__ __noinline__ Fold<V> join_exact(const Fold<V> *f, int stride, int n)
+{
+    Fold<V> t{all<V>(1.f), all<V>(0.f)};
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        t.h = step(f[i * stride].p, t.h, f[i * stride].h);
+        t.p = mul(f[i * stride].p, t.p);
+    }
+    return t;
+}
 
 // ---- between the blocks of a cluster -----------------------------------------------------------
 // Sends a fold to `slot` in block `rank` of the cluster, counted there on `bar`.
@@ -365,17 +433,14 @@ template <int V> struct Peers {
         const Fold<V> *f = slot + buf * split * 32 + lane;
         const Ch<V> start = carry;
         Ch<V> mine = carry;
-        for (int r = 0; r < split; ++r, f += 32) {
+#pragma unroll 1
+        for (int r = 0; r < split; ++r) {
             if (r == rank) mine = carry;
-            carry = fma(f->p, carry, f->h);
+            carry = fma(f[r * 32].p, carry, f[r * 32].h);
         }
         if (!finite(carry)) {
-            f = slot + buf * split * 32 + lane;
-            carry = start;
-            for (int r = 0; r < split; ++r, f += 32) {
-                if (r == rank) mine = carry;
-                carry = step(f->p, carry, f->h);
-            }
+            carry = apply_exact<V>(f, 32, split, start);
+            mine = apply_exact<V>(f, 32, rank, start);
         }
         return mine;
     }
@@ -420,6 +485,9 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
     const int nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
     unsigned char *const ring = smem + Sm::AGG + warp * Sm::SLOT;
     auto first_row = [&](int k) { return (k * split + rank) * TILE + warp * R; };
+    // Steps copied ahead: a slot is kept until its step is finished, with SPLIT one step later.
+    constexpr int AHEAD = SPLIT ? ST - 2 : ST - 1;
+    static_assert(AHEAD > 0, "ring too short");
     int in = 0, at = 0;  // ring slots of the next copy and the next step
     auto load = [&](int k) {
         if (k < steps) {
@@ -436,46 +504,39 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
 #pragma unroll
         for (int v = 0; v < V; ++v) carry.v[v] = a.h0[(size_t)bh * a.d + c + v];
 
+    // gates and what joins the state, for the rows of a step
     struct Step {
-        Ch<V> a[R], b[R];  // gates and what joins the state
+        Ch<V> a[R], b[R];
     };
+    auto slot_x = [&](int s) { return (const T *)(ring + s * Sm::STAGE) + lane * V; };
+    auto slot_g = [&](int s) { return (const G *)(ring + s * Sm::STAGE + sizeof(T) * R * CW) + lane * V; };
     // the rows of step k; their fold goes to the warps of the tile
     auto fold = [&](int k, Step &s) {
-        cp_wait<ST - 2>();
+        cp_wait<AHEAD - 1>();
         __syncwarp();
-        const T *sx = (const T *)(ring + at * Sm::STAGE) + lane * V;
-        const G *sg = (const G *)(ring + at * Sm::STAGE + sizeof(T) * R * CW) + lane * V;
+        load(k + AHEAD);  // into a slot whose step the whole warp has finished
+        const T *sx = slot_x(at);
+        const G *sg = slot_g(at);
         at = at + 1 == ST ? 0 : at + 1;
         const int rows = min(n - first_row(k), R);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const Ch<V> xv = get<V>(sx + i * CW);
-            Ch<V> w;
-            gate_of<KIND, COMP, V>(get<V>(sg + i * CW), s.a[i], w);
-            s.b[i] = COMP ? mul(w, xv) : xv;
-        }
-        if constexpr (ST == 2) __syncwarp();
-        load(k + ST - 1);  // into the slot that the whole warp has read
-        if (rows < R) {
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (i >= rows) {
-                    s.a[i] = all<V>(1.f);
-                    s.b[i] = all<V>(0.f);
-                }
-        }
         Fold<V> f;
-        auto run = [&](auto exact) {
+        if (rows == R) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const Ch<V> xv = get<V>(sx + i * CW);
+                Ch<V> w;
+                gate_of<KIND, COMP, V>(get<V>(sg + i * CW), s.a[i], w);
+                s.b[i] = COMP ? mul(w, xv) : xv;
+            }
             f.p = s.a[0];
             f.h = s.b[0];
 #pragma unroll
             for (int i = 1; i < R; ++i) {
-                f.h = row<decltype(exact)::value>(s.a[i], f.h, s.b[i]);
+                f.h = fma(s.a[i], f.h, s.b[i]);
                 f.p = mul(f.p, s.a[i]);
             }
-        };
-        run(std::false_type());
-        if (!finite(f.h)) run(std::true_type());
+        }
+        if (rows < R || !finite(f.h)) f = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
         agg[(k % REC_BUFS * REC_W + warp) * 32 + lane] = f;
         __syncthreads();
     };
@@ -483,17 +544,13 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
     auto whole_tile = [&](int k) {
         const Fold<V> *f = agg + k % REC_BUFS * REC_W * 32 + lane;
         Fold<V> t = f[0];
-        auto run = [&](auto exact) {
-            t = f[0];
 #pragma unroll
-            for (int w = 1; w < REC_W; ++w) {
-                const Fold<V> q = f[w * 32];
-                t.h = row<decltype(exact)::value>(q.p, t.h, q.h);
-                t.p = mul(q.p, t.p);
-            }
-        };
-        run(std::false_type());
-        if (!finite(t.h)) run(std::true_type());
+        for (int w = 1; w < REC_W; ++w) {
+            const Fold<V> q = f[w * 32];
+            t.h = fma(q.p, t.h, q.h);
+            t.p = mul(q.p, t.p);
+        }
+        if (!finite(t.h)) t = join_exact<V>(f, 32, REC_W);
         return t;
     };
     // h from the state before the tile to that before this warp; returns the one after the tile
@@ -501,71 +558,68 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
         const Fold<V> *f = agg + k % REC_BUFS * REC_W * 32 + lane;
         const Ch<V> start = h;
         Ch<V> e = h;
-        auto run = [&](auto exact) {
-            e = start;
 #pragma unroll
-            for (int w = 0; w < REC_W; ++w) {
-                if (w == warp) h = e;
-                const Fold<V> q = f[w * 32];
-                e = row<decltype(exact)::value>(q.p, e, q.h);
-            }
-        };
-        run(std::false_type());
-        if (!finite(e)) run(std::true_type());
+        for (int w = 0; w < REC_W; ++w) {
+            if (w == warp) h = e;
+            const Fold<V> q = f[w * 32];
+            e = fma(q.p, e, q.h);
+        }
+        if (!finite(e)) {
+            e = apply_exact<V>(f, 32, REC_W, start);
+            h = apply_exact<V>(f, 32, warp, start);
+        }
         return e;
     };
-    // the rows of step k from the state before them
-    auto finish = [&](int k, const Step &s, const Ch<V> &start) {
+    // the rows of step k, copied to slot sl, from the state before them
+    auto finish = [&](int k, int sl, const Step &s, const Ch<V> &start) {
         const int t0 = first_row(k), rows = min(n - t0, R);
         if (a.chunks && t0 % RC == 0 && t0 < a.L && on)
 #pragma unroll
             for (int v = 0; v < V; ++v) a.chunks[((size_t)bh * nc + t0 / RC) * a.d + c + v] = start.v[v];
-        T *const o = out + t0 * a.vo.l;
-        Ch<V> h;
-        auto run = [&](auto exact, auto whole) {
-            h = start;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                h = row<decltype(exact)::value>(s.a[i], h, s.b[i]);
-                if (on && (decltype(whole)::value || t0 + i < a.L))
-                    put<V>(o + i * a.vo.l + lane * V, decltype(whole)::value || i < rows ? h : all<V>(0.f));
-            }
-        };
+        T *const o = out + t0 * a.vo.l + lane * V;
+        Ch<V> h = start;
         if (rows == R) {
-            run(std::false_type(), std::true_type());
-            if (!finite(h)) run(std::true_type(), std::true_type());
-        } else {
-            run(std::true_type(), std::false_type());
+            T *p = o;
+#pragma unroll
+            for (int i = 0; i < R; ++i, p += a.vo.l) {
+                h = fma(s.a[i], h, s.b[i]);
+                if (on) put<V>(p, h);
+            }
         }
+        if ((rows < R || !finite(h)) && on && t0 < a.L)
+            finish_rows<T, G, KIND, COMP, V>(slot_x(sl), slot_g(sl), rows, min(a.L - t0, R), start, o, a.vo.l);
     };
 
 #pragma unroll
-    for (int k = 0; k < ST - 1; ++k) load(k);
+    for (int k = 0; k < AHEAD; ++k) load(k);
     if constexpr (!SPLIT) {
         Step s;
         for (int k = 0; k < steps; ++k) {
+            const int sl = at;
             fold(k, s);
             Ch<V> h = carry;
             carry = over_warps(k, h);
-            finish(k, s, h);
+            finish(k, sl, s, h);
         }
     } else {
         // The next step is folded before what the others sent for this one is waited for.
         Peers<V> peers;
         peers.init(smem + Sm::PEERS, split, rank, a.err);
-        Step s0, s1;
-        fold(0, s0);
+        Step now, next;
+        int sl = at;
+        fold(0, now);
         peers.publish(0, warp, lane, whole_tile(0));
-        auto turn = [&](int k, const Step &now, Step &next) {
-            if (k + 1 < steps) fold(k + 1, next);
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k) {
+            const int sl_next = at;
+            const bool more = k + 1 < steps;
+            if (more) fold(k + 1, next);
             Ch<V> h = peers.over(k, lane, carry);
-            if (k + 1 < steps) peers.publish(k + 1, warp, lane, whole_tile(k + 1));
+            if (more) peers.publish(k + 1, warp, lane, whole_tile(k + 1));
             over_warps(k, h);
-            finish(k, now, h);
-        };
-        for (int k = 0; k < steps; k += 2) {
-            turn(k, s0, s1);
-            if (k + 1 < steps) turn(k + 1, s1, s0);
+            finish(k, sl, now, h);
+            now = next;
+            sl = sl_next;
         }
         cluster_barrier();  // nothing is sent to a block that has ended
     }
