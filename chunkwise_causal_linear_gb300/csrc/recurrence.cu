@@ -35,7 +35,7 @@ namespace {
 constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the forward leaves
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
-constexpr int REC_MAX_SPLIT = 8;         // blocks of a portable cluster
+constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
 constexpr int FWD_R = 16, BWD_R = 8;     // rows of a warp
 static_assert(BWD_R * REC_W == RC && RC % FWD_R == 0, "backward tiles and forward warps start at chunks");
 
@@ -225,7 +225,7 @@ __device__ __forceinline__ void copy_by(T *slot, const T *src, long long stride,
         const T *p = src + r0 * stride + c;
         T *q = slot + r0 * ROW + c;
         if constexpr (BYTES == 2) {
-            constexpr int BATCH = 4;  // loads on the way at once
+            constexpr int BATCH = M;  // loads on the way at once
 #pragma unroll 1
             for (int i = 0; i < M; i += BATCH) {
                 T v[BATCH];
@@ -320,6 +320,19 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
     }
     return f;
 }
+// the state h after `rows` rows
+template <typename T, typename G, int KIND, bool COMP, int V>
+__device__ __noinline__ Ch<V> apply_rows(const T *sx, const G *sg, int rows, Ch<V> h)
+{
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
+        const Ch<V> x = get<V>(sx + i * 32 * V);
+        Ch<V> a, c;
+        gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        h = step(a, h, COMP ? mul(c, x) : x);
+    }
+    return h;
+}
 // out: this lane's channels of the first row; `present` rows of it exist
 template <typename T, typename G, int KIND, bool COMP, int V>
 __device__ __noinline__ void finish_rows(const T *sx, const G *sg, int rows, int present, Ch<V> h, T *out,
@@ -353,6 +366,47 @@ template <int V> __device__ __noinline__ Fold<V> join_exact(const Fold<V> *f, in
         t.p = mul(f[i * stride].p, t.p);
     }
     return t;
+}
+
+template <int V> struct BwdFold {
+    Ch<V> p, h, e;
+};
+template <typename T, typename G, int KIND, bool COMP, int V>
+__device__ __noinline__ BwdFold<V> fold_rows_bwd(const T *sx, const T *sd, const G *sg, int rows)
+{
+    const Fold<V> f = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
+    Ch<V> e = all<V>(0.f);
+#pragma unroll 1
+    for (int i = rows - 1; i >= 0; --i) {
+        Ch<V> a, c;
+        gate_of<KIND, false, V>(get<V>(sg + i * 32 * V), a, c);
+        e = forget(a, add(e, get<V>(sd + i * 32 * V)));
+    }
+    return {f.p, f.h, e};
+}
+// h, e: the state before these rows and what comes back from those behind them
+template <typename T, typename G, int KIND, bool COMP, int V>
+__device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *sg, int rows, int present, Ch<V> h,
+                                             Ch<V> e, T *dx, long long dx_stride, G *dg, long long dg_stride)
+{
+#pragma unroll 1
+    for (int i = present - 1; i >= 0; --i) {
+        Ch<V> rx = all<V>(0.f), rg = rx;
+        if (i < rows) {
+            const Ch<V> hb = apply_rows<T, G, KIND, COMP, V>(sx, sg, i, h);
+            const Ch<V> x = get<V>(sx + i * 32 * V);
+            Ch<V> a, c;
+            gate_of<KIND, COMP || KIND == LA_GATE_SIGMOID, V>(get<V>(sg + i * 32 * V), a, c);
+            e = add(e, get<V>(sd + i * 32 * V));
+            rx = COMP ? mul(c, e) : e;
+            const Ch<V> f = COMP ? fma(x, all<V>(-1.f), hb) : hb, ae = forget(a, e);
+            if (KIND == LA_GATE_VALUE) rg = mul(e, f);
+            else rg = forget(KIND == LA_GATE_LOG ? ae : forget(c, ae), f);
+            e = ae;
+        }
+        put<V>(dx + i * dx_stride, rx);
+        put<V>(dg + i * dg_stride, rg);
+    }
 }
 
 // ---- between the blocks of a cluster -----------------------------------------------------------
@@ -413,7 +467,7 @@ template <int V> struct Peers {
     {
         const int buf = k % REC_BUFS;
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<V>)));
-        if (warp < split) send<V>(slot + (buf * split + rank) * 32 + lane, &bar[buf], warp, f);
+        for (int r = warp; r < split; r += REC_W) send<V>(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
     }
     // The carry over the tiles of step k, `carry = P carry + H`: returns the carry before this
     // block's tile and leaves the one after the step.
@@ -684,155 +738,108 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         cp_wait<ST - 2>();
         __syncwarp();
         if constexpr (ST > 2) load(k + ST - 1);  // into the slot of step k - 1, which the whole warp has read
-        const T *sx = (const T *)(ring + at * Sm::STAGE) + lane * V, *sd = sx + R * CW;
-        const G *sg = (const G *)(ring + at * Sm::STAGE + 2 * sizeof(T) * R * CW) + lane * V;
+        const T *const sx = (const T *)(ring + at * Sm::STAGE) + lane * V, *const sd = sx + R * CW;
+        const G *const sg = (const G *)(ring + at * Sm::STAGE + 2 * sizeof(T) * R * CW) + lane * V;
         at = at + 1 == ST ? 0 : at + 1;
         // hb: w x, then the state before the row; cc: 1 - a
         Ch<V> ga[R], hb[R], cc[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const Ch<V> xv = get<V>(sx + i * CW);
-            gate_of<KIND, WANT_C, V>(get<V>(sg + i * CW), ga[i], cc[i]);
-            hb[i] = COMP ? mul(cc[i], xv) : xv;
-        }
-        if (rows < R) {
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (i >= rows) {
-                    ga[i] = all<V>(1.f);
-                    hb[i] = all<V>(0.f);
-                }
-        }
-        Ch<V> P, H, E;
-        auto fold = [&](auto exact, auto whole) {
-            P = all<V>(1.f);
-            H = E = all<V>(0.f);
+        BwdFold<V> f;
+        if (rows == R) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                H = row<decltype(exact)::value>(ga[i], H, hb[i]);
-                P = mul(P, ga[i]);
+                const Ch<V> xv = get<V>(sx + i * CW);
+                gate_of<KIND, WANT_C, V>(get<V>(sg + i * CW), ga[i], cc[i]);
+                hb[i] = COMP ? mul(cc[i], xv) : xv;
             }
+            f.p = ga[0];
+            f.h = hb[0];
 #pragma unroll
-            for (int i = R - 1; i >= 0; --i)
-                if (decltype(whole)::value || i < rows) {
-                    const Ch<V> e = add(E, get<V>(sd + i * CW));
-                    E = decltype(exact)::value ? forget(ga[i], e) : mul(ga[i], e);
-                }
-        };
-        if (rows == R) {
-            fold(std::false_type(), std::true_type());
-            if (!finite(H) || !finite(E)) fold(std::true_type(), std::true_type());
-        } else {
-            fold(std::true_type(), std::false_type());
+            for (int i = 1; i < R; ++i) {
+                f.h = fma(ga[i], f.h, hb[i]);
+                f.p = mul(f.p, ga[i]);
+            }
+            f.e = mul(ga[R - 1], get<V>(sd + (R - 1) * CW));
+#pragma unroll
+            for (int i = R - 2; i >= 0; --i) f.e = mul(ga[i], add(f.e, get<V>(sd + i * CW)));
         }
+        if (rows < R || !finite(f.h) || !finite(f.e)) f = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
         const int buf = k % REC_BUFS;
         Fold<V> *const here = agg + buf * REC_W * 32 + lane;
         Ch<V> *const front = ahead + buf * REC_W * 32 + lane;
-        here[warp * 32] = Fold<V>{P, E};
-        front[warp * 32] = H;
+        here[warp * 32] = Fold<V>{f.p, f.e};
+        front[warp * 32] = f.h;
         __syncthreads();
         Ch<V> e = carry;
         if constexpr (SPLIT) {
-            Fold<V> t;
-            auto run = [&](auto exact) {
-                t = here[(REC_W - 1) * 32];
+            Fold<V> t = here[(REC_W - 1) * 32];
 #pragma unroll
-                for (int w = REC_W - 2; w >= 0; --w) {
-                    const Fold<V> q = here[w * 32];
-                    t.h = row<decltype(exact)::value>(q.p, t.h, q.h);
-                    t.p = mul(q.p, t.p);
-                }
-            };
-            run(std::false_type());
-            if (!finite(t.h)) run(std::true_type());
+            for (int w = REC_W - 2; w >= 0; --w) {
+                const Fold<V> q = here[w * 32];
+                t.h = fma(q.p, t.h, q.h);
+                t.p = mul(q.p, t.p);
+            }
+            if (!finite(t.h)) t = join_exact<V>(here + (REC_W - 1) * 32, -32, REC_W);
             peers.publish(k, warp, lane, t);
         }
         // h over the warps before this one, e over those behind it
         {
             const Ch<V> start = h;
-            auto run = [&](auto exact) {
+#pragma unroll
+            for (int w = 0; w < REC_W - 1; ++w)
+                if (w < warp) h = fma(here[w * 32].p, h, front[w * 32]);
+            if (!finite(h)) {
                 h = start;
-                for (int w = 0; w < warp; ++w) h = row<decltype(exact)::value>(here[w * 32].p, h, front[w * 32]);
-            };
-            run(std::false_type());
-            if (!finite(h)) run(std::true_type());
+#pragma unroll 1
+                for (int w = 0; w < warp; ++w) h = step(here[w * 32].p, h, front[w * 32]);
+            }
         }
         if constexpr (SPLIT) e = peers.over(k, lane, carry);
         {
             const Ch<V> start = e;
-            Ch<V> f = e;
-            auto run = [&](auto exact) {
-                f = start;
+            Ch<V> t = e;
 #pragma unroll
-                for (int w = REC_W - 1; w >= 0; --w) {
-                    if (w == warp) e = f;
-                    const Fold<V> q = here[w * 32];
-                    f = row<decltype(exact)::value>(q.p, f, q.h);
-                }
-            };
-            run(std::false_type());
-            if (!finite(f)) run(std::true_type());
-            if constexpr (!SPLIT) carry = f;
+            for (int w = REC_W - 1; w >= 0; --w) {
+                if (w == warp) e = t;
+                const Fold<V> q = here[w * 32];
+                t = fma(q.p, t, q.h);
+            }
+            if (!finite(t)) {
+                t = apply_exact<V>(here + (REC_W - 1) * 32, -32, REC_W, start);
+                e = apply_exact<V>(here + (REC_W - 1) * 32, -32, REC_W - 1 - warp, start);
+            }
+            if constexpr (!SPLIT) carry = t;
         }
-        // run forward; on a result that is not finite once more, exactly, from w x
-        const Ch<V> hs = h;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const Ch<V> bx = hb[i];
-            hb[i] = h;
-            h = fma(ga[i], h, bx);
-        }
-        const bool tame = finite(h);
-        if (!tame) {
-            h = hs;
+        T *const ox = dx + t0 * a.vdx.l + lane * V;
+        G *const og = dg + t0 * a.vdg.l + lane * V;
+        const Ch<V> h0 = h, e0 = e;
+        bool tame = rows == R;
+        if (rows == R) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
+                const Ch<V> bx = hb[i];
                 hb[i] = h;
-                if (i < rows) {
-                    const Ch<V> xv = get<V>(sx + i * CW);
-                    h = step(ga[i], h, COMP ? mul(cc[i], xv) : xv);
-                }
+                h = fma(ga[i], h, bx);
             }
-        }
-        T *const ox = dx + t0 * a.vdx.l;
-        G *const og = dg + t0 * a.vdg.l;
-        // With EXACT = false e and h are finite, so a slope of 0 makes the product 0 by itself.
-        auto finish = [&](auto exact, auto whole, Ch<V> &e) {
-            constexpr bool EX = decltype(exact)::value, ALL = decltype(whole)::value;
+            // while h and e are finite, a slope of 0 makes its product 0 by itself
+            T *px = ox + (R - 1) * a.vdx.l;
+            G *pg = og + (R - 1) * a.vdg.l;
 #pragma unroll
-            for (int i = R - 1; i >= 0; --i) {
-                Ch<V> rx = all<V>(0.f), rg = rx;
-                if (ALL || i < rows) {
-                    e = add(e, get<V>(sd + i * CW));  // e_t
-                    rx = COMP ? mul(cc[i], e) : e;
-                    Ch<V> f = hb[i];
-                    if (COMP) f = fma(get<V>(sx + i * CW), all<V>(-1.f), f);
-                    if (KIND == LA_GATE_VALUE) {
-                        rg = mul(e, f);
-                        e = EX ? forget(ga[i], e) : mul(ga[i], e);
-                    } else {
-                        const Ch<V> ae = EX ? forget(ga[i], e) : mul(ga[i], e);
-                        const Ch<V> se = KIND == LA_GATE_LOG ? ae : EX ? forget(cc[i], ae) : mul(cc[i], ae);
-                        rg = EX ? forget(se, f) : mul(se, f);
-                        e = ae;
-                    }
+            for (int i = R - 1; i >= 0; --i, px -= a.vdx.l, pg -= a.vdg.l) {
+                e = add(e, get<V>(sd + i * CW));  // e_t
+                const Ch<V> rx = COMP ? mul(cc[i], e) : e, ae = mul(ga[i], e);
+                Ch<V> q = hb[i];
+                if (COMP) q = fma(get<V>(sx + i * CW), all<V>(-1.f), q);
+                const Ch<V> se = KIND == LA_GATE_VALUE ? e : KIND == LA_GATE_LOG ? ae : mul(cc[i], ae);
+                if (on) {
+                    put<V>(px, rx);
+                    put<V>(pg, mul(se, q));
                 }
-                if (on && (ALL || t0 + i < a.L)) {
-                    put<V>(ox + i * a.vdx.l + lane * V, rx);
-                    put<V>(og + i * a.vdg.l + lane * V, rg);
-                }
+                e = ae;
             }
-        };
-        if (rows == R) {
-            const Ch<V> e0 = e;
-            finish(std::false_type(), std::true_type(), e);
-            if (!tame || !finite(e)) {
-                e = e0;
-                finish(std::true_type(), std::true_type(), e);
-            }
-        } else if (tile >= 0) {
-            finish(std::true_type(), std::false_type(), e);
+            tame = finite(h) && finite(e);
         }
+        if (!tame && on && tile >= 0 && t0 < a.L)
+            finish_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows, min(a.L - t0, R), h0, e0, ox, a.vdx.l, og, a.vdg.l);
         if constexpr (ST == 2) {
             __syncwarp();
             load(k + 1);
@@ -860,16 +867,6 @@ __global__ void __launch_bounds__(STEP_THREADS) rec_step_kernel(const T *x, cons
 }
 
 // ---- host side ---------------------------------------------------------------------------------
-// Blocks of a cluster: a power of two (those of other sizes do not pack into the GPU: 9 made 32
-// clusters two waves), as many as the sequence has tiles for and one wave of two blocks an SM
-// holds.
-int choose_split(long long blocks, long long tiles, int sms)
-{
-    int split = 1;
-    while (split < REC_MAX_SPLIT && 2 * split * blocks <= 2ll * sms && split < tiles) split *= 2;
-    return split;
-}
-
 int granule(const void *p, const View &v, const RecArgs &a, size_t elem)
 {
     for (size_t g : {(size_t)16, (size_t)4})
@@ -877,26 +874,64 @@ int granule(const void *p, const View &v, const RecArgs &a, size_t elem)
     return 2;
 }
 
-template <typename Kern>
-int launch_rec(Kern kern, const RecArgs &a, size_t smem, cudaStream_t s)
-{
-    const long long blocks = (long long)a.B * a.H * a.ncb * a.split;
-    if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return LA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(REC_THREADS);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)a.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
-}
+// A kernel's launches: attributes set and cluster sizes looked up once per device.
+struct RecKernel {
+    const void *fn;
+    size_t (*smem)(int split);
+    bool ready[64];
+    int fit[64][REC_MAX_SPLIT + 1];  // clusters of that size on the GPU at once, 0 where not looked up
+
+    void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, int split) const
+    {
+        cfg = {};
+        cfg.blockDim = dim3(REC_THREADS);
+        cfg.dynamicSmemBytes = smem(split);
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = (unsigned)split;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = split > 1 ? 1 : 0;
+    }
+    bool prepare(int dev, bool split)
+    {
+        if (ready[dev]) return true;
+        const size_t most = smem(split ? REC_MAX_SPLIT : 1);
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
+            (split && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+            return false;
+        return ready[dev] = true;
+    }
+    // The largest cluster, and no more blocks of it than tiles, with which all blocks run at once:
+    // a second wave of clusters costs as much as the first (48 blocks, 16384 rows, bf16: 54 us with
+    // clusters of 5, 65 with 8, which take two waves, 63 with 4).
+    int choose(int dev, long long blocks, long long tiles)
+    {
+        for (int s = (int)std::min(tiles, (long long)REC_MAX_SPLIT); s > 1; --s) {
+            if (!fit[dev][s]) {
+                cudaLaunchConfig_t cfg;
+                cudaLaunchAttribute at;
+                config(cfg, at, s);
+                cfg.gridDim = dim3((unsigned)s);
+                int n = 0;
+                fit[dev][s] = cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0 ? n : -1;
+            }
+            if (fit[dev][s] >= blocks) return s;
+        }
+        return 1;
+    }
+    int launch(RecArgs &a, cudaStream_t stream) const
+    {
+        const long long blocks = (long long)a.B * a.H * a.ncb * a.split;
+        if (blocks > INT_MAX) return LA_ERR_SHAPE;
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute at;
+        config(cfg, at, a.split);
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.stream = stream;
+        void *args[] = {&a};
+        return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    }
+};
 
 // Calls f.template operator()<T, G, KIND, COMP>() for the runtime choice.
 template <typename F>
@@ -918,38 +953,54 @@ int dispatch(int dtype, int gate_dtype, int kind, int comp, F f)
                                 : by_kind(__nv_bfloat16(), __nv_bfloat16());
 }
 
-// Two channels a lane where pairs are whole and aligned and the blocks of 64 channels alone give
-// every SM one; else one channel a lane, for twice the blocks, and clusters over the rows.
 template <bool BWD>
 struct LaunchRec {
     static constexpr int TILE = REC_W * (BWD ? BWD_R : FWD_R);
     RecArgs &a;
-    int sms;
+    int sms, dev;
     cudaStream_t s;
-    template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT> int go() const
+
+    template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT> static RecKernel &kernel()
     {
-        const size_t smem = RecSmem<T, G, V, BWD>::bytes(a.split);
-        if constexpr (BWD) return launch_rec(rec_bwd_kernel<T, G, KIND, COMP, V, SPLIT>, a, smem, s);
-        else return launch_rec(rec_fwd_kernel<T, G, KIND, COMP, V, SPLIT>, a, smem, s);
+        static RecKernel k = {BWD ? (const void *)rec_bwd_kernel<T, G, KIND, COMP, V, SPLIT>
+                                  : (const void *)rec_fwd_kernel<T, G, KIND, COMP, V, SPLIT && V == 1>,
+                              &RecSmem<T, G, V, BWD>::bytes};
+        return k;
+    }
+    template <typename T, typename G, int KIND, bool COMP, int V> int with() const
+    {
+        const long long blocks = (long long)a.B * a.H * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
+        a.split = 1;
+        if (blocks <= sms && tiles > 1 && (BWD || V == 1)) {
+            RecKernel &k = kernel<T, G, KIND, COMP, V, true>();
+            if (!k.prepare(dev, true)) return LA_ERR_CUDA;
+            a.split = k.choose(dev, blocks, tiles);
+            if (a.split > 1) return k.launch(a, s);
+        }
+        RecKernel &k = kernel<T, G, KIND, COMP, V, false>();
+        return k.prepare(dev, false) ? k.launch(a, s) : LA_ERR_CUDA;
     }
     template <typename T> bool pairs(const void *p, const View &v) const
     {
         return !p || rows_aligned(p, v, a.B, a.H, a.L, sizeof(T), 2 * sizeof(T));
     }
+    // Two channels a lane for bf16 (pairs of fp32 would leave one block an SM) where pairs are whole
+    // and aligned: forward where the blocks of 64 channels alone give every SM one, because the
+    // split kernel holds two steps in registers; backward, where it holds one, where clusters of
+    // them do.  (B2 H12 L16384 d64 bf16 backward: 91 us with pairs, 114 without; forward B8 H16
+    // L8192 d128: 135 and 174.)
     template <typename T, typename G, int KIND, bool COMP> int operator()() const
     {
-        const long long heads = (long long)a.B * a.H;
-        a.split = 1;
-        // forward, pairs of fp32 inputs would take twice the shared memory and leave one block an SM
-        if constexpr (BWD || sizeof(T) + sizeof(G) == 4) {
+        if constexpr (sizeof(T) + sizeof(G) == 4) {
             a.ncb = (a.d + 63) / 64;
-            if (a.d % 2 == 0 && a.d > 32 && heads * a.ncb >= sms && pairs<T>(a.x, a.vx) && pairs<G>(a.g, a.vg) &&
+            const long long blocks = (long long)a.B * a.H * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
+            const long long most = BWD ? std::min(tiles, (long long)REC_MAX_SPLIT) : 1;
+            if (a.d % 2 == 0 && a.d > 32 && blocks * most >= sms && pairs<T>(a.x, a.vx) && pairs<G>(a.g, a.vg) &&
                 pairs<T>(a.out, a.vo) && pairs<T>(a.dout, a.vo) && pairs<T>(a.dx, a.vdx) && pairs<G>(a.dg, a.vdg))
-                return go<T, G, KIND, COMP, 2, false>();
+                return with<T, G, KIND, COMP, 2>();
         }
         a.ncb = (a.d + 31) / 32;
-        a.split = choose_split(heads * a.ncb, (a.L + TILE - 1) / TILE, sms);
-        return a.split > 1 ? go<T, G, KIND, COMP, 1, true>() : go<T, G, KIND, COMP, 1, false>();
+        return with<T, G, KIND, COMP, 1>();
     }
 };
 
@@ -1007,9 +1058,10 @@ int la_recurrence_fwd(const void *x, const void *gate, const float *h0, const in
     a.grx = granule(x, a.vx, a, e);
     a.grg = granule(gate, a.vg, a, dtype_size(gate_dtype));
     const int sms = device_sms();
+    int dev = 0;
     a.err = err_ptr();
-    if (sms <= 0 || !a.err) return LA_ERR_CUDA;
-    return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<false>{a, sms, (cudaStream_t)stream});
+    if (sms <= 0 || !a.err || cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
+    return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<false>{a, sms, dev, (cudaStream_t)stream});
 }
 
 int la_recurrence_bwd(const void *x, const void *gate, const float *chunk_states,
@@ -1044,9 +1096,10 @@ int la_recurrence_bwd(const void *x, const void *gate, const float *chunk_states
     a.grg = granule(gate, a.vg, a, eg);
     a.gro = granule(dout, a.vo, a, e);
     const int sms = device_sms();
+    int dev = 0;
     a.err = err_ptr();
-    if (sms <= 0 || !a.err) return LA_ERR_CUDA;
-    return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<true>{a, sms, (cudaStream_t)stream});
+    if (sms <= 0 || !a.err || cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
+    return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<true>{a, sms, dev, (cudaStream_t)stream});
 }
 
 int la_recurrence_step(const void *x, const void *gate, float *state, void *out, int B, int H,
