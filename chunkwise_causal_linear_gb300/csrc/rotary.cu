@@ -153,10 +153,12 @@ template <typename T, int VEC> int launch_rotary(RotArgs &a, int sms, cudaStream
     const int units = a.rot / (2 * VEC) + (a.d - a.rot + 2 * VEC - 1) / (2 * VEC);
     const long long blocks = ((long long)a.B * a.L * units + ROT_THREADS - 1) / ROT_THREADS;
     if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    // heads of a thread: as many as still leave every SM eight blocks
-    a.heads = ROT_HEADS;
+    // heads of a thread: at most ROT_HEADS, in even groups, and as many as still leave every SM eight
+    // blocks
+    const int most = std::max(a.H, a.Hk), even = (most + ROT_HEADS - 1) / ROT_HEADS;
+    a.heads = (most + even - 1) / even;
     auto groups = [&](int n) { return (n + a.heads - 1) / a.heads; };
-    while (a.heads > 1 && blocks * (groups(a.H) + groups(a.Hk)) < 8ll * sms) a.heads /= 2;
+    while (a.heads > 1 && blocks * (groups(a.H) + groups(a.Hk)) < 8ll * sms) a.heads = (a.heads + 1) / 2;
     while ((long long)groups(a.H) + groups(a.Hk) > 65535) a.heads *= 2;  // limit of the grid
     a.qgroups = groups(a.H);
     const int ny = a.qgroups + groups(a.Hk);
