@@ -7,9 +7,9 @@
 // c_t = a_t e_t, e_t = dout_t + c_{t+1}: c -> P c + E with the same P.
 //
 // The rows of one head's block of 32 V channels go through one cluster of S blocks (S = 1: one
-// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R rows (16
-// forward, 8 backward, which holds three values a row and channel), a lane holds V channels of
-// them in registers, V = 2 as pairs for the packed fp32 instructions.  Per step: fold the R rows,
+// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R rows (16, or
+// 8), a lane holds V channels of them in registers, V = 2 as pairs for the packed fp32
+// instructions.  Per step: fold the R rows,
 // put (P, H) into shared memory, one block barrier, run the carried state over the 8 warps.  With
 // S > 1 every block sends its tile's (P, H) into the others' shared memory (st.async, which
 // counts on an mbarrier there), and folds its next tile before it waits for what the others sent
@@ -36,8 +36,10 @@ constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the for
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
 constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
-constexpr int FWD_R = 16, BWD_R = 8;     // rows of a warp
-static_assert(BWD_R * REC_W == RC && RC % FWD_R == 0, "backward tiles and forward warps start at chunks");
+// Rows of a warp: backward, which holds three values a row and channel, 8 with pairs.
+__host__ __device__ constexpr int rec_rows(bool bwd, int V) { return bwd && V == 2 ? 8 : 16; }
+static_assert(rec_rows(true, 2) * REC_W % RC == 0 && RC % rec_rows(false, 1) == 0,
+              "backward tiles and some of the forward's warps start at chunks");
 
 struct RecArgs {
     const void *x, *g, *dout;
@@ -505,7 +507,7 @@ template <int V> struct Peers {
 // may be a step ahead of another that still reads), the rings, and what the blocks of the
 // cluster send.
 template <typename T, typename G, int V, bool BWD> struct RecSmem {
-    static constexpr int R = BWD ? BWD_R : FWD_R;
+    static constexpr int R = rec_rows(BWD, V);
     static constexpr size_t AGG = sizeof(Fold<V>) * REC_BUFS * REC_W * 32;
     static constexpr size_t AHEAD = BWD ? AGG / 2 : 0;  // backward: H beside (P, E)
     static constexpr size_t SLOT = (size_t)R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
@@ -524,7 +526,7 @@ template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
 __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a)
 {
     using Sm = RecSmem<T, G, V, false>;
-    constexpr int CW = 32 * V, ST = Sm::STAGES, R = FWD_R, TILE = R * REC_W;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = Sm::R, TILE = R * REC_W;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -689,7 +691,7 @@ template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
 __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a)
 {
     using Sm = RecSmem<T, G, V, true>;
-    constexpr int CW = 32 * V, ST = Sm::STAGES, R = BWD_R, TILE = RC;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = Sm::R, TILE = R * REC_W;
     constexpr bool WANT_C = COMP || KIND == LA_GATE_SIGMOID;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;            // (P, E) of the warps
@@ -704,7 +706,8 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
     const T *dout = (const T *)a.dout + row_of(a.vo, b, hd, 0) + c0;
     T *dx = (T *)a.dx + row_of(a.vdx, b, hd, 0) + c0;
     G *dg = (G *)a.dg + row_of(a.vdg, b, hd, 0) + c0;
-    const int n = rows_of(a, b), nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
+    const int n = rows_of(a, b), nc = (a.L + RC - 1) / RC;
+    const int nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
     unsigned char *const ring = smem + Sm::AGG + Sm::AHEAD + warp * Sm::SLOT;
     // a step's tiles run backwards; before the first tile there are none (negative rows)
     auto first_row = [&](int k) { return (nt - 1 - (k * split + rank)) * TILE + warp * R; };
@@ -734,10 +737,10 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         Ch<V> h = all<V>(0.f);  // the state before the tile
         if (on && tile >= 0)
 #pragma unroll
-            for (int v = 0; v < V; ++v) h.v[v] = a.chunks_in[((size_t)bh * nt + tile) * a.d + c + v];
+            for (int v = 0; v < V; ++v) h.v[v] = a.chunks_in[((size_t)bh * nc + tile * (TILE / RC)) * a.d + c + v];
         cp_wait<ST - 2>();
         __syncwarp();
-        if constexpr (ST > 2) load(k + ST - 1);  // into the slot of step k - 1, which the whole warp has read
+        load(k + ST - 1);  // into the slot of step k - 1, which the whole warp has finished
         const T *const sx = (const T *)(ring + at * Sm::STAGE) + lane * V, *const sd = sx + R * CW;
         const G *const sg = (const G *)(ring + at * Sm::STAGE + 2 * sizeof(T) * R * CW) + lane * V;
         at = at + 1 == ST ? 0 : at + 1;
@@ -840,10 +843,6 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         }
         if (!tame && on && tile >= 0 && t0 < a.L)
             finish_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows, min(a.L - t0, R), h0, e0, ox, a.vdx.l, og, a.vdg.l);
-        if constexpr (ST == 2) {
-            __syncwarp();
-            load(k + 1);
-        }
     }
     if constexpr (SPLIT) cluster_barrier();  // nothing is sent to a block that has ended
     if (a.dh0 && rank == 0 && warp == 0 && on)
@@ -955,7 +954,6 @@ int dispatch(int dtype, int gate_dtype, int kind, int comp, F f)
 
 template <bool BWD>
 struct LaunchRec {
-    static constexpr int TILE = REC_W * (BWD ? BWD_R : FWD_R);
     RecArgs &a;
     int sms, dev;
     cudaStream_t s;
@@ -969,6 +967,7 @@ struct LaunchRec {
     }
     template <typename T, typename G, int KIND, bool COMP, int V> int with() const
     {
+        constexpr int TILE = REC_W * rec_rows(BWD, V);
         const long long blocks = (long long)a.B * a.H * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
         a.split = 1;
         if (blocks <= sms && tiles > 1 && (BWD || V == 1)) {
@@ -991,7 +990,8 @@ struct LaunchRec {
     // L8192 d128: 135 and 174.)
     template <typename T, typename G, int KIND, bool COMP> int operator()() const
     {
-        if constexpr (sizeof(T) + sizeof(G) == 4) {
+        if constexpr (sizeof(T) + sizeof(G) == 4 || (BWD && sizeof(T) == 2)) {
+            constexpr int TILE = REC_W * rec_rows(BWD, 2);
             a.ncb = (a.d + 63) / 64;
             const long long blocks = (long long)a.B * a.H * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
             const long long most = BWD ? std::min(tiles, (long long)REC_MAX_SPLIT) : 1;
