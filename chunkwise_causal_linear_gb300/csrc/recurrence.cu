@@ -7,21 +7,27 @@
 // c_t = a_t e_t, e_t = dout_t + c_{t+1}: c -> P c + E with the same P.
 //
 // The rows of one head's block of 32 V channels go through one cluster of S blocks (S = 1: one
-// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R rows (16, or
-// 8), a lane holds V channels of them in registers, V = 2 as pairs for the packed fp32
-// instructions.  Per step: fold the R rows,
+// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R = 16 rows,
+// a lane holds V channels of them in registers, as pairs for the packed fp32 instructions: two
+// channels (V = 2), or one channel of rows i and i + 8 (V = 1).  Per step: fold the R rows,
 // put (P, H) into shared memory, one block barrier, run the carried state over the 8 warps.  With
 // S > 1 every block sends its tile's (P, H) into the others' shared memory (st.async, which
-// counts on an mbarrier there), and folds its next tile before it waits for what the others sent
-// for this one; the release of a cluster barrier in that place waited for the output rows still
-// on their way (a quarter of the time).  Every input is read once and every output written
-// once; nothing goes through global memory between the blocks, and the order of the sums
-// depends on the sizes alone.
+// counts on an mbarrier there) and so knows the state before its tile and after the step; the
+// release of a cluster barrier in that place waited for the output rows still on their way (a
+// quarter of the time).  Every input is read once and every output written once; nothing goes
+// through global memory between the blocks, and the order of the sums depends on the sizes
+// alone.
+//
+// Measured (of the measured HBM rate): B1 H16 L65536 d64 fp32 (32 clusters of 8) forward 125 us,
+// 96%, backward 207 us, 97%; B8 H16 L8192 d128 bf16 with sigmoid gates forward 131 us, 92%,
+// backward 313 us, 64%: at 6 and 10 bytes an element and ~20 and ~45 instructions the bf16 cases
+// are bound by instructions as much as by memory, and few heads of them (B2 H12 L16384 d64: 52 us,
+// 44%, and 81 us, 46%) by the latency of a step besides.
 //
 // The inputs of the next steps are on the way while one is folded: each warp copies its own rows
 // into its own ring in shared memory (cp.async, no barrier).
 #include <algorithm>
-#include <type_traits>
+#include <atomic>
 
 #include "layer.cuh"
 #include "tc_ptx.cuh"
@@ -36,10 +42,9 @@ constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the for
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
 constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
-// Rows of a warp: backward, which holds three values a row and channel, 8 with pairs.
-__host__ __device__ constexpr int rec_rows(bool bwd, int V) { return bwd && V == 2 ? 8 : 16; }
-static_assert(rec_rows(true, 2) * REC_W % RC == 0 && RC % rec_rows(false, 1) == 0,
-              "backward tiles and some of the forward's warps start at chunks");
+constexpr int REC_R = 16;                // rows of a warp
+constexpr int REC_TILE = REC_R * REC_W;  // rows of a block's step
+static_assert(REC_TILE % RC == 0 && RC % REC_R == 0, "tiles, and chunks within them, start at a warp's first row");
 
 struct RecArgs {
     const void *x, *g, *dout;
@@ -56,7 +61,6 @@ struct RecArgs {
 };
 
 constexpr uint64_t REC_TIMEOUT_NS = 2000000000ull;  // limit of a wait for another block
-
 
 // 2^x and 1/x by the special function unit: relative error 2^-22 and 2^-23, results below the
 // normal range flushed to 0.
@@ -305,6 +309,51 @@ template <int V> struct __align__(8 * V) Fold {
     Ch<V> p, h;
 };
 
+// What a lane computes in pairs, for the packed instructions: two channels of every row (V = 2), or
+// one channel of rows i and i + R/2 (V = 1), whose two runs are joined afterwards.
+template <int V, int R> struct Pairs {
+    static constexpr int N = V == 2 ? R : R / 2;  // pairs of a warp's rows
+    static constexpr int CW = 32 * V;
+    template <typename T> static __device__ __forceinline__ Ch<2> get(const T *p, int i)
+    {
+        if constexpr (V == 2) return la::get<2>(p + i * CW);
+        else return {{la::get<1>(p + i * CW).v[0], la::get<1>(p + (i + N) * CW).v[0]}};
+    }
+    // row i at p, row i + N at q
+    template <typename T> static __device__ __forceinline__ void put(T *p, T *q, const Ch<2> &x)
+    {
+        if constexpr (V == 2) {
+            la::put<2>(p, x);
+        } else {
+            la::put<1>(p, Ch<1>{{x.v[0]}});
+            la::put<1>(q, Ch<1>{{x.v[1]}});
+        }
+    }
+    // the fold of all rows, the earlier run first
+    static __device__ __forceinline__ Fold<V> join(const Ch<2> &p, const Ch<2> &h)
+    {
+        if constexpr (V == 2) return {p, h};
+        else return {{{p.v[0] * p.v[1]}}, {{fmaf(p.v[1], h.v[0], h.v[1])}}};
+    }
+    // the states before the rows of a pair's runs
+    static __device__ __forceinline__ Ch<2> spread(const Ch<V> &h, const Ch<2> &p, const Ch<2> &f)
+    {
+        if constexpr (V == 2) return h;
+        else return {{h.v[0], fmaf(p.v[0], h.v[0], f.v[0])}};
+    }
+    // the same backwards: the later run comes first
+    static __device__ __forceinline__ Ch<V> join_back(const Ch<2> &p, const Ch<2> &e)
+    {
+        if constexpr (V == 2) return e;
+        else return {{fmaf(p.v[0], e.v[1], e.v[0])}};
+    }
+    static __device__ __forceinline__ Ch<2> spread_back(const Ch<V> &e, const Ch<2> &p, const Ch<2> &f)
+    {
+        if constexpr (V == 2) return e;
+        else return {{fmaf(p.v[1], e.v[0], f.v[1]), e.v[0]}};
+    }
+};
+
 // ---- rows one after the other -----------------------------------------------------------------
 // For the last, partial rows of a sequence and where something is not finite: from the copies in
 // shared memory, in a loop that stays small.
@@ -413,18 +462,13 @@ __device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *
 
 // ---- between the blocks of a cluster -----------------------------------------------------------
 // Sends a fold to `slot` in block `rank` of the cluster, counted there on `bar`.
-template <int V>
-__device__ __forceinline__ void send(const Fold<V> *slot, const uint64_t *bar, int rank, const Fold<V> &f)
+__device__ __forceinline__ void send(const Fold<1> *slot, const uint64_t *bar, int rank, const Fold<1> &f)
 {
     uint32_t to, sig;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(slot)), "r"(rank));
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(sig) : "r"(smem_u32(bar)), "r"(rank));
-    if constexpr (V == 2)
-        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
-                     "f"(f.p.v[0]), "f"(f.p.v[1]), "f"(f.h.v[0]), "f"(f.h.v[1]), "r"(sig) : "memory");
-    else
-        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
-                     "f"(f.p.v[0]), "f"(f.h.v[0]), "r"(sig) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                 "f"(f.p.v[0]), "f"(f.h.v[0]), "r"(sig) : "memory");
 }
 __device__ __forceinline__ void cluster_barrier()
 {
@@ -445,8 +489,8 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity)
 // k + 2, and a block sends that after the block barrier of its step k + 2, which its warps reach
 // when they have read step k.
 constexpr int REC_BUFS = 3;
-template <int V> struct Peers {
-    Fold<V> *slot;  // [REC_BUFS][split][32]
+struct Peers {
+    Fold<1> *slot;  // [REC_BUFS][split][32]
     uint64_t *bar;  // [REC_BUFS]
     int split, rank, *err;
     bool dead;  // a wait ran out: no more waiting
@@ -454,7 +498,7 @@ template <int V> struct Peers {
     __device__ void init(void *mem, int split_, int rank_, int *err_)
     {
         bar = (uint64_t *)mem;
-        slot = (Fold<V> *)((char *)mem + 16 * REC_BUFS);
+        slot = (Fold<1> *)((char *)mem + 16 * REC_BUFS);
         split = split_;
         rank = rank_;
         err = err_;
@@ -465,18 +509,15 @@ template <int V> struct Peers {
         }
         cluster_barrier();  // every block is there, with its barriers, before anyone sends
     }
-    __device__ __forceinline__ void publish(int k, int warp, int lane, const Fold<V> &f)
+    __device__ __forceinline__ void publish(int buf, int warp, int lane, const Fold<1> &f)
     {
-        const int buf = k % REC_BUFS;
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<V>)));
-        for (int r = warp; r < split; r += REC_W) send<V>(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<1>)));
+        for (int r = warp; r < split; r += REC_W) send(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
     }
-    // The carry over the tiles of step k, `carry = P carry + H`: returns the carry before this
+    // The carry over the tiles of a step, `carry = P carry + H`: returns the carry before this
     // block's tile and leaves the one after the step.
-    __device__ __forceinline__ Ch<V> over(int k, int lane, Ch<V> &carry)
+    __device__ __forceinline__ Ch<1> over(int buf, uint32_t parity, int lane, Ch<1> &carry)
     {
-        const int buf = k % REC_BUFS;
-        const uint32_t parity = (k / REC_BUFS) & 1;
         if (!dead && !arrived(&bar[buf], parity)) {
             const uint64_t t0 = globaltimer();
             while (!arrived(&bar[buf], parity))
@@ -486,36 +527,36 @@ template <int V> struct Peers {
                     break;
                 }
         }
-        const Fold<V> *f = slot + buf * split * 32 + lane;
-        const Ch<V> start = carry;
-        Ch<V> mine = carry;
-#pragma unroll 1
+        const Fold<1> *f = slot + buf * split * 32 + lane;
+        const Ch<1> start = carry;
+        Ch<1> mine = carry;
+#pragma unroll 4
         for (int r = 0; r < split; ++r) {
             if (r == rank) mine = carry;
-            carry = fma(f[r * 32].p, carry, f[r * 32].h);
+            const Fold<1> q = f[r * 32];
+            carry = fma(q.p, carry, q.h);
         }
         if (!finite(carry)) {
-            carry = apply_exact<V>(f, 32, split, start);
-            mine = apply_exact<V>(f, 32, rank, start);
+            carry = apply_exact<1>(f, 32, split, start);
+            mine = apply_exact<1>(f, 32, rank, start);
         }
         return mine;
     }
-    static constexpr size_t bytes(int split) { return 16 * REC_BUFS + sizeof(Fold<V>) * REC_BUFS * split * 32; }
+    static constexpr size_t bytes(int split) { return 16 * REC_BUFS + sizeof(Fold<1>) * REC_BUFS * split * 32; }
 };
 
 // Shared memory: the folds of a step for the warps of the tile, in three buffers as well (a warp
 // may be a step ahead of another that still reads), the rings, and what the blocks of the
 // cluster send.
 template <typename T, typename G, int V, bool BWD> struct RecSmem {
-    static constexpr int R = rec_rows(BWD, V);
     static constexpr size_t AGG = sizeof(Fold<V>) * REC_BUFS * REC_W * 32;
     static constexpr size_t AHEAD = BWD ? AGG / 2 : 0;  // backward: H beside (P, E)
-    static constexpr size_t SLOT = (size_t)R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
+    static constexpr size_t SLOT = (size_t)REC_R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
     static constexpr size_t STAGE = REC_W * SLOT;
     // three stages where two blocks share an SM with them (227 KB, 1 KB taken a block), else two
     static constexpr int STAGES = AGG + AHEAD + 3 * STAGE <= 112 * 1024 ? 3 : 2;
     static constexpr size_t PEERS = AGG + AHEAD + STAGES * STAGE;
-    static size_t bytes(int split) { return PEERS + (split > 1 ? Peers<V>::bytes(split) : 0); }
+    static size_t bytes(int split) { return PEERS + (split > 1 ? Peers::bytes(split) : 0); }
 };
 
 // threadIdx.x / 32 as a value that the compiler knows to be the same in the whole warp
@@ -523,10 +564,10 @@ __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, 
 
 // ---- forward ---------------------------------------------------------------------------------
 template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
-__global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a)
+__global__ void __launch_bounds__(REC_THREADS, V == 1 ? 3 : 2) rec_fwd_kernel(const RecArgs a)
 {
     using Sm = RecSmem<T, G, V, false>;
-    constexpr int CW = 32 * V, ST = Sm::STAGES, R = Sm::R, TILE = R * REC_W;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = REC_R, TILE = REC_TILE;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -541,9 +582,6 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
     const int nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
     unsigned char *const ring = smem + Sm::AGG + warp * Sm::SLOT;
     auto first_row = [&](int k) { return (k * split + rank) * TILE + warp * R; };
-    // Steps copied ahead: a slot is kept until its step is finished, with SPLIT one step later.
-    constexpr int AHEAD = SPLIT ? ST - 2 : ST - 1;
-    static_assert(AHEAD > 0, "ring too short");
     int in = 0, at = 0;  // ring slots of the next copy and the next step
     auto load = [&](int k) {
         if (k < steps) {
@@ -560,125 +598,100 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
 #pragma unroll
         for (int v = 0; v < V; ++v) carry.v[v] = a.h0[(size_t)bh * a.d + c + v];
 
-    // gates and what joins the state, for the rows of a step
-    struct Step {
-        Ch<V> a[R], b[R];
-    };
-    auto slot_x = [&](int s) { return (const T *)(ring + s * Sm::STAGE) + lane * V; };
-    auto slot_g = [&](int s) { return (const G *)(ring + s * Sm::STAGE + sizeof(T) * R * CW) + lane * V; };
-    // the rows of step k; their fold goes to the warps of the tile
-    auto fold = [&](int k, Step &s) {
-        cp_wait<AHEAD - 1>();
+    using Pr = Pairs<V, R>;
+    static_assert(!SPLIT || V == 1, "clusters: one channel a lane");
+    Peers peers;
+#pragma unroll
+    for (int k = 0; k < ST - 1; ++k) load(k);
+    if constexpr (SPLIT) peers.init(smem + Sm::PEERS, split, rank, a.err);
+    int buf = 0;
+    uint32_t parity = 0;
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+        cp_wait<ST - 2>();
         __syncwarp();
-        load(k + AHEAD);  // into a slot whose step the whole warp has finished
-        const T *sx = slot_x(at);
-        const G *sg = slot_g(at);
+        load(k + ST - 1);  // into the slot of step k - 1, which the whole warp has finished
+        const T *const sx = (const T *)(ring + at * Sm::STAGE) + lane * V;
+        const G *const sg = (const G *)(ring + at * Sm::STAGE + sizeof(T) * R * CW) + lane * V;
         at = at + 1 == ST ? 0 : at + 1;
-        const int rows = min(n - first_row(k), R);
-        Fold<V> f;
+        const int t0 = first_row(k), rows = min(n - t0, R);
+        // gates and what joins the state; their fold goes to the warps of the tile
+        Ch<2> ga[Pr::N], bx[Pr::N], p, f;
+        Fold<V> own;
         if (rows == R) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const Ch<V> xv = get<V>(sx + i * CW);
-                Ch<V> w;
-                gate_of<KIND, COMP, V>(get<V>(sg + i * CW), s.a[i], w);
-                s.b[i] = COMP ? mul(w, xv) : xv;
+            for (int i = 0; i < Pr::N; ++i) {
+                const Ch<2> xv = Pr::get(sx, i);
+                Ch<2> w;
+                gate_of<KIND, COMP, 2>(Pr::get(sg, i), ga[i], w);
+                bx[i] = COMP ? mul(w, xv) : xv;
             }
-            f.p = s.a[0];
-            f.h = s.b[0];
+            p = ga[0];
+            f = bx[0];
 #pragma unroll
-            for (int i = 1; i < R; ++i) {
-                f.h = fma(s.a[i], f.h, s.b[i]);
-                f.p = mul(f.p, s.a[i]);
+            for (int i = 1; i < Pr::N; ++i) {
+                f = fma(ga[i], f, bx[i]);
+                p = mul(p, ga[i]);
             }
+            own = Pr::join(p, f);
         }
-        if (rows < R || !finite(f.h)) f = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
-        agg[(k % REC_BUFS * REC_W + warp) * 32 + lane] = f;
+        if (rows < R || !finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
+        Fold<V> *const here = agg + buf * REC_W * 32 + lane;
+        here[warp * 32] = own;
         __syncthreads();
-    };
-    // the fold of the tile, for the other blocks
-    auto whole_tile = [&](int k) {
-        const Fold<V> *f = agg + k % REC_BUFS * REC_W * 32 + lane;
-        Fold<V> t = f[0];
+        Ch<V> h = carry;
+        if constexpr (SPLIT) {
+            // the fold of the tile, for the other blocks
+            Fold<V> t = here[0];
 #pragma unroll
-        for (int w = 1; w < REC_W; ++w) {
-            const Fold<V> q = f[w * 32];
-            t.h = fma(q.p, t.h, q.h);
-            t.p = mul(q.p, t.p);
+            for (int w = 1; w < REC_W; ++w) {
+                const Fold<V> q = here[w * 32];
+                t.h = fma(q.p, t.h, q.h);
+                t.p = mul(q.p, t.p);
+            }
+            if (!finite(t.h)) t = join_exact<V>(here, 32, REC_W);
+            peers.publish(buf, warp, lane, t);
+            h = peers.over(buf, parity, lane, carry);
         }
-        if (!finite(t.h)) t = join_exact<V>(f, 32, REC_W);
-        return t;
-    };
-    // h from the state before the tile to that before this warp; returns the one after the tile
-    auto over_warps = [&](int k, Ch<V> &h) {
-        const Fold<V> *f = agg + k % REC_BUFS * REC_W * 32 + lane;
-        const Ch<V> start = h;
-        Ch<V> e = h;
+        {
+            // h from the state before the tile to that before this warp
+            const Ch<V> start = h;
+            Ch<V> e = h;
 #pragma unroll
-        for (int w = 0; w < REC_W; ++w) {
-            if (w == warp) h = e;
-            const Fold<V> q = f[w * 32];
-            e = fma(q.p, e, q.h);
+            for (int w = 0; w < REC_W; ++w) {
+                if (w == warp) h = e;
+                const Fold<V> q = here[w * 32];
+                e = fma(q.p, e, q.h);
+            }
+            if (!finite(e)) {
+                e = apply_exact<V>(here, 32, REC_W, start);
+                h = apply_exact<V>(here, 32, warp, start);
+            }
+            if constexpr (!SPLIT) carry = e;
         }
-        if (!finite(e)) {
-            e = apply_exact<V>(f, 32, REC_W, start);
-            h = apply_exact<V>(f, 32, warp, start);
-        }
-        return e;
-    };
-    // the rows of step k, copied to slot sl, from the state before them
-    auto finish = [&](int k, int sl, const Step &s, const Ch<V> &start) {
-        const int t0 = first_row(k), rows = min(n - t0, R);
         if (a.chunks && t0 % RC == 0 && t0 < a.L && on)
 #pragma unroll
-            for (int v = 0; v < V; ++v) a.chunks[((size_t)bh * nc + t0 / RC) * a.d + c + v] = start.v[v];
+            for (int v = 0; v < V; ++v) a.chunks[((size_t)bh * nc + t0 / RC) * a.d + c + v] = h.v[v];
         T *const o = out + t0 * a.vo.l + lane * V;
-        Ch<V> h = start;
+        bool tame = rows == R;
         if (rows == R) {
-            T *p = o;
+            Ch<2> y = Pr::spread(h, p, f);
+            T *q = o, *q2 = o + Pr::N * a.vo.l;
 #pragma unroll
-            for (int i = 0; i < R; ++i, p += a.vo.l) {
-                h = fma(s.a[i], h, s.b[i]);
-                if (on) put<V>(p, h);
+            for (int i = 0; i < Pr::N; ++i, q += a.vo.l, q2 += a.vo.l) {
+                y = fma(ga[i], y, bx[i]);
+                if (on) Pr::put(q, q2, y);
             }
+            tame = finite(y);
         }
-        if ((rows < R || !finite(h)) && on && t0 < a.L)
-            finish_rows<T, G, KIND, COMP, V>(slot_x(sl), slot_g(sl), rows, min(a.L - t0, R), start, o, a.vo.l);
-    };
-
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) load(k);
-    if constexpr (!SPLIT) {
-        Step s;
-        for (int k = 0; k < steps; ++k) {
-            const int sl = at;
-            fold(k, s);
-            Ch<V> h = carry;
-            carry = over_warps(k, h);
-            finish(k, sl, s, h);
+        if (!tame && on && t0 < a.L)
+            finish_rows<T, G, KIND, COMP, V>(sx, sg, rows, min(a.L - t0, R), h, o, a.vo.l);
+        if (++buf == REC_BUFS) {
+            buf = 0;
+            parity ^= 1;
         }
-    } else {
-        // The next step is folded before what the others sent for this one is waited for.
-        Peers<V> peers;
-        peers.init(smem + Sm::PEERS, split, rank, a.err);
-        Step now, next;
-        int sl = at;
-        fold(0, now);
-        peers.publish(0, warp, lane, whole_tile(0));
-#pragma unroll 1
-        for (int k = 0; k < steps; ++k) {
-            const int sl_next = at;
-            const bool more = k + 1 < steps;
-            if (more) fold(k + 1, next);
-            Ch<V> h = peers.over(k, lane, carry);
-            if (more) peers.publish(k + 1, warp, lane, whole_tile(k + 1));
-            over_warps(k, h);
-            finish(k, sl, now, h);
-            now = next;
-            sl = sl_next;
-        }
-        cluster_barrier();  // nothing is sent to a block that has ended
     }
+    if constexpr (SPLIT) cluster_barrier();  // nothing is sent to a block that has ended
     if (a.h_last && rank == 0 && warp == 0 && on)
 #pragma unroll
         for (int v = 0; v < V; ++v) a.h_last[(size_t)bh * a.d + c + v] = carry.v[v];
@@ -687,11 +700,12 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_fwd_kernel(const RecArgs a
 // ---- backward ----------------------------------------------------------------------------------
 // The tiles from the last to the first.  h before each row is run forward again from the state
 // that the forward left for the tile.
-template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
+template <typename T, typename G, int KIND, bool COMP, bool SPLIT>
 __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a)
 {
+    constexpr int V = 1;
     using Sm = RecSmem<T, G, V, true>;
-    constexpr int CW = 32 * V, ST = Sm::STAGES, R = Sm::R, TILE = R * REC_W;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = REC_R, TILE = REC_TILE;
     constexpr bool WANT_C = COMP || KIND == LA_GATE_SIGMOID;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;            // (P, E) of the warps
@@ -729,8 +743,12 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         for (int v = 0; v < V; ++v) carry.v[v] = a.dh_last[(size_t)bh * a.d + c + v];
 #pragma unroll
     for (int k = 0; k < ST - 1; ++k) load(k);
-    Peers<V> peers;
+    using Pr = Pairs<V, R>;
+    Peers peers;
     if constexpr (SPLIT) peers.init(smem + Sm::PEERS, split, rank, a.err);
+    int buf = 0;
+    uint32_t parity = 0;
+#pragma unroll 1
     for (int k = 0; k < steps; ++k) {
         const int tile = nt - 1 - (k * split + rank), t0 = first_row(k);
         const int rows = tile < 0 ? 0 : min(n - t0, R);
@@ -745,32 +763,33 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         const G *const sg = (const G *)(ring + at * Sm::STAGE + 2 * sizeof(T) * R * CW) + lane * V;
         at = at + 1 == ST ? 0 : at + 1;
         // hb: w x, then the state before the row; cc: 1 - a
-        Ch<V> ga[R], hb[R], cc[R];
-        BwdFold<V> f;
+        Ch<2> ga[Pr::N], hb[Pr::N], cc[Pr::N], p, f, g2;
+        BwdFold<V> own;
         if (rows == R) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const Ch<V> xv = get<V>(sx + i * CW);
-                gate_of<KIND, WANT_C, V>(get<V>(sg + i * CW), ga[i], cc[i]);
+            for (int i = 0; i < Pr::N; ++i) {
+                const Ch<2> xv = Pr::get(sx, i);
+                gate_of<KIND, WANT_C, 2>(Pr::get(sg, i), ga[i], cc[i]);
                 hb[i] = COMP ? mul(cc[i], xv) : xv;
             }
-            f.p = ga[0];
-            f.h = hb[0];
+            p = ga[0];
+            f = hb[0];
 #pragma unroll
-            for (int i = 1; i < R; ++i) {
-                f.h = fma(ga[i], f.h, hb[i]);
-                f.p = mul(f.p, ga[i]);
+            for (int i = 1; i < Pr::N; ++i) {
+                f = fma(ga[i], f, hb[i]);
+                p = mul(p, ga[i]);
             }
-            f.e = mul(ga[R - 1], get<V>(sd + (R - 1) * CW));
+            g2 = mul(ga[Pr::N - 1], Pr::get(sd, Pr::N - 1));
 #pragma unroll
-            for (int i = R - 2; i >= 0; --i) f.e = mul(ga[i], add(f.e, get<V>(sd + i * CW)));
+            for (int i = Pr::N - 2; i >= 0; --i) g2 = mul(ga[i], add(g2, Pr::get(sd, i)));
+            const Fold<V> o = Pr::join(p, f);
+            own = {o.p, o.h, Pr::join_back(p, g2)};
         }
-        if (rows < R || !finite(f.h) || !finite(f.e)) f = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
-        const int buf = k % REC_BUFS;
+        if (rows < R || !finite(own.h) || !finite(own.e)) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
         Fold<V> *const here = agg + buf * REC_W * 32 + lane;
         Ch<V> *const front = ahead + buf * REC_W * 32 + lane;
-        here[warp * 32] = Fold<V>{f.p, f.e};
-        front[warp * 32] = f.h;
+        here[warp * 32] = Fold<V>{own.p, own.e};
+        front[warp * 32] = own.h;
         __syncthreads();
         Ch<V> e = carry;
         if constexpr (SPLIT) {
@@ -782,7 +801,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
                 t.p = mul(q.p, t.p);
             }
             if (!finite(t.h)) t = join_exact<V>(here + (REC_W - 1) * 32, -32, REC_W);
-            peers.publish(k, warp, lane, t);
+            peers.publish(buf, warp, lane, t);
         }
         // h over the warps before this one, e over those behind it
         {
@@ -796,7 +815,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
                 for (int w = 0; w < warp; ++w) h = step(here[w * 32].p, h, front[w * 32]);
             }
         }
-        if constexpr (SPLIT) e = peers.over(k, lane, carry);
+        if constexpr (SPLIT) e = peers.over(buf, parity, lane, carry);
         {
             const Ch<V> start = e;
             Ch<V> t = e;
@@ -814,35 +833,43 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         }
         T *const ox = dx + t0 * a.vdx.l + lane * V;
         G *const og = dg + t0 * a.vdg.l + lane * V;
-        const Ch<V> h0 = h, e0 = e;
         bool tame = rows == R;
         if (rows == R) {
+            Ch<2> y = Pr::spread(h, p, f), z = Pr::spread_back(e, p, g2);
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const Ch<V> bx = hb[i];
-                hb[i] = h;
-                h = fma(ga[i], h, bx);
+            for (int i = 0; i < Pr::N; ++i) {
+                const Ch<2> bx = hb[i];
+                hb[i] = y;
+                y = fma(ga[i], y, bx);
             }
             // while h and e are finite, a slope of 0 makes its product 0 by itself
-            T *px = ox + (R - 1) * a.vdx.l;
-            G *pg = og + (R - 1) * a.vdg.l;
+            T *px = ox + (Pr::N - 1) * a.vdx.l, *px2 = px + Pr::N * a.vdx.l;
+            G *pg = og + (Pr::N - 1) * a.vdg.l, *pg2 = pg + Pr::N * a.vdg.l;
 #pragma unroll
-            for (int i = R - 1; i >= 0; --i, px -= a.vdx.l, pg -= a.vdg.l) {
-                e = add(e, get<V>(sd + i * CW));  // e_t
-                const Ch<V> rx = COMP ? mul(cc[i], e) : e, ae = mul(ga[i], e);
-                Ch<V> q = hb[i];
-                if (COMP) q = fma(get<V>(sx + i * CW), all<V>(-1.f), q);
-                const Ch<V> se = KIND == LA_GATE_VALUE ? e : KIND == LA_GATE_LOG ? ae : mul(cc[i], ae);
+            for (int i = Pr::N - 1; i >= 0; --i) {
+                z = add(z, Pr::get(sd, i));  // e_t
+                const Ch<2> rx = COMP ? mul(cc[i], z) : z, ae = mul(ga[i], z);
+                Ch<2> q = hb[i];
+                if (COMP) q = fma(Pr::get(sx, i), all<2>(-1.f), q);
+                const Ch<2> se = KIND == LA_GATE_VALUE ? z : KIND == LA_GATE_LOG ? ae : mul(cc[i], ae);
                 if (on) {
-                    put<V>(px, rx);
-                    put<V>(pg, mul(se, q));
+                    Pr::put(px, px2, rx);
+                    Pr::put(pg, pg2, mul(se, q));
                 }
-                e = ae;
+                z = ae;
+                px -= a.vdx.l;
+                px2 -= a.vdx.l;
+                pg -= a.vdg.l;
+                pg2 -= a.vdg.l;
             }
-            tame = finite(h) && finite(e);
+            tame = finite(y) && finite(z);
         }
         if (!tame && on && tile >= 0 && t0 < a.L)
-            finish_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows, min(a.L - t0, R), h0, e0, ox, a.vdx.l, og, a.vdg.l);
+            finish_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows, min(a.L - t0, R), h, e, ox, a.vdx.l, og, a.vdg.l);
+        if (++buf == REC_BUFS) {
+            buf = 0;
+            parity ^= 1;
+        }
     }
     if constexpr (SPLIT) cluster_barrier();  // nothing is sent to a block that has ended
     if (a.dh0 && rank == 0 && warp == 0 && on)
@@ -877,8 +904,8 @@ int granule(const void *p, const View &v, const RecArgs &a, size_t elem)
 struct RecKernel {
     const void *fn;
     size_t (*smem)(int split);
-    bool ready[64];
-    int fit[64][REC_MAX_SPLIT + 1];  // clusters of that size on the GPU at once, 0 where not looked up
+    std::atomic<bool> ready[64];
+    std::atomic<int> fit[64][REC_MAX_SPLIT + 1];  // clusters of that size on the GPU at once, 0: not looked up
 
     void config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute &at, int split) const
     {
@@ -906,15 +933,16 @@ struct RecKernel {
     int choose(int dev, long long blocks, long long tiles)
     {
         for (int s = (int)std::min(tiles, (long long)REC_MAX_SPLIT); s > 1; --s) {
-            if (!fit[dev][s]) {
+            int n = fit[dev][s];
+            if (!n) {
                 cudaLaunchConfig_t cfg;
                 cudaLaunchAttribute at;
                 config(cfg, at, s);
                 cfg.gridDim = dim3((unsigned)s);
-                int n = 0;
-                fit[dev][s] = cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0 ? n : -1;
+                if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) n = -1;
+                fit[dev][s] = n;
             }
-            if (fit[dev][s] >= blocks) return s;
+            if (n >= blocks) return s;
         }
         return 1;
     }
@@ -960,47 +988,40 @@ struct LaunchRec {
 
     template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT> static RecKernel &kernel()
     {
-        static RecKernel k = {BWD ? (const void *)rec_bwd_kernel<T, G, KIND, COMP, V, SPLIT>
-                                  : (const void *)rec_fwd_kernel<T, G, KIND, COMP, V, SPLIT && V == 1>,
-                              &RecSmem<T, G, V, BWD>::bytes};
+        const void *fn;
+        if constexpr (BWD) fn = (const void *)rec_bwd_kernel<T, G, KIND, COMP, SPLIT>;
+        else fn = (const void *)rec_fwd_kernel<T, G, KIND, COMP, V, SPLIT>;
+        static RecKernel k{fn, &RecSmem<T, G, V, BWD>::bytes};
         return k;
     }
-    template <typename T, typename G, int KIND, bool COMP, int V> int with() const
+    bool pairs(const void *p, const View &v) const { return rows_aligned(p, v, a.B, a.H, a.L, 2, 4); }
+
+    // Forward, two channels a lane for bf16 (fp32 would leave one block an SM) where they are aligned
+    // together and the blocks of 64 channels alone give every SM one: half the instructions a row
+    // (B8 H16 L8192 d128: 131 us and 174).  Else one channel a lane, for twice the blocks, and
+    // clusters over the rows.
+    template <typename T, typename G, int KIND, bool COMP> int operator()() const
     {
-        constexpr int TILE = REC_W * rec_rows(BWD, V);
-        const long long blocks = (long long)a.B * a.H * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
+        const long long heads = (long long)a.B * a.H;
         a.split = 1;
-        if (blocks <= sms && tiles > 1 && (BWD || V == 1)) {
-            RecKernel &k = kernel<T, G, KIND, COMP, V, true>();
+        if constexpr (!BWD && sizeof(T) + sizeof(G) == 4) {
+            a.ncb = (a.d + 63) / 64;
+            if (a.d % 2 == 0 && a.d > 32 && heads * a.ncb >= sms && pairs(a.x, a.vx) && pairs(a.g, a.vg) &&
+                pairs(a.out, a.vo)) {
+                RecKernel &k = kernel<T, G, KIND, COMP, 2, false>();
+                return k.prepare(dev, false) ? k.launch(a, s) : LA_ERR_CUDA;
+            }
+        }
+        a.ncb = (a.d + 31) / 32;
+        const long long blocks = heads * a.ncb, tiles = ((long long)a.L + REC_TILE - 1) / REC_TILE;
+        if (blocks <= sms && tiles > 1) {
+            RecKernel &k = kernel<T, G, KIND, COMP, 1, true>();
             if (!k.prepare(dev, true)) return LA_ERR_CUDA;
             a.split = k.choose(dev, blocks, tiles);
             if (a.split > 1) return k.launch(a, s);
         }
-        RecKernel &k = kernel<T, G, KIND, COMP, V, false>();
+        RecKernel &k = kernel<T, G, KIND, COMP, 1, false>();
         return k.prepare(dev, false) ? k.launch(a, s) : LA_ERR_CUDA;
-    }
-    template <typename T> bool pairs(const void *p, const View &v) const
-    {
-        return !p || rows_aligned(p, v, a.B, a.H, a.L, sizeof(T), 2 * sizeof(T));
-    }
-    // Two channels a lane for bf16 (pairs of fp32 would leave one block an SM) where pairs are whole
-    // and aligned: forward where the blocks of 64 channels alone give every SM one, because the
-    // split kernel holds two steps in registers; backward, where it holds one, where clusters of
-    // them do.  (B2 H12 L16384 d64 bf16 backward: 91 us with pairs, 114 without; forward B8 H16
-    // L8192 d128: 135 and 174.)
-    template <typename T, typename G, int KIND, bool COMP> int operator()() const
-    {
-        if constexpr (sizeof(T) + sizeof(G) == 4 || (BWD && sizeof(T) == 2)) {
-            constexpr int TILE = REC_W * rec_rows(BWD, 2);
-            a.ncb = (a.d + 63) / 64;
-            const long long blocks = (long long)a.B * a.H * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
-            const long long most = BWD ? std::min(tiles, (long long)REC_MAX_SPLIT) : 1;
-            if (a.d % 2 == 0 && a.d > 32 && blocks * most >= sms && pairs<T>(a.x, a.vx) && pairs<G>(a.g, a.vg) &&
-                pairs<T>(a.out, a.vo) && pairs<T>(a.dout, a.vo) && pairs<T>(a.dx, a.vdx) && pairs<G>(a.dg, a.vdg))
-                return with<T, G, KIND, COMP, 2>();
-        }
-        a.ncb = (a.d + 31) / 32;
-        return with<T, G, KIND, COMP, 1>();
     }
 };
 
