@@ -407,6 +407,16 @@ template <int V> __device__ __noinline__ Ch<V> apply_exact(const Fold<V> *f, int
     for (int i = 0; i < n; ++i) h = step(f[i * stride].p, h, f[i * stride].h);
     return h;
 }
+// The states before the warps of a tile, and the one after it, exactly; step -32 runs backwards.
+template <int V> __device__ __noinline__ Ch<V> begin_exact(Ch<V> *begin, const Fold<V> *f, int stride, Ch<V> h)
+{
+#pragma unroll 1
+    for (int i = 0; i < REC_W; ++i) {
+        begin[i * stride] = h;
+        h = step(f[i * stride].p, h, f[i * stride].h);
+    }
+    return h;
+}
 // n runs in a row as one.
 template <int V> __device__ __noinline__ Fold<V> join_exact(const Fold<V> *f, int stride, int n)
 {
@@ -484,11 +494,10 @@ __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// What the blocks of a cluster send one another: three buffers, each with its mbarrier.  Step k
-// uses buffer k % 3: a block sends for step k + 3 after it has what every block sent for step
-// k + 2, and a block sends that after the block barrier of its step k + 2, which its warps reach
-// when they have read step k.
-constexpr int REC_BUFS = 3;
+// What the blocks of a cluster send one another, read and sent by warp 0 of each: two buffers, each
+// with its mbarrier, used in turn.  A block sends for step k + 2 after it has what every block
+// sent for step k + 1, and a block's warp 0 sends that when it has read step k.
+constexpr int REC_BUFS = 2;
 struct Peers {
     Fold<1> *slot;  // [REC_BUFS][split][32]
     uint64_t *bar;  // [REC_BUFS]
@@ -509,10 +518,10 @@ struct Peers {
         }
         cluster_barrier();  // every block is there, with its barriers, before anyone sends
     }
-    __device__ __forceinline__ void publish(int buf, int warp, int lane, const Fold<1> &f)
+    __device__ __forceinline__ void publish(int buf, int lane, const Fold<1> &f)
     {
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<1>)));
-        for (int r = warp; r < split; r += REC_W) send(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
+        for (int r = 0; r < split; ++r) send(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
     }
     // The carry over the tiles of a step, `carry = P carry + H`: returns the carry before this
     // block's tile and leaves the one after the step.
@@ -545,17 +554,18 @@ struct Peers {
     static constexpr size_t bytes(int split) { return 16 * REC_BUFS + sizeof(Fold<1>) * REC_BUFS * split * 32; }
 };
 
-// Shared memory: the folds of a step for the warps of the tile, in three buffers as well (a warp
-// may be a step ahead of another that still reads), the rings, and what the blocks of the
-// cluster send.
+// Shared memory: the folds of the warps of a tile and the states before each of them, the rings, and
+// what the blocks of the cluster send.  One buffer of each is enough: folds are written before the
+// first block barrier of a step and read, by the warps that run the states over them, before the
+// second, after which the states are read.
 template <typename T, typename G, int V, bool BWD> struct RecSmem {
-    static constexpr size_t AGG = sizeof(Fold<V>) * REC_BUFS * REC_W * 32;
-    static constexpr size_t AHEAD = BWD ? AGG / 2 : 0;  // backward: H beside (P, E)
+    static constexpr size_t AGG = sizeof(Fold<V>) * REC_W * 32, START = sizeof(Ch<V>) * REC_W * 32;
+    static constexpr size_t HEAD = BWD ? AGG + 3 * START : AGG + START;  // backward: H, and both states
     static constexpr size_t SLOT = (size_t)REC_R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
     static constexpr size_t STAGE = REC_W * SLOT;
     // three stages where two blocks share an SM with them (227 KB, 1 KB taken a block), else two
-    static constexpr int STAGES = AGG + AHEAD + 3 * STAGE <= 112 * 1024 ? 3 : 2;
-    static constexpr size_t PEERS = AGG + AHEAD + STAGES * STAGE;
+    static constexpr int STAGES = HEAD + 3 * STAGE <= 112 * 1024 ? 3 : 2;
+    static constexpr size_t PEERS = HEAD + STAGES * STAGE;
     static size_t bytes(int split) { return PEERS + (split > 1 ? Peers::bytes(split) : 0); }
 };
 
@@ -569,7 +579,8 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 ? 3 : 2) rec_fwd_kernel(co
     using Sm = RecSmem<T, G, V, false>;
     constexpr int CW = 32 * V, ST = Sm::STAGES, R = REC_R, TILE = REC_TILE;
     extern __shared__ __align__(16) unsigned char smem[];
-    Fold<V> *const agg = (Fold<V> *)smem;
+    Fold<V> *const agg = (Fold<V> *)smem;            // folds of the warps
+    Ch<V> *const begin = (Ch<V> *)(smem + Sm::AGG);  // states before them
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0, blk = blockIdx.x / split;
     const int bh = blk / a.ncb, c0 = blk % a.ncb * CW, b = bh / a.H, hd = bh % a.H;
@@ -580,7 +591,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 ? 3 : 2) rec_fwd_kernel(co
     T *out = (T *)a.out + row_of(a.vo, b, hd, 0) + c0;
     const int n = rows_of(a, b), nc = (a.L + RC - 1) / RC;
     const int nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
-    unsigned char *const ring = smem + Sm::AGG + warp * Sm::SLOT;
+    unsigned char *const ring = smem + Sm::HEAD + warp * Sm::SLOT;
     auto first_row = [&](int k) { return (k * split + rank) * TILE + warp * R; };
     int in = 0, at = 0;  // ring slots of the next copy and the next step
     auto load = [&](int k) {
@@ -636,39 +647,36 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 ? 3 : 2) rec_fwd_kernel(co
             own = Pr::join(p, f);
         }
         if (rows < R || !finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
-        Fold<V> *const here = agg + buf * REC_W * 32 + lane;
-        here[warp * 32] = own;
+        agg[warp * 32 + lane] = own;
         __syncthreads();
-        Ch<V> h = carry;
-        if constexpr (SPLIT) {
-            // the fold of the tile, for the other blocks
-            Fold<V> t = here[0];
+        if (warp == 0) {
+            const Fold<V> *const f8 = agg + lane;
+            Ch<V> e = carry;
+            if constexpr (SPLIT) {
+                // the fold of the tile, for the other blocks
+                Fold<V> t = f8[0];
 #pragma unroll
-            for (int w = 1; w < REC_W; ++w) {
-                const Fold<V> q = here[w * 32];
-                t.h = fma(q.p, t.h, q.h);
-                t.p = mul(q.p, t.p);
+                for (int w = 1; w < REC_W; ++w) {
+                    const Fold<V> q = f8[w * 32];
+                    t.h = fma(q.p, t.h, q.h);
+                    t.p = mul(q.p, t.p);
+                }
+                if (!finite(t.h)) t = join_exact<V>(f8, 32, REC_W);
+                peers.publish(buf, lane, t);
+                e = peers.over(buf, parity, lane, carry);
             }
-            if (!finite(t.h)) t = join_exact<V>(here, 32, REC_W);
-            peers.publish(buf, warp, lane, t);
-            h = peers.over(buf, parity, lane, carry);
-        }
-        {
-            // h from the state before the tile to that before this warp
-            const Ch<V> start = h;
-            Ch<V> e = h;
+            const Ch<V> start = e;
 #pragma unroll
             for (int w = 0; w < REC_W; ++w) {
-                if (w == warp) h = e;
-                const Fold<V> q = here[w * 32];
+                begin[w * 32 + lane] = e;
+                const Fold<V> q = f8[w * 32];
                 e = fma(q.p, e, q.h);
             }
-            if (!finite(e)) {
-                e = apply_exact<V>(here, 32, REC_W, start);
-                h = apply_exact<V>(here, 32, warp, start);
-            }
+            if (!finite(e)) e = begin_exact<V>(begin + lane, f8, 32, start);
             if constexpr (!SPLIT) carry = e;
         }
+        __syncthreads();
+        const Ch<V> h = begin[warp * 32 + lane];
         if (a.chunks && t0 % RC == 0 && t0 < a.L && on)
 #pragma unroll
             for (int v = 0; v < V; ++v) a.chunks[((size_t)bh * nc + t0 / RC) * a.d + c + v] = h.v[v];
@@ -709,7 +717,8 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
     constexpr bool WANT_C = COMP || KIND == LA_GATE_SIGMOID;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;            // (P, E) of the warps
-    Ch<V> *const ahead = (Ch<V> *)(smem + Sm::AGG);  // their H
+    Ch<V> *const front = (Ch<V> *)(smem + Sm::AGG);  // their H
+    Ch<V> *const begin = front + REC_W * 32, *const behind = begin + REC_W * 32;  // states before, e behind them
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0, blk = blockIdx.x / split;
     const int bh = blk / a.ncb, c0 = blk % a.ncb * CW, b = bh / a.H, hd = bh % a.H;
@@ -722,7 +731,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
     G *dg = (G *)a.dg + row_of(a.vdg, b, hd, 0) + c0;
     const int n = rows_of(a, b), nc = (a.L + RC - 1) / RC;
     const int nt = (a.L + TILE - 1) / TILE, steps = (nt + split - 1) / split;
-    unsigned char *const ring = smem + Sm::AGG + Sm::AHEAD + warp * Sm::SLOT;
+    unsigned char *const ring = smem + Sm::HEAD + warp * Sm::SLOT;
     // a step's tiles run backwards; before the first tile there are none (negative rows)
     auto first_row = [&](int k) { return (nt - 1 - (k * split + rank)) * TILE + warp * R; };
     int in = 0, at = 0;
@@ -752,10 +761,11 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
     for (int k = 0; k < steps; ++k) {
         const int tile = nt - 1 - (k * split + rank), t0 = first_row(k);
         const int rows = tile < 0 ? 0 : min(n - t0, R);
-        Ch<V> h = all<V>(0.f);  // the state before the tile
-        if (on && tile >= 0)
+        Ch<V> before = all<V>(0.f);  // the state before the tile
+        if (warp == 1 && on && tile >= 0)
 #pragma unroll
-            for (int v = 0; v < V; ++v) h.v[v] = a.chunks_in[((size_t)bh * nc + tile * (TILE / RC)) * a.d + c + v];
+            for (int v = 0; v < V; ++v)
+                before.v[v] = a.chunks_in[((size_t)bh * nc + tile * (TILE / RC)) * a.d + c + v];
         cp_wait<ST - 2>();
         __syncwarp();
         load(k + ST - 1);  // into the slot of step k - 1, which the whole warp has finished
@@ -786,51 +796,51 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             own = {o.p, o.h, Pr::join_back(p, g2)};
         }
         if (rows < R || !finite(own.h) || !finite(own.e)) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
-        Fold<V> *const here = agg + buf * REC_W * 32 + lane;
-        Ch<V> *const front = ahead + buf * REC_W * 32 + lane;
-        here[warp * 32] = Fold<V>{own.p, own.e};
-        front[warp * 32] = own.h;
+        agg[warp * 32 + lane] = Fold<V>{own.p, own.e};
+        front[warp * 32 + lane] = own.h;
         __syncthreads();
-        Ch<V> e = carry;
-        if constexpr (SPLIT) {
-            Fold<V> t = here[(REC_W - 1) * 32];
+        const Fold<V> *const f8 = agg + lane;
+        if (warp == 0) {  // e over the warps, the last one first
+            Ch<V> e = carry;
+            if constexpr (SPLIT) {
+                Fold<V> t = f8[(REC_W - 1) * 32];
 #pragma unroll
-            for (int w = REC_W - 2; w >= 0; --w) {
-                const Fold<V> q = here[w * 32];
-                t.h = fma(q.p, t.h, q.h);
-                t.p = mul(q.p, t.p);
+                for (int w = REC_W - 2; w >= 0; --w) {
+                    const Fold<V> q = f8[w * 32];
+                    t.h = fma(q.p, t.h, q.h);
+                    t.p = mul(q.p, t.p);
+                }
+                if (!finite(t.h)) t = join_exact<V>(f8 + (REC_W - 1) * 32, -32, REC_W);
+                peers.publish(buf, lane, t);
+                e = peers.over(buf, parity, lane, carry);
             }
-            if (!finite(t.h)) t = join_exact<V>(here + (REC_W - 1) * 32, -32, REC_W);
-            peers.publish(buf, warp, lane, t);
-        }
-        // h over the warps before this one, e over those behind it
-        {
-            const Ch<V> start = h;
-#pragma unroll
-            for (int w = 0; w < REC_W - 1; ++w)
-                if (w < warp) h = fma(here[w * 32].p, h, front[w * 32]);
-            if (!finite(h)) {
-                h = start;
-#pragma unroll 1
-                for (int w = 0; w < warp; ++w) h = step(here[w * 32].p, h, front[w * 32]);
-            }
-        }
-        if constexpr (SPLIT) e = peers.over(buf, parity, lane, carry);
-        {
             const Ch<V> start = e;
-            Ch<V> t = e;
 #pragma unroll
             for (int w = REC_W - 1; w >= 0; --w) {
-                if (w == warp) e = t;
-                const Fold<V> q = here[w * 32];
-                t = fma(q.p, t, q.h);
+                behind[w * 32 + lane] = e;
+                const Fold<V> q = f8[w * 32];
+                e = fma(q.p, e, q.h);
             }
-            if (!finite(t)) {
-                t = apply_exact<V>(here + (REC_W - 1) * 32, -32, REC_W, start);
-                e = apply_exact<V>(here + (REC_W - 1) * 32, -32, REC_W - 1 - warp, start);
+            if (!finite(e)) e = begin_exact<V>(behind + (REC_W - 1) * 32 + lane, f8 + (REC_W - 1) * 32, -32, start);
+            if constexpr (!SPLIT) carry = e;
+        } else if (warp == 1) {  // h over the warps
+            Ch<V> h = before;
+#pragma unroll
+            for (int w = 0; w < REC_W; ++w) {
+                begin[w * 32 + lane] = h;
+                h = fma(f8[w * 32].p, h, front[w * 32 + lane]);
             }
-            if constexpr (!SPLIT) carry = t;
+            if (!finite(h)) {
+                h = before;
+#pragma unroll 1
+                for (int w = 0; w < REC_W; ++w) {
+                    begin[w * 32 + lane] = h;
+                    h = step(f8[w * 32].p, h, front[w * 32 + lane]);
+                }
+            }
         }
+        __syncthreads();
+        const Ch<V> h = begin[warp * 32 + lane], e = behind[warp * 32 + lane];
         T *const ox = dx + t0 * a.vdx.l + lane * V;
         G *const og = dg + t0 * a.vdg.l + lane * V;
         bool tame = rows == R;
