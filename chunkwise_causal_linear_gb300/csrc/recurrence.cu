@@ -7,22 +7,23 @@
 // c_t = a_t e_t, e_t = dout_t + c_{t+1}: c -> P c + E with the same P.
 //
 // The rows of one head's block of 32 V channels go through one cluster of S blocks (S = 1: one
-// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R = 16 rows,
-// a lane holds V channels of them in registers, as pairs for the packed fp32 instructions: two
-// channels (V = 2), or one channel of rows i and i + 8 (V = 1).  Per step: fold the R rows,
-// put (P, H) into shared memory, one block barrier, run the carried state over the 8 warps.  With
-// S > 1 every block sends its tile's (P, H) into the others' shared memory (st.async, which
-// counts on an mbarrier there) and so knows the state before its tile and after the step; the
-// release of a cluster barrier in that place waited for the output rows still on their way (a
-// quarter of the time).  Every input is read once and every output written once; nothing goes
+// block).  A step of the cluster covers S tiles, one per block; a tile is 8 warps of R rows (16
+// or 32), a lane holds V channels of them in registers, as pairs for the packed fp32 instructions:
+// two channels (V = 2), or one channel of rows i and i + R/2 (V = 1).  Per step: fold the R rows
+// and put (P, H) into shared memory; one warp runs the carried state over the 8 folds while the
+// others wait (when each did it for itself, that was a quarter of all instructions); every warp
+// finishes its rows from its state.  With S > 1 that warp first sends the tile's (P, H) into the
+// other blocks' shared memory (st.async, which counts on an mbarrier there) and so knows the
+// state before the tile and after the step; the release of a cluster barrier in that place waited
+// for the output rows still on their way (a quarter of the time).  Every input is read once and every output written once; nothing goes
 // through global memory between the blocks, and the order of the sums depends on the sizes
 // alone.
 //
-// Measured (of the measured HBM rate): B1 H16 L65536 d64 fp32 (32 clusters of 8) forward 125 us,
-// 96%, backward 207 us, 97%; B8 H16 L8192 d128 bf16 with sigmoid gates forward 131 us, 92%,
-// backward 313 us, 64%: at 6 and 10 bytes an element and ~20 and ~45 instructions the bf16 cases
-// are bound by instructions as much as by memory, and few heads of them (B2 H12 L16384 d64: 52 us,
-// 44%, and 81 us, 46%) by the latency of a step besides.
+// Measured (of the measured HBM rate): B1 H16 L65536 d64 fp32 (32 clusters of 8) forward 126 us,
+// 95%, backward 212 us, 94%; B8 H16 L8192 d128 bf16 with sigmoid gates forward 131 us, 92%,
+// backward 296 us, 68%: at 6 and 10 bytes an element and ~20 and ~50 instructions the bf16 cases
+// are bound by instructions as much as by memory, and few heads of them (B1 H8 L65536 d128: 98 us,
+// 61%, and 180 us, 56%) by the latency of a step besides.
 //
 // The inputs of the next steps are on the way while one is folded: each warp copies its own rows
 // into its own ring in shared memory (cp.async, no barrier).
@@ -42,10 +43,6 @@ constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the for
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
 constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
-constexpr int REC_R = 16;                // rows of a warp
-constexpr int REC_TILE = REC_R * REC_W;  // rows of a block's step
-static_assert(REC_TILE % RC == 0 && RC % REC_R == 0, "tiles, and chunks within them, start at a warp's first row");
-
 struct RecArgs {
     const void *x, *g, *dout;
     void *out, *dx, *dg;
@@ -558,10 +555,15 @@ struct Peers {
 // what the blocks of the cluster send.  One buffer of each is enough: folds are written before the
 // first block barrier of a step and read, by the warps that run the states over them, before the
 // second, after which the states are read.
-template <typename T, typename G, int V, bool BWD> struct RecSmem {
+// The rows of a warp are 16; in a cluster with bf16 activations 32 forward, where a step's fixed part
+// weighs more than the registers (B1 H8 L65536 d128: 98 us and 114; backward would need 96 registers
+// for three values a row).
+template <typename T, typename G, int V, bool BWD, bool SPLIT> struct RecSmem {
+    static constexpr int R = !BWD && SPLIT && sizeof(T) == 2 ? 32 : 16, TILE = R * REC_W;
+    static_assert(TILE % RC == 0 && (RC % R == 0), "tiles, and chunks within them, start at a warp's first row");
     static constexpr size_t AGG = sizeof(Fold<V>) * REC_W * 32, START = sizeof(Ch<V>) * REC_W * 32;
     static constexpr size_t HEAD = BWD ? AGG + 3 * START : AGG + START;  // backward: H, and both states
-    static constexpr size_t SLOT = (size_t)REC_R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
+    static constexpr size_t SLOT = (size_t)R * 32 * V * (sizeof(T) * (BWD ? 2 : 1) + sizeof(G));
     static constexpr size_t STAGE = REC_W * SLOT;
     // three stages where two blocks share an SM with them (227 KB, 1 KB taken a block), else two
     static constexpr int STAGES = HEAD + 3 * STAGE <= 112 * 1024 ? 3 : 2;
@@ -574,10 +576,11 @@ __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, 
 
 // ---- forward ---------------------------------------------------------------------------------
 template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
-__global__ void __launch_bounds__(REC_THREADS, V == 1 ? 3 : 2) rec_fwd_kernel(const RecArgs a)
+__global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false, SPLIT>::R == 16 ? 3 : 2)
+    rec_fwd_kernel(const RecArgs a)
 {
-    using Sm = RecSmem<T, G, V, false>;
-    constexpr int CW = 32 * V, ST = Sm::STAGES, R = REC_R, TILE = REC_TILE;
+    using Sm = RecSmem<T, G, V, false, SPLIT>;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = Sm::R, TILE = Sm::TILE;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;            // folds of the warps
     Ch<V> *const begin = (Ch<V> *)(smem + Sm::AGG);  // states before them
@@ -712,8 +715,8 @@ template <typename T, typename G, int KIND, bool COMP, bool SPLIT>
 __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a)
 {
     constexpr int V = 1;
-    using Sm = RecSmem<T, G, V, true>;
-    constexpr int CW = 32 * V, ST = Sm::STAGES, R = REC_R, TILE = REC_TILE;
+    using Sm = RecSmem<T, G, V, true, SPLIT>;
+    constexpr int CW = 32 * V, ST = Sm::STAGES, R = Sm::R, TILE = Sm::TILE;
     constexpr bool WANT_C = COMP || KIND == LA_GATE_SIGMOID;
     extern __shared__ __align__(16) unsigned char smem[];
     Fold<V> *const agg = (Fold<V> *)smem;            // (P, E) of the warps
@@ -1001,7 +1004,7 @@ struct LaunchRec {
         const void *fn;
         if constexpr (BWD) fn = (const void *)rec_bwd_kernel<T, G, KIND, COMP, SPLIT>;
         else fn = (const void *)rec_fwd_kernel<T, G, KIND, COMP, V, SPLIT>;
-        static RecKernel k{fn, &RecSmem<T, G, V, BWD>::bytes};
+        static RecKernel k{fn, &RecSmem<T, G, V, BWD, SPLIT>::bytes};
         return k;
     }
     bool pairs(const void *p, const View &v) const { return rows_aligned(p, v, a.B, a.H, a.L, 2, 4); }
@@ -1023,7 +1026,8 @@ struct LaunchRec {
             }
         }
         a.ncb = (a.d + 31) / 32;
-        const long long blocks = heads * a.ncb, tiles = ((long long)a.L + REC_TILE - 1) / REC_TILE;
+        constexpr int TILE = RecSmem<T, G, 1, BWD, true>::TILE;
+        const long long blocks = heads * a.ncb, tiles = ((long long)a.L + TILE - 1) / TILE;
         if (blocks <= sms && tiles > 1) {
             RecKernel &k = kernel<T, G, KIND, COMP, 1, true>();
             if (!k.prepare(dev, true)) return LA_ERR_CUDA;
