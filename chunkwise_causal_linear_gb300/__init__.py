@@ -616,13 +616,18 @@ def chunked_fwd_init(q, k, v, state0, zstate0=None, C=64, feature_map="identity"
     return out
 
 
+_dtype_codes = {}
+
+
 def _dtype_code(t):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return LA_BF16
-    if t.dtype == torch.float32:
-        return LA_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        import torch
+        _dtype_codes.update({torch.bfloat16: LA_BF16, torch.float32: LA_F32})
+        code = _dtype_codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 _GENERIC_WARN_TOKENS = 1 << 20
@@ -726,14 +731,16 @@ def _dense(t, shape, name, dtype, device):
     return t.data_ptr()
 
 
-def _launch(what, fn, device, stream, args):
-    """Calls fn(*args, stream) on the tensors' device; raises LAError on a bad status."""
+def _launch(what, device, stream, args):
+    """Calls the library's function `what` (args, stream) on the tensors' device; raises LAError
+    on a bad status."""
     import torch
     if device.type != "cuda":
         raise ValueError(f"{what}: CUDA tensors are needed, got {device}")
+    fn, index = getattr(_lib or lib(), what), device.index
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch.cuda.current_device():
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch._C._cuda_getDevice():
         rc = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -758,7 +765,7 @@ def recurrence_fwd(x, gate, h0=None, gate_kind="sigmoid", complement=False, leng
     chunks = None
     if save_chunks:
         chunks = torch.empty((B, H, -(-L // LA_RECURRENCE_CHUNK), d), dtype=f32, device=dev)
-    _launch("la_recurrence_fwd", lib().la_recurrence_fwd, dev, stream,
+    _launch("la_recurrence_fwd", dev, stream,
             (x.data_ptr(), gate.data_ptr(),
              _dense(h0, (B, H, d), "h0", f32, dev), _dense(lengths, (B,), "lengths", torch.int32, dev),
              out.data_ptr(), last.data_ptr(), _ptr(chunks), B, H, L, d,
@@ -781,7 +788,7 @@ def recurrence_bwd(x, gate, chunk_states, dout, dh_last=None, gate_kind="sigmoid
         dgate = torch.empty(shape, dtype=gate.dtype, device=dev)
     dh0 = torch.empty((B, H, d), dtype=f32, device=dev)
     nc = -(-L // LA_RECURRENCE_CHUNK)
-    _launch("la_recurrence_bwd", lib().la_recurrence_bwd, dev, stream,
+    _launch("la_recurrence_bwd", dev, stream,
             (x.data_ptr(), gate.data_ptr(),
              _dense(chunk_states, (B, H, nc, d), "chunk_states", f32, dev),
              _dense(lengths, (B,), "lengths", torch.int32, dev), dout.data_ptr(),
@@ -802,7 +809,7 @@ def recurrence_step(x, gate, state, gate_kind="sigmoid", complement=False, out=N
     dev = x.device
     if out is None:
         out = torch.empty(shape, dtype=x.dtype, device=dev)
-    _launch("la_recurrence_step", lib().la_recurrence_step, dev, stream,
+    _launch("la_recurrence_step", dev, stream,
             (_dense(x, shape, "x", x.dtype, dev), _dense(gate, shape, "gate", gate.dtype, dev),
              _dense(state, shape, "state", torch.float32, dev),
              _dense(out, shape, "out", x.dtype, dev), B, H, d, GATE_KINDS[gate_kind],
@@ -851,7 +858,7 @@ def rotary(q, k, table, positions=None, offset=0, layout="half", inverse=False, 
             k_out = torch.empty(kshape, dtype=dt, device=dev)
         ks = _view(k, kshape, "k", dt, dev)
         kos = _view(k_out, kshape, "k_out", dt, dev)
-    _launch("la_rotary", lib().la_rotary, dev, stream,
+    _launch("la_rotary", dev, stream,
             (q.data_ptr(), _ptr(k), q_out.data_ptr(),
              _ptr(k_out), _dense(table.turns, (table.rot // 2,), "table", torch.int64, dev),
              _dense(positions, (B, L), "positions", torch.int32, dev), int(offset), B, H, Hk, L, d,
@@ -872,7 +879,7 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="s
     dev, dt, f32 = x.device, x.dtype, torch.float32
     if out is None:
         out = torch.empty(last, dtype=dt, device=dev)
-    _launch("la_group_norm_fwd", lib().la_group_norm_fwd, dev, stream,
+    _launch("la_group_norm_fwd", dev, stream,
             (x.data_ptr(),
              _dense(weight, affine, "weight", f32, dev), _dense(bias, affine, "bias", f32, dev),
              _ptr(gate), out.data_ptr(), B, H, L, d, _view(x, shape, "x", dt, dev),
@@ -894,12 +901,12 @@ def group_norm_bwd(x, dout, weight=None, bias=None, gate=None, eps=1e-5, activat
         dx = torch.empty(shape, dtype=dt, device=dev)
     if gate is not None and dgate is None:
         dgate = torch.empty(last, dtype=dt, device=dev)
-    dw = torch.empty(H * d, dtype=f32, device=dev) if weight is not None else None
-    db = torch.empty(H * d, dtype=f32, device=dev) if bias is not None else None
+    dw = torch.empty(affine, dtype=f32, device=dev) if weight is not None else None
+    db = torch.empty(affine, dtype=f32, device=dev) if bias is not None else None
     need = la_group_norm_bwd_workspace_bytes(B, H, L, d) if dw is not None or db is not None else 0
     if need and (workspace is None or workspace.numel() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch("la_group_norm_bwd", lib().la_group_norm_bwd, dev, stream,
+    _launch("la_group_norm_bwd", dev, stream,
             (x.data_ptr(),
              _dense(weight, affine, "weight", f32, dev), _dense(bias, affine, "bias", f32, dev),
              _ptr(gate), dout.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), B, H, L, d,

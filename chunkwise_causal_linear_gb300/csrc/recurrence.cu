@@ -27,6 +27,8 @@
 //
 // The inputs of the next steps are on the way while one is folded: each warp copies its own rows
 // into its own ring in shared memory (cp.async, no barrier).
+#include <stdlib.h>
+
 #include <algorithm>
 #include <atomic>
 
@@ -55,9 +57,9 @@ struct RecArgs {
     int split;          // blocks of a cluster
     int grx, grg, gro;  // bytes per copy of x, gate, dout: 16, 4 or 2 (their alignment)
     int *err;           // device error word
+    unsigned long long timeout_ns;  // limit of a wait for another block
+    int debug_stall;    // test knob: nothing is sent to the other blocks (forces a timeout)
 };
-
-constexpr uint64_t REC_TIMEOUT_NS = 2000000000ull;  // limit of a wait for another block
 
 // 2^x and 1/x by the special function unit: relative error 2^-22 and 2^-23, results below the
 // normal range flushed to 0.
@@ -499,16 +501,19 @@ struct Peers {
     Fold<1> *slot;  // [REC_BUFS][split][32]
     uint64_t *bar;  // [REC_BUFS]
     int split, rank, *err;
-    bool dead;  // a wait ran out: no more waiting
+    unsigned long long timeout_ns;
+    bool dead, stall;  // a wait ran out: no more waiting; nothing is sent
 
-    __device__ void init(void *mem, int split_, int rank_, int *err_)
+    __device__ void init(void *mem, int rank_, const RecArgs &a)
     {
         bar = (uint64_t *)mem;
         slot = (Fold<1> *)((char *)mem + 16 * REC_BUFS);
-        split = split_;
+        split = a.split;
         rank = rank_;
-        err = err_;
+        err = a.err;
+        timeout_ns = a.timeout_ns;
         dead = false;
+        stall = a.debug_stall != 0;
         if (threadIdx.x == 0) {
             for (int i = 0; i < REC_BUFS; ++i) mbar_init(&bar[i], 1);
             mbar_init_fence();
@@ -518,7 +523,7 @@ struct Peers {
     __device__ __forceinline__ void publish(int buf, int lane, const Fold<1> &f)
     {
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<1>)));
-        for (int r = 0; r < split; ++r) send(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
+        for (int r = 0; r < split && !stall; ++r) send(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
     }
     // The carry over the tiles of a step, `carry = P carry + H`: returns the carry before this
     // block's tile and leaves the one after the step.
@@ -527,7 +532,7 @@ struct Peers {
         if (!dead && !arrived(&bar[buf], parity)) {
             const uint64_t t0 = globaltimer();
             while (!arrived(&bar[buf], parity))
-                if (globaltimer() - t0 > REC_TIMEOUT_NS) {
+                if (globaltimer() - t0 > timeout_ns) {
                     record_error(err, LA_ERR_TIMEOUT);
                     dead = true;
                     break;
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
     Peers peers;
 #pragma unroll
     for (int k = 0; k < ST - 1; ++k) load(k);
-    if constexpr (SPLIT) peers.init(smem + Sm::PEERS, split, rank, a.err);
+    if constexpr (SPLIT) peers.init(smem + Sm::PEERS, rank, a);
     int buf = 0;
     uint32_t parity = 0;
 #pragma unroll 1
@@ -757,7 +762,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
     for (int k = 0; k < ST - 1; ++k) load(k);
     using Pr = Pairs<V, R>;
     Peers peers;
-    if constexpr (SPLIT) peers.init(smem + Sm::PEERS, split, rank, a.err);
+    if constexpr (SPLIT) peers.init(smem + Sm::PEERS, rank, a);
     int buf = 0;
     uint32_t parity = 0;
 #pragma unroll 1
@@ -1039,6 +1044,14 @@ struct LaunchRec {
     }
 };
 
+// The limit of a wait, and the test knob that makes it run out.
+void set_limits(RecArgs &a)
+{
+    const char *e = getenv("LA_DEBUG_TIMEOUT_NS"), *st = getenv("LA_DEBUG_STALL");
+    a.timeout_ns = e && *e ? strtoull(e, nullptr, 10) : 2000000000ull;
+    a.debug_stall = st && *st && *st != '0';
+}
+
 struct LaunchStep {
     const void *x, *g;
     float *state;
@@ -1095,6 +1108,7 @@ int la_recurrence_fwd(const void *x, const void *gate, const float *h0, const in
     const int sms = device_sms();
     int dev = 0;
     a.err = err_ptr();
+    set_limits(a);
     if (sms <= 0 || !a.err || cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
     return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<false>{a, sms, dev, (cudaStream_t)stream});
 }
@@ -1133,6 +1147,7 @@ int la_recurrence_bwd(const void *x, const void *gate, const float *chunk_states
     const int sms = device_sms();
     int dev = 0;
     a.err = err_ptr();
+    set_limits(a);
     if (sms <= 0 || !a.err || cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
     return dispatch(dtype, gate_dtype, gate_kind, complement != 0, LaunchRec<true>{a, sms, dev, (cudaStream_t)stream});
 }

@@ -464,17 +464,22 @@ enum la_gate_kind {
  * a decay per token and channel.  A gate of 0 forgets everything before its row (the first
  * row of a packed document).  States, gates and sums are fp32; out is rounded once.
  *   x, out        [B, H, L, d], dtype `dtype`
- *   gate          [B, H, L, d], dtype `gate_dtype`; gates are meant to be in [0, 1] (others
- *                 are computed as the formula says, products of up to L of them in fp32)
+ *   gate          [B, H, L, d], dtype `gate_dtype`; gates are meant to be in [0, 1].  Others
+ *                 are computed as the formula says, but rows are combined through products of
+ *                 up to 256 gates in fp32: where those overflow, the result is not finite.
  *   h0            device fp32 [B, H, d], the state before row 0, or NULL for zero
  *   lengths       NULL, or device int [B]: sequence b ends after lengths[b] rows (clamped to
  *                 0..L).  Rows behind are not read; out is 0 there and the state stays.
  *   h_last        device fp32 [B, H, d], the state after the last row, or NULL; may be h0
  *   chunk_states  device fp32 [B, H, ceil(L / LA_RECURRENCE_CHUNK), d] or NULL: the states
  *                 before rows 0, 64, 128, ..., which la_recurrence_bwd reads
+ * A gate of 0 (value 0, log or sigmoid of -inf) forgets infinities and NaN too.  Outputs must not
+ * overlap inputs, but for h_last.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED (dtype, gate kind), LA_ERR_ARG
- * (strides) or LA_ERR_CUDA.  Asynchronous on `stream`, no workspace; the sums' order depends
- * on the sizes alone, so equal calls give equal bits.
+ * (strides, alignment) or LA_ERR_CUDA.  Asynchronous on `stream`, no workspace; the sums' order
+ * depends on the sizes and the GPU alone, so equal calls give equal bits.  Where few heads are
+ * cut along L, the blocks of a cluster wait for one another, each wait with a limit:
+ * LA_ERR_TIMEOUT from la_last_device_status.
  */
 int la_recurrence_fwd(const void *x, const void *gate, const float *h0, const int *lengths,
                       void *out, float *h_last, float *chunk_states, int B, int H, int L, int d,
@@ -492,7 +497,8 @@ int la_recurrence_fwd(const void *x, const void *gate, const float *h0, const in
  *   dh_last       device fp32 [B, H, d], the gradient of h_last, or NULL for zero
  *   dx, dgate     [B, H, L, d], dtype `dtype` and `gate_dtype`; fully overwritten, 0 behind a
  *                 sequence's end
- *   dh0           device fp32 [B, H, d] or NULL; may be dh_last
+ *   dh0           device fp32 [B, H, d] or NULL; may be dh_last.  Otherwise outputs must not
+ *                 overlap inputs.
  * Other arguments and errors as la_recurrence_fwd.
  */
 int la_recurrence_bwd(const void *x, const void *gate, const float *chunk_states,

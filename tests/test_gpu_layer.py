@@ -253,6 +253,88 @@ def test_offsets_past_32_bits(la):
     assert torch.equal(res.contiguous(), gx)
 
 
+def test_recurrence_without_the_optional_buffers(la):
+    """No h0, h_last, chunk states, dh_last, dh0: the rest is the same."""
+    import torch
+    rng = np.random.default_rng(17)
+    shape = (2, 1, 700, 64)
+    x, g, do = dev(rng.normal(size=shape), "bf16"), dev(rng.normal(size=shape), "bf16"), dev(rng.normal(size=shape), "bf16")
+    want, _, chunks = la.recurrence_fwd(x, g, save_chunks=True)
+    out = torch.empty_like(x)
+    kinds = (la.LA_GATE_SIGMOID, 0, la.LA_BF16, la.LA_BF16, torch.cuda.current_stream().cuda_stream)
+    p = [t.data_ptr() for t in (x, g, out)]
+    assert la.la_recurrence_fwd(p[0], p[1], None, None, p[2], None, None, *shape, None, None, None, *kinds) == la.LA_OK
+    assert torch.equal(out, want)
+    dx, dg, _ = la.recurrence_bwd(x, g, chunks, do)
+    rx, rg = torch.empty_like(x), torch.empty_like(g)
+    assert la.la_recurrence_bwd(p[0], p[1], chunks.data_ptr(), None, do.data_ptr(), None, rx.data_ptr(), rg.data_ptr(),
+                                None, *shape, None, None, None, None, None, *kinds) == la.LA_OK
+    assert torch.equal(rx, dx) and torch.equal(rg, dg)
+
+
+def test_recurrence_stalled_wait_times_out(la, monkeypatch):
+    """Blocks of a cluster that hear nothing of one another give up, say so, and leave the context
+    as it was."""
+    import time
+
+    import torch
+    rng = np.random.default_rng(18)
+    shape = (1, 1, 2000, 32)
+    x, g = dev(rng.normal(size=shape)), dev(rng.normal(size=shape))
+    stream = torch.cuda.current_stream().cuda_stream
+    want, _, chunks = la.recurrence_fwd(x, g, save_chunks=True)
+    dx = la.recurrence_bwd(x, g, chunks, x)[0]
+    assert la.la_last_device_status(stream) == la.LA_OK
+    monkeypatch.setenv("LA_DEBUG_STALL", "1")
+    monkeypatch.setenv("LA_DEBUG_TIMEOUT_NS", "100000000")  # 0.1 s
+    for call in (lambda: la.recurrence_fwd(x, g), lambda: la.recurrence_bwd(x, g, chunks, x)):
+        t0 = time.time()
+        call()
+        assert la.la_last_device_status(stream) == la.LA_ERR_TIMEOUT
+        assert time.time() - t0 < 20
+        assert la.la_last_device_status(stream) == la.LA_OK
+    monkeypatch.delenv("LA_DEBUG_STALL")
+    monkeypatch.delenv("LA_DEBUG_TIMEOUT_NS")
+    assert torch.equal(la.recurrence_fwd(x, g)[0], want) and torch.equal(la.recurrence_bwd(x, g, chunks, x)[0], dx)
+
+
+FIRST_CALLS = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import chunkwise_causal_linear_gb300 as la
+x = torch.randn(1, 2, 900, 64, device="cuda")
+table = la.rotary_table(64)
+w = torch.ones(128, device="cuda")
+S, _ = la.decode_state(1, 1, 8, 8)  # a call of the library before the capture, none of these operators
+q = torch.randn(1, 1, 8, device="cuda")
+la.decode_step(q, q, q, S)
+torch.cuda.synchronize()
+def step():
+    h, _, chunks = la.recurrence_fwd(x, x, save_chunks=True)
+    y = la.group_norm_fwd(h, w, w)
+    dh = la.group_norm_bwd(h, y, w, w)
+    return h, y, *dh[2:], *la.recurrence_bwd(x, x, chunks, dh[0]), la.rotary(x, None, table)[0]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(held, step()))
+print("captured first")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """The operators' first calls of a process, captured: nothing they set up disturbs the capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
 # ---- rotary positions ------------------------------------------------------------------------
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

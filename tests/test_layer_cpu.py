@@ -108,12 +108,14 @@ def test_group_norm_arguments():
         for eps in (0.0, -1.0, float("nan"), float("inf")):
             assert call(eps=eps) == la.LA_ERR_ARG
         assert call(act=2) == la.LA_ERR_UNSUPPORTED
+        assert call(d=8193) == la.LA_ERR_UNSUPPORTED
         assert call(dtype=2) == la.LA_ERR_UNSUPPORTED
     need = la.la_group_norm_bwd_workspace_bytes(2, 3, 5, 8)
     assert need > 0
     assert gn_bwd(dw=P) == la.LA_ERR_WORKSPACE
     assert gn_bwd(db=P, ws=P, wsb=need - 1) == la.LA_ERR_WORKSPACE
     assert la.la_group_norm_bwd_workspace_bytes(0, 3, 5, 8) == 0
+    assert la.la_group_norm_bwd_workspace_bytes(2, 3, 5, 8193) == 0
 
 
 # (name of a strides argument, is it an output's)
