@@ -166,6 +166,12 @@ __device__ __forceinline__ void gate_of(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
     }
 }
 
+// The gate input of a = 1, 1 - a = 0.
+template <int KIND> __device__ __forceinline__ float keep_gate()
+{
+    return KIND == LA_GATE_VALUE ? 1.f : KIND == LA_GATE_LOG ? 0.f : __int_as_float(0x7f800000);
+}
+
 // The state times a gate (or a product of gates), a gate of 0 forgetting infinities and NaN as
 // well.
 template <int V> __device__ __forceinline__ Ch<V> forget(const Ch<V> &a, const Ch<V> &h)
@@ -230,15 +236,15 @@ __device__ __forceinline__ void copy_by(T *slot, const T *src, long long stride,
         const T *p = src + r0 * stride + c;
         T *q = slot + r0 * ROW + c;
         if constexpr (BYTES == 2) {
-            constexpr int BATCH = M;  // loads on the way at once
+            if (nrow == R) {
+                T v[M];
+#pragma unroll
+                for (int j = 0; j < M; ++j, p += RP * stride) v[j] = *p;
+#pragma unroll
+                for (int j = 0; j < M; ++j) q[j * RP * ROW] = v[j];
+            } else {
 #pragma unroll 1
-            for (int i = 0; i < M; i += BATCH) {
-                T v[BATCH];
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j, p += RP * stride)
-                    if (r0 + (i + j) * RP < nrow) v[j] = *p;
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j, q += RP * ROW) *q = v[j];
+                for (int r = r0; r < nrow; r += RP, p += RP * stride, q += RP * ROW) *q = *p;
             }
         } else {
             const uint32_t dst = (uint32_t)__cvta_generic_to_shared(q);
@@ -248,20 +254,24 @@ __device__ __forceinline__ void copy_by(T *slot, const T *src, long long stride,
         }
     }
 }
-// The rare cases out of the way of the common one, which fits the instruction cache.
+// The rarer cases out of the way of the common one, which fits the instruction cache.  Rows that a
+// sequence does not have are filled with what leaves the state alone.
 template <typename T, int R, int CW>
-__device__ __noinline__ void copy_odd(T *slot, const T *src, long long stride, int nrow, int nch, int gran, int lane)
+__device__ __noinline__ void copy_odd(T *slot, const T *src, long long stride, int nrow, int nch, int gran, int lane,
+                                      float fill)
 {
     if (gran == 16) copy_by<T, R, CW, 16>(slot, src, stride, nrow, nch, lane);
     else if (gran == 4) copy_by<T, R, CW, 4>(slot, src, stride, nrow, nch, lane);
     else if constexpr (sizeof(T) == 2 && CW == 32) copy_by<T, R, CW, 2>(slot, src, stride, nrow, nch, lane);
+    for (int r = nrow; r < R; ++r)
+        for (int c = lane; c < CW; c += 32) slot[r * CW + c] = from_f32<T>(fill);
 }
 template <typename T, int R, int CW>
 __device__ __forceinline__ void copy_rows(T *slot, const T *src, long long stride, int nrow, int nch, int gran,
-                                          int lane)
+                                          int lane, float fill = 0.f)
 {
     if (nrow < R || gran != 16) {
-        if (nrow > 0) copy_odd<T, R, CW>(slot, src, stride, nrow, nch, gran, lane);
+        if (nrow > 0) copy_odd<T, R, CW>(slot, src, stride, nrow, nch, gran, lane, fill);
         return;
     }
     constexpr int E = 16 / sizeof(T), N = CW / E, RP = 32 / N;  // elements a copy, copies a row, rows at once
@@ -354,7 +364,7 @@ template <int V, int R> struct Pairs {
 };
 
 // ---- rows one after the other -----------------------------------------------------------------
-// For the last, partial rows of a sequence and where something is not finite: from the copies in
+// Where a sequence ends among a warp's rows and where something is not finite: from the copies in
 // shared memory, in a loop that stays small.
 template <typename T, typename G, int KIND, bool COMP, int V>
 __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
@@ -607,7 +617,8 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
             const int t0 = first_row(k), rows = min(n - t0, R);
             T *sx = (T *)(ring + in * Sm::STAGE);
             copy_rows<T, R, CW>(sx, x + t0 * a.vx.l, a.vx.l, rows, a.d - c0, a.grx, lane);
-            copy_rows<G, R, CW>((G *)(sx + R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane);
+            copy_rows<G, R, CW>((G *)(sx + R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane,
+                                keep_gate<KIND>());
         }
         cp_commit();
         in = in + 1 == ST ? 0 : in + 1;
@@ -636,8 +647,8 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
         const int t0 = first_row(k), rows = min(n - t0, R);
         // gates and what joins the state; their fold goes to the warps of the tile
         Ch<2> ga[Pr::N], bx[Pr::N], p, f;
-        Fold<V> own;
-        if (rows == R) {
+        Fold<V> own{all<V>(1.f), all<V>(0.f)};
+        if (rows > 0) {
 #pragma unroll
             for (int i = 0; i < Pr::N; ++i) {
                 const Ch<2> xv = Pr::get(sx, i);
@@ -653,8 +664,8 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
                 p = mul(p, ga[i]);
             }
             own = Pr::join(p, f);
+            if (!finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
         }
-        if (rows < R || !finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
         agg[warp * 32 + lane] = own;
         __syncthreads();
         if (warp == 0) {
@@ -749,7 +760,8 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             T *sx = (T *)(ring + in * Sm::STAGE), *sd = sx + R * CW;
             copy_rows<T, R, CW>(sx, x + t0 * a.vx.l, a.vx.l, rows, a.d - c0, a.grx, lane);
             copy_rows<T, R, CW>(sd, dout + t0 * a.vo.l, a.vo.l, rows, a.d - c0, a.gro, lane);
-            copy_rows<G, R, CW>((G *)(sd + R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane);
+            copy_rows<G, R, CW>((G *)(sd + R * CW), g + t0 * a.vg.l, a.vg.l, rows, a.d - c0, a.grg, lane,
+                                keep_gate<KIND>());
         }
         cp_commit();
         in = in + 1 == ST ? 0 : in + 1;
@@ -782,8 +794,8 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
         at = at + 1 == ST ? 0 : at + 1;
         // hb: w x, then the state before the row; cc: 1 - a
         Ch<2> ga[Pr::N], hb[Pr::N], cc[Pr::N], p, f, g2;
-        BwdFold<V> own;
-        if (rows == R) {
+        BwdFold<V> own{all<V>(1.f), all<V>(0.f), all<V>(0.f)};
+        if (rows > 0) {
 #pragma unroll
             for (int i = 0; i < Pr::N; ++i) {
                 const Ch<2> xv = Pr::get(sx, i);
@@ -802,8 +814,8 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             for (int i = Pr::N - 2; i >= 0; --i) g2 = mul(ga[i], add(g2, Pr::get(sd, i)));
             const Fold<V> o = Pr::join(p, f);
             own = {o.p, o.h, Pr::join_back(p, g2)};
+            if (!finite(own.h) || !finite(own.e)) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
         }
-        if (rows < R || !finite(own.h) || !finite(own.e)) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
         agg[warp * 32 + lane] = Fold<V>{own.p, own.e};
         front[warp * 32 + lane] = own.h;
         __syncthreads();
