@@ -687,66 +687,23 @@ def chunked_fwd(q, k, v, C=64, feature_map="identity", omega=None, normalize=Fal
 
 
 # ---- around the attention: recurrence, rotary positions, group norm ---------------------
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+_binding = None
 
 
-def _mismatch(name, t, shape, dtype, device):
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    raise TypeError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+def _layer_binding():
+    """The compiled binding of these operators (raises if it is missing)."""
+    global _binding
+    if _binding is None:
+        import importlib
 
-
-def _view(t, shape, name, dtype, device):
-    """Strides argument of a [B, H, L, d] tensor (None when contiguous)."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        _mismatch(name, t, shape, dtype, device)
-    if t.is_contiguous():
-        return None
-    sb, sh, sl, sd = t.stride()
-    if sd != 1 and shape[3] > 1:
-        raise ValueError(f"{name}: the channels (last axis) must be adjacent")
-    return ctypes.byref(la_strides(sb, sh, sl))
-
-
-def _view_last(t, shape, d, name, dtype, device):
-    """Strides argument of a [B, L, H*d] tensor, channels last (None when contiguous)."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        _mismatch(name, t, shape, dtype, device)
-    if t.is_contiguous():
-        return None
-    sb, sl, sd = t.stride()
-    if sd != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: the channels (last axis) must be adjacent")
-    return ctypes.byref(la_strides(sb, d, sl))
-
-
-def _dense(t, shape, name, dtype, device):
-    """Pointer of a contiguous tensor of that shape and type (None stays None)."""
-    if t is None:
-        return None
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _launch(what, device, stream, args):
-    """Calls the library's function `what` (args, stream) on the tensors' device; raises LAError
-    on a bad status."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError(f"{what}: CUDA tensors are needed, got {device}")
-    fn, index = getattr(_lib or lib(), what), device.index
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    if index == torch._C._cuda_getDevice():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
-    if rc != LA_OK:
-        raise LAError(rc, what)
+        import torch  # noqa: F401  (its libraries, which the binding links)
+        lib()
+        try:
+            _binding = importlib.import_module("._layer", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(_HERE, '_layer.so')} is missing or does not load ({e}); "
+                               "build it with `python -m chunkwise_causal_linear_gb300.build`") from e
+    return _binding
 
 
 def recurrence_fwd(x, gate, h0=None, gate_kind="sigmoid", complement=False, lengths=None,
@@ -756,65 +713,24 @@ def recurrence_fwd(x, gate, h0=None, gate_kind="sigmoid", complement=False, leng
     "sigmoid"; complement: w = 1 - a instead of 1.  h0 [B,H,d] fp32: the state before row 0.
     lengths [B] int32: rows behind a sequence's end are 0 and keep the state.  Returns (out,
     h_last [B,H,d] fp32), with save_chunks also the chunk states that recurrence_bwd reads."""
-    import torch
-    shape = B, H, L, d = x.shape
-    dev, f32 = x.device, torch.float32
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
-    last = torch.empty((B, H, d), dtype=f32, device=dev)
-    chunks = None
-    if save_chunks:
-        chunks = torch.empty((B, H, -(-L // LA_RECURRENCE_CHUNK), d), dtype=f32, device=dev)
-    _launch("la_recurrence_fwd", dev, stream,
-            (x.data_ptr(), gate.data_ptr(),
-             _dense(h0, (B, H, d), "h0", f32, dev), _dense(lengths, (B,), "lengths", torch.int32, dev),
-             out.data_ptr(), last.data_ptr(), _ptr(chunks), B, H, L, d,
-             _view(x, shape, "x", x.dtype, dev), _view(gate, shape, "gate", gate.dtype, dev),
-             _view(out, shape, "out", x.dtype, dev), GATE_KINDS[gate_kind], int(complement),
-             _dtype_code(x), _dtype_code(gate)))
-    return (out, last, chunks) if save_chunks else (out, last)
+    return (_binding or _layer_binding()).recurrence_fwd(x, gate, h0, GATE_KINDS[gate_kind], complement,
+                                                      lengths, save_chunks, out, stream)
 
 
 def recurrence_bwd(x, gate, chunk_states, dout, dh_last=None, gate_kind="sigmoid",
                    complement=False, lengths=None, dx=None, dgate=None, stream=None):
     """(dx, dgate, dh0) of recurrence_fwd(..., save_chunks=True) for dout [B,H,L,d] and dh_last
     [B,H,d] fp32 (None: zero); dh0 [B,H,d] fp32 is the gradient of h0."""
-    import torch
-    shape = B, H, L, d = x.shape
-    dev, f32 = x.device, torch.float32
-    if dx is None:
-        dx = torch.empty(shape, dtype=x.dtype, device=dev)
-    if dgate is None:
-        dgate = torch.empty(shape, dtype=gate.dtype, device=dev)
-    dh0 = torch.empty((B, H, d), dtype=f32, device=dev)
-    nc = -(-L // LA_RECURRENCE_CHUNK)
-    _launch("la_recurrence_bwd", dev, stream,
-            (x.data_ptr(), gate.data_ptr(),
-             _dense(chunk_states, (B, H, nc, d), "chunk_states", f32, dev),
-             _dense(lengths, (B,), "lengths", torch.int32, dev), dout.data_ptr(),
-             _dense(dh_last, (B, H, d), "dh_last", f32, dev), dx.data_ptr(), dgate.data_ptr(),
-             dh0.data_ptr(), B, H, L, d, _view(x, shape, "x", x.dtype, dev),
-             _view(gate, shape, "gate", gate.dtype, dev),
-             _view(dout, shape, "dout", x.dtype, dev), _view(dx, shape, "dx", x.dtype, dev),
-             _view(dgate, shape, "dgate", gate.dtype, dev), GATE_KINDS[gate_kind],
-             int(complement), _dtype_code(x), _dtype_code(gate)))
-    return dx, dgate, dh0
+    return (_binding or _layer_binding()).recurrence_bwd(x, gate, chunk_states, dout, dh_last,
+                                                      GATE_KINDS[gate_kind], complement, lengths, dx,
+                                                      dgate, stream)
 
 
 def recurrence_step(x, gate, state, gate_kind="sigmoid", complement=False, out=None, stream=None):
     """One decoding step of the recurrence: x, gate [B,H,d] (this token), state [B,H,d] fp32
     updated in place.  Returns out [B,H,d]."""
-    import torch
-    shape = B, H, d = x.shape
-    dev = x.device
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=dev)
-    _launch("la_recurrence_step", dev, stream,
-            (_dense(x, shape, "x", x.dtype, dev), _dense(gate, shape, "gate", gate.dtype, dev),
-             _dense(state, shape, "state", torch.float32, dev),
-             _dense(out, shape, "out", x.dtype, dev), B, H, d, GATE_KINDS[gate_kind],
-             int(complement), _dtype_code(x), _dtype_code(gate)))
-    return out
+    return (_binding or _layer_binding()).recurrence_step(x, gate, state, GATE_KINDS[gate_kind],
+                                                       complement, out, stream)
 
 
 class RotaryTable:
@@ -845,27 +761,9 @@ def rotary(q, k, table, positions=None, offset=0, layout="half", inverse=False, 
     positions [B,L] int32, or offset + t.  Strided views are allowed on both sides, and q_out=q,
     k_out=k for in place.  inverse turns back, which is also the gradient.  Returns (q_out,
     k_out)."""
-    import torch
-    shape = B, H, L, d = q.shape
-    dev, dt = q.device, q.dtype
-    if q_out is None:
-        q_out = torch.empty(shape, dtype=dt, device=dev)
-    Hk, ks, kos = 0, None, None
-    if k is not None:
-        Hk = k.shape[1]
-        kshape = (B, Hk, L, d)
-        if k_out is None:
-            k_out = torch.empty(kshape, dtype=dt, device=dev)
-        ks = _view(k, kshape, "k", dt, dev)
-        kos = _view(k_out, kshape, "k_out", dt, dev)
-    _launch("la_rotary", dev, stream,
-            (q.data_ptr(), _ptr(k), q_out.data_ptr(),
-             _ptr(k_out), _dense(table.turns, (table.rot // 2,), "table", torch.int64, dev),
-             _dense(positions, (B, L), "positions", torch.int32, dev), int(offset), B, H, Hk, L, d,
-             table.rot, _view(q, shape, "q", dt, dev), ks,
-             _view(q_out, shape, "q_out", dt, dev), kos, ROTARY_LAYOUTS[layout], int(inverse),
-             table.amplitude, _dtype_code(q)))
-    return q_out, k_out
+    return (_binding or _layer_binding()).rotary(q, k, table.turns, table.rot, table.amplitude, positions,
+                                              offset, ROTARY_LAYOUTS[layout], inverse, q_out, k_out,
+                                              stream)
 
 
 def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="silu", center=True,
@@ -873,47 +771,14 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="s
     """Group norm of x [B,H,L,d] over each head's channels (la_group_norm_fwd), channels last on
     the way out: y = xh weight + bias, out [B,L,H*d] = y act(gate) with gate [B,L,H*d], else
     act(y).  weight, bias: fp32, H*d values, or None; center=False leaves the mean in."""
-    import torch
-    shape = B, H, L, d = x.shape
-    last, affine = (B, L, H * d), (H * d,)
-    dev, dt, f32 = x.device, x.dtype, torch.float32
-    if out is None:
-        out = torch.empty(last, dtype=dt, device=dev)
-    _launch("la_group_norm_fwd", dev, stream,
-            (x.data_ptr(),
-             _dense(weight, affine, "weight", f32, dev), _dense(bias, affine, "bias", f32, dev),
-             _ptr(gate), out.data_ptr(), B, H, L, d, _view(x, shape, "x", dt, dev),
-             None if gate is None else _view_last(gate, last, d, "gate", dt, dev),
-             _view_last(out, last, d, "out", dt, dev), int(center), ACTIVATIONS[activation],
-             float(eps), _dtype_code(x)))
-    return out
+    return (_binding or _layer_binding()).group_norm_fwd(x, weight, bias, gate, eps, ACTIVATIONS[activation],
+                                                      center, out, stream)
 
 
 def group_norm_bwd(x, dout, weight=None, bias=None, gate=None, eps=1e-5, activation="silu",
                    center=True, dx=None, dgate=None, workspace=None, stream=None):
     """(dx, dgate, dweight, dbias) of group_norm_fwd for dout [B,L,H*d]; None where the forward
     had None."""
-    import torch
-    shape = B, H, L, d = x.shape
-    last, affine = (B, L, H * d), (H * d,)
-    dev, dt, f32 = x.device, x.dtype, torch.float32
-    if dx is None:
-        dx = torch.empty(shape, dtype=dt, device=dev)
-    if gate is not None and dgate is None:
-        dgate = torch.empty(last, dtype=dt, device=dev)
-    dw = torch.empty(affine, dtype=f32, device=dev) if weight is not None else None
-    db = torch.empty(affine, dtype=f32, device=dev) if bias is not None else None
-    need = la_group_norm_bwd_workspace_bytes(B, H, L, d) if dw is not None or db is not None else 0
-    if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch("la_group_norm_bwd", dev, stream,
-            (x.data_ptr(),
-             _dense(weight, affine, "weight", f32, dev), _dense(bias, affine, "bias", f32, dev),
-             _ptr(gate), dout.data_ptr(), dx.data_ptr(), _ptr(dgate), _ptr(dw), _ptr(db), B, H, L, d,
-             _view(x, shape, "x", dt, dev),
-             None if gate is None else _view_last(gate, last, d, "gate", dt, dev),
-             _view_last(dout, last, d, "dout", dt, dev), _view(dx, shape, "dx", dt, dev),
-             None if gate is None else _view_last(dgate, last, d, "dgate", dt, dev), int(center),
-             ACTIVATIONS[activation], float(eps), _dtype_code(x), workspace.data_ptr() if need else None,
-             need))
-    return dx, dgate, dw, db
+    return (_binding or _layer_binding()).group_norm_bwd(x, dout, weight, bias, gate, eps,
+                                                      ACTIVATIONS[activation], center, dx, dgate,
+                                                      workspace, stream)
