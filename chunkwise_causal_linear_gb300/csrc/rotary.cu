@@ -6,8 +6,8 @@
 // product p * theta would be off by a radian at p ~ 2^24.
 //
 // Bound by memory: every element is read and written once.  A thread holds the sines and cosines
-// of VEC pairs (16-byte vectors) of one token and goes over up to 8 heads with them; the first
-// heads' loads are on the way while the sines (~45 instructions a pair) are computed.
+// of VEC pairs (16-byte vectors) of one token and goes over up to 8 heads of q and k with them;
+// the first heads' loads are on the way while the sines (~30 instructions a pair) are computed.
 #include <math.h>
 
 #include <algorithm>
@@ -32,17 +32,25 @@ struct RotArgs {
     int B, H, Hk, L, d, rot;
     int layout, inverse;
     float amp;
-    int heads, qgroups;  // heads of a thread, groups of them in q
+    int heads;  // heads of a thread, q's first, then k's
 };
 
-// Sine and cosine of 2 pi f / 2^64.  The nearest quarter turn is taken off in integers; what is
-// left, at most an eighth of a turn, is exact to an fp32 rounding.
+// Sine and cosine of 2 pi f / 2^64, f rounded to 32 bits of a turn.  The nearest quarter turn is
+// taken off in integers; what is left, x at most an eighth of a turn, is exact to an fp32
+// rounding, and the series of sine and cosine to x^9 and x^10 are off by less than 2e-9 there.
 __device__ __forceinline__ void turn_sincos(unsigned long long f, float &s, float &c)
 {
-    const unsigned q = (unsigned)((f + (1ull << 61)) >> 62);
-    const long long r = (long long)(f - ((unsigned long long)q << 62));
-    float sr, cr;
-    sincospif((float)r * 0x1p-63f, &sr, &cr);
+    const unsigned hi = (unsigned)((f + 0x80000000ull) >> 32), q = (hi + (1u << 29)) >> 30;
+    const float x = (float)(int)(hi - (q << 30)) * (float)(6.283185307179586 / 4294967296.0), z = x * x;
+    float p = fmaf(z, 1.f / 362880, -1.f / 5040);
+    p = fmaf(z, p, 1.f / 120);
+    p = fmaf(z, p, -1.f / 6);
+    const float sr = fmaf(x * z, p, x);
+    float r = fmaf(z, -1.f / 3628800, 1.f / 40320);
+    r = fmaf(z, r, -1.f / 720);
+    r = fmaf(z, r, 1.f / 24);
+    r = fmaf(z, r, -0.5f);
+    const float cr = fmaf(z, r, 1.f);
     s = (q & 1) ? cr : sr;
     c = (q & 1) ? sr : cr;
     if (q & 2) s = -s;
@@ -52,6 +60,27 @@ __device__ __forceinline__ void turn_sincos(unsigned long long f, float &s, floa
 // VEC neighbouring elements as they are stored
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Vec {
     T v[VEC];
+};
+
+// The rows of a token head by head, q's and then k's.
+template <typename T> struct HeadRows {
+    T *p, *k;
+    long long step, kstep;
+    int left;  // heads of q still to come
+    __device__ HeadRows(const void *q, const View &vq, const void *k_, const View &vk, int H, int b, int t, int h)
+        : k((T *)k_ + row_of(vk, b, 0, t)), kstep(vk.h), left(H - h)
+    {
+        p = left > 0 ? (T *)q + row_of(vq, b, h, t) : k + (h - H) * kstep;
+        step = left > 0 ? vq.h : kstep;
+    }
+    __device__ __forceinline__ void next()
+    {
+        p += step;
+        if (--left == 0) {
+            p = k;
+            step = kstep;
+        }
+    }
 };
 
 // Unit u of a token: VEC pairs of the rotated channels, or two vectors of the copied ones.
@@ -74,11 +103,10 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
         b = (int)(row / (unsigned)a.L);
         t = (int)(row - (unsigned)b * a.L);
     }
-    const bool isq = (int)blockIdx.y < a.qgroups, pair = u < pair_units;
-    const int h0 = (isq ? blockIdx.y : blockIdx.y - a.qgroups) * a.heads, h1 = min(h0 + a.heads, isq ? a.H : a.Hk);
-    const View &vi = isq ? a.vq : a.vk, &vo = isq ? a.vqo : a.vko;
-    const T *in = (const T *)(isq ? a.q : a.k) + row_of(vi, b, h0, t);
-    T *out = (T *)(isq ? a.qo : a.ko) + row_of(vo, b, h0, t);
+    const bool pair = u < pair_units;
+    const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.H + a.Hk);
+    HeadRows<const T> in(a.q, a.vq, a.k, a.vk, a.H, b, t, h0);
+    HeadRows<T> out(a.qo, a.vqo, a.ko, a.vko, a.H, b, t, h0);
     const bool half = a.layout == LA_ROTARY_HALF;
     int c0, c1;  // the unit's two vectors
     bool two = true;
@@ -96,10 +124,10 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
 #pragma unroll
         for (int j = 0; j < ROT_AT_ONCE; ++j)
             if (h + j < h1) {
-                x[j] = *(const V *)(in + j * vi.h + c0);
-                y[j] = *(const V *)(in + j * vi.h + c1);
+                x[j] = *(const V *)(in.p + c0);
+                y[j] = *(const V *)(in.p + c1);
+                in.next();
             }
-        in += ROT_AT_ONCE * vi.h;
     };
     fetch(h0);
     float s[VEC], c[VEC];
@@ -141,10 +169,10 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
                         }
                     }
                 }
-                *(V *)(out + j * vo.h + c0) = x[j];
-                if (two) *(V *)(out + j * vo.h + c1) = y[j];
+                *(V *)(out.p + c0) = x[j];
+                if (two) *(V *)(out.p + c1) = y[j];
+                out.next();
             }
-        out += ROT_AT_ONCE * vo.h;
     }
 }
 
@@ -155,13 +183,12 @@ template <typename T, int VEC> int launch_rotary(RotArgs &a, int sms, cudaStream
     if (blocks > INT_MAX) return LA_ERR_SHAPE;
     // heads of a thread: at most ROT_HEADS, in even groups, and as many as still leave every SM eight
     // blocks
-    const int most = std::max(a.H, a.Hk), even = (most + ROT_HEADS - 1) / ROT_HEADS;
-    a.heads = (most + even - 1) / even;
-    auto groups = [&](int n) { return (n + a.heads - 1) / a.heads; };
-    while (a.heads > 1 && blocks * (groups(a.H) + groups(a.Hk)) < 8ll * sms) a.heads = (a.heads + 1) / 2;
-    while ((long long)groups(a.H) + groups(a.Hk) > 65535) a.heads *= 2;  // limit of the grid
-    a.qgroups = groups(a.H);
-    const int ny = a.qgroups + groups(a.Hk);
+    const int all = a.H + a.Hk, even = (all + ROT_HEADS - 1) / ROT_HEADS;
+    a.heads = (all + even - 1) / even;
+    auto groups = [&] { return (all + a.heads - 1) / a.heads; };
+    while (a.heads > 1 && blocks * groups() < 8ll * sms) a.heads = (a.heads + 1) / 2;
+    while (groups() > 65535) a.heads *= 2;  // limit of the grid
+    const int ny = groups();
     rotary_kernel<T, VEC><<<dim3((unsigned)blocks, (unsigned)ny), ROT_THREADS, 0, s>>>(a);
     return cudaPeekAtLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
