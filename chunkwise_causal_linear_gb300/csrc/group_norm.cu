@@ -32,59 +32,52 @@ struct GnArgs {
     int nb;  // blocks of a head
 };
 
-// ---- VEC neighbouring channels ----------------------------------------------------------------
-template <int VEC> __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&f)[VEC])
+// ---- VEC neighbouring channels, in pairs -------------------------------------------------------
+template <int VEC> constexpr int WIDTH = VEC > 1 ? 2 : 1;
+template <int VEC> using Vec = Ch<WIDTH<VEC>>;  // [VEC / WIDTH] of them hold VEC channels
+
+template <int VEC> __device__ __forceinline__ void load(const __nv_bfloat16 *p, Vec<VEC> *f)
 {
     if constexpr (VEC == 8) {
         const uint4 t = *(const uint4 *)p;
         const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = tcc::bf_lo(w[i]);
-            f[2 * i + 1] = tcc::bf_hi(w[i]);
-        }
+        for (int i = 0; i < 4; ++i) f[i] = {{tcc::bf_lo(w[i]), tcc::bf_hi(w[i])}};
     } else if constexpr (VEC == 2) {
-        const uint32_t t = *(const uint32_t *)p;
-        f[0] = tcc::bf_lo(t);
-        f[1] = tcc::bf_hi(t);
+        const uint32_t w = *(const uint32_t *)p;
+        f[0].v[0] = tcc::bf_lo(w);
+        f[0].v[1] = tcc::bf_hi(w);
     } else {
-        f[0] = __bfloat162float(*p);
+        f[0].v[0] = __bfloat162float(*p);
     }
 }
-template <int VEC> __device__ __forceinline__ void load(const float *p, float (&f)[VEC])
+template <int VEC> __device__ __forceinline__ void load(const float *p, Vec<VEC> *f)
 {
-    if constexpr (VEC % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            const float4 t = ((const float4 *)p)[i];
-            f[4 * i] = t.x;
-            f[4 * i + 1] = t.y;
-            f[4 * i + 2] = t.z;
-            f[4 * i + 3] = t.w;
-        }
+    if constexpr (VEC == 4) {
+        const float4 w = *(const float4 *)p;
+        f[0].v[0] = w.x;
+        f[0].v[1] = w.y;
+        f[1].v[0] = w.z;
+        f[1].v[1] = w.w;
     } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] = p[i];
+        f[0].v[0] = *p;
     }
 }
-__device__ __forceinline__ uint32_t bf_pair(float a, float b)
+__device__ __forceinline__ uint32_t bf_pair(const Ch<2> &f)
 {
-    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 t = __floats2bfloat162_rn(f.v[0], f.v[1]);
     return *(const uint32_t *)&t;
 }
-template <int VEC> __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[VEC])
+template <int VEC> __device__ __forceinline__ void store(__nv_bfloat16 *p, const Vec<VEC> *f)
 {
-    if constexpr (VEC == 8)
-        *(uint4 *)p = make_uint4(bf_pair(f[0], f[1]), bf_pair(f[2], f[3]), bf_pair(f[4], f[5]), bf_pair(f[6], f[7]));
-    else if constexpr (VEC == 2)
-        *(uint32_t *)p = bf_pair(f[0], f[1]);
-    else
-        *p = __float2bfloat16_rn(f[0]);
+    if constexpr (VEC == 8) *(uint4 *)p = make_uint4(bf_pair(f[0]), bf_pair(f[1]), bf_pair(f[2]), bf_pair(f[3]));
+    else if constexpr (VEC == 2) *(uint32_t *)p = bf_pair(f[0]);
+    else *p = __float2bfloat16_rn(f[0].v[0]);
 }
-template <int VEC> __device__ __forceinline__ void store(float *p, const float (&f)[VEC])
+template <int VEC> __device__ __forceinline__ void store(float *p, const Vec<VEC> *f)
 {
-    if constexpr (VEC == 4) *(float4 *)p = make_float4(f[0], f[1], f[2], f[3]);
-    else *p = f[0];
+    if constexpr (VEC == 4) *(float4 *)p = make_float4(f[0].v[0], f[0].v[1], f[1].v[0], f[1].v[1]);
+    else *p = f[0].v[0];
 }
 
 // ---- sums over the threads of a group, the same in every one of them ---------------------------
@@ -112,12 +105,15 @@ template <int TPG, int N> __device__ __forceinline__ void group_sum(float (&v)[N
 }
 
 // 1 / (1 + e^-z), off by at most (7 + 2.5 |z|) 2^-24 relatively; 0 where e^-z leaves the range.
-__device__ __forceinline__ float sigmoid(float z)
+template <int W> __device__ __forceinline__ Ch<W> sigmoid(const Ch<W> &z)
 {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+    Ch<W> e = mul(z, all<W>(-1.44269504f));
+#pragma unroll
+    for (int i = 0; i < W; ++i) e.v[i] = ex2(e.v[i]);
+    e = add(e, all<W>(1.f));
+#pragma unroll
+    for (int i = 0; i < W; ++i) e.v[i] = rcp(e.v[i]);
+    return e;
 }
 
 // The tokens of a block's group of threads, r = first, first + step, ..., and where a tensor's rows
@@ -154,7 +150,8 @@ template <typename T> struct Rows {
 };
 
 template <int VEC, int NV> struct Group {
-    float v[NV][VEC];
+    static constexpr int W = WIDTH<VEC>, N = VEC / W;
+    Vec<VEC> v[NV][N];
 };
 template <typename T, int VEC, int TPG, int NV>
 __device__ __forceinline__ void write(const Group<VEC, NV> &g, T *p, int lane, int d)
@@ -211,7 +208,7 @@ template <typename T, int VEC, int TPG, int NV, int ARRAYS, int BLOCKS> struct R
                 load<VEC>(p, g.v[i]);
             } else {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) g.v[i][e] = 0.f;
+                for (int e = 0; e < Group<VEC, NV>::N; ++e) g.v[i][e] = all<WIDTH<VEC>>(0.f);
             }
         }
     }
@@ -227,7 +224,7 @@ __device__ __forceinline__ void read(Group<VEC, NV> &g, const T *p, int lane, in
             load<VEC>(p + c, g.v[i]);
         } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) g.v[i][e] = 0.f;
+            for (int e = 0; e < Group<VEC, NV>::N; ++e) g.v[i][e] = all<WIDTH<VEC>>(0.f);
         }
     }
 }
@@ -283,41 +280,51 @@ template <typename T, int VEC, int TPG, int NV, int ARRAYS, int BLOCKS> struct S
     }
 };
 
+template <int W> __device__ __forceinline__ float total(const Ch<W> &c)
+{
+    if constexpr (W == 2) return c.v[0] + c.v[1];
+    else return c.v[0];
+}
+
 // x -> xh in place; returns rstd.  Channels past d count as nothing.
 template <int VEC, int TPG, int NV>
 __device__ __forceinline__ float normalise(Group<VEC, NV> &x, const GnArgs &a, int lane, float *sm)
 {
+    constexpr int W = Group<VEC, NV>::W, N = Group<VEC, NV>::N;
     if (a.center) {
-        float s[1] = {0.f};
+        Ch<W> c = all<W>(0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s[0] += x.v[i][e];
+            for (int e = 0; e < N; ++e) c = add(c, x.v[i][e]);
+        float s[1] = {total(c)};
         group_sum<TPG>(s, sm);
-        const float mean = s[0] * a.inv_d;
+        const Ch<W> mean = all<W>(-s[0] * a.inv_d);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if ((i * TPG + lane) * VEC < a.d)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) x.v[i][e] -= mean;
+                for (int e = 0; e < N; ++e) x.v[i][e] = add(x.v[i][e], mean);
     }
-    float q[1] = {0.f};
+    Ch<W> c = all<W>(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) q[0] = fmaf(x.v[i][e], x.v[i][e], q[0]);
+        for (int e = 0; e < N; ++e) c = fma(x.v[i][e], x.v[i][e], c);
+    float q[1] = {total(c)};
     group_sum<TPG>(q, sm);
     const float rstd = rsqrtf(fmaf(q[0], a.inv_d, a.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x.v[i][e] *= rstd;
+        for (int e = 0; e < N; ++e) x.v[i][e] = mul(x.v[i][e], all<W>(rstd));
     return rstd;
 }
 
 // Weight and bias of the block's head: in registers where they are few, else read again.
 template <int VEC, int TPG, int NV> struct Affine {
     static constexpr bool KEEP = NV * VEC <= 8;
+    static constexpr int W = WIDTH<VEC>;
     Group<VEC, KEEP ? NV : 1> w_, b_;
     const float *w, *b;
     int lane, d;
@@ -327,27 +334,26 @@ template <int VEC, int TPG, int NV> struct Affine {
         b = a.b ? a.b + (size_t)h * d : nullptr;
         if constexpr (KEEP)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) get(i, w_.v[i], b_.v[i]);
-    }
-    __device__ __forceinline__ void get(int i, float (&wv)[VEC], float (&bv)[VEC]) const
-    {
-        const int c = (i * TPG + lane) * VEC;
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            wv[e] = w && c + e < d ? w[c + e] : 1.f;
-            bv[e] = b && c + e < d ? b[c + e] : 0.f;
+                for (int e = 0; e < VEC / W; ++e) get(i, e, w_.v[i][e], b_.v[i][e]);
+    }
+    __device__ __forceinline__ void get(int i, int e, Ch<W> &wv, Ch<W> &bv) const
+    {
+        const int c = (i * TPG + lane) * VEC + e * W;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            wv.v[j] = w && c + j < d ? w[c + j] : 1.f;
+            bv.v[j] = b && c + j < d ? b[c + j] : 0.f;
         }
     }
-    __device__ __forceinline__ void at(int i, float (&wv)[VEC], float (&bv)[VEC]) const
+    __device__ __forceinline__ void at(int i, int e, Ch<W> &wv, Ch<W> &bv) const
     {
         if constexpr (KEEP) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                wv[e] = w_.v[i][e];
-                bv[e] = b_.v[i][e];
-            }
+            wv = w_.v[i][e];
+            bv = b_.v[i][e];
         } else {
-            get(i, wv, bv);
+            get(i, e, wv, bv);
         }
     }
 };
@@ -364,7 +370,7 @@ using SourceOf = Source<T, VEC, TPG, NV, (BWD ? 2 : 1) + GATE, blocks_per_sm<VEC
 template <typename T, int VEC, int TPG, int NV, bool GATE, bool SILU>
 __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(false)) gn_fwd_kernel(const GnArgs a)
 {
-    constexpr int GPB = GN_THREADS / TPG;
+    constexpr int GPB = GN_THREADS / TPG, W = WIDTH<VEC>, N = VEC / W;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float sm[GN_THREADS / 32];
     const int lane = threadIdx.x % TPG, group = threadIdx.x / TPG;
@@ -383,16 +389,15 @@ __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(false)) gn_
         src.next(in, on);
         normalise<VEC, TPG, NV>(x, a, lane, sm);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float w[VEC], b[VEC];
-            aff.at(i, w, b);
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float y = fmaf(x.v[i][e], w[e], b[e]), g = GATE ? z.v[i][e] : y;
-                const float f = SILU ? g * sigmoid(g) : g;
-                x.v[i][e] = GATE ? y * f : f;
+            for (int e = 0; e < N; ++e) {
+                Ch<W> w, b;
+                aff.at(i, e, w, b);
+                const Ch<W> y = fma(x.v[i][e], w, b), g = GATE ? z.v[i][e] : y;
+                const Ch<W> f = SILU ? mul(g, sigmoid(g)) : g;
+                x.v[i][e] = GATE ? mul(y, f) : f;
             }
-        }
         if (on) write<T, VEC, TPG, NV>(x, po.p, lane, a.d);
         at.next();
         po.next(at);
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(false)) gn_
 template <typename T, int VEC, int TPG, int NV, bool GATE, bool SILU>
 __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(true)) gn_bwd_kernel(const GnArgs a)
 {
-    constexpr int GPB = GN_THREADS / TPG;
+    constexpr int GPB = GN_THREADS / TPG, W = WIDTH<VEC>, N = VEC / W;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ float sm[2 * GN_THREADS / 32];
     const int lane = threadIdx.x % TPG, group = threadIdx.x / TPG;
@@ -420,42 +425,44 @@ __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(true)) gn_b
         const bool on = at.b < a.B;
         src.next(in, on);
         const float rstd = normalise<VEC, TPG, NV>(x, a, lane, sm);
-        float s[2] = {0.f, 0.f};  // sums of dy w and of dy w xh
+        Ch<W> s0 = all<W>(0.f), s1 = s0;  // sums of dy w and of dy w xh
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float w[VEC], b[VEC];
-            aff.at(i, w, b);
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float xh = x.v[i][e], y = fmaf(xh, w[e], b[e]), g = GATE ? z.v[i][e] : y;
-                float f = g, slope = 1.f;
+            for (int e = 0; e < N; ++e) {
+                Ch<W> w, b;
+                aff.at(i, e, w, b);
+                const Ch<W> xh = x.v[i][e], y = fma(xh, w, b), g = GATE ? z.v[i][e] : y;
+                Ch<W> f = g, slope = all<W>(1.f);
                 if (SILU) {
-                    const float sg = sigmoid(g);
-                    f = g * sg;
-                    slope = fmaf(f, 1.f - sg, sg);  // sg (1 + g (1 - sg))
+                    const Ch<W> sg = sigmoid(g);
+                    f = mul(g, sg);
+                    slope = fma(f, fma(sg, all<W>(-1.f), all<W>(1.f)), sg);  // sg (1 + g (1 - sg))
                 }
-                float dy = o.v[i][e];
+                Ch<W> dy = o.v[i][e];
                 if (GATE) {
-                    z.v[i][e] = dy * y * slope;  // dgate
-                    dy *= f;
+                    z.v[i][e] = mul(mul(dy, y), slope);  // dgate
+                    dy = mul(dy, f);
                 } else {
-                    dy *= slope;
+                    dy = mul(dy, slope);
                 }
-                dw.v[i][e] = fmaf(dy, xh, dw.v[i][e]);
-                db.v[i][e] += dy;
-                dy *= w[e];
+                dw.v[i][e] = fma(dy, xh, dw.v[i][e]);
+                db.v[i][e] = add(db.v[i][e], dy);
+                dy = mul(dy, w);
                 o.v[i][e] = dy;
-                s[0] += dy;
-                s[1] = fmaf(dy, xh, s[1]);
+                s0 = add(s0, dy);
+                s1 = fma(dy, xh, s1);
             }
-        }
+        float s[2] = {total(s0), total(s1)};
         group_sum<TPG>(s, sm);
-        const float m1 = a.center ? s[0] * a.inv_d : 0.f, m2 = s[1] * a.inv_d;
+        // dx = rstd (dy w - mean(dy w) - xh mean(dy w xh))
+        const Ch<W> m1 = all<W>(a.center ? -s[0] * a.inv_d * rstd : 0.f), m2 = all<W>(-s[1] * a.inv_d * rstd),
+                    r = all<W>(rstd);
         if (on) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) x.v[i][e] = rstd * (o.v[i][e] - m1 - x.v[i][e] * m2);
+                for (int e = 0; e < N; ++e) x.v[i][e] = fma(o.v[i][e], r, fma(x.v[i][e], m2, m1));
             write<T, VEC, TPG, NV>(x, pdx.p, lane, a.d);
             if (GATE) write<T, VEC, TPG, NV>(z, pdz.p, lane, a.d);
         }
@@ -474,8 +481,8 @@ __global__ void __launch_bounds__(GN_THREADS, blocks_per_sm<VEC, NV>(true)) gn_b
         if (c < a.d)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                sums[group * a.d + c + e] = dw.v[i][e];
-                sums[(GPB + group) * a.d + c + e] = db.v[i][e];
+                sums[group * a.d + c + e] = dw.v[i][e / W].v[e % W];
+                sums[(GPB + group) * a.d + c + e] = db.v[i][e / W].v[e % W];
             }
     }
     __syncthreads();
@@ -554,20 +561,28 @@ template <typename T, int VEC, int TPG, int NV, bool BWD> int launch_gn(const Gn
 template <typename T, int VEC, bool BWD> int by_size(const GnArgs &a, cudaStream_t s)
 {
     const int nv = (a.d + VEC - 1) / VEC;
-    if constexpr (VEC >= 4) {
+    if constexpr (VEC == 8) {
         if (nv <= 8) return launch_gn<T, VEC, 8, 1, BWD>(a, s);
         if (nv <= 16) return launch_gn<T, VEC, 16, 1, BWD>(a, s);
-    }
-    if (nv <= 32) return launch_gn<T, VEC, 32, 1, BWD>(a, s);
-    if (nv <= 64) return launch_gn<T, VEC, 32, 2, BWD>(a, s);
-    if (nv <= 128) return launch_gn<T, VEC, 32, 4, BWD>(a, s);
-    if constexpr (VEC <= 4)
-        if (nv <= 256) return launch_gn<T, VEC, 32, 8, BWD>(a, s);
-    if constexpr (VEC == 8) {
+        if (nv <= 32) return launch_gn<T, VEC, 32, 1, BWD>(a, s);
+        if (nv <= 64) return launch_gn<T, VEC, 32, 2, BWD>(a, s);
+        if (nv <= 128) return launch_gn<T, VEC, 32, 4, BWD>(a, s);
         if (nv <= 256) return launch_gn<T, VEC, 256, 1, BWD>(a, s);
         return launch_gn<T, VEC, 256, 4, BWD>(a, s);
+    } else if constexpr (VEC == 4) {
+        if (nv <= 8) return launch_gn<T, VEC, 8, 1, BWD>(a, s);
+        if (nv <= 16) return launch_gn<T, VEC, 8, 2, BWD>(a, s);
+        if (nv <= 32) return launch_gn<T, VEC, 16, 2, BWD>(a, s);
+        if (nv <= 64) return launch_gn<T, VEC, 32, 2, BWD>(a, s);
+        if (nv <= 128) return launch_gn<T, VEC, 32, 4, BWD>(a, s);
+        if (nv <= 256) return launch_gn<T, VEC, 32, 8, BWD>(a, s);
+        return launch_gn<T, VEC, 256, 8, BWD>(a, s);
     } else {
-        if (nv <= 256 * 4 / VEC) return launch_gn<T, VEC, 256, (4 / VEC > 1 ? 4 / VEC : 1), BWD>(a, s);
+        if (nv <= 32) return launch_gn<T, VEC, 32, 1, BWD>(a, s);
+        if (nv <= 64) return launch_gn<T, VEC, 32, 2, BWD>(a, s);
+        if (nv <= 128) return launch_gn<T, VEC, 32, 4, BWD>(a, s);
+        if (nv <= 256) return launch_gn<T, VEC, 32, 8, BWD>(a, s);
+        if (nv <= 1024) return launch_gn<T, VEC, 256, 4, BWD>(a, s);
         return launch_gn<T, VEC, 256, 32 / VEC, BWD>(a, s);
     }
 }

@@ -1,5 +1,5 @@
-// layer.cuh -- strided [B, H, L, d] views and their checks, shared by the operators that
-// stand around the attention (recurrence, rotary positions, group norm).
+// layer.cuh -- strided [B, H, L, d] views and their checks, and packed fp32 arithmetic, shared by
+// the operators that stand around the attention (recurrence, rotary positions, group norm).
 #pragma once
 
 #include <limits.h>
@@ -88,6 +88,65 @@ inline bool rows_aligned(const void *p, const View &v, int B, int H, int L, size
 {
     auto ok = [&](long long s, int n) { return n == 1 || (s * (long long)elem) % (long long)bytes == 0; };
     return aligned(p, bytes) && ok(v.b, B) && ok(v.h, H) && ok(v.l, L);
+}
+
+// ---- arithmetic ----------------------------------------------------------------------------
+// 2^x and 1/x by the special function unit: relative error 2^-22 and 2^-23, results below the
+// normal range flushed to 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// V neighbouring values of a thread; pairs use the packed fp32 instructions.
+template <int V> struct Ch {
+    float v[V];
+};
+template <int V> __device__ __forceinline__ Ch<V> all(float x)
+{
+    Ch<V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = x;
+    return r;
+}
+__device__ __forceinline__ Ch<1> fma(Ch<1> a, Ch<1> b, Ch<1> c) { return {{fmaf(a.v[0], b.v[0], c.v[0])}}; }
+__device__ __forceinline__ Ch<1> mul(Ch<1> a, Ch<1> b) { return {{a.v[0] * b.v[0]}}; }
+__device__ __forceinline__ Ch<1> add(Ch<1> a, Ch<1> b) { return {{a.v[0] + b.v[0]}}; }
+__device__ __forceinline__ Ch<2> fma(Ch<2> a, Ch<2> b, Ch<2> c)
+{
+    Ch<2> r;
+    asm("{ .reg .b64 x, y, z, w;\n"
+        "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 w, x, y, z; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.v[0]), "=f"(r.v[1])
+        : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]), "f"(c.v[0]), "f"(c.v[1]));
+    return r;
+}
+__device__ __forceinline__ Ch<2> mul(Ch<2> a, Ch<2> b)
+{
+    Ch<2> r;
+    asm("{ .reg .b64 x, y, w;\n"
+        "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+        "mul.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.v[0]), "=f"(r.v[1]) : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+    return r;
+}
+__device__ __forceinline__ Ch<2> add(Ch<2> a, Ch<2> b)
+{
+    Ch<2> r;
+    asm("{ .reg .b64 x, y, w;\n"
+        "mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5};\n"
+        "add.rn.f32x2 w, x, y; mov.b64 {%0, %1}, w; }"
+        : "=f"(r.v[0]), "=f"(r.v[1]) : "f"(a.v[0]), "f"(a.v[1]), "f"(b.v[0]), "f"(b.v[1]));
+    return r;
 }
 
 }  // namespace la
