@@ -6,7 +6,7 @@
 // product p * theta would be off by a radian at p ~ 2^24.
 //
 // Bound by memory: every element is read and written once.  A thread holds the sines and cosines
-// of VEC pairs (16-byte vectors) of one token and goes over up to 8 heads of q and k with them;
+// of VEC pairs (16-byte vectors) of one token and goes over up to 16 heads of q and k with them;
 // the first heads' loads are on the way while the sines (~30 instructions a pair) are computed.
 #include <math.h>
 
@@ -19,8 +19,11 @@ namespace la {
 namespace {
 
 constexpr int ROT_THREADS = 256;
-constexpr int ROT_AT_ONCE = 2;  // heads whose loads are on the way together
-constexpr int ROT_HEADS = 8;    // heads of a thread at most
+constexpr int ROT_HEADS = 16;  // heads of a thread at most (B8 H16 L8192 d128: 172 us, with 8 182)
+
+// Heads whose loads are on the way together: with 16-byte vectors two (with four the registers leave
+// two blocks an SM, 226 us), with single elements four.
+template <int VEC> constexpr int ROT_AT_ONCE = VEC > 1 ? 2 : 4;
 
 struct RotArgs {
     const void *q, *k;
@@ -119,10 +122,11 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
         two = c1 < a.d;
         if (!two) c1 = c0;
     }
-    V x[ROT_AT_ONCE], y[ROT_AT_ONCE];
+    constexpr int AT_ONCE = ROT_AT_ONCE<VEC>;
+    V x[AT_ONCE], y[AT_ONCE];
     auto fetch = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < ROT_AT_ONCE; ++j)
+        for (int j = 0; j < AT_ONCE; ++j)
             if (h + j < h1) {
                 x[j] = *(const V *)(in.p + c0);
                 y[j] = *(const V *)(in.p + c1);
@@ -140,10 +144,10 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
             c[e] *= a.amp;
         }
     }
-    for (int h = h0; h < h1; h += ROT_AT_ONCE) {
+    for (int h = h0; h < h1; h += AT_ONCE) {
         if (h != h0) fetch(h);
 #pragma unroll
-        for (int j = 0; j < ROT_AT_ONCE; ++j)
+        for (int j = 0; j < AT_ONCE; ++j)
             if (h + j < h1) {
                 if (pair && half) {
 #pragma unroll
