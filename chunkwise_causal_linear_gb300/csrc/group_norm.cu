@@ -540,10 +540,9 @@ template <typename T, int VEC, int TPG, int NV, bool BWD> int launch_gn(const Gn
         size_t smem = SourceOf<T, VEC, TPG, NV, decltype(gate)::value, BWD>::R::SMEM;
         if (BWD && a.part) smem = std::max(smem, sizeof(float) * 2 * (GN_THREADS / TPG) * a.d);
         if (smem > 47 * 1024 &&
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            status_of(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != LA_OK)
             return (int)LA_ERR_CUDA;
-        kern<<<(unsigned)blocks, GN_THREADS, smem, s>>>(a);
-        return cudaPeekAtLastError() == cudaSuccess ? (int)LA_OK : (int)LA_ERR_CUDA;
+        return launch(kern, dim3((unsigned)blocks), GN_THREADS, smem, s, a);
     };
     const bool silu = a.act == LA_ACT_SILU;
     const std::true_type yes;
@@ -695,7 +694,7 @@ int la_group_norm_bwd(const void *x, const float *weight, const float *bias, con
     if (rc2 != LA_OK || !a.part) return rc2;
     const long long join = ((long long)H * d + 31) / 32;
     if (join > INT_MAX) return LA_ERR_SHAPE;
-    return tcc::launch_dependent(gn_join_kernel, (int)join, GN_THREADS, 0, s, a) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    return status_of(tcc::launch_dependent(gn_join_kernel, (int)join, GN_THREADS, 0, s, a));
 }
 
 }  // extern "C"

@@ -90,6 +90,24 @@ inline bool rows_aligned(const void *p, const View &v, int B, int H, int L, size
     return aligned(p, bytes) && ok(v.b, B) && ok(v.h, H) && ok(v.l, L);
 }
 
+// A launch's own status, and no error left behind for the next call to find.
+inline int status_of(cudaError_t e)
+{
+    if (e == cudaSuccess) return LA_OK;
+    (void)cudaGetLastError();
+    return LA_ERR_CUDA;
+}
+template <typename... P, typename... A>
+inline int launch(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, const A &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    return status_of(cudaLaunchKernelEx(&cfg, kern, args...));
+}
+
 // ---- arithmetic ----------------------------------------------------------------------------
 // 2^x and 1/x by the special function unit: relative error 2^-22 and 2^-23, results below the
 // normal range flushed to 0.

@@ -15,9 +15,9 @@
 // finishes its rows from its state.  With S > 1 that warp first sends the tile's (P, H) into the
 // other blocks' shared memory (st.async, which counts on an mbarrier there) and so knows the
 // state before the tile and after the step; the release of a cluster barrier in that place waited
-// for the output rows still on their way (a quarter of the time).  Every input is read once and every output written once; nothing goes
-// through global memory between the blocks, and the order of the sums depends on the sizes
-// alone.
+// for the output rows still on their way (a quarter of the time).  Every input is read once and
+// every output written once; nothing goes through global memory between the blocks, and the order
+// of the sums depends on the sizes and the GPU alone.
 //
 // Measured (of the measured HBM rate): B1 H16 L65536 d64 fp32 (32 clusters of 8) forward 126 us,
 // 95%, backward 212 us, 94%; B8 H16 L8192 d128 bf16 with sigmoid gates forward 131 us, 92%,
@@ -45,6 +45,7 @@ constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the for
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
 constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
+
 struct RecArgs {
     const void *x, *g, *dout;
     void *out, *dx, *dg;
@@ -130,13 +131,9 @@ template <int V> __device__ __forceinline__ Ch<V> step(const Ch<V> &a, const Ch<
     for (int v = 0; v < V; ++v) r.v[v] = a.v[v] == 0.f ? b.v[v] : r.v[v];
     return r;
 }
-// One row.  EXACT = false leaves out the forgetting of infinities and NaN, which then stay to the
-// last row: whoever finds that one finite has the same value as with EXACT.
-template <bool EXACT, int V> __device__ __forceinline__ Ch<V> row(const Ch<V> &a, const Ch<V> &h, const Ch<V> &b)
-{
-    if constexpr (EXACT) return step(a, h, b);
-    else return fma(a, h, b);
-}
+// The common path leaves the forgetting of infinities and NaN out (a plain fma): they then stay to
+// the last row, so whoever finds that one finite has the exact value, and the others start again
+// with step().
 template <int V> __device__ __forceinline__ bool finite(const Ch<V> &h)
 {
     bool ok = true;
@@ -433,8 +430,8 @@ __device__ __forceinline__ void send(const Fold<1> *slot, const uint64_t *bar, i
 }
 __device__ __forceinline__ void cluster_barrier()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity)
 {
@@ -479,7 +476,7 @@ struct Peers {
     }
     // The carry over the tiles of a step, `carry = P carry + H`: returns the carry before this
     // block's tile and leaves the one after the step.
-    __device__ __forceinline__ Ch<1> over(int buf, uint32_t parity, int lane, Ch<1> &carry)
+    __device__ __forceinline__ Ch<1> over(int buf, uint32_t parity, int lane, bool on, Ch<1> &carry)
     {
         if (!dead && !arrived(&bar[buf], parity)) {
             const uint64_t t0 = globaltimer();
@@ -499,7 +496,7 @@ struct Peers {
             const Fold<1> q = f[r * 32];
             carry = fma(q.p, carry, q.h);
         }
-        if (!finite(carry)) {
+        if (on && !finite(carry)) {
             carry = apply_exact<1>(f, 32, split, start);
             mine = apply_exact<1>(f, 32, rank, start);
         }
@@ -545,7 +542,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
     const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0, blk = blockIdx.x / split;
     const int bh = blk / a.ncb, c0 = blk % a.ncb * CW, b = bh / a.H, hd = bh % a.H;
     const int c = c0 + lane * V;
-    const bool on = c < a.d;
+    const bool on = c < a.d;  // lanes without a channel compute on what shared memory holds
     const T *x = (const T *)a.x + row_of(a.vx, b, hd, 0) + c0;
     const G *g = (const G *)a.g + row_of(a.vg, b, hd, 0) + c0;
     T *out = (T *)a.out + row_of(a.vo, b, hd, 0) + c0;
@@ -606,7 +603,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
                 p = mul(p, ga[i]);
             }
             own = Pr::join(p, f);
-            if (!finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
+            if (on && !finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
         }
         agg[warp * 32 + lane] = own;
         __syncthreads();
@@ -622,9 +619,9 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
                     t.h = fma(q.p, t.h, q.h);
                     t.p = mul(q.p, t.p);
                 }
-                if (!finite(t.h)) t = join_exact<V>(f8, 32, REC_W);
+                if (on && !finite(t.h)) t = join_exact<V>(f8, 32, REC_W);
                 peers.publish(buf, lane, t);
-                e = peers.over(buf, parity, lane, carry);
+                e = peers.over(buf, parity, lane, on, carry);
             }
             const Ch<V> start = e;
 #pragma unroll
@@ -633,7 +630,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
                 const Fold<V> q = f8[w * 32];
                 e = fma(q.p, e, q.h);
             }
-            if (!finite(e)) e = begin_exact<V>(begin + lane, f8, 32, start);
+            if (on && !finite(e)) e = begin_exact<V>(begin + lane, f8, 32, start);
             if constexpr (!SPLIT) carry = e;
         }
         __syncthreads();
@@ -684,7 +681,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
     const int split = SPLIT ? a.split : 1, rank = SPLIT ? blockIdx.x % split : 0, blk = blockIdx.x / split;
     const int bh = blk / a.ncb, c0 = blk % a.ncb * CW, b = bh / a.H, hd = bh % a.H;
     const int c = c0 + lane * V;
-    const bool on = c < a.d;
+    const bool on = c < a.d;  // lanes without a channel compute on what shared memory holds
     const T *x = (const T *)a.x + row_of(a.vx, b, hd, 0) + c0;
     const G *g = (const G *)a.g + row_of(a.vg, b, hd, 0) + c0;
     const T *dout = (const T *)a.dout + row_of(a.vo, b, hd, 0) + c0;
@@ -756,7 +753,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             for (int i = Pr::N - 2; i >= 0; --i) g2 = mul(ga[i], add(g2, Pr::get(sd, i)));
             const Fold<V> o = Pr::join(p, f);
             own = {o.p, o.h, Pr::join_back(p, g2)};
-            if (!finite(own.h) || !finite(own.e)) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
+            if (on && (!finite(own.h) || !finite(own.e))) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
         }
         agg[warp * 32 + lane] = Fold<V>{own.p, own.e};
         front[warp * 32 + lane] = own.h;
@@ -772,9 +769,9 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
                     t.h = fma(q.p, t.h, q.h);
                     t.p = mul(q.p, t.p);
                 }
-                if (!finite(t.h)) t = join_exact<V>(f8 + (REC_W - 1) * 32, -32, REC_W);
+                if (on && !finite(t.h)) t = join_exact<V>(f8 + (REC_W - 1) * 32, -32, REC_W);
                 peers.publish(buf, lane, t);
-                e = peers.over(buf, parity, lane, carry);
+                e = peers.over(buf, parity, lane, on, carry);
             }
             const Ch<V> start = e;
 #pragma unroll
@@ -783,7 +780,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
                 const Fold<V> q = f8[w * 32];
                 e = fma(q.p, e, q.h);
             }
-            if (!finite(e)) e = begin_exact<V>(behind + (REC_W - 1) * 32 + lane, f8 + (REC_W - 1) * 32, -32, start);
+            if (on && !finite(e)) e = begin_exact<V>(behind + (REC_W - 1) * 32 + lane, f8 + (REC_W - 1) * 32, -32, start);
             if constexpr (!SPLIT) carry = e;
         } else if (warp == 1) {  // h over the warps
             Ch<V> h = before;
@@ -792,7 +789,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
                 begin[w * 32 + lane] = h;
                 h = fma(f8[w * 32].p, h, front[w * 32 + lane]);
             }
-            if (!finite(h)) {
+            if (on && !finite(h)) {
                 h = before;
 #pragma unroll 1
                 for (int w = 0; w < REC_W; ++w) {
@@ -894,8 +891,8 @@ struct RecKernel {
     {
         if (ready[dev]) return true;
         const size_t most = smem(split ? REC_MAX_SPLIT : 1);
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
-            (split && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+        if (status_of(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)) != LA_OK ||
+            (split && status_of(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != LA_OK))
             return false;
         return ready[dev] = true;
     }
@@ -911,7 +908,7 @@ struct RecKernel {
                 cudaLaunchAttribute at;
                 config(cfg, at, s);
                 cfg.gridDim = dim3((unsigned)s);
-                if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n <= 0) n = -1;
+                if (status_of(cudaOccupancyMaxActiveClusters(&n, fn, &cfg)) != LA_OK || n <= 0) n = -1;
                 fit[dev][s] = n;
             }
             if (n >= blocks) return s;
@@ -928,7 +925,7 @@ struct RecKernel {
         cfg.gridDim = dim3((unsigned)blocks);
         cfg.stream = stream;
         void *args[] = {&a};
-        return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+        return status_of(cudaLaunchKernelExC(&cfg, fn, args));
     }
 };
 
@@ -1015,8 +1012,7 @@ struct LaunchStep {
     template <typename T, typename G, int KIND, bool COMP> int operator()() const
     {
         const unsigned grid = (unsigned)((n + STEP_THREADS - 1) / STEP_THREADS);
-        rec_step_kernel<T, G, KIND, COMP><<<grid, STEP_THREADS, 0, s>>>((const T *)x, (const G *)g, state, (T *)out, n);
-        return cudaGetLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+        return la::launch(rec_step_kernel<T, G, KIND, COMP>, dim3(grid), STEP_THREADS, 0, s, (const T *)x, (const G *)g, state, (T *)out, n);
     }
 };
 

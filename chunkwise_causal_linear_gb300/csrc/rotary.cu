@@ -193,8 +193,7 @@ template <typename T, int VEC> int launch_rotary(RotArgs &a, int sms, cudaStream
     while (a.heads > 1 && blocks * groups() < 8ll * sms) a.heads = (a.heads + 1) / 2;
     while (groups() > 65535) a.heads *= 2;  // limit of the grid
     const int ny = groups();
-    rotary_kernel<T, VEC><<<dim3((unsigned)blocks, (unsigned)ny), ROT_THREADS, 0, s>>>(a);
-    return cudaPeekAtLastError() == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+    return launch(rotary_kernel<T, VEC>, dim3((unsigned)blocks, (unsigned)ny), ROT_THREADS, 0, s, a);
 }
 
 template <typename T, int VEC> bool whole_vectors(const RotArgs &a)
