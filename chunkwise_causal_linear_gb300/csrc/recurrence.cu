@@ -44,6 +44,7 @@ namespace {
 constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the forward leaves
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
+constexpr int BWD_R = 16;                // rows of a warp, backward
 constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
 
 struct RecArgs {
@@ -319,19 +320,6 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
     }
     return f;
 }
-// the state h after `rows` rows
-template <typename T, typename G, int KIND, bool COMP, int V>
-__device__ __noinline__ Ch<V> apply_rows(const T *sx, const G *sg, int rows, Ch<V> h)
-{
-#pragma unroll 1
-    for (int i = 0; i < rows; ++i) {
-        const Ch<V> x = get<V>(sx + i * 32 * V);
-        Ch<V> a, c;
-        gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
-        h = step(a, h, COMP ? mul(c, x) : x);
-    }
-    return h;
-}
 // out: this lane's channels of the first row; `present` rows of it exist
 template <typename T, typename G, int KIND, bool COMP, int V>
 __device__ __noinline__ void finish_rows(const T *sx, const G *sg, int rows, int present, Ch<V> h, T *out,
@@ -398,12 +386,20 @@ template <typename T, typename G, int KIND, bool COMP, int V>
 __device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *sg, int rows, int present, Ch<V> h,
                                              Ch<V> e, T *dx, long long dx_stride, G *dg, long long dg_stride)
 {
+    Ch<V> before[BWD_R];  // the state before each row
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
+        const Ch<V> x = get<V>(sx + i * 32 * V);
+        Ch<V> a, c;
+        gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        before[i] = h;
+        h = step(a, h, COMP ? mul(c, x) : x);
+    }
 #pragma unroll 1
     for (int i = present - 1; i >= 0; --i) {
         Ch<V> rx = all<V>(0.f), rg = rx;
         if (i < rows) {
-            const Ch<V> hb = apply_rows<T, G, KIND, COMP, V>(sx, sg, i, h);
-            const Ch<V> x = get<V>(sx + i * 32 * V);
+            const Ch<V> hb = before[i], x = get<V>(sx + i * 32 * V);
             Ch<V> a, c;
             gate_of<KIND, COMP || KIND == LA_GATE_SIGMOID, V>(get<V>(sg + i * 32 * V), a, c);
             e = add(e, get<V>(sd + i * 32 * V));
@@ -513,7 +509,7 @@ struct Peers {
 // weighs more than the registers (B1 H8 L65536 d128: 98 us and 114; backward would need 96 registers
 // for three values a row).
 template <typename T, typename G, int V, bool BWD, bool SPLIT> struct RecSmem {
-    static constexpr int R = !BWD && SPLIT && sizeof(T) == 2 ? 32 : 16, TILE = R * REC_W;
+    static constexpr int R = BWD ? BWD_R : SPLIT && sizeof(T) == 2 ? 32 : 16, TILE = R * REC_W;
     static_assert(TILE % RC == 0 && (RC % R == 0), "tiles, and chunks within them, start at a warp's first row");
     static constexpr size_t AGG = sizeof(Fold<V>) * REC_W * 32, START = sizeof(Ch<V>) * REC_W * 32;
     static constexpr size_t HEAD = BWD ? AGG + 3 * START : AGG + START;  // backward: H, and both states
