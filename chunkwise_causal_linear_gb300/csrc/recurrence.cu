@@ -161,37 +161,31 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 // Rows [0, nrow) and channels [0, nch) of a warp's rows into its ring slot, CW channels a row, in
 // copies of `gran` bytes: N copies make a row, a warp makes 32 / N rows at once.
-template <typename T, int R, int CW, int BYTES, int ROW = CW>
+template <typename T, int R, int CW, int BYTES>
 __device__ __forceinline__ void copy_by(T *slot, const T *src, long long stride, int nrow, int nch, int lane)
 {
-    constexpr int E = BYTES / sizeof(T), N = CW / E;
-    if constexpr (N > 32) {  // a row takes two instructions: by halves
-        copy_by<T, R, CW / 2, BYTES, ROW>(slot, src, stride, nrow, nch, lane);
-        copy_by<T, R, CW / 2, BYTES, ROW>(slot + CW / 2, src + CW / 2, stride, nrow, nch - CW / 2, lane);
-    } else {
-        constexpr int RP = 32 / N, M = R / RP;
-        static_assert(32 % N == 0 && R % RP == 0, "whole rows per warp instruction");
-        const int r0 = lane / N, c = lane % N * E;
-        if (c >= nch) return;
-        const T *p = src + r0 * stride + c;
-        T *q = slot + r0 * ROW + c;
-        if constexpr (BYTES == 2) {
-            if (nrow == R) {
-                T v[M];
+    constexpr int E = BYTES / sizeof(T), N = CW / E, RP = 32 / N, M = R / RP;
+    static_assert(32 % N == 0 && R % RP == 0, "whole rows per warp instruction");
+    const int r0 = lane / N, c = lane % N * E;
+    if (c >= nch) return;
+    const T *p = src + r0 * stride + c;
+    T *q = slot + r0 * CW + c;
+    if constexpr (BYTES == 2) {
+        if (nrow == R) {
+            T v[M];
 #pragma unroll
-                for (int j = 0; j < M; ++j, p += RP * stride) v[j] = *p;
+            for (int j = 0; j < M; ++j, p += RP * stride) v[j] = *p;
 #pragma unroll
-                for (int j = 0; j < M; ++j) q[j * RP * ROW] = v[j];
-            } else {
-#pragma unroll 1
-                for (int r = r0; r < nrow; r += RP, p += RP * stride, q += RP * ROW) *q = *p;
-            }
+            for (int j = 0; j < M; ++j) q[j * RP * CW] = v[j];
         } else {
-            const uint32_t dst = (uint32_t)__cvta_generic_to_shared(q);
-#pragma unroll
-            for (int j = 0; j < M; ++j, p += RP * stride)
-                if (r0 + j * RP < nrow) cp_async<BYTES>(dst + (uint32_t)sizeof(T) * j * RP * ROW, p);
+#pragma unroll 1
+            for (int r = r0; r < nrow; r += RP, p += RP * stride, q += RP * CW) *q = *p;
         }
+    } else {
+        const uint32_t dst = smem_u32(q);
+#pragma unroll
+        for (int j = 0; j < M; ++j, p += RP * stride)
+            if (r0 + j * RP < nrow) cp_async<BYTES>(dst + (uint32_t)sizeof(T) * j * RP * CW, p);
     }
 }
 // The rarer cases out of the way of the common one, which fits the instruction cache.  Rows that a
@@ -224,15 +218,11 @@ __device__ __forceinline__ void copy_rows(T *slot, const T *src, long long strid
             cp_async<16>(dst + (uint32_t)sizeof(T) * j * RP * CW, p);
 }
 
-// ---- V neighbouring channels (pairs are aligned and inside the channels together) -------------
+// ---- V neighbouring channels (pairs, of bf16, are aligned and inside the channels together) -----
 template <int V> __device__ __forceinline__ Ch<V> get(const float *p)
 {
-    if constexpr (V == 2) {
-        const float2 t = *(const float2 *)p;
-        return {{t.x, t.y}};
-    } else {
-        return {{*p}};
-    }
+    static_assert(V == 1, "pairs are of bf16");
+    return {{*p}};
 }
 template <int V> __device__ __forceinline__ Ch<V> get(const __nv_bfloat16 *p)
 {
@@ -245,8 +235,8 @@ template <int V> __device__ __forceinline__ Ch<V> get(const __nv_bfloat16 *p)
 }
 template <int V> __device__ __forceinline__ void put(float *p, const Ch<V> &x)
 {
-    if constexpr (V == 2) *(float2 *)p = make_float2(x.v[0], x.v[1]);
-    else *p = x.v[0];
+    static_assert(V == 1, "pairs are of bf16");
+    *p = x.v[0];
 }
 template <int V> __device__ __forceinline__ void put(__nv_bfloat16 *p, const Ch<V> &x)
 {

@@ -580,7 +580,8 @@ enum la_activation {
  *                 last (gate itself may be NULL)
  *   eps           > 0 and finite, else LA_ERR_ARG
  *   d             at most 8192, else LA_ERR_UNSUPPORTED
- * Statistics are fp32 over values held in fp32, the variance from centred values.
+ * Statistics are fp32 over values held in fp32, the variance from centred values.  Outputs must
+ * not overlap inputs.
  */
 int la_group_norm_fwd(const void *x, const float *weight, const float *bias, const void *gate,
                       void *out, int B, int H, int L, int d, const la_strides *x_strides,
@@ -592,7 +593,7 @@ int la_group_norm_fwd(const void *x, const float *weight, const float *bias, con
  * dgate (as gate; NULL if and only if gate is), dweight and dbias (device fp32 [H, d], each
  * may be NULL).  Statistics are recomputed from x.  dweight and dbias are summed in a fixed
  * order through the workspace of la_group_norm_bwd_workspace_bytes(...) bytes (0 when neither
- * is asked for).
+ * is asked for).  Outputs must not overlap inputs.
  */
 int la_group_norm_bwd(const void *x, const float *weight, const float *bias, const void *gate,
                       const void *dout, void *dx, void *dgate, float *dweight, float *dbias,
