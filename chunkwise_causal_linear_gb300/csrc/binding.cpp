@@ -9,6 +9,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <climits>
+
 #include "la_chunked.h"
 
 namespace {
@@ -93,16 +95,20 @@ struct Place {
     }
 };
 
-void sizes4(const Tensor &t, const char *name)
+// Axes of an input, each of a length that the C ABI's ints hold.
+void axes(const Tensor &t, int n, const char *name)
 {
-    if (t.dim() != 4) throw py::value_error(std::string(name) + " must have 4 axes, got " + text(t.sizes()));
+    if (t.dim() != n)
+        throw py::value_error(std::string(name) + " must have " + std::to_string(n) + " axes, got " + text(t.sizes()));
+    for (const int64_t len : t.sizes())
+        if (len > INT_MAX) throw py::value_error(std::string(name) + " is too long: " + text(t.sizes()));
 }
 
 py::object recurrence_fwd(const Tensor &x, const Tensor &gate, const OptTensor &h0, int gate_kind, bool complement,
                           const OptTensor &lengths, bool save_chunks, const OptTensor &out_, const OptStream &stream)
 {
     const char *what = "la_recurrence_fwd";
-    sizes4(x, "x");
+    axes(x, 4, "x");
     const at::Device dev = x.device();
     const at::ScalarType type = x.scalar_type();
     const int64_t B = x.size(0), H = x.size(1), L = x.size(2), d = x.size(3);
@@ -129,7 +135,7 @@ py::tuple recurrence_bwd(const Tensor &x, const Tensor &gate, const Tensor &chun
                          const OptTensor &dx_, const OptTensor &dgate_, const OptStream &stream)
 {
     const char *what = "la_recurrence_bwd";
-    sizes4(x, "x");
+    axes(x, 4, "x");
     const at::Device dev = x.device();
     const at::ScalarType type = x.scalar_type(), gate_type = gate.scalar_type();
     const int64_t B = x.size(0), H = x.size(1), L = x.size(2), d = x.size(3);
@@ -155,7 +161,7 @@ Tensor recurrence_step(const Tensor &x, const Tensor &gate, const Tensor &state,
                        const OptTensor &out_, const OptStream &stream)
 {
     const char *what = "la_recurrence_step";
-    if (x.dim() != 3) throw py::value_error("x must have 3 axes, got " + text(x.sizes()));
+    axes(x, 3, "x");
     const at::Device dev = x.device();
     const int dtype = code(x), gtype = code(gate);
     const Place place(dev, stream, what);
@@ -175,7 +181,7 @@ py::tuple rotary(const Tensor &q, const OptTensor &k, const Tensor &turns, int64
                  const OptTensor &k_out_, const OptStream &stream)
 {
     const char *what = "la_rotary";
-    sizes4(q, "q");
+    axes(q, 4, "q");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
     const int64_t B = q.size(0), H = q.size(1), L = q.size(2), d = q.size(3);
@@ -188,7 +194,7 @@ py::tuple rotary(const Tensor &q, const OptTensor &k, const Tensor &turns, int64
     OptTensor k_out;
     std::optional<Strides> sk, sko;
     if (k) {
-        sizes4(*k, "k");
+        axes(*k, 4, "k");
         Hk = k->size(1);
         const std::array<int64_t, 4> shape{B, Hk, L, d};
         sk.emplace(*k, shape, type, dev, "k");
@@ -208,7 +214,7 @@ Tensor group_norm_fwd(const Tensor &x, const OptTensor &weight, const OptTensor 
                       int activation, bool center, const OptTensor &out_, const OptStream &stream)
 {
     const char *what = "la_group_norm_fwd";
-    sizes4(x, "x");
+    axes(x, 4, "x");
     const at::Device dev = x.device();
     const at::ScalarType type = x.scalar_type();
     const int64_t B = x.size(0), H = x.size(1), L = x.size(2), d = x.size(3);
@@ -233,7 +239,7 @@ py::tuple group_norm_bwd(const Tensor &x, const Tensor &dout, const OptTensor &w
                          const OptTensor &dgate_, const OptTensor &workspace_, const OptStream &stream)
 {
     const char *what = "la_group_norm_bwd";
-    sizes4(x, "x");
+    axes(x, 4, "x");
     const at::Device dev = x.device();
     const at::ScalarType type = x.scalar_type();
     const int64_t B = x.size(0), H = x.size(1), L = x.size(2), d = x.size(3);

@@ -147,6 +147,23 @@ def test_alignment():
     assert gn_bwd(dout=ODD, dtype=la.LA_BF16) == la.LA_ERR_ARG
 
 
+def test_binding_refuses_lengths_past_32_bits():
+    """A length that the C ABI's ints do not hold is refused, not cut to its low 32 bits."""
+    torch = pytest.importorskip("torch")
+    for axis in range(4):
+        shape = [1, 1, 1, 1]
+        shape[axis] = (1 << 32) + 1
+        x = torch.zeros(1).expand(shape)
+        calls = [lambda: la.recurrence_fwd(x, x), lambda: la.recurrence_bwd(x, x, x, x),
+                 lambda: la.rotary(x, None, la.RotaryTable(torch.zeros(1, dtype=torch.int64), 2)),
+                 lambda: la.group_norm_fwd(x), lambda: la.group_norm_bwd(x, x)]
+        if axis:
+            calls.append(lambda: la.recurrence_step(x[0], x[0], x[0]))
+        for call in calls:
+            with pytest.raises(ValueError, match="too long"):
+                call()
+
+
 # ---- the rotary table --------------------------------------------------------------------
 def table(rot, base=10000.0, scaling=0, factor=1.0, original=0.0, fast=32.0, slow=1.0):
     out = (ctypes.c_ulonglong * max(1, rot // 2))()
