@@ -778,7 +778,8 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="s
 def group_norm_bwd(x, dout, weight=None, bias=None, gate=None, eps=1e-5, activation="silu",
                    center=True, dx=None, dgate=None, workspace=None, stream=None):
     """(dx, dgate, dweight, dbias) of group_norm_fwd for dout [B,L,H*d]; None where the forward
-    had None."""
+    had None.  workspace: contiguous device memory of la_group_norm_bwd_workspace_bytes, allocated
+    where it is None or smaller."""
     return (_binding or _layer_binding()).group_norm_bwd(x, dout, weight, bias, gate, eps,
                                                       ACTIVATIONS[activation], center, dx, dgate,
                                                       workspace, stream)

@@ -241,6 +241,8 @@ py::tuple group_norm_bwd(const Tensor &x, const Tensor &dout, const OptTensor &w
     const char *what = "la_group_norm_bwd";
     axes(x, 4, "x");
     const at::Device dev = x.device();
+    if (workspace_ && (workspace_->device() != dev || !workspace_->is_contiguous()))
+        throw py::value_error("workspace must be contiguous on " + dev.str());
     const at::ScalarType type = x.scalar_type();
     const int64_t B = x.size(0), H = x.size(1), L = x.size(2), d = x.size(3);
     const int dtype = code(x);

@@ -164,6 +164,17 @@ def test_binding_refuses_lengths_past_32_bits():
                 call()
 
 
+def test_group_norm_workspace_refusals():
+    """A workspace of another device, or one whose elements share memory, is refused."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(1, 1, 1, 8)
+    for workspace in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20),
+                      torch.zeros(1 << 16, dtype=torch.uint8, device="meta"),
+                      torch.zeros(1 << 16, 2, dtype=torch.uint8)[:, 0]):
+        with pytest.raises(ValueError, match="workspace must be contiguous on cpu"):
+            la.group_norm_bwd(x, x, weight=torch.ones(8), workspace=workspace)
+
+
 # ---- the rotary table --------------------------------------------------------------------
 def table(rot, base=10000.0, scaling=0, factor=1.0, original=0.0, fast=32.0, slow=1.0):
     out = (ctypes.c_ulonglong * max(1, rot // 2))()
