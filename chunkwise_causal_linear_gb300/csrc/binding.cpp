@@ -82,16 +82,26 @@ int code(const Tensor &t)
 
 void *ptr(const OptTensor &t) { return t ? t->data_ptr() : nullptr; }
 
-// The tensors' device made current, and the stream.
+// The tensors' device made current, and the stream.  A stream that the caller names is made current
+// too: what is allocated here belongs to it, and memory that is given back, as the workspace is at
+// the end of the call, is not handed to another stream while the kernels still use it.
 struct Place {
     c10::cuda::OptionalCUDAGuard guard;
+    c10::cuda::OptionalCUDAStreamGuard stream_guard;
     void *stream;
     Place(const at::Device &device, const OptStream &s, const char *what)
     {
         if (!device.is_cuda())
             throw py::value_error(std::string(what) + ": CUDA tensors are needed, got " + device.str());
         guard.set_device(device);
-        stream = s ? (void *)*s : (void *)c10::cuda::getCurrentCUDAStream(device.index()).stream();
+        if (s) {
+            // torch knows the legacy default stream by 0 only
+            const cudaStream_t given = *s == (int64_t)(intptr_t)cudaStreamLegacy ? nullptr : (cudaStream_t)*s;
+            stream_guard.reset_stream(c10::cuda::getStreamFromExternal(given, device.index()));
+            stream = given;
+        } else {
+            stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+        }
     }
 };
 

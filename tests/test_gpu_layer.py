@@ -223,6 +223,45 @@ def test_recurrence_aliases_and_streams(la):
     assert torch.equal(dx, first[0]) and torch.equal(dg, first[1]) and torch.equal(grad, first[2])
 
 
+@pytest.mark.parametrize("raw", [None, 0, 1, 2])
+def test_memory_of_a_named_stream(la, raw):
+    """What a call with stream= allocates belongs to that stream: a stream of one's own (None), and
+    the handles 0 and 1 (the default stream) and 2 (the thread's)."""
+    import torch
+    rng = np.random.default_rng(17)
+    side = torch.cuda.Stream()
+    handle = side.cuda_stream if raw is None else raw
+    owner = 0 if raw == 1 else handle
+    B, H, L, d = 2, 3, 200, 64
+    x, g, dout = (dev(rng.normal(size=(B, H, L, d))) for _ in range(3))
+    do = dev(rng.normal(size=(B, L, H * d)))
+    w = dev(rng.normal(size=H * d))
+    table = la.rotary_table(d)
+    torch.cuda.synchronize()
+
+    def calls(**on):
+        out, last, chunks = la.recurrence_fwd(x, g, save_chunks=True, **on)
+        dx, dg, dh0 = la.recurrence_bwd(x, g, chunks, dout, **on)
+        step = la.recurrence_step(x[:, :, 0].contiguous(), g[:, :, 0].contiguous(), last.clone(), **on)
+        q, k = la.rotary(x, g, table, **on)
+        y = la.group_norm_fwd(x, w, **on)
+        nx, _, dw, _ = la.group_norm_bwd(x, do, w, **on)
+        return out, last, chunks, dx, dg, dh0, step, q, k, y, nx, dw
+
+    want = calls()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.ExternalStream(owner) if owner else torch.cuda.default_stream()):
+        got = calls(stream=handle)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = la.group_norm_bwd(x, do, w, stream=handle)[::2] + la.rotary(x, g, table, stream=handle)
+    assert torch.cuda.current_stream().cuda_stream == 0
+    torch.cuda.synchronize()
+    segments = [(s["address"], s["total_size"], s["stream"]) for s in torch.cuda.memory_snapshot()]
+    for t in got:
+        assert [o for a, n, o in segments if a <= t.data_ptr() < a + n] == [owner]
+
+
 def test_offsets_past_32_bits(la):
     """Rows 2^31 elements apart, for every operator."""
     import torch
