@@ -236,7 +236,7 @@ int la_rotary_table(int rot, double base, int scaling, double factor, double ori
         // theta / (2 pi) to more than a double's digits: the product and its rounding error
         const double hi = theta * inv_hi, lo = fma(theta, inv_hi, -hi) + theta * inv_lo;
         const double whole = floor(hi);
-        if (!(whole < 9.0e15)) return LA_ERR_ARG;  // more than 2^53 turns per position
+        if (!(whole < 0x1p50)) return LA_ERR_ARG;  // beyond, lo 2^64 leaves 64 bits
         const double top = (hi - whole) * 0x1p32, top_i = floor(top);
         turns[j] = ((unsigned long long)top_i << 32) + (unsigned long long)((top - top_i) * 0x1p32) +
                    (unsigned long long)llrint(lo * 0x1p64);

@@ -535,8 +535,8 @@ enum la_rotary_scaling {
  * full turn per position, in units of 2^-64.  A position times that, modulo 2^64, is its
  * angle without any loss however far the position is.  The caller copies the table to the
  * device and keeps it.  fast, slow, original_length are read for LA_ROTARY_PARTS only (0 < slow
- * < fast).  LA_ERR_SHAPE for rot <= 0 or odd, LA_ERR_ARG for base <= 0, factor < 1 or values
- * that are not finite.
+ * < fast).  LA_ERR_SHAPE for rot <= 0 or odd, LA_ERR_ARG for base <= 0, factor < 1, values
+ * that are not finite, or more than 2^50 turns per position.
  */
 int la_rotary_table(int rot, double base, int scaling, double factor, double original_length,
                     double fast, double slow, unsigned long long *turns);

@@ -209,6 +209,20 @@ def test_rotary_table_refusals():
     assert la.la_rotary_table(4, 1e4, 0, 1.0, 0.0, 32.0, 1.0, None) == la.LA_ERR_NULL
 
 
+def test_rotary_table_of_many_turns():
+    """More turns per position than a double holds with digits to spare are refused; below that
+    the fraction of a turn is right to the digits of theta that pow() gives."""
+    from fractions import Fraction
+    assert table(4, base=1e-34)[0] == la.LA_ERR_ARG  # theta = 1e17: 1.6e16 turns
+    assert table(4, base=2.0 ** -106)[0] == la.LA_ERR_ARG  # 2^53 / (2 pi) = 1.4e15 turns, more than 2^50
+    rc, turns = table(4, base=2.0 ** -100)  # theta = 2^50, exactly
+    assert rc == la.LA_OK
+    inv = Fraction(15915494309189533576888376337251436203445964574046, 10 ** 50)  # 1 / (2 pi)
+    want = (2 ** 50 * inv) % 1
+    # inv_lo has 53 bits behind 2^-56: 2^50 2^-109, and the result is cut to 2^-64
+    assert abs(Fraction(turns[1], 2 ** 64) - want) <= Fraction(1, 2 ** 58)
+
+
 # ---- the 64-bit forms ---------------------------------------------------------------------
 def numeric(f, v, h=1e-6):
     """Central differences of a scalar function."""
