@@ -457,6 +457,10 @@ struct Peers {
     }
     __device__ __forceinline__ void publish(int buf, int lane, const Fold<1> &f)
     {
+        // after a wait that ran out, a barrier's phase may not have ended: it takes no further
+        // arrival.  The other blocks' waits run out too, before any block ends.
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) return;
         if (threadIdx.x == 0) mbar_arrive_expect_tx(&bar[buf], (uint32_t)(split * 32 * sizeof(Fold<1>)));
         for (int r = 0; r < split && !stall; ++r) send(slot + (buf * split + rank) * 32 + lane, &bar[buf], r, f);
     }

@@ -337,6 +337,30 @@ def test_recurrence_stalled_wait_times_out(la, monkeypatch):
     assert torch.equal(la.recurrence_fwd(x, g)[0], want) and torch.equal(la.recurrence_bwd(x, g, chunks, x)[0], dx)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_recurrence_stalled_wait_in_a_long_sequence(la, monkeypatch, dtype):
+    """The same with steps left after the one whose wait ran out: one wait a block, not one a step."""
+    import time
+
+    import torch
+    rng = np.random.default_rng(19)
+    shape = (1, 1, 30000, 32)
+    x, g = dev(rng.normal(size=shape), dtype), dev(rng.normal(size=shape), dtype)
+    stream = torch.cuda.current_stream().cuda_stream
+    want, _, chunks = la.recurrence_fwd(x, g, save_chunks=True)
+    dx = la.recurrence_bwd(x, g, chunks, x)[0]
+    assert la.la_last_device_status(stream) == la.LA_OK
+    with monkeypatch.context() as m:
+        m.setenv("LA_DEBUG_STALL", "1")
+        m.setenv("LA_DEBUG_TIMEOUT_NS", "400000000")  # 0.4 s; a wait a step would take 3 s or more
+        for call in (lambda: la.recurrence_fwd(x, g), lambda: la.recurrence_bwd(x, g, chunks, x)):
+            t0 = time.time()
+            call()
+            assert la.la_last_device_status(stream) == la.LA_ERR_TIMEOUT
+            assert time.time() - t0 < 2
+    assert torch.equal(la.recurrence_fwd(x, g)[0], want) and torch.equal(la.recurrence_bwd(x, g, chunks, x)[0], dx)
+
+
 FIRST_CALLS = """
 import sys
 sys.path.insert(0, {root!r})
