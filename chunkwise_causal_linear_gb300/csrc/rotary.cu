@@ -111,14 +111,17 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
     HeadRows<const T> in(a.q, a.vq, a.k, a.vk, a.H, b, t, h0);
     HeadRows<T> out(a.qo, a.vqo, a.ko, a.vko, a.H, b, t, h0);
     const bool half = a.layout == LA_ROTARY_HALF;
-    int c0, c1;  // the unit's two vectors
+    // the unit's two vectors, half of the turned or copied channels apart, so that neighbouring
+    // threads have neighbouring vectors; the elements of a pair where a vector is one
+    int c0, c1;
     bool two = true;
     if (pair) {
-        c0 = half ? u * VEC : 2 * u * VEC;
-        c1 = half ? c0 + a.rot / 2 : c0 + VEC;
+        const bool apart = half || VEC > 1;
+        c0 = apart ? u * VEC : 2 * u;
+        c1 = apart ? c0 + a.rot / 2 : c0 + 1;
     } else {
-        c0 = a.rot + 2 * (u - pair_units) * VEC;
-        c1 = c0 + VEC;
+        c0 = a.rot + (u - pair_units) * VEC;
+        c1 = c0 + (units - pair_units) * VEC;
         two = c1 < a.d;
         if (!two) c1 = c0;
     }
@@ -139,7 +142,9 @@ __global__ void __launch_bounds__(ROT_THREADS, 3) rotary_kernel(const RotArgs a)
         const unsigned long long p = (unsigned long long)(a.pos ? (long long)a.pos[(size_t)b * a.L + t] : a.offset + t);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            turn_sincos(p * a.turns[u * VEC + e], s[e], c[e]);
+            // interleaved vectors hold VEC / 2 pairs each
+            const int j = half || VEC == 1 ? u * VEC + e : ((e < VEC / 2 ? c0 : c1 - VEC) >> 1) + e;
+            turn_sincos(p * a.turns[j], s[e], c[e]);
             s[e] *= a.inverse ? -a.amp : a.amp;
             c[e] *= a.amp;
         }
