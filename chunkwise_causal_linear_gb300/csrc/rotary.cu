@@ -19,7 +19,7 @@ namespace la {
 namespace {
 
 constexpr int ROT_THREADS = 256;
-constexpr int ROT_HEADS = 16;  // heads of a thread at most (B8 H16 L8192 d128: 172 us, with 8 182)
+constexpr int ROT_HEADS = 16;  // heads of a thread at most (B8 H16 L8192 d128: 167 us, with 8 or 32 171)
 
 // Heads whose loads are on the way together: with 16-byte vectors two (with four the registers leave
 // two blocks an SM, 226 us), with single elements four.
@@ -190,12 +190,23 @@ template <typename T, int VEC> int launch_rotary(RotArgs &a, int sms, cudaStream
     const int units = a.rot / (2 * VEC) + (a.d - a.rot + 2 * VEC - 1) / (2 * VEC);
     const long long blocks = ((long long)a.B * a.L * units + ROT_THREADS - 1) / ROT_THREADS;
     if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    // heads of a thread: at most ROT_HEADS, in even groups, and as many as still leave every SM eight
-    // blocks
+    // heads of a thread: at most ROT_HEADS, in even groups, or half of them, a quarter, ...: where the
+    // waves of three blocks an SM, a thread's heads and its sines (as two heads) each, are the least.
+    // B1 H8 L4096 d128: 8.6 us with 8 heads, 10 with 4, 15 with 1; B2 H12 L16383 d64: 37.5 with 6 in
+    // 4.5 waves, 39 with 12 in 2.2
     const int all = a.H + a.Hk, even = (all + ROT_HEADS - 1) / ROT_HEADS;
     a.heads = (all + even - 1) / even;
     auto groups = [&] { return (all + a.heads - 1) / a.heads; };
-    while (a.heads > 1 && blocks * groups() < 8ll * sms) a.heads = (a.heads + 1) / 2;
+    auto cost = [&] { return (blocks * groups() + 3ll * sms - 1) / (3ll * sms) * (a.heads + 2); };
+    int best = a.heads;
+    for (long long least = cost(); a.heads > 1;) {
+        a.heads = (a.heads + 1) / 2;
+        if (cost() < least) {
+            least = cost();
+            best = a.heads;
+        }
+    }
+    a.heads = best;
     while (groups() > 65535) a.heads *= 2;  // limit of the grid
     const int ny = groups();
     return launch(rotary_kernel<T, VEC>, dim3((unsigned)blocks, (unsigned)ny), ROT_THREADS, 0, s, a);
