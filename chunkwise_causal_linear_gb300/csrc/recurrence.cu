@@ -116,6 +116,32 @@ template <int KIND> __device__ __forceinline__ float keep_gate()
     return KIND == LA_GATE_VALUE ? 1.f : KIND == LA_GATE_LOG ? 0.f : __int_as_float(0x7f800000);
 }
 
+// The gate input of a = 0.
+template <int KIND> __device__ __forceinline__ bool forgets(float g)
+{
+    return KIND == LA_GATE_VALUE ? g == 0.f : g == __int_as_float(0xff800000);
+}
+
+// A product of gates P is 0 if and only if one of them is, so that P, too, forgets what a gate of 0
+// forgets and nothing else.  One that fp32 rounds to 0 although no factor is 0 (gates of 0.44 over
+// 128 rows) is kept at the smallest number of its sign: a finite state comes out no farther off than
+// by a rounding of P, an infinity or NaN as itself.
+__device__ __forceinline__ float least(float p) { return copysignf(__int_as_float(1), p); }
+template <int V> __device__ __forceinline__ Ch<V> product(const Ch<V> &a, const Ch<V> &p)
+{
+    Ch<V> r = mul(a, p);
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.v[v] = r.v[v] == 0.f && a.v[v] != 0.f && p.v[v] != 0.f ? least(r.v[v]) : r.v[v];
+    return r;
+}
+template <int V> __device__ __forceinline__ bool is_zero(const Ch<V> &p)
+{
+    bool z = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) z = z || p.v[v] == 0.f;
+    return z;
+}
+
 // The state times a gate (or a product of gates), a gate of 0 forgetting infinities and NaN as
 // well.
 template <int V> __device__ __forceinline__ Ch<V> forget(const Ch<V> &a, const Ch<V> &h)
@@ -306,9 +332,23 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
         Ch<V> a, c;
         gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
         f.h = step(a, f.h, COMP ? mul(c, x) : x);
-        f.p = mul(f.p, a);
+        f.p = product(f.p, a);
     }
     return f;
+}
+// The product of a run's gates where the plain one is 0.
+template <typename G, int KIND, int V, int R> __device__ __forceinline__ Ch<V> product_exact(const G *sg, Ch<V> p)
+{
+    bool zero[V] = {};
+#pragma unroll 4
+    for (int i = 0; i < R; ++i) {
+        const Ch<V> g = get<V>(sg + i * 32 * V);
+#pragma unroll
+        for (int v = 0; v < V; ++v) zero[v] = zero[v] || forgets<KIND>(g.v[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.v[v] = zero[v] ? 0.f : p.v[v] == 0.f ? least(p.v[v]) : p.v[v];
+    return p;
 }
 // out: this lane's channels of the first row; `present` rows of it exist
 template <typename T, typename G, int KIND, bool COMP, int V>
@@ -350,7 +390,7 @@ template <int V> __device__ __noinline__ Fold<V> join_exact(const Fold<V> *f, in
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
         t.h = step(f[i * stride].p, t.h, f[i * stride].h);
-        t.p = mul(f[i * stride].p, t.p);
+        t.p = product(f[i * stride].p, t.p);
     }
     return t;
 }
@@ -594,6 +634,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
             }
             own = Pr::join(p, f);
             if (on && !finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
+            else if (on && is_zero(own.p)) own.p = product_exact<G, KIND, V, R>(sg, own.p);
         }
         agg[warp * 32 + lane] = own;
         __syncthreads();
@@ -603,13 +644,16 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
             if constexpr (SPLIT) {
                 // the fold of the tile, for the other blocks
                 Fold<V> t = f8[0];
+                bool zero = is_zero(t.p);
 #pragma unroll
                 for (int w = 1; w < REC_W; ++w) {
                     const Fold<V> q = f8[w * 32];
                     t.h = fma(q.p, t.h, q.h);
                     t.p = mul(q.p, t.p);
+                    zero = zero || is_zero(q.p);
                 }
                 if (on && !finite(t.h)) t = join_exact<V>(f8, 32, REC_W);
+                else if (!zero && is_zero(t.p)) t.p.v[0] = least(t.p.v[0]);
                 peers.publish(buf, lane, t);
                 e = peers.over(buf, parity, lane, on, carry);
             }
@@ -744,6 +788,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             const Fold<V> o = Pr::join(p, f);
             own = {o.p, o.h, Pr::join_back(p, g2)};
             if (on && (!finite(own.h) || !finite(own.e))) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
+            else if (on && is_zero(own.p)) own.p = product_exact<G, KIND, V, R>(sg, own.p);
         }
         agg[warp * 32 + lane] = Fold<V>{own.p, own.e};
         front[warp * 32 + lane] = own.h;
@@ -753,13 +798,16 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             Ch<V> e = carry;
             if constexpr (SPLIT) {
                 Fold<V> t = f8[(REC_W - 1) * 32];
+                bool zero = is_zero(t.p);
 #pragma unroll
                 for (int w = REC_W - 2; w >= 0; --w) {
                     const Fold<V> q = f8[w * 32];
                     t.h = fma(q.p, t.h, q.h);
                     t.p = mul(q.p, t.p);
+                    zero = zero || is_zero(q.p);
                 }
                 if (on && !finite(t.h)) t = join_exact<V>(f8 + (REC_W - 1) * 32, -32, REC_W);
+                else if (!zero && is_zero(t.p)) t.p.v[0] = least(t.p.v[0]);
                 peers.publish(buf, lane, t);
                 e = peers.over(buf, parity, lane, on, carry);
             }
