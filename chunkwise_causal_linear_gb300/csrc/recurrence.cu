@@ -122,6 +122,21 @@ template <int KIND> __device__ __forceinline__ bool forgets(float g)
     return KIND == LA_GATE_VALUE ? g == 0.f : g == __int_as_float(0xff800000);
 }
 
+// gate_of() flushes what is below the normal range.  Where something is not finite the difference
+// counts: an a of 0 forgets it, a 1 - a of 0 makes it NaN.  There, and in the decoding step, such a
+// gate is kept at the smallest number.
+template <int KIND, bool WANT_C, int V> __device__ __forceinline__ void gate_exact(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
+{
+    gate_of<KIND, WANT_C, V>(g, a, c);
+    if (KIND == LA_GATE_VALUE) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (a.v[v] == 0.f && !forgets<KIND>(g.v[v])) a.v[v] = __int_as_float(1);
+        if (WANT_C && KIND == LA_GATE_SIGMOID && c.v[v] == 0.f && fabsf(g.v[v]) < __int_as_float(0x7f800000))
+            c.v[v] = __int_as_float(1);
+    }
+}
+
 // A product of gates P is 0 if and only if one of them is, so that P, too, forgets what a gate of 0
 // forgets and nothing else.  One that fp32 rounds to 0 although no factor is 0 (gates of 0.44 over
 // 128 rows) is kept at the smallest number of its sign: a finite state comes out no farther off than
@@ -330,7 +345,7 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
     for (int i = 0; i < rows; ++i) {
         const Ch<V> x = get<V>(sx + i * 32 * V);
         Ch<V> a, c;
-        gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        gate_exact<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
         f.h = step(a, f.h, COMP ? mul(c, x) : x);
         f.p = product(f.p, a);
     }
@@ -360,7 +375,7 @@ __device__ __noinline__ void finish_rows(const T *sx, const G *sg, int rows, int
         if (i < rows) {
             const Ch<V> x = get<V>(sx + i * 32 * V);
             Ch<V> a, c;
-            gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+            gate_exact<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
             h = step(a, h, COMP ? mul(c, x) : x);
         }
         put<V>(out, i < rows ? h : all<V>(0.f));
@@ -406,7 +421,7 @@ __device__ __noinline__ BwdFold<V> fold_rows_bwd(const T *sx, const T *sd, const
 #pragma unroll 1
     for (int i = rows - 1; i >= 0; --i) {
         Ch<V> a, c;
-        gate_of<KIND, false, V>(get<V>(sg + i * 32 * V), a, c);
+        gate_exact<KIND, false, V>(get<V>(sg + i * 32 * V), a, c);
         e = forget(a, add(e, get<V>(sd + i * 32 * V)));
     }
     return {f.p, f.h, e};
@@ -421,7 +436,7 @@ __device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *
     for (int i = 0; i < rows; ++i) {
         const Ch<V> x = get<V>(sx + i * 32 * V);
         Ch<V> a, c;
-        gate_of<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        gate_exact<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
         before[i] = h;
         h = step(a, h, COMP ? mul(c, x) : x);
     }
@@ -431,12 +446,18 @@ __device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *
         if (i < rows) {
             const Ch<V> hb = before[i], x = get<V>(sx + i * 32 * V);
             Ch<V> a, c;
-            gate_of<KIND, COMP || KIND == LA_GATE_SIGMOID, V>(get<V>(sg + i * 32 * V), a, c);
+            gate_exact<KIND, COMP || KIND == LA_GATE_SIGMOID, V>(get<V>(sg + i * 32 * V), a, c);
             e = add(e, get<V>(sd + i * 32 * V));
             rx = COMP ? mul(c, e) : e;
             const Ch<V> f = COMP ? fma(x, all<V>(-1.f), hb) : hb, ae = forget(a, e);
-            if (KIND == LA_GATE_VALUE) rg = mul(e, f);
-            else rg = forget(KIND == LA_GATE_LOG ? ae : forget(c, ae), f);
+            const Ch<V> slope = KIND == LA_GATE_VALUE ? all<V>(1.f) : KIND == LA_GATE_LOG ? a : mul(c, a);
+            const Ch<V> se = KIND == LA_GATE_VALUE ? e : KIND == LA_GATE_LOG ? ae : mul(c, ae);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                // a small se is not to round an infinite f away
+                const float r = fabsf(f.v[v]) <= 3.402823466e38f ? se.v[v] * f.v[v] : slope.v[v] * (e.v[v] * f.v[v]);
+                rg.v[v] = slope.v[v] == 0.f ? 0.f : r;
+            }
             e = ae;
         }
         put<V>(dx + i * dx_stride, rx);
@@ -893,7 +914,7 @@ __global__ void __launch_bounds__(STEP_THREADS) rec_step_kernel(const T *x, cons
     const long long i = (long long)blockIdx.x * STEP_THREADS + threadIdx.x;
     if (i >= n) return;
     Ch<1> ga, c;
-    gate_of<KIND, COMP, 1>({{to_f32(g[i])}}, ga, c);
+    gate_exact<KIND, COMP, 1>({{to_f32(g[i])}}, ga, c);
     const Ch<1> xv{{to_f32(x[i])}}, h = step(ga, {{state[i]}}, COMP ? mul(c, xv) : xv);
     state[i] = h.v[0];
     out[i] = from_f32<T>(h.v[0]);

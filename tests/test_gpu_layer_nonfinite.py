@@ -124,3 +124,46 @@ def test_small_gates_do_not_forget(la, shape, gate, kind, complement, dtype, gat
     same_kind("dx", dx, wx)
     same_kind("dg", dg, wg, UNSIGNED)
     same_kind("dh0", dh0, w0)
+
+
+@pytest.mark.parametrize("kind", ["log", "sigmoid"])
+@pytest.mark.parametrize("g", [-88.0, -100.0, -300.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gates_below_the_normal_range_do_not_forget(la, kind, g, dtype):
+    """exp(-100) is not 0, though fp32 has no normal number for it."""
+    rng = np.random.default_rng(21)
+    for shape in ((1, 2, 700, 64), (2, 80, 40, 64)):
+        L = shape[2]
+        x, gate = rng.normal(size=shape), np.full(shape, 2.0 if kind == "sigmoid" else -0.1)
+        gate[:, :, L // 2] = g
+        x[0, 0, 3], x[-1, -1, 3] = np.inf, np.nan
+        tx, tg = dev(x, dtype), dev(gate, dtype)
+        want, _, last = forward(host(tx), host(tg), kind, False, None)
+        out, got_last = la.recurrence_fwd(tx, tg, gate_kind=kind)
+        same_kind("out", out, want)
+        same_kind("last", got_last, last)
+        state = dev(want[:, :, L // 2 - 1])
+        step = la.recurrence_step(tx[:, :, L // 2].contiguous(), tg[:, :, L // 2].contiguous(), state, gate_kind=kind)
+        same_kind("step", step, want[:, :, L // 2])
+        same_kind("state", state, want[:, :, L // 2])
+
+
+def test_complement_below_the_normal_range(la):
+    """1 - a of a logit of 100 is not 0 either: an infinite input comes through, and its gradient."""
+    rng = np.random.default_rng(23)
+    for shape in ((1, 2, 700, 64), (2, 80, 40, 64)):
+        x, g, dout = rng.normal(size=shape), np.full(shape, 2.0), rng.normal(size=shape)
+        row = shape[2] // 2
+        g[:, :, row] = 100.0
+        x[0, 0, row], dout[-1, -1, row] = np.inf, -np.inf
+        x, dout = host(dev(x)), host(dev(dout))
+        want, before, _ = forward(x, g, "sigmoid", True, None)
+        out, _, chunks = la.recurrence_fwd(dev(x), dev(g), complement=True, save_chunks=True)
+        same_kind("out", out, want)
+        wx, wg, w0 = backward(x, g, dout, before, "sigmoid", True)
+        dx, dg, dh0 = la.recurrence_bwd(dev(x), dev(g), chunks, dev(dout), complement=True)
+        same_kind("dx", dx, wx)
+        same_kind("dg", dg, wg, UNSIGNED)
+        same_kind("dh0", dh0, w0)
+        step = la.recurrence_step(dev(x[:, :, row]), dev(g[:, :, row]), dev(before[:, :, row]), complement=True)
+        same_kind("step", step, want[:, :, row])
