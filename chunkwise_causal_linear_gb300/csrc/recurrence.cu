@@ -140,21 +140,22 @@ template <int KIND, bool WANT_C, int V> __device__ __forceinline__ void gate_exa
 // A product of gates P is 0 if and only if one of them is, so that P, too, forgets what a gate of 0
 // forgets and nothing else.  One that fp32 rounds to 0 although no factor is 0 (gates of 0.44 over
 // 128 rows) is kept at the smallest number of its sign: a finite state comes out no farther off than
-// by a rounding of P, an infinity or NaN as itself.
+// by a rounding of P, an infinity or NaN as itself.  An infinite or NaN gate does not outlive a 0.
 __device__ __forceinline__ float least(float p) { return copysignf(__int_as_float(1), p); }
 template <int V> __device__ __forceinline__ Ch<V> product(const Ch<V> &a, const Ch<V> &p)
 {
     Ch<V> r = mul(a, p);
 #pragma unroll
-    for (int v = 0; v < V; ++v) r.v[v] = r.v[v] == 0.f && a.v[v] != 0.f && p.v[v] != 0.f ? least(r.v[v]) : r.v[v];
+    for (int v = 0; v < V; ++v) r.v[v] = a.v[v] == 0.f || p.v[v] == 0.f ? 0.f : r.v[v] == 0.f ? least(r.v[v]) : r.v[v];
     return r;
 }
-template <int V> __device__ __forceinline__ bool is_zero(const Ch<V> &p)
+// Not 0, infinite or NaN: then the plain product is the one above.
+template <int V> __device__ __forceinline__ bool regular(const Ch<V> &p)
 {
-    bool z = false;
+    bool ok = true;
 #pragma unroll
-    for (int v = 0; v < V; ++v) z = z || p.v[v] == 0.f;
-    return z;
+    for (int v = 0; v < V; ++v) ok = ok && fabsf(p.v[v]) > 0.f && fabsf(p.v[v]) <= 3.402823466e38f;
+    return ok;
 }
 
 // The state times a gate (or a product of gates), a gate of 0 forgetting infinities and NaN as
@@ -351,7 +352,7 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
     }
     return f;
 }
-// The product of a run's gates where the plain one is 0.
+// The product of a run's gates where the plain one is not regular.
 template <typename G, int KIND, int V, int R> __device__ __forceinline__ Ch<V> product_exact(const G *sg, Ch<V> p)
 {
     bool zero[V] = {};
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
             }
             own = Pr::join(p, f);
             if (on && !finite(own.h)) own = fold_rows<T, G, KIND, COMP, V>(sx, sg, rows);
-            else if (on && is_zero(own.p)) own.p = product_exact<G, KIND, V, R>(sg, own.p);
+            else if (on && !regular(own.p)) own.p = product_exact<G, KIND, V, R>(sg, own.p);
         }
         agg[warp * 32 + lane] = own;
         __syncthreads();
@@ -665,16 +666,16 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
             if constexpr (SPLIT) {
                 // the fold of the tile, for the other blocks
                 Fold<V> t = f8[0];
-                bool zero = is_zero(t.p);
+                bool zero = t.p.v[0] == 0.f;
 #pragma unroll
                 for (int w = 1; w < REC_W; ++w) {
                     const Fold<V> q = f8[w * 32];
                     t.h = fma(q.p, t.h, q.h);
                     t.p = mul(q.p, t.p);
-                    zero = zero || is_zero(q.p);
+                    zero = zero || q.p.v[0] == 0.f;
                 }
                 if (on && !finite(t.h)) t = join_exact<V>(f8, 32, REC_W);
-                else if (!zero && is_zero(t.p)) t.p.v[0] = least(t.p.v[0]);
+                else t.p.v[0] = zero ? 0.f : t.p.v[0] == 0.f ? least(t.p.v[0]) : t.p.v[0];
                 peers.publish(buf, lane, t);
                 e = peers.over(buf, parity, lane, on, carry);
             }
@@ -809,7 +810,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             const Fold<V> o = Pr::join(p, f);
             own = {o.p, o.h, Pr::join_back(p, g2)};
             if (on && (!finite(own.h) || !finite(own.e))) own = fold_rows_bwd<T, G, KIND, COMP, V>(sx, sd, sg, rows);
-            else if (on && is_zero(own.p)) own.p = product_exact<G, KIND, V, R>(sg, own.p);
+            else if (on && !regular(own.p)) own.p = product_exact<G, KIND, V, R>(sg, own.p);
         }
         agg[warp * 32 + lane] = Fold<V>{own.p, own.e};
         front[warp * 32 + lane] = own.h;
@@ -819,16 +820,16 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             Ch<V> e = carry;
             if constexpr (SPLIT) {
                 Fold<V> t = f8[(REC_W - 1) * 32];
-                bool zero = is_zero(t.p);
+                bool zero = t.p.v[0] == 0.f;
 #pragma unroll
                 for (int w = REC_W - 2; w >= 0; --w) {
                     const Fold<V> q = f8[w * 32];
                     t.h = fma(q.p, t.h, q.h);
                     t.p = mul(q.p, t.p);
-                    zero = zero || is_zero(q.p);
+                    zero = zero || q.p.v[0] == 0.f;
                 }
                 if (on && !finite(t.h)) t = join_exact<V>(f8 + (REC_W - 1) * 32, -32, REC_W);
-                else if (!zero && is_zero(t.p)) t.p.v[0] = least(t.p.v[0]);
+                else t.p.v[0] = zero ? 0.f : t.p.v[0] == 0.f ? least(t.p.v[0]) : t.p.v[0];
                 peers.publish(buf, lane, t);
                 e = peers.over(buf, parity, lane, on, carry);
             }

@@ -69,6 +69,8 @@ def same_kind(name, got, want, kinds=None):
 
 # the sign of an infinite gradient of the gate is that of h - x, which may be a rounding apart from 0
 UNSIGNED = {"NaN": np.isnan, "infinity": np.isinf}
+# an infinite gate makes infinities of either sign, whose sums NaN depend on how rows are grouped
+FINITE = {"finite": np.isfinite}
 
 
 def steady(kind, a):
@@ -167,3 +169,37 @@ def test_complement_below_the_normal_range(la):
         same_kind("dh0", dh0, w0)
         step = la.recurrence_step(dev(x[:, :, row]), dev(g[:, :, row]), dev(before[:, :, row]), complement=True)
         same_kind("step", step, want[:, :, row])
+
+
+@pytest.mark.parametrize("row", [0, 2, 16, 130])
+@pytest.mark.parametrize("apart", [1, 11, 200])
+@pytest.mark.parametrize("kind,bad", [("value", np.nan), ("value", np.inf), ("log", np.nan), ("log", np.inf),
+                                      ("sigmoid", np.nan)])
+def test_gate_zero_forgets_a_bad_gate(la, row, apart, kind, bad):
+    """A NaN or infinite gate reaches no row from the next gate of 0 on; backwards no row before it."""
+    rng = np.random.default_rng(22)
+    kinds = KINDS if np.isnan(bad) else FINITE
+    for shape, dtype in (((1, 2, 600, 64), "f32"), ((2, 80, 350, 34), "f32"), ((2, 80, 350, 34), "bf16")):
+        L, zero = shape[2], row + apart
+        x, g = rng.normal(size=shape), np.full(shape, steady(kind, 0.9))
+        g[:, :, row], g[:, :, zero] = bad, 0.0 if kind == "value" else -np.inf
+        tx, tg = dev(x, dtype), dev(g, dtype)
+        hx, hg = host(tx), host(tg)
+        want, before, last = forward(hx, hg, kind, False, None)
+        out, got_last, chunks = la.recurrence_fwd(tx, tg, gate_kind=kind, save_chunks=True)
+        same_kind("out", out, want, kinds)
+        same_kind("last", got_last, last, kinds)
+        same_kind("chunks", chunks, before[:, :, ::la.LA_RECURRENCE_CHUNK], kinds)
+        tail = ref.recurrence_bounds(hx[:, :, zero:], hg[:, :, zero:], kind, False)
+        check("rows behind", out[:, :, zero:], want[:, :, zero:], tail, dtype)
+        # backwards: the bad gate behind the zero one
+        g[:, :, row], g[:, :, zero] = g[:, :, zero].copy(), bad
+        tg = dev(g, dtype)
+        do = dev(rng.normal(size=shape), dtype)
+        want, before, _ = forward(hx, host(tg), kind, False, None)
+        wx, wg, w0 = backward(hx, host(tg), host(do), before, kind, False)
+        chunks = la.recurrence_fwd(tx, tg, gate_kind=kind, save_chunks=True)[2]
+        dx, dg, dh0 = la.recurrence_bwd(tx, tg, chunks, do, gate_kind=kind)
+        same_kind("dx", dx, wx, kinds)
+        same_kind("dg", dg, wg, kinds)
+        same_kind("dh0", dh0, w0, kinds)
