@@ -44,6 +44,7 @@ namespace {
 constexpr int RC = LA_RECURRENCE_CHUNK;  // rows between the states that the forward leaves
 constexpr int REC_W = 8;                 // warps of a tile
 constexpr int REC_THREADS = 32 * REC_W;
+template <typename T> constexpr bool ACC = sizeof(T) == 4;  // see gate_of
 constexpr int BWD_R = 16;                // rows of a warp, backward
 constexpr int REC_MAX_SPLIT = 16;        // blocks of a cluster; above 8 asks for the larger size this GPU has
 
@@ -63,25 +64,44 @@ struct RecArgs {
     int debug_stall;    // test knob: nothing is sent to the other blocks (forces a timeout)
 };
 
-// a and 1 - a from the gate input, 1 - a (computed where WANT_C) from its own formula where a is
-// close to 1.  With u = 2^-24 both are off by at most (9 + 1.3 |g|) u relatively: the argument
-// g log2(e) is rounded (1.3 |g| u), 2^x 4 u, the sum 1 u, the reciprocal 2 u, a product or
-// difference 1 u.  Accurate versions of the exponential and the quotient cost 20 more
-// instructions an element and made the bf16 kernel 1.6 times slower than with plain gates.
-template <int KIND, bool WANT_C, int V>
+// a and 1 - a from the gate input.  u = 2^-24.
+//
+// With bf16 activations both are off by at most (9 + 1.3 |g|) u relatively: the argument g log2(e) of
+// the special function unit's 2^x is rounded (1.3 |g| u), 2^x 4 u, the sum 1 u, the reciprocal 2 u, a
+// product or difference 1 u.  Next to 1, where a long memory adds the error of a up row by row, that
+// is 2 u (measured): half a step of the bf16 output after 32768 rows.
+//
+// With fp32 activations (FINE) an a next to 1 is good to a rounding: it is 1 less 1 - a, which alone
+// comes from the series or the exponential; and the exponential of a sigmoid has what its argument's
+// rounding left out multiplied in, so that the smaller of a and 1 - a is off by at most 9 u.
+constexpr float LOG2E = 1.44269504f, LN2 = 0.693147182f, LN2_REST = -1.90465432e-9f;  // log 2 = LN2 + LN2_REST
+template <int V> __device__ __forceinline__ Ch<V> pow2(Ch<V> t)
+{
+#pragma unroll
+    for (int v = 0; v < V; ++v) t.v[v] = ex2(t.v[v]);
+    return t;
+}
+template <int KIND, bool WANT_C, bool FINE, int V>
 __device__ __forceinline__ void gate_of(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
 {
-    constexpr float LOG2E = 1.44269504f;
     if (KIND == LA_GATE_VALUE) {
         a = g;
         if (WANT_C) c = fma(g, all<V>(-1.f), all<V>(1.f));
     } else if (KIND == LA_GATE_LOG) {
-        const Ch<V> t = mul(g, all<V>(LOG2E));
+        a = pow2(mul(g, all<V>(LOG2E)));
+        if (FINE && !WANT_C) {
+            // e^g by its series below 2^-4 (the first term left out is 2^-27); the error of the
+            // power counts 1 / (1 - a) <= 17 times elsewhere
+            Ch<V> p = fma(g, all<V>(1.f / 24), all<V>(1.f / 6));
+            p = fma(g, p, all<V>(0.5f));
+            p = fma(g, p, all<V>(1.f));
+            const Ch<V> near = fma(g, p, all<V>(1.f));
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.v[v] = ex2(t.v[v]);
+            for (int v = 0; v < V; ++v) a.v[v] = fabsf(g.v[v]) < 0.0625f ? near.v[v] : a.v[v];
+        }
         if (WANT_C) {
-            // -expm1(g): below log 2 from s = expm1(g / 2) by its series, expm1(g) = s (s + 2)
-            // (the first term left out is 2e-8 of the sum)
+            // below log 2 from s = expm1(g / 2) by its series, expm1(g) = s (s + 2) (the first term
+            // left out is 2e-8 of the sum)
             const Ch<V> y = mul(g, all<V>(0.5f));
             Ch<V> p = fma(y, all<V>(1.f / 5040), all<V>(1.f / 720));
             p = fma(y, p, all<V>(1.f / 120));
@@ -89,17 +109,37 @@ __device__ __forceinline__ void gate_of(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
             p = fma(y, p, all<V>(1.f / 6));
             p = fma(y, p, all<V>(0.5f));
             p = fma(y, p, all<V>(1.f));
-            const Ch<V> s = mul(y, p), n = mul(s, all<V>(-1.f));
-            const Ch<V> e = mul(n, add(s, all<V>(2.f))), f = fma(a, all<V>(-1.f), all<V>(1.f));
+            const Ch<V> s = mul(y, p), q = add(s, all<V>(2.f));
+            const Ch<V> e = mul(mul(s, all<V>(-1.f)), q), f = fma(a, all<V>(-1.f), all<V>(1.f)),
+                        near = fma(s, q, all<V>(1.f));
 #pragma unroll
-            for (int v = 0; v < V; ++v) c.v[v] = fabsf(g.v[v]) < 0.693f ? e.v[v] : f.v[v];
+            for (int v = 0; v < V; ++v) {
+                const bool series = fabsf(g.v[v]) < 0.693f;
+                c.v[v] = series ? e.v[v] : f.v[v];
+                if (FINE && series) a.v[v] = near.v[v];
+            }
+        }
+    } else if (FINE) {
+        // -|g|, not below what 2^x makes 0 of: the argument's rest is then finite.  A NaN stays.
+        Ch<V> m;
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.v[v]) : "f"(-fabsf(g.v[v])), "f"(-150.f));
+        // e^m = 2^t e^(m - t log 2), whose last exponent is below 2^-16
+        const Ch<V> t = mul(m, all<V>(LOG2E)), rest = fma(t, all<V>(-LN2_REST), fma(t, all<V>(-LN2), m));
+        Ch<V> e = pow2(t);
+        e = fma(e, rest, e);
+        Ch<V> r = add(e, all<V>(1.f));
+#pragma unroll
+        for (int v = 0; v < V; ++v) r.v[v] = rcp(r.v[v]);
+        const Ch<V> less = mul(e, r), more = fma(less, all<V>(-1.f), all<V>(1.f));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            a.v[v] = g.v[v] < 0.f ? less.v[v] : more.v[v];
+            if (WANT_C) c.v[v] = g.v[v] < 0.f ? more.v[v] : less.v[v];
         }
     } else {
         // a = 1 / (1 + e), 1 - a = e a; where e is so large that a is 0, 1 - a is 1
-        Ch<V> e = mul(g, all<V>(-LOG2E));
-#pragma unroll
-        for (int v = 0; v < V; ++v) e.v[v] = ex2(e.v[v]);
-        const Ch<V> d = add(e, all<V>(1.f));
+        const Ch<V> e = pow2(mul(g, all<V>(-LOG2E))), d = add(e, all<V>(1.f));
 #pragma unroll
         for (int v = 0; v < V; ++v) a.v[v] = rcp(d.v[v]);
         if (WANT_C) {
@@ -125,9 +165,10 @@ template <int KIND> __device__ __forceinline__ bool forgets(float g)
 // gate_of() flushes what is below the normal range.  Where something is not finite the difference
 // counts: an a of 0 forgets it, a 1 - a of 0 makes it NaN.  There, and in the decoding step, such a
 // gate is kept at the smallest number.
-template <int KIND, bool WANT_C, int V> __device__ __forceinline__ void gate_exact(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
+template <int KIND, bool WANT_C, bool FINE, int V>
+__device__ __forceinline__ void gate_exact(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
 {
-    gate_of<KIND, WANT_C, V>(g, a, c);
+    gate_of<KIND, WANT_C, FINE, V>(g, a, c);
     if (KIND == LA_GATE_VALUE) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -346,7 +387,7 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
     for (int i = 0; i < rows; ++i) {
         const Ch<V> x = get<V>(sx + i * 32 * V);
         Ch<V> a, c;
-        gate_exact<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        gate_exact<KIND, COMP, ACC<T>, V>(get<V>(sg + i * 32 * V), a, c);
         f.h = step(a, f.h, COMP ? mul(c, x) : x);
         f.p = product(f.p, a);
     }
@@ -376,7 +417,7 @@ __device__ __noinline__ void finish_rows(const T *sx, const G *sg, int rows, int
         if (i < rows) {
             const Ch<V> x = get<V>(sx + i * 32 * V);
             Ch<V> a, c;
-            gate_exact<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+            gate_exact<KIND, COMP, ACC<T>, V>(get<V>(sg + i * 32 * V), a, c);
             h = step(a, h, COMP ? mul(c, x) : x);
         }
         put<V>(out, i < rows ? h : all<V>(0.f));
@@ -422,7 +463,7 @@ __device__ __noinline__ BwdFold<V> fold_rows_bwd(const T *sx, const T *sd, const
 #pragma unroll 1
     for (int i = rows - 1; i >= 0; --i) {
         Ch<V> a, c;
-        gate_exact<KIND, false, V>(get<V>(sg + i * 32 * V), a, c);
+        gate_exact<KIND, false, ACC<T>, V>(get<V>(sg + i * 32 * V), a, c);
         e = forget(a, add(e, get<V>(sd + i * 32 * V)));
     }
     return {f.p, f.h, e};
@@ -437,7 +478,7 @@ __device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *
     for (int i = 0; i < rows; ++i) {
         const Ch<V> x = get<V>(sx + i * 32 * V);
         Ch<V> a, c;
-        gate_exact<KIND, COMP, V>(get<V>(sg + i * 32 * V), a, c);
+        gate_exact<KIND, COMP, ACC<T>, V>(get<V>(sg + i * 32 * V), a, c);
         before[i] = h;
         h = step(a, h, COMP ? mul(c, x) : x);
     }
@@ -447,7 +488,7 @@ __device__ __noinline__ void finish_rows_bwd(const T *sx, const T *sd, const G *
         if (i < rows) {
             const Ch<V> hb = before[i], x = get<V>(sx + i * 32 * V);
             Ch<V> a, c;
-            gate_exact<KIND, COMP || KIND == LA_GATE_SIGMOID, V>(get<V>(sg + i * 32 * V), a, c);
+            gate_exact<KIND, COMP || KIND == LA_GATE_SIGMOID, ACC<T>, V>(get<V>(sg + i * 32 * V), a, c);
             e = add(e, get<V>(sd + i * 32 * V));
             rx = COMP ? mul(c, e) : e;
             const Ch<V> f = COMP ? fma(x, all<V>(-1.f), hb) : hb, ae = forget(a, e);
@@ -581,8 +622,16 @@ template <typename T, typename G, int V, bool BWD, bool SPLIT> struct RecSmem {
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
 
 // ---- forward ---------------------------------------------------------------------------------
+// Blocks an SM that the registers are to leave room for.  With fp32 activations and gates shared memory
+// holds two, and the exact gates take more than 80 registers (B1 H16 L65536 d64, log gates: 124 us, with
+// the bound of three blocks 144); gates that are values need fewer (124 us, with the bound of two 130).
+template <typename T, typename G, int KIND, int V, int R> constexpr int fwd_blocks()
+{
+    return V == 1 && R == 16 && (sizeof(T) + sizeof(G) < 8 || KIND == LA_GATE_VALUE) ? 3 : 2;
+}
+
 template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
-__global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false, SPLIT>::R == 16 ? 3 : 2)
+__global__ void __launch_bounds__(REC_THREADS, fwd_blocks<T, G, KIND, V, RecSmem<T, G, V, false, SPLIT>::R>())
     rec_fwd_kernel(const RecArgs a)
 {
     using Sm = RecSmem<T, G, V, false, SPLIT>;
@@ -644,7 +693,7 @@ __global__ void __launch_bounds__(REC_THREADS, V == 1 && RecSmem<T, G, V, false,
             for (int i = 0; i < Pr::N; ++i) {
                 const Ch<2> xv = Pr::get(sx, i);
                 Ch<2> w;
-                gate_of<KIND, COMP, 2>(Pr::get(sg, i), ga[i], w);
+                gate_of<KIND, COMP, ACC<T>, 2>(Pr::get(sg, i), ga[i], w);
                 bx[i] = COMP ? mul(w, xv) : xv;
             }
             p = ga[0];
@@ -794,7 +843,7 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
 #pragma unroll
             for (int i = 0; i < Pr::N; ++i) {
                 const Ch<2> xv = Pr::get(sx, i);
-                gate_of<KIND, WANT_C, 2>(Pr::get(sg, i), ga[i], cc[i]);
+                gate_of<KIND, WANT_C, ACC<T>, 2>(Pr::get(sg, i), ga[i], cc[i]);
                 hb[i] = COMP ? mul(cc[i], xv) : xv;
             }
             p = ga[0];
@@ -915,7 +964,7 @@ __global__ void __launch_bounds__(STEP_THREADS) rec_step_kernel(const T *x, cons
     const long long i = (long long)blockIdx.x * STEP_THREADS + threadIdx.x;
     if (i >= n) return;
     Ch<1> ga, c;
-    gate_exact<KIND, COMP, 1>({{to_f32(g[i])}}, ga, c);
+    gate_exact<KIND, COMP, ACC<T>, 1>({{to_f32(g[i])}}, ga, c);
     const Ch<1> xv{{to_f32(x[i])}}, h = step(ga, {{state[i]}}, COMP ? mul(c, xv) : xv);
     state[i] = h.v[0];
     out[i] = from_f32<T>(h.v[0]);

@@ -467,6 +467,10 @@ enum la_gate_kind {
  *   gate          [B, H, L, d], dtype `gate_dtype`; gates are meant to be in [0, 1].  Others
  *                 are computed as the formula says, but rows are combined through products of
  *                 up to 256 gates in fp32: where those overflow, the result is not finite.
+ *                 With u = 2^-24, a and 1 - a are evaluated in fp32 to (9 + 1.3 |g|) u
+ *                 relatively, values below 2^-126 absolutely; for fp32 activations an a above 1/2
+ *                 (log gates: above 15/16, or with complement) is off by u/2 and 9 u of 1 - a,
+ *                 so that long memories keep their gain.
  *   h0            device fp32 [B, H, d], the state before row 0, or NULL for zero
  *   lengths       NULL, or device int [B]: sequence b ends after lengths[b] rows (clamped to
  *                 0..L).  Rows behind are not read; out is 0 there and the state stays.
