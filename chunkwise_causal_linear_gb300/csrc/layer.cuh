@@ -167,4 +167,29 @@ __device__ __forceinline__ Ch<2> add(Ch<2> a, Ch<2> b)
     return r;
 }
 
+__device__ __forceinline__ float min_nan(float x, float y)  // a NaN stays
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+// e^x to 5 u (u = 2^-24) for x of [-150, 88.7] (or NaN): the power of two 4 u, and what the rounding of
+// its argument left out, |x| u and more, multiplied in.
+template <int V> __device__ __forceinline__ Ch<V> exp_fine(const Ch<V> &x)
+{
+    constexpr float LOG2E = 1.44269504f, LN2 = 0.693147182f, LN2_REST = -1.90465432e-9f;  // log 2 = LN2 + LN2_REST
+    // e^x = 2^t e^(x - t log 2), whose last exponent is below 2^-16
+    const Ch<V> t = mul(x, all<V>(LOG2E)), rest = fma(t, all<V>(-LN2_REST), fma(t, all<V>(-LN2), x));
+    Ch<V> e;
+#pragma unroll
+    for (int v = 0; v < V; ++v) e.v[v] = ex2(t.v[v]);
+    return fma(e, rest, e);
+}
+
 }  // namespace la

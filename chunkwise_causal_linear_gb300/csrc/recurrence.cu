@@ -74,7 +74,7 @@ struct RecArgs {
 // With fp32 activations (FINE) an a next to 1 is good to a rounding: it is 1 less 1 - a, which alone
 // comes from the series or the exponential; and the exponential of a sigmoid has what its argument's
 // rounding left out multiplied in, so that the smaller of a and 1 - a is off by at most 9 u.
-constexpr float LOG2E = 1.44269504f, LN2 = 0.693147182f, LN2_REST = -1.90465432e-9f;  // log 2 = LN2 + LN2_REST
+constexpr float LOG2E = 1.44269504f;
 template <int V> __device__ __forceinline__ Ch<V> pow2(Ch<V> t)
 {
 #pragma unroll
@@ -120,14 +120,10 @@ __device__ __forceinline__ void gate_of(const Ch<V> &g, Ch<V> &a, Ch<V> &c)
             }
         }
     } else if (FINE) {
-        // -|g|, not below what 2^x makes 0 of: the argument's rest is then finite.  A NaN stays.
-        Ch<V> m;
+        Ch<V> e;
 #pragma unroll
-        for (int v = 0; v < V; ++v) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m.v[v]) : "f"(-fabsf(g.v[v])), "f"(-150.f));
-        // e^m = 2^t e^(m - t log 2), whose last exponent is below 2^-16
-        const Ch<V> t = mul(m, all<V>(LOG2E)), rest = fma(t, all<V>(-LN2_REST), fma(t, all<V>(-LN2), m));
-        Ch<V> e = pow2(t);
-        e = fma(e, rest, e);
+        for (int v = 0; v < V; ++v) e.v[v] = max_nan(-fabsf(g.v[v]), -150.f);
+        e = exp_fine(e);
         Ch<V> r = add(e, all<V>(1.f));
 #pragma unroll
         for (int v = 0; v < V; ++v) r.v[v] = rcp(r.v[v]);

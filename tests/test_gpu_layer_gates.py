@@ -135,3 +135,34 @@ def test_steady_long_memory(la, kind, g, gate_dtype):
         bound[:, :, t] = N
     check("out", out, want, bound)
     check("last", last, wlast, N)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_silu_of_the_group_norm(la, dtype, gated):
+    """SiLU and its slope over logits to 80: y is the bias where the weight is 0.
+
+    fp32: the sigmoid s is off by 9 u relatively, f = z s by 10 u; the slope s + f (1 - s) by 9 u s, the
+    error of 1 - s (9 u s and a rounding) times |f|, 10 u |f| (1 - s) and a rounding: 10 u (s + 2 |f|) in
+    all.  bf16: (8 + 2.5 |z|) u in place of 9 u, and the rounding of the output.  A sigmoid below the
+    normal range is 0."""
+    import torch
+    H, d, n = 64, 128, 64 * 128
+    z = dev(inputs("sigmoid", np.random.default_rng(44), n), dtype)
+    x = dev(np.random.default_rng(45).normal(size=(1, H, 1, d)), dtype)
+    w, b = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda") if gated else z.float()
+    gate = z.view(1, 1, n) if gated else None
+    ones = torch.ones(1, 1, n, dtype=x.dtype, device="cuda")
+    out = host(la.group_norm_fwd(x, w, b, gate=gate)).ravel()
+    dx, dgate, dw, db = la.group_norm_bwd(x, ones, w, b, gate=gate)
+    v = host(z)
+    s, c = 1 / (1 + np.exp(-v)), 1 / (1 + np.exp(v))
+    f, slope = v * s, s + v * s * c
+    k = U * (9 if dtype == "f32" else 8 + 2.5 * np.abs(v))
+    f_b = (k + U) * np.abs(f) + TINY * np.abs(v)
+    slope_b = (k + U) * (s + 2 * np.abs(f)) + TINY * np.abs(v)
+    close("out", out, f, ref.stored(f_b, f, dtype), v)
+    # the gradient of the bias (y act(z) with a gate, act(y) without) is fp32 in either type
+    close("dbias", host(db), f if gated else slope, f_b if gated else slope_b, v)
+    if gated:  # dout y slope, y = 1
+        close("dgate", host(dgate).ravel(), slope, ref.stored(slope_b + 3 * U * np.abs(slope), slope, dtype), v)
