@@ -9,6 +9,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "layer.cuh"
@@ -552,27 +553,44 @@ int blocks_of_head(int B, int H, int L, int d, int sms, bool bwd)
     return (int)std::max(1ll, std::min(want, (rows + gpb - 1) / gpb));
 }
 
+template <auto KERN> using constant = std::integral_constant<decltype(KERN), KERN>;
+
+// A kernel's limit of dynamic shared memory, set once per device.
+template <auto KERN> bool raise_smem_limit(size_t bytes)
+{
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done[dev]) return true;
+    if (status_of(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) != LA_OK) return false;
+    return done[dev] = true;
+}
+
 template <typename T, int VEC, int TPG, int NV, bool BWD> int launch_gn(const GnArgs &a, cudaStream_t s)
 {
     const long long blocks = (long long)a.nb * a.H;
     if (blocks > INT_MAX) return LA_ERR_SHAPE;
-    auto go = [&](auto kern, auto gate) {
-        size_t smem = SourceOf<T, VEC, TPG, NV, decltype(gate)::value, BWD>::R::SMEM;
+    auto go = [&](auto kernel, auto gate) {
+        constexpr auto kern = decltype(kernel)::value;
+        constexpr size_t ring = SourceOf<T, VEC, TPG, NV, decltype(gate)::value, BWD>::R::SMEM;
+        // the limit is set once, to the most that any d asks for: two threads with different d must not
+        // undercut each other between the attribute and the launch
+        constexpr size_t most = std::max(ring, BWD ? sizeof(float) * 2 * GN_THREADS * VEC * NV : 0);
+        if (most > 47 * 1024 && !raise_smem_limit<kern>(most)) return (int)LA_ERR_CUDA;
+        size_t smem = ring;
         if (BWD && a.part) smem = std::max(smem, sizeof(float) * 2 * (GN_THREADS / TPG) * a.d);
-        if (smem > 47 * 1024 &&
-            status_of(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != LA_OK)
-            return (int)LA_ERR_CUDA;
         return launch(kern, dim3((unsigned)blocks), GN_THREADS, smem, s, a);
     };
     const bool silu = a.act == LA_ACT_SILU;
     const std::true_type yes;
     const std::false_type no;
-    if constexpr (BWD)
-        return a.gate ? silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, true, true>, yes) : go(gn_bwd_kernel<T, VEC, TPG, NV, true, false>, yes)
-                      : silu ? go(gn_bwd_kernel<T, VEC, TPG, NV, false, true>, no) : go(gn_bwd_kernel<T, VEC, TPG, NV, false, false>, no);
-    else
-        return a.gate ? silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, true, true>, yes) : go(gn_fwd_kernel<T, VEC, TPG, NV, true, false>, yes)
-                      : silu ? go(gn_fwd_kernel<T, VEC, TPG, NV, false, true>, no) : go(gn_fwd_kernel<T, VEC, TPG, NV, false, false>, no);
+    auto choose = [&](auto gate, auto silu) {
+        constexpr bool GATE = decltype(gate)::value, SILU = decltype(silu)::value;
+        if constexpr (BWD) return go(constant<gn_bwd_kernel<T, VEC, TPG, NV, GATE, SILU>>(), gate);
+        else return go(constant<gn_fwd_kernel<T, VEC, TPG, NV, GATE, SILU>>(), gate);
+    };
+    if (a.gate) return silu ? choose(yes, yes) : choose(yes, no);
+    return silu ? choose(no, yes) : choose(no, no);
 }
 
 // Threads and vectors of a group by its number of vectors: the fewest registers that hold it, a
