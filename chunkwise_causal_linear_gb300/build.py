@@ -5,7 +5,8 @@ torch-tensor binding of the operators around the attention).
 
 Each .cu file is compiled on its own (in parallel) with nvcc for sm_103a only, then
 linked into chunkwise_causal_linear_gb300/liblachunked.so.  binding.cpp is compiled with g++
-against the installed torch and linked with that library into _layer.so.
+against the installed torch (one with CUDA) and linked with that library into _layer.so; another torch
+or Python builds it again.
 """
 from __future__ import annotations
 
@@ -21,8 +22,16 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblachunked.so")
 LAYER = os.path.join(HERE, "_layer.so")
+STAMP = os.path.join(BUILD, "binding.stamp")  # what _layer.so was built against
+
+
+def cuda_torch(path):
+    """The torch to bind to: None without one that has CUDA, and then the C ABI alone is built."""
+    return path if path and os.path.exists(os.path.join(path, "lib", "libc10_cuda.so")) else None
+
+
 _spec = importlib.util.find_spec("torch")
-TORCH = os.path.dirname(_spec.origin) if _spec else None  # without it the C ABI alone is built
+TORCH = cuda_torch(os.path.dirname(_spec.origin) if _spec else None)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "simt.cu", "tc.cu", "tc_favor.cu", "tc_loglinear.cu", "tc_wide.cu", "decode.cu", "noncausal.cu", "noalloc.cu", "bwd.cu", "bwd_ll.cu",
            "recurrence.cu", "rotary.cu", "group_norm.cu"]
@@ -38,9 +47,26 @@ def _deps():
     return files
 
 
+def binding_stamp() -> str:
+    """The torch (place and version) and the Python that a binding built now is for."""
+    with open(os.path.join(TORCH, "version.py")) as f:
+        version = f.read()
+    return f"{TORCH}\n{sysconfig.get_config_var('SOABI')}\n{version}"
+
+
+def _read(path):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def up_to_date() -> bool:
     libs = [LIB, LAYER] if TORCH else [LIB]
     if not all(os.path.exists(f) for f in libs):
+        return False
+    if TORCH and _read(STAMP) != binding_stamp():
         return False
     t = min(os.path.getmtime(f) for f in libs)
     return all(os.path.getmtime(f) <= t for f in _deps())
@@ -98,6 +124,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
          "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}", f"-Wl,-rpath,{torch_lib}", "-ltorch", "-ltorch_cpu",
          "-ltorch_python", "-lc10", "-lc10_cuda"], "link of _layer.so")
     os.replace(tmp, LAYER)
+    with open(STAMP, "w") as f:
+        f.write(binding_stamp())
     return LIB
 
 
