@@ -591,6 +591,17 @@ struct Peers {
         }
         return mine;
     }
+    // Behind the last barrier of the cluster: where the wait of the last step ran out, a block that came
+    // late has sent since then, and its folds may still be on their way into this block's memory.  They
+    // take microseconds; a block that gave up earlier gets nothing any more (those behind it gave up
+    // in the next step), and neither waits longer than this.
+    __device__ __forceinline__ void settle(int buf, uint32_t parity)
+    {
+        if (!dead) return;
+        const uint64_t t0 = globaltimer();
+        while (!arrived(&bar[buf], parity) && globaltimer() - t0 < 1000000) {
+        }
+    }
     static constexpr size_t bytes(int split) { return 16 * REC_BUFS + sizeof(Fold<1>) * REC_BUFS * split * 32; }
 };
 
@@ -758,7 +769,10 @@ __global__ void __launch_bounds__(REC_THREADS, fwd_blocks<T, G, KIND, V, RecSmem
             parity ^= 1;
         }
     }
-    if constexpr (SPLIT) cluster_barrier();  // nothing is sent to a block that has ended
+    if constexpr (SPLIT) {
+        cluster_barrier();  // nothing is sent to a block that has ended
+        if (warp == 0) peers.settle(buf == 0 ? REC_BUFS - 1 : buf - 1, buf == 0 ? parity ^ 1 : parity);
+    }
     if (a.h_last && rank == 0 && warp == 0 && on)
 #pragma unroll
         for (int v = 0; v < V; ++v) a.h_last[(size_t)bh * a.d + c + v] = carry.v[v];
@@ -945,7 +959,10 @@ __global__ void __launch_bounds__(REC_THREADS, 2) rec_bwd_kernel(const RecArgs a
             parity ^= 1;
         }
     }
-    if constexpr (SPLIT) cluster_barrier();  // nothing is sent to a block that has ended
+    if constexpr (SPLIT) {
+        cluster_barrier();  // nothing is sent to a block that has ended
+        if (warp == 0) peers.settle(buf == 0 ? REC_BUFS - 1 : buf - 1, buf == 0 ? parity ^ 1 : parity);
+    }
     if (a.dh0 && rank == 0 && warp == 0 && on)
 #pragma unroll
         for (int v = 0; v < V; ++v) a.dh0[(size_t)bh * a.d + c + v] = carry.v[v];
