@@ -629,16 +629,16 @@ template <typename T, typename G, int V, bool BWD, bool SPLIT> struct RecSmem {
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
 
 // ---- forward ---------------------------------------------------------------------------------
-// Blocks an SM that the registers are to leave room for.  With fp32 activations and gates shared memory
-// holds two, and the exact gates take more than 80 registers (B1 H16 L65536 d64, log gates: 124 us, with
-// the bound of three blocks 144); gates that are values need fewer (124 us, with the bound of two 130).
-template <typename T, typename G, int KIND, int V, int R> constexpr int fwd_blocks()
+// Blocks an SM that the registers are to leave room for.  The exact gates of fp32 activations take more
+// than the 80 registers of three blocks (B1 H16 L65536 d64, log gates: 125 us and 144, with bf16 gates
+// 120 and 127); gates that are values do not (124 us, with the bound of two 130).
+template <typename T, int KIND, int V, int R> constexpr int fwd_blocks()
 {
-    return V == 1 && R == 16 && (sizeof(T) + sizeof(G) < 8 || KIND == LA_GATE_VALUE) ? 3 : 2;
+    return V == 1 && R == 16 && (sizeof(T) < 4 || KIND == LA_GATE_VALUE) ? 3 : 2;
 }
 
 template <typename T, typename G, int KIND, bool COMP, int V, bool SPLIT>
-__global__ void __launch_bounds__(REC_THREADS, fwd_blocks<T, G, KIND, V, RecSmem<T, G, V, false, SPLIT>::R>())
+__global__ void __launch_bounds__(REC_THREADS, fwd_blocks<T, KIND, V, RecSmem<T, G, V, false, SPLIT>::R>())
     rec_fwd_kernel(const RecArgs a)
 {
     using Sm = RecSmem<T, G, V, false, SPLIT>;
