@@ -192,6 +192,7 @@ py::tuple rotary(const Tensor &q, const OptTensor &k, const Tensor &turns, int64
 {
     const char *what = "la_rotary";
     axes(q, 4, "q");
+    if (k_out_ && !k) throw py::value_error("k_out is given without k");
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
     const int64_t B = q.size(0), H = q.size(1), L = q.size(2), d = q.size(3);
@@ -250,6 +251,7 @@ py::tuple group_norm_bwd(const Tensor &x, const Tensor &dout, const OptTensor &w
 {
     const char *what = "la_group_norm_bwd";
     axes(x, 4, "x");
+    if (dgate_ && !gate) throw py::value_error("dgate is given without gate");
     const at::Device dev = x.device();
     if (workspace_ && (workspace_->device() != dev || !workspace_->is_contiguous()))
         throw py::value_error("workspace must be contiguous on " + dev.str());
