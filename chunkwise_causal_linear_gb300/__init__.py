@@ -759,8 +759,8 @@ def rotary(q, k, table, positions=None, offset=0, layout="half", inverse=False, 
            k_out=None, stream=None):
     """q [B,H,L,d] and k [B,Hk,L,d] (k may be None) turned by their positions (la_rotary):
     positions [B,L] int32, or offset + t.  Strided views are allowed on both sides, and q_out=q,
-    k_out=k for in place.  inverse turns back, which is also the gradient.  Returns (q_out,
-    k_out)."""
+    k_out=k for in place (k_out only with k).  inverse turns back, which is also the gradient.  Returns
+    (q_out, k_out)."""
     return (_binding or _layer_binding()).rotary(q, k, table.turns, table.rot, table.amplitude, positions,
                                               offset, ROTARY_LAYOUTS[layout], inverse, q_out, k_out,
                                               stream)
@@ -778,8 +778,8 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, eps=1e-5, activation="s
 def group_norm_bwd(x, dout, weight=None, bias=None, gate=None, eps=1e-5, activation="silu",
                    center=True, dx=None, dgate=None, workspace=None, stream=None):
     """(dx, dgate, dweight, dbias) of group_norm_fwd for dout [B,L,H*d]; None where the forward
-    had None.  workspace: contiguous device memory of la_group_norm_bwd_workspace_bytes, allocated
-    where it is None or smaller."""
+    had None, and dgate is taken with gate only.  workspace: contiguous device memory of
+    la_group_norm_bwd_workspace_bytes, allocated where it is None or smaller."""
     return (_binding or _layer_binding()).group_norm_bwd(x, dout, weight, bias, gate, eps,
                                                       ACTIVATIONS[activation], center, dx, dgate,
                                                       workspace, stream)

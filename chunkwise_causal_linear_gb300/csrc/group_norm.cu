@@ -544,7 +544,9 @@ __global__ void __launch_bounds__(GN_THREADS) gn_join_kernel(const GnArgs a)
 // ---- host side -----------------------------------------------------------------------------------
 // Blocks of a head: one wave of the GPU in all, because a block's ring takes some rows to fill;
 // forward up to three where each still has 48 turns (B8 H16 L8192 d128: 126 us with three waves,
-// 132 with one; B2 H12 L16384 d64: 31 with one, 34 with three).  None without a token.
+// 132 with one; B2 H12 L16384 d64: 31 with one, 34 with three).  The rows of a block's turn are taken
+// from d alone; by_size() gives 32 (bf16, d <= 64) to 1 (single elements, d > 256), so that with few
+// tokens some blocks have none and only write their sums of 0, and wide odd groups have more turns.
 int blocks_of_head(int B, int H, int L, int d, int sms, bool bwd)
 {
     const long long rows = (long long)B * L, gpb = d > 1024 ? 1 : d > 256 ? 8 : 16;

@@ -19,11 +19,12 @@
 // every output written once; nothing goes through global memory between the blocks, and the order
 // of the sums depends on the sizes and the GPU alone.
 //
-// Measured (of the measured HBM rate): B1 H16 L65536 d64 fp32 (32 clusters of 8) forward 126 us,
-// 95%, backward 212 us, 94%; B8 H16 L8192 d128 bf16 with sigmoid gates forward 131 us, 92%,
-// backward 296 us, 68%: at 6 and 10 bytes an element and ~20 and ~50 instructions the bf16 cases
-// are bound by instructions as much as by memory, and few heads of them (B1 H8 L65536 d128: 98 us,
-// 61%, and 180 us, 56%) by the latency of a step besides.
+// Measured (of the measured HBM rate): B1 H16 L65536 d64 fp32 (32 clusters of 8) forward 124 us,
+// 97%, backward 209 us, 96%; B8 H16 L8192 d128 bf16 with sigmoid gates forward 129 us, 93%,
+// backward 295 us, 68%: at 6 and 10 bytes an element and ~20 and ~50 instructions the bf16 cases
+// are bound by instructions as much as by memory, and few heads of them (B1 H8 L65536 d128: 96 us,
+// 62%, and 183 us, 55%; 24 and 50 instructions, issued 46% and 49% of the time) by the latency of a
+// step besides.
 //
 // The inputs of the next steps are on the way while one is folded: each warp copies its own rows
 // into its own ring in shared memory (cp.async, no barrier).

@@ -2,8 +2,9 @@
 // frequency (sm_103a).
 //
 // A frequency is kept as a 64-bit fraction of a full turn per position, so the angle of
-// position p is p * turns modulo 2^64: one integer product, exact however far p is.  An fp32
-// product p * theta would be off by a radian at p ~ 2^24.
+// position p is p * turns modulo 2^64: one integer product without a rounding, off by p times what
+// the frequency is off (2^-54 of a turn, that of its 64-bit arithmetic).  An fp32 product p * theta
+// would be off by a radian at p ~ 2^24.
 //
 // Bound by memory: every element is read and written once.  A thread holds the sines and cosines
 // of VEC pairs (16-byte vectors) of one token and goes over up to 16 heads of q and k with them;

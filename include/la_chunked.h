@@ -477,8 +477,9 @@ enum la_gate_kind {
  *   h_last        device fp32 [B, H, d], the state after the last row, or NULL; may be h0
  *   chunk_states  device fp32 [B, H, ceil(L / LA_RECURRENCE_CHUNK), d] or NULL: the states
  *                 before rows 0, 64, 128, ..., which la_recurrence_bwd reads
- * A gate of 0 (value 0, log or sigmoid of -inf) forgets infinities and NaN too.  Outputs must not
- * overlap inputs, but for h_last.
+ * A gate of 0 (value 0, log or sigmoid of -inf) forgets infinities and NaN too, those of gates before
+ * it among them; no other gate does, however small.  Outputs must not overlap inputs, but for
+ * h_last.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED (dtype, gate kind), LA_ERR_ARG
  * (strides, alignment) or LA_ERR_CUDA.  Asynchronous on `stream`, no workspace; the sums' order
  * depends on the sizes and the GPU alone, so equal calls give equal bits.  Where few heads are
@@ -537,8 +538,7 @@ enum la_rotary_scaling {
 /*
  * la_rotary_table -- host only: fills turns[0..rot/2) with the frequencies as fractions of a
  * full turn per position, in units of 2^-64.  A position times that, modulo 2^64, is its
- * angle without any loss however far the position is.  The caller copies the table to the
- * device and keeps it.  fast, slow, original_length are read for LA_ROTARY_PARTS only (0 < slow
+ * angle without a further rounding.  The caller copies the table to the device and keeps it.  fast, slow, original_length are read for LA_ROTARY_PARTS only (0 < slow
  * < fast).  LA_ERR_SHAPE for rot <= 0 or odd, LA_ERR_ARG for base <= 0, factor < 1, values
  * that are not finite, or more than 2^50 turns per position.
  */
@@ -556,7 +556,9 @@ int la_rotary_table(int rot, double base, int scaling, double factor, double ori
  *   turns         device copy of la_rotary_table's array, rot/2 entries (rot = 0: may be NULL)
  *   positions     device int [B, L], or NULL: row t of every sequence is at offset + t
  *   rot           even, 0 <= rot <= d
- * Angles are exact to 2^-33 of a turn, sines and cosines fp32; each output is rounded once.
+ * Angles are position times the table's frequency to 2^-33 of a turn, sines and cosines fp32; each
+ * output is rounded once.  The frequencies are those of 64-bit arithmetic, off by up to 2^-54 of a
+ * turn, so the angle at position p is off by p times that (2^31: 2^-23 of a turn).
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED, LA_ERR_ARG or LA_ERR_CUDA.
  */
 int la_rotary(const void *q, const void *k, void *q_out, void *k_out,
