@@ -390,7 +390,8 @@ __device__ __noinline__ Fold<V> fold_rows(const T *sx, const G *sg, int rows)
     }
     return f;
 }
-// The product of a run's gates where the plain one is not regular.
+// The product of a run's gates where the plain one is not regular.  Where every run has one (sigmoid
+// gates of logits around -4, B1 H8 L65536 d128 bf16) the look at the gates takes 14 us of 103.
 template <typename G, int KIND, int V, int R> __device__ __forceinline__ Ch<V> product_exact(const G *sg, Ch<V> p)
 {
     bool zero[V] = {};
