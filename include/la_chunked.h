@@ -587,8 +587,8 @@ enum la_activation {
  *   eps           > 0 and finite, else LA_ERR_ARG
  *   d             at most 8192, else LA_ERR_UNSUPPORTED
  * Statistics are fp32 over values held in fp32, the variance from centred values.  SiLU's sigmoid
- * is off by 9 2^-24 relatively for fp32, (7 + 2.5 |z|) 2^-24 for bf16.  Outputs must not overlap
- * inputs.
+ * is off by 9 2^-24 relatively for fp32, (7 + 2.5 |z|) 2^-24 for bf16, and 0 where it is below
+ * 2^-126.  Outputs must not overlap inputs.
  */
 int la_group_norm_fwd(const void *x, const float *weight, const float *bias, const void *gate,
                       void *out, int B, int H, int L, int d, const la_strides *x_strides,
