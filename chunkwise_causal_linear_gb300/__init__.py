@@ -54,7 +54,9 @@ EXPORTS = ("la_chunked_fwd", "la_chunked_fwd_path", "la_chunked_fwd_host",
            "la_chunked_bwd_ll_workspace_bytes", "la_chunked_state",
            "la_state_combine", "la_chunked_fwd_init", "la_recurrence_fwd", "la_recurrence_bwd",
            "la_recurrence_step", "la_rotary_table", "la_rotary", "la_group_norm_fwd",
-           "la_group_norm_bwd", "la_group_norm_bwd_workspace_bytes", "la_version")
+           "la_group_norm_bwd", "la_group_norm_bwd_workspace_bytes", "la_gated_fwd",
+           "la_gated_workspace_bytes", "la_gated_bwd", "la_gated_bwd_workspace_bytes",
+           "la_gated_step", "la_version")
 
 
 class la_feature_map(ctypes.Structure):
@@ -171,6 +173,16 @@ def lib() -> ctypes.CDLL:
             L.la_group_norm_bwd.restype = i
             L.la_group_norm_bwd_workspace_bytes.argtypes = [i] * 4
             L.la_group_norm_bwd_workspace_bytes.restype = sz
+            L.la_gated_fwd.argtypes = [p] * 9 + [i] * 7 + [stp] * 5 + [f, i, p, sz, p, i]
+            L.la_gated_fwd.restype = i
+            L.la_gated_workspace_bytes.argtypes = [i] * 6
+            L.la_gated_workspace_bytes.restype = sz
+            L.la_gated_bwd.argtypes = [p] * 14 + [i] * 6 + [stp] * 8 + [f, i, p, sz, p, i]
+            L.la_gated_bwd.restype = i
+            L.la_gated_bwd_workspace_bytes.argtypes = [i] * 7
+            L.la_gated_bwd_workspace_bytes.restype = sz
+            L.la_gated_step.argtypes = [p] * 7 + [i] * 6 + [stp] * 4 + [f, i, p]
+            L.la_gated_step.restype = i
             L.la_version.argtypes = []
             L.la_version.restype = ctypes.c_char_p
             _lib = L
@@ -390,6 +402,38 @@ def la_group_norm_bwd(x, weight, bias, gate, dout, dx, dgate, dweight, dbias, B,
 
 def la_group_norm_bwd_workspace_bytes(B, H, L, d) -> int:
     return lib().la_group_norm_bwd_workspace_bytes(B, H, L, d)
+
+
+def la_gated_fwd(q, k, v, log_decay, state0, state, slots, lengths, out, B, H, Hk, L, dk, dv, n_slots,
+                 q_strides, k_strides, v_strides, g_strides, out_strides, scale, dtype, workspace,
+                 workspace_bytes, stream, path) -> int:
+    return lib().la_gated_fwd(q, k, v, log_decay, state0, state, slots, lengths, out, B, H, Hk, L, dk, dv,
+                              n_slots, q_strides, k_strides, v_strides, g_strides, out_strides, scale,
+                              dtype, workspace, workspace_bytes, stream, path)
+
+
+def la_gated_workspace_bytes(B, H, L, dk, dv, dtype) -> int:
+    return lib().la_gated_workspace_bytes(B, H, L, dk, dv, dtype)
+
+
+def la_gated_bwd(q, k, v, log_decay, state0, lengths, dout, dstate, grad_q, grad_k, grad_v, dlog_decay,
+                 dlog_decay_head, dstate0, B, H, Hk, L, dk, dv, q_strides, k_strides, v_strides, g_strides,
+                 dout_strides, dq_strides, dk_strides, dv_strides, scale, dtype, workspace,
+                 workspace_bytes, stream, path) -> int:
+    return lib().la_gated_bwd(q, k, v, log_decay, state0, lengths, dout, dstate, grad_q, grad_k, grad_v,
+                              dlog_decay, dlog_decay_head, dstate0, B, H, Hk, L, dk, dv, q_strides,
+                              k_strides, v_strides, g_strides, dout_strides, dq_strides, dk_strides,
+                              dv_strides, scale, dtype, workspace, workspace_bytes, stream, path)
+
+
+def la_gated_bwd_workspace_bytes(B, H, Hk, L, dk, dv, dtype) -> int:
+    return lib().la_gated_bwd_workspace_bytes(B, H, Hk, L, dk, dv, dtype)
+
+
+def la_gated_step(q, k, v, log_decay, state, slots, out, B, H, Hk, dk, dv, n_slots, q_strides, k_strides,
+                  v_strides, g_strides, scale, dtype, stream) -> int:
+    return lib().la_gated_step(q, k, v, log_decay, state, slots, out, B, H, Hk, dk, dv, n_slots, q_strides,
+                               k_strides, v_strides, g_strides, scale, dtype, stream)
 
 
 def la_version() -> str:
@@ -783,3 +827,33 @@ def group_norm_bwd(x, dout, weight=None, bias=None, gate=None, eps=1e-5, activat
     return (_binding or _layer_binding()).group_norm_bwd(x, dout, weight, bias, gate, eps,
                                                       ACTIVATIONS[activation], center, dx, dgate,
                                                       workspace, stream)
+
+
+# ---- gated attention ----------------------------------------------------------------------
+def gated_fwd(q, k, v, log_decay, scale=1.0, state0=None, lengths=None, slots=None, state=None, out=None,
+              workspace=None, stream=None, path=LA_PATH_AUTO):
+    """Causal linear attention with a decay per head, or per token and head (la_gated_fwd): S_t =
+    exp(g_t) S_{t-1} + k_t v_t^T, out_t = scale q_t^T S_t, for CUDA tensors q [B,H,L,dk], k [B,Hk,L,dk],
+    v [B,Hk,L,dv] (bf16 or fp32, strided views allowed; H / Hk heads share a key head) and log_decay fp32
+    [H] or [B,H,L].  state0, state [B,H,dk,dv] fp32: the states before the first and behind the last
+    row; with slots [B] int32 they are pools [n,H,dk,dv] in which sequence b's lies at slots[b] (the same
+    tensor for both updates the pool in place).  lengths [B] int32: rows behind a sequence's end are not
+    used.  Returns (out [B,H,L,dv], state); without slots a state is allocated where none is given."""
+    return (_binding or _layer_binding()).gated_fwd(q, k, v, log_decay, scale, state0, lengths, slots, state,
+                                                    out, workspace, stream, path)
+
+
+def gated_bwd(q, k, v, log_decay, dout, scale=1.0, state0=None, lengths=None, dstate=None, dq=None, dk=None,
+              dv=None, decay_grad=True, workspace=None, stream=None, path=LA_PATH_AUTO):
+    """(dq, dk, dv, dlog_decay, dstate0) of gated_fwd for dout [B,H,L,dv] and dstate [B,H,dk,dv] fp32, the
+    gradient of the state behind the last row (None: zero).  dlog_decay has log_decay's shape (None
+    without decay_grad); dk and dv of a shared key head are the sums over its heads."""
+    return (_binding or _layer_binding()).gated_bwd(q, k, v, log_decay, dout, scale, state0, lengths, dstate, dq,
+                                                    dk, dv, decay_grad, workspace, stream, path)
+
+
+def gated_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, stream=None):
+    """One decoding step of the gated attention: q [B,H,dk], k [B,Hk,dk], v [B,Hk,dv] (this token),
+    log_decay fp32 [H] or [B,H], state [B,H,dk,dv] fp32, or with slots [B] int32 a pool [n,H,dk,dv],
+    updated in place.  Returns out [B,H,dv]."""
+    return (_binding or _layer_binding()).gated_step(q, k, v, log_decay, state, scale, slots, out, stream)

@@ -1,5 +1,5 @@
-// binding.cpp -- the torch-tensor forms of the operators around the attention (recurrence, rotary
-// positions, group norm) as a compiled Python module.
+// binding.cpp -- the torch-tensor forms of the gated attention and of the operators around the attention
+// (recurrence, rotary positions, group norm) as a compiled Python module.
 //
 // Argument checks, output allocation and the call into the C ABI, nothing else.  Compiled because
 // these calls are short: a decoding step's kernel takes 1 to 3 us, and marshalling it through
@@ -288,6 +288,144 @@ py::tuple group_norm_bwd(const Tensor &x, const Tensor &dout, const OptTensor &w
     return py::make_tuple(dx, dgate, dw, db);
 }
 
+// log_decay: fp32 [H], [B, H, L] or (without L) [B, H].
+la_strides gate_strides(const Tensor &g, int64_t B, int64_t H, int64_t L, const at::Device &dev)
+{
+    if (g.scalar_type() != at::kFloat || g.device() != dev)
+        throw py::type_error("log_decay must be Float on " + dev.str() + ", got " + at::toString(g.scalar_type()) + " on " +
+                             g.device().str());
+    if (g.dim() == 1 && g.size(0) == H) return {0, g.stride(0), 0};
+    if (L < 0 && g.dim() == 2 && g.size(0) == B && g.size(1) == H) return {g.stride(0), g.stride(1), 0};
+    if (L >= 0 && g.dim() == 3 && g.size(0) == B && g.size(1) == H && g.size(2) == L)
+        return {g.stride(0), g.stride(1), g.stride(2)};
+    throw py::value_error("log_decay must have one value per head or per token and head, got " + text(g.sizes()));
+}
+
+void *room(OptTensor &workspace, size_t need, const at::Device &dev)
+{
+    if (workspace && (workspace->device() != dev || !workspace->is_contiguous()))
+        throw py::value_error("workspace must be contiguous on " + dev.str());
+    if (!need) return nullptr;
+    if (!workspace || workspace->nbytes() < need)
+        workspace = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
+    return workspace->data_ptr();
+}
+
+py::tuple gated_fwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &log_decay, double scale,
+                    const OptTensor &state0, const OptTensor &lengths, const OptTensor &slots, const OptTensor &state_,
+                    const OptTensor &out_, OptTensor workspace, const OptStream &stream, int path)
+{
+    const char *what = "la_gated_fwd";
+    axes(q, 4, "q");
+    axes(k, 4, "k");
+    axes(v, 4, "v");
+    const at::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const int64_t B = q.size(0), H = q.size(1), L = q.size(2), d = q.size(3), Hk = k.size(1), e = v.size(3);
+    const int dtype = code(q);
+    const Place place(dev, stream, what);
+    const std::array<int64_t, 4> kshape{B, Hk, L, d}, vshape{B, Hk, L, e}, oshape{B, H, L, e};
+    const Strides sq(q, q.sizes(), type, dev, "q"), sk(k, kshape, type, dev, "k"), sv(v, vshape, type, dev, "v");
+    const la_strides sg = gate_strides(log_decay, B, H, L, dev);
+    const int *n = dense<int>(lengths, {B}, at::kInt, dev, "lengths"), *at_ = dense<int>(slots, {B}, at::kInt, dev, "slots");
+    OptTensor state = state_;
+    int64_t pool = B;
+    if (slots) {
+        if (!state0 && !state) throw py::value_error("slots are given without a pool of states");
+        const Tensor &p = state ? *state : *state0;
+        axes(p, 4, "state");
+        pool = p.size(0);
+    } else if (!state) {
+        state = at::empty({B, H, d, e}, q.options().dtype(at::kFloat));
+    }
+    const float *s0 = dense<float>(state0, {pool, H, d, e}, at::kFloat, dev, "state0");
+    float *s1 = dense<float>(state, {pool, H, d, e}, at::kFloat, dev, "state");
+    const Tensor out = out_ ? *out_ : at::empty(oshape, q.options());
+    const Strides so(out, oshape, type, dev, "out");
+    const size_t need = la_gated_workspace_bytes((int)B, (int)H, (int)L, (int)d, (int)e, dtype);
+    void *ws = room(workspace, need, dev);
+    const int rc = la_gated_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), (const float *)log_decay.data_ptr(), s0, s1, at_,
+                                n, out.data_ptr(), (int)B, (int)H, (int)Hk, (int)L, (int)d, (int)e, (int)pool, sq.p, sk.p,
+                                sv.p, &sg, so.p, (float)scale, dtype, ws, need, place.stream, path);
+    if (rc != LA_OK) fail(rc, what);
+    return py::make_tuple(out, state);
+}
+
+py::tuple gated_bwd(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &log_decay, const Tensor &dout,
+                    double scale, const OptTensor &state0, const OptTensor &lengths, const OptTensor &dstate,
+                    const OptTensor &dq_, const OptTensor &dk_, const OptTensor &dv_, bool decay_grad, OptTensor workspace,
+                    const OptStream &stream, int path)
+{
+    const char *what = "la_gated_bwd";
+    axes(q, 4, "q");
+    axes(k, 4, "k");
+    axes(v, 4, "v");
+    const at::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const int64_t B = q.size(0), H = q.size(1), L = q.size(2), d = q.size(3), Hk = k.size(1), e = v.size(3);
+    const int dtype = code(q);
+    const Place place(dev, stream, what);
+    const std::array<int64_t, 4> kshape{B, Hk, L, d}, vshape{B, Hk, L, e}, oshape{B, H, L, e};
+    const Strides sq(q, q.sizes(), type, dev, "q"), sk(k, kshape, type, dev, "k"), sv(v, vshape, type, dev, "v"),
+        so(dout, oshape, type, dev, "dout");
+    const la_strides sg = gate_strides(log_decay, B, H, L, dev);
+    const int *n = dense<int>(lengths, {B}, at::kInt, dev, "lengths");
+    const float *s0 = dense<float>(state0, {B, H, d, e}, at::kFloat, dev, "state0"),
+                *ds = dense<float>(dstate, {B, H, d, e}, at::kFloat, dev, "dstate");
+    const Tensor dq = dq_ ? *dq_ : at::empty(q.sizes(), q.options()), dk = dk_ ? *dk_ : at::empty(kshape, q.options()),
+                 dv = dv_ ? *dv_ : at::empty(vshape, q.options());
+    const Strides sdq(dq, q.sizes(), type, dev, "dq"), sdk(dk, kshape, type, dev, "dk"), sdv(dv, vshape, type, dev, "dv");
+    const auto f32 = q.options().dtype(at::kFloat);
+    const bool heads = log_decay.dim() == 1;
+    OptTensor dg;
+    if (decay_grad) dg = heads ? at::empty({H}, f32) : at::empty({B, H, L}, f32);
+    const Tensor dstate0 = at::empty({B, H, d, e}, f32);
+    const size_t need = la_gated_bwd_workspace_bytes((int)B, (int)H, (int)Hk, (int)L, (int)d, (int)e, dtype);
+    void *ws = room(workspace, need, dev);
+    const int rc = la_gated_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), (const float *)log_decay.data_ptr(), s0, n,
+                                dout.data_ptr(), ds, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                heads ? nullptr : (float *)ptr(dg), heads ? (float *)ptr(dg) : nullptr,
+                                (float *)dstate0.data_ptr(), (int)B, (int)H, (int)Hk, (int)L, (int)d, (int)e, sq.p, sk.p, sv.p,
+                                &sg, so.p, sdq.p, sdk.p, sdv.p, (float)scale, dtype, ws, need, place.stream, path);
+    if (rc != LA_OK) fail(rc, what);
+    return py::make_tuple(dq, dk, dv, dg, dstate0);
+}
+
+// Strides of a [B, H, d] tensor.
+la_strides step_strides(const Tensor &t, at::IntArrayRef shape, at::ScalarType type, const at::Device &dev, const char *name)
+{
+    check(t, shape, type, dev, name);
+    if (t.stride(2) != 1 && shape[2] > 1) throw py::value_error(std::string(name) + ": the channels (last axis) must be adjacent");
+    return {t.stride(0), t.stride(1), 0};
+}
+
+Tensor gated_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &log_decay, const Tensor &state,
+                  double scale, const OptTensor &slots, const OptTensor &out_, const OptStream &stream)
+{
+    const char *what = "la_gated_step";
+    axes(q, 3, "q");
+    axes(k, 3, "k");
+    axes(v, 3, "v");
+    axes(state, 4, "state");
+    const at::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const int64_t B = q.size(0), H = q.size(1), d = q.size(2), Hk = k.size(1), e = v.size(2);
+    const int dtype = code(q);
+    const Place place(dev, stream, what);
+    const la_strides sq = step_strides(q, q.sizes(), type, dev, "q"), sk = step_strides(k, {B, Hk, d}, type, dev, "k"),
+                     sv = step_strides(v, {B, Hk, e}, type, dev, "v"), sg = gate_strides(log_decay, B, H, -1, dev);
+    const int *at_ = dense<int>(slots, {B}, at::kInt, dev, "slots");
+    const int64_t pool = slots ? state.size(0) : B;
+    float *s = dense<float>(state, {pool, H, d, e}, at::kFloat, dev, "state");
+    const Tensor out = out_ ? *out_ : at::empty({B, H, e}, q.options());
+    void *o = dense<void>(out, {B, H, e}, type, dev, "out");
+    const int rc = la_gated_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), (const float *)log_decay.data_ptr(), s, at_, o,
+                                 (int)B, (int)H, (int)Hk, (int)d, (int)e, (int)pool, &sq, &sk, &sv, &sg, (float)scale, dtype,
+                                 place.stream);
+    if (rc != LA_OK) fail(rc, what);
+    return out;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_layer, m)
@@ -298,4 +436,7 @@ PYBIND11_MODULE(_layer, m)
     m.def("rotary", &rotary);
     m.def("group_norm_fwd", &group_norm_fwd);
     m.def("group_norm_bwd", &group_norm_bwd);
+    m.def("gated_fwd", &gated_fwd);
+    m.def("gated_bwd", &gated_bwd);
+    m.def("gated_step", &gated_step);
 }

@@ -614,6 +614,95 @@ int la_group_norm_bwd(const void *x, const float *weight, const float *bias, con
  * (0 on invalid arguments). */
 size_t la_group_norm_bwd_workspace_bytes(int B, int H, int L, int d);
 
+/* ---- gated attention: a decay for each head, or for each token and head ----
+ *
+ * la_gated_fwd -- causal linear attention whose state is decayed by data, for every head
+ *     S_t = a_t S_{t-1} + k_t v_t^T,      out_t = scale q_t^T S_t,      a_t = exp(log_decay_t),
+ * the chunked form for prompts and training; la_gated_step is its recurrent form for single tokens and
+ * la_gated_bwd its gradients.  la_decay_fwd is the case of one constant for all heads.  Identity features,
+ * no normaliser (la_group_norm_fwd follows instead).
+ *   q             [B, H, L, dk], dtype `dtype`
+ *   k, v          [B, Hk, L, dk] and [B, Hk, L, dv]; H a multiple of Hk: H / Hk neighbouring heads share a
+ *                 key head, each with its own decay and state
+ *   log_decay     device fp32 [B, H, L] by strides (NULL: contiguous); {0, 1, 0} takes a constant for each
+ *                 head.  Meant to be at most 0; -inf forgets everything before its row (the first row of
+ *                 a packed document).  Others are computed as the formula says where the products of a
+ *                 chunk's decays stay finite.
+ *   state0        device fp32 state before row 0, or NULL for zero; state: the state behind the last row,
+ *                 or NULL; may be state0.  Without slots both are [B, H, dk, dv] (la_decode_step's layout).
+ *   slots         NULL, or device int [B]: the states lie in pools [n_slots, H, dk, dv], sequence b's at
+ *                 slots[b].  A negative slot is none: the sequence starts from zero and its last state is
+ *                 not kept; so is one of n_slots or more, which la_last_device_status reports as
+ *                 LA_ERR_DEVICE.  No two sequences may share a slot; the other slots keep their values.
+ *   lengths       NULL, or device int [B]: sequence b ends after lengths[b] rows (clamped to 0..L).  Rows
+ *                 behind are not used, whatever they hold; out is 0 there and the state stays.
+ *   out           [B, H, L, dv], dtype `dtype`
+ *   dk, dv        at most 256, B * H at most 65535
+ *   scale         finite, else LA_ERR_ARG
+ *   path          enum la_path.  LA_PATH_SIMT takes every case, in fp32 row by row.
+ *   workspace     device memory of la_gated_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0)
+ * States, decays and sums are fp32; out is rounded once.  q, k, v are meant to be finite: an infinity or
+ * NaN in a row may reach every row of its chunk of 64 and those behind; only rows behind a sequence's
+ * end, and what a log decay of -inf lies between in different chunks, keep theirs.  The order of the sums
+ * depends on the sizes and the GPU alone, so equal calls give equal bits.  Outputs must not overlap
+ * inputs, but for state.
+ * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED, LA_ERR_ARG (strides, alignment, scale),
+ * LA_ERR_WORKSPACE or LA_ERR_CUDA.  Asynchronous on `stream`.
+ */
+int la_gated_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                 const float *state0, float *state, const int *slots, const int *lengths, void *out,
+                 int B, int H, int Hk, int L, int dk, int dv, int n_slots,
+                 const la_strides *q_strides, const la_strides *k_strides,
+                 const la_strides *v_strides, const la_strides *g_strides,
+                 const la_strides *out_strides, float scale, int dtype, void *workspace,
+                 size_t workspace_bytes, void *stream, int path);
+
+/* Workspace bytes la_gated_fwd needs for these sizes on the current device, whatever the path (0 when
+ * none, or on invalid arguments). */
+size_t la_gated_workspace_bytes(int B, int H, int L, int dk, int dv, int dtype);
+
+/*
+ * la_gated_bwd -- its gradients.  With D_t = scale q_t dout_t^T + a_{t+1} D_{t+1} (dstate behind the last
+ * row), the gradient of S_t:
+ *     dq_t = scale S_t dout_t,    dk_t = D_t v_t,    dv_t = D_t^T k_t,
+ *     dlog_decay_t = <D_t, a_t S_{t-1}>,    dstate0 = a_0 D_0.
+ * The states are formed again from k, v and log_decay; nothing of the forward pass is kept.
+ *   dout          [B, H, L, dv], dtype `dtype`
+ *   dstate        device fp32 [B, H, dk, dv], the gradient of the state behind the last row, or NULL for zero
+ *   dq, dk, dv    as q, k, v, fully overwritten, 0 behind a sequence's end; dk and dv of a shared key
+ *                 head are the sums over its heads
+ *   dlog_decay    device fp32 contiguous [B, H, L], or NULL
+ *   dlog_decay_head  device fp32 [H]: its sums over sequences and rows, the gradient of a constant for
+ *                 each head; or NULL.  Without both the decays' gradient is not formed.
+ *   dstate0       device fp32 [B, H, dk, dv] or NULL; may be dstate.  Otherwise outputs must not overlap
+ *                 inputs.
+ *   workspace     la_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned
+ * Other arguments and errors as la_gated_fwd (no slots).
+ */
+int la_gated_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                 const float *state0, const int *lengths, const void *dout, const float *dstate,
+                 void *grad_q, void *grad_k, void *grad_v, float *dlog_decay,
+                 float *dlog_decay_head, float *dstate0, int B, int H, int Hk, int L, int dk, int dv,
+                 const la_strides *q_strides, const la_strides *k_strides,
+                 const la_strides *v_strides, const la_strides *g_strides,
+                 const la_strides *dout_strides, const la_strides *dq_strides,
+                 const la_strides *dk_strides, const la_strides *dv_strides, float scale, int dtype,
+                 void *workspace, size_t workspace_bytes, void *stream, int path);
+
+/* Workspace bytes la_gated_bwd needs (0 on invalid arguments). */
+size_t la_gated_bwd_workspace_bytes(int B, int H, int Hk, int L, int dk, int dv, int dtype);
+
+/* One decoding step: state = a state + k v^T, out = scale q^T state.  q [B, H, dk], k [B, Hk, dk], v
+ * [B, Hk, dv], log_decay [B, H] by the strides' b and h (NULL: contiguous), out contiguous [B, H, dv];
+ * state fp32, [B, H, dk, dv] or by slots a pool, updated in place.  A sequence without a slot starts
+ * from zero and its state is not kept.  Stepping t = 0..L-1 reproduces la_gated_fwd's rows.  Other
+ * arguments and errors as la_gated_fwd. */
+int la_gated_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                  const int *slots, void *out, int B, int H, int Hk, int dk, int dv, int n_slots,
+                  const la_strides *q_strides, const la_strides *k_strides,
+                  const la_strides *v_strides, const la_strides *g_strides, float scale, int dtype,
+                  void *stream);
+
 /* Library version string, e.g. "0.1.0". */
 const char *la_version(void);
 
