@@ -36,12 +36,15 @@ LA_GATE_VALUE, LA_GATE_LOG, LA_GATE_SIGMOID = 0, 1, 2
 LA_RECURRENCE_CHUNK = 64
 LA_ROTARY_HALF, LA_ROTARY_INTERLEAVED = 0, 1
 LA_ROTARY_PLAIN, LA_ROTARY_LINEAR, LA_ROTARY_PARTS = 0, 1, 2
-LA_ACT_NONE, LA_ACT_SILU = 0, 1
+LA_ACT_NONE, LA_ACT_SILU, LA_ACT_SIGMOID = 0, 1, 2
+LA_NORM_NONE, LA_NORM_RMS, LA_NORM_LAYER = 0, 1, 2
 
 GATE_KINDS = {"value": LA_GATE_VALUE, "log": LA_GATE_LOG, "sigmoid": LA_GATE_SIGMOID}
 ROTARY_LAYOUTS = {"half": LA_ROTARY_HALF, "interleaved": LA_ROTARY_INTERLEAVED}
 ROTARY_SCALINGS = {"none": LA_ROTARY_PLAIN, "linear": LA_ROTARY_LINEAR, "parts": LA_ROTARY_PARTS}
 ACTIVATIONS = {"none": LA_ACT_NONE, "silu": LA_ACT_SILU}
+GATE_ACTIVATIONS = {**ACTIVATIONS, "sigmoid": LA_ACT_SIGMOID}
+NORMS = {"none": LA_NORM_NONE, "rms": LA_NORM_RMS, "layer": LA_NORM_LAYER}
 FEATURE_MAPS = {"identity": LA_FM_IDENTITY, "elu1": LA_FM_ELU1, "favor": LA_FM_FAVOR}
 
 # every function the header declares (checked by the tests against include/la_chunked.h)
@@ -56,7 +59,8 @@ EXPORTS = ("la_chunked_fwd", "la_chunked_fwd_path", "la_chunked_fwd_host",
            "la_recurrence_step", "la_rotary_table", "la_rotary", "la_group_norm_fwd",
            "la_group_norm_bwd", "la_group_norm_bwd_workspace_bytes", "la_gated_fwd",
            "la_gated_workspace_bytes", "la_gated_bwd", "la_gated_bwd_workspace_bytes",
-           "la_gated_step", "la_version")
+           "la_gated_step", "la_block_norm_fwd", "la_block_norm_bwd",
+           "la_block_norm_bwd_workspace_bytes", "la_version")
 
 
 class la_feature_map(ctypes.Structure):
@@ -183,6 +187,12 @@ def lib() -> ctypes.CDLL:
             L.la_gated_bwd_workspace_bytes.restype = sz
             L.la_gated_step.argtypes = [p] * 7 + [i] * 6 + [stp] * 4 + [f, i, p]
             L.la_gated_step.restype = i
+            L.la_block_norm_fwd.argtypes = [p] * 9 + [i] * 3 + [stp] * 5 + [i] * 3 + [f] * 3 + [i, i, p]
+            L.la_block_norm_fwd.restype = i
+            L.la_block_norm_bwd.argtypes = [p] * 16 + [i] * 3 + [stp] * 8 + [i] * 3 + [f] * 3 + [i, i, p, sz, p]
+            L.la_block_norm_bwd.restype = i
+            L.la_block_norm_bwd_workspace_bytes.argtypes = [i] * 3
+            L.la_block_norm_bwd_workspace_bytes.restype = sz
             L.la_version.argtypes = []
             L.la_version.restype = ctypes.c_char_p
             _lib = L
@@ -434,6 +444,31 @@ def la_gated_step(q, k, v, log_decay, state, slots, out, B, H, Hk, dk, dv, n_slo
                   v_strides, g_strides, scale, dtype, stream) -> int:
     return lib().la_gated_step(q, k, v, log_decay, state, slots, out, B, H, Hk, dk, dv, n_slots, q_strides,
                                k_strides, v_strides, g_strides, scale, dtype, stream)
+
+
+def la_block_norm_fwd(y, residual, gate, post_weight, post_bias, pre_weight, pre_bias, h, n, B, L, d, y_strides,
+                      residual_strides, gate_strides, h_strides, n_strides, post_norm, pre_norm, activation,
+                      residual_scale, branch_scale, eps, dtype, residual_dtype, stream) -> int:
+    return lib().la_block_norm_fwd(y, residual, gate, post_weight, post_bias, pre_weight, pre_bias, h, n, B, L, d,
+                                   y_strides, residual_strides, gate_strides, h_strides, n_strides, post_norm,
+                                   pre_norm, activation, residual_scale, branch_scale, eps, dtype,
+                                   residual_dtype, stream)
+
+
+def la_block_norm_bwd(y, residual, gate, post_weight, post_bias, pre_weight, pre_bias, dh, dn, dresidual, dy, dgate,
+                      dpost_weight, dpost_bias, dpre_weight, dpre_bias, B, L, d, y_strides, residual_strides,
+                      gate_strides, dh_strides, dn_strides, dresidual_strides, dy_strides, dgate_strides, post_norm,
+                      pre_norm, activation, residual_scale, branch_scale, eps, dtype, residual_dtype, workspace,
+                      workspace_bytes, stream) -> int:
+    return lib().la_block_norm_bwd(y, residual, gate, post_weight, post_bias, pre_weight, pre_bias, dh, dn, dresidual,
+                                   dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias, B, L, d, y_strides,
+                                   residual_strides, gate_strides, dh_strides, dn_strides, dresidual_strides,
+                                   dy_strides, dgate_strides, post_norm, pre_norm, activation, residual_scale,
+                                   branch_scale, eps, dtype, residual_dtype, workspace, workspace_bytes, stream)
+
+
+def la_block_norm_bwd_workspace_bytes(B, L, d) -> int:
+    return lib().la_block_norm_bwd_workspace_bytes(B, L, d)
 
 
 def la_version() -> str:
@@ -857,3 +892,31 @@ def gated_step(q, k, v, log_decay, state, scale=1.0, slots=None, out=None, strea
     log_decay fp32 [H] or [B,H], state [B,H,dk,dv] fp32, or with slots [B] int32 a pool [n,H,dk,dv],
     updated in place.  Returns out [B,H,dv]."""
     return (_binding or _layer_binding()).gated_step(q, k, v, log_decay, state, scale, slots, out, stream)
+
+
+# ---- norms around a block -----------------------------------------------------------------
+def block_norm_fwd(y, residual, gate=None, activation="silu", post_norm="rms", post_weight=None, post_bias=None,
+                   pre_norm="rms", pre_weight=None, pre_bias=None, residual_scale=1.0, branch_scale=1.0, eps=1e-5,
+                   h=None, n=None, stream=None):
+    """(h, n) behind a block with the output y and before the next one (la_block_norm_fwd): h = residual_scale
+    residual + branch_scale act(gate) (norm(y) post_weight + post_bias), n = norm(h) pre_weight + pre_bias, for
+    CUDA tensors [B,L,d] (strided views allowed).  y and gate bf16 or fp32; residual of the same type or
+    fp32.  post_norm: "none", "rms" or "layer"; pre_norm: "rms", "layer" or "none", which leaves n out (None).
+    activation of the gate: "none", "silu" or "sigmoid".  weights and biases: fp32 [d] or None.  h=residual
+    and n=y work in place."""
+    return (_binding or _layer_binding()).block_norm_fwd(y, residual, gate, GATE_ACTIVATIONS[activation],
+                                                         NORMS[post_norm], post_weight, post_bias, NORMS[pre_norm],
+                                                         pre_weight, pre_bias, residual_scale, branch_scale, eps, h, n,
+                                                         stream)
+
+
+def block_norm_bwd(y, residual, dh, dn, gate=None, activation="silu", post_norm="rms", post_weight=None,
+                   post_bias=None, pre_norm="rms", pre_weight=None, pre_bias=None, residual_scale=1.0,
+                   branch_scale=1.0, eps=1e-5, dr=None, dy=None, dgate=None, workspace=None, stream=None):
+    """Gradients of block_norm_fwd for dh (None: zero) and dn (None with pre_norm "none"), as a dict: dy, dr, and
+    dgate, dpost_w, dpost_b, dpre_w, dpre_b (None where the forward had None).  workspace: contiguous
+    device memory of la_block_norm_bwd_workspace_bytes, allocated where it is None or smaller."""
+    return (_binding or _layer_binding()).block_norm_bwd(y, residual, dh, dn, gate, GATE_ACTIVATIONS[activation],
+                                                         NORMS[post_norm], post_weight, post_bias, NORMS[pre_norm],
+                                                         pre_weight, pre_bias, residual_scale, branch_scale, eps, dr,
+                                                         dy, dgate, workspace, stream)

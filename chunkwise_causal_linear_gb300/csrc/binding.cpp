@@ -1,5 +1,5 @@
 // binding.cpp -- the torch-tensor forms of the gated attention and of the operators around the attention
-// (recurrence, rotary positions, group norm) as a compiled Python module.
+// (recurrence, rotary positions, group norm, norms around a block) as a compiled Python module.
 //
 // Argument checks, output allocation and the call into the C ABI, nothing else.  Compiled because
 // these calls are short: a decoding step's kernel takes 1 to 3 us, and marshalling it through
@@ -426,6 +426,97 @@ Tensor gated_step(const Tensor &q, const Tensor &k, const Tensor &v, const Tenso
     return out;
 }
 
+// Strides of a [B, L, d] tensor.
+struct RowStrides {
+    la_strides s{};
+    const la_strides *p = nullptr;
+    RowStrides(const OptTensor &t, at::IntArrayRef shape, at::ScalarType type, const at::Device &dev, const char *name)
+    {
+        if (!t) return;
+        check(*t, shape, type, dev, name);
+        if (t->is_contiguous()) return;
+        if (t->stride(2) != 1 && shape[2] > 1)
+            throw py::value_error(std::string(name) + ": the channels (last axis) must be adjacent");
+        s = {t->stride(0), 0, t->stride(1)};
+        p = &s;
+    }
+    RowStrides(const RowStrides &) = delete;
+};
+
+py::tuple block_norm_fwd(const Tensor &y, const Tensor &residual, const OptTensor &gate, int activation, int post,
+                         const OptTensor &post_w, const OptTensor &post_b, int pre, const OptTensor &pre_w,
+                         const OptTensor &pre_b, double rs, double bs, double eps, const OptTensor &h_, const OptTensor &n_,
+                         const OptStream &stream)
+{
+    const char *what = "la_block_norm_fwd";
+    axes(y, 3, "y");
+    const at::Device dev = y.device();
+    const at::ScalarType type = y.scalar_type(), rtype = residual.scalar_type();
+    const int dtype = code(y), rcode = code(residual);
+    const Place place(dev, stream, what);
+    const at::IntArrayRef shape = y.sizes();
+    const int64_t d = shape[2];
+    if (pre == LA_NORM_NONE && (n_ || pre_w || pre_b)) throw py::value_error("n or its weights are given without a norm");
+    const RowStrides sy(y, shape, type, dev, "y"), sr(residual, shape, rtype, dev, "residual"), sg(gate, shape, type, dev, "gate");
+    const float *w1 = dense<float>(post_w, {d}, at::kFloat, dev, "post_weight"), *b1 = dense<float>(post_b, {d}, at::kFloat, dev, "post_bias"),
+                *w2 = dense<float>(pre_w, {d}, at::kFloat, dev, "pre_weight"), *b2 = dense<float>(pre_b, {d}, at::kFloat, dev, "pre_bias");
+    const Tensor h = h_ ? *h_ : at::empty(shape, residual.options());
+    OptTensor n = n_;
+    if (!n && pre != LA_NORM_NONE) n = at::empty(shape, y.options());
+    const RowStrides sh(h, shape, rtype, dev, "h"), sn(n, shape, type, dev, "n");
+    const int rc = la_block_norm_fwd(y.data_ptr(), residual.data_ptr(), ptr(gate), w1, b1, w2, b2, h.data_ptr(), ptr(n),
+                                     (int)shape[0], (int)shape[1], (int)d, sy.p, sr.p, sg.p, sh.p, sn.p, post, pre, activation,
+                                     (float)rs, (float)bs, (float)eps, dtype, rcode, place.stream);
+    if (rc != LA_OK) fail(rc, what);
+    return py::make_tuple(h, n);
+}
+
+py::dict block_norm_bwd(const Tensor &y, const Tensor &residual, const OptTensor &dh, const OptTensor &dn, const OptTensor &gate,
+                        int activation, int post, const OptTensor &post_w, const OptTensor &post_b, int pre,
+                        const OptTensor &pre_w, const OptTensor &pre_b, double rs, double bs, double eps, const OptTensor &dr_,
+                        const OptTensor &dy_, const OptTensor &dgate_, OptTensor workspace, const OptStream &stream)
+{
+    const char *what = "la_block_norm_bwd";
+    axes(y, 3, "y");
+    if (dgate_ && !gate) throw py::value_error("dgate is given without gate");
+    if (pre == LA_NORM_NONE && (dn || pre_w || pre_b)) throw py::value_error("dn or its weights are given without a norm");
+    const at::Device dev = y.device();
+    const at::ScalarType type = y.scalar_type(), rtype = residual.scalar_type();
+    const int dtype = code(y), rcode = code(residual);
+    const Place place(dev, stream, what);
+    const at::IntArrayRef shape = y.sizes();
+    const int64_t B = shape[0], L = shape[1], d = shape[2];
+    const RowStrides sy(y, shape, type, dev, "y"), sr(residual, shape, rtype, dev, "residual"), sg(gate, shape, type, dev, "gate"),
+        sdh(dh, shape, rtype, dev, "dh"), sdn(dn, shape, type, dev, "dn");
+    const float *w1 = dense<float>(post_w, {d}, at::kFloat, dev, "post_weight"), *b1 = dense<float>(post_b, {d}, at::kFloat, dev, "post_bias"),
+                *w2 = dense<float>(pre_w, {d}, at::kFloat, dev, "pre_weight"), *b2 = dense<float>(pre_b, {d}, at::kFloat, dev, "pre_bias");
+    const Tensor dr = dr_ ? *dr_ : at::empty(shape, residual.options()), dy = dy_ ? *dy_ : at::empty(shape, y.options());
+    OptTensor dgate, dw1, db1, dw2, db2;
+    if (gate) dgate = dgate_ ? *dgate_ : at::empty(shape, y.options());
+    const RowStrides sdr(dr, shape, rtype, dev, "dr"), sdy(dy, shape, type, dev, "dy"), sdg(dgate, shape, type, dev, "dgate");
+    const auto f32 = y.options().dtype(at::kFloat);
+    if (post_w) dw1 = at::empty({d}, f32);
+    if (post_b) db1 = at::empty({d}, f32);
+    if (pre_w && dn) dw2 = at::empty({d}, f32);
+    if (pre_b && dn) db2 = at::empty({d}, f32);
+    const size_t need = dw1 || db1 || dw2 || db2 ? la_block_norm_bwd_workspace_bytes((int)B, (int)L, (int)d) : 0;
+    void *ws = room(workspace, need, dev);
+    const int rc = la_block_norm_bwd(y.data_ptr(), residual.data_ptr(), ptr(gate), w1, b1, w2, b2, ptr(dh), ptr(dn), dr.data_ptr(),
+                                     dy.data_ptr(), ptr(dgate), (float *)ptr(dw1), (float *)ptr(db1), (float *)ptr(dw2),
+                                     (float *)ptr(db2), (int)B, (int)L, (int)d, sy.p, sr.p, sg.p, sdh.p, sdn.p, sdr.p, sdy.p, sdg.p,
+                                     post, pre, activation, (float)rs, (float)bs, (float)eps, dtype, rcode, ws, need, place.stream);
+    if (rc != LA_OK) fail(rc, what);
+    py::dict out;
+    out["dy"] = dy;
+    out["dr"] = dr;
+    out["dgate"] = dgate;
+    out["dpost_w"] = dw1;
+    out["dpost_b"] = db1;
+    out["dpre_w"] = dw2;
+    out["dpre_b"] = db2;
+    return out;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_layer, m)
@@ -436,6 +527,8 @@ PYBIND11_MODULE(_layer, m)
     m.def("rotary", &rotary);
     m.def("group_norm_fwd", &group_norm_fwd);
     m.def("group_norm_bwd", &group_norm_bwd);
+    m.def("block_norm_fwd", &block_norm_fwd);
+    m.def("block_norm_bwd", &block_norm_bwd);
     m.def("gated_fwd", &gated_fwd);
     m.def("gated_bwd", &gated_bwd);
     m.def("gated_step", &gated_step);

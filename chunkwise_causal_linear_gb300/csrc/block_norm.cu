@@ -1,0 +1,625 @@
+// block_norm.cu -- the norms around a block, fused with its gate and the residual sum (sm_103a):
+//
+//     h = residual_scale r + branch_scale act(gate) (norm(y) w_post + b_post),
+//     n = norm(h) w_pre + b_pre,
+//
+// and the gradients of both. norm is the root mean square's (x / sqrt(mean(x^2) + eps)), the layer's
+// (centred first) or none (y as it is: w_post is a layer scale then).
+//
+// Bound by memory: y, r and gate are read once, h and n written once; apart, the two norms, the gate and the
+// sum would read and write h and the norm's output once more each. A row is held in the registers of NT
+// threads, 8 channels a thread (16 for rows above 4096), so that its statistics, centred variance and
+// both norms come from that one read; the next row's loads are issued before the row's sums, whose barriers
+// they hide. The gradients recompute the statistics from y and r (32-bit sums; h before its rounding)
+// instead of reading them, and keep the sums for the weights' gradients in the threads' registers; the
+// groups' sums are joined by a second kernel in a fixed order.
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "layer.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+
+namespace {
+
+constexpr int BN_MAX_D = 8192;
+constexpr int BN_SIGMOID = LA_ACT_SIGMOID;
+
+struct BnArgs {
+    const void *y, *r, *gate, *dh, *dn;
+    void *h, *n, *dr, *dy, *dgate;
+    const float *post_w, *post_b, *pre_w, *pre_b;
+    float *part;  // [groups][4][d]: sums for post_w, post_b, pre_w, pre_b
+    View vy, vr, vg, vh, vn, vdh, vdn, vdr, vdy, vdg;
+    long long rows;
+    int L, d, post, pre, act;
+    float rs, bs, eps, inv_d;
+};
+
+// ---- VEC neighbouring channels as they lie in memory, and as fp32 ------------------------------
+template <typename T, int VEC> struct Raw;
+template <> struct Raw<__nv_bfloat16, 8> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *(const uint4 *)p; }
+    __device__ __forceinline__ void get(float *f) const
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = tcc::bf_lo(u[i]);
+            f[2 * i + 1] = tcc::bf_hi(u[i]);
+        }
+    }
+};
+template <> struct Raw<float, 8> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = ((const float4 *)p)[0];
+        b = ((const float4 *)p)[1];
+    }
+    __device__ __forceinline__ void get(float *f) const
+    {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+};
+template <typename T> struct Raw<T, 1> {
+    T v;
+    __device__ __forceinline__ void load(const T *p) { v = *p; }
+    __device__ __forceinline__ void get(float *f) const { f[0] = to_f32(v); }
+};
+template <int VEC> __device__ __forceinline__ void put(__nv_bfloat16 *p, const float *f)
+{
+    if constexpr (VEC == 8) {
+        *(uint4 *)p = make_uint4(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]), ptx::pack_bf16x2(f[4], f[5]),
+                                 ptx::pack_bf16x2(f[6], f[7]));
+    } else {
+        *p = __float2bfloat16_rn(f[0]);
+    }
+}
+template <int VEC> __device__ __forceinline__ void put(float *p, const float *f)
+{
+    if constexpr (VEC == 8) {
+        ((float4 *)p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        ((float4 *)p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        *p = f[0];
+    }
+}
+// VEC values of a vector of weights, `one` where there is none
+template <int VEC> __device__ __forceinline__ void weights(const float *w, int c, float one, float *f)
+{
+    if (!w) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = one;
+    } else if constexpr (VEC == 8) {
+        const float4 a = __ldg((const float4 *)(w + c)), b = __ldg((const float4 *)(w + c) + 1);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+        f[0] = __ldg(w + c);
+    }
+}
+
+// ---- sums over the threads of a row, the same in every one of them -----------------------------
+// Two places in turn, so that one barrier a sum is enough: who writes a place again has passed the
+// barrier behind the sum that everyone read it for.
+template <int NT> struct Sums {
+    float *sm;  // [2][NT / 32][2]
+    int turn = 0;
+    template <int N> __device__ __forceinline__ void operator()(float (&v)[N])
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if constexpr (NT > 32) {
+            constexpr int W = NT / 32;
+            const int t = threadIdx.x % NT;
+            float *p = sm + turn * W * 2;
+            turn ^= 1;
+            if ((t & 31) == 0)
+#pragma unroll
+                for (int i = 0; i < N; ++i) p[(t >> 5) * 2 + i] = v[i];
+            if constexpr (NT >= 256) __syncthreads();  // one row a block
+            else ptx::named_bar(1 + threadIdx.x / NT, NT);
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += p[w * 2 + i];
+        }
+    }
+};
+
+// 1 / (1 + e^-z): for fp32 by the exact division and exponential, for bf16, whose outputs are rounded by
+// up to 2^-8, to (5 + |z|) 2^-23.
+template <typename T> __device__ __forceinline__ float sigmoid(float z)
+{
+    if constexpr (std::is_same<T, float>::value) return 1.f / (1.f + expf(-z));
+    else return __fdividef(1.f, 1.f + __expf(-z));
+}
+
+// A row's mean and 1/deviation, x centred in place where the kind asks for it.
+template <int NT, int N> __device__ __forceinline__ float statistics(float (&x)[N], const bool (&in)[N], int kind, const BnArgs &a, Sums<NT> &sum)
+{
+    if (kind == LA_NORM_LAYER) {
+        float m[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[0] += x[i];
+        sum(m);
+        m[0] *= a.inv_d;
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = in[i] ? x[i] - m[0] : 0.f;
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[0] = fmaf(x[i], x[i], s[0]);
+    sum(s);
+    return rsqrtf(fmaf(s[0], a.inv_d, a.eps));
+}
+
+template <int NT> constexpr int bn_block = NT < 256 ? 256 : NT;
+
+template <typename T, typename R, int VEC, int NT, int NC>
+__global__ void __launch_bounds__(bn_block<NT>) bn_fwd_kernel(const BnArgs a)
+{
+    constexpr int N = VEC * NC, GROUPS = bn_block<NT> / NT;
+    __shared__ float sm[GROUPS * 2 * (NT / 32) * 2];
+    const int tid = threadIdx.x % NT, group = threadIdx.x / NT;
+    Sums<NT> sum{sm + group * 2 * (NT / 32) * 2};
+    const long long first = (long long)blockIdx.x * GROUPS + group, step = (long long)gridDim.x * GROUPS;
+    int at[NC];
+    bool in[N];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        at[c] = (c * NT + tid) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) in[c * VEC + i] = at[c] < a.d;
+    }
+    Raw<T, VEC> ry[NC], rg[NC];
+    Raw<R, VEC> rr[NC];
+    auto fetch = [&](long long row) {
+        const int b = (int)(row / a.L), t = (int)(row % a.L);
+        const T *y = (const T *)a.y + row_of(a.vy, b, 0, t), *g = (const T *)a.gate + row_of(a.vg, b, 0, t);
+        const R *r = (const R *)a.r + row_of(a.vr, b, 0, t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c * VEC]) {
+                ry[c].load(y + at[c]);
+                rr[c].load(r + at[c]);
+                if (a.gate) rg[c].load(g + at[c]);
+            }
+    };
+    if (first < a.rows) fetch(first);
+    for (long long row = first; row < a.rows; row += step) {
+        float u[N], h[N], z[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = h[i] = z[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c * VEC]) {
+                ry[c].get(u + c * VEC);
+                rr[c].get(h + c * VEC);
+                if (a.gate) rg[c].get(z + c * VEC);
+            }
+        if (row + step < a.rows) fetch(row + step);
+        const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<NT>(u, in, a.post, a, sum);
+        const int b = (int)(row / a.L), t = (int)(row % a.L);
+        R *const ho = (R *)a.h + row_of(a.vh, b, 0, t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c * VEC]) {
+                float w[VEC], bias[VEC];
+                weights<VEC>(a.post_w, at[c], 1.f, w);
+                weights<VEC>(a.post_b, at[c], 0.f, bias);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int j = c * VEC + i;
+                    float act = a.bs;
+                    if (a.gate) {
+                        if (a.act == LA_ACT_NONE) act *= z[j];
+                        else act *= sigmoid<T>(z[j]) * (a.act == LA_ACT_SILU ? z[j] : 1.f);
+                    }
+                    h[j] = fmaf(act, fmaf(u[j] * k1, w[i], bias[i]), a.rs * h[j]);
+                }
+                put<VEC>(ho + at[c], h + c * VEC);
+            }
+        if (a.n) {
+            const float k2 = statistics<NT>(h, in, a.pre, a, sum);
+            T *const no = (T *)a.n + row_of(a.vn, b, 0, t);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c * VEC]) {
+                    float w[VEC], bias[VEC], o[VEC];
+                    weights<VEC>(a.pre_w, at[c], 1.f, w);
+                    weights<VEC>(a.pre_b, at[c], 0.f, bias);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) o[i] = fmaf(h[c * VEC + i] * k2, w[i], bias[i]);
+                    put<VEC>(no + at[c], o);
+                }
+        }
+    }
+}
+
+// dx of x/deviation (centred) from dxh, in place, with xh: (dxh - xh mean(dxh xh) [- mean(dxh)]) k.
+template <int NT, int N> __device__ __forceinline__ void norm_back(float (&dxh)[N], const float (&xh)[N], const bool (&in)[N], float k,
+                                                                   int kind, const BnArgs &a, Sums<NT> &sum)
+{
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        s[0] = fmaf(dxh[i], xh[i], s[0]);
+        s[1] += dxh[i];
+    }
+    sum(s);
+    const float m0 = s[0] * a.inv_d, m1 = kind == LA_NORM_LAYER ? s[1] * a.inv_d : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) dxh[i] = in[i] ? (dxh[i] - fmaf(xh[i], m0, m1)) * k : 0.f;
+}
+
+template <typename T, typename R, int VEC, int NT, int NC>
+__global__ void __launch_bounds__(bn_block<NT>) bn_bwd_kernel(const BnArgs a)
+{
+    constexpr int N = VEC * NC, GROUPS = bn_block<NT> / NT;
+    __shared__ float sm[GROUPS * 2 * (NT / 32) * 2];
+    const int tid = threadIdx.x % NT, group = threadIdx.x / NT;
+    Sums<NT> sum{sm + group * 2 * (NT / 32) * 2};
+    const long long first = (long long)blockIdx.x * GROUPS + group, step = (long long)gridDim.x * GROUPS;
+    int at[NC];
+    bool in[N];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        at[c] = (c * NT + tid) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) in[c * VEC + i] = at[c] < a.d;
+    }
+    float total[4][N];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) total[k][i] = 0.f;
+    Raw<T, VEC> ry[NC], rg[NC], rdn[NC];
+    Raw<R, VEC> rr[NC], rdh[NC];
+    auto fetch = [&](long long row) {
+        const int b = (int)(row / a.L), t = (int)(row % a.L);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c * VEC]) {
+                ry[c].load((const T *)a.y + row_of(a.vy, b, 0, t) + at[c]);
+                rr[c].load((const R *)a.r + row_of(a.vr, b, 0, t) + at[c]);
+                if (a.gate) rg[c].load((const T *)a.gate + row_of(a.vg, b, 0, t) + at[c]);
+                if (a.dh) rdh[c].load((const R *)a.dh + row_of(a.vdh, b, 0, t) + at[c]);
+                if (a.dn) rdn[c].load((const T *)a.dn + row_of(a.vdn, b, 0, t) + at[c]);
+            }
+    };
+    if (first < a.rows) fetch(first);
+    for (long long row = first; row < a.rows; row += step) {
+        float u[N], h[N], z[N], dh[N], dn[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = h[i] = z[i] = dh[i] = dn[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c * VEC]) {
+                ry[c].get(u + c * VEC);
+                rr[c].get(h + c * VEC);
+                if (a.gate) rg[c].get(z + c * VEC);
+                if (a.dh) rdh[c].get(dh + c * VEC);
+                if (a.dn) rdn[c].get(dn + c * VEC);
+            }
+        if (row + step < a.rows) fetch(row + step);
+        const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<NT>(u, in, a.post, a, sum);
+        const int b = (int)(row / a.L), t = (int)(row % a.L);
+        float act[N];  // act(gate), times branch_scale
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float w[VEC], bias[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = bias[i] = 0.f;
+            if (in[c * VEC]) {
+                weights<VEC>(a.post_w, at[c], 1.f, w);
+                weights<VEC>(a.post_b, at[c], 0.f, bias);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int j = c * VEC + i;
+                act[j] = a.bs;
+                if (a.gate) {
+                    if (a.act == LA_ACT_NONE) act[j] *= z[j];
+                    else act[j] *= sigmoid<T>(z[j]) * (a.act == LA_ACT_SILU ? z[j] : 1.f);
+                }
+                u[j] *= k1;  // xh of y from here on
+                h[j] = in[j] ? fmaf(act[j], fmaf(u[j], w[i], bias[i]), a.rs * h[j]) : 0.f;
+            }
+        }
+        if (a.dn) {
+            const float k2 = statistics<NT>(h, in, a.pre, a, sum);
+            float g[N];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                float w[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) w[i] = 0.f;
+                if (in[c * VEC]) weights<VEC>(a.pre_w, at[c], 1.f, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int j = c * VEC + i;
+                    h[j] *= k2;
+                    total[2][j] = fmaf(dn[j], h[j], total[2][j]);
+                    total[3][j] += dn[j];
+                    g[j] = dn[j] * w[i];
+                }
+            }
+            norm_back<NT>(g, h, in, k2, a.pre, a, sum);
+#pragma unroll
+            for (int i = 0; i < N; ++i) dh[i] += g[i];
+        }
+        // dh is the whole gradient of h
+        R *const dr = (R *)a.dr + row_of(a.vdr, b, 0, t);
+        T *const dg = (T *)a.dgate + row_of(a.vdg, b, 0, t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float w[VEC], bias[VEC], o[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = bias[i] = 0.f;
+            if (in[c * VEC]) {
+                weights<VEC>(a.post_w, at[c], 1.f, w);
+                weights<VEC>(a.post_b, at[c], 0.f, bias);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] = a.rs * dh[c * VEC + i];
+                put<VEC>(dr + at[c], o);
+                if (a.gate) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const int j = c * VEC + i;
+                        float slope = 1.f;
+                        if (a.act != LA_ACT_NONE) {
+                            const float s = sigmoid<T>(z[j]);
+                            slope = a.act == LA_ACT_SILU ? s * fmaf(z[j], 1.f - s, 1.f) : s * (1.f - s);
+                        }
+                        o[i] = a.bs * dh[j] * fmaf(u[j], w[i], bias[i]) * slope;
+                    }
+                    put<VEC>(dg + at[c], o);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int j = c * VEC + i;
+                const float du = dh[j] * act[j];
+                total[0][j] = fmaf(du, u[j], total[0][j]);
+                total[1][j] += du;
+                dh[j] = du * w[i];
+            }
+        }
+        if (a.post != LA_NORM_NONE) norm_back<NT>(dh, u, in, k1, a.post, a, sum);
+        T *const dy = (T *)a.dy + row_of(a.vdy, b, 0, t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c * VEC]) put<VEC>(dy + at[c], dh + c * VEC);
+    }
+    if (a.part)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c * VEC]) put<VEC>(a.part + (first * 4 + k) * a.d + at[c], total[k] + c * VEC);
+}
+
+struct BnJoin {
+    const float *part;
+    float *out[4];
+    int groups, d;
+};
+// 32 channels a block, the groups' sums in 8 runs of every eighth one, joined in order.
+__global__ void __launch_bounds__(256) bn_join_kernel(const BnJoin a)
+{
+    __shared__ float sm[8][32];
+    const int k = blockIdx.y, x = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    if (!a.out[k]) return;
+    float s = 0.f;
+    if (c < a.d)
+#pragma unroll 8
+        for (int g = run; g < a.groups; g += 8) s += a.part[((long long)g * 4 + k) * a.d + c];
+    sm[run][x] = s;
+    __syncthreads();
+    if (run == 0 && c < a.d) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sm[i][x];
+        a.out[k][c] = s;
+    }
+}
+
+// ---- which kernel takes a row -----------------------------------------------------------------
+// 8 channels a thread where every row can be read 16 bytes at a time; else one by one.
+struct Shape {
+    int nt, block;
+};
+Shape shape_of(int d, bool wide)
+{
+    if (!wide) return d <= 256 ? Shape{32, 256} : Shape{512, 512};
+    const int nt = d <= 256 ? 32 : d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : 512;
+    return {nt, std::max(nt, 256)};
+}
+// Groups that run at once: as many blocks as fit two or more to an SM, each row group looping over its rows.
+int groups_of(long long rows, const Shape &s, int sms, int per_sm)
+{
+    const int per_block = s.block / s.nt;
+    const long long blocks = std::min<long long>((rows + per_block - 1) / per_block, (long long)sms * per_sm);
+    return (int)blocks * per_block;
+}
+constexpr int FWD_THREADS = 1024, BWD_THREADS = 512;  // of an SM's threads that the grids count on
+
+template <typename T, typename R, typename F> int by_shape(int d, bool wide, F &&f)
+{
+    (void)sizeof(T);
+    (void)sizeof(R);
+    if (!wide)
+        return d <= 256 ? f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>(), std::integral_constant<int, 8>())
+                        : f(std::integral_constant<int, 1>(), std::integral_constant<int, 512>(), std::integral_constant<int, 16>());
+    std::integral_constant<int, 8> v;
+    std::integral_constant<int, 1> one;
+    std::integral_constant<int, 2> two;
+    if (d <= 256) return f(v, std::integral_constant<int, 32>(), one);
+    if (d <= 512) return f(v, std::integral_constant<int, 64>(), one);
+    if (d <= 1024) return f(v, std::integral_constant<int, 128>(), one);
+    if (d <= 2048) return f(v, std::integral_constant<int, 256>(), one);
+    if (d <= 4096) return f(v, std::integral_constant<int, 512>(), one);
+    return f(v, std::integral_constant<int, 512>(), two);
+}
+template <typename F> int by_types(int dtype, int rtype, F &&f)
+{
+    if (dtype == LA_F32) return f(0.f, 0.f);
+    if (rtype == LA_F32) return f(__nv_bfloat16(), 0.f);
+    return f(__nv_bfloat16(), __nv_bfloat16());
+}
+
+View row_view(const la_strides *s, int L, int d)
+{
+    if (s) return View{s->b, 0, s->l};
+    return View{(long long)L * d, 0, d};
+}
+
+bool bn_args_ok(int post, int pre, bool has_pre, int act, int d, int dtype, int rtype)
+{
+    if (post < LA_NORM_NONE || post > LA_NORM_LAYER || act < LA_ACT_NONE || act > BN_SIGMOID) return false;
+    if (has_pre && pre != LA_NORM_RMS && pre != LA_NORM_LAYER) return false;
+    if (!dtype_ok(dtype) || !dtype_ok(rtype) || (dtype == LA_F32 && rtype != LA_F32)) return false;
+    return d <= BN_MAX_D;
+}
+
+}  // namespace
+
+}  // namespace la
+
+using namespace la;
+
+extern "C" {
+
+int la_block_norm_fwd(const void *y, const void *residual, const void *gate, const float *post_weight, const float *post_bias,
+                      const float *pre_weight, const float *pre_bias, void *h, void *n, int B, int L, int d,
+                      const la_strides *y_strides, const la_strides *residual_strides, const la_strides *gate_strides,
+                      const la_strides *h_strides, const la_strides *n_strides, int post_norm, int pre_norm, int activation,
+                      float residual_scale, float branch_scale, float eps, int dtype, int residual_dtype, void *stream)
+{
+    if (!y || !residual || !h) return LA_ERR_NULL;
+    if (!sizes_ok(B, 1, L, d)) return LA_ERR_SHAPE;
+    if (!bn_args_ok(post_norm, pre_norm, n != nullptr, activation, d, dtype, residual_dtype)) return LA_ERR_UNSUPPORTED;
+    BnArgs a = {};
+    a.y = y; a.r = residual; a.gate = gate; a.h = h; a.n = n;
+    a.post_w = post_weight; a.post_b = post_bias; a.pre_w = pre_weight; a.pre_b = pre_bias;
+    a.vy = row_view(y_strides, L, d);
+    a.vr = row_view(residual_strides, L, d);
+    a.vg = row_view(gate_strides, L, d);
+    a.vh = row_view(h_strides, L, d);
+    a.vn = row_view(n_strides, L, d);
+    if (!input_view_ok(a.vy, B, 1, L) || !input_view_ok(a.vr, B, 1, L) || (gate && !input_view_ok(a.vg, B, 1, L)) ||
+        !output_view_ok(a.vh, B, 1, L, d) || (n && !output_view_ok(a.vn, B, 1, L, d)) || !(eps > 0.f) || !isfinite(eps) ||
+        !isfinite(residual_scale) || !isfinite(branch_scale))
+        return LA_ERR_ARG;
+    const size_t es = dtype_size(dtype), er = dtype_size(residual_dtype);
+    if (!aligned(y, es) || !aligned(gate, es) || !aligned(n, es) || !aligned(residual, er) || !aligned(h, er) ||
+        !aligned(post_weight, 4) || !aligned(post_bias, 4) || !aligned(pre_weight, 4) || !aligned(pre_bias, 4))
+        return LA_ERR_ARG;
+    a.rows = (long long)B * L;
+    a.L = L; a.d = d; a.post = post_norm; a.pre = pre_norm; a.act = activation;
+    a.rs = residual_scale; a.bs = branch_scale; a.eps = eps; a.inv_d = 1.f / (float)d;
+    const int sms = device_sms();
+    if (sms <= 0) return LA_ERR_CUDA;
+    auto ok = [&](const void *p, const View &v, size_t e) { return !p || rows_aligned(p, v, B, 1, L, e, 16); };
+    const bool wide = d % 8 == 0 && ok(y, a.vy, es) && ok(residual, a.vr, er) && ok(gate, a.vg, es) && ok(h, a.vh, er) &&
+                      ok(n, a.vn, es) && aligned(post_weight, 16) && aligned(post_bias, 16) && aligned(pre_weight, 16) &&
+                      aligned(pre_bias, 16);
+    const Shape s = shape_of(d, wide);
+    const int grid = groups_of(a.rows, s, sms, std::max(1, FWD_THREADS / s.block)) / (s.block / s.nt);
+    return by_types(dtype, residual_dtype, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        return by_shape<T, R>(d, wide, [&](auto v, auto nt, auto nc) {
+            return launch(bn_fwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt>, 0, (cudaStream_t)stream, a);
+        });
+    });
+}
+
+size_t la_block_norm_bwd_workspace_bytes(int B, int L, int d)
+{
+    if (!sizes_ok(B, 1, L, d) || d > BN_MAX_D) return 0;
+    const int sms = device_sms() > 0 ? device_sms() : 152;
+    size_t most = 0;  // whichever way the rows are aligned
+    for (const bool wide : {false, true}) {
+        const Shape s = shape_of(d, wide);
+        most = std::max(most, (size_t)groups_of((long long)B * L, s, sms, std::max(1, BWD_THREADS / s.block)));
+    }
+    return most * 4 * d * sizeof(float);
+}
+
+int la_block_norm_bwd(const void *y, const void *residual, const void *gate, const float *post_weight, const float *post_bias,
+                      const float *pre_weight, const float *pre_bias, const void *dh, const void *dn, void *dresidual, void *dy,
+                      void *dgate, float *dpost_weight, float *dpost_bias, float *dpre_weight, float *dpre_bias, int B, int L,
+                      int d, const la_strides *y_strides, const la_strides *residual_strides, const la_strides *gate_strides,
+                      const la_strides *dh_strides, const la_strides *dn_strides, const la_strides *dresidual_strides,
+                      const la_strides *dy_strides, const la_strides *dgate_strides, int post_norm, int pre_norm, int activation,
+                      float residual_scale, float branch_scale, float eps, int dtype, int residual_dtype, void *workspace,
+                      size_t workspace_bytes, void *stream)
+{
+    if (!y || !residual || !dresidual || !dy || (!dh && !dn) || !gate != !dgate) return LA_ERR_NULL;
+    if (!dn && (dpre_weight || dpre_bias)) return LA_ERR_NULL;
+    if (!sizes_ok(B, 1, L, d)) return LA_ERR_SHAPE;
+    if (!bn_args_ok(post_norm, pre_norm, dn != nullptr, activation, d, dtype, residual_dtype)) return LA_ERR_UNSUPPORTED;
+    BnArgs a = {};
+    a.y = y; a.r = residual; a.gate = gate; a.dh = dh; a.dn = dn;
+    a.dr = dresidual; a.dy = dy; a.dgate = dgate;
+    a.post_w = post_weight; a.post_b = post_bias; a.pre_w = pre_weight; a.pre_b = pre_bias;
+    a.vy = row_view(y_strides, L, d);
+    a.vr = row_view(residual_strides, L, d);
+    a.vg = row_view(gate_strides, L, d);
+    a.vdh = row_view(dh_strides, L, d);
+    a.vdn = row_view(dn_strides, L, d);
+    a.vdr = row_view(dresidual_strides, L, d);
+    a.vdy = row_view(dy_strides, L, d);
+    a.vdg = row_view(dgate_strides, L, d);
+    if (!input_view_ok(a.vy, B, 1, L) || !input_view_ok(a.vr, B, 1, L) || (gate && !input_view_ok(a.vg, B, 1, L)) ||
+        (dh && !input_view_ok(a.vdh, B, 1, L)) || (dn && !input_view_ok(a.vdn, B, 1, L)) || !output_view_ok(a.vdr, B, 1, L, d) ||
+        !output_view_ok(a.vdy, B, 1, L, d) || (gate && !output_view_ok(a.vdg, B, 1, L, d)) || !(eps > 0.f) || !isfinite(eps) ||
+        !isfinite(residual_scale) || !isfinite(branch_scale))
+        return LA_ERR_ARG;
+    const size_t es = dtype_size(dtype), er = dtype_size(residual_dtype);
+    if (!aligned(y, es) || !aligned(gate, es) || !aligned(dn, es) || !aligned(dy, es) || !aligned(dgate, es) ||
+        !aligned(residual, er) || !aligned(dh, er) || !aligned(dresidual, er) || !aligned(post_weight, 4) ||
+        !aligned(post_bias, 4) || !aligned(pre_weight, 4) || !aligned(pre_bias, 4) || !aligned(dpost_weight, 4) ||
+        !aligned(dpost_bias, 4) || !aligned(dpre_weight, 4) || !aligned(dpre_bias, 4) || !aligned(workspace, 16))
+        return LA_ERR_ARG;
+    a.rows = (long long)B * L;
+    a.L = L; a.d = d; a.post = post_norm; a.pre = pre_norm; a.act = activation;
+    a.rs = residual_scale; a.bs = branch_scale; a.eps = eps; a.inv_d = 1.f / (float)d;
+    const int sms = device_sms();
+    if (sms <= 0) return LA_ERR_CUDA;
+    auto ok = [&](const void *p, const View &v, size_t e) { return !p || rows_aligned(p, v, B, 1, L, e, 16); };
+    const bool wide = d % 8 == 0 && ok(y, a.vy, es) && ok(residual, a.vr, er) && ok(gate, a.vg, es) && ok(dh, a.vdh, er) &&
+                      ok(dn, a.vdn, es) && ok(dresidual, a.vdr, er) && ok(dy, a.vdy, es) && ok(dgate, a.vdg, es) &&
+                      aligned(post_weight, 16) && aligned(post_bias, 16) && aligned(pre_weight, 16) && aligned(pre_bias, 16);
+    const Shape s = shape_of(d, wide);
+    const int groups = groups_of(a.rows, s, sms, std::max(1, BWD_THREADS / s.block)), grid = groups / (s.block / s.nt);
+    const bool sums = dpost_weight || dpost_bias || dpre_weight || dpre_bias;
+    if (sums) {
+        if (!workspace || workspace_bytes < (size_t)groups * 4 * d * sizeof(float)) return LA_ERR_WORKSPACE;
+        a.part = (float *)workspace;
+    }
+    const int rc = by_types(dtype, residual_dtype, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        return by_shape<T, R>(d, wide, [&](auto v, auto nt, auto nc) {
+            return launch(bn_bwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt>, 0, (cudaStream_t)stream, a);
+        });
+    });
+    if (rc != LA_OK || !sums) return rc;
+    const BnJoin j{a.part, {dpost_weight, dpost_bias, dpre_weight, dpre_bias}, groups, d};
+    return launch(bn_join_kernel, dim3((unsigned)((d + 31) / 32), 4), 256, 0, (cudaStream_t)stream, j);
+}
+
+}  // extern "C"

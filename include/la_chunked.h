@@ -571,7 +571,8 @@ int la_rotary(const void *q, const void *k, void *q_out, void *k_out,
 /* ---- group norm with an activation, channels last ---- */
 enum la_activation {
     LA_ACT_NONE = 0, /* act(y) = y                                                        */
-    LA_ACT_SILU = 1  /* act(y) = y / (1 + exp(-y))                                        */
+    LA_ACT_SILU = 1, /* act(y) = y / (1 + exp(-y))                                        */
+    LA_ACT_SIGMOID = 2 /* act(y) = 1 / (1 + exp(-y)); the gate of la_block_norm_fwd only   */
 };
 
 /*
@@ -613,6 +614,66 @@ int la_group_norm_bwd(const void *x, const float *weight, const float *bias, con
 /* Workspace bytes la_group_norm_bwd needs for these sizes when weight gradients are asked for
  * (0 on invalid arguments). */
 size_t la_group_norm_bwd_workspace_bytes(int B, int H, int L, int d);
+
+/* ---- norms around a block, with its gate and the residual sum ---- */
+enum la_norm_kind {
+    LA_NORM_NONE = 0, /* x                                                                 */
+    LA_NORM_RMS = 1,  /* x / sqrt(mean(x^2) + eps)                                          */
+    LA_NORM_LAYER = 2 /* (x - mean) / sqrt(var + eps)                                       */
+};
+
+/*
+ * la_block_norm_fwd -- behind a block, and before the next one:
+ *     h = residual_scale r + branch_scale act(gate) (norm(y) post_weight + post_bias),
+ *     n = norm(h) pre_weight + pre_bias,
+ * over rows of d channels.  y is the block's output, r the residual stream before it, h behind it, n the
+ * next block's input.  With post_norm LA_NORM_NONE post_weight is a layer scale.
+ *   y, gate, n    [B, L, d], dtype `dtype`; gate may be NULL (act is 1), n may be NULL (only h is formed)
+ *   residual, h   [B, L, d], dtype `residual_dtype`: `dtype`, or LA_F32
+ *   strides       of the axes B and L (b and l; h is not read); NULL: contiguous.  0 broadcasts an input.
+ *   *_weight, *_bias  device fp32 [d] or NULL (1 and 0)
+ *   post_norm, pre_norm  enum la_norm_kind; pre_norm is not LA_NORM_NONE where n is given
+ *   activation    enum la_activation, of the gate
+ *   scales, eps   finite, eps > 0, else LA_ERR_ARG
+ *   d             at most 8192, else LA_ERR_UNSUPPORTED
+ * Statistics are fp32 over values held in fp32, n's over h before it is rounded; each output is rounded
+ * once.  h may be residual, and n may be y, with the same strides; otherwise outputs must not overlap
+ * inputs.
+ */
+int la_block_norm_fwd(const void *y, const void *residual, const void *gate,
+                      const float *post_weight, const float *post_bias, const float *pre_weight,
+                      const float *pre_bias, void *h, void *n, int B, int L, int d,
+                      const la_strides *y_strides, const la_strides *residual_strides,
+                      const la_strides *gate_strides, const la_strides *h_strides,
+                      const la_strides *n_strides, int post_norm, int pre_norm, int activation,
+                      float residual_scale, float branch_scale, float eps, int dtype,
+                      int residual_dtype, void *stream);
+
+/*
+ * la_block_norm_bwd -- its gradients from dh (as h; the gradient that reaches h by the residual stream, NULL
+ * for zero) and dn (as n; NULL where n was not used): dresidual (as residual), dy (as y), dgate (as gate,
+ * NULL if and only if gate is; a broadcast gate's is the whole [B, L, d]), and device fp32 [d] or NULL each
+ * dpost_weight, dpost_bias, dpre_weight, dpre_bias (the last two with dn only).  Statistics and h are formed
+ * again from y and r, so the forward's h may be gone.  The weights' sums are taken in a fixed order through the
+ * workspace of la_block_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned (not needed without them).
+ * dresidual may be dh, and dy may be dn, with the same strides; otherwise outputs must not overlap inputs.
+ */
+int la_block_norm_bwd(const void *y, const void *residual, const void *gate,
+                      const float *post_weight, const float *post_bias, const float *pre_weight,
+                      const float *pre_bias, const void *dh, const void *dn, void *dresidual,
+                      void *dy, void *dgate, float *dpost_weight, float *dpost_bias,
+                      float *dpre_weight, float *dpre_bias, int B, int L, int d,
+                      const la_strides *y_strides, const la_strides *residual_strides,
+                      const la_strides *gate_strides, const la_strides *dh_strides,
+                      const la_strides *dn_strides, const la_strides *dresidual_strides,
+                      const la_strides *dy_strides, const la_strides *dgate_strides, int post_norm,
+                      int pre_norm, int activation, float residual_scale, float branch_scale,
+                      float eps, int dtype, int residual_dtype, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Workspace bytes la_block_norm_bwd needs for these sizes when weight gradients are asked for (0 on
+ * invalid arguments). */
+size_t la_block_norm_bwd_workspace_bytes(int B, int L, int d);
 
 /* ---- gated attention: a decay for each head, or for each token and head ----
  *
