@@ -34,7 +34,7 @@ _spec = importlib.util.find_spec("torch")
 TORCH = cuda_torch(os.path.dirname(_spec.origin) if _spec else None)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["api.cu", "simt.cu", "tc.cu", "tc_favor.cu", "tc_loglinear.cu", "tc_wide.cu", "decode.cu", "noncausal.cu", "noalloc.cu", "bwd.cu", "bwd_ll.cu",
-           "recurrence.cu", "rotary.cu", "group_norm.cu", "gated.cu",
+           "recurrence.cu", "rotary.cu", "group_norm.cu", "gated.cu", "gated_tc.cu",
            "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -856,18 +856,20 @@ int la_gated_fwd(const void *q, const void *k, const void *v, const float *log_d
     p.dtype = dtype;
     p.ws = (float *)workspace;
     p.stream = (cudaStream_t)stream;
-    if (path == LA_PATH_TC) return LA_ERR_UNSUPPORTED;
+    const bool tc = path != LA_PATH_SIMT && gated_tc_fwd_ok(p);
+    if (path == LA_PATH_TC && !tc) return LA_ERR_UNSUPPORTED;
     if ((p.sms = device_sms()) <= 0 || !(p.err = err_ptr())) return LA_ERR_CUDA;
-    const size_t need = gated_simt_fwd_ws(B, H, L, dk, dv, p.sms);
+    const size_t need = tc ? gated_tc_fwd_ws(B, H, L, dk, dv, p.sms) : gated_simt_fwd_ws(B, H, L, dk, dv, p.sms);
     if (need && (!workspace || workspace_bytes < need)) return LA_ERR_WORKSPACE;
-    return gated_simt_fwd(p);
+    return tc ? gated_tc_fwd(p) : gated_simt_fwd(p);
 }
 
 size_t la_gated_workspace_bytes(int B, int H, int L, int dk, int dv, int dtype)
 {
-    const int sms = device_sms();
     if (!gated_sizes_ok(B, H, H, L, dk, dv) || dk > 256 || dv > 256 || !dtype_ok(dtype)) return 0;
-    return gated_simt_fwd_ws(B, H, L, dk, dv, sms > 0 ? sms : 152);
+    const int n = device_sms(), sms = n > 0 ? n : 152;
+    const size_t simt = gated_simt_fwd_ws(B, H, L, dk, dv, sms);
+    return dtype == LA_BF16 ? std::max(simt, gated_tc_fwd_ws(B, H, L, dk, dv, sms)) : simt;
 }
 
 int la_gated_bwd(const void *q, const void *k, const void *v, const float *log_decay, const float *state0,
@@ -907,18 +909,21 @@ int la_gated_bwd(const void *q, const void *k, const void *v, const float *log_d
     p.dtype = dtype;
     p.ws = (float *)workspace;
     p.stream = (cudaStream_t)stream;
-    if (path == LA_PATH_TC) return LA_ERR_UNSUPPORTED;
+    const bool tc = path != LA_PATH_SIMT && gated_tc_bwd_ok(p);
+    if (path == LA_PATH_TC && !tc) return LA_ERR_UNSUPPORTED;
     if ((p.sms = device_sms()) <= 0 || !(p.err = err_ptr())) return LA_ERR_CUDA;
-    if (!workspace || workspace_bytes < gated_simt_bwd_ws(B, H, Hk, L, dk, dv, p.sms)) return LA_ERR_WORKSPACE;
+    const size_t need = tc ? gated_tc_bwd_ws(B, H, Hk, L, dk, dv, p.sms) : gated_simt_bwd_ws(B, H, Hk, L, dk, dv, p.sms);
+    if (!workspace || workspace_bytes < need) return LA_ERR_WORKSPACE;
     if ((double)B * H * bwd_segments(B, H, L, dk, dv, p.sms) > INT_MAX / 4) return LA_ERR_SHAPE;  // grids
-    return gated_simt_bwd(p);
+    return tc ? gated_tc_bwd(p) : gated_simt_bwd(p);
 }
 
 size_t la_gated_bwd_workspace_bytes(int B, int H, int Hk, int L, int dk, int dv, int dtype)
 {
-    const int sms = device_sms();
     if (!gated_sizes_ok(B, H, Hk, L, dk, dv) || dk > 256 || dv > 256 || !dtype_ok(dtype)) return 0;
-    return gated_simt_bwd_ws(B, H, Hk, L, dk, dv, sms > 0 ? sms : 152);
+    const int n = device_sms(), sms = n > 0 ? n : 152;
+    const size_t simt = gated_simt_bwd_ws(B, H, Hk, L, dk, dv, sms);
+    return dtype == LA_BF16 ? std::max(simt, gated_tc_bwd_ws(B, H, Hk, L, dk, dv, sms)) : simt;
 }
 
 int la_gated_step(const void *q, const void *k, const void *v, const float *log_decay, float *state, const int *slots,

@@ -61,4 +61,12 @@ size_t gated_simt_bwd_ws(int B, int H, int Hk, int L, int d, int e, int sms);
 int gated_simt_fwd(const GatedArgs &p);
 int gated_simt_bwd(const GatedArgs &p);
 
+// The tensor cores' path: bf16, 64 or 128 channels, rows of 16-byte alignment, no broadcast.
+bool gated_tc_fwd_ok(const GatedArgs &p);
+bool gated_tc_bwd_ok(const GatedArgs &p);
+size_t gated_tc_fwd_ws(int B, int H, int L, int d, int e, int sms);
+size_t gated_tc_bwd_ws(int B, int H, int Hk, int L, int d, int e, int sms);
+int gated_tc_fwd(const GatedArgs &p);
+int gated_tc_bwd(const GatedArgs &p);
+
 }  // namespace la

@@ -1,0 +1,855 @@
+// gated_tc.cu -- the gated attention on the tensor cores (sm_103a): bf16, 64 or 128 channels.
+//
+// One sweep computes S <- a S + y z^T, out = x^T S over a head's rows, in chunks of 64. With G the sums of
+// the chunk's log decays up to and with each row, S the state before the chunk:
+//
+//     out_i = e_i x_i^T S + sum_{j<=i} w_ij (x_i . y_j) z_j,     e_i = exp(G_i), w_ij = exp(G_i - G_j),
+//     S    <- exp(G_63) S + sum_j f_j y_j z_j^T,                 f_j = exp(G_63 - G_j).
+//
+// No weight is above 1, and none is a quotient, so no decay is too fast; the log decays are data and differ
+// by row, so no factor of theirs can be moved into an operand. A row whose decay is 0 cuts the chunk:
+// pairs across it are 0. From the last row on (the gradients of k and v) e and f change places and
+// the mask turns. The forward pass is the sweep of (q, k, v), dq that of (dout, v, k), dk that of (v, dout, q)
+// and dv that of (k, q, dout), the last two from the end.
+//
+// Products per chunk (bf16 operands, fp32 sums; DX, DZ: 64 or 128 channels of x, y and of z):
+//     scores  A     = X Y^T            M 64   N 64   K DX     both K-major
+//     state   dS^T  = Z^T Y~           M DZ   N DX   K 64     both MN-major; Y~ = f Y in three bf16 parts
+//     inter   Oi^T  = S^T X^T          M DZ   N 64   K DX     S^T from TMEM, in NS bf16 parts
+//     intra   Oa^T  = Z^T P^T          M DZ   N 64   K 64     P = w A
+//     inner   A2    = W Z^T            M 64   N 64   K DZ     backward only, see below
+// What is rounded to bf16: P once, and S once where only a bf16 output reads it (NS = 1; the output's own
+// rounding is as large). The state itself is fp32 in registers: dS is summed by itself and joins it by one
+// rounding a chunk, and Y~'s three parts hold f Y to 2^-24, so that states are those of fp32 arithmetic. The
+// decays' gradient reads the inter rows, there S too has three parts.
+//
+// Warps (640 threads, one block an SM): 0 loads tiles by TMA into a ring and forms the chunks' weights
+// (64-bit sums); 1 issues the products; 4-11 form Y~ and P; 12-19 hold the state (S^T, row = lane of
+// their TMEM quadrant, half of the columns each), write its copy and store the rows.
+//
+// The decays' gradient (DOT) needs R_i = q_i . dq_i and C_j = k_j . dk_j without the rows' own pairs. Over
+// earlier chunks they are the products of the inter rows with a fourth tile (q or k, W); inside the chunk
+// R and C are the row and column sums of w_ij (dout_i . v_j) (q_i . k_j), which the dq sweep forms from both
+// score blocks in fp32 (INNER). Every 1024 rows the sweeps store S and D for the anchors.
+//
+// Bound: 1024 bytes a row and head at 128 channels against about 25 to 36 products of 64 to 128 rows a
+// chunk, which take about as long as the memory.
+#include <algorithm>
+#include <atomic>
+#include <stdlib.h>
+
+#include "gated.cuh"
+#include "tc_common.cuh"
+
+namespace la {
+
+using namespace ptx;
+using namespace tcc;
+
+namespace {
+
+constexpr int GT_THREADS = 640;
+constexpr int GT_C = 64;      // rows of a chunk
+constexpr int GT_SLOTS = 8;   // ring of the chunks' weights
+constexpr int PY0 = 4, ST0 = 12;  // first warp of each group of eight
+
+struct GtArgs {
+    CUtensorMap mx, my, mz, mw;
+    const float *g;
+    View vg, vo;
+    void *out;
+    int out_f32;
+    int sx, sy, sz, sw;  // heads of the state to a head of the operand
+    int B, H, L, e;      // e: channels of out
+    float yscale, oscale;
+    int reverse, totals, inner;
+    int seg_rows, nseg;
+    const int *lengths, *slots;
+    int n_slots;
+    const float *init;
+    float *fin, *decay;
+    int by_seg;
+    int rs, cs;          // element (x channel, z channel) of a stored state
+    float *anchors;      // S at the anchors' starts (causal; one more behind the last) or D at their ends
+    int anchor_chunks, n_anchors;
+    float *dot;          // DOT: [4][B H][L] inter parts, then (inner) [2] row sums
+    float *dotc;         // inner: [4][B H][L] column sums
+    int *err;
+    unsigned long long timeout_ns;
+};
+
+struct Weights {          // of one chunk
+    float4 row[GT_C];     // G in units of a doubling, hi and lo; the run of rows between decays of 0
+    float kw[GT_C];       // of Y's rows (f, or e in reverse), times yscale
+    float rw[GT_C];       // of the inter rows (e, or f in reverse), times oscale
+    float a, em, pad[2];  // decay over the chunk, and that minus 1
+};
+
+template <int DX, int DZ, bool DOT> struct GtLayout {
+    static constexpr int NS = DOT ? 3 : 1;  // bf16 parts of the state's copy
+    static constexpr int X = GT_C * DX * 2, Z = GT_C * DZ * 2, W = DOT ? Z : 0;
+    static constexpr int STAGE = 2 * X + Z + W;
+    static constexpr int YT = 3 * X, P = GT_C * GT_C * 2;
+    static constexpr int FIXED = YT + 2 * P + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
+    static constexpr int STAGES = (232448 - FIXED) / STAGE >= 4 ? 4 : (232448 - FIXED) / STAGE;
+    static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_W = OFF_P + 2 * P,
+                         OFF_BAR = OFF_W + GT_SLOTS * (int)sizeof(Weights), ALLOC = OFF_BAR + 256 + 1024;
+    // TMEM columns
+    static constexpr uint32_t T_SC = 0, T_DS = NS * (DX / 2), T_OI = T_DS + DX, T_OA = T_OI + 64, T_A = T_OA + 64;
+    // the second score block has columns of its own where they are left, else those of Oi
+    static constexpr bool A2_OWN = T_A + 128 <= 512;
+    static constexpr uint32_t T_A2 = A2_OWN ? T_A + 64 : T_OI;
+    static_assert(T_A + 64 <= 512 && ALLOC <= 232448 && STAGES >= 2, "fits");
+    static_assert(STAGE % 1024 == 0 && YT % 1024 == 0, "swizzle atoms");
+};
+
+__device__ __forceinline__ uint32_t pair_at(const uint8_t *tile, int row, int c)  // channels c, c + 1 of a swizzled tile
+{
+    return *(const uint32_t *)(tile + (c >> 6) * (GT_C * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2);
+}
+
+// x in three bf16 parts, two at a time: hi + mid + lo = x to 2^-24.
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    hi = pack_bf16x2(x0, x1);
+    x0 -= bf_lo(hi);
+    x1 -= bf_hi(hi);
+    mid = pack_bf16x2(x0, x1);
+    lo = pack_bf16x2(x0 - bf_lo(mid), x1 - bf_hi(mid));
+}
+
+template <int DX, int DZ, bool DOT>
+__global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_constant__ GtArgs a)
+{
+    using Lay = GtLayout<DX, DZ, DOT>;
+    constexpr int C = GT_C, NST = Lay::STAGES, NS = Lay::NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *const sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Weights *const weights = (Weights *)(sm + Lay::OFF_W);
+    uint64_t *const bars = (uint64_t *)(sm + Lay::OFF_BAR);
+    uint64_t *const full = bars, *const stage_free = full + NST, *const yt_ready = stage_free + NST, *const state_done = yt_ready + 1,
+             *const s_ready = state_done + 1, *const scores_done = s_ready + 1, *const sc_free = scores_done + 1,
+             *const p_ready = sc_free + 1, *const o_done = p_ready + 2, *const o_free = o_done + 1, *const drain = o_free + 1;
+    uint32_t *const tmem_slot = (uint32_t *)(sm + Lay::OFF_BAR + 224);
+    volatile int *const abort_flag = (volatile int *)(sm + Lay::OFF_BAR + 228);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int BH = a.B * a.H, bh = blockIdx.x % BH, seg = blockIdx.x / BH, b = bh / a.H, h = bh % a.H;
+    const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L),
+              te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
+    const int nch = (te - t0 + C - 1) / C;
+    const bool totals = a.totals != 0, rev = a.reverse != 0, inner = DOT && a.inner != 0;
+    const int slot = gated_slot(a.slots, b, a.n_slots, tid == 0 ? a.err : nullptr);
+    const Ctl ctl{abort_flag, a.err, a.timeout_ns};
+    auto chunk_of = [&](int c) { return rev ? nch - 1 - c : c; };  // c-th chunk of the sweep
+
+    auto tile_x = [&](int s) { return sm + s * Lay::STAGE; };
+    auto tile_y = [&](int s) { return tile_x(s) + Lay::X; };
+    auto tile_z = [&](int s) { return tile_y(s) + Lay::X; };
+    auto tile_w = [&](int s) { return tile_z(s) + Lay::Z; };
+    uint8_t *const yt = sm + Lay::OFF_YT, *const p_tile = sm + Lay::OFF_P;
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 2);                       // the TMA's bytes, the weights
+            mbar_init(&stage_free[i], DOT && !totals ? 9 : 1);  // the products, and the readers of W
+        }
+        mbar_init(yt_ready, 8);
+        mbar_init(state_done, 1);
+        mbar_init(s_ready, 8);
+        mbar_init(scores_done, 1);
+        mbar_init(sc_free, 8);
+        mbar_init(p_ready, 8);  // by chunks in turn: P of the next one may be done before this one's is awaited
+        mbar_init(p_ready + 1, 8);
+        mbar_init(o_done, 1);
+        mbar_init(o_free, 8);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_phase(bar, parity, ctl)) != 0; };
+    auto arrive = [&](uint64_t *bar) {  // of a warp whose lanes have all done their part
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ tiles and weights
+        const float *const gp = a.g + b * a.vg.b + h * a.vg.h;
+        auto gate = [&](int c, int i) {  // log decay of row i of the sweep's chunk c; 0 behind the end
+            const int t = t0 + chunk_of(c) * C + i;
+            return c < nch && t < te ? gp[(long long)t * a.vg.l] : 0.f;
+        };
+        int issued = 0;
+        float g0 = gate(0, 2 * lane), g1 = gate(0, 2 * lane + 1);
+        for (int c = 0; c < nch; ++c) {
+            const int s = c % NST;
+            if (c >= NST && !wait(&stage_free[s], ((c / NST) - 1) & 1)) break;
+            if (lane == 0) {
+                const int row = t0 + chunk_of(c) * C;
+                mbar_arrive_expect_tx(&full[s], totals ? Lay::X + Lay::Z : Lay::STAGE);
+                for (int k = 0; k < DX / 64; ++k) {
+                    if (!totals) tma_load_4d(tile_x(s) + k * C * 128, &a.mx, k * 64, row, h / a.sx, b, &full[s]);
+                    tma_load_4d(tile_y(s) + k * C * 128, &a.my, k * 64, row, h / a.sy, b, &full[s]);
+                }
+                for (int k = 0; k < DZ / 64; ++k) {
+                    tma_load_4d(tile_z(s) + k * C * 128, &a.mz, k * 64, row, h / a.sz, b, &full[s]);
+                    if (DOT && !totals) tma_load_4d(tile_w(s) + k * C * 128, &a.mw, k * 64, row, h / a.sw, b, &full[s]);
+                }
+            }
+            issued = c + 1;
+            const float n0 = gate(c + 1, 2 * lane), n1 = gate(c + 1, 2 * lane + 1);  // on its way meanwhile
+            // sums of the rows 0 .. i, in 64 bits; rows whose decay is 0 count as cuts instead
+            const bool z0 = expf(g0) == 0.f, z1 = expf(g1) == 0.f;
+            const double d0 = z0 ? 0.0 : (double)g0, d1 = z1 ? 0.0 : (double)g1;
+            double run = d0 + d1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double u = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += u;
+            }
+            const double all = __shfl_sync(0xffffffffu, run, 31), G1 = run, G0 = run - d1;
+            const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
+            const uint32_t below = (1u << lane) - 1u;
+            const int cuts = __popc(m0) + __popc(m1);
+            const int r0 = __popc(m0 & (below | (1u << lane))) + __popc(m1 & below), r1 = r0 + (z1 ? 1 : 0);
+            Weights &w = weights[c % GT_SLOTS];
+            constexpr double LOG2E = 1.4426950408889634074;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const double G = i ? G1 : G0;
+                const int run_id = i ? r1 : r0;
+                const double G2 = G * LOG2E;
+                const float hi = (float)G2, lo = (float)(G2 - (double)hi);
+                w.row[2 * lane + i] = make_float4(hi, lo, __int_as_float(run_id), 0.f);
+                const float start = run_id == 0 ? expf((float)G) : 0.f, end = run_id == cuts ? expf((float)(all - G)) : 0.f;
+                w.kw[2 * lane + i] = a.yscale * (rev ? start : end);
+                w.rw[2 * lane + i] = a.oscale * (rev ? end : start);
+            }
+            if (lane == 0) {
+                w.a = cuts ? 0.f : expf((float)all);
+                w.em = cuts ? -1.f : expm1f((float)all);
+            }
+            g0 = n0;
+            g1 = n1;
+            arrive(&full[s]);
+        }
+        // never leave the CTA with loads in flight: wait for every issued stage to land
+        if (lane == 0)
+            for (int c = (issued > NST ? issued - NST : 0); c < issued; ++c) {
+                const uint64_t begin = globaltimer();
+                while (!mbar_try_sleep(&full[c % NST], (c / NST) & 1, 200000u))
+                    if (globaltimer() - begin > ctl.timeout_ns) break;
+            }
+        if (a.decay) {
+            double s = 0;
+            for (int t = t0 + lane; t < te; t += 32) s += (double)gp[(long long)t * a.vg.l];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0) a.decay[(long long)seg * BH + bh] = (float)exp(s);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            constexpr uint32_t ID_SC = idesc_bf16_f32(C, C, 0, 0), ID_INTER = idesc_bf16_f32(DZ, C, 0, 0),
+                               ID_STATE = idesc_bf16_f32(DZ, DX, 1, 1), ID_INTRA = idesc_bf16_f32(DZ, C, 1, 0);
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, ctl); };
+            auto scores = [&](int c) {
+                const int s = c % NST;
+                if (!wait1(&full[s], (c / NST) & 1)) return false;
+                tc_fence_after();
+                const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024), dy = smem_desc(smem_u32(tile_y(s)), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < DX / 16; ++k) {
+                    const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
+                    mma_ss(tmem + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0);
+                }
+                if (inner) {
+                    const uint64_t dw = smem_desc(smem_u32(tile_w(s)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < DZ / 16; ++k) {
+                        const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
+                        mma_ss(tmem + Lay::T_A2, desc_add(dw, o), desc_add(dz, o), ID_SC, k > 0);
+                    }
+                }
+                mma_commit(scores_done);
+                return true;
+            };
+            // Oi's columns hold the second scores of the next chunk: these wait for the rows' readers
+            const bool late = inner && !Lay::A2_OWN;
+            bool ok = totals || nch == 0 || scores(0);
+            for (int c = 0; ok && c < nch; ++c) {
+                const int s = c % NST;
+                const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
+                // the state before the chunk is in place, dS has been read
+                if (!(ok = wait1(s_ready, c & 1))) break;
+                if (!totals) {
+                    if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
+                    if (late && !(ok = wait1(sc_free, c & 1))) break;
+                    tc_fence_after();
+                    const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024);
+#pragma unroll
+                    for (int p = 0; p < NS; ++p)
+#pragma unroll
+                        for (int k = 0; k < DX / 16; ++k)
+                            mma_ts(tmem + Lay::T_OI, tmem + Lay::T_SC + p * (DX / 2) + k * 8,
+                                   desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32), ID_INTER, p + k > 0);
+                }
+                if (!(ok = wait1(yt_ready, c & 1))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        mma_ss(tmem + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0);
+                }
+                mma_commit(state_done);
+                if (totals) {
+                    mma_commit(&stage_free[s]);
+                    continue;
+                }
+                if (!late) {
+                    if (!(ok = wait1(sc_free, c & 1))) break;
+                    if (c + 1 < nch && !(ok = scores(c + 1))) break;
+                }
+                if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
+                tc_fence_after();
+                const uint64_t dp = smem_desc(smem_u32(p_tile + (c & 1) * Lay::P), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    mma_ss(tmem + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0);
+                mma_commit(o_done);
+                mma_commit(&stage_free[s]);
+                if (late && c + 1 < nch) {
+                    if (!(ok = wait1(o_free, c & 1))) break;
+                    if (!(ok = scores(c + 1))) break;
+                }
+            }
+            // every product issued above has completed before TMEM is released
+            mma_commit(drain);
+            const uint64_t begin = globaltimer();
+            while (!mbar_try_sleep(drain, 0, 200000u))
+                if (globaltimer() - begin > ctl.timeout_ns) break;
+        }
+    } else if (warp >= PY0 && warp < ST0) {
+        // ------------------------------------------------------------ Y~ and P
+        const int pw = warp - PY0, ft = 32 * pw + lane, q4 = warp & 3, half = pw >> 2;
+        constexpr int G = DX / 8, RG = 256 / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG, ..
+        const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
+        const int ta = 16 * q4 + (lane >> 2), tb = ta + 8, cpos = lane & 3;
+        for (int c = 0; c < nch; ++c) {
+            const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
+            const Weights &w = weights[c % GT_SLOTS];
+            if (!wait(&full[s], (c / NST) & 1)) break;
+            if (c > 0 && !wait(state_done, (c - 1) & 1)) break;  // Y~ of the chunk before has been read
+            const uint8_t *src = tile_y(s) + off;
+            uint4 v[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) v[n] = *(const uint4 *)(src + n * RG * 128);
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const int r = rg + n * RG;
+                const float kw = w.kw[r];
+                uint32_t u[4] = {v[n].x, v[n].y, v[n].z, v[n].w}, hi[4], mid[4], lo[4];
+                // rows behind the end count as zeros, whatever they hold
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    split3(r < nv ? bf_lo(u[i]) * kw : 0.f, r < nv ? bf_hi(u[i]) * kw : 0.f, hi[i], mid[i], lo[i]);
+                uint8_t *d = yt + off + n * RG * 128;
+                *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                *(uint4 *)(d + 2 * Lay::X) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (nv < C)
+                for (int e = ft; e < (C - nv) * (DZ / 8); e += 256) {
+                    const int r = nv + e / (DZ / 8), p = e % (DZ / 8);
+                    *(uint4 *)(tile_z(s) + (p >> 3) * C * 128 + r * 128 + ((p & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+            fence_async_smem();
+            arrive(yt_ready);
+            if (totals) continue;
+            if (!wait(scores_done, c & 1)) break;
+            tc_fence_after();
+            uint32_t r1[32], r2[32];  // the first 16
+            tmem_ld16x256_x4(tmem + Lay::T_A + ((uint32_t)(32 * q4) << 16) + 32 * half, r1);
+            if (inner) tmem_ld16x256_x4(tmem + Lay::T_A2 + ((uint32_t)(32 * q4) << 16) + 32 * half, r2);
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive(sc_free);
+            const float4 ga = w.row[ta], gb = w.row[tb];
+            float sa = 0.f, sb = 0.f, sc[8];
+            uint8_t *const pt = p_tile + (c & 1) * Lay::P;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float p[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int col = 32 * half + 8 * k + 2 * cpos + (u & 1), row = u < 2 ? ta : tb;
+                    const float4 gc = w.row[col], gr = u < 2 ? ga : gb;
+                    const bool in = (rev ? col >= row : col <= row) && row < nv && col < nv &&
+                                    __float_as_int(gc.z) == __float_as_int(gr.z);
+                    const float dlt = (gr.x - gc.x) + (gr.y - gc.y);
+                    const float wt = ex2(rev ? -dlt : dlt), sco = __uint_as_float(r1[4 * k + u]);
+                    p[u] = in ? a.yscale * (sco * wt) : 0.f;
+                    if (inner) {
+                        const float x = in && col != row ? a.oscale * (sco * wt) * __uint_as_float(r2[4 * k + u]) : 0.f;
+                        if (u < 2) sa += x;
+                        else sb += x;
+                        if (u < 2) sc[2 * k + u] = x;
+                        else sc[2 * k + u - 2] += x;
+                    }
+                }
+                const int ch = 4 * half + k;
+                *(uint32_t *)(pt + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = pack_bf16x2(p[0], p[1]);
+                *(uint32_t *)(pt + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = pack_bf16x2(p[2], p[3]);
+            }
+            fence_async_smem();
+            arrive(p_ready + (c & 1));
+            if (inner) {
+                sa += __shfl_xor_sync(0xffffffffu, sa, 1);
+                sb += __shfl_xor_sync(0xffffffffu, sb, 1);
+                sa += __shfl_xor_sync(0xffffffffu, sa, 2);
+                sb += __shfl_xor_sync(0xffffffffu, sb, 2);
+                float *const rp = a.dot + ((long long)(4 + half) * BH + bh) * a.L + row0;
+                if (cpos == 0) {
+                    if (ta < nv) rp[ta] = sa;
+                    if (tb < nv) rp[tb] = sb;
+                }
+                int at = 0;
+#pragma unroll
+                for (int o = 4, n = 4; o < 32; o <<= 1, n >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n) {
+                            const float send = up ? sc[i] : sc[i + n], keep = up ? sc[i + n] : sc[i];
+                            sc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                    at += up ? n : 0;
+                }
+                const int col = 32 * half + 8 * (at >> 1) + 2 * cpos + (at & 1);
+                if (col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
+            }
+        }
+    } else if (warp >= ST0) {
+        // ------------------------------------------------------------ the state, and the rows
+        const int q4 = warp & 3, half = (warp - ST0) >> 2;
+        const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+        const int j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
+        const bool live = DZ == 128 || lane < 16;
+        constexpr int NX = DX / 2;  // x channels half * NX ..
+        const long long n_state = (long long)DX * DZ;
+        const long long at = (a.by_seg ? (long long)seg * BH + bh : (long long)slot * a.H + h) * n_state;
+        float S[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) S[i] = 0.f;
+        auto place = [&](int i) { return (long long)(half * NX + i) * a.rs + (long long)j * a.cs; };
+        if (a.init && !totals && live && (a.by_seg || slot >= 0)) {
+            const float *p = a.init + at;
+            if (a.rs == 1) {
+#pragma unroll
+                for (int i = 0; i < NX; i += 4) {
+                    const float4 v = *(const float4 *)(p + place(i));
+                    S[i] = v.x; S[i + 1] = v.y; S[i + 2] = v.z; S[i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NX; ++i) S[i] = p[place(i)];
+            }
+        }
+        auto store = [&](float *p) {
+            if (!live) return;
+            if (a.rs == 1) {
+#pragma unroll
+                for (int i = 0; i < NX; i += 4) *(float4 *)(p + place(i)) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NX; ++i) p[place(i)] = S[i];
+            }
+        };
+        auto anchor = [&](int k) { store(a.anchors + ((long long)k * BH + bh) * n_state); };
+        auto copy = [&]() {
+            if (!totals) {
+#pragma unroll
+                for (int i = 0; i < NX; i += 16) {
+                    uint32_t part[3][8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        if (NS == 1) part[0][u] = pack_bf16x2(S[i + 2 * u], S[i + 2 * u + 1]);
+                        else split3(S[i + 2 * u], S[i + 2 * u + 1], part[0][u], part[1][u], part[2][u]);
+                    }
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) tmem_st8(tmem + lanes + Lay::T_SC + p * (DX / 2) + (half * NX + i) / 2, part[p]);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            arrive(s_ready);
+        };
+        const int first_anchor = a.anchors ? t0 / (a.anchor_chunks * C) : 0;
+        const int anchors_here = a.anchors ? (t1 - t0 + a.anchor_chunks * C - 1) / (a.anchor_chunks * C) : 0;
+        if (a.anchors && rev)  // those that end behind the sequence
+            for (int k = (nch + a.anchor_chunks - 1) / a.anchor_chunks; k < anchors_here; ++k) anchor(first_anchor + k);
+        copy();
+        bool ok = true;
+        for (int c = 0; c < nch; ++c) {
+            const int s = c % NST, cc = chunk_of(c), row0 = t0 + cc * C, nv = min(C, te - row0);
+            const Weights &w = weights[c % GT_SLOTS];
+            if (a.anchors) {
+                if (rev && (c == 0 || (cc + 1) % a.anchor_chunks == 0)) anchor(first_anchor + cc / a.anchor_chunks);
+                if (!rev && cc % a.anchor_chunks == 0) anchor(first_anchor + cc / a.anchor_chunks);
+            }
+            if (!(ok = wait(state_done, c & 1))) break;
+            tc_fence_after();
+            const float da = w.a, em = w.em;
+            // next to 1 by the decay minus 1, whose rounding does not grow with the chunks
+            const bool near = da > 0.5f, none = da == 0.f;
+            const float m = near ? em : da;
+#pragma unroll
+            for (int i = 0; i < NX; i += 16) {
+                uint32_t d[16];
+                tmem_ld16(tmem + lanes + Lay::T_DS + half * NX + i, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) {
+                    const float ds = __uint_as_float(d[u]);
+                    S[i + u] = none ? ds : fmaf(S[i + u], m, near ? S[i + u] + ds : ds);
+                }
+            }
+            copy();
+            if (totals) continue;
+            if (!(ok = wait(o_done, c & 1))) break;
+            tc_fence_after();
+            constexpr int RB = DOT ? 8 : 16;  // rows at a time, by what the registers hold
+#pragma unroll
+            for (int k = 0; k < 32 / RB; ++k) {
+                const int i0 = 32 * half + RB * k;
+                uint32_t oi[RB], oa[RB];
+                if constexpr (DOT) {
+                    tmem_ld8(tmem + lanes + Lay::T_OI + i0, oi);
+                    tmem_ld8(tmem + lanes + Lay::T_OA + i0, oa);
+                } else {
+                    tmem_ld16(tmem + lanes + Lay::T_OI + i0, oi);
+                    tmem_ld16(tmem + lanes + Lay::T_OA + i0, oa);
+                }
+                tmem_wait_ld();
+                if (k == 32 / RB - 1) {
+                    tc_fence_before();
+                    arrive(o_free);
+                }
+                float dot[RB];
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    const float x = w.rw[i0 + i] * __uint_as_float(oi[i]);
+                    const float o = fmaf(a.oscale, __uint_as_float(oa[i]), x);
+                    if (DOT) {
+                        const uint32_t q = pair_at(tile_w(s), i0 + i, j & ~1);
+                        dot[i] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
+                    }
+                    if (live && i0 + i < nv) {
+                        const long long at_o = row_of(a.vo, b, h, row0 + i0 + i) + j;
+                        if (a.out_f32) ((float *)a.out)[at_o] = o;
+                        else ((__nv_bfloat16 *)a.out)[at_o] = __float2bfloat16_rn(o);
+                    }
+                }
+                if (DOT) {
+                    // over the quadrant's channels; a lane goes on with half of the rows each time
+                    int r = 0;
+#pragma unroll
+                    for (int o = 16, n = RB / 2; n > 0; o >>= 1, n >>= 1) {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int i = 0; i < RB / 2; ++i)
+                            if (i < n) {
+                                const float send = up ? dot[i] : dot[i + n], keep = up ? dot[i + n] : dot[i];
+                                dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                            }
+                        r += up ? n : 0;
+                    }
+                    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
+                    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
+                    if (!(lane & 3) && i0 + r < nv) a.dot[((long long)q4 * BH + bh) * a.L + row0 + i0 + r] = dot[0];
+                }
+            }
+            if (DOT) arrive(&stage_free[s]);
+        }
+        if (ok) {
+            if (a.anchors && !rev) {
+                for (int k = (nch + a.anchor_chunks - 1) / a.anchor_chunks; k < anchors_here; ++k) anchor(first_anchor + k);
+                if (seg == a.nseg - 1) anchor(a.n_anchors);
+            }
+            if (a.fin && (a.by_seg || slot >= 0)) store(a.fin + at);
+            // rows behind the sequence's end
+            if (!totals && a.out)
+                for (int t = te + (warp - ST0); t < t1; t += 8)
+                    for (int i = lane; i < DZ; i += 32) {
+                        const long long o = row_of(a.vo, b, h, t) + i;
+                        if (a.out_f32) ((float *)a.out)[o] = 0.f;
+                        else ((__nv_bfloat16 *)a.out)[o] = __float2bfloat16_rn(0.f);
+                    }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+// [B, n, L, d] bf16 by strides; boxes of 64 channels x 64 rows of one head, 128-byte swizzle, rows past L
+// zero.
+bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, int d)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)L, (cuuint64_t)n, (cuuint64_t)B};
+    auto stride = [&](long long s, int len) { return (cuuint64_t)(len > 1 ? s * 2 : d * 2); };
+    cuuint64_t strides[3] = {stride(v.l, L), stride(v.h, n), stride(v.b, B)};
+    cuuint32_t box[4] = {64, GT_C, 1, 1}, es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DX, int DZ, bool DOT> int launch_dims(const GtArgs &a, cudaStream_t stream)
+{
+    using Lay = GtLayout<DX, DZ, DOT>;
+    static std::atomic<uint64_t> done{0};  // devices whose limit is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
+    if (dev >= 64 || !(done.load() >> dev & 1)) {
+        const int rc = status_of(cudaFuncSetAttribute(gated_tc_kernel<DX, DZ, DOT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC));
+        if (rc != LA_OK) return rc;
+        if (dev < 64) done |= 1ull << dev;
+    }
+    return launch(gated_tc_kernel<DX, DZ, DOT>, dim3((unsigned)(a.B * a.H * a.nseg)), GT_THREADS, (size_t)Lay::ALLOC, stream, a);
+}
+template <bool DOT> int launch_dot(const GtArgs &a, int dx, int dz, cudaStream_t s)
+{
+    if (dx == 64) return dz == 64 ? launch_dims<64, 64, DOT>(a, s) : launch_dims<64, 128, DOT>(a, s);
+    return dz == 64 ? launch_dims<128, 64, DOT>(a, s) : launch_dims<128, 128, DOT>(a, s);
+}
+
+struct Operand {
+    const void *p = nullptr;
+    View v = {};
+    int n = 0, d = 0;  // heads, channels
+};
+
+struct Pass {
+    Operand x, y, z, w;  // x.p NULL: totals; w.p NULL: no DOT
+    GtArgs a = {};
+};
+
+int launch_pass(const GatedArgs &p, Pass &s)
+{
+    GtArgs &a = s.a;
+    a.B = p.B; a.H = p.H; a.L = p.L;
+    a.g = p.g; a.vg = p.vg;
+    a.lengths = p.lengths;
+    a.err = p.err;
+    a.e = s.z.d;
+    a.totals = s.x.p == nullptr;
+    a.timeout_ns = 2000000000ull;
+    if (const char *e = getenv("LA_DEBUG_TIMEOUT_NS"); e && *e) a.timeout_ns = strtoull(e, nullptr, 10);
+    a.sx = a.sw = 1;
+    a.sy = p.H / s.y.n;
+    a.sz = p.H / s.z.n;
+    if (!map4(&a.my, s.y.p, s.y.v, p.B, s.y.n, p.L, s.y.d) || !map4(&a.mz, s.z.p, s.z.v, p.B, s.z.n, p.L, s.z.d)) return LA_ERR_CUDA;
+    if (s.x.p) {
+        a.sx = p.H / s.x.n;
+        if (!map4(&a.mx, s.x.p, s.x.v, p.B, s.x.n, p.L, s.x.d)) return LA_ERR_CUDA;
+    }
+    if (!s.w.p) return launch_dot<false>(a, s.y.d, s.z.d, p.stream);
+    a.sw = p.H / s.w.n;
+    if (!map4(&a.mw, s.w.p, s.w.v, p.B, s.w.n, p.L, s.w.d)) return LA_ERR_CUDA;
+    return launch_dot<true>(a, s.y.d, s.z.d, p.stream);
+}
+
+bool tc_dim(int d) { return d == 64 || d == 128; }
+bool tc_view(const void *p, const View &v, int B, int n, int L)
+{
+    auto ok = [&](long long s, int len) { return len == 1 || (s > 0 && s < (1ll << 38)); };
+    return rows_aligned(p, v, B, n, L, 2, 16) && ok(v.b, B) && ok(v.h, n) && ok(v.l, L);
+}
+
+// Segments of a head's rows, one block each: where the heads alone leave half of the SMs idle, as many as fill
+// them, of 256 rows at least. The segments' sums are a pass over y and z, half of the sweep's bytes,
+// which a split into two would not win back.
+int tc_segments(int BH, int L, int sms)
+{
+    const int want = std::min(sms / BH, (L + 255) / 256);
+    return want < 2 ? 1 : want;
+}
+int chunk_rows(int L, int nseg) { return ((L + nseg - 1) / nseg + GT_C - 1) / GT_C * GT_C; }
+
+struct TcBwdSpace {
+    size_t T, A, U, S, D, y, r, c, dk, dv, dg, all;
+    int rows, nseg, anchor, n_anchors;
+    TcBwdSpace(int B, int H, int Hk, int L, int d, int e, int sms)
+    {
+        const size_t heads = (size_t)B * H, n = (size_t)d * e;
+        const int want = tc_segments(B * H, L, sms);
+        rows = chunk_rows(L, want);
+        // segments of more than one anchor are whole anchors
+        if (want > 1 && rows > GATED_ANCHOR) rows = (rows + GATED_ANCHOR - 1) / GATED_ANCHOR * GATED_ANCHOR;
+        nseg = (L + rows - 1) / rows;
+        anchor = nseg > 1 && rows < GATED_ANCHOR ? rows : GATED_ANCHOR;
+        n_anchors = (L + anchor - 1) / anchor;
+        size_t at = 0;
+        auto take = [&](size_t k) { const size_t o = at; at += (k + 3) & ~(size_t)3; return o; };
+        T = take(nseg > 1 ? nseg * heads * n : 0);
+        U = take(nseg > 1 ? nseg * heads * n : 0);
+        A = take(nseg > 1 ? nseg * heads : 0);
+        S = take((n_anchors + 1) * heads * n);
+        D = take(n_anchors * heads * n);
+        y = take(n_anchors * heads);
+        r = take(6 * heads * L);
+        c = take(8 * heads * L);
+        dk = take(H > Hk ? heads * L * d : 0);
+        dv = take(H > Hk ? heads * L * e : 0);
+        dg = take(heads * L);
+        all = at;
+    }
+};
+
+}  // namespace
+
+bool gated_tc_fwd_ok(const GatedArgs &p)
+{
+    return p.dtype == LA_BF16 && tc_dim(p.d) && tc_dim(p.e) && tc_view(p.q, p.vq, p.B, p.H, p.L) &&
+           tc_view(p.k, p.vk, p.B, p.Hk, p.L) && tc_view(p.v, p.vv, p.B, p.Hk, p.L);
+}
+bool gated_tc_bwd_ok(const GatedArgs &p) { return gated_tc_fwd_ok(p) && tc_view(p.dout, p.vo, p.B, p.H, p.L) && aligned(p.state0, 16) && aligned(p.dstate, 16) && aligned(p.dstate0, 16); }
+
+size_t gated_tc_fwd_ws(int B, int H, int L, int d, int e, int sms)
+{
+    if (!tc_dim(d) || !tc_dim(e)) return 0;
+    const int rows = chunk_rows(L, tc_segments(B * H, L, sms)), nseg = (L + rows - 1) / rows;
+    return nseg == 1 ? 0 : sizeof(float) * (size_t)nseg * B * H * ((size_t)d * e + 1);
+}
+size_t gated_tc_bwd_ws(int B, int H, int Hk, int L, int d, int e, int sms)
+{
+    return tc_dim(d) && tc_dim(e) ? sizeof(float) * TcBwdSpace(B, H, Hk, L, d, e, sms).all : 0;
+}
+
+int gated_tc_fwd(const GatedArgs &p)
+{
+    const int rows = chunk_rows(p.L, tc_segments(p.B * p.H, p.L, p.sms)), nseg = (p.L + rows - 1) / rows, n = p.d * p.e;
+    Pass s;
+    s.y = {p.k, p.vk, p.Hk, p.d};
+    s.z = {p.v, p.vv, p.Hk, p.e};
+    s.a.seg_rows = rows; s.a.nseg = nseg;
+    s.a.rs = p.e; s.a.cs = 1;
+    s.a.yscale = 1.f; s.a.oscale = p.scale;
+    int rc;
+    if (nseg > 1) {
+        float *T = p.ws, *A = T + (size_t)nseg * p.B * p.H * n;
+        Pass t = s;
+        t.a.by_seg = 1;
+        t.a.fin = T;
+        t.a.decay = A;
+        if ((rc = launch_pass(p, t)) != LA_OK) return rc;
+        if ((rc = gated_scan(p, T, A, nseg, n, p.state0, p.slots, p.state, nullptr, false)) != LA_OK) return rc;
+        s.a.by_seg = 1;
+        s.a.init = T;
+    } else {
+        s.a.slots = p.slots; s.a.n_slots = p.n_slots;
+        s.a.init = p.state0;
+        s.a.fin = p.state;
+    }
+    s.x = {p.q, p.vq, p.H, p.d};
+    s.a.out = p.out; s.a.vo = p.vo;
+    return launch_pass(p, s);
+}
+
+int gated_tc_bwd(const GatedArgs &p)
+{
+    const TcBwdSpace w(p.B, p.H, p.Hk, p.L, p.d, p.e, p.sms);
+    const int n = p.d * p.e, group = p.H / p.Hk;
+    const size_t heads = (size_t)p.B * p.H;
+    float *const ws = p.ws;
+    const bool dg = p.dg || p.dg_head;
+    const Operand q{p.q, p.vq, p.H, p.d}, k{p.k, p.vk, p.Hk, p.d}, v{p.v, p.vv, p.Hk, p.e}, g{p.dout, p.vo, p.H, p.e};
+    int rc;
+    Pass base;
+    base.a.seg_rows = w.rows; base.a.nseg = w.nseg;
+    base.a.by_seg = w.nseg > 1;
+    base.a.yscale = base.a.oscale = 1.f;
+    base.a.anchor_chunks = w.anchor / GT_C; base.a.n_anchors = w.n_anchors;
+    if (w.nseg > 1) {
+        Pass s = base;  // states at the segments' starts
+        s.y = k; s.z = v;
+        s.a.rs = p.e; s.a.cs = 1;
+        s.a.fin = ws + w.T; s.a.decay = ws + w.A;
+        if ((rc = launch_pass(p, s)) != LA_OK) return rc;
+        if ((rc = gated_scan(p, ws + w.T, ws + w.A, w.nseg, n, p.state0, nullptr, nullptr, nullptr, false)) != LA_OK) return rc;
+        s = base;  // the states' gradients at their ends
+        s.y = q; s.z = g;
+        s.a.reverse = 1;
+        s.a.rs = p.e; s.a.cs = 1;
+        s.a.yscale = p.scale;
+        s.a.fin = ws + w.U;
+        if ((rc = launch_pass(p, s)) != LA_OK) return rc;
+        if ((rc = gated_scan(p, ws + w.U, ws + w.A, w.nseg, n, p.dstate, nullptr, p.dstate0, nullptr, true)) != LA_OK) return rc;
+    }
+    Pass s = base;  // dq = S dout
+    s.x = g; s.y = v; s.z = k;
+    s.a.rs = 1; s.a.cs = p.e;
+    s.a.init = w.nseg > 1 ? ws + w.T : p.state0;
+    s.a.oscale = p.scale;
+    s.a.out = p.dq; s.a.vo = p.vdq;
+    if (dg) {
+        s.w = q;
+        s.a.inner = 1;
+        s.a.dot = ws + w.r; s.a.dotc = ws + w.c + 4 * heads * p.L;
+        s.a.anchors = ws + w.S;
+    }
+    if ((rc = launch_pass(p, s)) != LA_OK) return rc;
+    auto per_head = [&](int c) { return View{(long long)p.H * p.L * c, (long long)p.L * c, c}; };
+    s = base;  // dk = D v
+    s.x = v; s.y = g; s.z = q;
+    s.a.reverse = 1;
+    s.a.rs = 1; s.a.cs = p.e;
+    s.a.init = w.nseg > 1 ? ws + w.U : p.dstate;
+    s.a.yscale = p.scale;
+    s.a.out = p.dk; s.a.vo = p.vdk;
+    if (group > 1) {
+        s.a.out = ws + w.dk; s.a.vo = per_head(p.d); s.a.out_f32 = 1;
+    }
+    if (dg) {
+        s.w = k;
+        s.a.dot = ws + w.c;
+        s.a.anchors = ws + w.D;
+    }
+    if ((rc = launch_pass(p, s)) != LA_OK) return rc;
+    s = base;  // dv = D^T k
+    s.x = k; s.y = q; s.z = g;
+    s.a.reverse = 1;
+    s.a.rs = p.e; s.a.cs = 1;
+    s.a.init = w.nseg > 1 ? ws + w.U : p.dstate;
+    if (w.nseg == 1) s.a.fin = p.dstate0;  // the last reader of dstate
+    s.a.yscale = p.scale;
+    s.a.out = p.dv; s.a.vo = p.vdv;
+    if (group > 1) {
+        s.a.out = ws + w.dv; s.a.vo = per_head(p.e); s.a.out_f32 = 1;
+    }
+    if ((rc = launch_pass(p, s)) != LA_OK) return rc;
+    if (group > 1) {
+        if ((rc = gated_share(p, ws + w.dk, p.dk, p.vdk, p.d)) != LA_OK) return rc;
+        if ((rc = gated_share(p, ws + w.dv, p.dv, p.vdv, p.e)) != LA_OK) return rc;
+    }
+    if (dg) {
+        if ((rc = gated_products(p, ws + w.D, ws + w.S + heads * n, ws + w.y, w.n_anchors, n)) != LA_OK) return rc;
+        if ((rc = gated_log_decay(p, ws + w.r, 6, ws + w.c, 8, ws + w.y, w.anchor, w.n_anchors, p.dg ? p.dg : ws + w.dg)) != LA_OK)
+            return rc;
+    }
+    return LA_OK;
+}
+
+}  // namespace la

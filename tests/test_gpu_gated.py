@@ -43,6 +43,43 @@ def test_forward(size, kind, dtype):
         assert la.la_last_device_status(None) == la.LA_OK
 
 
+TC_SIZES = [(1, 2, 2, 1, 64, 64), (2, 4, 2, 65, 64, 128), (2, 2, 1, 127, 128, 64), (1, 2, 2, 700, 128, 128),
+            (10, 16, 16, 70, 64, 64), (1, 1, 1, 3000, 64, 128)]
+
+
+@pytest.mark.parametrize("size", TC_SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_paths(size):
+    """Both paths named: few heads (cut into segments) and many, each pair of widths."""
+    B, H, Hk, L, d, e = size
+    q, k, v, g, s0, n, do, ds = ref.draw(*size, BF16, "token", True, True, seed=20)
+    want, wstate = ref.forward(q, k, v, g, 0.1, s0, n)
+    small = L * d * e * B * H <= 40e6
+    m = ref.magnitudes(q, k, v, g, 0.1, s0, n, *((do, ds) if small else ()))
+    grads = ref.backward(q, k, v, g, do, 0.1, s0, n, ds) if small else None
+    for path in (la.LA_PATH_TC, la.LA_PATH_SIMT):
+        out, state = la.gated_fwd(gpu(q), gpu(k), gpu(v), gpu(g), scale=0.1, state0=gpu(s0), lengths=gpu(n), path=path)
+        close("out", out, want, m["out"], BF16, steps_of(L, d, e))
+        close("state", state, wstate, m["state"], F32, steps_of(L, d, e))
+        if small:
+            check_grads(grads_of(q, k, v, g, do, 0.1, s0, n, ds, path=path), grads, m, BF16, g, steps_of(L, d, e))
+        assert la.la_last_device_status(None) == la.LA_OK
+
+
+def test_the_tensor_cores_refuse():
+    """LA_PATH_TC is refused where it does not apply: type, widths, alignment, broadcast."""
+    q, k, v, g, _, _, do, _ = ref.draw(1, 2, 2, 40, 64, 64, BF16)
+    q, k, v, g, do = (gpu(x) for x in (q, k, v, g, do))
+    odd = torch.zeros(1, 2, 40, 65, dtype=BF16, device="cuda")[..., 1:]
+    one = k[:, :1].expand(1, 2, 40, 64)
+    for a in ((q.float(), k.float(), v.float()), (q[..., :40], k[..., :40], v), (odd, k, v), (q, one, v)):
+        with pytest.raises(la.LAError) as e:
+            la.gated_fwd(*a, g, path=la.LA_PATH_TC)
+        assert e.value.status == la.LA_ERR_UNSUPPORTED
+        with pytest.raises(la.LAError) as e:
+            la.gated_bwd(*a, g, do.to(a[0].dtype), path=la.LA_PATH_TC)
+        assert e.value.status == la.LA_ERR_UNSUPPORTED
+
+
 def grads_of(q, k, v, g, do, scale, s0, n, ds, **kw):
     names = ("dq", "dk", "dv", "dg", "dstate0")
     return dict(zip(names, la.gated_bwd(gpu(q), gpu(k), gpu(v), gpu(g), gpu(do), scale=scale, state0=gpu(s0),
@@ -81,8 +118,14 @@ def test_without_the_decays_gradient(dtype):
     q, k, v, g, s0, n, do, ds = ref.draw(2, 4, 2, 150, 64, 64, dtype, "token", True, True, seed=3)
     a, b = grads_of(q, k, v, g, do, 0.2, s0, n, ds), grads_of(q, k, v, g, do, 0.2, s0, n, ds, decay_grad=False)
     assert b["dg"] is None
-    for name in ("dq", "dk", "dv", "dstate0"):
-        assert torch.equal(a[name], b[name])
+    if dtype == F32:
+        for name in ("dq", "dk", "dv", "dstate0"):
+            assert torch.equal(a[name], b[name])
+        return
+    # the tensor cores read one bf16 part of the state where no decay's gradient needs three
+    want = ref.backward(q, k, v, g, do, 0.2, s0, n, ds)
+    m = ref.magnitudes(q, k, v, g, 0.2, s0, n, do, ds)
+    check_grads(b | dict(dg=a["dg"]), want, m, dtype, g, steps_of(150, 64, 64))
 
 
 def step_inputs(q, k, v, g, t):
