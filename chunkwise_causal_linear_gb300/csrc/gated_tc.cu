@@ -78,8 +78,10 @@ struct GtArgs {
     unsigned long long timeout_ns;
 };
 
+constexpr float GT_CUT = 16384.f;  // doublings that a decay of 0 counts for in G: no pair reaches across
+
 struct Weights {          // of one chunk
-    float4 row[GT_C];     // G in units of a doubling, hi and lo; the run of rows between decays of 0
+    float2 row[GT_C];     // G (-G in reverse) in doublings, hi and lo
     float kw[GT_C];       // of Y's rows (f, or e in reverse), times yscale
     float rw[GT_C];       // of the inter rows (e, or f in reverse), times oscale
     float a, em, pad[2];  // decay over the chunk, and that minus 1
@@ -108,14 +110,25 @@ __device__ __forceinline__ uint32_t pair_at(const uint8_t *tile, int row, int c)
     return *(const uint32_t *)(tile + (c >> 6) * (GT_C * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2);
 }
 
-// x in three bf16 parts, two at a time: hi + mid + lo = x to 2^-24.
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+// Two values in three bf16 parts each: hi + mid + lo = x to 2^-24.
+__device__ __forceinline__ Ch<2> less(const Ch<2> &x, uint32_t part)
 {
-    hi = pack_bf16x2(x0, x1);
-    x0 -= bf_lo(hi);
-    x1 -= bf_hi(hi);
-    mid = pack_bf16x2(x0, x1);
-    lo = pack_bf16x2(x0 - bf_lo(mid), x1 - bf_hi(mid));
+    return add(x, Ch<2>{{-bf_lo(part), -bf_hi(part)}});
+}
+__device__ __forceinline__ void split3(Ch<2> x, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    hi = pack_bf16x2(x.v[0], x.v[1]);
+    x = less(x, hi);
+    mid = pack_bf16x2(x.v[0], x.v[1]);
+    x = less(x, mid);
+    lo = pack_bf16x2(x.v[0], x.v[1]);
+}
+
+// wait_phase with the clock read only once a wait was long: the timer is far from the SM.
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, const Ctl &ctl)
+{
+    if (mbar_try(bar, parity) || mbar_try_sleep(bar, parity, 200000u)) return true;
+    return wait_phase(bar, parity, ctl);
 }
 
 template <int DX, int DZ, bool DOT>
@@ -172,7 +185,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_phase(bar, parity, ctl)) != 0; };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_long(bar, parity, ctl)) != 0; };
     auto arrive = [&](uint64_t *bar) {  // of a warp whose lanes have all done their part
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -224,9 +237,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             for (int i = 0; i < 2; ++i) {
                 const double G = i ? G1 : G0;
                 const int run_id = i ? r1 : r0;
-                const double G2 = G * LOG2E;
+                // hi and lo together hold differences of rows to 2^-24 of what lies between two cuts
+                double G2 = G * LOG2E - (double)GT_CUT * run_id;
+                if (rev) G2 = -G2;
                 const float hi = (float)G2, lo = (float)(G2 - (double)hi);
-                w.row[2 * lane + i] = make_float4(hi, lo, __int_as_float(run_id), 0.f);
+                w.row[2 * lane + i] = make_float2(hi, lo);
                 const float start = run_id == 0 ? expf((float)G) : 0.f, end = run_id == cuts ? expf((float)(all - G)) : 0.f;
                 w.kw[2 * lane + i] = a.yscale * (rev ? start : end);
                 w.rw[2 * lane + i] = a.oscale * (rev ? end : start);
@@ -258,7 +273,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         if (lane == 0) {
             constexpr uint32_t ID_SC = idesc_bf16_f32(C, C, 0, 0), ID_INTER = idesc_bf16_f32(DZ, C, 0, 0),
                                ID_STATE = idesc_bf16_f32(DZ, DX, 1, 1), ID_INTRA = idesc_bf16_f32(DZ, C, 1, 0);
-            auto wait1 = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, ctl); };
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) { return wait_long(bar, parity, ctl); };
             auto scores = [&](int c) {
                 const int s = c % NST;
                 if (!wait1(&full[s], (c / NST) & 1)) return false;
@@ -355,12 +370,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const int r = rg + n * RG;
-                const float kw = w.kw[r];
+                const Ch<2> kw = all<2>(w.kw[r]);
                 uint32_t u[4] = {v[n].x, v[n].y, v[n].z, v[n].w}, hi[4], mid[4], lo[4];
-                // rows behind the end count as zeros, whatever they hold
+                if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    split3(r < nv ? bf_lo(u[i]) * kw : 0.f, r < nv ? bf_hi(u[i]) * kw : 0.f, hi[i], mid[i], lo[i]);
+                for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
                 uint8_t *d = yt + off + n * RG * 128;
                 *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
@@ -382,27 +396,30 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             tmem_wait_ld();
             tc_fence_before();
             arrive(sc_free);
-            const float4 ga = w.row[ta], gb = w.row[tb];
+            const float2 ga = w.row[ta], gb = w.row[tb];
+            // columns of a row that count, from the row itself towards the sweep's start
+            const uint32_t na = ta < nv ? (rev ? nv - ta : ta + 1) : 0, nb = tb < nv ? (rev ? nv - tb : tb + 1) : 0;
             float sa = 0.f, sb = 0.f, sc[8];
             uint8_t *const pt = p_tile + (c & 1) * Lay::P;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                const int col = 32 * half + 8 * k + 2 * cpos;
+                const float4 gc = *(const float4 *)&w.row[col];  // of col and col + 1
                 float p[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int col = 32 * half + 8 * k + 2 * cpos + (u & 1), row = u < 2 ? ta : tb;
-                    const float4 gc = w.row[col], gr = u < 2 ? ga : gb;
-                    const bool in = (rev ? col >= row : col <= row) && row < nv && col < nv &&
-                                    __float_as_int(gc.z) == __float_as_int(gr.z);
-                    const float dlt = (gr.x - gc.x) + (gr.y - gc.y);
-                    const float wt = ex2(rev ? -dlt : dlt), sco = __uint_as_float(r1[4 * k + u]);
-                    p[u] = in ? a.yscale * (sco * wt) : 0.f;
+                    const int cu = col + (u & 1), row = u < 2 ? ta : tb;
+                    const float2 gr = u < 2 ? ga : gb;
+                    const bool in = (uint32_t)(rev ? cu - row : row - cu) < (u < 2 ? na : nb);
+                    const float wt = ex2((gr.x - (u & 1 ? gc.z : gc.x)) + (gr.y - (u & 1 ? gc.w : gc.y)));
+                    const float x = __uint_as_float(r1[4 * k + u]) * wt;
+                    p[u] = in ? a.yscale * x : 0.f;
                     if (inner) {
-                        const float x = in && col != row ? a.oscale * (sco * wt) * __uint_as_float(r2[4 * k + u]) : 0.f;
-                        if (u < 2) sa += x;
-                        else sb += x;
-                        if (u < 2) sc[2 * k + u] = x;
-                        else sc[2 * k + u - 2] += x;
+                        const float y = in && cu != row ? a.oscale * x * __uint_as_float(r2[4 * k + u]) : 0.f;
+                        if (u < 2) sa += y;
+                        else sb += y;
+                        if (u < 2) sc[2 * k + u] = y;
+                        else sc[2 * k + u - 2] += y;
                     }
                 }
                 const int ch = 4 * half + k;
@@ -444,11 +461,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         const int j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
         const bool live = DZ == 128 || lane < 16;
         constexpr int NX = DX / 2;  // x channels half * NX ..
-        const long long n_state = (long long)DX * DZ;
+        const long long n_state = (long long)DX * DZ, out0 = row_of(a.vo, b, h, 0) + j;
         const long long at = (a.by_seg ? (long long)seg * BH + bh : (long long)slot * a.H + h) * n_state;
-        float S[NX];
+        Ch<2> S[NX / 2];
 #pragma unroll
-        for (int i = 0; i < NX; ++i) S[i] = 0.f;
+        for (int i = 0; i < NX / 2; ++i) S[i] = all<2>(0.f);
         auto place = [&](int i) { return (long long)(half * NX + i) * a.rs + (long long)j * a.cs; };
         if (a.init && !totals && live && (a.by_seg || slot >= 0)) {
             const float *p = a.init + at;
@@ -456,21 +473,22 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
 #pragma unroll
                 for (int i = 0; i < NX; i += 4) {
                     const float4 v = *(const float4 *)(p + place(i));
-                    S[i] = v.x; S[i + 1] = v.y; S[i + 2] = v.z; S[i + 3] = v.w;
+                    S[i / 2] = {{v.x, v.y}};
+                    S[i / 2 + 1] = {{v.z, v.w}};
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < NX; ++i) S[i] = p[place(i)];
+                for (int i = 0; i < NX; ++i) S[i / 2].v[i & 1] = p[place(i)];
             }
         }
         auto store = [&](float *p) {
             if (!live) return;
             if (a.rs == 1) {
 #pragma unroll
-                for (int i = 0; i < NX; i += 4) *(float4 *)(p + place(i)) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                for (int i = 0; i < NX; i += 4) *(float4 *)(p + place(i)) = make_float4(S[i / 2].v[0], S[i / 2].v[1], S[i / 2 + 1].v[0], S[i / 2 + 1].v[1]);
             } else {
 #pragma unroll
-                for (int i = 0; i < NX; ++i) p[place(i)] = S[i];
+                for (int i = 0; i < NX; ++i) p[place(i)] = S[i / 2].v[i & 1];
             }
         };
         auto anchor = [&](int k) { store(a.anchors + ((long long)k * BH + bh) * n_state); };
@@ -481,8 +499,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     uint32_t part[3][8];
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
-                        if (NS == 1) part[0][u] = pack_bf16x2(S[i + 2 * u], S[i + 2 * u + 1]);
-                        else split3(S[i + 2 * u], S[i + 2 * u + 1], part[0][u], part[1][u], part[2][u]);
+                        const Ch<2> &x = S[i / 2 + u];
+                        if (NS == 1) part[0][u] = pack_bf16x2(x.v[0], x.v[1]);
+                        else split3(x, part[0][u], part[1][u], part[2][u]);
                     }
 #pragma unroll
                     for (int p = 0; p < NS; ++p) tmem_st8(tmem + lanes + Lay::T_SC + p * (DX / 2) + (half * NX + i) / 2, part[p]);
@@ -510,16 +529,22 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             const float da = w.a, em = w.em;
             // next to 1 by the decay minus 1, whose rounding does not grow with the chunks
             const bool near = da > 0.5f, none = da == 0.f;
-            const float m = near ? em : da;
+            const Ch<2> m = all<2>(near ? em : da);
 #pragma unroll
             for (int i = 0; i < NX; i += 16) {
                 uint32_t d[16];
                 tmem_ld16(tmem + lanes + Lay::T_DS + half * NX + i, d);
                 tmem_wait_ld();
+                if (none) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    const float ds = __uint_as_float(d[u]);
-                    S[i + u] = none ? ds : fmaf(S[i + u], m, near ? S[i + u] + ds : ds);
+                    for (int u = 0; u < 16; ++u) S[(i + u) / 2].v[u & 1] = __uint_as_float(d[u]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        Ch<2> &x = S[i / 2 + u];
+                        const Ch<2> ds{{__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])}};
+                        x = fma(x, m, near ? add(x, ds) : ds);
+                    }
                 }
             }
             copy();
@@ -544,19 +569,30 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     arrive(o_free);
                 }
                 float dot[RB];
+                const int lim = live ? nv - i0 : 0;
 #pragma unroll
-                for (int i = 0; i < RB; ++i) {
-                    const float x = w.rw[i0 + i] * __uint_as_float(oi[i]);
-                    const float o = fmaf(a.oscale, __uint_as_float(oa[i]), x);
-                    if (DOT) {
-                        const uint32_t q = pair_at(tile_w(s), i0 + i, j & ~1);
-                        dot[i] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
+                for (int i = 0; i < RB; i += 4) {
+                    const float4 rw = *(const float4 *)&w.rw[i0 + i];
+                    const float r4[4] = {rw.x, rw.y, rw.z, rw.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float x = r4[u] * __uint_as_float(oi[i + u]);
+                        if (DOT) {
+                            const uint32_t q = pair_at(tile_w(s), i0 + i + u, j & ~1);
+                            dot[i + u] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
+                        }
+                        oa[i + u] = __float_as_uint(fmaf(a.oscale, __uint_as_float(oa[i + u]), x));
                     }
-                    if (live && i0 + i < nv) {
-                        const long long at_o = row_of(a.vo, b, h, row0 + i0 + i) + j;
-                        if (a.out_f32) ((float *)a.out)[at_o] = o;
-                        else ((__nv_bfloat16 *)a.out)[at_o] = __float2bfloat16_rn(o);
-                    }
+                }
+                const long long at_o = out0 + (long long)(row0 + i0) * a.vo.l;
+                if (a.out_f32) {
+#pragma unroll
+                    for (int i = 0; i < RB; ++i)
+                        if (i < lim) ((float *)a.out)[at_o + i * a.vo.l] = __uint_as_float(oa[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RB; ++i)
+                        if (i < lim) ((__nv_bfloat16 *)a.out)[at_o + i * a.vo.l] = __float2bfloat16_rn(__uint_as_float(oa[i]));
                 }
                 if (DOT) {
                     // over the quadrant's channels; a lane goes on with half of the rows each time
