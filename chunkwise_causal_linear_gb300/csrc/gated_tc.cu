@@ -25,7 +25,8 @@
 //
 // Warps (640 threads, one block an SM): 0 loads tiles by TMA into a ring and forms the chunks' weights
 // (64-bit sums); 1 issues the products; 4-11 form Y~ and P; 12-19 hold the state (S^T, row = lane of
-// their TMEM quadrant, half of the columns each), write its copy and store the rows.
+// their TMEM quadrant, half of the columns each) and write its copy. Both groups store the rows, half
+// each (with DOT the second one all of them, while W's tile is held).
 //
 // The decays' gradient (DOT) needs R_i = q_i . dq_i and C_j = k_j . dk_j without the rows' own pairs. Over
 // earlier chunks they are the products of the inter rows with a fourth tile (q or k, W); inside the chunk
@@ -87,6 +88,15 @@ struct Weights {          // of one chunk
     float a, em, pad[2];  // decay over the chunk, and that minus 1
 };
 
+// A log decay above -104 in units of 2^-44 doublings, to a unit: the product with log2 e in two parts.
+constexpr float UNIT = 5.684341886080801e-14f, UNITS = 17592186044416.f;
+__device__ __forceinline__ long long doublings(float g)
+{
+    constexpr float LOG2E = 1.44269502f, LOG2E_REST = 1.92596303e-8f;
+    const float p = g * LOG2E, rest = fmaf(g, LOG2E_REST, fmaf(g, LOG2E, -p));
+    return __float2ll_rn(p * UNITS) + __float2ll_rn(rest * UNITS);
+}
+
 template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr int NS = DOT ? 3 : 1;  // bf16 parts of the state's copy
     static constexpr int X = GT_C * DX * 2, Z = GT_C * DZ * 2, W = DOT ? Z : 0;
@@ -97,7 +107,9 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_W = OFF_P + 2 * P,
                          OFF_BAR = OFF_W + GT_SLOTS * (int)sizeof(Weights), ALLOC = OFF_BAR + 256 + 1024;
     // TMEM columns
-    static constexpr uint32_t T_SC = 0, T_DS = NS * (DX / 2), T_OI = T_DS + DX, T_OA = T_OI + 64, T_A = T_OA + 64;
+    // one part: two copies of the state in turn, so that a chunk's sum need not wait for its inter product
+    static constexpr int COPIES = DOT ? 1 : 2;
+    static constexpr uint32_t T_SC = 0, T_DS = NS * COPIES * (DX / 2), T_OI = T_DS + DX, T_OA = T_OI + 64, T_A = T_OA + 64;
     // the second score block has columns of its own where they are left, else those of Oi
     static constexpr bool A2_OWN = T_A + 128 <= 512;
     static constexpr uint32_t T_A2 = A2_OWN ? T_A + 64 : T_OI;
@@ -124,11 +136,16 @@ __device__ __forceinline__ void split3(Ch<2> x, uint32_t &hi, uint32_t &mid, uin
     lo = pack_bf16x2(x.v[0], x.v[1]);
 }
 
-// wait_phase with the clock read only once a wait was long: the timer is far from the SM.
+// wait_phase with the clock read only once a wait was long (the timer is far from the SM), and its loop
+// out of line: a chunk has some twenty waits.
+__device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, volatile int *abort, int *err, unsigned long long timeout_ns)
+{
+    return wait_phase(bar, parity, Ctl{abort, err, timeout_ns});
+}
 __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, const Ctl &ctl)
 {
-    if (mbar_try(bar, parity) || mbar_try_sleep(bar, parity, 200000u)) return true;
-    return wait_phase(bar, parity, ctl);
+    if (mbar_try_sleep(bar, parity, 200000u)) return true;
+    return wait_longer(bar, parity, ctl.abort, ctl.err, ctl.timeout_ns);
 }
 
 template <int DX, int DZ, bool DOT>
@@ -175,7 +192,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         mbar_init(p_ready, 8);  // by chunks in turn: P of the next one may be done before this one's is awaited
         mbar_init(p_ready + 1, 8);
         mbar_init(o_done, 1);
-        mbar_init(o_free, 8);
+        mbar_init(o_free, DOT ? 8 : 16);
         mbar_init(drain, 1);
         *abort_flag = 0;
         mbar_init_fence();
@@ -189,6 +206,83 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     auto arrive = [&](uint64_t *bar) {  // of a warp whose lanes have all done their part
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
+    };
+
+    // Rows first .. first + N - 1 of the sweep's chunk c, the channels of this warp's TMEM quadrant: the inter rows
+    // weighted, the intra rows added, stored; with DOT the inter rows' products with W's.
+    const int q4 = warp & 3, j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
+    const bool live = DZ == 128 || lane < 16;
+    const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+    const long long out0 = row_of(a.vo, b, h, 0) + j;
+    const uint32_t step_o = (uint32_t)a.vo.l * (a.out_f32 ? 4 : 2);
+    auto rows = [&](int c, int first) {
+        constexpr int RB = DOT ? 8 : 16, N = DOT ? 32 : 16;  // rows at a time, by what the registers hold
+        const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
+        const Weights &w = weights[c % GT_SLOTS];
+#pragma unroll
+        for (int k = 0; k < N / RB; ++k) {
+            const int i0 = first + RB * k;
+            uint32_t oi[RB], oa[RB];
+            if constexpr (DOT) {
+                tmem_ld8(tmem + lanes + Lay::T_OI + i0, oi);
+                tmem_ld8(tmem + lanes + Lay::T_OA + i0, oa);
+            } else {
+                tmem_ld16(tmem + lanes + Lay::T_OI + i0, oi);
+                tmem_ld16(tmem + lanes + Lay::T_OA + i0, oa);
+            }
+            tmem_wait_ld();
+            if (k == N / RB - 1) {
+                tc_fence_before();
+                arrive(o_free);
+            }
+            float dot[RB];
+            const int lim = live ? nv - i0 : 0;
+#pragma unroll
+            for (int i = 0; i < RB; i += 4) {
+                const float4 rw = *(const float4 *)&w.rw[i0 + i];
+                const float r4[4] = {rw.x, rw.y, rw.z, rw.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float x = r4[u] * __uint_as_float(oi[i + u]);
+                    if (DOT) {
+                        const uint32_t q = pair_at(tile_w(s), i0 + i + u, j & ~1);
+                        dot[i + u] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
+                    }
+                    oa[i + u] = __float_as_uint(fmaf(a.oscale, __uint_as_float(oa[i + u]), x));
+                }
+            }
+            const long long at_o = out0 + (long long)(row0 + i0) * a.vo.l;
+            // 32-bit steps of a row's bytes: one instruction an address
+            if (a.out_f32) {
+                char *const p = (char *)((float *)a.out + at_o);
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    if (i < lim) *(float *)(p + (uint64_t)(uint32_t)i * step_o) = __uint_as_float(oa[i]);
+            } else {
+                char *const p = (char *)((__nv_bfloat16 *)a.out + at_o);
+#pragma unroll
+                for (int i = 0; i < RB; ++i)
+                    if (i < lim) *(__nv_bfloat16 *)(p + (uint64_t)(uint32_t)i * step_o) = __float2bfloat16_rn(__uint_as_float(oa[i]));
+            }
+            if (DOT) {
+                // over the quadrant's channels; a lane goes on with half of the rows each time
+                int r = 0;
+#pragma unroll
+                for (int o = 16, n = RB / 2; n > 0; o >>= 1, n >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int i = 0; i < RB / 2; ++i)
+                        if (i < n) {
+                            const float send = up ? dot[i] : dot[i + n], keep = up ? dot[i + n] : dot[i];
+                            dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                    r += up ? n : 0;
+                }
+                dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
+                dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
+                if (!(lane & 3) && i0 + r < nv) a.dot[((long long)q4 * BH + bh) * a.L + row0 + i0 + r] = dot[0];
+            }
+        }
     };
 
     if (warp == 0) {
@@ -217,38 +311,42 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             }
             issued = c + 1;
             const float n0 = gate(c + 1, 2 * lane), n1 = gate(c + 1, 2 * lane + 1);  // on its way meanwhile
-            // sums of the rows 0 .. i, in 64 bits; rows whose decay is 0 count as cuts instead
+            // sums of the rows 0 .. i in units of 2^-44 doublings; rows whose decay is 0 count as cuts
+            // instead. (Sums in 64-bit floating point took 4,700 cycles a chunk, as long as all the rest.)
             const bool z0 = expf(g0) == 0.f, z1 = expf(g1) == 0.f;
-            const double d0 = z0 ? 0.0 : (double)g0, d1 = z1 ? 0.0 : (double)g1;
-            double run = d0 + d1;
+            const bool odd = __any_sync(0xffffffffu, !(g0 < 88.f) || !(g1 < 88.f));  // NaN, or a decay past fp32
+            const long long d0 = z0 ? 0 : doublings(g0), d1 = z1 ? 0 : doublings(g1);
+            long long run = d0 + d1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double u = __shfl_up_sync(0xffffffffu, run, o);
+                const long long u = __shfl_up_sync(0xffffffffu, run, o);
                 if (lane >= o) run += u;
             }
-            const double all = __shfl_sync(0xffffffffu, run, 31), G1 = run, G0 = run - d1;
+            const long long whole = __shfl_sync(0xffffffffu, run, 31);
             const uint32_t m0 = __ballot_sync(0xffffffffu, z0), m1 = __ballot_sync(0xffffffffu, z1);
             const uint32_t below = (1u << lane) - 1u;
             const int cuts = __popc(m0) + __popc(m1);
             const int r0 = __popc(m0 & (below | (1u << lane))) + __popc(m1 & below), r1 = r0 + (z1 ? 1 : 0);
             Weights &w = weights[c % GT_SLOTS];
-            constexpr double LOG2E = 1.4426950408889634074;
+            const float bad = odd ? __int_as_float(0x7fffffff) : 0.f;
+            const float sign = rev ? -1.f : 1.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const double G = i ? G1 : G0;
-                const int run_id = i ? r1 : r0;
+                const long long G = i ? run : run - d1;
+                const int id = i ? r1 : r0;
                 // hi and lo together hold differences of rows to 2^-24 of what lies between two cuts
-                double G2 = G * LOG2E - (double)GT_CUT * run_id;
-                if (rev) G2 = -G2;
-                const float hi = (float)G2, lo = (float)(G2 - (double)hi);
-                w.row[2 * lane + i] = make_float2(hi, lo);
-                const float start = run_id == 0 ? expf((float)G) : 0.f, end = run_id == cuts ? expf((float)(all - G)) : 0.f;
-                w.kw[2 * lane + i] = a.yscale * (rev ? start : end);
-                w.rw[2 * lane + i] = a.oscale * (rev ? end : start);
+                const float g2 = (float)G * UNIT, rest = (float)(G - (long long)(float)G) * UNIT;
+                const float cut = -GT_CUT * (float)id, hi = cut + g2, lo = (g2 - (hi - cut)) + rest;
+                w.row[2 * lane + i] = make_float2(sign * hi + bad, sign * lo);
+                const float start = id == 0 ? exp2f(g2) * fmaf(rest, 0.693147181f, 1.f) : 0.f;
+                const float end = id == cuts ? exp2f((float)(whole - G) * UNIT) : 0.f;
+                w.kw[2 * lane + i] = a.yscale * (rev ? start : end) + bad;
+                w.rw[2 * lane + i] = a.oscale * (rev ? end : start) + bad;
             }
             if (lane == 0) {
-                w.a = cuts ? 0.f : expf((float)all);
-                w.em = cuts ? -1.f : expm1f((float)all);
+                const float g2 = (float)whole * UNIT;
+                w.a = (cuts ? 0.f : exp2f(g2)) + bad;
+                w.em = (cuts ? -1.f : expm1f(g2 * 0.693147181f)) + bad;
             }
             g0 = n0;
             g1 = n1;
@@ -298,22 +396,26 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             // Oi's columns hold the second scores of the next chunk: these wait for the rows' readers
             const bool late = inner && !Lay::A2_OWN;
             bool ok = totals || nch == 0 || scores(0);
+            auto inter = [&](int c) {
+                const uint64_t dx = smem_desc(smem_u32(tile_x(c % NST)), 16, 1024);
+                const uint32_t sc = tmem + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
+#pragma unroll
+                for (int p = 0; p < NS; ++p)
+#pragma unroll
+                    for (int k = 0; k < DX / 16; ++k)
+                        mma_ts(tmem + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32),
+                               ID_INTER, p + k > 0);
+            };
             for (int c = 0; ok && c < nch; ++c) {
                 const int s = c % NST;
                 const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
                 // the state before the chunk is in place, dS has been read
                 if (!(ok = wait1(s_ready, c & 1))) break;
-                if (!totals) {
+                if (DOT) {  // the one copy of the state is written again once dS is there: read it before
                     if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
                     if (late && !(ok = wait1(sc_free, c & 1))) break;
                     tc_fence_after();
-                    const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024);
-#pragma unroll
-                    for (int p = 0; p < NS; ++p)
-#pragma unroll
-                        for (int k = 0; k < DX / 16; ++k)
-                            mma_ts(tmem + Lay::T_OI, tmem + Lay::T_SC + p * (DX / 2) + k * 8,
-                                   desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32), ID_INTER, p + k > 0);
+                    inter(c);
                 }
                 if (!(ok = wait1(yt_ready, c & 1))) break;
                 tc_fence_after();
@@ -332,6 +434,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 if (!late) {
                     if (!(ok = wait1(sc_free, c & 1))) break;
                     if (c + 1 < nch && !(ok = scores(c + 1))) break;
+                }
+                if (!DOT) {
+                    if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
+                    tc_fence_after();
+                    inter(c);
                 }
                 if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
                 tc_fence_after();
@@ -354,15 +461,16 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         }
     } else if (warp >= PY0 && warp < ST0) {
         // ------------------------------------------------------------ Y~ and P
-        const int pw = warp - PY0, ft = 32 * pw + lane, q4 = warp & 3, half = pw >> 2;
+        const int pw = warp - PY0, ft = 32 * pw + lane, half = pw >> 2;
         constexpr int G = DX / 8, RG = 256 / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG, ..
         const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
         const int ta = 16 * q4 + (lane >> 2), tb = ta + 8, cpos = lane & 3;
+        bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
             const Weights &w = weights[c % GT_SLOTS];
-            if (!wait(&full[s], (c / NST) & 1)) break;
-            if (c > 0 && !wait(state_done, (c - 1) & 1)) break;  // Y~ of the chunk before has been read
+            if (!(ok = wait(&full[s], (c / NST) & 1))) break;
+            if (c > 0 && !(ok = wait(state_done, (c - 1) & 1))) break;  // Y~ of the chunk before has been read
             const uint8_t *src = tile_y(s) + off;
             uint4 v[NR];
 #pragma unroll
@@ -388,7 +496,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             fence_async_smem();
             arrive(yt_ready);
             if (totals) continue;
-            if (!wait(scores_done, c & 1)) break;
+            if (!DOT && c > 0) {  // the other half of the rows of the chunk before
+                if (!(ok = wait(o_done, (c - 1) & 1))) break;
+                tc_fence_after();
+                rows(c - 1, 32 * half + 16);
+            }
+            if (!(ok = wait(scores_done, c & 1))) break;
             tc_fence_after();
             uint32_t r1[32], r2[32];  // the first 16
             tmem_ld16x256_x4(tmem + Lay::T_A + ((uint32_t)(32 * q4) << 16) + 32 * half, r1);
@@ -454,14 +567,15 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 if (col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
             }
         }
+        if (!DOT && !totals && ok && nch > 0 && wait(o_done, (nch - 1) & 1)) {
+            tc_fence_after();
+            rows(nch - 1, 32 * half + 16);
+        }
     } else if (warp >= ST0) {
         // ------------------------------------------------------------ the state, and the rows
-        const int q4 = warp & 3, half = (warp - ST0) >> 2;
-        const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-        const int j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
-        const bool live = DZ == 128 || lane < 16;
+        const int half = (warp - ST0) >> 2;
         constexpr int NX = DX / 2;  // x channels half * NX ..
-        const long long n_state = (long long)DX * DZ, out0 = row_of(a.vo, b, h, 0) + j;
+        const long long n_state = (long long)DX * DZ;
         const long long at = (a.by_seg ? (long long)seg * BH + bh : (long long)slot * a.H + h) * n_state;
         Ch<2> S[NX / 2];
 #pragma unroll
@@ -492,7 +606,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             }
         };
         auto anchor = [&](int k) { store(a.anchors + ((long long)k * BH + bh) * n_state); };
-        auto copy = [&]() {
+        auto copy = [&](int c) {  // of the state before chunk c
             if (!totals) {
 #pragma unroll
                 for (int i = 0; i < NX; i += 16) {
@@ -504,7 +618,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                         else split3(x, part[0][u], part[1][u], part[2][u]);
                     }
 #pragma unroll
-                    for (int p = 0; p < NS; ++p) tmem_st8(tmem + lanes + Lay::T_SC + p * (DX / 2) + (half * NX + i) / 2, part[p]);
+                    for (int p = 0; p < NS; ++p) tmem_st8(tmem + lanes + Lay::T_SC + (p + c % Lay::COPIES) * (DX / 2) + (half * NX + i) / 2, part[p]);
                 }
                 tmem_wait_st();
             }
@@ -515,10 +629,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         const int anchors_here = a.anchors ? (t1 - t0 + a.anchor_chunks * C - 1) / (a.anchor_chunks * C) : 0;
         if (a.anchors && rev)  // those that end behind the sequence
             for (int k = (nch + a.anchor_chunks - 1) / a.anchor_chunks; k < anchors_here; ++k) anchor(first_anchor + k);
-        copy();
+        copy(0);
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
-            const int s = c % NST, cc = chunk_of(c), row0 = t0 + cc * C, nv = min(C, te - row0);
+            const int s = c % NST, cc = chunk_of(c);
             const Weights &w = weights[c % GT_SLOTS];
             if (a.anchors) {
                 if (rev && (c == 0 || (cc + 1) % a.anchor_chunks == 0)) anchor(first_anchor + cc / a.anchor_chunks);
@@ -547,72 +661,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     }
                 }
             }
-            copy();
+            copy(c + 1);
             if (totals) continue;
             if (!(ok = wait(o_done, c & 1))) break;
             tc_fence_after();
-            constexpr int RB = DOT ? 8 : 16;  // rows at a time, by what the registers hold
-#pragma unroll
-            for (int k = 0; k < 32 / RB; ++k) {
-                const int i0 = 32 * half + RB * k;
-                uint32_t oi[RB], oa[RB];
-                if constexpr (DOT) {
-                    tmem_ld8(tmem + lanes + Lay::T_OI + i0, oi);
-                    tmem_ld8(tmem + lanes + Lay::T_OA + i0, oa);
-                } else {
-                    tmem_ld16(tmem + lanes + Lay::T_OI + i0, oi);
-                    tmem_ld16(tmem + lanes + Lay::T_OA + i0, oa);
-                }
-                tmem_wait_ld();
-                if (k == 32 / RB - 1) {
-                    tc_fence_before();
-                    arrive(o_free);
-                }
-                float dot[RB];
-                const int lim = live ? nv - i0 : 0;
-#pragma unroll
-                for (int i = 0; i < RB; i += 4) {
-                    const float4 rw = *(const float4 *)&w.rw[i0 + i];
-                    const float r4[4] = {rw.x, rw.y, rw.z, rw.w};
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float x = r4[u] * __uint_as_float(oi[i + u]);
-                        if (DOT) {
-                            const uint32_t q = pair_at(tile_w(s), i0 + i + u, j & ~1);
-                            dot[i + u] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
-                        }
-                        oa[i + u] = __float_as_uint(fmaf(a.oscale, __uint_as_float(oa[i + u]), x));
-                    }
-                }
-                const long long at_o = out0 + (long long)(row0 + i0) * a.vo.l;
-                if (a.out_f32) {
-#pragma unroll
-                    for (int i = 0; i < RB; ++i)
-                        if (i < lim) ((float *)a.out)[at_o + i * a.vo.l] = __uint_as_float(oa[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < RB; ++i)
-                        if (i < lim) ((__nv_bfloat16 *)a.out)[at_o + i * a.vo.l] = __float2bfloat16_rn(__uint_as_float(oa[i]));
-                }
-                if (DOT) {
-                    // over the quadrant's channels; a lane goes on with half of the rows each time
-                    int r = 0;
-#pragma unroll
-                    for (int o = 16, n = RB / 2; n > 0; o >>= 1, n >>= 1) {
-                        const bool up = lane & o;
-#pragma unroll
-                        for (int i = 0; i < RB / 2; ++i)
-                            if (i < n) {
-                                const float send = up ? dot[i] : dot[i + n], keep = up ? dot[i + n] : dot[i];
-                                dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                            }
-                        r += up ? n : 0;
-                    }
-                    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
-                    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
-                    if (!(lane & 3) && i0 + r < nv) a.dot[((long long)q4 * BH + bh) * a.L + row0 + i0 + r] = dot[0];
-                }
-            }
+            rows(c, 32 * half);
             if (DOT) arrive(&stage_free[s]);
         }
         if (ok) {
@@ -708,6 +761,7 @@ int launch_pass(const GatedArgs &p, Pass &s)
 }
 
 bool tc_dim(int d) { return d == 64 || d == 128; }
+bool tc_out(const View &v) { return v.l < (1ll << 30); }  // a row's bytes fit 32 bits
 bool tc_view(const void *p, const View &v, int B, int n, int L)
 {
     auto ok = [&](long long s, int len) { return len == 1 || (s > 0 && s < (1ll << 38)); };
@@ -759,9 +813,13 @@ struct TcBwdSpace {
 bool gated_tc_fwd_ok(const GatedArgs &p)
 {
     return p.dtype == LA_BF16 && tc_dim(p.d) && tc_dim(p.e) && tc_view(p.q, p.vq, p.B, p.H, p.L) &&
-           tc_view(p.k, p.vk, p.B, p.Hk, p.L) && tc_view(p.v, p.vv, p.B, p.Hk, p.L);
+           tc_view(p.k, p.vk, p.B, p.Hk, p.L) && tc_view(p.v, p.vv, p.B, p.Hk, p.L) && tc_out(p.vo);
 }
-bool gated_tc_bwd_ok(const GatedArgs &p) { return gated_tc_fwd_ok(p) && tc_view(p.dout, p.vo, p.B, p.H, p.L) && aligned(p.state0, 16) && aligned(p.dstate, 16) && aligned(p.dstate0, 16); }
+bool gated_tc_bwd_ok(const GatedArgs &p)
+{
+    return gated_tc_fwd_ok(p) && tc_view(p.dout, p.vo, p.B, p.H, p.L) && tc_out(p.vdq) && tc_out(p.vdk) && tc_out(p.vdv) &&
+           aligned(p.state0, 16) && aligned(p.dstate, 16) && aligned(p.dstate0, 16);
+}
 
 size_t gated_tc_fwd_ws(int B, int H, int L, int d, int e, int sms)
 {
