@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(128) log_decay_kernel(const LogDecayArgs a)
         }
         s += carry;
         // a decay of 0 has no gradient: every pair across it is 0
-        if (t >= t0) a.dg[(long long)bh * a.L + t] = expf(a.g[row_of(a.vg, b, h, t)]) == 0.f ? 0.f : (float)s;
+        if (t >= t0) a.dg[(long long)bh * a.L + t] = a.g[row_of(a.vg, b, h, t)] < GATED_CUT ? 0.f : (float)s;
         carry = __shfl_sync(0xffffffffu, s, 31);
     }
 }

@@ -10,6 +10,9 @@ namespace la {
 // the decays' gradient without the sums behind them.
 constexpr int GATED_ANCHOR = 1024;
 
+// A log decay below this counts as -inf: exp of it is 0 in fp32.
+constexpr float GATED_CUT = -104.f;
+
 struct GatedArgs {
     const void *q, *k, *v, *dout;
     void *out, *dq, *dk, *dv;

@@ -23,8 +23,8 @@
 // rounding a chunk, and Y~'s three parts hold f Y to 2^-24, so that states are those of fp32 arithmetic. The
 // decays' gradient reads the inter rows, there S too has three parts.
 //
-// Warps (640 threads, one block an SM): 0 loads tiles by TMA into a ring and forms the chunks' weights
-// (64-bit sums); 1 issues the products; 4-11 form Y~ and P; 12-19 hold the state (S^T, row = lane of
+// Warps (640 threads, one block an SM): 0 loads tiles by TMA into a ring, 3 forms the chunks' weights (64-bit
+// sums); 1 and 2 issue the products; 4-11 form Y~ and P; 12-19 hold the state (S^T, row = lane of
 // their TMEM quadrant, half of the columns each) and write its copy. Both groups store the rows, half
 // each (with DOT the second one all of them, while W's tile is held).
 //
@@ -63,7 +63,7 @@ struct GtArgs {
     int sx, sy, sz, sw;  // heads of the state to a head of the operand
     int B, H, L, e;      // e: channels of out
     float yscale, oscale;
-    int reverse, totals, inner;
+    int reverse, totals;
     int seg_rows, nseg;
     const int *lengths, *slots;
     int n_slots;
@@ -107,7 +107,7 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_W = OFF_P + 2 * P,
                          OFF_BAR = OFF_W + GT_SLOTS * (int)sizeof(Weights), ALLOC = OFF_BAR + 256 + 1024;
     // TMEM columns
-    // one part: two copies of the state in turn, so that a chunk's sum need not wait for its inter product
+    // one part: two copies of the state in turn, so that the next one need not wait for the inter product
     static constexpr int COPIES = DOT ? 1 : 2;
     static constexpr uint32_t T_SC = 0, T_DS = NS * COPIES * (DX / 2), T_OI = T_DS + DX, T_OA = T_OI + 64, T_A = T_OA + 64;
     // the second score block has columns of its own where they are left, else those of Oi
@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t pair_at(const uint8_t *tile, int row, int c)
 // Two values in three bf16 parts each: hi + mid + lo = x to 2^-24.
 __device__ __forceinline__ Ch<2> less(const Ch<2> &x, uint32_t part)
 {
-    return add(x, Ch<2>{{-bf_lo(part), -bf_hi(part)}});
+    return fma(Ch<2>{{bf_lo(part), bf_hi(part)}}, all<2>(-1.f), x);
 }
 __device__ __forceinline__ void split3(Ch<2> x, uint32_t &hi, uint32_t &mid, uint32_t &lo)
 {
@@ -148,7 +148,7 @@ __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, const 
     return wait_longer(bar, parity, ctl.abort, ctl.err, ctl.timeout_ns);
 }
 
-template <int DX, int DZ, bool DOT>
+template <int DX, int DZ, bool DOT, bool INNER>
 __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_constant__ GtArgs a)
 {
     using Lay = GtLayout<DX, DZ, DOT>;
@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     uint64_t *const bars = (uint64_t *)(sm + Lay::OFF_BAR);
     uint64_t *const full = bars, *const stage_free = full + NST, *const yt_ready = stage_free + NST, *const state_done = yt_ready + 1,
              *const s_ready = state_done + 1, *const scores_done = s_ready + 1, *const sc_free = scores_done + 1,
-             *const p_ready = sc_free + 1, *const o_done = p_ready + 2, *const o_free = o_done + 1, *const drain = o_free + 1;
+             *const p_ready = sc_free + 1, *const o_done = p_ready + 2, *const o_free = o_done + 1,
+             *const inter_done = o_free + 1, *const drain = inter_done + 1;
     uint32_t *const tmem_slot = (uint32_t *)(sm + Lay::OFF_BAR + 224);
     volatile int *const abort_flag = (volatile int *)(sm + Lay::OFF_BAR + 228);
 
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L),
               te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
     const int nch = (te - t0 + C - 1) / C;
-    const bool totals = a.totals != 0, rev = a.reverse != 0, inner = DOT && a.inner != 0;
+    const bool totals = a.totals != 0, rev = INNER ? false : a.reverse != 0;
     const int slot = gated_slot(a.slots, b, a.n_slots, tid == 0 ? a.err : nullptr);
     const Ctl ctl{abort_flag, a.err, a.timeout_ns};
     auto chunk_of = [&](int c) { return rev ? nch - 1 - c : c; };  // c-th chunk of the sweep
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 2);                       // the TMA's bytes, the weights
-            mbar_init(&stage_free[i], DOT && !totals ? 9 : 1);  // the products, and the readers of W
+            mbar_init(&stage_free[i], totals ? 1 : DOT ? 10 : 2);  // both issuers' products, and the readers of W
         }
         mbar_init(yt_ready, 8);
         mbar_init(state_done, 1);
@@ -193,7 +194,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         mbar_init(p_ready + 1, 8);
         mbar_init(o_done, 1);
         mbar_init(o_free, DOT ? 8 : 16);
-        mbar_init(drain, 1);
+        mbar_init(inter_done, 1);
+        mbar_init(drain, 2);
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -216,20 +218,15 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     const long long out0 = row_of(a.vo, b, h, 0) + j;
     const uint32_t step_o = (uint32_t)a.vo.l * (a.out_f32 ? 4 : 2);
     auto rows = [&](int c, int first) {
-        constexpr int RB = DOT ? 8 : 16, N = DOT ? 32 : 16;  // rows at a time, by what the registers hold
+        constexpr int RB = 8, N = DOT ? 32 : 16;  // 8 rows at a time, by what the registers hold
         const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
         const Weights &w = weights[c % GT_SLOTS];
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < N / RB; ++k) {
             const int i0 = first + RB * k;
             uint32_t oi[RB], oa[RB];
-            if constexpr (DOT) {
-                tmem_ld8(tmem + lanes + Lay::T_OI + i0, oi);
-                tmem_ld8(tmem + lanes + Lay::T_OA + i0, oa);
-            } else {
-                tmem_ld16(tmem + lanes + Lay::T_OI + i0, oi);
-                tmem_ld16(tmem + lanes + Lay::T_OA + i0, oa);
-            }
+            tmem_ld8(tmem + lanes + Lay::T_OI + i0, oi);
+            tmem_ld8(tmem + lanes + Lay::T_OA + i0, oa);
             tmem_wait_ld();
             if (k == N / RB - 1) {
                 tc_fence_before();
@@ -248,7 +245,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                         const uint32_t q = pair_at(tile_w(s), i0 + i + u, j & ~1);
                         dot[i + u] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
                     }
-                    oa[i + u] = __float_as_uint(fmaf(a.oscale, __uint_as_float(oa[i + u]), x));
+                    oa[i + u] = __float_as_uint(__uint_as_float(oa[i + u]) + x);
                 }
             }
             const long long at_o = out0 + (long long)(row0 + i0) * a.vo.l;
@@ -260,9 +257,19 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     if (i < lim) *(float *)(p + (uint64_t)(uint32_t)i * step_o) = __uint_as_float(oa[i]);
             } else {
                 char *const p = (char *)((__nv_bfloat16 *)a.out + at_o);
+                if (lim >= RB) {
 #pragma unroll
-                for (int i = 0; i < RB; ++i)
-                    if (i < lim) *(__nv_bfloat16 *)(p + (uint64_t)(uint32_t)i * step_o) = __float2bfloat16_rn(__uint_as_float(oa[i]));
+                    for (int i = 0; i < RB; ++i)
+                        *(__nv_bfloat16 *)(p + (uint64_t)(uint32_t)i * step_o) = __float2bfloat16_rn(__uint_as_float(oa[i]));
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < lim; ++i) {
+                        uint32_t o = 0;
+#pragma unroll
+                        for (int u = 0; u < RB; ++u) o = u == i ? oa[u] : o;
+                        *(__nv_bfloat16 *)(p + (uint64_t)(uint32_t)i * step_o) = __float2bfloat16_rn(__uint_as_float(o));
+                    }
+                }
             }
             if (DOT) {
                 // over the quadrant's channels; a lane goes on with half of the rows each time
@@ -286,18 +293,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     };
 
     if (warp == 0) {
-        // ------------------------------------------------------------ tiles and weights
-        const float *const gp = a.g + b * a.vg.b + h * a.vg.h;
-        auto gate = [&](int c, int i) {  // log decay of row i of the sweep's chunk c; 0 behind the end
-            const int t = t0 + chunk_of(c) * C + i;
-            return c < nch && t < te ? gp[(long long)t * a.vg.l] : 0.f;
-        };
-        int issued = 0;
-        float g0 = gate(0, 2 * lane), g1 = gate(0, 2 * lane + 1);
-        for (int c = 0; c < nch; ++c) {
-            const int s = c % NST;
-            if (c >= NST && !wait(&stage_free[s], ((c / NST) - 1) & 1)) break;
-            if (lane == 0) {
+        // ------------------------------------------------------------ tiles
+        if (lane == 0) {
+            int issued = 0;
+            for (int c = 0; c < nch; ++c) {
+                const int s = c % NST;
+                if (c >= NST && !wait_long(&stage_free[s], ((c / NST) - 1) & 1, ctl)) break;
                 const int row = t0 + chunk_of(c) * C;
                 mbar_arrive_expect_tx(&full[s], totals ? Lay::X + Lay::Z : Lay::STAGE);
                 for (int k = 0; k < DX / 64; ++k) {
@@ -308,12 +309,30 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     tma_load_4d(tile_z(s) + k * C * 128, &a.mz, k * 64, row, h / a.sz, b, &full[s]);
                     if (DOT && !totals) tma_load_4d(tile_w(s) + k * C * 128, &a.mw, k * 64, row, h / a.sw, b, &full[s]);
                 }
+                issued = c + 1;
             }
-            issued = c + 1;
+            // never leave the CTA with loads in flight: wait for every issued stage to land
+            for (int c = (issued > NST ? issued - NST : 0); c < issued; ++c) {
+                const uint64_t begin = globaltimer();
+                while (!mbar_try_sleep(&full[c % NST], (c / NST) & 1, 200000u))
+                    if (*abort_flag || globaltimer() - begin > ctl.timeout_ns) break;
+            }
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ weights
+        // Formed and written a ring ahead of the tiles: place c % 8 was last read for chunk c - 8, and the tiles
+        // of chunk c - 1 - NST are free, so every reader has gone past chunk c - 7 at least.
+        const float *const gp = a.g + b * a.vg.b + h * a.vg.h;
+        auto gate = [&](int c, int i) {  // log decay of row i of the sweep's chunk c; 0 behind the end
+            const int t = t0 + chunk_of(c) * C + i;
+            return c < nch && t < te ? gp[(long long)t * a.vg.l] : 0.f;
+        };
+        float g0 = gate(0, 2 * lane), g1 = gate(0, 2 * lane + 1);
+        for (int c = 0; c < nch; ++c) {
             const float n0 = gate(c + 1, 2 * lane), n1 = gate(c + 1, 2 * lane + 1);  // on its way meanwhile
             // sums of the rows 0 .. i in units of 2^-44 doublings; rows whose decay is 0 count as cuts
             // instead. (Sums in 64-bit floating point took 4,700 cycles a chunk, as long as all the rest.)
-            const bool z0 = expf(g0) == 0.f, z1 = expf(g1) == 0.f;
+            const bool z0 = g0 < GATED_CUT, z1 = g1 < GATED_CUT;
             const bool odd = __any_sync(0xffffffffu, !(g0 < 88.f) || !(g1 < 88.f));  // NaN, or a decay past fp32
             const long long d0 = z0 ? 0 : doublings(g0), d1 = z1 ? 0 : doublings(g1);
             long long run = d0 + d1;
@@ -350,15 +369,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             }
             g0 = n0;
             g1 = n1;
+            const int s = c % NST;
+            if (c >= NST && !wait(&stage_free[s], ((c / NST) - 1) & 1)) break;
             arrive(&full[s]);
         }
-        // never leave the CTA with loads in flight: wait for every issued stage to land
-        if (lane == 0)
-            for (int c = (issued > NST ? issued - NST : 0); c < issued; ++c) {
-                const uint64_t begin = globaltimer();
-                while (!mbar_try_sleep(&full[c % NST], (c / NST) & 1, 200000u))
-                    if (globaltimer() - begin > ctl.timeout_ns) break;
-            }
         if (a.decay) {
             double s = 0;
             for (int t = t0 + lane; t < te; t += 32) s += (double)gp[(long long)t * a.vg.l];
@@ -366,8 +380,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (lane == 0) a.decay[(long long)seg * BH + bh] = (float)exp(s);
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 2) {
         // ------------------------------------------------------------ products
+        // Two issuing threads, on SM sub-partitions of their own: a product takes one about a hundred cycles
+        // beside the other warps, and the chain of the states' sums need not queue behind the rest.
         if (lane == 0) {
             constexpr uint32_t ID_SC = idesc_bf16_f32(C, C, 0, 0), ID_INTER = idesc_bf16_f32(DZ, C, 0, 0),
                                ID_STATE = idesc_bf16_f32(DZ, DX, 1, 1), ID_INTRA = idesc_bf16_f32(DZ, C, 1, 0);
@@ -382,7 +398,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
                     mma_ss(tmem + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0);
                 }
-                if (inner) {
+                if (INNER) {
                     const uint64_t dw = smem_desc(smem_u32(tile_w(s)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < DZ / 16; ++k) {
@@ -393,64 +409,59 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 mma_commit(scores_done);
                 return true;
             };
-            // Oi's columns hold the second scores of the next chunk: these wait for the rows' readers
-            const bool late = inner && !Lay::A2_OWN;
-            bool ok = totals || nch == 0 || scores(0);
-            auto inter = [&](int c) {
-                const uint64_t dx = smem_desc(smem_u32(tile_x(c % NST)), 16, 1024);
-                const uint32_t sc = tmem + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
+            if (warp == 2) {
+                for (int c = 0; c < nch; ++c) {
+                    const int s = c % NST;
+                    if (!wait1(s_ready, c & 1)) break;  // dS has been read
+                    if (!wait1(yt_ready, c & 1)) break;
+                    tc_fence_after();
+                    const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
 #pragma unroll
-                for (int p = 0; p < NS; ++p)
+                    for (int p = 0; p < 3; ++p) {
+                        const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
 #pragma unroll
-                    for (int k = 0; k < DX / 16; ++k)
-                        mma_ts(tmem + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32),
-                               ID_INTER, p + k > 0);
-            };
-            for (int c = 0; ok && c < nch; ++c) {
-                const int s = c % NST;
-                const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
-                // the state before the chunk is in place, dS has been read
-                if (!(ok = wait1(s_ready, c & 1))) break;
-                if (DOT) {  // the one copy of the state is written again once dS is there: read it before
+                        for (int k = 0; k < C / 16; ++k)
+                            mma_ss(tmem + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0);
+                    }
+                    mma_commit(state_done);
+                    mma_commit(&stage_free[s]);
+                }
+            } else if (!totals) {
+                // the second scores of the next chunk lie in Oi's columns: they wait for the rows' readers
+                constexpr bool late = INNER && !Lay::A2_OWN;
+                bool ok = nch == 0 || scores(0);
+                for (int c = 0; ok && c < nch; ++c) {
+                    const int s = c % NST;
+                    if (!(ok = wait1(s_ready, c & 1))) break;  // the copy of the state before the chunk
                     if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
                     if (late && !(ok = wait1(sc_free, c & 1))) break;
                     tc_fence_after();
-                    inter(c);
-                }
-                if (!(ok = wait1(yt_ready, c & 1))) break;
-                tc_fence_after();
+                    const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024);
+                    const uint32_t sc = tmem + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
+                    for (int p = 0; p < NS; ++p)
+#pragma unroll
+                        for (int k = 0; k < DX / 16; ++k)
+                            mma_ts(tmem + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32),
+                                   ID_INTER, p + k > 0);
+                    if (DOT) mma_commit(inter_done);
+                    if (!late) {
+                        if (!(ok = wait1(sc_free, c & 1))) break;
+                        if (c + 1 < nch && !(ok = scores(c + 1))) break;
+                    }
+                    if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
+                    tc_fence_after();
+                    const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024),
+                                   dp = smem_desc(smem_u32(p_tile + (c & 1) * Lay::P), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        mma_ss(tmem + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0);
-                }
-                mma_commit(state_done);
-                if (totals) {
+                        mma_ss(tmem + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0);
+                    mma_commit(o_done);
                     mma_commit(&stage_free[s]);
-                    continue;
-                }
-                if (!late) {
-                    if (!(ok = wait1(sc_free, c & 1))) break;
-                    if (c + 1 < nch && !(ok = scores(c + 1))) break;
-                }
-                if (!DOT) {
-                    if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
-                    tc_fence_after();
-                    inter(c);
-                }
-                if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
-                tc_fence_after();
-                const uint64_t dp = smem_desc(smem_u32(p_tile + (c & 1) * Lay::P), 16, 1024);
-#pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    mma_ss(tmem + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0);
-                mma_commit(o_done);
-                mma_commit(&stage_free[s]);
-                if (late && c + 1 < nch) {
-                    if (!(ok = wait1(o_free, c & 1))) break;
-                    if (!(ok = scores(c + 1))) break;
+                    if (late && c + 1 < nch) {
+                        if (!(ok = wait1(o_free, c & 1))) break;
+                        if (!(ok = scores(c + 1))) break;
+                    }
                 }
             }
             // every product issued above has completed before TMEM is released
@@ -465,28 +476,36 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         constexpr int G = DX / 8, RG = 256 / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG, ..
         const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
         const int ta = 16 * q4 + (lane >> 2), tb = ta + 8, cpos = lane & 3;
-        bool ok = true;
-        for (int c = 0; c < nch; ++c) {
+        // the rows of a chunk are stored during the next one, between its Y~ and its P
+        const int passes = DOT || totals || nch == 0 ? nch : nch + 1;
+        for (int c = 0; c < passes; ++c) {
             const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
             const Weights &w = weights[c % GT_SLOTS];
-            if (!(ok = wait(&full[s], (c / NST) & 1))) break;
-            if (c > 0 && !(ok = wait(state_done, (c - 1) & 1))) break;  // Y~ of the chunk before has been read
-            const uint8_t *src = tile_y(s) + off;
-            uint4 v[NR];
+            if (c < nch) {
+            if (!wait(&full[s], (c / NST) & 1)) break;
+            if (c > 0 && !wait(state_done, (c - 1) & 1)) break;  // Y~ of the chunk before has been read
+            // Loops over a chunk stay rolled where registers allow: the roles' code together is more than the
+            // instruction caches next to the schedulers hold.
+#pragma unroll 1
+            for (int n = 0; n < NR; n += 2) {
+                const uint8_t *const src = tile_y(s) + off + n * RG * 128;
+                uint8_t *const dst = yt + off + n * RG * 128;
+                uint4 v[2];
 #pragma unroll
-            for (int n = 0; n < NR; ++n) v[n] = *(const uint4 *)(src + n * RG * 128);
+                for (int m = 0; m < 2; ++m) v[m] = *(const uint4 *)(src + m * RG * 128);
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const int r = rg + n * RG;
-                const Ch<2> kw = all<2>(w.kw[r]);
-                uint32_t u[4] = {v[n].x, v[n].y, v[n].z, v[n].w}, hi[4], mid[4], lo[4];
-                if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
+                for (int m = 0; m < 2; ++m) {
+                    const int r = rg + (n + m) * RG;
+                    const Ch<2> kw = all<2>(w.kw[r]);
+                    uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w}, hi[4], mid[4], lo[4];
+                    if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
 #pragma unroll
-                for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
-                uint8_t *d = yt + off + n * RG * 128;
-                *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                *(uint4 *)(d + 2 * Lay::X) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
+                    uint8_t *const d = dst + m * RG * 128;
+                    *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *(uint4 *)(d + 2 * Lay::X) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             if (nv < C)
                 for (int e = ft; e < (C - nv) * (DZ / 8); e += 256) {
@@ -496,27 +515,34 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             fence_async_smem();
             arrive(yt_ready);
             if (totals) continue;
-            if (!DOT && c > 0) {  // the other half of the rows of the chunk before
-                if (!(ok = wait(o_done, (c - 1) & 1))) break;
+            }
+            if (!DOT && c > 0) {
+                if (!wait(o_done, (c - 1) & 1)) break;
                 tc_fence_after();
                 rows(c - 1, 32 * half + 16);
+                if (c == nch) break;
             }
-            if (!(ok = wait(scores_done, c & 1))) break;
+            if (!wait(scores_done, c & 1)) break;
             tc_fence_after();
-            uint32_t r1[32], r2[32];  // the first 16
-            tmem_ld16x256_x4(tmem + Lay::T_A + ((uint32_t)(32 * q4) << 16) + 32 * half, r1);
-            if (inner) tmem_ld16x256_x4(tmem + Lay::T_A2 + ((uint32_t)(32 * q4) << 16) + 32 * half, r2);
-            tmem_wait_ld();
-            tc_fence_before();
-            arrive(sc_free);
             const float2 ga = w.row[ta], gb = w.row[tb];
             // columns of a row that count, from the row itself towards the sweep's start
             const uint32_t na = ta < nv ? (rev ? nv - ta : ta + 1) : 0, nb = tb < nv ? (rev ? nv - tb : tb + 1) : 0;
-            float sa = 0.f, sb = 0.f, sc[8];
+            const float ps = a.yscale * a.oscale;
+            float sa = 0.f, sb = 0.f, sc[INNER ? 8 : 1];
             uint8_t *const pt = p_tile + (c & 1) * Lay::P;
+#pragma unroll(INNER ? 2 : 1)
+            for (int k2 = 0; k2 < 2; ++k2) {
+            uint32_t r1[8], r2[8];
+            tmem_ld16x256_x2(tmem + Lay::T_A + lanes + 32 * half + 16 * k2, r1);
+            if (INNER) tmem_ld16x256_x2(tmem + Lay::T_A2 + lanes + 32 * half + 16 * k2, r2);
+            tmem_wait_ld();
+            if (k2 == 1) {
+                tc_fence_before();
+                arrive(sc_free);
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int col = 32 * half + 8 * k + 2 * cpos;
+            for (int kk = 0; kk < 2; ++kk) {
+                const int k = 2 * k2 + kk, col = 32 * half + 8 * k + 2 * cpos;
                 const float4 gc = *(const float4 *)&w.row[col];  // of col and col + 1
                 float p[4];
 #pragma unroll
@@ -525,10 +551,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     const float2 gr = u < 2 ? ga : gb;
                     const bool in = (uint32_t)(rev ? cu - row : row - cu) < (u < 2 ? na : nb);
                     const float wt = ex2((gr.x - (u & 1 ? gc.z : gc.x)) + (gr.y - (u & 1 ? gc.w : gc.y)));
-                    const float x = __uint_as_float(r1[4 * k + u]) * wt;
-                    p[u] = in ? a.yscale * x : 0.f;
-                    if (inner) {
-                        const float y = in && cu != row ? a.oscale * x * __uint_as_float(r2[4 * k + u]) : 0.f;
+                    const float x = ps * (__uint_as_float(r1[4 * kk + u]) * wt);
+                    p[u] = in ? x : 0.f;
+                    if (INNER) {
+                        const float y = in && cu != row ? x * __uint_as_float(r2[4 * kk + u]) : 0.f;
                         if (u < 2) sa += y;
                         else sb += y;
                         if (u < 2) sc[2 * k + u] = y;
@@ -539,9 +565,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 *(uint32_t *)(pt + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = pack_bf16x2(p[0], p[1]);
                 *(uint32_t *)(pt + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = pack_bf16x2(p[2], p[3]);
             }
+            }
             fence_async_smem();
             arrive(p_ready + (c & 1));
-            if (inner) {
+            if (INNER) {
                 sa += __shfl_xor_sync(0xffffffffu, sa, 1);
                 sb += __shfl_xor_sync(0xffffffffu, sb, 1);
                 sa += __shfl_xor_sync(0xffffffffu, sa, 2);
@@ -566,10 +593,6 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 const int col = 32 * half + 8 * (at >> 1) + 2 * cpos + (at & 1);
                 if (col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
             }
-        }
-        if (!DOT && !totals && ok && nch > 0 && wait(o_done, (nch - 1) & 1)) {
-            tc_fence_after();
-            rows(nch - 1, 32 * half + 16);
         }
     } else if (warp >= ST0) {
         // ------------------------------------------------------------ the state, and the rows
@@ -642,25 +665,23 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             tc_fence_after();
             const float da = w.a, em = w.em;
             // next to 1 by the decay minus 1, whose rounding does not grow with the chunks
-            const bool near = da > 0.5f, none = da == 0.f;
-            const Ch<2> m = all<2>(near ? em : da);
+            const bool near = da > 0.5f;
+            const Ch<2> m = all<2>(near ? em : da), one = all<2>(near ? 1.f : 0.f);
+            if (da == 0.f)  // forgets infinities and NaN too
+#pragma unroll
+                for (int i = 0; i < NX / 2; ++i) S[i] = all<2>(0.f);
 #pragma unroll
             for (int i = 0; i < NX; i += 16) {
                 uint32_t d[16];
                 tmem_ld16(tmem + lanes + Lay::T_DS + half * NX + i, d);
                 tmem_wait_ld();
-                if (none) {
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) S[(i + u) / 2].v[u & 1] = __uint_as_float(d[u]);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        Ch<2> &x = S[i / 2 + u];
-                        const Ch<2> ds{{__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])}};
-                        x = fma(x, m, near ? add(x, ds) : ds);
-                    }
+                for (int u = 0; u < 8; ++u) {
+                    Ch<2> &x = S[i / 2 + u];
+                    x = fma(x, m, fma(x, one, Ch<2>{{__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])}}));
                 }
             }
+            if (DOT && !(ok = wait(inter_done, c & 1))) break;  // the copy has been read
             copy(c + 1);
             if (totals) continue;
             if (!(ok = wait(o_done, c & 1))) break;
@@ -705,23 +726,23 @@ bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, i
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DX, int DZ, bool DOT> int launch_dims(const GtArgs &a, cudaStream_t stream)
+template <int DX, int DZ, bool DOT, bool INNER> int launch_dims(const GtArgs &a, cudaStream_t stream)
 {
     using Lay = GtLayout<DX, DZ, DOT>;
     static std::atomic<uint64_t> done{0};  // devices whose limit is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LA_ERR_CUDA;
     if (dev >= 64 || !(done.load() >> dev & 1)) {
-        const int rc = status_of(cudaFuncSetAttribute(gated_tc_kernel<DX, DZ, DOT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC));
+        const int rc = status_of(cudaFuncSetAttribute(gated_tc_kernel<DX, DZ, DOT, INNER>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC));
         if (rc != LA_OK) return rc;
         if (dev < 64) done |= 1ull << dev;
     }
-    return launch(gated_tc_kernel<DX, DZ, DOT>, dim3((unsigned)(a.B * a.H * a.nseg)), GT_THREADS, (size_t)Lay::ALLOC, stream, a);
+    return launch(gated_tc_kernel<DX, DZ, DOT, INNER>, dim3((unsigned)(a.B * a.H * a.nseg)), GT_THREADS, (size_t)Lay::ALLOC, stream, a);
 }
-template <bool DOT> int launch_dot(const GtArgs &a, int dx, int dz, cudaStream_t s)
+template <bool DOT, bool INNER> int launch_dot(const GtArgs &a, int dx, int dz, cudaStream_t s)
 {
-    if (dx == 64) return dz == 64 ? launch_dims<64, 64, DOT>(a, s) : launch_dims<64, 128, DOT>(a, s);
-    return dz == 64 ? launch_dims<128, 64, DOT>(a, s) : launch_dims<128, 128, DOT>(a, s);
+    if (dx == 64) return dz == 64 ? launch_dims<64, 64, DOT, INNER>(a, s) : launch_dims<64, 128, DOT, INNER>(a, s);
+    return dz == 64 ? launch_dims<128, 64, DOT, INNER>(a, s) : launch_dims<128, 128, DOT, INNER>(a, s);
 }
 
 struct Operand {
@@ -732,6 +753,7 @@ struct Operand {
 
 struct Pass {
     Operand x, y, z, w;  // x.p NULL: totals; w.p NULL: no DOT
+    bool inner = false;
     GtArgs a = {};
 };
 
@@ -754,10 +776,10 @@ int launch_pass(const GatedArgs &p, Pass &s)
         a.sx = p.H / s.x.n;
         if (!map4(&a.mx, s.x.p, s.x.v, p.B, s.x.n, p.L, s.x.d)) return LA_ERR_CUDA;
     }
-    if (!s.w.p) return launch_dot<false>(a, s.y.d, s.z.d, p.stream);
+    if (!s.w.p) return launch_dot<false, false>(a, s.y.d, s.z.d, p.stream);
     a.sw = p.H / s.w.n;
     if (!map4(&a.mw, s.w.p, s.w.v, p.B, s.w.n, p.L, s.w.d)) return LA_ERR_CUDA;
-    return launch_dot<true>(a, s.y.d, s.z.d, p.stream);
+    return s.inner ? launch_dot<true, true>(a, s.y.d, s.z.d, p.stream) : launch_dot<true, false>(a, s.y.d, s.z.d, p.stream);
 }
 
 bool tc_dim(int d) { return d == 64 || d == 128; }
@@ -900,7 +922,7 @@ int gated_tc_bwd(const GatedArgs &p)
     s.a.out = p.dq; s.a.vo = p.vdq;
     if (dg) {
         s.w = q;
-        s.a.inner = 1;
+        s.inner = true;
         s.a.dot = ws + w.r; s.a.dotc = ws + w.c + 4 * heads * p.L;
         s.a.anchors = ws + w.S;
     }

@@ -273,6 +273,13 @@ LA_DEV void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[32])  // fills r[0..1
         : "r"(taddr)
         : "memory");
 }
+LA_DEV void tmem_ld16x256_x2(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
 LA_DEV void tmem_ld16x256_x1(uint32_t taddr, uint32_t (&r)[4])
 {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
