@@ -382,12 +382,15 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         }
     } else if (warp == 1 || warp == 2) {
         // ------------------------------------------------------------ products
-        // Two issuing threads, on SM sub-partitions of their own: a product takes one about a hundred cycles
-        // beside the other warps, and the chain of the states' sums need not queue behind the rest.
-        if (lane == 0) {
+        // Two issuing warps, on SM sub-partitions of their own: a product takes one about a hundred cycles
+        // beside the other warps, and the chain of the states' sums need not queue behind the rest. The
+        // whole warp runs the loop and one lane of it issues, so that descriptors stay in uniform registers.
+        {
+            const uint32_t one = elect_one(), tm = __reduce_or_sync(0xffffffffu, tmem);
+            const int nch_u = (int)__reduce_or_sync(0xffffffffu, (uint32_t)nch);
             constexpr uint32_t ID_SC = idesc_bf16_f32(C, C, 0, 0), ID_INTER = idesc_bf16_f32(DZ, C, 0, 0),
                                ID_STATE = idesc_bf16_f32(DZ, DX, 1, 1), ID_INTRA = idesc_bf16_f32(DZ, C, 1, 0);
-            auto wait1 = [&](uint64_t *bar, uint32_t parity) { return wait_long(bar, parity, ctl); };
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_long(bar, parity, ctl)) != 0; };
             auto scores = [&](int c) {
                 const int s = c % NST;
                 if (!wait1(&full[s], (c / NST) & 1)) return false;
@@ -396,21 +399,21 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
 #pragma unroll
                 for (int k = 0; k < DX / 16; ++k) {
                     const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
-                    mma_ss(tmem + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0);
+                    mma_ss_if(tm + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0, one);
                 }
                 if (INNER) {
                     const uint64_t dw = smem_desc(smem_u32(tile_w(s)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < DZ / 16; ++k) {
                         const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
-                        mma_ss(tmem + Lay::T_A2, desc_add(dw, o), desc_add(dz, o), ID_SC, k > 0);
+                        mma_ss_if(tm + Lay::T_A2, desc_add(dw, o), desc_add(dz, o), ID_SC, k > 0, one);
                     }
                 }
-                mma_commit(scores_done);
+                mma_commit_if(scores_done, one);
                 return true;
             };
             if (warp == 2) {
-                for (int c = 0; c < nch; ++c) {
+                for (int c = 0; c < nch_u; ++c) {
                     const int s = c % NST;
                     if (!wait1(s_ready, c & 1)) break;  // dS has been read
                     if (!wait1(yt_ready, c & 1)) break;
@@ -421,33 +424,33 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                         const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
 #pragma unroll
                         for (int k = 0; k < C / 16; ++k)
-                            mma_ss(tmem + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0);
+                            mma_ss_if(tm + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0, one);
                     }
-                    mma_commit(state_done);
-                    mma_commit(&stage_free[s]);
+                    mma_commit_if(state_done, one);
+                    mma_commit_if(&stage_free[s], one);
                 }
             } else if (!totals) {
                 // the second scores of the next chunk lie in Oi's columns: they wait for the rows' readers
                 constexpr bool late = INNER && !Lay::A2_OWN;
-                bool ok = nch == 0 || scores(0);
-                for (int c = 0; ok && c < nch; ++c) {
+                bool ok = nch_u == 0 || scores(0);
+                for (int c = 0; ok && c < nch_u; ++c) {
                     const int s = c % NST;
                     if (!(ok = wait1(s_ready, c & 1))) break;  // the copy of the state before the chunk
                     if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
                     if (late && !(ok = wait1(sc_free, c & 1))) break;
                     tc_fence_after();
                     const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024);
-                    const uint32_t sc = tmem + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
+                    const uint32_t sc = tm + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
 #pragma unroll
                     for (int p = 0; p < NS; ++p)
 #pragma unroll
                         for (int k = 0; k < DX / 16; ++k)
-                            mma_ts(tmem + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32),
-                                   ID_INTER, p + k > 0);
-                    if (DOT) mma_commit(inter_done);
+                            mma_ts_if(tm + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32),
+                                   ID_INTER, p + k > 0, one);
+                    if (DOT) mma_commit_if(inter_done, one);
                     if (!late) {
                         if (!(ok = wait1(sc_free, c & 1))) break;
-                        if (c + 1 < nch && !(ok = scores(c + 1))) break;
+                        if (c + 1 < nch_u && !(ok = scores(c + 1))) break;
                     }
                     if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
                     tc_fence_after();
@@ -455,17 +458,17 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                                    dp = smem_desc(smem_u32(p_tile + (c & 1) * Lay::P), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        mma_ss(tmem + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0);
-                    mma_commit(o_done);
-                    mma_commit(&stage_free[s]);
-                    if (late && c + 1 < nch) {
+                        mma_ss_if(tm + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0, one);
+                    mma_commit_if(o_done, one);
+                    mma_commit_if(&stage_free[s], one);
+                    if (late && c + 1 < nch_u) {
                         if (!(ok = wait1(o_free, c & 1))) break;
                         if (!(ok = scores(c + 1))) break;
                     }
                 }
             }
             // every product issued above has completed before TMEM is released
-            mma_commit(drain);
+            mma_commit_if(drain, one);
             const uint64_t begin = globaltimer();
             while (!mbar_try_sleep(drain, 0, 200000u))
                 if (globaltimer() - begin > ctl.timeout_ns) break;

@@ -191,6 +191,38 @@ LA_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t 
         "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+// The same for a whole warp, of which the lane with `one` set issues (elect_one): a loop that the warp runs
+// together keeps the descriptors in uniform registers.
+LA_DEV uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r;
+}
+LA_DEV void mma_ss_if(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one)
+{
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
+}
+LA_DEV void mma_ts_if(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one)
+{
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
+}
+LA_DEV void mma_commit_if(uint64_t *bar, uint32_t one)
+{
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_u32(bar)),
+        "r"(one)
+        : "memory");
+}
 // the mbarrier arrives once every tcgen05 op issued so far by this thread has completed
 LA_DEV void mma_commit(uint64_t *bar)
 {
