@@ -55,7 +55,7 @@ constexpr int GT_SLOTS = 8;   // ring of the chunks' weights
 constexpr int PY0 = 4, ST0 = 12;  // first warp of each group of eight
 
 struct GtArgs {
-    CUtensorMap mx, my, mz, mw;
+    CUtensorMap mx, my, mz, mw, mo;
     const float *g;
     View vg, vo;
     void *out;
@@ -82,7 +82,7 @@ struct GtArgs {
 constexpr float GT_CUT = 16384.f;  // doublings that a decay of 0 counts for in G: no pair reaches across
 
 struct Weights {          // of one chunk
-    float2 row[GT_C];     // G (-G in reverse) in doublings, hi and lo
+    float hi[GT_C], lo[GT_C];  // G (-G in reverse) in doublings
     float kw[GT_C];       // of Y's rows (f, or e in reverse), times yscale
     float rw[GT_C];       // of the inter rows (e, or f in reverse), times oscale
     float a, em, pad[2];  // decay over the chunk, and that minus 1
@@ -102,9 +102,12 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr int X = GT_C * DX * 2, Z = GT_C * DZ * 2, W = DOT ? Z : 0;
     static constexpr int STAGE = 2 * X + Z + W;
     static constexpr int YT = 3 * X, P = GT_C * GT_C * 2;
-    static constexpr int FIXED = YT + 2 * P + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
+    static constexpr int PS = DOT ? 2 : 1;           // places of P
+    static constexpr int OUT = 16 * (DZ / 4) * 2;    // a warp's 16 rows of its quadrant's channels
+    static constexpr int OUTS = 16 * OUT;            // 16 warps, or 8 with two each
+    static constexpr int FIXED = YT + PS * P + OUTS + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
     static constexpr int STAGES = (232448 - FIXED) / STAGE >= 4 ? 4 : (232448 - FIXED) / STAGE;
-    static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_W = OFF_P + 2 * P,
+    static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_O = OFF_P + PS * P, OFF_W = OFF_O + OUTS,
                          OFF_BAR = OFF_W + GT_SLOTS * (int)sizeof(Weights), ALLOC = OFF_BAR + 256 + 1024;
     // TMEM columns
     // one part: two copies of the state in turn, so that the next one need not wait for the inter product
@@ -114,13 +117,8 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr bool A2_OWN = T_A + 128 <= 512;
     static constexpr uint32_t T_A2 = A2_OWN ? T_A + 64 : T_OI;
     static_assert(T_A + 64 <= 512 && ALLOC <= 232448 && STAGES >= 2, "fits");
-    static_assert(STAGE % 1024 == 0 && YT % 1024 == 0, "swizzle atoms");
+    static_assert(STAGE % 1024 == 0 && YT % 1024 == 0 && OUT % 512 == 0, "swizzle atoms");
 };
-
-__device__ __forceinline__ uint32_t pair_at(const uint8_t *tile, int row, int c)  // channels c, c + 1 of a swizzled tile
-{
-    return *(const uint32_t *)(tile + (c >> 6) * (GT_C * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2);
-}
 
 // Two values in three bf16 parts each: hi + mid + lo = x to 2^-24.
 __device__ __forceinline__ Ch<2> less(const Ch<2> &x, uint32_t part)
@@ -144,7 +142,7 @@ __device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, volatil
 }
 __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, const Ctl &ctl)
 {
-    if (mbar_try_sleep(bar, parity, 200000u)) return true;
+    if (mbar_try(bar, parity)) return true;
     return wait_longer(bar, parity, ctl.abort, ctl.err, ctl.timeout_ns);
 }
 
@@ -158,7 +156,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     Weights *const weights = (Weights *)(sm + Lay::OFF_W);
     uint64_t *const bars = (uint64_t *)(sm + Lay::OFF_BAR);
     uint64_t *const full = bars, *const stage_free = full + NST, *const yt_ready = stage_free + NST, *const state_done = yt_ready + 1,
-             *const s_ready = state_done + 1, *const scores_done = s_ready + 1, *const sc_free = scores_done + 1,
+             *const s_ready = state_done + 1, *const scores_done = s_ready + 2, *const sc_free = scores_done + 1,
              *const p_ready = sc_free + 1, *const o_done = p_ready + 2, *const o_free = o_done + 1,
              *const inter_done = o_free + 1, *const drain = inter_done + 1;
     uint32_t *const tmem_slot = (uint32_t *)(sm + Lay::OFF_BAR + 224);
@@ -187,13 +185,16 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         }
         mbar_init(yt_ready, 8);
         mbar_init(state_done, 1);
+        // by chunks in turn: the issuer of the inter products may be a whole phase behind that of dS, and of two
+        // completed phases of one barrier a waiter could not tell the first
         mbar_init(s_ready, 8);
+        mbar_init(s_ready + 1, 8);
         mbar_init(scores_done, 1);
         mbar_init(sc_free, 8);
         mbar_init(p_ready, 8);  // by chunks in turn: P of the next one may be done before this one's is awaited
         mbar_init(p_ready + 1, 8);
         mbar_init(o_done, 1);
-        mbar_init(o_free, DOT ? 8 : 16);
+        mbar_init(o_free, 16);  // 16 rows of a quadrant each
         mbar_init(inter_done, 1);
         mbar_init(drain, 2);
         *abort_flag = 0;
@@ -210,85 +211,112 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // Rows first .. first + N - 1 of the sweep's chunk c, the channels of this warp's TMEM quadrant: the inter rows
-    // weighted, the intra rows added, stored; with DOT the inter rows' products with W's.
-    const int q4 = warp & 3, j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
-    const bool live = DZ == 128 || lane < 16;
+    // Rows first .. first + 15 of the sweep's chunk c, the channels of this warp's TMEM quadrant: the inter rows
+    // weighted, the intra rows added, stored; with DOT the inter rows' products with W's. Lane l reads channel
+    // l / 4 of each block of 8 and rows 2 (l % 4) and the next one of two blocks: pairs of rows, which stmatrix
+    // turns into rows of channels (two-byte stores from a lane a channel took ten times the instructions).
+    constexpr int HALVES = DZ / 64;  // blocks of 16 channels of a quadrant
+    const int q4 = warp & 3, cpos = lane & 3;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-    const long long out0 = row_of(a.vo, b, h, 0) + j;
-    const uint32_t step_o = (uint32_t)a.vo.l * (a.out_f32 ? 4 : 2);
-    auto rows = [&](int c, int first) {
-        constexpr int RB = 8, N = DOT ? 32 : 16;  // 8 rows at a time, by what the registers hold
+    const long long out0 = row_of(a.vo, b, h, 0);
+    // block of 8 rows and 8 channels that this lane addresses (of four, then the next 8 rows)
+    const int at_row = (lane & 7) + (DZ == 64 ? 8 * (lane >> 4) : 0),
+              at_ch = DZ == 64 ? (lane >> 3) & 1 : lane >> 3;
+    // 64- or 32-byte rows of the warp's own tile, in the TMA's swizzle for them
+    const uint32_t o_tile = smem_u32(sm + Lay::OFF_O) + (DOT ? 2 * ((warp - ST0) & 7) : (warp - PY0) & 15) * Lay::OUT;
+    const uint32_t o_at = at_row * (DZ / 2) + ((at_ch ^ (DZ == 64 ? (at_row >> 2) & 1 : (at_row >> 1) & 3)) << 4);
+    auto rows = [&](int c, int first, int place) {
         const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
         const Weights &w = weights[c % GT_SLOTS];
-#pragma unroll 1
-        for (int k = 0; k < N / RB; ++k) {
-            const int i0 = first + RB * k;
-            uint32_t oi[RB], oa[RB];
-            tmem_ld8(tmem + lanes + Lay::T_OI + i0, oi);
-            tmem_ld8(tmem + lanes + Lay::T_OA + i0, oa);
-            tmem_wait_ld();
-            if (k == N / RB - 1) {
-                tc_fence_before();
-                arrive(o_free);
+        uint32_t oi[HALVES][8], oa[HALVES][8];
+#pragma unroll
+        for (int i = 0; i < HALVES; ++i) {
+            tmem_ld16x256_x2(tmem + lanes + ((uint32_t)(16 * i) << 16) + Lay::T_OI + first, oi[i]);
+            tmem_ld16x256_x2(tmem + lanes + ((uint32_t)(16 * i) << 16) + Lay::T_OA + first, oa[i]);
+        }
+        const float2 rw[2] = {*(const float2 *)&w.rw[first + 2 * cpos], *(const float2 *)&w.rw[first + 8 + 2 * cpos]};
+        if (lane == 0) tma_wait_read_all();  // the tile's last store has read it
+        tmem_wait_ld();
+        tc_fence_before();
+        arrive(o_free);
+        Ch<2> dot[2] = {all<2>(0.f), all<2>(0.f)};
+        uint32_t wt[HALVES][4];
+        if (DOT) {
+            // W's blocks as O's: channels of the quadrant, rows first + 8 k
+#pragma unroll
+            for (int k = 0; k < HALVES; ++k) {
+                const int t = first + 8 * k + at_row, cg = (DZ / 32) * q4 + at_ch;
+                ldmatrix_t(smem_u32(tile_w(s)) + (cg >> 3) * C * 128 + t * 128 + (((cg & 7) ^ (t & 7)) << 4), wt[k]);
             }
-            float dot[RB];
-            const int lim = live ? nv - i0 : 0;
+        }
+        Ch<2> y[HALVES][4];  // [][2 k + g]: rows 8 k .., channels 8 g ..
 #pragma unroll
-            for (int i = 0; i < RB; i += 4) {
-                const float4 rw = *(const float4 *)&w.rw[i0 + i];
-                const float r4[4] = {rw.x, rw.y, rw.z, rw.w};
+        for (int i = 0; i < HALVES; ++i)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float x = r4[u] * __uint_as_float(oi[i + u]);
-                    if (DOT) {
-                        const uint32_t q = pair_at(tile_w(s), i0 + i + u, j & ~1);
-                        dot[i + u] = live ? x * ((j & 1) ? bf_hi(q) : bf_lo(q)) : 0.f;
-                    }
-                    oa[i + u] = __float_as_uint(__uint_as_float(oa[i + u]) + x);
+            for (int e = 0; e < 4; ++e) {
+                const Ch<2> r{{rw[e >> 1].x, rw[e >> 1].y}};
+                const Ch<2> xi{{__uint_as_float(oi[i][2 * e]), __uint_as_float(oi[i][2 * e + 1])}},
+                    xa{{__uint_as_float(oa[i][2 * e]), __uint_as_float(oa[i][2 * e + 1])}};
+                y[i][e] = fma(r, xi, xa);
+                if (DOT) {
+                    const uint32_t u = DZ == 128 ? wt[e >> 1][2 * i + (e & 1)] : wt[0][e];
+                    dot[e >> 1] = fma(mul(r, xi), Ch<2>{{bf_lo(u), bf_hi(u)}}, dot[e >> 1]);
                 }
             }
-            const long long at_o = out0 + (long long)(row0 + i0) * a.vo.l;
-            // 32-bit steps of a row's bytes: one instruction an address
-            if (a.out_f32) {
-                char *const p = (char *)((float *)a.out + at_o);
+        if (first + 16 > nv)  // rows behind the sequence's end are 0
 #pragma unroll
-                for (int i = 0; i < RB; ++i)
-                    if (i < lim) *(float *)(p + (uint64_t)(uint32_t)i * step_o) = __uint_as_float(oa[i]);
+            for (int i = 0; i < HALVES; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (first + 8 * (e >> 1) + 2 * cpos + u >= nv) y[i][e].v[u] = 0.f;
+        if (!a.out_f32) {
+            const uint32_t tile = o_tile + place * Lay::OUT;
+            uint32_t o[HALVES][4];
+#pragma unroll
+            for (int i = 0; i < HALVES; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = pack_bf16x2(y[i][e].v[0], y[i][e].v[1]);
+            __syncwarp();  // lane 0 has waited
+            if constexpr (DZ == 128) {
+                stmatrix_t(tile + o_at, o[0][0], o[0][1], o[1][0], o[1][1]);
+                stmatrix_t(tile + 8 * (DZ / 2) + o_at, o[0][2], o[0][3], o[1][2], o[1][3]);
             } else {
-                char *const p = (char *)((__nv_bfloat16 *)a.out + at_o);
-                if (lim >= RB) {
+                stmatrix_t(tile + o_at, o[0][0], o[0][1], o[0][2], o[0][3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_4d(&a.mo, tile, (DZ / 4) * q4, row0 + first, h, b);
+                tma_commit_group();
+            }
+        } else {
+            float *const p = (float *)a.out + out0 + (DZ / 4) * q4 + (lane >> 2);
 #pragma unroll
-                    for (int i = 0; i < RB; ++i)
-                        *(__nv_bfloat16 *)(p + (uint64_t)(uint32_t)i * step_o) = __float2bfloat16_rn(__uint_as_float(oa[i]));
-                } else {
-#pragma unroll 1
-                    for (int i = 0; i < lim; ++i) {
-                        uint32_t o = 0;
+            for (int i = 0; i < HALVES; ++i)
 #pragma unroll
-                        for (int u = 0; u < RB; ++u) o = u == i ? oa[u] : o;
-                        *(__nv_bfloat16 *)(p + (uint64_t)(uint32_t)i * step_o) = __float2bfloat16_rn(__uint_as_float(o));
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int t = row0 + first + 8 * (e >> 1) + 2 * cpos + u;
+                        if (t < a.L) p[(long long)t * a.vo.l + 16 * i + 8 * (e & 1)] = y[i][e].v[u];
                     }
-                }
-            }
-            if (DOT) {
-                // over the quadrant's channels; a lane goes on with half of the rows each time
-                int r = 0;
+        }
+        if (DOT) {
+            // over the channels: lanes l / 4; a lane goes on with half of its four rows each time
+            float v[4] = {dot[0].v[0], dot[0].v[1], dot[1].v[0], dot[1].v[1]};
+            const bool up = lane & 4, up2 = lane & 8;
 #pragma unroll
-                for (int o = 16, n = RB / 2; n > 0; o >>= 1, n >>= 1) {
-                    const bool up = lane & o;
-#pragma unroll
-                    for (int i = 0; i < RB / 2; ++i)
-                        if (i < n) {
-                            const float send = up ? dot[i] : dot[i + n], keep = up ? dot[i + n] : dot[i];
-                            dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                        }
-                    r += up ? n : 0;
-                }
-                dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
-                dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
-                if (!(lane & 3) && i0 + r < nv) a.dot[((long long)q4 * BH + bh) * a.L + row0 + i0 + r] = dot[0];
+            for (int i = 0; i < 2; ++i) {
+                const float send = up ? v[i] : v[i + 2], keep = up ? v[i + 2] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 4);
             }
+            float d = up2 ? v[1] : v[0];
+            d += __shfl_xor_sync(0xffffffffu, up2 ? v[0] : v[1], 8);
+            d += __shfl_xor_sync(0xffffffffu, d, 16);
+            const int t = first + (up ? 8 : 0) + 2 * cpos + (up2 ? 1 : 0);
+            if (!(lane & 16) && t < nv) a.dot[((long long)q4 * BH + bh) * a.L + row0 + t] = d;
         }
     };
 
@@ -356,7 +384,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 // hi and lo together hold differences of rows to 2^-24 of what lies between two cuts
                 const float g2 = (float)G * UNIT, rest = (float)(G - (long long)(float)G) * UNIT;
                 const float cut = -GT_CUT * (float)id, hi = cut + g2, lo = (g2 - (hi - cut)) + rest;
-                w.row[2 * lane + i] = make_float2(sign * hi + bad, sign * lo);
+                w.hi[2 * lane + i] = sign * hi + bad;
+                w.lo[2 * lane + i] = sign * lo;
                 const float start = id == 0 ? exp2f(g2) * fmaf(rest, 0.693147181f, 1.f) : 0.f;
                 const float end = id == cuts ? exp2f((float)(whole - G) * UNIT) : 0.f;
                 w.kw[2 * lane + i] = a.yscale * (rev ? start : end) + bad;
@@ -415,7 +444,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (warp == 2) {
                 for (int c = 0; c < nch_u; ++c) {
                     const int s = c % NST;
-                    if (!wait1(s_ready, c & 1)) break;  // dS has been read
+                    if (!wait1(s_ready + (c & 1), (c >> 1) & 1)) break;  // dS has been read
                     if (!wait1(yt_ready, c & 1)) break;
                     tc_fence_after();
                     const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
@@ -435,7 +464,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 bool ok = nch_u == 0 || scores(0);
                 for (int c = 0; ok && c < nch_u; ++c) {
                     const int s = c % NST;
-                    if (!(ok = wait1(s_ready, c & 1))) break;  // the copy of the state before the chunk
+                    if (!(ok = wait1(s_ready + (c & 1), (c >> 1) & 1))) break;  // the copy of the state before the chunk
                     if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
                     if (late && !(ok = wait1(sc_free, c & 1))) break;
                     tc_fence_after();
@@ -455,7 +484,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
                     tc_fence_after();
                     const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024),
-                                   dp = smem_desc(smem_u32(p_tile + (c & 1) * Lay::P), 16, 1024);
+                                   dp = smem_desc(smem_u32(p_tile + (c % Lay::PS) * Lay::P), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
                         mma_ss_if(tm + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0, one);
@@ -478,7 +507,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         const int pw = warp - PY0, ft = 32 * pw + lane, half = pw >> 2;
         constexpr int G = DX / 8, RG = 256 / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG, ..
         const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
-        const int ta = 16 * q4 + (lane >> 2), tb = ta + 8, cpos = lane & 3;
+        const int ta = 16 * q4 + (lane >> 2), tb = ta + 8;
         // the rows of a chunk are stored during the next one, between its Y~ and its P
         const int passes = DOT || totals || nch == 0 ? nch : nch + 1;
         for (int c = 0; c < passes; ++c) {
@@ -522,64 +551,73 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (!DOT && c > 0) {
                 if (!wait(o_done, (c - 1) & 1)) break;
                 tc_fence_after();
-                rows(c - 1, 32 * half + 16);
+                rows(c - 1, 32 * half + 16, 0);
                 if (c == nch) break;
             }
-            if (!wait(scores_done, c & 1)) break;
+            // (with the rows' products of the chunk before, those of this chunk's scores are done)
+            if ((DOT || c == 0) && !wait(scores_done, c & 1)) break;
             tc_fence_after();
-            const float2 ga = w.row[ta], gb = w.row[tb];
-            // columns of a row that count, from the row itself towards the sweep's start
-            const uint32_t na = ta < nv ? (rev ? nv - ta : ta + 1) : 0, nb = tb < nv ? (rev ? nv - tb : tb + 1) : 0;
-            const float ps = a.yscale * a.oscale;
-            float sa = 0.f, sb = 0.f, sc[INNER ? 8 : 1];
-            uint8_t *const pt = p_tile + (c & 1) * Lay::P;
-#pragma unroll(INNER ? 2 : 1)
-            for (int k2 = 0; k2 < 2; ++k2) {
-            uint32_t r1[8], r2[8];
-            tmem_ld16x256_x2(tmem + Lay::T_A + lanes + 32 * half + 16 * k2, r1);
-            if (INNER) tmem_ld16x256_x2(tmem + Lay::T_A2 + lanes + 32 * half + 16 * k2, r2);
-            tmem_wait_ld();
-            if (k2 == 1) {
-                tc_fence_before();
-                arrive(sc_free);
+            // columns lo <= col < hi of a row count: up to the row itself, or in reverse from it on
+            const int col0 = 32 * half + 2 * cpos;
+            int from[2], to[2];
+            Ch<2> ghi[2], glo[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = r ? tb : ta;
+                from[r] = (rev ? row : 0) - col0;
+                to[r] = (row >= nv ? 0 : rev ? nv : row + 1) - col0;
+                ghi[r] = all<2>(w.hi[row]);
+                glo[r] = all<2>(w.lo[row]);
             }
+            const Ch<2> ps = all<2>(a.yscale * a.oscale), minus = all<2>(-1.f);
+            float sum[2] = {0.f, 0.f}, sc[INNER ? 8 : 1];
+            uint8_t *const pt = p_tile + (c % Lay::PS) * Lay::P;
+            uint32_t r1[32], r2[32];  // the first 16
+            tmem_ld16x256_x4(tmem + Lay::T_A + lanes + 32 * half, r1);
+            if (INNER) tmem_ld16x256_x4(tmem + Lay::T_A2 + lanes + 32 * half, r2);
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive(sc_free);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const int k = 2 * k2 + kk, col = 32 * half + 8 * k + 2 * cpos;
-                const float4 gc = *(const float4 *)&w.row[col];  // of col and col + 1
-                float p[4];
+            for (int k = 0; k < 4; ++k) {
+                const float2 h2 = *(const float2 *)&w.hi[col0 + 8 * k], l2 = *(const float2 *)&w.lo[col0 + 8 * k];
+                const Ch<2> chi{{h2.x, h2.y}}, clo{{l2.x, l2.y}};
+                uint32_t p[2];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int cu = col + (u & 1), row = u < 2 ? ta : tb;
-                    const float2 gr = u < 2 ? ga : gb;
-                    const bool in = (uint32_t)(rev ? cu - row : row - cu) < (u < 2 ? na : nb);
-                    const float wt = ex2((gr.x - (u & 1 ? gc.z : gc.x)) + (gr.y - (u & 1 ? gc.w : gc.y)));
-                    const float x = ps * (__uint_as_float(r1[4 * kk + u]) * wt);
-                    p[u] = in ? x : 0.f;
-                    if (INNER) {
-                        const float y = in && cu != row ? x * __uint_as_float(r2[4 * kk + u]) : 0.f;
-                        if (u < 2) sa += y;
-                        else sb += y;
-                        if (u < 2) sc[2 * k + u] = y;
-                        else sc[2 * k + u - 2] += y;
+                for (int r = 0; r < 2; ++r) {
+                    const int e = 4 * k + 2 * r;
+                    const Ch<2> d = add(fma(chi, minus, ghi[r]), fma(clo, minus, glo[r])), wt{{ex2(d.v[0]), ex2(d.v[1])}};
+                    Ch<2> x = mul(mul(Ch<2>{{__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])}}, wt), ps);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const bool in = 8 * k + u >= from[r] && 8 * k + u < to[r];
+                        if (INNER) {
+                            const bool own = 8 * k + u == (r ? tb : ta) - col0;
+                            const float y = in && !own ? x.v[u] * __uint_as_float(r2[e + u]) : 0.f;
+                            sum[r] += y;
+                            if (r == 0) sc[2 * k + u] = y;
+                            else sc[2 * k + u] += y;
+                        }
+                        x.v[u] = in ? x.v[u] : 0.f;
                     }
+                    p[r] = pack_bf16x2(x.v[0], x.v[1]);
                 }
                 const int ch = 4 * half + k;
-                *(uint32_t *)(pt + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = pack_bf16x2(p[0], p[1]);
-                *(uint32_t *)(pt + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = pack_bf16x2(p[2], p[3]);
-            }
+                *(uint32_t *)(pt + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = p[0];
+                *(uint32_t *)(pt + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = p[1];
             }
             fence_async_smem();
             arrive(p_ready + (c & 1));
             if (INNER) {
-                sa += __shfl_xor_sync(0xffffffffu, sa, 1);
-                sb += __shfl_xor_sync(0xffffffffu, sb, 1);
-                sa += __shfl_xor_sync(0xffffffffu, sa, 2);
-                sb += __shfl_xor_sync(0xffffffffu, sb, 2);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+                }
                 float *const rp = a.dot + ((long long)(4 + half) * BH + bh) * a.L + row0;
                 if (cpos == 0) {
-                    if (ta < nv) rp[ta] = sa;
-                    if (tb < nv) rp[tb] = sb;
+                    if (ta < nv) rp[ta] = sum[0];
+                    if (tb < nv) rp[tb] = sum[1];
                 }
                 int at = 0;
 #pragma unroll
@@ -600,6 +638,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     } else if (warp >= ST0) {
         // ------------------------------------------------------------ the state, and the rows
         const int half = (warp - ST0) >> 2;
+        const int j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
+        const bool live = DZ == 128 || lane < 16;
         constexpr int NX = DX / 2;  // x channels half * NX ..
         const long long n_state = (long long)DX * DZ;
         const long long at = (a.by_seg ? (long long)seg * BH + bh : (long long)slot * a.H + h) * n_state;
@@ -649,7 +689,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 tmem_wait_st();
             }
             tc_fence_before();
-            arrive(s_ready);
+            arrive(s_ready + (c & 1));
         };
         const int first_anchor = a.anchors ? t0 / (a.anchor_chunks * C) : 0;
         const int anchors_here = a.anchors ? (t1 - t0 + a.anchor_chunks * C - 1) / (a.anchor_chunks * C) : 0;
@@ -689,7 +729,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (totals) continue;
             if (!(ok = wait(o_done, c & 1))) break;
             tc_fence_after();
-            rows(c, 32 * half);
+            rows(c, 32 * half, 0);
+            if (DOT) rows(c, 32 * half + 16, 1);
             if (DOT) arrive(&stage_free[s]);
         }
         if (ok) {
@@ -698,16 +739,17 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 if (seg == a.nseg - 1) anchor(a.n_anchors);
             }
             if (a.fin && (a.by_seg || slot >= 0)) store(a.fin + at);
-            // rows behind the sequence's end
+            // rows behind the chunks
             if (!totals && a.out)
-                for (int t = te + (warp - ST0); t < t1; t += 8)
+                for (int t = t0 + nch * C + (warp - ST0); t < t1; t += 8)
                     for (int i = lane; i < DZ; i += 32) {
-                        const long long o = row_of(a.vo, b, h, t) + i;
+                        const long long o = out0 + (long long)t * a.vo.l + i;
                         if (a.out_f32) ((float *)a.out)[o] = 0.f;
                         else ((__nv_bfloat16 *)a.out)[o] = __float2bfloat16_rn(0.f);
                     }
         }
     }
+    if (warp >= PY0 && lane == 0) tma_wait_read_all();  // the stores have read their tiles
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -717,7 +759,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
 // ---- host side -----------------------------------------------------------------------------------
 // [B, n, L, d] bf16 by strides; boxes of 64 channels x 64 rows of one head, 128-byte swizzle, rows past L
 // zero.
-bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, int d)
+bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, int d, bool out = false)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -725,8 +767,14 @@ bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, i
     auto stride = [&](long long s, int len) { return (cuuint64_t)(len > 1 ? s * 2 : d * 2); };
     cuuint64_t strides[3] = {stride(v.l, L), stride(v.h, n), stride(v.b, B)};
     cuuint32_t box[4] = {64, GT_C, 1, 1}, es[4] = {1, 1, 1, 1};
+    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (out) {  // a warp's 16 rows of a quadrant's channels
+        box[0] = (cuuint32_t)d / 4;
+        box[1] = 16;
+        swizzle = d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+    }
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DX, int DZ, bool DOT, bool INNER> int launch_dims(const GtArgs &a, cudaStream_t stream)
@@ -777,6 +825,7 @@ int launch_pass(const GatedArgs &p, Pass &s)
     if (!map4(&a.my, s.y.p, s.y.v, p.B, s.y.n, p.L, s.y.d) || !map4(&a.mz, s.z.p, s.z.v, p.B, s.z.n, p.L, s.z.d)) return LA_ERR_CUDA;
     if (s.x.p) {
         a.sx = p.H / s.x.n;
+        if (!a.out_f32 && !map4(&a.mo, a.out, a.vo, p.B, p.H, p.L, s.z.d, true)) return LA_ERR_CUDA;
         if (!map4(&a.mx, s.x.p, s.x.v, p.B, s.x.n, p.L, s.x.d)) return LA_ERR_CUDA;
     }
     if (!s.w.p) return launch_dot<false, false>(a, s.y.d, s.z.d, p.stream);
@@ -786,7 +835,6 @@ int launch_pass(const GatedArgs &p, Pass &s)
 }
 
 bool tc_dim(int d) { return d == 64 || d == 128; }
-bool tc_out(const View &v) { return v.l < (1ll << 30); }  // a row's bytes fit 32 bits
 bool tc_view(const void *p, const View &v, int B, int n, int L)
 {
     auto ok = [&](long long s, int len) { return len == 1 || (s > 0 && s < (1ll << 38)); };
@@ -835,14 +883,16 @@ struct TcBwdSpace {
 
 }  // namespace
 
-bool gated_tc_fwd_ok(const GatedArgs &p)
+static bool inputs_ok(const GatedArgs &p)
 {
     return p.dtype == LA_BF16 && tc_dim(p.d) && tc_dim(p.e) && tc_view(p.q, p.vq, p.B, p.H, p.L) &&
-           tc_view(p.k, p.vk, p.B, p.Hk, p.L) && tc_view(p.v, p.vv, p.B, p.Hk, p.L) && tc_out(p.vo);
+           tc_view(p.k, p.vk, p.B, p.Hk, p.L) && tc_view(p.v, p.vv, p.B, p.Hk, p.L);
 }
+bool gated_tc_fwd_ok(const GatedArgs &p) { return inputs_ok(p) && tc_view(p.out, p.vo, p.B, p.H, p.L); }
 bool gated_tc_bwd_ok(const GatedArgs &p)
 {
-    return gated_tc_fwd_ok(p) && tc_view(p.dout, p.vo, p.B, p.H, p.L) && tc_out(p.vdq) && tc_out(p.vdk) && tc_out(p.vdv) &&
+    return inputs_ok(p) && tc_view(p.dout, p.vo, p.B, p.H, p.L) && tc_view(p.dq, p.vdq, p.B, p.H, p.L) &&
+           tc_view(p.dk, p.vdk, p.B, p.Hk, p.L) && tc_view(p.dv, p.vdv, p.B, p.Hk, p.L) &&
            aligned(p.state0, 16) && aligned(p.dstate, 16) && aligned(p.dstate0, 16);
 }
 
