@@ -23,10 +23,12 @@
 // rounding a chunk, and Y~'s three parts hold f Y to 2^-24, so that states are those of fp32 arithmetic. The
 // decays' gradient reads the inter rows, there S too has three parts.
 //
-// Warps (640 threads, one block an SM): 0 loads tiles by TMA into a ring, 3 forms the chunks' weights (64-bit
-// sums); 1 and 2 issue the products; 4-11 form Y~ and P; 12-19 hold the state (S^T, row = lane of
-// their TMEM quadrant, half of the columns each) and write its copy. Both groups store the rows, half
-// each (with DOT the second one all of them, while W's tile is held).
+// Warps (640 threads, one block an SM): 0 loads tiles by TMA into a ring, 2 and 3 form the chunks' weights (64-bit
+// sums), 1 issues the products. The 16 others all do the same, a part each: Y~, the rows of the chunk
+// before, P, the state's update (S^T in registers: a lane of the warp's TMEM quadrant, a quarter of the columns) and
+// its copy. The order hides each product behind a step that does not need it; and warps that run the
+// same steps together share the instructions they fetch (with one group for Y~ and P and one for the state
+// and the rows, fetching was the largest stall, and a chunk took 4,300 cycles).
 //
 // The decays' gradient (DOT) needs R_i = q_i . dq_i and C_j = k_j . dk_j without the rows' own pairs. Over
 // earlier chunks they are the products of the inter rows with a fourth tile (q or k, W); inside the chunk
@@ -52,10 +54,10 @@ namespace {
 constexpr int GT_THREADS = 640;
 constexpr int GT_C = 64;      // rows of a chunk
 constexpr int GT_SLOTS = 8;   // ring of the chunks' weights
-constexpr int PY0 = 4, ST0 = 12;  // first warp of each group of eight
+constexpr int GT_W0 = 4, GT_WORKERS = 16;  // the workers: warps 4 .. 19
 
 struct GtArgs {
-    CUtensorMap mx, my, mz, mw, mo;
+    CUtensorMap mx, my, mz, mw;
     const float *g;
     View vg, vo;
     void *out;
@@ -73,7 +75,7 @@ struct GtArgs {
     int rs, cs;          // element (x channel, z channel) of a stored state
     float *anchors;      // S at the anchors' starts (causal; one more behind the last) or D at their ends
     int anchor_chunks, n_anchors;
-    float *dot;          // DOT: [4][B H][L] inter parts, then (inner) [2] row sums
+    float *dot;          // DOT: [4][B H][L] inter parts, then (inner) [4] row sums
     float *dotc;         // inner: [4][B H][L] column sums
     int *err;
     unsigned long long timeout_ns;
@@ -102,12 +104,11 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr int X = GT_C * DX * 2, Z = GT_C * DZ * 2, W = DOT ? Z : 0;
     static constexpr int STAGE = 2 * X + Z + W;
     static constexpr int YT = 3 * X, P = GT_C * GT_C * 2;
-    static constexpr int PS = DOT ? 2 : 1;           // places of P
-    static constexpr int OUT = 16 * (DZ / 4) * 2;    // a warp's 16 rows of its quadrant's channels
-    static constexpr int OUTS = 16 * OUT;            // 16 warps, or 8 with two each
-    static constexpr int FIXED = YT + PS * P + OUTS + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
+    static constexpr int OUT = 16 * (DZ / 4) * 2;    // a worker's 16 rows of its quadrant's channels
+    static constexpr int OUTS = GT_WORKERS * OUT;
+    static constexpr int FIXED = YT + P + OUTS + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
     static constexpr int STAGES = (232448 - FIXED) / STAGE >= 4 ? 4 : (232448 - FIXED) / STAGE;
-    static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_O = OFF_P + PS * P, OFF_W = OFF_O + OUTS,
+    static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_O = OFF_P + P, OFF_W = OFF_O + OUTS,
                          OFF_BAR = OFF_W + GT_SLOTS * (int)sizeof(Weights), ALLOC = OFF_BAR + 256 + 1024;
     // TMEM columns
     // one part: two copies of the state in turn, so that the next one need not wait for the inter product
@@ -117,7 +118,7 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr bool A2_OWN = T_A + 128 <= 512;
     static constexpr uint32_t T_A2 = A2_OWN ? T_A + 64 : T_OI;
     static_assert(T_A + 64 <= 512 && ALLOC <= 232448 && STAGES >= 2, "fits");
-    static_assert(STAGE % 1024 == 0 && YT % 1024 == 0 && OUT % 512 == 0, "swizzle atoms");
+    static_assert(STAGE % 1024 == 0 && YT % 1024 == 0, "swizzle atoms");
 };
 
 // Two values in three bf16 parts each: hi + mid + lo = x to 2^-24.
@@ -156,8 +157,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     Weights *const weights = (Weights *)(sm + Lay::OFF_W);
     uint64_t *const bars = (uint64_t *)(sm + Lay::OFF_BAR);
     uint64_t *const full = bars, *const stage_free = full + NST, *const yt_ready = stage_free + NST, *const state_done = yt_ready + 1,
-             *const s_ready = state_done + 1, *const scores_done = s_ready + 2, *const sc_free = scores_done + 1,
-             *const p_ready = sc_free + 1, *const o_done = p_ready + 2, *const o_free = o_done + 1,
+             *const s_ready = state_done + 1, *const scores_done = s_ready + 1, *const sc_free = scores_done + 1,
+             *const p_ready = sc_free + 1, *const o_done = p_ready + 1, *const o_free = o_done + 1,
              *const inter_done = o_free + 1, *const drain = inter_done + 1;
     uint32_t *const tmem_slot = (uint32_t *)(sm + Lay::OFF_BAR + 224);
     volatile int *const abort_flag = (volatile int *)(sm + Lay::OFF_BAR + 228);
@@ -181,22 +182,20 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 2);                       // the TMA's bytes, the weights
-            mbar_init(&stage_free[i], totals ? 1 : DOT ? 10 : 2);  // both issuers' products, and the readers of W
+            mbar_init(&stage_free[i], DOT && !totals ? 1 + GT_WORKERS : 1);  // the products, and the readers of W
         }
-        mbar_init(yt_ready, 8);
+        mbar_init(yt_ready, GT_WORKERS);
         mbar_init(state_done, 1);
-        // by chunks in turn: the issuer of the inter products may be a whole phase behind that of dS, and of two
-        // completed phases of one barrier a waiter could not tell the first
-        mbar_init(s_ready, 8);
-        mbar_init(s_ready + 1, 8);
+        // No phase of a barrier completes before everyone has waited for the one before it, or a waiter could take
+        // it for that one: the workers go round together, and each step of theirs needs the issuer's last one.
+        mbar_init(s_ready, GT_WORKERS);
         mbar_init(scores_done, 1);
-        mbar_init(sc_free, 8);
-        mbar_init(p_ready, 8);  // by chunks in turn: P of the next one may be done before this one's is awaited
-        mbar_init(p_ready + 1, 8);
+        mbar_init(sc_free, GT_WORKERS);
+        mbar_init(p_ready, GT_WORKERS);
         mbar_init(o_done, 1);
-        mbar_init(o_free, 16);  // 16 rows of a quadrant each
+        mbar_init(o_free, GT_WORKERS);
         mbar_init(inter_done, 1);
-        mbar_init(drain, 2);
+        mbar_init(drain, 1);
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -211,22 +210,24 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // Rows first .. first + 15 of the sweep's chunk c, the channels of this warp's TMEM quadrant: the inter rows
-    // weighted, the intra rows added, stored; with DOT the inter rows' products with W's. Lane l reads channel
-    // l / 4 of each block of 8 and rows 2 (l % 4) and the next one of two blocks: pairs of rows, which stmatrix
-    // turns into rows of channels (two-byte stores from a lane a channel took ten times the instructions).
-    constexpr int HALVES = DZ / 64;  // blocks of 16 channels of a quadrant
-    const int q4 = warp & 3, cpos = lane & 3;
+    // ---- a worker's place: quadrant q4 of TMEM, part `part` of four of the columns or rows
+    const int q4 = warp & 3, part = (warp - GT_W0) >> 2, cpos = lane & 3;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const long long out0 = row_of(a.vo, b, h, 0);
-    // block of 8 rows and 8 channels that this lane addresses (of four, then the next 8 rows)
-    const int at_row = (lane & 7) + (DZ == 64 ? 8 * (lane >> 4) : 0),
-              at_ch = DZ == 64 ? (lane >> 3) & 1 : lane >> 3;
-    // 64- or 32-byte rows of the warp's own tile, in the TMA's swizzle for them
-    const uint32_t o_tile = smem_u32(sm + Lay::OFF_O) + (DOT ? 2 * ((warp - ST0) & 7) : (warp - PY0) & 15) * Lay::OUT;
-    const uint32_t o_at = at_row * (DZ / 2) + ((at_ch ^ (DZ == 64 ? (at_row >> 2) & 1 : (at_row >> 1) & 3)) << 4);
-    auto rows = [&](int c, int first, int place) {
-        const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
+    constexpr int HALVES = DZ / 64;  // blocks of 16 channels of a quadrant
+    // block of 8 rows and 8 channels that this lane addresses for stmatrix and ldmatrix (of four, then the
+    // next 8 rows), and its place in the worker's tile of 64- or 32-byte rows, free of bank conflicts
+    const int at_row = (lane & 7) + (DZ == 64 ? 8 * (lane >> 4) : 0), at_ch = DZ == 64 ? (lane >> 3) & 1 : lane >> 3;
+    uint8_t *const o_tile = sm + Lay::OFF_O + ((warp - GT_W0) & 15) * Lay::OUT;
+    auto o_place = [](int row, int ch) { return row * (DZ / 2) + ((ch ^ (DZ == 64 ? (row >> 2) & 1 : (row >> 1) & 3)) << 4); };
+
+    // A quarter of the rows of the sweep's chunk c, the channels of the quadrant: the inter rows weighted, the intra
+    // rows added, stored; with DOT the inter rows' products with W's. Lane l reads channel l / 4 of each block
+    // of 8 and rows 2 (l % 4) and the next one of two blocks; stmatrix turns these pairs of rows into rows of
+    // channels, which leave 16 bytes a lane. (Two-byte stores from a lane a channel took ten times the
+    // instructions; TMA stores, 50 cycles of the unit each, were slower than these.)
+    auto rows = [&](int c) {
+        const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0), first = 16 * part;
         const Weights &w = weights[c % GT_SLOTS];
         uint32_t oi[HALVES][8], oa[HALVES][8];
 #pragma unroll
@@ -235,10 +236,6 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             tmem_ld16x256_x2(tmem + lanes + ((uint32_t)(16 * i) << 16) + Lay::T_OA + first, oa[i]);
         }
         const float2 rw[2] = {*(const float2 *)&w.rw[first + 2 * cpos], *(const float2 *)&w.rw[first + 8 + 2 * cpos]};
-        if (lane == 0) tma_wait_read_all();  // the tile's last store has read it
-        tmem_wait_ld();
-        tc_fence_before();
-        arrive(o_free);
         Ch<2> dot[2] = {all<2>(0.f), all<2>(0.f)};
         uint32_t wt[HALVES][4];
         if (DOT) {
@@ -249,6 +246,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 ldmatrix_t(smem_u32(tile_w(s)) + (cg >> 3) * C * 128 + t * 128 + (((cg & 7) ^ (t & 7)) << 4), wt[k]);
             }
         }
+        tmem_wait_ld();
+        tc_fence_before();
+        arrive(o_free);
         Ch<2> y[HALVES][4];  // [][2 k + g]: rows 8 k .., channels 8 g ..
 #pragma unroll
         for (int i = 0; i < HALVES; ++i)
@@ -263,33 +263,28 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     dot[e >> 1] = fma(mul(r, xi), Ch<2>{{bf_lo(u), bf_hi(u)}}, dot[e >> 1]);
                 }
             }
-        if (first + 16 > nv)  // rows behind the sequence's end are 0
-#pragma unroll
-            for (int i = 0; i < HALVES; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        if (first + 8 * (e >> 1) + 2 * cpos + u >= nv) y[i][e].v[u] = 0.f;
         if (!a.out_f32) {
-            const uint32_t tile = o_tile + place * Lay::OUT;
             uint32_t o[HALVES][4];
 #pragma unroll
             for (int i = 0; i < HALVES; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] = pack_bf16x2(y[i][e].v[0], y[i][e].v[1]);
-            __syncwarp();  // lane 0 has waited
+            const uint32_t tile = smem_u32(o_tile) + o_place(at_row, at_ch);
+            __syncwarp();  // the tile's last rows have been read
             if constexpr (DZ == 128) {
-                stmatrix_t(tile + o_at, o[0][0], o[0][1], o[1][0], o[1][1]);
-                stmatrix_t(tile + 8 * (DZ / 2) + o_at, o[0][2], o[0][3], o[1][2], o[1][3]);
+                stmatrix_t(tile, o[0][0], o[0][1], o[1][0], o[1][1]);
+                stmatrix_t(tile + 8 * (DZ / 2), o[0][2], o[0][3], o[1][2], o[1][3]);
             } else {
-                stmatrix_t(tile + o_at, o[0][0], o[0][1], o[0][2], o[0][3]);
+                stmatrix_t(tile, o[0][0], o[0][1], o[0][2], o[0][3]);
             }
-            fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                tma_store_4d(&a.mo, tile, (DZ / 4) * q4, row0 + first, h, b);
-                tma_commit_group();
+            constexpr int PIECES = DZ / 32;  // of 16 bytes in a row
+            const int r = lane / PIECES, p = lane % PIECES;
+            __nv_bfloat16 *const g = (__nv_bfloat16 *)a.out + out0 + (long long)(row0 + first + r) * a.vo.l + (DZ / 4) * q4 + 8 * p;
+#pragma unroll
+            for (int i = 0; i < 16 * PIECES / 32; ++i) {
+                const int rr = r + i * (32 / PIECES);
+                if (first + rr < nv) *(uint4 *)(g + (long long)(i * (32 / PIECES)) * a.vo.l) = *(const uint4 *)(o_tile + o_place(rr, p));
             }
         } else {
             float *const p = (float *)a.out + out0 + (DZ / 4) * q4 + (lane >> 2);
@@ -299,8 +294,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 for (int e = 0; e < 4; ++e)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int t = row0 + first + 8 * (e >> 1) + 2 * cpos + u;
-                        if (t < a.L) p[(long long)t * a.vo.l + 16 * i + 8 * (e & 1)] = y[i][e].v[u];
+                        const int t = first + 8 * (e >> 1) + 2 * cpos + u;
+                        if (t < nv) p[(long long)(row0 + t) * a.vo.l + 16 * i + 8 * (e & 1)] = y[i][e].v[u];
                     }
         }
         if (DOT) {
@@ -343,21 +338,107 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             for (int c = (issued > NST ? issued - NST : 0); c < issued; ++c) {
                 const uint64_t begin = globaltimer();
                 while (!mbar_try_sleep(&full[c % NST], (c / NST) & 1, 200000u))
-                    if (*abort_flag || globaltimer() - begin > ctl.timeout_ns) break;
+                    if (globaltimer() - begin > ctl.timeout_ns) break;
             }
         }
-    } else if (warp == 3) {
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        // The whole warp runs the loop and one lane of it issues, so that descriptors stay in uniform registers (a
+        // product takes 35 cycles to issue instead of 100). In the order in which the workers get ready for them.
+        const uint32_t one = elect_one(), tm = __reduce_or_sync(0xffffffffu, tmem);
+        const int n = (int)__reduce_or_sync(0xffffffffu, (uint32_t)nch);
+        constexpr uint32_t ID_SC = idesc_bf16_f32(C, C, 0, 0), ID_INTER = idesc_bf16_f32(DZ, C, 0, 0),
+                           ID_STATE = idesc_bf16_f32(DZ, DX, 1, 1), ID_INTRA = idesc_bf16_f32(DZ, C, 1, 0);
+        auto scores = [&](int c) {
+            const int s = c % NST;
+            if (!wait(&full[s], (c / NST) & 1)) return false;
+            tc_fence_after();
+            const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024), dy = smem_desc(smem_u32(tile_y(s)), 16, 1024);
+#pragma unroll
+            for (int k = 0; k < DX / 16; ++k) {
+                const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
+                mma_ss_if(tm + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0, one);
+            }
+            if (INNER) {
+                const uint64_t dw = smem_desc(smem_u32(tile_w(s)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < DZ / 16; ++k) {
+                    const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
+                    mma_ss_if(tm + Lay::T_A2, desc_add(dw, o), desc_add(dz, o), ID_SC, k > 0, one);
+                }
+            }
+            mma_commit_if(scores_done, one);
+            return true;
+        };
+        // the second scores of the next chunk lie in Oi's columns: they wait for the rows' readers
+        constexpr bool late = INNER && !Lay::A2_OWN;
+        bool ok = totals || n == 0 || scores(0);
+        for (int c = 0; ok && c < n; ++c) {
+            const int s = c % NST;
+            const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
+            if (!(ok = wait(s_ready, c & 1))) break;  // the state's copy, and dS has been read
+            if (!(ok = wait(yt_ready, c & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    mma_ss_if(tm + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0, one);
+            }
+            mma_commit_if(state_done, one);
+            if (totals) {
+                mma_commit_if(&stage_free[s], one);
+                continue;
+            }
+            if (c > 0 && !(ok = wait(o_free, (c - 1) & 1))) break;
+            if (late && !(ok = wait(sc_free, c & 1))) break;
+            tc_fence_after();
+            const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024);
+            const uint32_t sc = tm + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
+#pragma unroll
+            for (int p = 0; p < NS; ++p)
+#pragma unroll
+                for (int k = 0; k < DX / 16; ++k)
+                    mma_ts_if(tm + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32), ID_INTER,
+                              p + k > 0, one);
+            if (DOT) mma_commit_if(inter_done, one);
+            if (!late) {
+                if (!(ok = wait(sc_free, c & 1))) break;
+                if (c + 1 < n && !(ok = scores(c + 1))) break;
+            }
+            if (!(ok = wait(p_ready, c & 1))) break;
+            tc_fence_after();
+            const uint64_t dp = smem_desc(smem_u32(p_tile), 16, 1024);
+#pragma unroll
+            for (int k = 0; k < C / 16; ++k)
+                mma_ss_if(tm + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0, one);
+            mma_commit_if(o_done, one);
+            mma_commit_if(&stage_free[s], one);
+            if (late && c + 1 < n) {
+                if (!(ok = wait(o_free, c & 1))) break;
+                if (!(ok = scores(c + 1))) break;
+            }
+        }
+        // every product issued above has completed before TMEM is released
+        mma_commit_if(drain, one);
+        const uint64_t begin = globaltimer();
+        while (!mbar_try_sleep(drain, 0, 200000u))
+            if (globaltimer() - begin > ctl.timeout_ns) break;
+    } else if (warp < GT_W0) {
         // ------------------------------------------------------------ weights
-        // Formed and written a ring ahead of the tiles: place c % 8 was last read for chunk c - 8, and the tiles
-        // of chunk c - 1 - NST are free, so every reader has gone past chunk c - 7 at least.
+        // Two warps take the chunks in turn: one alone needs 2,400 cycles a chunk, about what all the rest takes. Formed
+        // and written a ring ahead of the tiles: place c % 8 was last read for chunk c - 8, and the tiles of chunk
+        // c - 2 - NST are free, NST at most 4, so every reader has gone past chunk c - 7.
         const float *const gp = a.g + b * a.vg.b + h * a.vg.h;
         auto gate = [&](int c, int i) {  // log decay of row i of the sweep's chunk c; 0 behind the end
             const int t = t0 + chunk_of(c) * C + i;
             return c < nch && t < te ? gp[(long long)t * a.vg.l] : 0.f;
         };
-        float g0 = gate(0, 2 * lane), g1 = gate(0, 2 * lane + 1);
-        for (int c = 0; c < nch; ++c) {
-            const float n0 = gate(c + 1, 2 * lane), n1 = gate(c + 1, 2 * lane + 1);  // on its way meanwhile
+        const int c0 = warp - 2;
+        float g0 = gate(c0, 2 * lane), g1 = gate(c0, 2 * lane + 1);
+        for (int c = c0; c < nch; c += 2) {
+            const float n0 = gate(c + 2, 2 * lane), n1 = gate(c + 2, 2 * lane + 1);  // on its way meanwhile
             // sums of the rows 0 .. i in units of 2^-44 doublings; rows whose decay is 0 count as cuts
             // instead. (Sums in 64-bit floating point took 4,700 cycles a chunk, as long as all the rest.)
             const bool z0 = g0 < GATED_CUT, z1 = g1 < GATED_CUT;
@@ -402,251 +483,24 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (c >= NST && !wait(&stage_free[s], ((c / NST) - 1) & 1)) break;
             arrive(&full[s]);
         }
-        if (a.decay) {
+        if (a.decay && c0 == 0) {
             double s = 0;
             for (int t = t0 + lane; t < te; t += 32) s += (double)gp[(long long)t * a.vg.l];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
             if (lane == 0) a.decay[(long long)seg * BH + bh] = (float)exp(s);
         }
-    } else if (warp == 1 || warp == 2) {
-        // ------------------------------------------------------------ products
-        // Two issuing warps, on SM sub-partitions of their own: a product takes one about a hundred cycles
-        // beside the other warps, and the chain of the states' sums need not queue behind the rest. The
-        // whole warp runs the loop and one lane of it issues, so that descriptors stay in uniform registers.
-        {
-            const uint32_t one = elect_one(), tm = __reduce_or_sync(0xffffffffu, tmem);
-            const int nch_u = (int)__reduce_or_sync(0xffffffffu, (uint32_t)nch);
-            constexpr uint32_t ID_SC = idesc_bf16_f32(C, C, 0, 0), ID_INTER = idesc_bf16_f32(DZ, C, 0, 0),
-                               ID_STATE = idesc_bf16_f32(DZ, DX, 1, 1), ID_INTRA = idesc_bf16_f32(DZ, C, 1, 0);
-            auto wait1 = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_long(bar, parity, ctl)) != 0; };
-            auto scores = [&](int c) {
-                const int s = c % NST;
-                if (!wait1(&full[s], (c / NST) & 1)) return false;
-                tc_fence_after();
-                const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024), dy = smem_desc(smem_u32(tile_y(s)), 16, 1024);
-#pragma unroll
-                for (int k = 0; k < DX / 16; ++k) {
-                    const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
-                    mma_ss_if(tm + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0, one);
-                }
-                if (INNER) {
-                    const uint64_t dw = smem_desc(smem_u32(tile_w(s)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < DZ / 16; ++k) {
-                        const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
-                        mma_ss_if(tm + Lay::T_A2, desc_add(dw, o), desc_add(dz, o), ID_SC, k > 0, one);
-                    }
-                }
-                mma_commit_if(scores_done, one);
-                return true;
-            };
-            if (warp == 2) {
-                for (int c = 0; c < nch_u; ++c) {
-                    const int s = c % NST;
-                    if (!wait1(s_ready + (c & 1), (c >> 1) & 1)) break;  // dS has been read
-                    if (!wait1(yt_ready, c & 1)) break;
-                    tc_fence_after();
-                    const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
-#pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            mma_ss_if(tm + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0, one);
-                    }
-                    mma_commit_if(state_done, one);
-                    mma_commit_if(&stage_free[s], one);
-                }
-            } else if (!totals) {
-                // the second scores of the next chunk lie in Oi's columns: they wait for the rows' readers
-                constexpr bool late = INNER && !Lay::A2_OWN;
-                bool ok = nch_u == 0 || scores(0);
-                for (int c = 0; ok && c < nch_u; ++c) {
-                    const int s = c % NST;
-                    if (!(ok = wait1(s_ready + (c & 1), (c >> 1) & 1))) break;  // the copy of the state before the chunk
-                    if (c > 0 && !(ok = wait1(o_free, (c - 1) & 1))) break;
-                    if (late && !(ok = wait1(sc_free, c & 1))) break;
-                    tc_fence_after();
-                    const uint64_t dx = smem_desc(smem_u32(tile_x(s)), 16, 1024);
-                    const uint32_t sc = tm + Lay::T_SC + (c % Lay::COPIES) * (DX / 2);
-#pragma unroll
-                    for (int p = 0; p < NS; ++p)
-#pragma unroll
-                        for (int k = 0; k < DX / 16; ++k)
-                            mma_ts_if(tm + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32),
-                                   ID_INTER, p + k > 0, one);
-                    if (DOT) mma_commit_if(inter_done, one);
-                    if (!late) {
-                        if (!(ok = wait1(sc_free, c & 1))) break;
-                        if (c + 1 < nch_u && !(ok = scores(c + 1))) break;
-                    }
-                    if (!(ok = wait1(p_ready + (c & 1), (c >> 1) & 1))) break;
-                    tc_fence_after();
-                    const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024),
-                                   dp = smem_desc(smem_u32(p_tile + (c % Lay::PS) * Lay::P), 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        mma_ss_if(tm + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0, one);
-                    mma_commit_if(o_done, one);
-                    mma_commit_if(&stage_free[s], one);
-                    if (late && c + 1 < nch_u) {
-                        if (!(ok = wait1(o_free, c & 1))) break;
-                        if (!(ok = scores(c + 1))) break;
-                    }
-                }
-            }
-            // every product issued above has completed before TMEM is released
-            mma_commit_if(drain, one);
-            const uint64_t begin = globaltimer();
-            while (!mbar_try_sleep(drain, 0, 200000u))
-                if (globaltimer() - begin > ctl.timeout_ns) break;
-        }
-    } else if (warp >= PY0 && warp < ST0) {
-        // ------------------------------------------------------------ Y~ and P
-        const int pw = warp - PY0, ft = 32 * pw + lane, half = pw >> 2;
-        constexpr int G = DX / 8, RG = 256 / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG, ..
-        const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
-        const int ta = 16 * q4 + (lane >> 2), tb = ta + 8;
-        // the rows of a chunk are stored during the next one, between its Y~ and its P
-        const int passes = DOT || totals || nch == 0 ? nch : nch + 1;
-        for (int c = 0; c < passes; ++c) {
-            const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
-            const Weights &w = weights[c % GT_SLOTS];
-            if (c < nch) {
-            if (!wait(&full[s], (c / NST) & 1)) break;
-            if (c > 0 && !wait(state_done, (c - 1) & 1)) break;  // Y~ of the chunk before has been read
-            // Loops over a chunk stay rolled where registers allow: the roles' code together is more than the
-            // instruction caches next to the schedulers hold.
-#pragma unroll 1
-            for (int n = 0; n < NR; n += 2) {
-                const uint8_t *const src = tile_y(s) + off + n * RG * 128;
-                uint8_t *const dst = yt + off + n * RG * 128;
-                uint4 v[2];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) v[m] = *(const uint4 *)(src + m * RG * 128);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int r = rg + (n + m) * RG;
-                    const Ch<2> kw = all<2>(w.kw[r]);
-                    uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w}, hi[4], mid[4], lo[4];
-                    if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
-                    uint8_t *const d = dst + m * RG * 128;
-                    *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *(uint4 *)(d + 2 * Lay::X) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            if (nv < C)
-                for (int e = ft; e < (C - nv) * (DZ / 8); e += 256) {
-                    const int r = nv + e / (DZ / 8), p = e % (DZ / 8);
-                    *(uint4 *)(tile_z(s) + (p >> 3) * C * 128 + r * 128 + ((p & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                }
-            fence_async_smem();
-            arrive(yt_ready);
-            if (totals) continue;
-            }
-            if (!DOT && c > 0) {
-                if (!wait(o_done, (c - 1) & 1)) break;
-                tc_fence_after();
-                rows(c - 1, 32 * half + 16, 0);
-                if (c == nch) break;
-            }
-            // (with the rows' products of the chunk before, those of this chunk's scores are done)
-            if ((DOT || c == 0) && !wait(scores_done, c & 1)) break;
-            tc_fence_after();
-            // columns lo <= col < hi of a row count: up to the row itself, or in reverse from it on
-            const int col0 = 32 * half + 2 * cpos;
-            int from[2], to[2];
-            Ch<2> ghi[2], glo[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = r ? tb : ta;
-                from[r] = (rev ? row : 0) - col0;
-                to[r] = (row >= nv ? 0 : rev ? nv : row + 1) - col0;
-                ghi[r] = all<2>(w.hi[row]);
-                glo[r] = all<2>(w.lo[row]);
-            }
-            const Ch<2> ps = all<2>(a.yscale * a.oscale), minus = all<2>(-1.f);
-            float sum[2] = {0.f, 0.f}, sc[INNER ? 8 : 1];
-            uint8_t *const pt = p_tile + (c % Lay::PS) * Lay::P;
-            uint32_t r1[32], r2[32];  // the first 16
-            tmem_ld16x256_x4(tmem + Lay::T_A + lanes + 32 * half, r1);
-            if (INNER) tmem_ld16x256_x4(tmem + Lay::T_A2 + lanes + 32 * half, r2);
-            tmem_wait_ld();
-            tc_fence_before();
-            arrive(sc_free);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 h2 = *(const float2 *)&w.hi[col0 + 8 * k], l2 = *(const float2 *)&w.lo[col0 + 8 * k];
-                const Ch<2> chi{{h2.x, h2.y}}, clo{{l2.x, l2.y}};
-                uint32_t p[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int e = 4 * k + 2 * r;
-                    const Ch<2> d = add(fma(chi, minus, ghi[r]), fma(clo, minus, glo[r])), wt{{ex2(d.v[0]), ex2(d.v[1])}};
-                    Ch<2> x = mul(mul(Ch<2>{{__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])}}, wt), ps);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const bool in = 8 * k + u >= from[r] && 8 * k + u < to[r];
-                        if (INNER) {
-                            const bool own = 8 * k + u == (r ? tb : ta) - col0;
-                            const float y = in && !own ? x.v[u] * __uint_as_float(r2[e + u]) : 0.f;
-                            sum[r] += y;
-                            if (r == 0) sc[2 * k + u] = y;
-                            else sc[2 * k + u] += y;
-                        }
-                        x.v[u] = in ? x.v[u] : 0.f;
-                    }
-                    p[r] = pack_bf16x2(x.v[0], x.v[1]);
-                }
-                const int ch = 4 * half + k;
-                *(uint32_t *)(pt + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = p[0];
-                *(uint32_t *)(pt + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = p[1];
-            }
-            fence_async_smem();
-            arrive(p_ready + (c & 1));
-            if (INNER) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-                }
-                float *const rp = a.dot + ((long long)(4 + half) * BH + bh) * a.L + row0;
-                if (cpos == 0) {
-                    if (ta < nv) rp[ta] = sum[0];
-                    if (tb < nv) rp[tb] = sum[1];
-                }
-                int at = 0;
-#pragma unroll
-                for (int o = 4, n = 4; o < 32; o <<= 1, n >>= 1) {
-                    const bool up = lane & o;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < n) {
-                            const float send = up ? sc[i] : sc[i + n], keep = up ? sc[i + n] : sc[i];
-                            sc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                        }
-                    at += up ? n : 0;
-                }
-                const int col = 32 * half + 8 * (at >> 1) + 2 * cpos + (at & 1);
-                if (col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
-            }
-        }
-    } else if (warp >= ST0) {
-        // ------------------------------------------------------------ the state, and the rows
-        const int half = (warp - ST0) >> 2;
+    } else {
+        // ------------------------------------------------------------ workers
         const int j = DZ == 128 ? 32 * q4 + lane : 16 * q4 + (lane & 15);  // z channel
         const bool live = DZ == 128 || lane < 16;
-        constexpr int NX = DX / 2;  // x channels half * NX ..
+        constexpr int NX = DX / 4;  // x channels part * NX ..
         const long long n_state = (long long)DX * DZ;
         const long long at = (a.by_seg ? (long long)seg * BH + bh : (long long)slot * a.H + h) * n_state;
         Ch<2> S[NX / 2];
 #pragma unroll
         for (int i = 0; i < NX / 2; ++i) S[i] = all<2>(0.f);
-        auto place = [&](int i) { return (long long)(half * NX + i) * a.rs + (long long)j * a.cs; };
+        auto place = [&](int i) { return (long long)(part * NX + i) * a.rs + (long long)j * a.cs; };
         if (a.init && !totals && live && (a.by_seg || slot >= 0)) {
             const float *p = a.init + at;
             if (a.rs == 1) {
@@ -665,7 +519,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (!live) return;
             if (a.rs == 1) {
 #pragma unroll
-                for (int i = 0; i < NX; i += 4) *(float4 *)(p + place(i)) = make_float4(S[i / 2].v[0], S[i / 2].v[1], S[i / 2 + 1].v[0], S[i / 2 + 1].v[1]);
+                for (int i = 0; i < NX; i += 4)
+                    *(float4 *)(p + place(i)) = make_float4(S[i / 2].v[0], S[i / 2].v[1], S[i / 2 + 1].v[0], S[i / 2 + 1].v[1]);
             } else {
 #pragma unroll
                 for (int i = 0; i < NX; ++i) p[place(i)] = S[i / 2].v[i & 1];
@@ -676,62 +531,187 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (!totals) {
 #pragma unroll
                 for (int i = 0; i < NX; i += 16) {
-                    uint32_t part[3][8];
+                    uint32_t p[3][8];
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         const Ch<2> &x = S[i / 2 + u];
-                        if (NS == 1) part[0][u] = pack_bf16x2(x.v[0], x.v[1]);
-                        else split3(x, part[0][u], part[1][u], part[2][u]);
+                        if (NS == 1) p[0][u] = pack_bf16x2(x.v[0], x.v[1]);
+                        else split3(x, p[0][u], p[1][u], p[2][u]);
                     }
 #pragma unroll
-                    for (int p = 0; p < NS; ++p) tmem_st8(tmem + lanes + Lay::T_SC + (p + c % Lay::COPIES) * (DX / 2) + (half * NX + i) / 2, part[p]);
+                    for (int k = 0; k < NS; ++k)
+                        tmem_st8(tmem + lanes + Lay::T_SC + (k + c % Lay::COPIES) * (DX / 2) + (part * NX + i) / 2, p[k]);
                 }
                 tmem_wait_st();
             }
             tc_fence_before();
-            arrive(s_ready + (c & 1));
+            arrive(s_ready);
         };
         const int first_anchor = a.anchors ? t0 / (a.anchor_chunks * C) : 0;
         const int anchors_here = a.anchors ? (t1 - t0 + a.anchor_chunks * C - 1) / (a.anchor_chunks * C) : 0;
         if (a.anchors && rev)  // those that end behind the sequence
             for (int k = (nch + a.anchor_chunks - 1) / a.anchor_chunks; k < anchors_here; ++k) anchor(first_anchor + k);
         copy(0);
+
+        const int ft = 32 * (warp - GT_W0) + lane;
+        constexpr int G = DX / 8, RG = 32 * GT_WORKERS / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG
+        const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
+        const int ta = 16 * q4 + (lane >> 2), tb = ta + 8, col0 = 16 * part + 2 * cpos;
+        const Ch<2> ps = all<2>(a.yscale * a.oscale), minus = all<2>(-1.f);
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
-            const int s = c % NST, cc = chunk_of(c);
+            const int s = c % NST, cc = chunk_of(c), row0 = t0 + cc * C, nv = min(C, te - row0);
             const Weights &w = weights[c % GT_SLOTS];
             if (a.anchors) {
                 if (rev && (c == 0 || (cc + 1) % a.anchor_chunks == 0)) anchor(first_anchor + cc / a.anchor_chunks);
                 if (!rev && cc % a.anchor_chunks == 0) anchor(first_anchor + cc / a.anchor_chunks);
             }
+            // ---- Y~ (the one before has been read: dS of the chunk before was waited for)
+            if (!(ok = wait(&full[s], (c / NST) & 1))) break;
+            {
+                const uint8_t *const src = tile_y(s) + off;
+                uint8_t *const dst = yt + off;
+                uint4 v[NR];
+#pragma unroll
+                for (int m = 0; m < NR; ++m) v[m] = *(const uint4 *)(src + m * RG * 128);
+#pragma unroll
+                for (int m = 0; m < NR; ++m) {
+                    const int r = rg + m * RG;
+                    const Ch<2> kw = all<2>(w.kw[r]);
+                    uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w}, hi[4], mid[4], lo[4];
+                    if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
+                    uint8_t *const d = dst + m * RG * 128;
+                    *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    *(uint4 *)(d + 2 * Lay::X) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            if (nv < C)
+                for (int e = ft; e < (C - nv) * (DZ / 8); e += 32 * GT_WORKERS) {
+                    const int r = nv + e / (DZ / 8), p = e % (DZ / 8);
+                    *(uint4 *)(tile_z(s) + (p >> 3) * C * 128 + r * 128 + ((p & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+            fence_async_smem();
+            arrive(yt_ready);
+            if (!totals) {
+                // ---- the rows of the chunk before
+                if (!DOT && c > 0) {
+                    if (!(ok = wait(o_done, (c - 1) & 1))) break;
+                    tc_fence_after();
+                    rows(c - 1);
+                }
+                // ---- P. Its one place has been read; with the intra product of the chunk before, this chunk's scores
+                // are done too (not with DOT, whose issuer may take them up later).
+                if ((DOT || c == 0) && !(ok = wait(scores_done, c & 1))) break;
+                tc_fence_after();
+                uint32_t r1[8], r2[8];
+                tmem_ld16x256_x2(tmem + Lay::T_A + lanes + 16 * part, r1);
+                if (INNER) tmem_ld16x256_x2(tmem + Lay::T_A2 + lanes + 16 * part, r2);
+                // columns from <= col < to of a row count: up to the row itself, or in reverse from it on
+                int from[2], to[2];
+                Ch<2> ghi[2], glo[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = r ? tb : ta;
+                    from[r] = (rev ? row : 0) - col0;
+                    to[r] = (row >= nv ? 0 : rev ? nv : row + 1) - col0;
+                    ghi[r] = all<2>(w.hi[row]);
+                    glo[r] = all<2>(w.lo[row]);
+                }
+                float sum[2] = {0.f, 0.f}, sc[4];
+                tmem_wait_ld();
+                tc_fence_before();
+                arrive(sc_free);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 h2 = *(const float2 *)&w.hi[col0 + 8 * k], l2 = *(const float2 *)&w.lo[col0 + 8 * k];
+                    const Ch<2> chi{{h2.x, h2.y}}, clo{{l2.x, l2.y}};
+                    uint32_t p[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int e = 4 * k + 2 * r;
+                        const Ch<2> d = add(fma(chi, minus, ghi[r]), fma(clo, minus, glo[r])), wt{{ex2(d.v[0]), ex2(d.v[1])}};
+                        Ch<2> x = mul(mul(Ch<2>{{__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])}}, wt), ps);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const bool in = 8 * k + u >= from[r] && 8 * k + u < to[r];
+                            if (INNER) {
+                                const bool own = 8 * k + u == (r ? tb : ta) - col0;
+                                const float y = in && !own ? x.v[u] * __uint_as_float(r2[e + u]) : 0.f;
+                                sum[r] += y;
+                                if (r == 0) sc[2 * k + u] = y;
+                                else sc[2 * k + u] += y;
+                            }
+                            x.v[u] = in ? x.v[u] : 0.f;
+                        }
+                        p[r] = pack_bf16x2(x.v[0], x.v[1]);
+                    }
+                    const int ch = 2 * part + k;
+                    *(uint32_t *)(p_tile + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = p[0];
+                    *(uint32_t *)(p_tile + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = p[1];
+                }
+                fence_async_smem();
+                arrive(p_ready);
+                if (INNER) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+                        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+                    }
+                    float *const rp = a.dot + ((long long)(4 + part) * BH + bh) * a.L + row0;
+                    if (cpos == 0) {
+                        if (ta < nv) rp[ta] = sum[0];
+                        if (tb < nv) rp[tb] = sum[1];
+                    }
+                    int at_c = 0;
+#pragma unroll
+                    for (int o = 4, n = 2; n > 0; o <<= 1, n >>= 1) {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (i < n) {
+                                const float send = up ? sc[i] : sc[i + n], keep = up ? sc[i + n] : sc[i];
+                                sc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                            }
+                        at_c += up ? n : 0;
+                    }
+                    sc[0] += __shfl_xor_sync(0xffffffffu, sc[0], 16);
+                    const int col = col0 + 8 * (at_c >> 1) + (at_c & 1);
+                    if (!(lane & 16) && col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
+                }
+            }
+            // ---- the state: next to 1 by the decay minus 1, whose rounding does not grow with the chunks
             if (!(ok = wait(state_done, c & 1))) break;
             tc_fence_after();
+            uint32_t d[NX / 16][16];
+#pragma unroll
+            for (int i = 0; i < NX / 16; ++i) tmem_ld16(tmem + lanes + Lay::T_DS + part * NX + 16 * i, d[i]);
             const float da = w.a, em = w.em;
-            // next to 1 by the decay minus 1, whose rounding does not grow with the chunks
             const bool near = da > 0.5f;
             const Ch<2> m = all<2>(near ? em : da), one = all<2>(near ? 1.f : 0.f);
             if (da == 0.f)  // forgets infinities and NaN too
 #pragma unroll
                 for (int i = 0; i < NX / 2; ++i) S[i] = all<2>(0.f);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < NX; i += 16) {
-                uint32_t d[16];
-                tmem_ld16(tmem + lanes + Lay::T_DS + half * NX + i, d);
-                tmem_wait_ld();
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    Ch<2> &x = S[i / 2 + u];
-                    x = fma(x, m, fma(x, one, Ch<2>{{__uint_as_float(d[2 * u]), __uint_as_float(d[2 * u + 1])}}));
-                }
+            for (int i = 0; i < NX / 2; ++i) {
+                const Ch<2> ds{{__uint_as_float(d[i / 8][2 * (i % 8)]), __uint_as_float(d[i / 8][2 * (i % 8) + 1])}};
+                S[i] = fma(S[i], m, fma(S[i], one, ds));
             }
             if (DOT && !(ok = wait(inter_done, c & 1))) break;  // the copy has been read
             copy(c + 1);
-            if (totals) continue;
-            if (!(ok = wait(o_done, c & 1))) break;
+            if (DOT) {
+                if (!(ok = wait(o_done, c & 1))) break;
+                tc_fence_after();
+                rows(c);
+                arrive(&stage_free[s]);
+            }
+        }
+        if (!DOT && !totals && ok && nch > 0 && (ok = wait(o_done, (nch - 1) & 1))) {
             tc_fence_after();
-            rows(c, 32 * half, 0);
-            if (DOT) rows(c, 32 * half + 16, 1);
-            if (DOT) arrive(&stage_free[s]);
+            rows(nch - 1);
         }
         if (ok) {
             if (a.anchors && !rev) {
@@ -739,9 +719,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 if (seg == a.nseg - 1) anchor(a.n_anchors);
             }
             if (a.fin && (a.by_seg || slot >= 0)) store(a.fin + at);
-            // rows behind the chunks
+            // rows behind the sequence's end
             if (!totals && a.out)
-                for (int t = t0 + nch * C + (warp - ST0); t < t1; t += 8)
+                for (int t = te + (warp - GT_W0); t < t1; t += GT_WORKERS)
                     for (int i = lane; i < DZ; i += 32) {
                         const long long o = out0 + (long long)t * a.vo.l + i;
                         if (a.out_f32) ((float *)a.out)[o] = 0.f;
@@ -749,7 +729,6 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     }
         }
     }
-    if (warp >= PY0 && lane == 0) tma_wait_read_all();  // the stores have read their tiles
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -759,7 +738,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
 // ---- host side -----------------------------------------------------------------------------------
 // [B, n, L, d] bf16 by strides; boxes of 64 channels x 64 rows of one head, 128-byte swizzle, rows past L
 // zero.
-bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, int d, bool out = false)
+bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, int d)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
@@ -767,14 +746,8 @@ bool map4(CUtensorMap *m, const void *ptr, const View &v, int B, int n, int L, i
     auto stride = [&](long long s, int len) { return (cuuint64_t)(len > 1 ? s * 2 : d * 2); };
     cuuint64_t strides[3] = {stride(v.l, L), stride(v.h, n), stride(v.b, B)};
     cuuint32_t box[4] = {64, GT_C, 1, 1}, es[4] = {1, 1, 1, 1};
-    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-    if (out) {  // a warp's 16 rows of a quadrant's channels
-        box[0] = (cuuint32_t)d / 4;
-        box[1] = 16;
-        swizzle = d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
-    }
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DX, int DZ, bool DOT, bool INNER> int launch_dims(const GtArgs &a, cudaStream_t stream)
@@ -825,7 +798,6 @@ int launch_pass(const GatedArgs &p, Pass &s)
     if (!map4(&a.my, s.y.p, s.y.v, p.B, s.y.n, p.L, s.y.d) || !map4(&a.mz, s.z.p, s.z.v, p.B, s.z.n, p.L, s.z.d)) return LA_ERR_CUDA;
     if (s.x.p) {
         a.sx = p.H / s.x.n;
-        if (!a.out_f32 && !map4(&a.mo, a.out, a.vo, p.B, p.H, p.L, s.z.d, true)) return LA_ERR_CUDA;
         if (!map4(&a.mx, s.x.p, s.x.v, p.B, s.x.n, p.L, s.x.d)) return LA_ERR_CUDA;
     }
     if (!s.w.p) return launch_dot<false, false>(a, s.y.d, s.z.d, p.stream);
@@ -872,7 +844,7 @@ struct TcBwdSpace {
         S = take((n_anchors + 1) * heads * n);
         D = take(n_anchors * heads * n);
         y = take(n_anchors * heads);
-        r = take(6 * heads * L);
+        r = take(8 * heads * L);
         c = take(8 * heads * L);
         dk = take(H > Hk ? heads * L * d : 0);
         dv = take(H > Hk ? heads * L * e : 0);
@@ -1015,7 +987,7 @@ int gated_tc_bwd(const GatedArgs &p)
     }
     if (dg) {
         if ((rc = gated_products(p, ws + w.D, ws + w.S + heads * n, ws + w.y, w.n_anchors, n)) != LA_OK) return rc;
-        if ((rc = gated_log_decay(p, ws + w.r, 6, ws + w.c, 8, ws + w.y, w.anchor, w.n_anchors, p.dg ? p.dg : ws + w.dg)) != LA_OK)
+        if ((rc = gated_log_decay(p, ws + w.r, 8, ws + w.c, 8, ws + w.y, w.anchor, w.n_anchors, p.dg ? p.dg : ws + w.dg)) != LA_OK)
             return rc;
     }
     return LA_OK;

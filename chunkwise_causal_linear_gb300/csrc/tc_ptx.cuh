@@ -142,12 +142,6 @@ LA_DEV void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, 
                  "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
                  : "memory");
 }
-LA_DEV void tma_store_4d(const CUtensorMap *map, uint32_t src, int x, int y, int z, int w)
-{
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
-                 "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
 // Four 8x8 blocks of 16-bit values, transposed on the way: lane l gives the address of row l % 8 of block l / 8
 // in memory, and holds of each block column l / 4 of memory, rows 2 (l % 4) and the next one.
 LA_DEV void stmatrix_t(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3)
