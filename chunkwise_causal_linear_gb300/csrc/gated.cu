@@ -584,10 +584,11 @@ template <typename T, int V> __global__ void __launch_bounds__(STEP_THREADS) ste
 
 int fwd_segments(int B, int H, int L, int d, int e, int sms)
 {
-    // twice as many blocks as SMs, of 128 rows at least; the segments' sums cost two thirds of a sweep,
-    // so that two segments would not pay
+    // twice as many blocks as SMs, of 32 rows at least; the segments' sums cost two thirds of a sweep,
+    // so that two segments would not pay. (A row takes a block about half a microsecond however few blocks there are:
+    // B5 H6 L777 with 128 rows at least 136 us, with 32 105.)
     const double blocks = (double)B * H * tiles_of(d, e);
-    const int want = (int)std::min(1024.0, std::floor(2.0 * sms / blocks)), most = (L + 127) / 128;
+    const int want = (int)std::min(1024.0, std::floor(2.0 * sms / blocks)), most = (L + 31) / 32;
     const int n = std::min(want, most);
     return n < 3 ? 1 : n;
 }

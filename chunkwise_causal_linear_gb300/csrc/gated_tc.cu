@@ -526,7 +526,13 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 for (int i = 0; i < NX; ++i) p[place(i)] = S[i / 2].v[i & 1];
             }
         };
-        auto anchor = [&](int k) { store(a.anchors + ((long long)k * BH + bh) * n_state); };
+        // In a layout of their own, a warp's lanes next to one another: S and D are only multiplied element by element
+        auto anchor = [&](int k) {
+            float *const p = a.anchors + ((long long)k * BH + bh) * n_state + (long long)part * NX * DZ + j;
+            if (live)
+#pragma unroll
+                for (int i = 0; i < NX; ++i) p[i * DZ] = S[i / 2].v[i & 1];
+        };
         auto copy = [&](int c) {  // of the state before chunk c
             if (!totals) {
 #pragma unroll
@@ -558,6 +564,11 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         const int gi = ft % G, rg = ft / G, off = (gi >> 3) * C * 128 + (((gi & 7) ^ (rg & 7)) << 4) + rg * 128;
         const int ta = 16 * q4 + (lane >> 2), tb = ta + 8, col0 = 16 * part + 2 * cpos;
         const Ch<2> ps = all<2>(a.yscale * a.oscale), minus = all<2>(-1.f);
+        if (rev ? part < q4 : part > q4)
+            for (int k = 0; k < 2; ++k) {
+                *(uint32_t *)(p_tile + ta * 128 + (((2 * part + k) ^ (ta & 7)) << 4) + 4 * cpos) = 0;
+                *(uint32_t *)(p_tile + tb * 128 + (((2 * part + k) ^ (tb & 7)) << 4) + 4 * cpos) = 0;
+            }
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int s = c % NST, cc = chunk_of(c), row0 = t0 + cc * C, nv = min(C, te - row0);
@@ -620,10 +631,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     ghi[r] = all<2>(w.hi[row]);
                     glo[r] = all<2>(w.lo[row]);
                 }
-                float sum[2] = {0.f, 0.f}, sc[4];
+                float sum[2] = {0.f, 0.f}, sc[4] = {0.f, 0.f, 0.f, 0.f};
                 tmem_wait_ld();
                 tc_fence_before();
                 arrive(sc_free);
+                // (blocks behind the diagonal are 0: written once, before the loop)
+                if (rev ? part >= q4 : part <= q4)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float2 h2 = *(const float2 *)&w.hi[col0 + 8 * k], l2 = *(const float2 *)&w.lo[col0 + 8 * k];
