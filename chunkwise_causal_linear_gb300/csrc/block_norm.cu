@@ -9,8 +9,9 @@
 // Bound by memory: y, r and gate are read once, h and n written once; apart, the two norms, the gate and the
 // sum would read and write h and the norm's output once more each. A row is held in the registers of NT
 // threads, 8 channels a thread (16 for rows above 4096), so that its statistics, centred variance and
-// both norms come from that one read; the next row's loads are issued before the row's sums, whose barriers
-// they hide. The gradients recompute the statistics from y and r (32-bit sums; h before its rounding)
+// both norms come from that one read. Each thread copies its channels of the next rows ahead into places of
+// its own in shared memory (cp.async, a ring of rows, no barrier), which costs no registers and hides the
+// sums' barriers; rows that cannot be read 16 bytes at a time are loaded one row ahead. The gradients recompute the statistics from y and r (32-bit sums; h before its rounding)
 // instead of reading them, and keep the sums for the weights' gradients in the threads' registers; the
 // groups' sums are joined by a second kernel in a fixed order.
 #include <math.h>
@@ -33,7 +34,8 @@ struct BnArgs {
     const void *y, *r, *gate, *dh, *dn;
     void *h, *n, *dr, *dy, *dgate;
     const float *post_w, *post_b, *pre_w, *pre_b;
-    float *part;  // [groups][4][d]: sums for post_w, post_b, pre_w, pre_b
+    float *part;  // [blocks][4][d]: sums for post_w, post_b, pre_w, pre_b
+    int sums;     // bit k: the k-th of them is wanted
     View vy, vr, vg, vh, vn, vdh, vdn, vdr, vdy, vdg;
     long long rows;
     int L, d, post, pre, act;
@@ -167,8 +169,70 @@ template <int NT, int N> __device__ __forceinline__ float statistics(float (&x)[
 
 template <int NT> constexpr int bn_block = NT < 256 ? 256 : NT;
 
+// Rows on their way to a thread: three, or what shared memory holds of the widest rows.
+template <int VEC, int STAGE> constexpr int AHEAD = VEC != 8 ? 1 : 3 * STAGE <= 204800 ? 3 : 2 * STAGE <= 204800 ? 2 : 1;
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A thread's channels of a tensor, some rows ahead: ring places in shared memory for vectors, registers one
+// row ahead for single channels.
+template <typename X, int VEC, int NC, int BLOCK> struct Ahead {
+    static constexpr int BYTES = VEC == 8 ? NC * BLOCK * 8 * (int)sizeof(X) : 0;  // of one row of the block
+    Raw<X, VEC> raw[VEC == 8 ? 1 : NC];
+    uint32_t base;  // this thread's place in the ring's first row
+    int step;       // bytes between rows of the ring
+    __device__ __forceinline__ void place(uint32_t smem, int stage_bytes)
+    {
+        base = smem + threadIdx.x * 16;
+        step = stage_bytes;
+    }
+    __device__ __forceinline__ void fetch(const X *p, int slot, const int (&at)[NC], int d)
+    {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (at[c] < d) {
+                if constexpr (VEC == 8) {
+#pragma unroll
+                    for (int h = 0; h < (int)sizeof(X) / 2; ++h)
+                        copy16(base + slot * step + (c * (int)sizeof(X) / 2 + h) * BLOCK * 16, p + at[c] + h * 4);
+                } else {
+                    raw[c].load(p + at[c]);
+                }
+            }
+    }
+    __device__ __forceinline__ void get(float *f, int slot, int c) const
+    {
+        if constexpr (VEC == 8) {
+            const uint32_t a = base + slot * step + c * ((int)sizeof(X) / 2) * BLOCK * 16;
+            const uint4 u = ptx::lds128(a);
+            Raw<X, 8> r;
+            if constexpr (sizeof(X) == 2) {
+                r.w = u;
+            } else {
+                const uint4 v = ptx::lds128(a + BLOCK * 16);
+                r.a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+                r.b = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+            }
+            r.get(f);
+        } else {
+            raw[c].get(f);
+        }
+    }
+};
+template <int VEC> __device__ __forceinline__ void row_issued()
+{
+    if constexpr (VEC == 8) asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int VEC, int PF> __device__ __forceinline__ void row_arrived()
+{
+    if constexpr (VEC == 8) asm volatile("cp.async.wait_group %0;" ::"n"(PF - 1) : "memory");
+}
+
 template <typename T, typename R, int VEC, int NT, int NC>
-__global__ void __launch_bounds__(bn_block<NT>) bn_fwd_kernel(const BnArgs a)
+__global__ void __launch_bounds__(bn_block<NT>, 1) bn_fwd_kernel(const BnArgs a)
 {
     constexpr int N = VEC * NC, GROUPS = bn_block<NT> / NT;
     __shared__ float sm[GROUPS * 2 * (NT / 32) * 2];
@@ -183,33 +247,40 @@ __global__ void __launch_bounds__(bn_block<NT>) bn_fwd_kernel(const BnArgs a)
 #pragma unroll
         for (int i = 0; i < VEC; ++i) in[c * VEC + i] = at[c] < a.d;
     }
-    Raw<T, VEC> ry[NC], rg[NC];
-    Raw<R, VEC> rr[NC];
-    auto fetch = [&](long long row) {
-        const int b = (int)(row / a.L), t = (int)(row % a.L);
-        const T *y = (const T *)a.y + row_of(a.vy, b, 0, t), *g = (const T *)a.gate + row_of(a.vg, b, 0, t);
-        const R *r = (const R *)a.r + row_of(a.vr, b, 0, t);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (in[c * VEC]) {
-                ry[c].load(y + at[c]);
-                rr[c].load(r + at[c]);
-                if (a.gate) rg[c].load(g + at[c]);
-            }
+    extern __shared__ __align__(16) uint8_t ring[];
+    constexpr int BLOCK = bn_block<NT>, BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES, STAGE = 2 * BT + BR,
+                  PF = AHEAD<VEC, STAGE>;
+    Ahead<T, VEC, NC, BLOCK> ry, rg;
+    Ahead<R, VEC, NC, BLOCK> rr;
+    const uint32_t ring_at = ptx::smem_u32(ring);
+    ry.place(ring_at, STAGE);
+    rg.place(ring_at + BT, STAGE);
+    rr.place(ring_at + 2 * BT, STAGE);
+    auto fetch = [&](long long row, int slot) {
+        if (row < a.rows) {
+            const int b = (int)(row / a.L), t = (int)(row % a.L);
+            ry.fetch((const T *)a.y + row_of(a.vy, b, 0, t), slot, at, a.d);
+            rr.fetch((const R *)a.r + row_of(a.vr, b, 0, t), slot, at, a.d);
+            if (a.gate) rg.fetch((const T *)a.gate + row_of(a.vg, b, 0, t), slot, at, a.d);
+        }
+        row_issued<VEC>();
     };
-    if (first < a.rows) fetch(first);
-    for (long long row = first; row < a.rows; row += step) {
+#pragma unroll
+    for (int i = 0; i < PF; ++i) fetch(first + i * step, i);
+    int slot = 0;
+    for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
         float u[N], h[N], z[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) u[i] = h[i] = z[i] = 0.f;
+        row_arrived<VEC, PF>();
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             if (in[c * VEC]) {
-                ry[c].get(u + c * VEC);
-                rr[c].get(h + c * VEC);
-                if (a.gate) rg[c].get(z + c * VEC);
+                ry.get(u + c * VEC, slot, c);
+                rr.get(h + c * VEC, slot, c);
+                if (a.gate) rg.get(z + c * VEC, slot, c);
             }
-        if (row + step < a.rows) fetch(row + step);
+        fetch(row + PF * step, slot);
         const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<NT>(u, in, a.post, a, sum);
         const int b = (int)(row / a.L), t = (int)(row % a.L);
         R *const ho = (R *)a.h + row_of(a.vh, b, 0, t);
@@ -265,7 +336,7 @@ template <int NT, int N> __device__ __forceinline__ void norm_back(float (&dxh)[
 }
 
 template <typename T, typename R, int VEC, int NT, int NC>
-__global__ void __launch_bounds__(bn_block<NT>) bn_bwd_kernel(const BnArgs a)
+__global__ void __launch_bounds__(bn_block<NT>, 1) bn_bwd_kernel(const BnArgs a)
 {
     constexpr int N = VEC * NC, GROUPS = bn_block<NT> / NT;
     __shared__ float sm[GROUPS * 2 * (NT / 32) * 2];
@@ -285,35 +356,46 @@ __global__ void __launch_bounds__(bn_block<NT>) bn_bwd_kernel(const BnArgs a)
     for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < N; ++i) total[k][i] = 0.f;
-    Raw<T, VEC> ry[NC], rg[NC], rdn[NC];
-    Raw<R, VEC> rr[NC], rdh[NC];
-    auto fetch = [&](long long row) {
-        const int b = (int)(row / a.L), t = (int)(row % a.L);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (in[c * VEC]) {
-                ry[c].load((const T *)a.y + row_of(a.vy, b, 0, t) + at[c]);
-                rr[c].load((const R *)a.r + row_of(a.vr, b, 0, t) + at[c]);
-                if (a.gate) rg[c].load((const T *)a.gate + row_of(a.vg, b, 0, t) + at[c]);
-                if (a.dh) rdh[c].load((const R *)a.dh + row_of(a.vdh, b, 0, t) + at[c]);
-                if (a.dn) rdn[c].load((const T *)a.dn + row_of(a.vdn, b, 0, t) + at[c]);
-            }
+    extern __shared__ __align__(16) uint8_t ring[];
+    constexpr int BLOCK = bn_block<NT>, BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES,
+                  STAGE = 3 * BT + 2 * BR, PF = AHEAD<VEC, STAGE>;
+    Ahead<T, VEC, NC, BLOCK> ry, rg, rdn;
+    Ahead<R, VEC, NC, BLOCK> rr, rdh;
+    const uint32_t ring_at = ptx::smem_u32(ring);
+    ry.place(ring_at, STAGE);
+    rg.place(ring_at + BT, STAGE);
+    rdn.place(ring_at + 2 * BT, STAGE);
+    rr.place(ring_at + 3 * BT, STAGE);
+    rdh.place(ring_at + 3 * BT + BR, STAGE);
+    auto fetch = [&](long long row, int slot) {
+        if (row < a.rows) {
+            const int b = (int)(row / a.L), t = (int)(row % a.L);
+            ry.fetch((const T *)a.y + row_of(a.vy, b, 0, t), slot, at, a.d);
+            rr.fetch((const R *)a.r + row_of(a.vr, b, 0, t), slot, at, a.d);
+            if (a.gate) rg.fetch((const T *)a.gate + row_of(a.vg, b, 0, t), slot, at, a.d);
+            if (a.dh) rdh.fetch((const R *)a.dh + row_of(a.vdh, b, 0, t), slot, at, a.d);
+            if (a.dn) rdn.fetch((const T *)a.dn + row_of(a.vdn, b, 0, t), slot, at, a.d);
+        }
+        row_issued<VEC>();
     };
-    if (first < a.rows) fetch(first);
-    for (long long row = first; row < a.rows; row += step) {
+#pragma unroll
+    for (int i = 0; i < PF; ++i) fetch(first + i * step, i);
+    int slot = 0;
+    for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
         float u[N], h[N], z[N], dh[N], dn[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) u[i] = h[i] = z[i] = dh[i] = dn[i] = 0.f;
+        row_arrived<VEC, PF>();
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             if (in[c * VEC]) {
-                ry[c].get(u + c * VEC);
-                rr[c].get(h + c * VEC);
-                if (a.gate) rg[c].get(z + c * VEC);
-                if (a.dh) rdh[c].get(dh + c * VEC);
-                if (a.dn) rdn[c].get(dn + c * VEC);
+                ry.get(u + c * VEC, slot, c);
+                rr.get(h + c * VEC, slot, c);
+                if (a.gate) rg.get(z + c * VEC, slot, c);
+                if (a.dh) rdh.get(dh + c * VEC, slot, c);
+                if (a.dn) rdn.get(dn + c * VEC, slot, c);
             }
-        if (row + step < a.rows) fetch(row + step);
+        fetch(row + PF * step, slot);
         const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<NT>(u, in, a.post, a, sum);
         const int b = (int)(row / a.L), t = (int)(row % a.L);
         float act[N];  // act(gate), times branch_scale
@@ -403,57 +485,88 @@ __global__ void __launch_bounds__(bn_block<NT>) bn_bwd_kernel(const BnArgs a)
         for (int c = 0; c < NC; ++c)
             if (in[c * VEC]) put<VEC>(dy + at[c], dh + c * VEC);
     }
-    if (a.part)
+    if (a.part) {
+        // the block's row groups one after the other into shared memory, then the block's sums
+        float *const acc = (float *)ring;  // [4][d], where the rows were
+        if (VEC == 8) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if constexpr (GROUPS > 1) {
+            for (int g = 0; g < GROUPS; ++g) {
+                __syncthreads();
+                if (group == g)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k)
+                        if (a.sums >> k & 1)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                if (in[c * VEC]) put<VEC>(a.part + (first * 4 + k) * a.d + at[c], total[k] + c * VEC);
+                            for (int i = 0; i < N; ++i)
+                                if (in[i]) {
+                                    float *const p = acc + k * a.d + at[i / VEC] + i % VEC;
+                                    *p = g == 0 ? total[k][i] : *p + total[k][i];
+                                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 4 * a.d; i += BLOCK)
+                if (a.sums >> (i / a.d) & 1) a.part[(long long)blockIdx.x * 4 * a.d + i] = acc[i];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (a.sums >> k & 1)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (in[c * VEC]) put<VEC>(a.part + ((long long)blockIdx.x * 4 + k) * a.d + at[c], total[k] + c * VEC);
+        }
+    }
 }
 
 struct BnJoin {
     const float *part;
     float *out[4];
-    int groups, d;
+    int blocks, d;
 };
-// 32 channels a block, the groups' sums in 8 runs of every eighth one, joined in order.
-__global__ void __launch_bounds__(256) bn_join_kernel(const BnJoin a)
+// 32 channels a block, the blocks' sums in 32 runs of every 32nd one, joined in order.
+__global__ void __launch_bounds__(1024) bn_join_kernel(const BnJoin a)
 {
-    __shared__ float sm[8][32];
+    __shared__ float sm[32][33];
     const int k = blockIdx.y, x = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
     if (!a.out[k]) return;
     float s = 0.f;
     if (c < a.d)
 #pragma unroll 8
-        for (int g = run; g < a.groups; g += 8) s += a.part[((long long)g * 4 + k) * a.d + c];
+        for (int g = run; g < a.blocks; g += 32) s += a.part[((long long)g * 4 + k) * a.d + c];
     sm[run][x] = s;
     __syncthreads();
-    if (run == 0 && c < a.d) {
+    // 32 runs of a channel to the lanes of one warp
+    s = sm[x][run];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sm[i][x];
-        a.out[k][c] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (x == 0 && blockIdx.x * 32 + run < a.d) a.out[k][blockIdx.x * 32 + run] = s;
 }
 
 // ---- which kernel takes a row -----------------------------------------------------------------
 // 8 channels a thread where every row can be read 16 bytes at a time; else one by one.
-struct Shape {
-    int nt, block;
-};
-Shape shape_of(int d, bool wide)
+// Shared memory of a kernel: the ring, or where row groups share a block the sums that it is reused for.
+template <typename T, typename R, int VEC, int NT, int NC, bool BWD> constexpr int ring_bytes(int d)
 {
-    if (!wide) return d <= 256 ? Shape{32, 256} : Shape{512, 512};
-    const int nt = d <= 256 ? 32 : d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : 512;
-    return {nt, std::max(nt, 256)};
+    constexpr int bt = Ahead<T, VEC, NC, bn_block<NT>>::BYTES, br = Ahead<R, VEC, NC, bn_block<NT>>::BYTES,
+                  stage = BWD ? 3 * bt + 2 * br : 2 * bt + br, ring = AHEAD<VEC, stage> * stage;
+    return BWD && NT < bn_block<NT> ? std::max(ring, 16 * d) : ring;
 }
-// Groups that run at once: as many blocks as fit two or more to an SM, each row group looping over its rows.
-int groups_of(long long rows, const Shape &s, int sms, int per_sm)
+
+// Blocks of a kernel that run at once on an SM, with its shared memory limit set; once a device and kernel.
+template <auto KERN> int blocks_at_once(int block, int smem)
 {
-    const int per_block = s.block / s.nt;
-    const long long blocks = std::min<long long>((rows + per_block - 1) / per_block, (long long)sms * per_sm);
-    return (int)blocks * per_block;
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if ((n = known[dev].load()) > 0) return n;
+    if (cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERN, block, (size_t)smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[dev].store(n);
+    return n;
 }
-constexpr int FWD_THREADS = 1024, BWD_THREADS = 512;  // of an SM's threads that the grids count on
+constexpr int BN_MOST_BLOCKS = 8;  // of an SM: 2048 threads in blocks of 256
 
 template <typename T, typename R, typename F> int by_shape(int d, bool wide, F &&f)
 {
@@ -535,13 +648,15 @@ int la_block_norm_fwd(const void *y, const void *residual, const void *gate, con
     const bool wide = d % 8 == 0 && ok(y, a.vy, es) && ok(residual, a.vr, er) && ok(gate, a.vg, es) && ok(h, a.vh, er) &&
                       ok(n, a.vn, es) && aligned(post_weight, 16) && aligned(post_bias, 16) && aligned(pre_weight, 16) &&
                       aligned(pre_bias, 16);
-    const Shape s = shape_of(d, wide);
-    const int grid = groups_of(a.rows, s, sms, std::max(1, FWD_THREADS / s.block)) / (s.block / s.nt);
     return by_types(dtype, residual_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
         return by_shape<T, R>(d, wide, [&](auto v, auto nt, auto nc) {
-            return launch(bn_fwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt>, 0, (cudaStream_t)stream, a);
+            constexpr int per_block = bn_block<nt> / nt, smem = ring_bytes<T, R, v, nt, nc, false>(0);
+            const int at_once = blocks_at_once<bn_fwd_kernel<T, R, v, nt, nc>>(bn_block<nt>, smem);
+            if (at_once <= 0) return (int)LA_ERR_CUDA;
+            const long long grid = std::min<long long>((a.rows + per_block - 1) / per_block, (long long)sms * at_once);
+            return launch(bn_fwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt>, smem, (cudaStream_t)stream, a);
         });
     });
 }
@@ -549,13 +664,10 @@ int la_block_norm_fwd(const void *y, const void *residual, const void *gate, con
 size_t la_block_norm_bwd_workspace_bytes(int B, int L, int d)
 {
     if (!sizes_ok(B, 1, L, d) || d > BN_MAX_D) return 0;
+    // as many blocks as an SM may hold, each at most one for a row
     const int sms = device_sms() > 0 ? device_sms() : 152;
-    size_t most = 0;  // whichever way the rows are aligned
-    for (const bool wide : {false, true}) {
-        const Shape s = shape_of(d, wide);
-        most = std::max(most, (size_t)groups_of((long long)B * L, s, sms, std::max(1, BWD_THREADS / s.block)));
-    }
-    return most * 4 * d * sizeof(float);
+    const long long blocks = std::min<long long>((long long)B * L, (long long)sms * BN_MOST_BLOCKS);
+    return (size_t)blocks * 4 * d * sizeof(float);
 }
 
 int la_block_norm_bwd(const void *y, const void *residual, const void *gate, const float *post_weight, const float *post_bias,
@@ -603,23 +715,27 @@ int la_block_norm_bwd(const void *y, const void *residual, const void *gate, con
     const bool wide = d % 8 == 0 && ok(y, a.vy, es) && ok(residual, a.vr, er) && ok(gate, a.vg, es) && ok(dh, a.vdh, er) &&
                       ok(dn, a.vdn, es) && ok(dresidual, a.vdr, er) && ok(dy, a.vdy, es) && ok(dgate, a.vdg, es) &&
                       aligned(post_weight, 16) && aligned(post_bias, 16) && aligned(pre_weight, 16) && aligned(pre_bias, 16);
-    const Shape s = shape_of(d, wide);
-    const int groups = groups_of(a.rows, s, sms, std::max(1, BWD_THREADS / s.block)), grid = groups / (s.block / s.nt);
-    const bool sums = dpost_weight || dpost_bias || dpre_weight || dpre_bias;
-    if (sums) {
-        if (!workspace || workspace_bytes < (size_t)groups * 4 * d * sizeof(float)) return LA_ERR_WORKSPACE;
-        a.part = (float *)workspace;
-    }
+    a.sums = (dpost_weight ? 1 : 0) | (dpost_bias ? 2 : 0) | (dpre_weight ? 4 : 0) | (dpre_bias ? 8 : 0);
+    long long blocks = 0;
     const int rc = by_types(dtype, residual_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
         return by_shape<T, R>(d, wide, [&](auto v, auto nt, auto nc) {
-            return launch(bn_bwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt>, 0, (cudaStream_t)stream, a);
+            constexpr int per_block = bn_block<nt> / nt;
+            const int most = v == 8 ? 8 * nt * nc : nt * nc, smem = ring_bytes<T, R, v, nt, nc, true>(most);  // for every d of it
+            const int at_once = blocks_at_once<bn_bwd_kernel<T, R, v, nt, nc>>(bn_block<nt>, smem);
+            if (at_once <= 0) return (int)LA_ERR_CUDA;
+            blocks = std::min<long long>((a.rows + per_block - 1) / per_block, (long long)sms * std::min(at_once, BN_MOST_BLOCKS));
+            if (a.sums) {
+                if (!workspace || workspace_bytes < (size_t)blocks * 4 * d * sizeof(float)) return (int)LA_ERR_WORKSPACE;
+                a.part = (float *)workspace;
+            }
+            return launch(bn_bwd_kernel<T, R, v, nt, nc>, dim3((unsigned)blocks), bn_block<nt>, smem, (cudaStream_t)stream, a);
         });
     });
-    if (rc != LA_OK || !sums) return rc;
-    const BnJoin j{a.part, {dpost_weight, dpost_bias, dpre_weight, dpre_bias}, groups, d};
-    return launch(bn_join_kernel, dim3((unsigned)((d + 31) / 32), 4), 256, 0, (cudaStream_t)stream, j);
+    if (rc != LA_OK || !a.sums) return rc;
+    const BnJoin j{a.part, {dpost_weight, dpost_bias, dpre_weight, dpre_bias}, (int)blocks, d};
+    return launch(bn_join_kernel, dim3((unsigned)((d + 31) / 32), 4), 1024, 0, (cudaStream_t)stream, j);
 }
 
 }  // extern "C"
