@@ -34,7 +34,7 @@ struct BnArgs {
     const void *y, *r, *gate, *dh, *dn;
     void *h, *n, *dr, *dy, *dgate;
     const float *post_w, *post_b, *pre_w, *pre_b;
-    float *part;  // [blocks][4][d]: sums for post_w, post_b, pre_w, pre_b
+    float *part;  // [blocks][4][d]: sums for post_w, pre_w, post_b, pre_b
     int sums;     // bit k: the k-th of them is wanted
     View vy, vr, vg, vh, vn, vdh, vdn, vdr, vdy, vdg;
     long long rows;
@@ -108,10 +108,28 @@ template <int VEC> __device__ __forceinline__ void weights(const float *w, int c
     }
 }
 
+// A thread's N channels as pairs for the packed instructions, or one by one.
+template <int VEC> constexpr int WIDTH = VEC > 1 ? 2 : 1;
+template <int W> __device__ __forceinline__ Ch<W> less(const Ch<W> &x, const Ch<W> &y) { return fma(y, all<W>(-1.f), x); }
+template <int W, int M> __device__ __forceinline__ float over(const Ch<W> (&x)[M])  // sum
+{
+    Ch<W> s = x[0];
+#pragma unroll
+    for (int i = 1; i < M; ++i) s = add(s, x[i]);
+    return W == 2 ? s.v[0] + s.v[W - 1] : s.v[0];
+}
+template <int W, int M> __device__ __forceinline__ float over(const Ch<W> (&x)[M], const Ch<W> (&y)[M])  // of products
+{
+    Ch<W> s = mul(x[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < M; ++i) s = fma(x[i], y[i], s);
+    return W == 2 ? s.v[0] + s.v[W - 1] : s.v[0];
+}
+
 // ---- sums over the threads of a row, the same in every one of them -----------------------------
 // Two places in turn, so that one barrier a sum is enough: who writes a place again has passed the
 // barrier behind the sum that everyone read it for.
-template <int NT> struct Sums {
+template <int NT, bool WHOLE> struct Sums {  // WHOLE: the row's threads are the block
     float *sm;  // [2][NT / 32][2]
     int turn = 0;
     template <int N> __device__ __forceinline__ void operator()(float (&v)[N])
@@ -125,17 +143,17 @@ template <int NT> struct Sums {
             const int t = threadIdx.x % NT;
             float *p = sm + turn * W * 2;
             turn ^= 1;
-            if ((t & 31) == 0)
-#pragma unroll
-                for (int i = 0; i < N; ++i) p[(t >> 5) * 2 + i] = v[i];
-            if constexpr (NT >= 256) __syncthreads();  // one row a block
+            if ((t & 31) == 0) *(float2 *)(p + (t >> 5) * 2) = make_float2(v[0], N > 1 ? v[N - 1] : 0.f);
+            if constexpr (WHOLE) __syncthreads();
             else ptx::named_bar(1 + threadIdx.x / NT, NT);
+            Ch<2> s = all<2>(0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = 0.f;
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-#pragma unroll
-                for (int i = 0; i < N; ++i) v[i] += p[w * 2 + i];
+            for (int w = 0; w < W; ++w) {
+                const float2 q = *(const float2 *)(p + w * 2);
+                s = add(s, Ch<2>{{q.x, q.y}});
+            }
+            v[0] = s.v[0];
+            if (N > 1) v[N - 1] = s.v[1];
         }
     }
 };
@@ -145,27 +163,48 @@ template <int NT> struct Sums {
 template <typename T> __device__ __forceinline__ float sigmoid(float z)
 {
     if constexpr (std::is_same<T, float>::value) return 1.f / (1.f + expf(-z));
-    else return __fdividef(1.f, 1.f + __expf(-z));
+    else return rcp(1.f + ex2(-1.44269504f * z));
 }
 
-// A row's mean and 1/deviation, x centred in place where the kind asks for it.
-template <int NT, int N> __device__ __forceinline__ float statistics(float (&x)[N], const bool (&in)[N], int kind, const BnArgs &a, Sums<NT> &sum)
+// Channels of chunks that are not there, back to 0.
+template <int VEC, int W, int M, int NC> __device__ __forceinline__ void clear(Ch<W> (&x)[M], const bool (&in)[NC])
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+        if (!in[i * W / VEC]) x[i] = all<W>(0.f);
+}
+
+// A row's 1/deviation; x centred in place where the kind asks for it.
+template <int VEC, int W, int M, int NC, typename S>
+__device__ __forceinline__ float statistics(Ch<W> (&x)[M], const bool (&in)[NC], int kind, const BnArgs &a, S &sum)
 {
     if (kind == LA_NORM_LAYER) {
-        float m[1] = {0.f};
-#pragma unroll
-        for (int i = 0; i < N; ++i) m[0] += x[i];
+        float m[1] = {over(x)};
         sum(m);
-        m[0] *= a.inv_d;
+        const Ch<W> mean = all<W>(m[0] * a.inv_d);
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = in[i] ? x[i] - m[0] : 0.f;
+        for (int i = 0; i < M; ++i) x[i] = less(x[i], mean);
+        clear<VEC>(x, in);
     }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[0] = fmaf(x[i], x[i], s[0]);
+    float s[1] = {over(x, x)};
     sum(s);
     return rsqrtf(fmaf(s[0], a.inv_d, a.eps));
 }
+
+// Row numbers b, t of B x L stepping by a fixed number of rows, without a division a row.
+struct RowAt {
+    int b, t;
+    __device__ __forceinline__ RowAt(long long row, int L) : b((int)(row / L)), t((int)(row % L)) {}
+    __device__ __forceinline__ void next(int step_b, int step_t, int L)
+    {
+        b += step_b;
+        t += step_t;
+        if (t >= L) {
+            t -= L;
+            ++b;
+        }
+    }
+};
 
 template <int NT> constexpr int bn_block = NT < 256 ? 256 : NT;
 
@@ -231,22 +270,46 @@ template <int VEC, int PF> __device__ __forceinline__ void row_arrived()
     if constexpr (VEC == 8) asm volatile("cp.async.wait_group %0;" ::"n"(PF - 1) : "memory");
 }
 
+// What both kernels begin with: the row group's first row, its channels, and the gate's activation.
+#define BN_ROWS(STEP_ROWS)                                                                                             \
+    constexpr int N = VEC * NC, W = WIDTH<VEC>, M = N / W, GROUPS = bn_block<NT> / NT;                                  \
+    __shared__ __align__(16) float sm[GROUPS * 2 * (NT / 32) * 2];                                                       \
+    const int tid = threadIdx.x % NT, group = threadIdx.x / NT;                                                        \
+    Sums<NT, GROUPS == 1> sum{sm + group * 2 * (NT / 32) * 2};                                                          \
+    const long long first = (long long)blockIdx.x * GROUPS + group, STEP_ROWS = (long long)gridDim.x * GROUPS;          \
+    const int step_b = (int)(STEP_ROWS / a.L), step_t = (int)(STEP_ROWS % a.L);                                         \
+    int at[NC];                                                                                                         \
+    bool in[NC];                                                                                                        \
+    _Pragma("unroll") for (int c = 0; c < NC; ++c)                                                                      \
+    {                                                                                                                   \
+        at[c] = (c * NT + tid) * VEC;                                                                                   \
+        in[c] = at[c] < a.d;                                                                                            \
+    }
+
+// V channels of a chunk at f as pairs
+template <int W, int M> __device__ __forceinline__ float *flat(Ch<W> (&x)[M], int i) { return &x[i / W].v[i % W]; }
+
+// act(z), and s = sigmoid(z) where the activation has it.
+template <typename T, int W, int M> __device__ __forceinline__ void activate(const Ch<W> (&z)[M], Ch<W> (&s)[M], Ch<W> (&act)[M], const BnArgs &a)
+{
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        if (!a.gate) {
+            act[i] = all<W>(1.f);
+        } else if (a.act == LA_ACT_NONE) {
+            act[i] = z[i];
+        } else {
+#pragma unroll
+            for (int u = 0; u < W; ++u) s[i].v[u] = sigmoid<T>(z[i].v[u]);
+            act[i] = a.act == LA_ACT_SILU ? mul(z[i], s[i]) : s[i];
+        }
+    }
+}
+
 template <typename T, typename R, int VEC, int NT, int NC>
 __global__ void __launch_bounds__(bn_block<NT>, 1) bn_fwd_kernel(const BnArgs a)
 {
-    constexpr int N = VEC * NC, GROUPS = bn_block<NT> / NT;
-    __shared__ float sm[GROUPS * 2 * (NT / 32) * 2];
-    const int tid = threadIdx.x % NT, group = threadIdx.x / NT;
-    Sums<NT> sum{sm + group * 2 * (NT / 32) * 2};
-    const long long first = (long long)blockIdx.x * GROUPS + group, step = (long long)gridDim.x * GROUPS;
-    int at[NC];
-    bool in[N];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        at[c] = (c * NT + tid) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) in[c * VEC + i] = at[c] < a.d;
-    }
+    BN_ROWS(step)
     extern __shared__ __align__(16) uint8_t ring[];
     constexpr int BLOCK = bn_block<NT>, BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES, STAGE = 2 * BT + BR,
                   PF = AHEAD<VEC, STAGE>;
@@ -256,109 +319,98 @@ __global__ void __launch_bounds__(bn_block<NT>, 1) bn_fwd_kernel(const BnArgs a)
     ry.place(ring_at, STAGE);
     rg.place(ring_at + BT, STAGE);
     rr.place(ring_at + 2 * BT, STAGE);
+    RowAt ahead(first, a.L), now(first, a.L);
     auto fetch = [&](long long row, int slot) {
         if (row < a.rows) {
-            const int b = (int)(row / a.L), t = (int)(row % a.L);
-            ry.fetch((const T *)a.y + row_of(a.vy, b, 0, t), slot, at, a.d);
-            rr.fetch((const R *)a.r + row_of(a.vr, b, 0, t), slot, at, a.d);
-            if (a.gate) rg.fetch((const T *)a.gate + row_of(a.vg, b, 0, t), slot, at, a.d);
+            ry.fetch((const T *)a.y + row_of(a.vy, ahead.b, 0, ahead.t), slot, at, a.d);
+            rr.fetch((const R *)a.r + row_of(a.vr, ahead.b, 0, ahead.t), slot, at, a.d);
+            if (a.gate) rg.fetch((const T *)a.gate + row_of(a.vg, ahead.b, 0, ahead.t), slot, at, a.d);
         }
+        ahead.next(step_b, step_t, a.L);
         row_issued<VEC>();
     };
 #pragma unroll
     for (int i = 0; i < PF; ++i) fetch(first + i * step, i);
     int slot = 0;
     for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
-        float u[N], h[N], z[N];
+        Ch<W> u[M], h[M], act[M];
+        {
+            Ch<W> z[M], sg[M];
 #pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = h[i] = z[i] = 0.f;
-        row_arrived<VEC, PF>();
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (in[c * VEC]) {
-                ry.get(u + c * VEC, slot, c);
-                rr.get(h + c * VEC, slot, c);
-                if (a.gate) rg.get(z + c * VEC, slot, c);
-            }
-        fetch(row + PF * step, slot);
-        const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<NT>(u, in, a.post, a, sum);
-        const int b = (int)(row / a.L), t = (int)(row % a.L);
-        R *const ho = (R *)a.h + row_of(a.vh, b, 0, t);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (in[c * VEC]) {
-                float w[VEC], bias[VEC];
-                weights<VEC>(a.post_w, at[c], 1.f, w);
-                weights<VEC>(a.post_b, at[c], 0.f, bias);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int j = c * VEC + i;
-                    float act = a.bs;
-                    if (a.gate) {
-                        if (a.act == LA_ACT_NONE) act *= z[j];
-                        else act *= sigmoid<T>(z[j]) * (a.act == LA_ACT_SILU ? z[j] : 1.f);
-                    }
-                    h[j] = fmaf(act, fmaf(u[j] * k1, w[i], bias[i]), a.rs * h[j]);
-                }
-                put<VEC>(ho + at[c], h + c * VEC);
-            }
-        if (a.n) {
-            const float k2 = statistics<NT>(h, in, a.pre, a, sum);
-            T *const no = (T *)a.n + row_of(a.vn, b, 0, t);
+            for (int i = 0; i < M; ++i) u[i] = h[i] = z[i] = all<W>(0.f);
+            row_arrived<VEC, PF>();
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-                if (in[c * VEC]) {
-                    float w[VEC], bias[VEC], o[VEC];
-                    weights<VEC>(a.pre_w, at[c], 1.f, w);
-                    weights<VEC>(a.pre_b, at[c], 0.f, bias);
+                if (in[c]) {
+                    ry.get(flat(u, c * VEC), slot, c);
+                    rr.get(flat(h, c * VEC), slot, c);
+                    if (a.gate) rg.get(flat(z, c * VEC), slot, c);
+                }
+            fetch(row + PF * step, slot);
+            activate<T>(z, sg, act, a);
+        }
+        const Ch<W> k1 = all<W>(a.bs * (a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum))), bs = all<W>(a.bs),
+                    rs = all<W>(a.rs);
+        R *const ho = (R *)a.h + row_of(a.vh, now.b, 0, now.t);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) o[i] = fmaf(h[c * VEC + i] * k2, w[i], bias[i]);
-                    put<VEC>(no + at[c], o);
+        for (int c = 0; c < NC; ++c)
+            if (in[c]) {
+                Ch<W> w[VEC / W], bias[VEC / W];
+                weights<VEC>(a.post_w, at[c], 1.f, w[0].v);
+                if (a.post_b) weights<VEC>(a.post_b, at[c], 0.f, bias[0].v);
+#pragma unroll
+                for (int i = 0; i < VEC / W; ++i) {
+                    const int m = c * VEC / W + i;
+                    Ch<W> x = mul(mul(u[m], k1), w[i]);
+                    if (a.post_b) x = fma(bias[i], bs, x);
+                    h[m] = fma(act[m], x, mul(rs, h[m]));
+                }
+                put<VEC>(ho + at[c], flat(h, c * VEC));
+            }
+        if (a.n) {
+            const Ch<W> k2 = all<W>(statistics<VEC>(h, in, a.pre, a, sum));
+            T *const no = (T *)a.n + row_of(a.vn, now.b, 0, now.t);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c]) {
+                    Ch<W> w[VEC / W], bias[VEC / W], o[VEC / W];
+                    weights<VEC>(a.pre_w, at[c], 1.f, w[0].v);
+                    weights<VEC>(a.pre_b, at[c], 0.f, bias[0].v);
+#pragma unroll
+                    for (int i = 0; i < VEC / W; ++i) o[i] = fma(mul(h[c * VEC / W + i], k2), w[i], bias[i]);
+                    put<VEC>(no + at[c], o[0].v);
                 }
         }
+        now.next(step_b, step_t, a.L);
     }
 }
 
 // dx of x/deviation (centred) from dxh, in place, with xh: (dxh - xh mean(dxh xh) [- mean(dxh)]) k.
-template <int NT, int N> __device__ __forceinline__ void norm_back(float (&dxh)[N], const float (&xh)[N], const bool (&in)[N], float k,
-                                                                   int kind, const BnArgs &a, Sums<NT> &sum)
+template <int VEC, int W, int M, int NC, typename S>
+__device__ __forceinline__ void norm_back(Ch<W> (&dxh)[M], const Ch<W> (&xh)[M], const bool (&in)[NC], float k, int kind, const BnArgs &a,
+                                          S &sum)
 {
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        s[0] = fmaf(dxh[i], xh[i], s[0]);
-        s[1] += dxh[i];
-    }
+    float s[2] = {over(dxh, xh), kind == LA_NORM_LAYER ? over(dxh) : 0.f};
     sum(s);
-    const float m0 = s[0] * a.inv_d, m1 = kind == LA_NORM_LAYER ? s[1] * a.inv_d : 0.f;
+    const Ch<W> m0 = all<W>(-s[0] * a.inv_d), m1 = all<W>(-s[1] * a.inv_d), kk = all<W>(k);
 #pragma unroll
-    for (int i = 0; i < N; ++i) dxh[i] = in[i] ? (dxh[i] - fmaf(xh[i], m0, m1)) * k : 0.f;
+    for (int i = 0; i < M; ++i) dxh[i] = mul(add(dxh[i], fma(xh[i], m0, m1)), kk);  // k last: what cancels is not scaled up first
+    if (kind == LA_NORM_LAYER) clear<VEC>(dxh, in);
 }
 
-template <typename T, typename R, int VEC, int NT, int NC>
+// BIAS: sums for the biases too.
+template <typename T, typename R, int VEC, int NT, int NC, bool BIAS>
 __global__ void __launch_bounds__(bn_block<NT>, 1) bn_bwd_kernel(const BnArgs a)
 {
-    constexpr int N = VEC * NC, GROUPS = bn_block<NT> / NT;
-    __shared__ float sm[GROUPS * 2 * (NT / 32) * 2];
-    const int tid = threadIdx.x % NT, group = threadIdx.x / NT;
-    Sums<NT> sum{sm + group * 2 * (NT / 32) * 2};
-    const long long first = (long long)blockIdx.x * GROUPS + group, step = (long long)gridDim.x * GROUPS;
-    int at[NC];
-    bool in[N];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        at[c] = (c * NT + tid) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) in[c * VEC + i] = at[c] < a.d;
-    }
-    float total[4][N];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int i = 0; i < N; ++i) total[k][i] = 0.f;
+    BN_ROWS(step)
     extern __shared__ __align__(16) uint8_t ring[];
     constexpr int BLOCK = bn_block<NT>, BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES,
                   STAGE = 3 * BT + 2 * BR, PF = AHEAD<VEC, STAGE>;
+    Ch<W> total[BIAS ? 4 : 2][M];  // post_w, pre_w, post_b, pre_b
+#pragma unroll
+    for (int k = 0; k < (BIAS ? 4 : 2); ++k)
+#pragma unroll
+        for (int i = 0; i < M; ++i) total[k][i] = all<W>(0.f);
     Ahead<T, VEC, NC, BLOCK> ry, rg, rdn;
     Ahead<R, VEC, NC, BLOCK> rr, rdh;
     const uint32_t ring_at = ptx::smem_u32(ring);
@@ -367,123 +419,133 @@ __global__ void __launch_bounds__(bn_block<NT>, 1) bn_bwd_kernel(const BnArgs a)
     rdn.place(ring_at + 2 * BT, STAGE);
     rr.place(ring_at + 3 * BT, STAGE);
     rdh.place(ring_at + 3 * BT + BR, STAGE);
+    RowAt ahead(first, a.L), now(first, a.L);
     auto fetch = [&](long long row, int slot) {
         if (row < a.rows) {
-            const int b = (int)(row / a.L), t = (int)(row % a.L);
-            ry.fetch((const T *)a.y + row_of(a.vy, b, 0, t), slot, at, a.d);
-            rr.fetch((const R *)a.r + row_of(a.vr, b, 0, t), slot, at, a.d);
-            if (a.gate) rg.fetch((const T *)a.gate + row_of(a.vg, b, 0, t), slot, at, a.d);
-            if (a.dh) rdh.fetch((const R *)a.dh + row_of(a.vdh, b, 0, t), slot, at, a.d);
-            if (a.dn) rdn.fetch((const T *)a.dn + row_of(a.vdn, b, 0, t), slot, at, a.d);
+            ry.fetch((const T *)a.y + row_of(a.vy, ahead.b, 0, ahead.t), slot, at, a.d);
+            rr.fetch((const R *)a.r + row_of(a.vr, ahead.b, 0, ahead.t), slot, at, a.d);
+            if (a.gate) rg.fetch((const T *)a.gate + row_of(a.vg, ahead.b, 0, ahead.t), slot, at, a.d);
+            if (a.dh) rdh.fetch((const R *)a.dh + row_of(a.vdh, ahead.b, 0, ahead.t), slot, at, a.d);
+            if (a.dn) rdn.fetch((const T *)a.dn + row_of(a.vdn, ahead.b, 0, ahead.t), slot, at, a.d);
         }
+        ahead.next(step_b, step_t, a.L);
         row_issued<VEC>();
     };
 #pragma unroll
     for (int i = 0; i < PF; ++i) fetch(first + i * step, i);
     int slot = 0;
     for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
-        float u[N], h[N], z[N], dh[N], dn[N];
+        Ch<W> u[M], h[M], z[M], sg[M], act[M], dh[M], dn[M];
 #pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = h[i] = z[i] = dh[i] = dn[i] = 0.f;
+        for (int i = 0; i < M; ++i) u[i] = h[i] = z[i] = dh[i] = dn[i] = all<W>(0.f);
         row_arrived<VEC, PF>();
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            if (in[c * VEC]) {
-                ry.get(u + c * VEC, slot, c);
-                rr.get(h + c * VEC, slot, c);
-                if (a.gate) rg.get(z + c * VEC, slot, c);
-                if (a.dh) rdh.get(dh + c * VEC, slot, c);
-                if (a.dn) rdn.get(dn + c * VEC, slot, c);
+            if (in[c]) {
+                ry.get(flat(u, c * VEC), slot, c);
+                rr.get(flat(h, c * VEC), slot, c);
+                if (a.gate) rg.get(flat(z, c * VEC), slot, c);
+                if (a.dh) rdh.get(flat(dh, c * VEC), slot, c);
+                if (a.dn) rdn.get(flat(dn, c * VEC), slot, c);
             }
         fetch(row + PF * step, slot);
-        const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<NT>(u, in, a.post, a, sum);
-        const int b = (int)(row / a.L), t = (int)(row % a.L);
-        float act[N];  // act(gate), times branch_scale
+        activate<T>(z, sg, act, a);
+        const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum);
+        const Ch<W> k1w = all<W>(k1), bs = all<W>(a.bs), rs = all<W>(a.rs);
+        // x = w xh + b of the norm behind the block
+        auto post = [&](int c, Ch<W> (&w)[VEC / W], Ch<W> (&x)[VEC / W]) {
+            weights<VEC>(a.post_w, at[c], 1.f, w[0].v);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float w[VEC], bias[VEC];
+            for (int i = 0; i < VEC / W; ++i) x[i] = mul(u[c * VEC / W + i], w[i]);
+            if (a.post_b) {
+                Ch<W> bias[VEC / W];
+                weights<VEC>(a.post_b, at[c], 0.f, bias[0].v);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) w[i] = bias[i] = 0.f;
-            if (in[c * VEC]) {
-                weights<VEC>(a.post_w, at[c], 1.f, w);
-                weights<VEC>(a.post_b, at[c], 0.f, bias);
+                for (int i = 0; i < VEC / W; ++i) x[i] = add(x[i], bias[i]);
             }
+        };
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int j = c * VEC + i;
-                act[j] = a.bs;
-                if (a.gate) {
-                    if (a.act == LA_ACT_NONE) act[j] *= z[j];
-                    else act[j] *= sigmoid<T>(z[j]) * (a.act == LA_ACT_SILU ? z[j] : 1.f);
-                }
-                u[j] *= k1;  // xh of y from here on
-                h[j] = in[j] ? fmaf(act[j], fmaf(u[j], w[i], bias[i]), a.rs * h[j]) : 0.f;
-            }
+        for (int i = 0; i < M; ++i) {
+            u[i] = mul(u[i], k1w);  // xh of y from here on
+            act[i] = mul(act[i], bs);
         }
         if (a.dn) {
-            const float k2 = statistics<NT>(h, in, a.pre, a, sum);
-            float g[N];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                float w[VEC];
+            for (int c = 0; c < NC; ++c)
+                if (in[c]) {
+                    Ch<W> w[VEC / W], x[VEC / W];
+                    post(c, w, x);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) w[i] = 0.f;
-                if (in[c * VEC]) weights<VEC>(a.pre_w, at[c], 1.f, w);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const int j = c * VEC + i;
-                    h[j] *= k2;
-                    total[2][j] = fmaf(dn[j], h[j], total[2][j]);
-                    total[3][j] += dn[j];
-                    g[j] = dn[j] * w[i];
+                    for (int i = 0; i < VEC / W; ++i) {
+                        const int m = c * VEC / W + i;
+                        h[m] = fma(act[m], x[i], mul(rs, h[m]));
+                    }
                 }
-            }
-            norm_back<NT>(g, h, in, k2, a.pre, a, sum);
+            const float k2 = statistics<VEC>(h, in, a.pre, a, sum);
+            const Ch<W> k2w = all<W>(k2);
+            Ch<W> g[M];
 #pragma unroll
-            for (int i = 0; i < N; ++i) dh[i] += g[i];
+            for (int i = 0; i < M; ++i) {
+                h[i] = mul(h[i], k2w);
+                total[1][i] = fma(dn[i], h[i], total[1][i]);
+                if (BIAS) total[BIAS ? 3 : 0][i] = add(total[BIAS ? 3 : 0][i], dn[i]);
+                g[i] = dn[i];
+            }
+            if (a.pre_w)
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (in[c]) {
+                        Ch<W> w[VEC / W];
+                        weights<VEC>(a.pre_w, at[c], 1.f, w[0].v);
+#pragma unroll
+                        for (int i = 0; i < VEC / W; ++i) g[c * VEC / W + i] = mul(dn[c * VEC / W + i], w[i]);
+                    }
+            norm_back<VEC>(g, h, in, k2, a.pre, a, sum);
+#pragma unroll
+            for (int i = 0; i < M; ++i) dh[i] = add(dh[i], g[i]);
         }
         // dh is the whole gradient of h
-        R *const dr = (R *)a.dr + row_of(a.vdr, b, 0, t);
-        T *const dg = (T *)a.dgate + row_of(a.vdg, b, 0, t);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float w[VEC], bias[VEC], o[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) w[i] = bias[i] = 0.f;
-            if (in[c * VEC]) {
-                weights<VEC>(a.post_w, at[c], 1.f, w);
-                weights<VEC>(a.post_b, at[c], 0.f, bias);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = a.rs * dh[c * VEC + i];
-                put<VEC>(dr + at[c], o);
-                if (a.gate) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const int j = c * VEC + i;
-                        float slope = 1.f;
-                        if (a.act != LA_ACT_NONE) {
-                            const float s = sigmoid<T>(z[j]);
-                            slope = a.act == LA_ACT_SILU ? s * fmaf(z[j], 1.f - s, 1.f) : s * (1.f - s);
-                        }
-                        o[i] = a.bs * dh[j] * fmaf(u[j], w[i], bias[i]) * slope;
-                    }
-                    put<VEC>(dg + at[c], o);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int j = c * VEC + i;
-                const float du = dh[j] * act[j];
-                total[0][j] = fmaf(du, u[j], total[0][j]);
-                total[1][j] += du;
-                dh[j] = du * w[i];
-            }
-        }
-        if (a.post != LA_NORM_NONE) norm_back<NT>(dh, u, in, k1, a.post, a, sum);
-        T *const dy = (T *)a.dy + row_of(a.vdy, b, 0, t);
+        R *const dr = (R *)a.dr + row_of(a.vdr, now.b, 0, now.t);
+        T *const dg = (T *)a.dgate + row_of(a.vdg, now.b, 0, now.t);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            if (in[c * VEC]) put<VEC>(dy + at[c], dh + c * VEC);
+            if (in[c]) {
+                Ch<W> w[VEC / W], x[VEC / W], o[VEC / W];
+#pragma unroll
+                for (int i = 0; i < VEC / W; ++i) o[i] = mul(rs, dh[c * VEC / W + i]);
+                put<VEC>(dr + at[c], o[0].v);
+                post(c, w, x);
+                if (a.gate) {
+#pragma unroll
+                    for (int i = 0; i < VEC / W; ++i) {
+                        const int m = c * VEC / W + i;
+                        o[i] = mul(mul(bs, dh[m]), x[i]);
+                        // slope: s (1 + z (1 - s)), s (1 - s), or 1
+                        if (a.act != LA_ACT_NONE) {
+                            const Ch<W> rest = less(all<W>(1.f), sg[m]);
+                            o[i] = mul(o[i], mul(sg[m], a.act == LA_ACT_SILU ? fma(z[m], rest, all<W>(1.f)) : rest));
+                        }
+                    }
+                    put<VEC>(dg + at[c], o[0].v);
+                }
+#pragma unroll
+                for (int i = 0; i < VEC / W; ++i) {
+                    const int m = c * VEC / W + i;
+                    const Ch<W> du = mul(dh[m], act[m]);
+                    total[0][m] = fma(du, u[m], total[0][m]);
+                    if (BIAS) total[BIAS ? 2 : 0][m] = add(total[BIAS ? 2 : 0][m], du);
+                    dh[m] = mul(du, w[i]);
+                }
+            }
+        if (a.post != LA_NORM_NONE) {
+            clear<VEC>(dh, in);
+            norm_back<VEC>(dh, u, in, k1, a.post, a, sum);
+        }
+        T *const dy = (T *)a.dy + row_of(a.vdy, now.b, 0, now.t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (in[c]) put<VEC>(dy + at[c], flat(dh, c * VEC));
+        now.next(step_b, step_t, a.L);
     }
     if (a.part) {
         // the block's row groups one after the other into shared memory, then the block's sums
@@ -494,13 +556,13 @@ __global__ void __launch_bounds__(bn_block<NT>, 1) bn_bwd_kernel(const BnArgs a)
                 __syncthreads();
                 if (group == g)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < (BIAS ? 4 : 2); ++k)
                         if (a.sums >> k & 1)
 #pragma unroll
                             for (int i = 0; i < N; ++i)
-                                if (in[i]) {
+                                if (in[i / VEC]) {
                                     float *const p = acc + k * a.d + at[i / VEC] + i % VEC;
-                                    *p = g == 0 ? total[k][i] : *p + total[k][i];
+                                    *p = g == 0 ? total[k][i / W].v[i % W] : *p + total[k][i / W].v[i % W];
                                 }
             }
             __syncthreads();
@@ -508,11 +570,11 @@ __global__ void __launch_bounds__(bn_block<NT>, 1) bn_bwd_kernel(const BnArgs a)
                 if (a.sums >> (i / a.d) & 1) a.part[(long long)blockIdx.x * 4 * a.d + i] = acc[i];
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < (BIAS ? 4 : 2); ++k)
                 if (a.sums >> k & 1)
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        if (in[c * VEC]) put<VEC>(a.part + ((long long)blockIdx.x * 4 + k) * a.d + at[c], total[k] + c * VEC);
+                        if (in[c]) put<VEC>(a.part + ((long long)blockIdx.x * 4 + k) * a.d + at[c], flat(total[k], c * VEC));
         }
     }
 }
@@ -568,10 +630,8 @@ template <auto KERN> int blocks_at_once(int block, int smem)
 }
 constexpr int BN_MOST_BLOCKS = 8;  // of an SM: 2048 threads in blocks of 256
 
-template <typename T, typename R, typename F> int by_shape(int d, bool wide, F &&f)
+template <bool WIDE, typename F> int by_shape(int d, bool wide, F &&f)
 {
-    (void)sizeof(T);
-    (void)sizeof(R);
     if (!wide)
         return d <= 256 ? f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>(), std::integral_constant<int, 8>())
                         : f(std::integral_constant<int, 1>(), std::integral_constant<int, 512>(), std::integral_constant<int, 16>());
@@ -579,10 +639,17 @@ template <typename T, typename R, typename F> int by_shape(int d, bool wide, F &
     std::integral_constant<int, 1> one;
     std::integral_constant<int, 2> two;
     if (d <= 256) return f(v, std::integral_constant<int, 32>(), one);
-    if (d <= 512) return f(v, std::integral_constant<int, 64>(), one);
-    if (d <= 1024) return f(v, std::integral_constant<int, 128>(), one);
-    if (d <= 2048) return f(v, std::integral_constant<int, 256>(), one);
-    if (d <= 4096) return f(v, std::integral_constant<int, 512>(), one);
+    if constexpr (WIDE) {
+        if (d <= 512) return f(v, std::integral_constant<int, 32>(), two);
+        if (d <= 1024) return f(v, std::integral_constant<int, 64>(), two);
+        if (d <= 2048) return f(v, std::integral_constant<int, 128>(), two);
+        if (d <= 4096) return f(v, std::integral_constant<int, 256>(), two);
+    } else {
+        if (d <= 512) return f(v, std::integral_constant<int, 64>(), one);
+        if (d <= 1024) return f(v, std::integral_constant<int, 128>(), one);
+        if (d <= 2048) return f(v, std::integral_constant<int, 256>(), one);
+        if (d <= 4096) return f(v, std::integral_constant<int, 512>(), one);
+    }
     return f(v, std::integral_constant<int, 512>(), two);
 }
 template <typename F> int by_types(int dtype, int rtype, F &&f)
@@ -651,7 +718,7 @@ int la_block_norm_fwd(const void *y, const void *residual, const void *gate, con
     return by_types(dtype, residual_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        return by_shape<T, R>(d, wide, [&](auto v, auto nt, auto nc) {
+        return by_shape<false>(d, wide, [&](auto v, auto nt, auto nc) {
             constexpr int per_block = bn_block<nt> / nt, smem = ring_bytes<T, R, v, nt, nc, false>(0);
             const int at_once = blocks_at_once<bn_fwd_kernel<T, R, v, nt, nc>>(bn_block<nt>, smem);
             if (at_once <= 0) return (int)LA_ERR_CUDA;
@@ -715,26 +782,29 @@ int la_block_norm_bwd(const void *y, const void *residual, const void *gate, con
     const bool wide = d % 8 == 0 && ok(y, a.vy, es) && ok(residual, a.vr, er) && ok(gate, a.vg, es) && ok(dh, a.vdh, er) &&
                       ok(dn, a.vdn, es) && ok(dresidual, a.vdr, er) && ok(dy, a.vdy, es) && ok(dgate, a.vdg, es) &&
                       aligned(post_weight, 16) && aligned(post_bias, 16) && aligned(pre_weight, 16) && aligned(pre_bias, 16);
-    a.sums = (dpost_weight ? 1 : 0) | (dpost_bias ? 2 : 0) | (dpre_weight ? 4 : 0) | (dpre_bias ? 8 : 0);
+    a.sums = (dpost_weight ? 1 : 0) | (dpre_weight ? 2 : 0) | (dpost_bias ? 4 : 0) | (dpre_bias ? 8 : 0);
     long long blocks = 0;
     const int rc = by_types(dtype, residual_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        return by_shape<T, R>(d, wide, [&](auto v, auto nt, auto nc) {
+        return by_shape<true>(d, wide, [&](auto v, auto nt, auto nc) {
             constexpr int per_block = bn_block<nt> / nt;
             const int most = v == 8 ? 8 * nt * nc : nt * nc, smem = ring_bytes<T, R, v, nt, nc, true>(most);  // for every d of it
-            const int at_once = blocks_at_once<bn_bwd_kernel<T, R, v, nt, nc>>(bn_block<nt>, smem);
-            if (at_once <= 0) return (int)LA_ERR_CUDA;
-            blocks = std::min<long long>((a.rows + per_block - 1) / per_block, (long long)sms * std::min(at_once, BN_MOST_BLOCKS));
-            if (a.sums) {
-                if (!workspace || workspace_bytes < (size_t)blocks * 4 * d * sizeof(float)) return (int)LA_ERR_WORKSPACE;
-                a.part = (float *)workspace;
-            }
-            return launch(bn_bwd_kernel<T, R, v, nt, nc>, dim3((unsigned)blocks), bn_block<nt>, smem, (cudaStream_t)stream, a);
+            auto run = [&](auto bias) {
+                const int at_once = blocks_at_once<bn_bwd_kernel<T, R, v, nt, nc, bias>>(bn_block<nt>, smem);
+                if (at_once <= 0) return (int)LA_ERR_CUDA;
+                blocks = std::min<long long>((a.rows + per_block - 1) / per_block, (long long)sms * std::min(at_once, BN_MOST_BLOCKS));
+                if (a.sums) {
+                    if (!workspace || workspace_bytes < (size_t)blocks * 4 * d * sizeof(float)) return (int)LA_ERR_WORKSPACE;
+                    a.part = (float *)workspace;
+                }
+                return launch(bn_bwd_kernel<T, R, v, nt, nc, bias>, dim3((unsigned)blocks), bn_block<nt>, smem, (cudaStream_t)stream, a);
+            };
+            return dpost_bias || dpre_bias ? run(std::true_type()) : run(std::false_type());
         });
     });
     if (rc != LA_OK || !a.sums) return rc;
-    const BnJoin j{a.part, {dpost_weight, dpost_bias, dpre_weight, dpre_bias}, (int)blocks, d};
+    const BnJoin j{a.part, {dpost_weight, dpre_weight, dpost_bias, dpre_bias}, (int)blocks, d};
     return launch(bn_join_kernel, dim3((unsigned)((d + 31) / 32), 4), 1024, 0, (cudaStream_t)stream, j);
 }
 
