@@ -206,10 +206,11 @@ struct RowAt {
     }
 };
 
-template <int NT> constexpr int bn_block = NT < 256 ? 256 : NT;
+template <int NT, bool BWD> constexpr int bn_block = NT < (BWD ? 128 : 256) ? (BWD ? 128 : 256) : NT;
 
-// Rows on their way to a thread: three, or what shared memory holds of the widest rows.
-template <int VEC, int STAGE> constexpr int AHEAD = VEC != 8 ? 1 : 3 * STAGE <= 204800 ? 3 : 2 * STAGE <= 204800 ? 2 : 1;
+// Rows on their way to a thread: three, or what 384 threads of an SM can have of its shared memory (200 KB for 512).
+template <int VEC, int STAGE, int BLOCK>
+constexpr int AHEAD = VEC != 8 ? 1 : 3 * STAGE <= (BLOCK < 356 ? BLOCK * 576 : 204800) ? 3 : 2 * STAGE <= (BLOCK < 356 ? BLOCK * 576 : 204800) ? 2 : 1;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
@@ -272,7 +273,7 @@ template <int VEC, int PF> __device__ __forceinline__ void row_arrived()
 
 // What both kernels begin with: the row group's first row, its channels, and the gate's activation.
 #define BN_ROWS(STEP_ROWS)                                                                                             \
-    constexpr int N = VEC * NC, W = WIDTH<VEC>, M = N / W, GROUPS = bn_block<NT> / NT;                                  \
+    constexpr int N = VEC * NC, W = WIDTH<VEC>, M = N / W, GROUPS = BLOCK / NT;                                         \
     __shared__ __align__(16) float sm[GROUPS * 2 * (NT / 32) * 2];                                                       \
     const int tid = threadIdx.x % NT, group = threadIdx.x / NT;                                                        \
     Sums<NT, GROUPS == 1> sum{sm + group * 2 * (NT / 32) * 2};                                                          \
@@ -307,12 +308,13 @@ template <typename T, int W, int M> __device__ __forceinline__ void activate(con
 }
 
 template <typename T, typename R, int VEC, int NT, int NC>
-__global__ void __launch_bounds__(bn_block<NT>, 1) bn_fwd_kernel(const BnArgs a)
+__global__ void __launch_bounds__(bn_block<NT, false>, 1) bn_fwd_kernel(const BnArgs a)
 {
+    constexpr int BLOCK = bn_block<NT, false>;
     BN_ROWS(step)
     extern __shared__ __align__(16) uint8_t ring[];
-    constexpr int BLOCK = bn_block<NT>, BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES, STAGE = 2 * BT + BR,
-                  PF = AHEAD<VEC, STAGE>;
+    constexpr int BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES, STAGE = 2 * BT + BR,
+                  PF = AHEAD<VEC, STAGE, BLOCK>;
     Ahead<T, VEC, NC, BLOCK> ry, rg;
     Ahead<R, VEC, NC, BLOCK> rr;
     const uint32_t ring_at = ptx::smem_u32(ring);
@@ -400,12 +402,13 @@ __device__ __forceinline__ void norm_back(Ch<W> (&dxh)[M], const Ch<W> (&xh)[M],
 
 // BIAS: sums for the biases too.
 template <typename T, typename R, int VEC, int NT, int NC, bool BIAS>
-__global__ void __launch_bounds__(bn_block<NT>, 1) bn_bwd_kernel(const BnArgs a)
+__global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 ? 3 : 1) bn_bwd_kernel(const BnArgs a)
 {
+    constexpr int BLOCK = bn_block<NT, true>;
     BN_ROWS(step)
     extern __shared__ __align__(16) uint8_t ring[];
-    constexpr int BLOCK = bn_block<NT>, BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES,
-                  STAGE = 3 * BT + 2 * BR, PF = AHEAD<VEC, STAGE>;
+    constexpr int BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES,
+                  STAGE = 3 * BT + 2 * BR, PF = AHEAD<VEC, STAGE, BLOCK>;
     Ch<W> total[BIAS ? 4 : 2][M];  // post_w, pre_w, post_b, pre_b
 #pragma unroll
     for (int k = 0; k < (BIAS ? 4 : 2); ++k)
@@ -608,9 +611,9 @@ __global__ void __launch_bounds__(1024) bn_join_kernel(const BnJoin a)
 // Shared memory of a kernel: the ring, or where row groups share a block the sums that it is reused for.
 template <typename T, typename R, int VEC, int NT, int NC, bool BWD> constexpr int ring_bytes(int d)
 {
-    constexpr int bt = Ahead<T, VEC, NC, bn_block<NT>>::BYTES, br = Ahead<R, VEC, NC, bn_block<NT>>::BYTES,
-                  stage = BWD ? 3 * bt + 2 * br : 2 * bt + br, ring = AHEAD<VEC, stage> * stage;
-    return BWD && NT < bn_block<NT> ? std::max(ring, 16 * d) : ring;
+    constexpr int block = bn_block<NT, BWD>, bt = Ahead<T, VEC, NC, block>::BYTES, br = Ahead<R, VEC, NC, block>::BYTES,
+                  stage = BWD ? 3 * bt + 2 * br : 2 * bt + br, ring = AHEAD<VEC, stage, block> * stage;
+    return BWD && NT < block ? std::max(ring, 16 * d) : ring;
 }
 
 // Blocks of a kernel that run at once on an SM, with its shared memory limit set; once a device and kernel.
@@ -628,28 +631,22 @@ template <auto KERN> int blocks_at_once(int block, int smem)
     known[dev].store(n);
     return n;
 }
-constexpr int BN_MOST_BLOCKS = 8;  // of an SM: 2048 threads in blocks of 256
+constexpr int BN_MOST_BLOCKS = 8;  // of an SM
 
-template <bool WIDE, typename F> int by_shape(int d, bool wide, F &&f)
+template <typename F> int by_shape(int d, bool wide, F &&f)
 {
     if (!wide)
         return d <= 256 ? f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>(), std::integral_constant<int, 8>())
                         : f(std::integral_constant<int, 1>(), std::integral_constant<int, 512>(), std::integral_constant<int, 16>());
+    // 16 channels a thread: half the sums' and the rows' overhead of 8 (B8 L8192 d2048: 307 and 837 us with 8)
     std::integral_constant<int, 8> v;
     std::integral_constant<int, 1> one;
     std::integral_constant<int, 2> two;
     if (d <= 256) return f(v, std::integral_constant<int, 32>(), one);
-    if constexpr (WIDE) {
-        if (d <= 512) return f(v, std::integral_constant<int, 32>(), two);
-        if (d <= 1024) return f(v, std::integral_constant<int, 64>(), two);
-        if (d <= 2048) return f(v, std::integral_constant<int, 128>(), two);
-        if (d <= 4096) return f(v, std::integral_constant<int, 256>(), two);
-    } else {
-        if (d <= 512) return f(v, std::integral_constant<int, 64>(), one);
-        if (d <= 1024) return f(v, std::integral_constant<int, 128>(), one);
-        if (d <= 2048) return f(v, std::integral_constant<int, 256>(), one);
-        if (d <= 4096) return f(v, std::integral_constant<int, 512>(), one);
-    }
+    if (d <= 512) return f(v, std::integral_constant<int, 32>(), two);
+    if (d <= 1024) return f(v, std::integral_constant<int, 64>(), two);
+    if (d <= 2048) return f(v, std::integral_constant<int, 128>(), two);
+    if (d <= 4096) return f(v, std::integral_constant<int, 256>(), two);
     return f(v, std::integral_constant<int, 512>(), two);
 }
 template <typename F> int by_types(int dtype, int rtype, F &&f)
@@ -718,12 +715,12 @@ int la_block_norm_fwd(const void *y, const void *residual, const void *gate, con
     return by_types(dtype, residual_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        return by_shape<false>(d, wide, [&](auto v, auto nt, auto nc) {
-            constexpr int per_block = bn_block<nt> / nt, smem = ring_bytes<T, R, v, nt, nc, false>(0);
-            const int at_once = blocks_at_once<bn_fwd_kernel<T, R, v, nt, nc>>(bn_block<nt>, smem);
+        return by_shape(d, wide, [&](auto v, auto nt, auto nc) {
+            constexpr int per_block = bn_block<nt, false> / nt, smem = ring_bytes<T, R, v, nt, nc, false>(0);
+            const int at_once = blocks_at_once<bn_fwd_kernel<T, R, v, nt, nc>>(bn_block<nt, false>, smem);
             if (at_once <= 0) return (int)LA_ERR_CUDA;
             const long long grid = std::min<long long>((a.rows + per_block - 1) / per_block, (long long)sms * at_once);
-            return launch(bn_fwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt>, smem, (cudaStream_t)stream, a);
+            return launch(bn_fwd_kernel<T, R, v, nt, nc>, dim3((unsigned)grid), bn_block<nt, false>, smem, (cudaStream_t)stream, a);
         });
     });
 }
@@ -787,18 +784,18 @@ int la_block_norm_bwd(const void *y, const void *residual, const void *gate, con
     const int rc = by_types(dtype, residual_dtype, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        return by_shape<true>(d, wide, [&](auto v, auto nt, auto nc) {
-            constexpr int per_block = bn_block<nt> / nt;
+        return by_shape(d, wide, [&](auto v, auto nt, auto nc) {
+            constexpr int per_block = bn_block<nt, true> / nt;
             const int most = v == 8 ? 8 * nt * nc : nt * nc, smem = ring_bytes<T, R, v, nt, nc, true>(most);  // for every d of it
             auto run = [&](auto bias) {
-                const int at_once = blocks_at_once<bn_bwd_kernel<T, R, v, nt, nc, bias>>(bn_block<nt>, smem);
+                const int at_once = blocks_at_once<bn_bwd_kernel<T, R, v, nt, nc, bias>>(bn_block<nt, true>, smem);
                 if (at_once <= 0) return (int)LA_ERR_CUDA;
                 blocks = std::min<long long>((a.rows + per_block - 1) / per_block, (long long)sms * std::min(at_once, BN_MOST_BLOCKS));
                 if (a.sums) {
                     if (!workspace || workspace_bytes < (size_t)blocks * 4 * d * sizeof(float)) return (int)LA_ERR_WORKSPACE;
                     a.part = (float *)workspace;
                 }
-                return launch(bn_bwd_kernel<T, R, v, nt, nc, bias>, dim3((unsigned)blocks), bn_block<nt>, smem, (cudaStream_t)stream, a);
+                return launch(bn_bwd_kernel<T, R, v, nt, nc, bias>, dim3((unsigned)blocks), bn_block<nt, true>, smem, (cudaStream_t)stream, a);
             };
             return dpost_bias || dpre_bias ? run(std::true_type()) : run(std::false_type());
         });
