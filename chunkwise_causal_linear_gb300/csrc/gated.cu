@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(1024) head_sum_kernel(const HeadSumArgs a)
 }
 
 // ---- the decoding step ---------------------------------------------------------------------------
-constexpr int STEP_THREADS = 128, STEP_COLS = 32, STEP_AHEAD = 8;
+constexpr int STEP_THREADS = 128, STEP_AHEAD = 8;
 
 struct StepArgs {
     const void *q, *k, *v;
@@ -508,14 +508,17 @@ struct StepArgs {
     int *err;
 };
 
-// Bound by the state, read and written once.  A block takes 32 columns of a head, 128 bytes of each of
-// its rows, so that a few heads reach every SM; V columns of a thread's rows are on their way at once.
-template <typename T, int V> __global__ void __launch_bounds__(STEP_THREADS) step_kernel(const StepArgs a)
+// Bound by the state, read and written once.  A block takes COLS columns of a head, and V columns of eight of a
+// thread's rows are on their way at once.  With few heads 32 columns, so that they reach every SM (B8 H16 d128
+// 6.3 us, 8.4 with 128); with many 128, rows of 512 bytes (B64 H32 d128, 268 MB: 51.5 us, 77% of measured copy
+// bandwidth, 60 with 32).
+template <typename T, int V, int COLS> __global__ void __launch_bounds__(STEP_THREADS, 6) step_kernel(const StepArgs a)
 {
-    constexpr int LC = STEP_COLS / V, RG = STEP_THREADS / LC;  // lanes along the columns, row groups
-    __shared__ float sums[STEP_THREADS / 32][STEP_COLS];
+    static_assert(COLS / V <= 32, "each warp covers the columns");
+    constexpr int LC = COLS / V, RG = STEP_THREADS / LC;  // lanes along the columns, row groups
+    __shared__ float sums[STEP_THREADS / 32][COLS];
     const int tile = blockIdx.x % a.tiles, bh = blockIdx.x / a.tiles, b = bh / a.H, h = bh % a.H, hk = h / a.group;
-    const int lc = threadIdx.x % LC, rg = threadIdx.x / LC, col = tile * STEP_COLS + V * lc;
+    const int lc = threadIdx.x % LC, rg = threadIdx.x / LC, col = tile * COLS + V * lc;
     const int slot = gated_slot(a.slots, b, a.n_slots, threadIdx.x == 0 ? a.err : nullptr);
     const bool in = col < a.e;  // V divides e
     float *const S = a.state + ((long long)slot * a.H + h) * a.d * a.e + col;
@@ -574,11 +577,11 @@ template <typename T, int V> __global__ void __launch_bounds__(STEP_THREADS) ste
         for (int i = 0; i < V; ++i) sums[threadIdx.x >> 5][V * lc + i] = o[i];
     __syncthreads();
     const int c = threadIdx.x;
-    if (c < STEP_COLS && tile * STEP_COLS + c < a.e) {
+    if (c < COLS && tile * COLS + c < a.e) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < STEP_THREADS / 32; ++w) s += sums[w][c];
-        ((T *)a.out)[row_of(a.vo, b, h, 0) + tile * STEP_COLS + c] = from_f32<T>(a.scale * s);
+        ((T *)a.out)[row_of(a.vo, b, h, 0) + tile * COLS + c] = from_f32<T>(a.scale * s);
     }
 }
 
@@ -951,15 +954,18 @@ int la_gated_step(const void *q, const void *k, const void *v, const float *log_
         return LA_ERR_ARG;
     a.B = B; a.H = H; a.group = H / Hk; a.d = dk; a.e = dv; a.n_slots = n_slots;
     a.scale = scale;
-    a.tiles = (dv + STEP_COLS - 1) / STEP_COLS;
     if (!(a.err = err_ptr())) return LA_ERR_CUDA;
+    const bool wide = dv % 4 == 0 && aligned(state, 16), many = wide && dv > 64 && (long long)B * H >= 4ll * device_sms();
+    const int cols = many ? 128 : 32;
+    a.tiles = (dv + cols - 1) / cols;
     const dim3 grid((unsigned)((long long)B * H * a.tiles));
-    const bool wide = dv % 4 == 0 && aligned(state, 16);
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == LA_F32)
-        return wide ? launch(step_kernel<float, 4>, grid, STEP_THREADS, 0, s, a) : launch(step_kernel<float, 1>, grid, STEP_THREADS, 0, s, a);
-    return wide ? launch(step_kernel<__nv_bfloat16, 4>, grid, STEP_THREADS, 0, s, a)
-                : launch(step_kernel<__nv_bfloat16, 1>, grid, STEP_THREADS, 0, s, a);
+    auto run = [&](auto t) {
+        using T = decltype(t);
+        if (many) return launch(step_kernel<T, 4, 128>, grid, STEP_THREADS, 0, s, a);
+        return wide ? launch(step_kernel<T, 4, 32>, grid, STEP_THREADS, 0, s, a) : launch(step_kernel<T, 1, 32>, grid, STEP_THREADS, 0, s, a);
+    };
+    return dtype == LA_F32 ? run(0.f) : run(__nv_bfloat16());
 }
 
 }  // extern "C"

@@ -101,14 +101,15 @@ __device__ __forceinline__ long long doublings(float g)
 
 template <int DX, int DZ, bool DOT> struct GtLayout {
     static constexpr int NS = DOT ? 3 : 1;  // bf16 parts of the state's copy
-    static constexpr int X = GT_C * DX * 2, Z = GT_C * DZ * 2, W = DOT ? Z : 0;
-    static constexpr int STAGE = 2 * X + Z + W;
+    static constexpr int X = GT_C * DX * 2, Z = GT_C * DZ * 2;
+    static constexpr int STAGE = 2 * X + Z;
+    static constexpr int WST = 3, WR = DOT ? WST * Z : 0;  // W's tiles are held longer: a ring of their own
     static constexpr int YT = 3 * X, P = GT_C * GT_C * 2;
     static constexpr int OUT = 16 * (DZ / 4) * 2;    // a worker's 16 rows of its quadrant's channels
     static constexpr int OUTS = GT_WORKERS * OUT;
-    static constexpr int FIXED = YT + P + OUTS + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
+    static constexpr int FIXED = WR + YT + P + OUTS + GT_SLOTS * (int)sizeof(Weights) + 256 + 1024;
     static constexpr int STAGES = (232448 - FIXED) / STAGE >= 4 ? 4 : (232448 - FIXED) / STAGE;
-    static constexpr int OFF_YT = STAGES * STAGE, OFF_P = OFF_YT + YT, OFF_O = OFF_P + P, OFF_W = OFF_O + OUTS,
+    static constexpr int OFF_WR = STAGES * STAGE, OFF_YT = OFF_WR + WR, OFF_P = OFF_YT + YT, OFF_O = OFF_P + P, OFF_W = OFF_O + OUTS,
                          OFF_BAR = OFF_W + GT_SLOTS * (int)sizeof(Weights), ALLOC = OFF_BAR + 256 + 1024;
     // TMEM columns
     // one part: two copies of the state in turn, so that the next one need not wait for the inter product
@@ -159,7 +160,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     uint64_t *const full = bars, *const stage_free = full + NST, *const yt_ready = stage_free + NST, *const state_done = yt_ready + 1,
              *const s_ready = state_done + 1, *const scores_done = s_ready + 1, *const sc_free = scores_done + 1,
              *const p_ready = sc_free + 1, *const o_done = p_ready + 1, *const o_free = o_done + 1,
-             *const inter_done = o_free + 1, *const drain = inter_done + 1;
+             *const inter_done = o_free + 1, *const drain = inter_done + 1,
+             *const w_free = drain + 1;
     uint32_t *const tmem_slot = (uint32_t *)(sm + Lay::OFF_BAR + 224);
     volatile int *const abort_flag = (volatile int *)(sm + Lay::OFF_BAR + 228);
 
@@ -176,14 +178,15 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     auto tile_x = [&](int s) { return sm + s * Lay::STAGE; };
     auto tile_y = [&](int s) { return tile_x(s) + Lay::X; };
     auto tile_z = [&](int s) { return tile_y(s) + Lay::X; };
-    auto tile_w = [&](int s) { return tile_z(s) + Lay::Z; };
+    auto tile_w = [&](int c) { return sm + Lay::OFF_WR + (c % Lay::WST) * Lay::Z; };  // of chunk c
     uint8_t *const yt = sm + Lay::OFF_YT, *const p_tile = sm + Lay::OFF_P;
 
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 2);                       // the TMA's bytes, the weights
-            mbar_init(&stage_free[i], DOT && !totals ? 1 + GT_WORKERS : 1);  // the products, and the readers of W
+            mbar_init(&stage_free[i], 1);
         }
+        for (int i = 0; i < Lay::WST; ++i) mbar_init(&w_free[i], GT_WORKERS);
         mbar_init(yt_ready, GT_WORKERS);
         mbar_init(state_done, 1);
         // No phase of a barrier completes before everyone has waited for the one before it, or a waiter could take
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     // channels, which leave 16 bytes a lane. (Two-byte stores from a lane a channel took ten times the
     // instructions; TMA stores, 50 cycles of the unit each, were slower than these.)
     auto rows = [&](int c) {
-        const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0), first = 16 * part;
+        const int row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0), first = 16 * part;
         const Weights &w = weights[c % GT_SLOTS];
         uint32_t oi[HALVES][8], oa[HALVES][8];
 #pragma unroll
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
 #pragma unroll
             for (int k = 0; k < HALVES; ++k) {
                 const int t = first + 8 * k + at_row, cg = (DZ / 32) * q4 + at_ch;
-                ldmatrix_t(smem_u32(tile_w(s)) + (cg >> 3) * C * 128 + t * 128 + (((cg & 7) ^ (t & 7)) << 4), wt[k]);
+                ldmatrix_t(smem_u32(tile_w(c)) + (cg >> 3) * C * 128 + t * 128 + (((cg & 7) ^ (t & 7)) << 4), wt[k]);
             }
         }
         tmem_wait_ld();
@@ -322,15 +325,16 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             for (int c = 0; c < nch; ++c) {
                 const int s = c % NST;
                 if (c >= NST && !wait_long(&stage_free[s], ((c / NST) - 1) & 1, ctl)) break;
+                if (DOT && c >= Lay::WST && !wait_long(&w_free[c % Lay::WST], ((c / Lay::WST) - 1) & 1, ctl)) break;
                 const int row = t0 + chunk_of(c) * C;
-                mbar_arrive_expect_tx(&full[s], totals ? Lay::X + Lay::Z : Lay::STAGE);
+                mbar_arrive_expect_tx(&full[s], totals ? Lay::X + Lay::Z : Lay::STAGE + (DOT ? Lay::Z : 0));
                 for (int k = 0; k < DX / 64; ++k) {
                     if (!totals) tma_load_4d(tile_x(s) + k * C * 128, &a.mx, k * 64, row, h / a.sx, b, &full[s]);
                     tma_load_4d(tile_y(s) + k * C * 128, &a.my, k * 64, row, h / a.sy, b, &full[s]);
                 }
                 for (int k = 0; k < DZ / 64; ++k) {
                     tma_load_4d(tile_z(s) + k * C * 128, &a.mz, k * 64, row, h / a.sz, b, &full[s]);
-                    if (DOT && !totals) tma_load_4d(tile_w(s) + k * C * 128, &a.mw, k * 64, row, h / a.sw, b, &full[s]);
+                    if (DOT && !totals) tma_load_4d(tile_w(c) + k * C * 128, &a.mw, k * 64, row, h / a.sw, b, &full[s]);
                 }
                 issued = c + 1;
             }
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 mma_ss_if(tm + Lay::T_A, desc_add(dx, o), desc_add(dy, o), ID_SC, k > 0, one);
             }
             if (INNER) {
-                const uint64_t dw = smem_desc(smem_u32(tile_w(s)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
+                const uint64_t dw = smem_desc(smem_u32(tile_w(c)), 16, 1024), dz = smem_desc(smem_u32(tile_z(s)), 16, 1024);
 #pragma unroll
                 for (int k = 0; k < DZ / 16; ++k) {
                     const uint32_t o = (k >> 2) * C * 128 + (k & 3) * 32;
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                     mma_ts_if(tm + Lay::T_OI, sc + p * (DX / 2) + k * 8, desc_add(dx, (k >> 2) * C * 128 + (k & 3) * 32), ID_INTER,
                               p + k > 0, one);
             if (DOT) mma_commit_if(inter_done, one);
-            if (!late) {
+            if (!DOT) {
                 if (!(ok = wait(sc_free, c & 1))) break;
                 if (c + 1 < n && !(ok = scores(c + 1))) break;
             }
@@ -415,8 +419,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 mma_ss_if(tm + Lay::T_OA, desc_add(dz, k * 2048), desc_add(dp, k * 32), ID_INTRA, k > 0, one);
             mma_commit_if(o_done, one);
             mma_commit_if(&stage_free[s], one);
-            if (late && c + 1 < n) {
-                if (!(ok = wait(o_free, c & 1))) break;
+            if (DOT && c + 1 < n) {  // after the rows' products, which the workers wait for in the same round
+                if (!(ok = wait(sc_free, c & 1))) break;
+                if (late && !(ok = wait(o_free, c & 1))) break;
                 if (!(ok = scores(c + 1))) break;
             }
         }
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 if (!(ok = wait(o_done, c & 1))) break;
                 tc_fence_after();
                 rows(c);
-                arrive(&stage_free[s]);
+                arrive(&w_free[c % Lay::WST]);
             }
         }
         if (!DOT && !totals && ok && nch > 0 && (ok = wait(o_done, (nch - 1) & 1))) {
