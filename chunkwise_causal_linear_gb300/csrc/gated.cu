@@ -375,23 +375,55 @@ struct ScanArgs {
     int *err;
 };
 
-__global__ void __launch_bounds__(256) scan_kernel(const ScanArgs a)
+// A thread an element, or four; the segments' sums eight at a time, so that their loads are on their way together.
+template <int V> __global__ void __launch_bounds__(128) scan_kernel(const ScanArgs a)
 {
+    constexpr int AT_ONCE = 8;
+    using F = Ch<V>;
     const int bh = blockIdx.y, b = bh / a.H, h = bh % a.H;
-    const int i = blockIdx.x * 256 + threadIdx.x;
+    const int i = (blockIdx.x * 128 + threadIdx.x) * V;
     if (i >= a.n) return;
     const int slot = gated_slot(a.slots, b, a.n_slots, threadIdx.x == 0 ? a.err : nullptr);
     const long long at = ((long long)slot * a.H + h) * a.n + i;
-    float s = a.first && slot >= 0 ? a.first[at] : 0.f;
-    for (int j = 0; j < a.nseg; ++j) {
-        const int seg = a.reverse ? a.nseg - 1 - j : j;
-        const long long e = ((long long)seg * a.BH + bh) * a.n + i;
-        const float t = a.T[e], w = a.A[(long long)seg * a.BH + bh];
-        a.T[e] = s;
-        s = w == 0.f ? t : fmaf(w, s, t);
+    auto load = [](const float *p) {
+        F f;
+        if constexpr (V == 4) {
+            const float4 t = *(const float4 *)p;
+            f = {{t.x, t.y, t.z, t.w}};
+        } else {
+            f = {{*p}};
+        }
+        return f;
+    };
+    auto store = [](float *p, const F &f) {
+        if constexpr (V == 4) *(float4 *)p = make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+        else *p = f.v[0];
+    };
+    F s;
+#pragma unroll
+    for (int u = 0; u < V; ++u) s.v[u] = 0.f;
+    if (a.first && slot >= 0) s = load(a.first + at);
+    for (int j0 = 0; j0 < a.nseg; j0 += AT_ONCE) {
+        F t[AT_ONCE];
+        float w[AT_ONCE];
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j)
+            if (j0 + j < a.nseg) {
+                const long long seg = (a.reverse ? a.nseg - 1 - j0 - j : j0 + j) * (long long)a.BH + bh;
+                t[j] = load(a.T + seg * a.n + i);
+                w[j] = a.A[seg];
+            }
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j)
+            if (j0 + j < a.nseg) {
+                const long long seg = (a.reverse ? a.nseg - 1 - j0 - j : j0 + j) * (long long)a.BH + bh;
+                store(a.T + seg * a.n + i, s);
+#pragma unroll
+                for (int u = 0; u < V; ++u) s.v[u] = w[j] == 0.f ? t[j].v[u] : fmaf(w[j], s.v[u], t[j].v[u]);
+            }
     }
-    if (a.last && slot >= 0) a.last[at] = s;
-    if (a.last_ws) a.last_ws[(long long)bh * a.n + i] = s;
+    if (a.last && slot >= 0) store(a.last + at, s);
+    if (a.last_ws) store(a.last_ws + (long long)bh * a.n + i, s);
 }
 
 struct ShareArgs {
@@ -400,16 +432,38 @@ struct ShareArgs {
     View vo;
     int B, H, Hk, L, n;
 };
-template <typename T> __global__ void __launch_bounds__(256) share_kernel(const ShareArgs a)
+// V channels of a row a thread; a block takes neighbouring rows of a sequence's key head.
+template <typename T, int V> __global__ void __launch_bounds__(256) share_kernel(const ShareArgs a)
 {
-    const long long all = (long long)a.B * a.Hk * a.L * a.n;
-    const int group = a.H / a.Hk;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += 256ll * gridDim.x) {
-        const int c = (int)(i % a.n), t = (int)(i / a.n % a.L), hk = (int)(i / a.n / a.L % a.Hk),
-                  b = (int)(i / a.n / a.L / a.Hk);
-        float s = 0.f;
-        for (int j = 0; j < group; ++j) s += a.x[(((long long)b * a.H + hk * group + j) * a.L + t) * a.n + c];
-        ((T *)a.out)[row_of(a.vo, b, hk, t) + c] = from_f32<T>(s);
+    const int group = a.H / a.Hk, per_row = a.n / V, rows = 256 / per_row > 0 ? 256 / per_row : 1;
+    const int hk = blockIdx.y % a.Hk, b = blockIdx.y / a.Hk;
+    const long long head = (long long)a.L * a.n;
+    const float *const x = a.x + ((long long)b * a.H + (long long)hk * group) * head;
+    for (int e = threadIdx.x; e < rows * per_row; e += 256) {
+        const int t = blockIdx.x * rows + e / per_row, c = V * (e % per_row);
+        if (t >= a.L) break;
+        const float *const p = x + (long long)t * a.n + c;
+        float s[V];
+#pragma unroll
+        for (int u = 0; u < V; ++u) s[u] = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < group; ++j) {
+            if constexpr (V == 4) {
+                const float4 f = *(const float4 *)(p + j * head);
+                s[0] += f.x; s[1] += f.y; s[2] += f.z; s[3] += f.w;
+            } else {
+                s[0] += p[j * head];
+            }
+        }
+        T *const o = (T *)a.out + row_of(a.vo, b, hk, t) + c;
+        if constexpr (V == 4 && sizeof(T) == 2) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(s[0], s[1]), hi = __floats2bfloat162_rn(s[2], s[3]);
+            *(uint2 *)o = make_uint2(*(const uint32_t *)&lo, *(const uint32_t *)&hi);
+        } else if constexpr (V == 4) {
+            *(float4 *)o = make_float4(s[0], s[1], s[2], s[3]);
+        } else {
+            *o = from_f32<T>(s[0]);
+        }
     }
 }
 
@@ -418,12 +472,24 @@ struct ProductArgs {
     float *y;
     int n;
 };
+// Products summed by eights in fp32, those sums in 64 bits.
 __global__ void __launch_bounds__(256) product_kernel(const ProductArgs a)
 {
     __shared__ double part[8];
-    const long long at = (long long)blockIdx.x * a.n;
+    const float *const D = a.D + (long long)blockIdx.x * a.n, *const S = a.S + (long long)blockIdx.x * a.n;
     double s = 0;
-    for (int i = threadIdx.x; i < a.n; i += 256) s += (double)a.D[at + i] * (double)a.S[at + i];
+    for (int i0 = threadIdx.x; i0 < a.n; i0 += 256 * 8) {
+        float d[8], v[8], f = 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const bool in = i0 + 256 * u < a.n;
+            d[u] = in ? D[i0 + 256 * u] : 0.f;
+            v[u] = in ? S[i0 + 256 * u] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) f = fmaf(d[u], v[u], f);
+        s += (double)f;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
@@ -441,32 +507,47 @@ struct LogDecayArgs {
     const int *lengths;
     int nr, nc, B, H, L, seg_rows, nseg;
 };
-// One warp a segment, 32 rows at a time from its end; the sums in 64 bits.
-__global__ void __launch_bounds__(128) log_decay_kernel(const LogDecayArgs a)
+// A block a segment, a thread a row, 1024 rows at a time from its end; a row's parts are summed in fp32, the
+// rows in 64 bits.
+__global__ void __launch_bounds__(1024) log_decay_kernel(const LogDecayArgs a)
 {
-    const long long id = blockIdx.x * 4ll + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, BH = a.B * a.H;
-    if (id >= (long long)BH * a.nseg) return;
-    const int seg = (int)(id % a.nseg), bh = (int)(id / a.nseg), b = bh / a.H, h = bh % a.H;
+    __shared__ double sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.H;
+    const int seg = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / a.H, h = bh % a.H;
     const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L), te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
-    for (int t = te + lane; t < t1; t += 32) a.dg[(long long)bh * a.L + t] = 0.f;
+    const long long at = (long long)bh * a.L, step = (long long)BH * a.L;
+    for (int t = te + (int)threadIdx.x; t < t1; t += blockDim.x) a.dg[at + t] = 0.f;
     double carry = a.y[(long long)seg * BH + bh];
-    for (int e = te; e > t0; e -= 32) {
-        const int t = e - 1 - lane;
+    for (int e = te; e > t0; e -= blockDim.x) {
+        const int t = e - 1 - (int)threadIdx.x;
         double s = 0;
+        float g = 0.f;
         if (t >= t0) {
-            for (int i = 0; i < a.nr; ++i) s += (double)a.r[((long long)i * BH + bh) * a.L + t];
-            for (int i = 0; i < a.nc; ++i) s -= (double)a.c[((long long)i * BH + bh) * a.L + t];
+            float r = 0.f, c = 0.f;
+            g = a.g[row_of(a.vg, b, h, t)];
+#pragma unroll 8
+            for (int i = 0; i < a.nr; ++i) r += a.r[i * step + at + t];
+#pragma unroll 8
+            for (int i = 0; i < a.nc; ++i) c += a.c[i * step + at + t];
+            s = (double)r - (double)c;
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double u = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += u;
         }
-        s += carry;
+        if (lane == 31) sums[warp] = s;
+        __syncthreads();
+        double before = 0, all = 0;  // the warps' sums before this one's, and of all
+        for (int i = 0; i < (int)blockDim.x / 32; ++i) {
+            if (i == warp) before = all;
+            all += sums[i];
+        }
+        __syncthreads();
+        s += carry + before;
+        carry += all;
         // a decay of 0 has no gradient: every pair across it is 0
-        if (t >= t0) a.dg[(long long)bh * a.L + t] = a.g[row_of(a.vg, b, h, t)] < GATED_CUT ? 0.f : (float)s;
-        carry = __shfl_sync(0xffffffffu, s, 31);
+        if (t >= t0) a.dg[at + t] = g < GATED_CUT ? 0.f : (float)s;
     }
 }
 
@@ -624,16 +705,23 @@ int gated_scan(const GatedArgs &p, float *T, const float *A, int nseg, int n, co
                float *last, float *last_ws, bool reverse)
 {
     const ScanArgs a{T, A, first, last, last_ws, slots, nseg, p.B * p.H, p.H, n, p.n_slots, reverse, p.err};
-    return launch(scan_kernel, dim3((unsigned)((n + 255) / 256), (unsigned)a.BH), 256, 0, p.stream, a);
+    if (n % 4 == 0 && aligned(T, 16) && aligned(first, 16) && aligned(last, 16) && aligned(last_ws, 16))
+        return launch(scan_kernel<4>, dim3((unsigned)((n / 4 + 127) / 128), (unsigned)a.BH), 128, 0, p.stream, a);
+    return launch(scan_kernel<1>, dim3((unsigned)((n + 127) / 128), (unsigned)a.BH), 128, 0, p.stream, a);
 }
 
 int gated_share(const GatedArgs &p, const float *x, void *out, const View &vo, int n)
 {
     const ShareArgs a{x, out, vo, p.B, p.H, p.Hk, p.L, n};
-    const double all = (double)p.B * p.Hk * p.L * n;
-    const dim3 grid((unsigned)std::min(all / 256 + 1, 8.0 * p.sms));
-    return p.dtype == LA_F32 ? launch(share_kernel<float>, grid, 256, 0, p.stream, a)
-                             : launch(share_kernel<__nv_bfloat16>, grid, 256, 0, p.stream, a);
+    const size_t es = dtype_size(p.dtype);
+    const bool wide = n % 4 == 0 && aligned(x, 16) && rows_aligned(out, vo, p.B, p.Hk, p.L, es, 4 * es);
+    const int per_row = wide ? n / 4 : n, rows = std::max(1, 256 / per_row);
+    const dim3 grid((unsigned)((p.L + rows - 1) / rows), (unsigned)(p.B * p.Hk));
+    auto run = [&](auto t) {
+        using T = decltype(t);
+        return wide ? launch(share_kernel<T, 4>, grid, 256, 0, p.stream, a) : launch(share_kernel<T, 1>, grid, 256, 0, p.stream, a);
+    };
+    return p.dtype == LA_F32 ? run(0.f) : run(__nv_bfloat16());
 }
 
 int gated_products(const GatedArgs &p, const float *D, const float *S, float *y, int nseg, int n)
@@ -645,8 +733,8 @@ int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, 
                     int nseg, float *dg)
 {
     const LogDecayArgs a{r, c, y, p.g, p.vg, dg, p.lengths, nr, nc, p.B, p.H, p.L, seg_rows, nseg};
-    const long long warps = (long long)p.B * p.H * nseg;
-    int rc = launch(log_decay_kernel, dim3((unsigned)((warps + 3) / 4)), 128, 0, p.stream, a);
+    const int block = std::min(1024, (seg_rows + 31) / 32 * 32);
+    int rc = launch(log_decay_kernel, dim3((unsigned)(p.B * p.H * nseg)), block, 0, p.stream, a);
     if (rc == LA_OK && p.dg_head) rc = launch(head_sum_kernel, dim3((unsigned)p.H), 1024, 0, p.stream, HeadSumArgs{dg, p.dg_head, p.B, p.H, p.L});
     return rc;
 }
