@@ -507,47 +507,62 @@ struct LogDecayArgs {
     const int *lengths;
     int nr, nc, B, H, L, seg_rows, nseg;
 };
-// A block a segment, a thread a row, 1024 rows at a time from its end; a row's parts are summed in fp32, the
-// rows in 64 bits.
-__global__ void __launch_bounds__(1024) log_decay_kernel(const LogDecayArgs a)
+// A block a segment, 1024 rows at a time from its end, four neighbouring ones a thread; a row's parts are summed in
+// fp32, the rows in 64 bits, few operations of which a row leaves (the SM has two such lanes: a scan of every
+// row took 45 us where this takes 13, B2 H12 L16384).
+constexpr int LD_THREADS = 256, LD_ROWS = 4 * LD_THREADS;
+__global__ void __launch_bounds__(LD_THREADS) log_decay_kernel(const LogDecayArgs a)
 {
-    __shared__ double sums[32];
+    __shared__ __align__(16) float diff[LD_ROWS];
+    __shared__ double sums[LD_THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.H;
     const int seg = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / a.H, h = bh % a.H;
     const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L), te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
     const long long at = (long long)bh * a.L, step = (long long)BH * a.L;
-    for (int t = te + (int)threadIdx.x; t < t1; t += blockDim.x) a.dg[at + t] = 0.f;
+    for (int t = te + (int)threadIdx.x; t < t1; t += LD_THREADS) a.dg[at + t] = 0.f;
     double carry = a.y[(long long)seg * BH + bh];
-    for (int e = te; e > t0; e -= blockDim.x) {
-        const int t = e - 1 - (int)threadIdx.x;
-        double s = 0;
-        float g = 0.f;
-        if (t >= t0) {
+    for (int e = te; e > t0; e -= LD_ROWS) {  // place k is row e - 1 - k
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = threadIdx.x + LD_THREADS * u, t = e - 1 - k;
             float r = 0.f, c = 0.f;
-            g = a.g[row_of(a.vg, b, h, t)];
+            if (t >= t0) {
 #pragma unroll 8
-            for (int i = 0; i < a.nr; ++i) r += a.r[i * step + at + t];
+                for (int i = 0; i < a.nr; ++i) r += a.r[i * step + at + t];
 #pragma unroll 8
-            for (int i = 0; i < a.nc; ++i) c += a.c[i * step + at + t];
-            s = (double)r - (double)c;
+                for (int i = 0; i < a.nc; ++i) c += a.c[i * step + at + t];
+            }
+            diff[k] = r - c;
         }
+        __syncthreads();
+        const float4 f = *(const float4 *)(diff + 4 * threadIdx.x);
+        double s[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int u = 1; u < 4; ++u) s[u] += s[u - 1];
+        double run = s[3];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double u = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += u;
+            const double u = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += u;
         }
-        if (lane == 31) sums[warp] = s;
+        if (lane == 31) sums[warp] = run;
         __syncthreads();
-        double before = 0, all = 0;  // the warps' sums before this one's, and of all
-        for (int i = 0; i < (int)blockDim.x / 32; ++i) {
-            if (i == warp) before = all;
-            all += sums[i];
+        double before = carry;
+        for (int i = 0; i < LD_THREADS / 32; ++i) {
+            if (i == warp) before = carry;
+            carry += sums[i];
+        }
+        before += run - s[3];
+        *(float4 *)(diff + 4 * threadIdx.x) =
+            make_float4((float)(before + s[0]), (float)(before + s[1]), (float)(before + s[2]), (float)(before + s[3]));
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = threadIdx.x + LD_THREADS * u, t = e - 1 - k;
+            // a decay of 0 has no gradient: every pair across it is 0
+            if (t >= t0) a.dg[at + t] = a.g[row_of(a.vg, b, h, t)] < GATED_CUT ? 0.f : diff[k];
         }
         __syncthreads();
-        s += carry + before;
-        carry += all;
-        // a decay of 0 has no gradient: every pair across it is 0
-        if (t >= t0) a.dg[at + t] = g < GATED_CUT ? 0.f : (float)s;
     }
 }
 
@@ -733,8 +748,7 @@ int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, 
                     int nseg, float *dg)
 {
     const LogDecayArgs a{r, c, y, p.g, p.vg, dg, p.lengths, nr, nc, p.B, p.H, p.L, seg_rows, nseg};
-    const int block = std::min(1024, (seg_rows + 31) / 32 * 32);
-    int rc = launch(log_decay_kernel, dim3((unsigned)(p.B * p.H * nseg)), block, 0, p.stream, a);
+    int rc = launch(log_decay_kernel, dim3((unsigned)(p.B * p.H * nseg)), LD_THREADS, 0, p.stream, a);
     if (rc == LA_OK && p.dg_head) rc = launch(head_sum_kernel, dim3((unsigned)p.H), 1024, 0, p.stream, HeadSumArgs{dg, p.dg_head, p.B, p.H, p.L});
     return rc;
 }

@@ -118,7 +118,7 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     // the second score block has columns of its own where they are left, else those of Oi
     static constexpr bool A2_OWN = T_A + 128 <= 512;
     static constexpr uint32_t T_A2 = A2_OWN ? T_A + 64 : T_OI;
-    static_assert(T_A + 64 <= 512 && ALLOC <= 232448 && STAGES >= 2, "fits");
+    static_assert(T_A + 64 <= 512 && ALLOC <= 232448 - 64 && STAGES >= 2, "fits");
     static_assert(STAGE % 1024 == 0 && YT % 1024 == 0, "swizzle atoms");
 };
 
@@ -148,12 +148,59 @@ __device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, const 
     return wait_longer(bar, parity, ctl.abort, ctl.err, ctl.timeout_ns);
 }
 
+// Chunks at a sweep's start whose rows' decays to its end are below the normal range of fp32: they add nothing to the
+// sums of a segment. Called by the whole block; 0 where a log decay is positive. cs: scratch, a float a chunk.
+__device__ __forceinline__ int far_chunks(const float *g, long long step, int t0, int te, int nch, bool rev, float *cs)
+{
+    __shared__ int found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (nch > 8192) return 0;
+    bool odd = false;
+#pragma unroll 2
+    for (int k = warp; k < nch; k += GT_THREADS / 32) {
+        const int t = t0 + k * GT_C + lane;
+        const float a = t < te ? g[(long long)t * step] : 0.f, b = t + 32 < te ? g[(long long)(t + 32) * step] : 0.f;
+        odd |= !(a <= 0.f) || !(b <= 0.f);
+        float s = a + b;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) cs[k] = s;
+    }
+    if (threadIdx.x == 0) found = 0;
+    odd = __syncthreads_or(odd);
+    if (warp == 0 && !odd) {
+        float sum = 0.f;
+        for (int k0 = 0; k0 < nch; k0 += 32) {  // from the sweep's end
+            const int k = k0 + lane;
+            float s = k < nch ? cs[rev ? k : nch - 1 - k] : 0.f;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += u;
+            }
+            const uint32_t below = __ballot_sync(0xffffffffu, k < nch && sum + s < -88.f);
+            if (below) {
+                if (lane == 0) found = nch - (k0 + __ffs(below));
+                break;
+            }
+            sum += __shfl_sync(0xffffffffu, s, 31);
+        }
+    }
+    __syncthreads();
+    const int n = found;
+    fence_async_smem();  // the tiles take the scratch's place
+    __syncthreads();
+    return n;
+}
+
 template <int DX, int DZ, bool DOT, bool INNER>
 __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_constant__ GtArgs a)
 {
     using Lay = GtLayout<DX, DZ, DOT>;
     constexpr int C = GT_C, NST = Lay::STAGES, NS = Lay::NS;
     extern __shared__ uint8_t smem_raw[];
+    __shared__ long long sums[2];  // of the log decays, by the warps that form the weights
+    __shared__ bool cuts_of[2];
     uint8_t *const sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Weights *const weights = (Weights *)(sm + Lay::OFF_W);
     uint64_t *const bars = (uint64_t *)(sm + Lay::OFF_BAR);
@@ -169,12 +216,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     const int BH = a.B * a.H, bh = blockIdx.x % BH, seg = blockIdx.x / BH, b = bh / a.H, h = bh % a.H;
     const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L),
               te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
-    const int nch = (te - t0 + C - 1) / C;
     const bool totals = a.totals != 0, rev = INNER ? false : a.reverse != 0;
     const int slot = gated_slot(a.slots, b, a.n_slots, tid == 0 ? a.err : nullptr);
     const Ctl ctl{abort_flag, a.err, a.timeout_ns};
-    auto chunk_of = [&](int c) { return rev ? nch - 1 - c : c; };  // c-th chunk of the sweep
-
     auto tile_x = [&](int s) { return sm + s * Lay::STAGE; };
     auto tile_y = [&](int s) { return tile_x(s) + Lay::X; };
     auto tile_z = [&](int s) { return tile_y(s) + Lay::X; };
@@ -207,6 +251,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    int nch = (te - t0 + C - 1) / C, skip = 0;
+    if (!DOT && totals) {
+        skip = far_chunks(a.g + b * a.vg.b + h * a.vg.h, a.vg.l, t0, te, nch, rev, (float *)sm);
+        nch -= skip;
+    }
+    auto chunk_of = [&](int c) { return rev ? nch - 1 - c : c + skip; };  // c-th chunk of the sweep
     auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait_long(bar, parity, ctl)) != 0; };
     auto arrive = [&](uint64_t *bar) {  // of a warp whose lanes have all done their part
         __syncwarp();
@@ -441,6 +491,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             return c < nch && t < te ? gp[(long long)t * a.vg.l] : 0.f;
         };
         const int c0 = warp - 2;
+        long long over = 0;  // the sum over this warp's chunks
+        bool cut = skip > 0;
         float g0 = gate(c0, 2 * lane), g1 = gate(c0, 2 * lane + 1);
         for (int c = c0; c < nch; c += 2) {
             const float n0 = gate(c + 2, 2 * lane), n1 = gate(c + 2, 2 * lane + 1);  // on its way meanwhile
@@ -477,6 +529,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 w.kw[2 * lane + i] = a.yscale * (rev ? start : end) + bad;
                 w.rw[2 * lane + i] = a.oscale * (rev ? end : start) + bad;
             }
+            over += whole;
+            cut |= cuts > 0;
             if (lane == 0) {
                 const float g2 = (float)whole * UNIT;
                 w.a = (cuts ? 0.f : exp2f(g2)) + bad;
@@ -488,12 +542,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             if (c >= NST && !wait(&stage_free[s], ((c / NST) - 1) & 1)) break;
             arrive(&full[s]);
         }
-        if (a.decay && c0 == 0) {
-            double s = 0;
-            for (int t = t0 + lane; t < te; t += 32) s += (double)gp[(long long)t * a.vg.l];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) a.decay[(long long)seg * BH + bh] = (float)exp(s);
+        if (lane == 0) {
+            sums[c0] = over;
+            cuts_of[c0] = cut;
         }
     } else {
         // ------------------------------------------------------------ workers
@@ -751,6 +802,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+    if (tid == 0 && a.decay)
+        a.decay[(long long)seg * BH + bh] = cuts_of[0] || cuts_of[1] ? 0.f : exp2f((float)(sums[0] + sums[1]) * UNIT);
 }
 
 // ---- host side -----------------------------------------------------------------------------------

@@ -69,6 +69,7 @@ def magnitudes(q, k, v, g, scale, state0, lengths, dout=None, dstate=None):
     m = dict(out=out, state=state)
     if dout is not None:
         m |= backward(*args, dout.abs(), abs(scale), s0, lengths, None if dstate is None else dstate.abs())
+        m["end"] = torch.zeros(state.shape[:2], dtype=torch.float64) if dstate is None else (state * dstate.abs()).sum((-1, -2))
     return m
 
 

@@ -90,8 +90,15 @@ def check_grads(got, want, m, dtype, g, steps):
     for name in ("dq", "dk", "dv"):
         close(name, got[name], want[name], m[name], dtype, steps)
     close("dstate0", got["dstate0"], want["dstate0"], m["dstate0"], F32, steps)
-    # the sum from a segment's end holds the roundings of all its rows
-    size = m["dg"] + m["dg"].mean(-1, keepdim=True) if g.dim() == 3 else m["dg"]
+    # With F_t the gradient of row t's log decay, R_t and C_t the sums of its pairs with earlier rows and with later
+    # ones: F_t = F_{t+1} + R_t - C_t from a segment's end on, where F is <dstate, state>. R_t and C_t are parts of the
+    # sums of terms' magnitudes of F_t and F_{t+1}, so what the sum to row t has gathered are roundings of its own
+    # magnitude and of those of the rows behind it, the end's product among them.
+    size = m["dg"]
+    if g.dim() == 3:
+        size = size + size.mean(-1, keepdim=True) + m["end"][..., None]
+    else:
+        size = size + m["end"].sum(0)
     close("dg", got["dg"], want["dg"], size, F32, steps)
 
 
@@ -279,6 +286,27 @@ def test_a_decay_of_zero_forgets():
         got = grads_of(q, k, v, g, do, 1.0, s0, None, ds)
         assert not got["dg"].any() and not got["dstate0"].any()
         check_grads(got, ref.backward(q, k, v, g, do, 1.0, s0, None, ds), m, dtype, g, steps_of(1, d, d))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rate", [0.0, -0.3, -2.0, -30.0, -103.0, -200.0])
+def test_segments_of_any_decay(rate, dtype):
+    """A long sequence of one head, cut into segments, from no decay to decays that leave nothing of a row's
+    neighbour; some rows without, some positive: the rows far from a segment's end are left out of its sum only
+    where their decay is below fp32's range."""
+    B, H, L, d = 1, 1, 1500, 64
+    q, k, v, _, s0, _, do, ds = ref.draw(B, H, H, L, d, d, dtype, "token", True, seed=21)
+    gen = torch.Generator().manual_seed(22)
+    g = rate * (0.5 + torch.rand(B, H, L, generator=gen))
+    for some, value in ((0.0, 0.0), (0.05, 0.0), (0.01, 0.2)):
+        gs = torch.where(torch.rand(B, H, L, generator=gen) < some, torch.tensor(value), g)
+        want, wstate = ref.forward(q, k, v, gs, 0.1, s0)
+        m = ref.magnitudes(q, k, v, gs, 0.1, s0, None, do, ds)
+        out, state = la.gated_fwd(gpu(q), gpu(k), gpu(v), gpu(gs), scale=0.1, state0=gpu(s0))
+        close("out", out, want, m["out"], dtype, steps_of(L, d, d))
+        close("state", state, wstate, m["state"], F32, steps_of(L, d, d))
+        check_grads(grads_of(q, k, v, gs, do, 0.1, s0, None, ds), ref.backward(q, k, v, gs, do, 0.1, s0, None, ds), m, dtype,
+                    gs, steps_of(L, d, d))
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
