@@ -118,7 +118,7 @@ template <int DX, int DZ, bool DOT> struct GtLayout {
     // the second score block has columns of its own where they are left, else those of Oi
     static constexpr bool A2_OWN = T_A + 128 <= 512;
     static constexpr uint32_t T_A2 = A2_OWN ? T_A + 64 : T_OI;
-    static_assert(T_A + 64 <= 512 && ALLOC <= 232448 - 64 && STAGES >= 2, "fits");
+    static_assert(T_A + 64 <= 512 && ALLOC <= 232448 - 64 && STAGES >= (DOT ? 2 : 3), "fits");
     static_assert(STAGE % 1024 == 0 && YT % 1024 == 0, "swizzle atoms");
 };
 
@@ -211,6 +211,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
              *const w_free = drain + 1;
     uint32_t *const tmem_slot = (uint32_t *)(sm + Lay::OFF_BAR + 224);
     volatile int *const abort_flag = (volatile int *)(sm + Lay::OFF_BAR + 228);
+
+    // The totals pass works on two chunks at a time: the second place of Y~ is the tiles of X, which it does not load,
+    // that of dS the columns of Oi and after, the second barriers are ones that it does not need otherwise.
+    uint64_t *const y_done[2] = {yt_ready, sc_free}, *const ds_done[2] = {state_done, scores_done}, *const ds_free[2] = {s_ready, p_ready};
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int BH = a.B * a.H, bh = blockIdx.x % BH, seg = blockIdx.x / BH, b = bh / a.H, h = bh % a.H;
@@ -426,25 +430,36 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         };
         // the second scores of the next chunk lie in Oi's columns: they wait for the rows' readers
         constexpr bool late = INNER && !Lay::A2_OWN;
-        bool ok = totals || n == 0 || scores(0);
+        auto sums_of = [&](int c, uint32_t y0, uint32_t y_step, uint32_t column) {  // dS of chunk c
+            const uint64_t dz = smem_desc(smem_u32(tile_z(c % NST)), C * 128, 1024);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                const uint64_t dy = smem_desc(y0 + p * y_step, C * 128, 1024);
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    mma_ss_if(tm + column, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0, one);
+            }
+        };
+        if (!DOT && totals)
+            for (int c = 0; c < n; ++c) {
+                const int i = c & 1;
+                if (c >= 2 && !wait(ds_free[i], ((c >> 1) - 1) & 1)) break;
+                if (!wait(y_done[i], (c >> 1) & 1)) break;
+                tc_fence_after();
+                if (i) sums_of(c, smem_u32(tile_x(0)), Lay::STAGE, Lay::T_OI);
+                else sums_of(c, smem_u32(yt), Lay::X, Lay::T_DS);
+                mma_commit_if(ds_done[i], one);
+                mma_commit_if(&stage_free[c % NST], one);
+            }
+        bool ok = n > 0 && !totals && scores(0);
         for (int c = 0; ok && c < n; ++c) {
             const int s = c % NST;
             const uint64_t dz = smem_desc(smem_u32(tile_z(s)), C * 128, 1024);
             if (!(ok = wait(s_ready, c & 1))) break;  // the state's copy, and dS has been read
             if (!(ok = wait(yt_ready, c & 1))) break;
             tc_fence_after();
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                const uint64_t dy = smem_desc(smem_u32(yt + p * Lay::X), C * 128, 1024);
-#pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    mma_ss_if(tm + Lay::T_DS, desc_add(dz, k * 2048), desc_add(dy, k * 2048), ID_STATE, p + k > 0, one);
-            }
+            sums_of(c, smem_u32(yt), Lay::X, Lay::T_DS);
             mma_commit_if(state_done, one);
-            if (totals) {
-                mma_commit_if(&stage_free[s], one);
-                continue;
-            }
             if (c > 0 && !(ok = wait(o_free, (c - 1) & 1))) break;
             if (late && !(ok = wait(sc_free, c & 1))) break;
             tc_fence_after();
@@ -590,22 +605,20 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 for (int i = 0; i < NX; ++i) p[i * DZ] = S[i / 2].v[i & 1];
         };
         auto copy = [&](int c) {  // of the state before chunk c
-            if (!totals) {
 #pragma unroll
-                for (int i = 0; i < NX; i += 16) {
-                    uint32_t p[3][8];
+            for (int i = 0; i < NX; i += 16) {
+                uint32_t p[3][8];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const Ch<2> &x = S[i / 2 + u];
-                        if (NS == 1) p[0][u] = pack_bf16x2(x.v[0], x.v[1]);
-                        else split3(x, p[0][u], p[1][u], p[2][u]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < NS; ++k)
-                        tmem_st8(tmem + lanes + Lay::T_SC + (k + c % Lay::COPIES) * (DX / 2) + (part * NX + i) / 2, p[k]);
+                for (int u = 0; u < 8; ++u) {
+                    const Ch<2> &x = S[i / 2 + u];
+                    if (NS == 1) p[0][u] = pack_bf16x2(x.v[0], x.v[1]);
+                    else split3(x, p[0][u], p[1][u], p[2][u]);
                 }
-                tmem_wait_st();
+#pragma unroll
+                for (int k = 0; k < NS; ++k)
+                    tmem_st8(tmem + lanes + Lay::T_SC + (k + c % Lay::COPIES) * (DX / 2) + (part * NX + i) / 2, p[k]);
             }
+            tmem_wait_st();
             tc_fence_before();
             arrive(s_ready);
         };
@@ -613,7 +626,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         const int anchors_here = a.anchors ? (t1 - t0 + a.anchor_chunks * C - 1) / (a.anchor_chunks * C) : 0;
         if (a.anchors && rev)  // those that end behind the sequence
             for (int k = (nch + a.anchor_chunks - 1) / a.anchor_chunks; k < anchors_here; ++k) anchor(first_anchor + k);
-        copy(0);
+        if (!totals) copy(0);
 
         const int ft = 32 * (warp - GT_W0) + lane;
         constexpr int G = DX / 8, RG = 32 * GT_WORKERS / G, NR = C / RG;  // 16-byte pieces of a row; rows rg, rg + RG
@@ -625,8 +638,74 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 *(uint32_t *)(p_tile + ta * 128 + (((2 * part + k) ^ (ta & 7)) << 4) + 4 * cpos) = 0;
                 *(uint32_t *)(p_tile + tb * 128 + (((2 * part + k) ^ (tb & 7)) << 4) + 4 * cpos) = 0;
             }
+        auto form_y = [&](int c, uint8_t *y0, int y_step) {
+            const int s = c % NST, row0 = t0 + chunk_of(c) * C, nv = min(C, te - row0);
+            const Weights &w = weights[c % GT_SLOTS];
+            const uint8_t *const src = tile_y(s) + off;
+            uint8_t *const dst = y0 + off;
+            uint4 v[NR];
+#pragma unroll
+            for (int m = 0; m < NR; ++m) v[m] = *(const uint4 *)(src + m * RG * 128);
+#pragma unroll
+            for (int m = 0; m < NR; ++m) {
+                const int r = rg + m * RG;
+                const Ch<2> kw = all<2>(w.kw[r]);
+                uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w}, hi[4], mid[4], lo[4];
+                if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
+                uint8_t *const d = dst + m * RG * 128;
+                *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4 *)(d + y_step) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                *(uint4 *)(d + 2 * y_step) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (nv < C)
+                for (int e = ft; e < (C - nv) * (DZ / 8); e += 32 * GT_WORKERS) {
+                    const int r = nv + e / (DZ / 8), p = e % (DZ / 8);
+                    *(uint4 *)(tile_z(s) + (p >> 3) * C * 128 + r * 128 + ((p & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+            fence_async_smem();
+        };
+        // The state over chunk c; next to 1 by the decay minus 1, whose rounding does not grow with the chunks.
+        auto advance = [&](int c, uint32_t column, auto read) {
+            uint32_t d[NX / 16][16];
+#pragma unroll
+            for (int i = 0; i < NX / 16; ++i) tmem_ld16(tmem + lanes + column + part * NX + 16 * i, d[i]);
+            const Weights &w = weights[c % GT_SLOTS];
+            const float da = w.a, em = w.em;
+            const bool near = da > 0.5f;
+            const Ch<2> m = all<2>(near ? em : da), one = all<2>(near ? 1.f : 0.f);
+            if (da == 0.f)  // forgets infinities and NaN too
+#pragma unroll
+                for (int i = 0; i < NX / 2; ++i) S[i] = all<2>(0.f);
+            tmem_wait_ld();
+            read();
+#pragma unroll
+            for (int i = 0; i < NX / 2; ++i) {
+                const Ch<2> ds{{__uint_as_float(d[i / 8][2 * (i % 8)]), __uint_as_float(d[i / 8][2 * (i % 8) + 1])}};
+                S[i] = fma(S[i], m, fma(S[i], one, ds));
+            }
+        };
         bool ok = true;
-        for (int c = 0; c < nch; ++c) {
+        if (!DOT && totals)
+            for (int c = 0; c <= nch; ++c) {  // Y~ of one chunk, then the sum of the one before
+                if (c < nch) {
+                    if (!(ok = wait(&full[c % NST], (c / NST) & 1))) break;
+                    if (c & 1) form_y(c, tile_x(0), Lay::STAGE);
+                    else form_y(c, yt, Lay::X);
+                    arrive(y_done[c & 1]);
+                }
+                if (c > 0) {
+                    const int i = (c - 1) & 1;
+                    if (!(ok = wait(ds_done[i], ((c - 1) >> 1) & 1))) break;
+                    tc_fence_after();
+                    advance(c - 1, i ? Lay::T_OI : Lay::T_DS, [&]() {
+                        tc_fence_before();
+                        arrive(ds_free[i]);
+                    });
+                }
+            }
+        for (int c = 0; !totals && c < nch; ++c) {
             const int s = c % NST, cc = chunk_of(c), row0 = t0 + cc * C, nv = min(C, te - row0);
             const Weights &w = weights[c % GT_SLOTS];
             if (a.anchors) {
@@ -635,140 +714,99 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             }
             // ---- Y~ (the one before has been read: dS of the chunk before was waited for)
             if (!(ok = wait(&full[s], (c / NST) & 1))) break;
-            {
-                const uint8_t *const src = tile_y(s) + off;
-                uint8_t *const dst = yt + off;
-                uint4 v[NR];
-#pragma unroll
-                for (int m = 0; m < NR; ++m) v[m] = *(const uint4 *)(src + m * RG * 128);
-#pragma unroll
-                for (int m = 0; m < NR; ++m) {
-                    const int r = rg + m * RG;
-                    const Ch<2> kw = all<2>(w.kw[r]);
-                    uint32_t u[4] = {v[m].x, v[m].y, v[m].z, v[m].w}, hi[4], mid[4], lo[4];
-                    if (r >= nv) u[0] = u[1] = u[2] = u[3] = 0;  // behind the end: zeros, whatever is there
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) split3(mul(Ch<2>{{bf_lo(u[i]), bf_hi(u[i])}}, kw), hi[i], mid[i], lo[i]);
-                    uint8_t *const d = dst + m * RG * 128;
-                    *(uint4 *)d = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *(uint4 *)(d + Lay::X) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *(uint4 *)(d + 2 * Lay::X) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            if (nv < C)
-                for (int e = ft; e < (C - nv) * (DZ / 8); e += 32 * GT_WORKERS) {
-                    const int r = nv + e / (DZ / 8), p = e % (DZ / 8);
-                    *(uint4 *)(tile_z(s) + (p >> 3) * C * 128 + r * 128 + ((p & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                }
-            fence_async_smem();
+            form_y(c, yt, Lay::X);
             arrive(yt_ready);
-            if (!totals) {
-                // ---- the rows of the chunk before
-                if (!DOT && c > 0) {
-                    if (!(ok = wait(o_done, (c - 1) & 1))) break;
-                    tc_fence_after();
-                    rows(c - 1);
-                }
-                // ---- P. Its one place has been read; with the intra product of the chunk before, this chunk's scores
-                // are done too (not with DOT, whose issuer may take them up later).
-                if ((DOT || c == 0) && !(ok = wait(scores_done, c & 1))) break;
+            // ---- the rows of the chunk before
+            if (!DOT && c > 0) {
+                if (!(ok = wait(o_done, (c - 1) & 1))) break;
                 tc_fence_after();
-                uint32_t r1[8], r2[8];
-                tmem_ld16x256_x2(tmem + Lay::T_A + lanes + 16 * part, r1);
-                if (INNER) tmem_ld16x256_x2(tmem + Lay::T_A2 + lanes + 16 * part, r2);
-                // columns from <= col < to of a row count: up to the row itself, or in reverse from it on
-                int from[2], to[2];
-                Ch<2> ghi[2], glo[2];
+                rows(c - 1);
+            }
+            // ---- P. Its one place has been read; with the intra product of the chunk before, this chunk's scores
+            // are done too (not with DOT, whose issuer may take them up later).
+            if ((DOT || c == 0) && !(ok = wait(scores_done, c & 1))) break;
+            tc_fence_after();
+            uint32_t r1[8], r2[8];
+            tmem_ld16x256_x2(tmem + Lay::T_A + lanes + 16 * part, r1);
+            if (INNER) tmem_ld16x256_x2(tmem + Lay::T_A2 + lanes + 16 * part, r2);
+            // columns from <= col < to of a row count: up to the row itself, or in reverse from it on
+            int from[2], to[2];
+            Ch<2> ghi[2], glo[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = r ? tb : ta;
+                from[r] = (rev ? row : 0) - col0;
+                to[r] = (row >= nv ? 0 : rev ? nv : row + 1) - col0;
+                ghi[r] = all<2>(w.hi[row]);
+                glo[r] = all<2>(w.lo[row]);
+            }
+            float sum[2] = {0.f, 0.f}, sc[4] = {0.f, 0.f, 0.f, 0.f};
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive(sc_free);
+            // (blocks behind the diagonal are 0: written once, before the loop)
+            if (rev ? part >= q4 : part <= q4)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 h2 = *(const float2 *)&w.hi[col0 + 8 * k], l2 = *(const float2 *)&w.lo[col0 + 8 * k];
+                const Ch<2> chi{{h2.x, h2.y}}, clo{{l2.x, l2.y}};
+                uint32_t p[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int row = r ? tb : ta;
-                    from[r] = (rev ? row : 0) - col0;
-                    to[r] = (row >= nv ? 0 : rev ? nv : row + 1) - col0;
-                    ghi[r] = all<2>(w.hi[row]);
-                    glo[r] = all<2>(w.lo[row]);
-                }
-                float sum[2] = {0.f, 0.f}, sc[4] = {0.f, 0.f, 0.f, 0.f};
-                tmem_wait_ld();
-                tc_fence_before();
-                arrive(sc_free);
-                // (blocks behind the diagonal are 0: written once, before the loop)
-                if (rev ? part >= q4 : part <= q4)
+                    const int e = 4 * k + 2 * r;
+                    const Ch<2> d = add(fma(chi, minus, ghi[r]), fma(clo, minus, glo[r])), wt{{ex2(d.v[0]), ex2(d.v[1])}};
+                    Ch<2> x = mul(mul(Ch<2>{{__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])}}, wt), ps);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 h2 = *(const float2 *)&w.hi[col0 + 8 * k], l2 = *(const float2 *)&w.lo[col0 + 8 * k];
-                    const Ch<2> chi{{h2.x, h2.y}}, clo{{l2.x, l2.y}};
-                    uint32_t p[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int e = 4 * k + 2 * r;
-                        const Ch<2> d = add(fma(chi, minus, ghi[r]), fma(clo, minus, glo[r])), wt{{ex2(d.v[0]), ex2(d.v[1])}};
-                        Ch<2> x = mul(mul(Ch<2>{{__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])}}, wt), ps);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const bool in = 8 * k + u >= from[r] && 8 * k + u < to[r];
-                            if (INNER) {
-                                const bool own = 8 * k + u == (r ? tb : ta) - col0;
-                                const float y = in && !own ? x.v[u] * __uint_as_float(r2[e + u]) : 0.f;
-                                sum[r] += y;
-                                if (r == 0) sc[2 * k + u] = y;
-                                else sc[2 * k + u] += y;
-                            }
-                            x.v[u] = in ? x.v[u] : 0.f;
+                    for (int u = 0; u < 2; ++u) {
+                        const bool in = 8 * k + u >= from[r] && 8 * k + u < to[r];
+                        if (INNER) {
+                            const bool own = 8 * k + u == (r ? tb : ta) - col0;
+                            const float y = in && !own ? x.v[u] * __uint_as_float(r2[e + u]) : 0.f;
+                            sum[r] += y;
+                            if (r == 0) sc[2 * k + u] = y;
+                            else sc[2 * k + u] += y;
                         }
-                        p[r] = pack_bf16x2(x.v[0], x.v[1]);
+                        x.v[u] = in ? x.v[u] : 0.f;
                     }
-                    const int ch = 2 * part + k;
-                    *(uint32_t *)(p_tile + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = p[0];
-                    *(uint32_t *)(p_tile + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = p[1];
+                    p[r] = pack_bf16x2(x.v[0], x.v[1]);
                 }
-                fence_async_smem();
-                arrive(p_ready);
-                if (INNER) {
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-                        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-                    }
-                    float *const rp = a.dot + ((long long)(4 + part) * BH + bh) * a.L + row0;
-                    if (cpos == 0) {
-                        if (ta < nv) rp[ta] = sum[0];
-                        if (tb < nv) rp[tb] = sum[1];
-                    }
-                    int at_c = 0;
-#pragma unroll
-                    for (int o = 4, n = 2; n > 0; o <<= 1, n >>= 1) {
-                        const bool up = lane & o;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (i < n) {
-                                const float send = up ? sc[i] : sc[i + n], keep = up ? sc[i + n] : sc[i];
-                                sc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-                            }
-                        at_c += up ? n : 0;
-                    }
-                    sc[0] += __shfl_xor_sync(0xffffffffu, sc[0], 16);
-                    const int col = col0 + 8 * (at_c >> 1) + (at_c & 1);
-                    if (!(lane & 16) && col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
-                }
+                const int ch = 2 * part + k;
+                *(uint32_t *)(p_tile + ta * 128 + ((ch ^ (ta & 7)) << 4) + 4 * cpos) = p[0];
+                *(uint32_t *)(p_tile + tb * 128 + ((ch ^ (tb & 7)) << 4) + 4 * cpos) = p[1];
             }
-            // ---- the state: next to 1 by the decay minus 1, whose rounding does not grow with the chunks
+            fence_async_smem();
+            arrive(p_ready);
+            if (INNER) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+                    sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+                }
+                float *const rp = a.dot + ((long long)(4 + part) * BH + bh) * a.L + row0;
+                if (cpos == 0) {
+                    if (ta < nv) rp[ta] = sum[0];
+                    if (tb < nv) rp[tb] = sum[1];
+                }
+                int at_c = 0;
+#pragma unroll
+                for (int o = 4, n = 2; n > 0; o <<= 1, n >>= 1) {
+                    const bool up = lane & o;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (i < n) {
+                            const float send = up ? sc[i] : sc[i + n], keep = up ? sc[i + n] : sc[i];
+                            sc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                    at_c += up ? n : 0;
+                }
+                sc[0] += __shfl_xor_sync(0xffffffffu, sc[0], 16);
+                const int col = col0 + 8 * (at_c >> 1) + (at_c & 1);
+                if (!(lane & 16) && col < nv) a.dotc[((long long)q4 * BH + bh) * a.L + row0 + col] = sc[0];
+            }
+            // ---- the state
             if (!(ok = wait(state_done, c & 1))) break;
             tc_fence_after();
-            uint32_t d[NX / 16][16];
-#pragma unroll
-            for (int i = 0; i < NX / 16; ++i) tmem_ld16(tmem + lanes + Lay::T_DS + part * NX + 16 * i, d[i]);
-            const float da = w.a, em = w.em;
-            const bool near = da > 0.5f;
-            const Ch<2> m = all<2>(near ? em : da), one = all<2>(near ? 1.f : 0.f);
-            if (da == 0.f)  // forgets infinities and NaN too
-#pragma unroll
-                for (int i = 0; i < NX / 2; ++i) S[i] = all<2>(0.f);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < NX / 2; ++i) {
-                const Ch<2> ds{{__uint_as_float(d[i / 8][2 * (i % 8)]), __uint_as_float(d[i / 8][2 * (i % 8) + 1])}};
-                S[i] = fma(S[i], m, fma(S[i], one, ds));
-            }
+            advance(c, Lay::T_DS, []() {});
             if (DOT && !(ok = wait(inter_done, c & 1))) break;  // the copy has been read
             copy(c + 1);
             if (DOT) {
