@@ -700,13 +700,18 @@ size_t la_block_norm_bwd_workspace_bytes(int B, int L, int d);
  *   out           [B, H, L, dv], dtype `dtype`
  *   dk, dv        at most 256, B * H at most 65535
  *   scale         finite, else LA_ERR_ARG
- *   path          enum la_path.  LA_PATH_SIMT takes every case, in fp32 row by row.
+ *   path          enum la_path.  LA_PATH_SIMT takes every case, in fp32 row by row.  LA_PATH_TC takes bf16 with
+ *                 dk and dv of 64 or 128 each, rows of q, k, v and out on 16-byte boundaries and no stride of
+ *                 0 (LA_ERR_UNSUPPORTED otherwise); LA_PATH_AUTO takes it there, for any length.
  *   workspace     device memory of la_gated_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0)
- * States, decays and sums are fp32; out is rounded once.  q, k, v are meant to be finite: an infinity or
- * NaN in a row may reach every row of its chunk of 64 and those behind; only rows behind a sequence's
- * end, and what a log decay of -inf lies between in different chunks, keep theirs.  The order of the sums
- * depends on the sizes and the GPU alone, so equal calls give equal bits.  Outputs must not overlap
- * inputs, but for state.
+ * States, decays and sums are fp32; out is rounded once.  LA_PATH_TC rounds two operands of its products to
+ * bf16 (each off by 2^-8 of itself at most): a row's weighted scores, and the state where only out reads it; the
+ * state itself is summed to fp32.  A log decay below -104, whose decay fp32 does not hold, counts as -inf.
+ * q, k, v are meant to be finite: an infinity or NaN in a row may reach every row of its chunk of 64 and
+ * those behind; only rows behind a sequence's end, and what a log decay of -inf lies between in
+ * different chunks, keep theirs.  The order of the sums depends on the sizes, the path, the GPU and the
+ * decays alone, so equal calls give equal bits.  Outputs must not overlap inputs, but for state.
+ * Every wait inside LA_PATH_TC has a limit: LA_ERR_TIMEOUT from la_last_device_status.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED, LA_ERR_ARG (strides, alignment, scale),
  * LA_ERR_WORKSPACE or LA_ERR_CUDA.  Asynchronous on `stream`.
  */
@@ -734,11 +739,15 @@ size_t la_gated_workspace_bytes(int B, int H, int L, int dk, int dv, int dtype);
  *                 head are the sums over its heads
  *   dlog_decay    device fp32 contiguous [B, H, L], or NULL
  *   dlog_decay_head  device fp32 [H]: its sums over sequences and rows, the gradient of a constant for
- *                 each head; or NULL.  Without both the decays' gradient is not formed.
+ *                 each head; or NULL.  Without both the decays' gradient is not formed.  It is summed
+ *                 back over up to 1024 rows from products of states, so it is off by a few fp32
+ *                 roundings of the largest values (and of <dstate, state>) among those rows.  It is 0 itself
+ *                 where the decay is, and for a first row without state0.
  *   dstate0       device fp32 [B, H, dk, dv] or NULL; may be dstate.  Otherwise outputs must not overlap
  *                 inputs.
  *   workspace     la_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned
- * Other arguments and errors as la_gated_fwd (no slots).
+ * Other arguments and errors as la_gated_fwd (no slots); LA_PATH_TC also wants dout, dq, dk, dv as q, and state0,
+ * dstate and dstate0 on 16-byte boundaries.
  */
 int la_gated_bwd(const void *q, const void *k, const void *v, const float *log_decay,
                  const float *state0, const int *lengths, const void *dout, const float *dstate,
