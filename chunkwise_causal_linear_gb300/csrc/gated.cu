@@ -14,9 +14,9 @@
 //
 // sweep_kernel runs the recurrence row by row in fp32: a thread holds 16 x 8 elements of the state, in
 // pairs of rows for the packed instructions, and a row costs three of them per pair: decay, product
-// with x, new pair.  It is bound by the fp32 pipes (24 dk dv operations of a packed pair's half a row and
-// head); rows of the operands reach shared memory by cp.async one tile ahead.  Few heads are cut into segments
-// whose sums are formed first.
+// with x, new pair (1.5 dk dv instructions of fp32 a row and head).  Short sequences are bound by the latency of a
+// row's steps, about 0.5 us, long ones by the fp32 pipes; rows of the operands reach shared memory by cp.async one
+// tile ahead.  Few heads are cut into segments whose sums are formed first.
 #include <math.h>
 
 #include <algorithm>
@@ -505,7 +505,7 @@ struct LogDecayArgs {
     View vg;
     float *dg;
     const int *lengths;
-    int nr, nc, B, H, L, seg_rows, nseg;
+    int nr, nc, B, H, L, seg_rows, nseg, initial;
 };
 // A block a segment, 1024 rows at a time from its end, four neighbouring ones a thread; a row's parts are summed in
 // fp32, the rows in 64 bits, few operations of which a row leaves (the SM has two such lanes: a scan of every
@@ -559,8 +559,9 @@ __global__ void __launch_bounds__(LD_THREADS) log_decay_kernel(const LogDecayArg
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int k = threadIdx.x + LD_THREADS * u, t = e - 1 - k;
-            // a decay of 0 has no gradient: every pair across it is 0
-            if (t >= t0) a.dg[at + t] = a.g[row_of(a.vg, b, h, t)] < GATED_CUT ? 0.f : diff[k];
+            // a decay of 0 has no gradient: every pair across it is 0; nor has one with nothing before it
+            const bool none = t >= t0 && (a.g[row_of(a.vg, b, h, t)] < GATED_CUT || (t == 0 && !a.initial));
+            if (t >= t0) a.dg[at + t] = none ? 0.f : diff[k];
         }
         __syncthreads();
     }
@@ -747,7 +748,7 @@ int gated_products(const GatedArgs &p, const float *D, const float *S, float *y,
 int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, int nc, const float *y, int seg_rows,
                     int nseg, float *dg)
 {
-    const LogDecayArgs a{r, c, y, p.g, p.vg, dg, p.lengths, nr, nc, p.B, p.H, p.L, seg_rows, nseg};
+    const LogDecayArgs a{r, c, y, p.g, p.vg, dg, p.lengths, nr, nc, p.B, p.H, p.L, seg_rows, nseg, p.state0 != nullptr};
     int rc = launch(log_decay_kernel, dim3((unsigned)(p.B * p.H * nseg)), LD_THREADS, 0, p.stream, a);
     if (rc == LA_OK && p.dg_head) rc = launch(head_sum_kernel, dim3((unsigned)p.H), 1024, 0, p.stream, HeadSumArgs{dg, p.dg_head, p.B, p.H, p.L});
     return rc;

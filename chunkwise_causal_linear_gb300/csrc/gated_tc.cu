@@ -63,7 +63,7 @@ struct GtArgs {
     void *out;
     int out_f32;
     int sx, sy, sz, sw;  // heads of the state to a head of the operand
-    int B, H, L, e;      // e: channels of out
+    int B, H, L;
     float yscale, oscale;
     int reverse, totals;
     int seg_rows, nseg;
@@ -897,7 +897,6 @@ int launch_pass(const GatedArgs &p, Pass &s)
     a.g = p.g; a.vg = p.vg;
     a.lengths = p.lengths;
     a.err = p.err;
-    a.e = s.z.d;
     a.totals = s.x.p == nullptr;
     a.timeout_ns = 2000000000ull;
     if (const char *e = getenv("LA_DEBUG_TIMEOUT_NS"); e && *e) a.timeout_ns = strtoull(e, nullptr, 10);

@@ -272,6 +272,17 @@ def test_odd_alignment_and_broadcast(dtype):
     check_grads(got, ref.backward(q, k, v, g, do, 1.0), m, dtype, g, steps_of(L, d, d))
 
 
+@pytest.mark.parametrize("dtype,d", [(F32, 40), (BF16, 64)], ids=["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 2, 300])
+def test_the_first_decay_without_a_state(L, dtype, d):
+    """Nothing is before the first row: its decay's gradient is 0 itself, not a difference's rounding."""
+    q, k, v, g, _, _, do, ds = (gpu(x) for x in ref.draw(3, 4, 2, L, d, d, dtype, seed=L))
+    dg = la.gated_bwd(q, k, v, g, do, dstate=ds)[3]
+    assert not dg[:, :, 0].any() and (L == 1 or dg[:, :, 1].any())
+    if L == 1:
+        assert not la.gated_bwd(q, k, v, -torch.rand(4, device="cuda"), do, dstate=ds)[3].any()
+
+
 def test_a_decay_of_zero_forgets():
     """-inf at every row: each row sees its own pair only, and the decays have no gradient."""
     B, H, L, d = 1, 2, 70, 64
@@ -360,6 +371,63 @@ def test_captured_and_on_another_stream():
         assert torch.equal(x, y)
 
 
+def test_two_calls_at_once():
+    """Calls on two streams whose kernels overlap, each with a workspace of its own."""
+    sizes = [(1, 3, 3, 3000, 64, 64), (2, 4, 2, 900, 128, 128)]
+    ins = [[gpu(x) for x in ref.draw(*size, BF16, "token", True, True, seed=23 + i)] for i, size in enumerate(sizes)]
+
+    def call(i):
+        q, k, v, g, s0, n, do, ds = ins[i]
+        return [*la.gated_fwd(q, k, v, g, state0=s0, lengths=n), *la.gated_bwd(q, k, v, g, do, state0=s0, lengths=n, dstate=ds)]
+
+    want = [call(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = call(i)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert la.la_last_device_status(None) == la.LA_OK
+
+
+FIRST = """
+import torch, chunkwise_causal_linear_gb300 as la
+torch.manual_seed(0)
+q, k, v = (torch.randn(1, 2, 700, 64, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+g = -torch.rand(1, 2, 700, device="cuda")
+y = torch.randn(3, 5, 256, device="cuda")
+pool = torch.zeros(1, 2, 64, 64, device="cuda")
+x = torch.randn(1, 1, 8, device="cuda")
+la.decode_step(x, x, x, la.decode_state(1, 1, 8, 8)[0])  # the library's first call, none of these operators
+torch.cuda.synchronize()
+def call():
+    a = list(la.gated_fwd(q, k, v, g)) + list(la.gated_bwd(q, k, v, g, v))
+    b = list(la.block_norm_fwd(y, y)) + [x for x in la.block_norm_bwd(y, y, y, y).values() if x is not None]
+    pool.zero_()
+    return a + b + [la.gated_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g[:, :, 0], pool)]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = call()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, call()))
+"""
+
+
+def test_first_calls_in_a_capture():
+    """A process whose first calls of these operators are captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
 def test_a_layer_of_it():
     """As a mixer uses it: rotary positions, gated attention, group norm with a gate; prompts and their
     gradients against the 64-bit forms."""
@@ -394,3 +462,12 @@ def test_a_layer_of_it():
                 m | dict(dstate0=torch.ones(B, H, d, d)), F32, g, steps_of(L, d, d))
     back = la.rotary(dq, dk, table, inverse=True)
     assert all(torch.isfinite(x).all() for x in back)
+    # and the norms around the layer
+    res = gpu(torch.randn(B, L, H * d, generator=torch.Generator().manual_seed(5)))
+    h, n = la.block_norm_fwd(out, res, post_norm="none", pre_norm="rms")
+    wh = res.double().cpu() + out.double().cpu()
+    assert (h.double().cpu() - wh).abs().max() <= 2 * ref.U * float(wh.abs().max())
+    wn = wh / (wh.square().mean(-1, keepdim=True) + 1e-5).sqrt()
+    assert (n.double().cpu() - wn).abs().max() <= 64 * ref.U * float(wn.abs().max())
+    got = la.block_norm_bwd(out, res, None, res, post_norm="none", pre_norm="rms")
+    assert torch.equal(got["dy"], got["dr"])
