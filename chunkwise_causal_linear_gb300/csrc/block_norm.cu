@@ -8,12 +8,15 @@
 //
 // Bound by memory: y, r and gate are read once, h and n written once; apart, the two norms, the gate and the
 // sum would read and write h and the norm's output once more each. A row is held in the registers of NT
-// threads, 8 channels a thread (16 for rows above 4096), so that its statistics, centred variance and
+// threads, 8 channels each (16 in rows above 1536), so that its statistics, centred variance and
 // both norms come from that one read. Each thread copies its channels of the next rows ahead into places of
 // its own in shared memory (cp.async, a ring of rows, no barrier), which costs no registers and hides the
-// sums' barriers; rows that cannot be read 16 bytes at a time are loaded one row ahead. The gradients recompute the statistics from y and r (32-bit sums; h before its rounding)
-// instead of reading them, and keep the sums for the weights' gradients in the threads' registers; the
-// groups' sums are joined by a second kernel in a fixed order.
+// sums' barriers; rows that cannot be read 16 bytes at a time are loaded one row ahead, forwards. The gradients
+// recompute the statistics from y and r (32-bit sums; h before its rounding) instead of reading them, and keep
+// the sums for the weights' gradients in the threads' registers; the groups' sums are joined by a second kernel in a
+// fixed order. Forwards the copies bind (B8 L8192 d2048 229 us, 86% of the measured copy rate), the gradients are bound
+// by up to five sums over the row's threads, one after the other, and their instructions (518 us, 61%; of the schedulers'
+// slots 45% are used).
 #include <math.h>
 
 #include <algorithm>
@@ -206,11 +209,18 @@ struct RowAt {
     }
 };
 
-template <int NT, bool BWD> constexpr int bn_block = NT < (BWD ? 128 : 256) ? (BWD ? 128 : 256) : NT;
+template <int NT, bool BWD> constexpr int bn_block = BWD ? (128 % NT == 0 ? 128 : NT) : 256 % NT == 0 ? 256 : NT < 192 ? 192 : NT;
+// Threads of the gradients' kernel that an SM is to hold, and with that the registers of each (128 or 168): 16 channels
+// of a row of up to 2048 spill at 128 (d2048 518 us, 562 at 128), longer rows are waited for too long with one block
+// (d4096 431 us with two of 256, 477 with one).
+template <int NT, int NC> constexpr int bn_threads = NC == 1 || (NC == 2 && NT >= 256) ? 512 : 384;
+template <int NT, int NC>
+constexpr int bn_held = bn_threads<NT, NC> < bn_block<NT, true> ? 1 : bn_threads<NT, NC> / bn_block<NT, true>;
 
-// Rows on their way to a thread: three, or what 384 threads of an SM can have of its shared memory (200 KB for 512).
-template <int VEC, int STAGE, int BLOCK>
-constexpr int AHEAD = VEC != 8 ? 1 : 3 * STAGE <= (BLOCK < 356 ? BLOCK * 576 : 204800) ? 3 : 2 * STAGE <= (BLOCK < 356 ? BLOCK * 576 : 204800) ? 2 : 1;
+// Rows on their way to a thread: three, or what the threads of an SM can have of its shared memory.
+template <int VEC, int STAGE, int BLOCK, int THREADS = 384>
+constexpr int AHEAD = VEC != 8 ? 1 : 3 * STAGE <= std::min(BLOCK * (221184 / THREADS), 204800) ? 3
+                               : 2 * STAGE <= std::min(BLOCK * (221184 / THREADS), 204800) ? 2 : 1;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
@@ -402,13 +412,13 @@ __device__ __forceinline__ void norm_back(Ch<W> (&dxh)[M], const Ch<W> (&xh)[M],
 
 // BIAS: sums for the biases too.
 template <typename T, typename R, int VEC, int NT, int NC, bool BIAS>
-__global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 ? 3 : 1) bn_bwd_kernel(const BnArgs a)
+__global__ void __launch_bounds__(bn_block<NT, true>, bn_held<NT, NC>) bn_bwd_kernel(const BnArgs a)
 {
     constexpr int BLOCK = bn_block<NT, true>;
     BN_ROWS(step)
     extern __shared__ __align__(16) uint8_t ring[];
     constexpr int BT = Ahead<T, VEC, NC, BLOCK>::BYTES, BR = Ahead<R, VEC, NC, BLOCK>::BYTES,
-                  STAGE = 3 * BT + 2 * BR, PF = AHEAD<VEC, STAGE, BLOCK>;
+                  STAGE = 3 * BT + 2 * BR, PF = AHEAD<VEC, STAGE, BLOCK, bn_threads<NT, NC>>;
     Ch<W> total[BIAS ? 4 : 2][M];  // post_w, pre_w, post_b, pre_b
 #pragma unroll
     for (int k = 0; k < (BIAS ? 4 : 2); ++k)
@@ -438,21 +448,23 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 
     for (int i = 0; i < PF; ++i) fetch(first + i * step, i);
     int slot = 0;
     for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
-        Ch<W> u[M], h[M], z[M], sg[M], act[M], dh[M], dn[M];
-#pragma unroll
-        for (int i = 0; i < M; ++i) u[i] = h[i] = z[i] = dh[i] = dn[i] = all<W>(0.f);
+        // what is needed late (dn, dh, and the gate once more) stays in the ring until then: registers held over
+        // the sums are what the kernel has least of
+        Ch<W> u[M], h[M], sg[M], act[M], dh[M];
         row_arrived<VEC, PF>();
+        {
+            Ch<W> z[M];
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (in[c]) {
-                ry.get(flat(u, c * VEC), slot, c);
-                rr.get(flat(h, c * VEC), slot, c);
-                if (a.gate) rg.get(flat(z, c * VEC), slot, c);
-                if (a.dh) rdh.get(flat(dh, c * VEC), slot, c);
-                if (a.dn) rdn.get(flat(dn, c * VEC), slot, c);
-            }
-        fetch(row + PF * step, slot);
-        activate<T>(z, sg, act, a);
+            for (int i = 0; i < M; ++i) u[i] = h[i] = z[i] = dh[i] = all<W>(0.f);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c]) {
+                    ry.get(flat(u, c * VEC), slot, c);
+                    rr.get(flat(h, c * VEC), slot, c);
+                    if (a.gate) rg.get(flat(z, c * VEC), slot, c);
+                }
+            activate<T>(z, sg, act, a);
+        }
         const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum);
         const Ch<W> k1w = all<W>(k1), bs = all<W>(a.bs), rs = all<W>(a.rs);
         // x = w xh + b of the norm behind the block
@@ -486,27 +498,32 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 
                 }
             const float k2 = statistics<VEC>(h, in, a.pre, a, sum);
             const Ch<W> k2w = all<W>(k2);
-            Ch<W> g[M];
 #pragma unroll
-            for (int i = 0; i < M; ++i) {
-                h[i] = mul(h[i], k2w);
-                total[1][i] = fma(dn[i], h[i], total[1][i]);
-                if (BIAS) total[BIAS ? 3 : 0][i] = add(total[BIAS ? 3 : 0][i], dn[i]);
-                g[i] = dn[i];
-            }
-            if (a.pre_w)
+            for (int c = 0; c < NC; ++c)
+                if (in[c]) {
+                    Ch<W> w[VEC / W], dn[VEC / W];
+                    rdn.get(dn[0].v, slot, c);
+                    weights<VEC>(a.pre_w, at[c], 1.f, w[0].v);
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    if (in[c]) {
-                        Ch<W> w[VEC / W];
-                        weights<VEC>(a.pre_w, at[c], 1.f, w[0].v);
-#pragma unroll
-                        for (int i = 0; i < VEC / W; ++i) g[c * VEC / W + i] = mul(dn[c * VEC / W + i], w[i]);
+                    for (int i = 0; i < VEC / W; ++i) {
+                        const int m = c * VEC / W + i;
+                        h[m] = mul(h[m], k2w);
+                        total[1][m] = fma(dn[i], h[m], total[1][m]);
+                        if (BIAS) total[BIAS ? 3 : 0][m] = add(total[BIAS ? 3 : 0][m], dn[i]);
+                        dh[m] = mul(dn[i], w[i]);
                     }
-            norm_back<VEC>(g, h, in, k2, a.pre, a, sum);
-#pragma unroll
-            for (int i = 0; i < M; ++i) dh[i] = add(dh[i], g[i]);
+                }
+            norm_back<VEC>(dh, h, in, k2, a.pre, a, sum);
         }
+        if (a.dh)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (in[c]) {
+                    Ch<W> x[VEC / W];
+                    rdh.get(x[0].v, slot, c);
+#pragma unroll
+                    for (int i = 0; i < VEC / W; ++i) dh[c * VEC / W + i] = add(x[i], dh[c * VEC / W + i]);
+                }
         // dh is the whole gradient of h
         R *const dr = (R *)a.dr + row_of(a.vdr, now.b, 0, now.t);
         T *const dg = (T *)a.dgate + row_of(a.vdg, now.b, 0, now.t);
@@ -519,6 +536,8 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 
                 put<VEC>(dr + at[c], o[0].v);
                 post(c, w, x);
                 if (a.gate) {
+                    Ch<W> z[VEC / W];
+                    if (a.act == LA_ACT_SILU) rg.get(z[0].v, slot, c);
 #pragma unroll
                     for (int i = 0; i < VEC / W; ++i) {
                         const int m = c * VEC / W + i;
@@ -526,7 +545,7 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 
                         // slope: s (1 + z (1 - s)), s (1 - s), or 1
                         if (a.act != LA_ACT_NONE) {
                             const Ch<W> rest = less(all<W>(1.f), sg[m]);
-                            o[i] = mul(o[i], mul(sg[m], a.act == LA_ACT_SILU ? fma(z[m], rest, all<W>(1.f)) : rest));
+                            o[i] = mul(o[i], mul(sg[m], a.act == LA_ACT_SILU ? fma(z[i], rest, all<W>(1.f)) : rest));
                         }
                     }
                     put<VEC>(dg + at[c], o[0].v);
@@ -548,6 +567,7 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_block<NT, true> == 128 
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             if (in[c]) put<VEC>(dy + at[c], flat(dh, c * VEC));
+        fetch(row + PF * step, slot);
         now.next(step_b, step_t, a.L);
     }
     if (a.part) {
@@ -612,7 +632,7 @@ __global__ void __launch_bounds__(1024) bn_join_kernel(const BnJoin a)
 template <typename T, typename R, int VEC, int NT, int NC, bool BWD> constexpr int ring_bytes(int d)
 {
     constexpr int block = bn_block<NT, BWD>, bt = Ahead<T, VEC, NC, block>::BYTES, br = Ahead<R, VEC, NC, block>::BYTES,
-                  stage = BWD ? 3 * bt + 2 * br : 2 * bt + br, ring = AHEAD<VEC, stage, block> * stage;
+                  stage = BWD ? 3 * bt + 2 * br : 2 * bt + br, ring = AHEAD<VEC, stage, block, BWD ? bn_threads<NT, NC> : 384> * stage;
     return BWD && NT < block ? std::max(ring, 16 * d) : ring;
 }
 
@@ -635,19 +655,35 @@ constexpr int BN_MOST_BLOCKS = 8;  // of an SM
 
 template <typename F> int by_shape(int d, bool wide, F &&f)
 {
-    if (!wide)
-        return d <= 256 ? f(std::integral_constant<int, 1>(), std::integral_constant<int, 32>(), std::integral_constant<int, 8>())
-                        : f(std::integral_constant<int, 1>(), std::integral_constant<int, 512>(), std::integral_constant<int, 16>());
-    // 16 channels a thread: half the sums' and the rows' overhead of 8 (B8 L8192 d2048: 307 and 837 us with 8)
-    std::integral_constant<int, 8> v;
     std::integral_constant<int, 1> one;
     std::integral_constant<int, 2> two;
-    if (d <= 256) return f(v, std::integral_constant<int, 32>(), one);
-    if (d <= 512) return f(v, std::integral_constant<int, 32>(), two);
-    if (d <= 1024) return f(v, std::integral_constant<int, 64>(), two);
-    if (d <= 2048) return f(v, std::integral_constant<int, 128>(), two);
-    if (d <= 4096) return f(v, std::integral_constant<int, 256>(), two);
-    return f(v, std::integral_constant<int, 512>(), two);
+    std::integral_constant<int, 8> v;
+    std::integral_constant<int, 32> t32;
+    std::integral_constant<int, 64> t64;
+    std::integral_constant<int, 128> t128;
+    std::integral_constant<int, 256> t256;
+    std::integral_constant<int, 512> t512;
+    if (!wide) {
+        // single channels, 8 a thread (16 for the longest rows): as few threads as hold the row, so that none idles
+        // (B8 L4096 d500: 1850 us with 512 threads a row)
+        if (d <= 256) return f(one, t32, v);
+        if (d <= 512) return f(one, t64, v);
+        if (d <= 1024) return f(one, t128, v);
+        if (d <= 2048) return f(one, t256, v);
+        if (d <= 4096) return f(one, t512, v);
+        return f(one, t512, std::integral_constant<int, 16>());
+    }
+    // 8 channels a thread for rows up to 1536: their registers allow more rows at once (B2 L16384 d768 78 us and, with
+    // all sums, 167; 86 and 267 with 16). 16 beyond: half the sums' and the rows' overhead (B8 L8192 d2048
+    // 229 and 518 us, the gradients 580 with 8).
+    if (d <= 256) return f(v, t32, one);
+    if (d <= 512) return f(v, t64, one);
+    if (d <= 768) return f(v, std::integral_constant<int, 96>(), one);
+    if (d <= 1024) return f(v, t128, one);
+    if (d <= 1536) return f(v, std::integral_constant<int, 192>(), one);
+    if (d <= 2048) return f(v, t128, two);
+    if (d <= 4096) return f(v, t256, two);
+    return f(v, t512, two);
 }
 template <typename F> int by_types(int dtype, int rtype, F &&f)
 {
@@ -797,7 +833,9 @@ int la_block_norm_bwd(const void *y, const void *residual, const void *gate, con
                 }
                 return launch(bn_bwd_kernel<T, R, v, nt, nc, bias>, dim3((unsigned)blocks), bn_block<nt, true>, smem, (cudaStream_t)stream, a);
             };
-            return dpost_bias || dpre_bias ? run(std::true_type()) : run(std::false_type());
+            if constexpr (v == 8)
+                if (!dpost_bias && !dpre_bias) return run(std::false_type());
+            return run(std::true_type());
         });
     });
     if (rc != LA_OK || !a.sums) return rc;

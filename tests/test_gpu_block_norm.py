@@ -143,6 +143,14 @@ def test_only_one_gradient():
 
 
 @pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16-f32", "bf16"])
+@pytest.mark.parametrize("size", [(2, 1300, 500), (2, 1300, 520), (3, 1100, 768), (1, 1300, 1001), (1, 1000, 1504), (1, 700, 2003), (1, 400, 4001),
+                                  (1, 333, 5001)], ids=lambda s: "x".join(map(str, s)))
+def test_several_rows_a_group(size, types):
+    """Every split of a row over threads, each group with more than one row."""
+    check(*size, *types, True, "rms", "layer", seed=6)
+
+
+@pytest.mark.parametrize("types", TYPES, ids=["f32", "bf16-f32", "bf16"])
 def test_views_in_place_and_broadcast(types):
     """Views of wider rows, odd offsets, in place, and one gate for all rows (stride 0)."""
     B, L, d = 2, 70, 256
