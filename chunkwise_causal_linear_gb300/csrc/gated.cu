@@ -682,13 +682,13 @@ template <typename T, int V, int COLS> __global__ void __launch_bounds__(STEP_TH
     }
 }
 
+constexpr int SEG_LEAST = 16;
 int fwd_segments(int B, int H, int L, int d, int e, int sms)
 {
-    // twice as many blocks as SMs, of 32 rows at least; the segments' sums cost two thirds of a sweep,
-    // so that two segments would not pay. (A row takes a block about half a microsecond however few blocks there are:
-    // B5 H6 L777 with 128 rows at least 136 us, with 32 105.)
-    const double blocks = (double)B * H * tiles_of(d, e);
-    const int want = (int)std::min(1024.0, std::floor(2.0 * sms / blocks)), most = (L + 31) / 32;
+    // eight warps an SM, as many as the state's registers allow, of 32 rows at least; the segments' sums cost two thirds
+    // of a sweep, so that two segments would not pay. (A row takes a warp about half a microsecond however few there are.)
+    const double warps = (double)B * H * tiles_of(d, e) * warps_of(d, e);
+    const int want = (int)std::min(1024.0, std::floor(8.0 * sms / warps)), most = (L + SEG_LEAST - 1) / SEG_LEAST;
     const int n = std::min(want, most);
     return n < 3 ? 1 : n;
 }
