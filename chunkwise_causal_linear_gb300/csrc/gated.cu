@@ -75,10 +75,9 @@ __device__ __forceinline__ void stage(float *dst, int ld, const float *src, Row 
             copy16(dst + i * ld + c, src + row(i) + c);
         }
     } else {
-        for (int e = threadIdx.x; e < n * len; e += blockDim.x) {
-            const int i = e / len, c = e % len;
-            copy4(dst + i * ld + c, src + row(i) + c);
-        }
+        for (int c = threadIdx.x; c < len; c += blockDim.x)
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) copy4(dst + i * ld + c, src + row(i) + c);
     }
 }
 template <typename Row>
@@ -98,9 +97,15 @@ __device__ __forceinline__ void stage(float *dst, int ld, const __nv_bfloat16 *s
                                    __uint_as_float(w[2 * k + 1] << 16), __uint_as_float(w[2 * k + 1] & 0xFFFF0000u));
         }
     } else {
-        for (int e = threadIdx.x; e < n * len; e += blockDim.x) {
-            const int i = e / len, c = e % len;
-            dst[i * ld + c] = __bfloat162float(src[row(i) + c]);
+        // a channel of every row of the tile at once: the loads wait together, and no element costs a division
+        for (int c = threadIdx.x; c < len; c += blockDim.x) {
+            __nv_bfloat16 v[SWEEP_ROWS];
+#pragma unroll
+            for (int i = 0; i < SWEEP_ROWS; ++i)
+                if (i < n) v[i] = src[row(i) + c];
+#pragma unroll
+            for (int i = 0; i < SWEEP_ROWS; ++i)
+                if (i < n) dst[i * ld + c] = __bfloat162float(v[i]);
         }
     }
 }
