@@ -506,10 +506,12 @@ __global__ void __launch_bounds__(256) product_kernel(const ProductArgs a)
 }
 
 struct LogDecayArgs {
-    const float *r, *c, *y, *g;
+    const float *r, *c, *g;
+    float *y;  // [seg][heads]: <D, S> at the segments' ends; with `sums`, out: the segments' sums
     View vg;
     float *dg;
     const int *lengths;
+    int sums;
     int nr, nc, B, H, L, seg_rows, nseg, initial;
 };
 // A block a segment, 1024 rows at a time from its end, four neighbouring ones a thread; a row's parts are summed in
@@ -524,7 +526,9 @@ __global__ void __launch_bounds__(LD_THREADS) log_decay_kernel(const LogDecayArg
     const int seg = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / a.H, h = bh % a.H;
     const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L), te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
     const long long at = (long long)bh * a.L, step = (long long)BH * a.L;
-    for (int t = te + (int)threadIdx.x; t < t1; t += LD_THREADS) a.dg[at + t] = 0.f;
+    if (a.dg)
+        for (int t = te + (int)threadIdx.x; t < t1; t += LD_THREADS) a.dg[at + t] = 0.f;
+    double all = 0;
     double carry = a.y[(long long)seg * BH + bh];
     for (int e = te; e > t0; e -= LD_ROWS) {  // place k is row e - 1 - k
 #pragma unroll
@@ -561,36 +565,51 @@ __global__ void __launch_bounds__(LD_THREADS) log_decay_kernel(const LogDecayArg
         *(float4 *)(diff + 4 * threadIdx.x) =
             make_float4((float)(before + s[0]), (float)(before + s[1]), (float)(before + s[2]), (float)(before + s[3]));
         __syncthreads();
+        float four = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int k = threadIdx.x + LD_THREADS * u, t = e - 1 - k;
             // a decay of 0 has no gradient: every pair across it is 0; nor has one with nothing before it
             const bool none = t >= t0 && (a.g[row_of(a.vg, b, h, t)] < GATED_CUT || (t == 0 && !a.initial));
-            if (t >= t0) a.dg[at + t] = none ? 0.f : diff[k];
+            const float x = t < t0 || none ? 0.f : diff[k];
+            if (a.dg && t >= t0) a.dg[at + t] = x;
+            four += x;
         }
+        all += (double)four;
         __syncthreads();
+    }
+    if (!a.sums) return;
+    // the segment's sum for the head's; fours in fp32 and the whole rounded once, as its terms are
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    __syncthreads();
+    if (lane == 0) sums[warp] = all;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < LD_THREADS / 32; ++i) all += sums[i];
+        a.y[(long long)seg * BH + bh] = (float)all;
     }
 }
 
 struct HeadSumArgs {
-    const float *dg;
+    const float *sums;  // [seg][B][H]
     float *out;
-    int B, H, L;
+    int B, H, nseg;
 };
-// Over the rows and sequences of one head, in a fixed order.
-__global__ void __launch_bounds__(1024) head_sum_kernel(const HeadSumArgs a)
+// Over the segments and sequences of one head, in a fixed order.
+__global__ void __launch_bounds__(256) head_sum_kernel(const HeadSumArgs a)
 {
-    __shared__ double part[32];
+    __shared__ double part[8];
     const int h = blockIdx.x;
+    const long long n = (long long)a.nseg * a.B;
     double s = 0;
-    for (int b = 0; b < a.B; ++b)
-        for (int t = threadIdx.x; t < a.L; t += 1024) s += (double)a.dg[((long long)b * a.H + h) * a.L + t];
+    for (long long i = threadIdx.x; i < n; i += 256) s += (double)a.sums[i * a.H + h];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < 32; ++i) s += part[i];
+        for (int i = 1; i < 8; ++i) s += part[i];
         a.out[h] = (float)s;
     }
 }
@@ -750,12 +769,11 @@ int gated_products(const GatedArgs &p, const float *D, const float *S, float *y,
     return launch(product_kernel, dim3((unsigned)(nseg * p.B * p.H)), 256, 0, p.stream, ProductArgs{D, S, y, n});
 }
 
-int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, int nc, const float *y, int seg_rows,
-                    int nseg, float *dg)
+int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, int nc, float *y, int seg_rows, int nseg)
 {
-    const LogDecayArgs a{r, c, y, p.g, p.vg, dg, p.lengths, nr, nc, p.B, p.H, p.L, seg_rows, nseg, p.state0 != nullptr};
+    const LogDecayArgs a{r, c, p.g, y, p.vg, p.dg, p.lengths, p.dg_head != nullptr, nr, nc, p.B, p.H, p.L, seg_rows, nseg, p.state0 != nullptr};
     int rc = launch(log_decay_kernel, dim3((unsigned)(p.B * p.H * nseg)), LD_THREADS, 0, p.stream, a);
-    if (rc == LA_OK && p.dg_head) rc = launch(head_sum_kernel, dim3((unsigned)p.H), 1024, 0, p.stream, HeadSumArgs{dg, p.dg_head, p.B, p.H, p.L});
+    if (rc == LA_OK && p.dg_head) rc = launch(head_sum_kernel, dim3((unsigned)p.H), 256, 0, p.stream, HeadSumArgs{y, p.dg_head, p.B, p.H, nseg});
     return rc;
 }
 
@@ -801,7 +819,7 @@ int gated_simt_fwd(const GatedArgs &p)
 namespace {
 // Floats of the backward pass's workspace, part by part.
 struct BwdSpace {
-    size_t S, A, D, y, r, c, dk, dv, dg, all;
+    size_t S, A, D, y, r, c, dk, dv, all;
     int nr, nc;
     BwdSpace(int B, int H, int Hk, int L, int d, int e, int nseg)
     {
@@ -818,7 +836,6 @@ struct BwdSpace {
         c = take(nc * rows);
         dk = take(H > Hk ? rows * d : 0);
         dv = take(H > Hk ? rows * e : 0);
-        dg = take(rows);
         all = at;
     }
 };
@@ -910,7 +927,7 @@ int gated_simt_bwd(const GatedArgs &p)
     }
     if (dg) {
         if ((rc = gated_products(p, ws + w.D, ws + w.S + heads * n, ws + w.y, nseg, n)) != LA_OK) return rc;
-        if ((rc = gated_log_decay(p, ws + w.r, w.nr, ws + w.c, w.nc, ws + w.y, rows, nseg, p.dg ? p.dg : ws + w.dg)) != LA_OK)
+        if ((rc = gated_log_decay(p, ws + w.r, w.nr, ws + w.c, w.nc, ws + w.y, rows, nseg)) != LA_OK)
             return rc;
     }
     return LA_OK;

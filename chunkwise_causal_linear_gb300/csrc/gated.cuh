@@ -55,8 +55,8 @@ int gated_scan(const GatedArgs &p, float *T, const float *A, int nseg, int n, co
 int gated_share(const GatedArgs &p, const float *x, void *out, const View &vo, int n);
 // dg out of the rows' parts: r and c [parts][heads][L], the anchors' products y [nseg][heads], rows of
 // a segment; then its sums over the rows of each head, where they are wanted.
-int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, int nc, const float *y, int seg_rows,
-                    int nseg, float *dg);
+int gated_log_decay(const GatedArgs &p, const float *r, int nr, const float *c, int nc, float *y, int seg_rows,
+                    int nseg);
 int gated_products(const GatedArgs &p, const float *D, const float *S, float *y, int nseg, int n);
 
 size_t gated_simt_fwd_ws(int B, int H, int L, int d, int e, int sms);

@@ -937,7 +937,7 @@ int tc_segments(int BH, int L, int sms)
 int chunk_rows(int L, int nseg) { return ((L + nseg - 1) / nseg + GT_C - 1) / GT_C * GT_C; }
 
 struct TcBwdSpace {
-    size_t T, A, U, S, D, y, r, c, dk, dv, dg, all;
+    size_t T, A, U, S, D, y, r, c, dk, dv, all;
     int rows, nseg, anchor, n_anchors;
     TcBwdSpace(int B, int H, int Hk, int L, int d, int e, int sms)
     {
@@ -961,7 +961,6 @@ struct TcBwdSpace {
         c = take(8 * heads * L);
         dk = take(H > Hk ? heads * L * d : 0);
         dv = take(H > Hk ? heads * L * e : 0);
-        dg = take(heads * L);
         all = at;
     }
 };
@@ -1100,7 +1099,7 @@ int gated_tc_bwd(const GatedArgs &p)
     }
     if (dg) {
         if ((rc = gated_products(p, ws + w.D, ws + w.S + heads * n, ws + w.y, w.n_anchors, n)) != LA_OK) return rc;
-        if ((rc = gated_log_decay(p, ws + w.r, 8, ws + w.c, 8, ws + w.y, w.anchor, w.n_anchors, p.dg ? p.dg : ws + w.dg)) != LA_OK)
+        if ((rc = gated_log_decay(p, ws + w.r, 8, ws + w.c, 8, ws + w.y, w.anchor, w.n_anchors)) != LA_OK)
             return rc;
     }
     return LA_OK;
