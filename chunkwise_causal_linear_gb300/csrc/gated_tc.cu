@@ -93,6 +93,7 @@ struct Weights {          // of one chunk
 };
 
 // A log decay above -104 in units of 2^-44 doublings, to a unit: the product with log2 e in two parts.
+constexpr int UNIT_BITS = 44;
 constexpr float UNIT = 5.684341886080801e-14f, UNITS = 17592186044416.f;
 __device__ __forceinline__ long long doublings(float g)
 {
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     using Lay = GtLayout<DX, DZ, DOT>;
     constexpr int C = GT_C, NST = Lay::STAGES, NS = Lay::NS;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ long long sums[2];  // of the log decays, by the warps that form the weights
+    __shared__ long long sums[2], doubled[2];  // of the log decays, by the warps that form the weights: units, doublings
     __shared__ bool cuts_of[2];
     uint8_t *const sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Weights *const weights = (Weights *)(sm + Lay::OFF_W);
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             return c < nch && t < te ? gp[(long long)t * a.vg.l] : 0.f;
         };
         const int c0 = warp - 2;
-        long long over = 0;  // the sum over this warp's chunks
+        long long over = 0, whole_over = 0;  // the sum over this warp's chunks: units below a doubling, doublings
         bool cut = skip > 0;
         float g0 = gate(c0, 2 * lane), g1 = gate(c0, 2 * lane + 1);
         for (int c = c0; c < nch; c += 2) {
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
             // instead. (Sums in 64-bit floating point took 4,700 cycles a chunk, as long as all the rest.)
             const bool z0 = g0 < GATED_CUT, z1 = g1 < GATED_CUT;
             const bool odd = __any_sync(0xffffffffu, !(g0 < 88.f) || !(g1 < 88.f));  // NaN, or a decay past fp32
-            const long long d0 = z0 ? 0 : doublings(g0), d1 = z1 ? 0 : doublings(g1);
+            const long long d0 = z0 || odd ? 0 : doublings(g0), d1 = z1 || odd ? 0 : doublings(g1);
             long long run = d0 + d1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -560,7 +561,9 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
                 w.kw[2 * lane + i] = a.yscale * (rev ? start : end) + bad;
                 w.rw[2 * lane + i] = a.oscale * (rev ? end : start) + bad;
             }
-            over += whole;
+            over += whole;  // 64 bits of units hold 2^19 doublings, which a segment's rows may pass
+            whole_over += over >> UNIT_BITS;
+            over &= (1ll << UNIT_BITS) - 1;
             cut |= cuts > 0;
             if (lane == 0) {
                 const float g2 = (float)whole * UNIT;
@@ -575,6 +578,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
         }
         if (lane == 0) {
             sums[c0] = over;
+            doubled[c0] = whole_over;
             cuts_of[c0] = cut;
         }
     } else {
@@ -857,8 +861,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1) gated_tc_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
-    if (tid == 0 && a.decay)
-        a.decay[(long long)seg * BH + bh] = cuts_of[0] || cuts_of[1] ? 0.f : exp2f((float)(sums[0] + sums[1]) * UNIT);
+    if (tid == 0 && a.decay) {
+        // past 2^17 doublings either way it is 0 or infinite all the same
+        const long long over = min(max(doubled[0] + doubled[1], -(1ll << 17)), 1ll << 17);
+        const long long units = (over << UNIT_BITS) + sums[0] + sums[1];
+        a.decay[(long long)seg * BH + bh] = cuts_of[0] || cuts_of[1] ? 0.f : exp2f((float)units * UNIT);
+    }
 }
 
 // ---- host side -----------------------------------------------------------------------------------
