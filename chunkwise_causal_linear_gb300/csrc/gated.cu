@@ -516,12 +516,15 @@ struct LogDecayArgs {
 };
 // A block a segment, 1024 rows at a time from its end, four neighbouring ones a thread; a row's parts are summed in
 // fp32, the rows in 64 bits, few operations of which a row leaves (the SM has two such lanes: a scan of every
-// row took 45 us where this takes 13, B2 H12 L16384).
+// row took 45 us where this takes 13, B2 H12 L16384). The sums start again at every row whose decay is 0: its gradient is
+// 0, every pair across it is, and what is behind it, infinities and NaN too, is not the rows' before it.
 constexpr int LD_THREADS = 256, LD_ROWS = 4 * LD_THREADS;
 __global__ void __launch_bounds__(LD_THREADS) log_decay_kernel(const LogDecayArgs a)
 {
     __shared__ __align__(16) float diff[LD_ROWS];
+    __shared__ __align__(4) uint8_t cut[LD_ROWS];
     __shared__ double sums[LD_THREADS / 32];
+    __shared__ bool starts[LD_THREADS / 32];  // a reset among the warp's rows
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, BH = a.B * a.H;
     const int seg = blockIdx.x / BH, bh = blockIdx.x % BH, b = bh / a.H, h = bh % a.H;
     const int t0 = seg * a.seg_rows, t1 = min(t0 + a.seg_rows, a.L), te = max(t0, min(t1, gated_rows(a.lengths, b, a.L)));
@@ -535,43 +538,58 @@ __global__ void __launch_bounds__(LD_THREADS) log_decay_kernel(const LogDecayArg
         for (int u = 0; u < 4; ++u) {
             const int k = threadIdx.x + LD_THREADS * u, t = e - 1 - k;
             float r = 0.f, c = 0.f;
+            bool none = false;
             if (t >= t0) {
+                none = a.g[row_of(a.vg, b, h, t)] < GATED_CUT;
 #pragma unroll 8
                 for (int i = 0; i < a.nr; ++i) r += a.r[i * step + at + t];
 #pragma unroll 8
                 for (int i = 0; i < a.nc; ++i) c += a.c[i * step + at + t];
             }
-            diff[k] = r - c;
+            diff[k] = none ? 0.f : r - c;
+            cut[k] = none;
         }
         __syncthreads();
         const float4 f = *(const float4 *)(diff + 4 * threadIdx.x);
+        const uint32_t at_cut = *(const uint32_t *)(cut + 4 * threadIdx.x);  // a byte a row
         double s[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int u = 1; u < 4; ++u) s[u] += s[u - 1];
+        for (int u = 1; u < 4; ++u)
+            if (!(at_cut >> (8 * u) & 1)) s[u] += s[u - 1];
+        // over the lanes behind the last one with a reset
+        const uint32_t m = __ballot_sync(0xffffffffu, at_cut != 0), upto = m & (0xffffffffu >> (31 - lane));
+        const int from = upto ? 31 - __clz(upto) : 0;
         double run = s[3];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double u = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += u;
+            if (lane - o >= from) run += u;
         }
-        if (lane == 31) sums[warp] = run;
+        if (lane == 31) {
+            sums[warp] = run;
+            starts[warp] = m != 0;
+        }
         __syncthreads();
         double before = carry;
         for (int i = 0; i < LD_THREADS / 32; ++i) {
             if (i == warp) before = carry;
-            carry += sums[i];
+            carry = starts[i] ? sums[i] : carry + sums[i];
         }
-        before += run - s[3];
-        *(float4 *)(diff + 4 * threadIdx.x) =
-            make_float4((float)(before + s[0]), (float)(before + s[1]), (float)(before + s[2]), (float)(before + s[3]));
+        const double left = __shfl_up_sync(0xffffffffu, run, 1);  // of the lanes before this one
+        const bool fresh = m & ((1u << lane) - 1u);
+        before = lane == 0 ? before : fresh ? left : before + left;
+        float4 x;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)  // with no reset up to this row, what is before the thread's too
+            (&x.x)[u] = (float)(at_cut & (0xffffffffu >> (24 - 8 * u)) ? s[u] : before + s[u]);
+        *(float4 *)(diff + 4 * threadIdx.x) = x;
         __syncthreads();
         float four = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int k = threadIdx.x + LD_THREADS * u, t = e - 1 - k;
-            // a decay of 0 has no gradient: every pair across it is 0; nor has one with nothing before it
-            const bool none = t >= t0 && (a.g[row_of(a.vg, b, h, t)] < GATED_CUT || (t == 0 && !a.initial));
-            const float x = t < t0 || none ? 0.f : diff[k];
+            // a first row with nothing before it has no gradient either
+            const float x = t < t0 || cut[k] || (t == 0 && !a.initial) ? 0.f : diff[k];
             if (a.dg && t >= t0) a.dg[at + t] = x;
             four += x;
         }
