@@ -161,12 +161,22 @@ template <int NT, bool WHOLE> struct Sums {  // WHOLE: the row's threads are the
     }
 };
 
-// 1 / (1 + e^-z): for fp32 by the exact division and exponential, for bf16, whose outputs are rounded by
-// up to 2^-8, to (5 + |z|) 2^-23.
-template <typename T> __device__ __forceinline__ float sigmoid(float z)
+// s = 1 / (1 + e^-z) and 1 - s, both from e^-|z|: the smaller one is e / (1 + e), so neither is a difference, and a slope of
+// s (1 - s) is as exact far out as near 0. For fp32 by the exact division and exponential; for bf16, whose outputs are
+// rounded by up to 2^-8, to (5 + |z|) 2^-23, and 0 where e^-|z| is below the normal range (|z| > 87.3).
+template <typename T> __device__ __forceinline__ void sigmoid(float z, float &s, float &rest)
 {
-    if constexpr (std::is_same<T, float>::value) return 1.f / (1.f + expf(-z));
-    else return rcp(1.f + ex2(-1.44269504f * z));
+    float e, large;
+    if constexpr (std::is_same<T, float>::value) {
+        e = expf(-fabsf(z));
+        large = 1.f / (1.f + e);
+    } else {
+        e = ex2(-1.44269504f * fabsf(z));
+        large = rcp(1.f + e);
+    }
+    const float small = e * large;
+    s = z < 0.f ? small : large;
+    rest = z < 0.f ? large : small;
 }
 
 // Channels of chunks that are not there, back to 0.
@@ -300,8 +310,8 @@ template <int VEC, int PF> __device__ __forceinline__ void row_arrived()
 // V channels of a chunk at f as pairs
 template <int W, int M> __device__ __forceinline__ float *flat(Ch<W> (&x)[M], int i) { return &x[i / W].v[i % W]; }
 
-// act(z), and s = sigmoid(z) where the activation has it.
-template <typename T, int W, int M> __device__ __forceinline__ void activate(const Ch<W> (&z)[M], Ch<W> (&s)[M], Ch<W> (&act)[M], const BnArgs &a)
+// act(z), and its slope where it is not 1.
+template <typename T, int W, int M> __device__ __forceinline__ void activate(const Ch<W> (&z)[M], Ch<W> (&slope)[M], Ch<W> (&act)[M], const BnArgs &a)
 {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
@@ -310,9 +320,11 @@ template <typename T, int W, int M> __device__ __forceinline__ void activate(con
         } else if (a.act == LA_ACT_NONE) {
             act[i] = z[i];
         } else {
+            Ch<W> s, rest;
 #pragma unroll
-            for (int u = 0; u < W; ++u) s[i].v[u] = sigmoid<T>(z[i].v[u]);
-            act[i] = a.act == LA_ACT_SILU ? mul(z[i], s[i]) : s[i];
+            for (int u = 0; u < W; ++u) sigmoid<T>(z[i].v[u], s.v[u], rest.v[u]);
+            act[i] = a.act == LA_ACT_SILU ? mul(z[i], s) : s;
+            slope[i] = mul(s, a.act == LA_ACT_SILU ? fma(z[i], rest, all<W>(1.f)) : rest);
         }
     }
 }
@@ -347,7 +359,7 @@ __global__ void __launch_bounds__(bn_block<NT, false>, 1) bn_fwd_kernel(const Bn
     for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
         Ch<W> u[M], h[M], act[M];
         {
-            Ch<W> z[M], sg[M];
+            Ch<W> z[M], slope[M];
 #pragma unroll
             for (int i = 0; i < M; ++i) u[i] = h[i] = z[i] = all<W>(0.f);
             row_arrived<VEC, PF>();
@@ -359,7 +371,7 @@ __global__ void __launch_bounds__(bn_block<NT, false>, 1) bn_fwd_kernel(const Bn
                     if (a.gate) rg.get(flat(z, c * VEC), slot, c);
                 }
             fetch(row + PF * step, slot);
-            activate<T>(z, sg, act, a);
+            activate<T>(z, slope, act, a);
         }
         const Ch<W> k1 = all<W>(a.bs * (a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum))), bs = all<W>(a.bs),
                     rs = all<W>(a.rs);
@@ -448,9 +460,9 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_held<NT, NC>) bn_bwd_ke
     for (int i = 0; i < PF; ++i) fetch(first + i * step, i);
     int slot = 0;
     for (long long row = first; row < a.rows; row += step, slot = slot + 1 == PF ? 0 : slot + 1) {
-        // what is needed late (dn, dh, and the gate once more) stays in the ring until then: registers held over
+        // what is needed late (dn and dh) stays in the ring until then: registers held over
         // the sums are what the kernel has least of
-        Ch<W> u[M], h[M], sg[M], act[M], dh[M];
+        Ch<W> u[M], h[M], slope[M], act[M], dh[M];
         row_arrived<VEC, PF>();
         {
             Ch<W> z[M];
@@ -463,7 +475,7 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_held<NT, NC>) bn_bwd_ke
                     rr.get(flat(h, c * VEC), slot, c);
                     if (a.gate) rg.get(flat(z, c * VEC), slot, c);
                 }
-            activate<T>(z, sg, act, a);
+            activate<T>(z, slope, act, a);
         }
         const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum);
         const Ch<W> k1w = all<W>(k1), bs = all<W>(a.bs), rs = all<W>(a.rs);
@@ -536,17 +548,11 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_held<NT, NC>) bn_bwd_ke
                 put<VEC>(dr + at[c], o[0].v);
                 post(c, w, x);
                 if (a.gate) {
-                    Ch<W> z[VEC / W];
-                    if (a.act == LA_ACT_SILU) rg.get(z[0].v, slot, c);
 #pragma unroll
                     for (int i = 0; i < VEC / W; ++i) {
                         const int m = c * VEC / W + i;
                         o[i] = mul(mul(bs, dh[m]), x[i]);
-                        // slope: s (1 + z (1 - s)), s (1 - s), or 1
-                        if (a.act != LA_ACT_NONE) {
-                            const Ch<W> rest = less(all<W>(1.f), sg[m]);
-                            o[i] = mul(o[i], mul(sg[m], a.act == LA_ACT_SILU ? fma(z[i], rest, all<W>(1.f)) : rest));
-                        }
+                        if (a.act != LA_ACT_NONE) o[i] = mul(o[i], slope[m]);
                     }
                     put<VEC>(dg + at[c], o[0].v);
                 }
