@@ -996,7 +996,7 @@ int la_gated_fwd(const void *q, const void *k, const void *v, const float *log_d
         return LA_ERR_ARG;
     const size_t es = dtype_size(dtype);
     if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(out, es) || !aligned(log_decay, 4) ||
-        !aligned(state0, 4) || !aligned(state, 4) || !aligned(workspace, 16))
+        !aligned(state0, 4) || !aligned(state, 4) || !aligned(slots, 4) || !aligned(lengths, 4) || !aligned(workspace, 16))
         return LA_ERR_ARG;
     p.B = B; p.H = H; p.Hk = Hk; p.L = L; p.d = dk; p.e = dv; p.n_slots = n_slots;
     p.scale = scale;
@@ -1049,7 +1049,7 @@ int la_gated_bwd(const void *q, const void *k, const void *v, const float *log_d
     const size_t es = dtype_size(dtype);
     if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(dout, es) || !aligned(grad_q, es) ||
         !aligned(grad_k, es) || !aligned(grad_v, es) || !aligned(log_decay, 4) || !aligned(state0, 4) || !aligned(dstate, 4) ||
-        !aligned(dlog_decay, 4) || !aligned(dlog_decay_head, 4) || !aligned(dstate0, 4) || !aligned(workspace, 16))
+        !aligned(dlog_decay, 4) || !aligned(dlog_decay_head, 4) || !aligned(dstate0, 4) || !aligned(lengths, 4) || !aligned(workspace, 16))
         return LA_ERR_ARG;
     p.B = B; p.H = H; p.Hk = Hk; p.L = L; p.d = dk; p.e = dv;
     p.scale = scale;
@@ -1093,7 +1093,8 @@ int la_gated_step(const void *q, const void *k, const void *v, const float *log_
         !input_view_ok(a.vg, B, H, 1) || !isfinite(scale))
         return LA_ERR_ARG;
     const size_t es = dtype_size(dtype);
-    if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(out, es) || !aligned(log_decay, 4) || !aligned(state, 4))
+    if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(out, es) || !aligned(log_decay, 4) || !aligned(state, 4) ||
+        !aligned(slots, 4))
         return LA_ERR_ARG;
     a.B = B; a.H = H; a.group = H / Hk; a.d = dk; a.e = dv; a.n_slots = n_slots;
     a.scale = scale;
