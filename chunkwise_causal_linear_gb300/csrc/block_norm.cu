@@ -163,9 +163,14 @@ template <int NT, bool WHOLE> struct Sums {  // WHOLE: the row's threads are the
 
 // s = 1 / (1 + e^-z) and 1 - s, both from e^-|z|: the smaller one is e / (1 + e), so neither is a difference, and a slope of
 // s (1 - s) is as exact far out as near 0. For fp32 by the exact division and exponential; for bf16, whose outputs are
-// rounded by up to 2^-8, to (5 + |z|) 2^-23, and 0 where e^-|z| is below the normal range (|z| > 87.3).
-template <typename T> __device__ __forceinline__ void sigmoid(float z, float &s, float &rest)
+// rounded by up to 2^-8, to (5 + |z|) 2^-23, and 0 where e^-|z| is below the normal range (|z| > 87.3). Without a SLOPE to
+// form bf16 needs no e^-|z|: s is as exact from e^-z, and takes less (B8 L8192 d2048 forward 228 us, 231 otherwise).
+template <typename T, bool SLOPE> __device__ __forceinline__ void sigmoid(float z, float &s, float &rest)
 {
+    if constexpr (!SLOPE && !std::is_same<T, float>::value) {
+        s = rcp(1.f + ex2(-1.44269504f * z));
+        return;
+    }
     float e, large;
     if constexpr (std::is_same<T, float>::value) {
         e = expf(-fabsf(z));
@@ -311,7 +316,8 @@ template <int VEC, int PF> __device__ __forceinline__ void row_arrived()
 template <int W, int M> __device__ __forceinline__ float *flat(Ch<W> (&x)[M], int i) { return &x[i / W].v[i % W]; }
 
 // act(z), and its slope where it is not 1.
-template <typename T, int W, int M> __device__ __forceinline__ void activate(const Ch<W> (&z)[M], Ch<W> (&slope)[M], Ch<W> (&act)[M], const BnArgs &a)
+template <typename T, bool SLOPE, int W, int M>
+__device__ __forceinline__ void activate(const Ch<W> (&z)[M], Ch<W> (&slope)[M], Ch<W> (&act)[M], const BnArgs &a)
 {
 #pragma unroll
     for (int i = 0; i < M; ++i) {
@@ -322,9 +328,9 @@ template <typename T, int W, int M> __device__ __forceinline__ void activate(con
         } else {
             Ch<W> s, rest;
 #pragma unroll
-            for (int u = 0; u < W; ++u) sigmoid<T>(z[i].v[u], s.v[u], rest.v[u]);
+            for (int u = 0; u < W; ++u) sigmoid<T, SLOPE>(z[i].v[u], s.v[u], rest.v[u]);
             act[i] = a.act == LA_ACT_SILU ? mul(z[i], s) : s;
-            slope[i] = mul(s, a.act == LA_ACT_SILU ? fma(z[i], rest, all<W>(1.f)) : rest);
+            if constexpr (SLOPE) slope[i] = mul(s, a.act == LA_ACT_SILU ? fma(z[i], rest, all<W>(1.f)) : rest);
         }
     }
 }
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(bn_block<NT, false>, 1) bn_fwd_kernel(const Bn
                     if (a.gate) rg.get(flat(z, c * VEC), slot, c);
                 }
             fetch(row + PF * step, slot);
-            activate<T>(z, slope, act, a);
+            activate<T, false>(z, slope, act, a);
         }
         const Ch<W> k1 = all<W>(a.bs * (a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum))), bs = all<W>(a.bs),
                     rs = all<W>(a.rs);
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(bn_block<NT, true>, bn_held<NT, NC>) bn_bwd_ke
                     rr.get(flat(h, c * VEC), slot, c);
                     if (a.gate) rg.get(flat(z, c * VEC), slot, c);
                 }
-            activate<T>(z, slope, act, a);
+            activate<T, true>(z, slope, act, a);
         }
         const float k1 = a.post == LA_NORM_NONE ? 1.f : statistics<VEC>(u, in, a.post, a, sum);
         const Ch<W> k1w = all<W>(k1), bs = all<W>(a.bs), rs = all<W>(a.rs);
