@@ -15,7 +15,7 @@
 // recompute the statistics from y and r (32-bit sums; h before its rounding) instead of reading them, and keep
 // the sums for the weights' gradients in the threads' registers; the groups' sums are joined by a second kernel in a
 // fixed order. Forwards the copies bind (B8 L8192 d2048 229 us, 86% of the measured copy rate), the gradients are bound
-// by up to five sums over the row's threads, one after the other, and their instructions (518 us, 61%; of the schedulers'
+// by up to five sums over the row's threads, one after the other, and their instructions (480 us, 66%; of the schedulers'
 // slots 45% are used).
 #include <math.h>
 
@@ -226,8 +226,9 @@ struct RowAt {
 
 template <int NT, bool BWD> constexpr int bn_block = BWD ? (128 % NT == 0 ? 128 : NT) : 256 % NT == 0 ? 256 : NT < 192 ? 192 : NT;
 // Threads of the gradients' kernel that an SM is to hold, and with that the registers of each (128 or 168): 16 channels
-// of a row of up to 2048 spill at 128 (d2048 518 us, 562 at 128), longer rows are waited for too long with one block
-// (d4096 431 us with two of 256, 477 with one).
+// of a row of up to 2048 spill at 128 with the biases' sums (B8 L8192 d2048 580 us, 711 at 128; fp32 d2048 without them 585 and
+// 627; bf16 without them fit: 480 and 450), longer rows are waited for too long with one block (B4 L4096 d4096 240 us with
+// two of 256, 335 with one).
 template <int NT, int NC> constexpr int bn_threads = NC == 1 || (NC == 2 && NT >= 256) ? 512 : 384;
 template <int NT, int NC>
 constexpr int bn_held = bn_threads<NT, NC> < bn_block<NT, true> ? 1 : bn_threads<NT, NC> / bn_block<NT, true>;
@@ -685,9 +686,9 @@ template <typename F> int by_shape(int d, bool wide, F &&f)
         if (d <= 4096) return f(one, t512, v);
         return f(one, t512, std::integral_constant<int, 16>());
     }
-    // 8 channels a thread for rows up to 1536: their registers allow more rows at once (B2 L16384 d768 78 us and, with
-    // all sums, 167; 86 and 267 with 16). 16 beyond: half the sums' and the rows' overhead (B8 L8192 d2048
-    // 229 and 518 us, the gradients 580 with 8).
+    // 8 channels a thread for rows up to 1536: their registers allow more rows at once (B2 L16384 d768 76 us and the
+    // gradients 147, with all sums 169; 83, 158 and 222 with 16). 16 beyond: half the sums' and the rows' overhead (B8 L8192
+    // d2048 228 and 480 us; 303 and 565 with 8).
     if (d <= 256) return f(v, t32, one);
     if (d <= 512) return f(v, t64, one);
     if (d <= 768) return f(v, std::integral_constant<int, 96>(), one);

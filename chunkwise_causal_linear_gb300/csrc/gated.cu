@@ -10,13 +10,15 @@
 //
 // dg without a state per row: <D_t, a_t S_{t-1}> - <D_{t+1}, a_{t+1} S_t> = R_t - C_t with R_t = q_t . dq_t
 // and C_t = k_t . dk_t, each without the row's own pair, which both hold.  It is summed from the end
-// of a segment, where <D, S> is formed from the states, so that roundings gather over one segment only.
+// of a segment, where <D, S> is formed from the states, so that roundings gather over one segment only, and again
+// from every row whose decay is 0, where it is 0.
 //
 // sweep_kernel runs the recurrence row by row in fp32: a thread holds 16 x 8 elements of the state, in
 // pairs of rows for the packed instructions, and a row costs three of them per pair: decay, product
-// with x, new pair (1.5 dk dv instructions of fp32 a row and head).  Short sequences are bound by the latency of a
-// row's steps, about 0.5 us, long ones by the fp32 pipes; rows of the operands reach shared memory by cp.async one
-// tile ahead.  Few heads are cut into segments whose sums are formed first.
+// with x, new pair (1.5 dk dv instructions of fp32 a row and head).  Bound by the latency of a row's steps, 0.5 to 0.63 us,
+// short sequences and long ones: with one warp a scheduler, as B8 H16 d128 has, L1024 takes 642 us, of which the fp32
+// pipes are busy 30%.  Rows of the operands reach shared memory by cp.async one tile ahead.  Few heads are cut into
+// segments whose sums are formed first.
 #include <math.h>
 
 #include <algorithm>
@@ -649,7 +651,7 @@ struct StepArgs {
 
 // Bound by the state, read and written once.  A block takes COLS columns of a head, and V columns of eight of a
 // thread's rows are on their way at once.  With few heads 32 columns, so that they reach every SM (B8 H16 d128
-// 6.3 us, 8.4 with 128); with many 128, rows of 512 bytes (B64 H32 d128, 268 MB: 51.5 us, 77% of measured copy
+// 6.3 us, 8.4 with 128); with many 128, rows of 512 bytes (B64 H32 d128, 268 MB: 52.9 us, 75% of measured copy
 // bandwidth, 60 with 32).
 template <typename T, int V, int COLS> __global__ void __launch_bounds__(STEP_THREADS, 6) step_kernel(const StepArgs a)
 {
@@ -727,7 +729,7 @@ template <typename T, int V, int COLS> __global__ void __launch_bounds__(STEP_TH
 constexpr int SEG_LEAST = 16;
 int fwd_segments(int B, int H, int L, int d, int e, int sms)
 {
-    // eight warps an SM, as many as the state's registers allow, of 32 rows at least; the segments' sums cost two thirds
+    // eight warps an SM, as many as the state's registers allow, of 16 rows at least; the segments' sums cost two thirds
     // of a sweep, so that two segments would not pay. (A row takes a warp about half a microsecond however few there are.)
     const double warps = (double)B * H * tiles_of(d, e) * warps_of(d, e);
     const int want = (int)std::min(1024.0, std::floor(8.0 * sms / warps)), most = (L + SEG_LEAST - 1) / SEG_LEAST;

@@ -36,7 +36,7 @@
 // score blocks in fp32 (INNER). Every 1024 rows the sweeps store S and D for the anchors.
 //
 // Bound: at 128 channels a chunk reads and writes 64 KB, 2,500 cycles of an SM's share of the memory; it takes 4,100
-// (B8 H16 L8192 259 us, 62% of the measured copy rate): the workers' instructions and the
+// (B8 H16 L8192 262 us, 61% of the measured copy rate): the workers' instructions and the
 // round of products and waits that one chunk's state makes. With DOT 6,000: three parts of the state are copied and
 // multiplied.
 #include <algorithm>
@@ -946,9 +946,9 @@ bool tc_view(const void *p, const View &v, int B, int n, int L)
     return rows_aligned(p, v, B, n, L, 2, 16) && ok(v.b, B) && ok(v.h, n) && ok(v.l, L);
 }
 
-// Segments of a head's rows, one block each: where the heads alone leave half of the SMs idle, as many as fill
-// them, of 256 rows at least. The segments' sums are a pass over y and z, half of the sweep's bytes,
-// which a split into two would not win back.
+// Segments of a head's rows, one block each: where the heads alone leave half of the SMs idle or more, as many as
+// run at once (two from a third to a half of the SMs), of 256 rows at least. The segments' sums are a pass over y and z,
+// half of the sweep's bytes. More heads keep one each: further segments would wait for a second round of blocks.
 int tc_segments(int BH, int L, int sms)
 {
     const int want = std::min(sms / BH, (L + 255) / 256);

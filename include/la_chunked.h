@@ -637,8 +637,8 @@ enum la_norm_kind {
  *   scales, eps   finite, eps > 0, else LA_ERR_ARG
  *   d             at most 8192, else LA_ERR_UNSUPPORTED
  * Statistics are fp32 over values held in fp32, n's over h before it is rounded; each output is rounded
- * once.  h may be residual, and n may be y, with the same strides; otherwise outputs must not overlap
- * inputs.
+ * once.  The sigmoid of a bf16 gate z is taken to (5 + |z|) 2^-23 of itself, and as 0 below -87.3.  h may be
+ * residual, and n may be y, with the same strides; otherwise outputs must not overlap inputs.
  */
 int la_block_norm_fwd(const void *y, const void *residual, const void *gate,
                       const float *post_weight, const float *post_bias, const float *pre_weight,
@@ -654,7 +654,7 @@ int la_block_norm_fwd(const void *y, const void *residual, const void *gate,
  * for zero) and dn (as n; NULL where n was not used): dresidual (as residual), dy (as y), dgate (as gate,
  * NULL if and only if gate is; a broadcast gate's is the whole [B, L, d]), and device fp32 [d] or NULL each
  * dpost_weight, dpost_bias, dpre_weight, dpre_bias (the last two with dn only).  Statistics and h are formed
- * again from y and r, so the forward's h may be gone.  The weights' sums are taken in a fixed order through the
+ * again from y and r, so the forward's h may be gone.  The weights' sums are fp32, in a fixed order, through the
  * workspace of la_block_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned (not needed without them).
  * dresidual may be dh, and dy may be dn, with the same strides; otherwise outputs must not overlap inputs.
  */
@@ -702,15 +702,20 @@ size_t la_block_norm_bwd_workspace_bytes(int B, int L, int d);
  *   scale         finite, else LA_ERR_ARG
  *   path          enum la_path.  LA_PATH_SIMT takes every case, in fp32 row by row.  LA_PATH_TC takes bf16 with
  *                 dk and dv of 64 or 128 each, rows of q, k, v and out on 16-byte boundaries and no stride of
- *                 0 (LA_ERR_UNSUPPORTED otherwise); LA_PATH_AUTO takes it there, for any length.
+ *                 0 (LA_ERR_UNSUPPORTED otherwise); LA_PATH_AUTO takes it there, for any length.  All else (fp32,
+ *                 other widths, k expanded over heads) goes row by row, 10 to 20 times as long.
  *   workspace     device memory of la_gated_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0)
  * States, decays and sums are fp32; out is rounded once.  LA_PATH_TC rounds two operands of its products to
  * bf16 (each off by 2^-8 of itself at most): a row's weighted scores, and the state where only out reads it; the
- * state itself is summed to fp32.  A log decay below -104, whose decay fp32 does not hold, counts as -inf.
- * q, k, v are meant to be finite: an infinity or NaN in a row may reach every row of its chunk of 64 and
- * those behind; only rows behind a sequence's end, and what a log decay of -inf lies between in
- * different chunks, keep theirs.  The order of the sums depends on the sizes, the path, the GPU and the
- * decays alone, so equal calls give equal bits.  Outputs must not overlap inputs, but for state.
+ * state itself is summed to fp32.  A log decay below -104, whose decay fp32 does not hold, counts as -inf, and a
+ * product of decays below e^-88 may count as 0.  LA_PATH_SIMT decays the state once a row: there, as in
+ * la_gated_step, log decays above -2^-25 leave it as it is, which L rows add up to L 2^-25 at most.
+ * q, k, v and states are meant to be finite.  An infinity or NaN in a row may reach every row of its chunk
+ * of 64 and those behind, up to the first log decay of -inf in a later chunk; one in state0 (a slot
+ * that holds anything) up to the first -inf.  From that row on, out and the state are those of finite inputs.
+ * (LA_PATH_SIMT: only rows from the bad one to the next -inf.)  Rows behind a sequence's end reach nothing.
+ * The order of the sums depends on the sizes, the path, the GPU and the decays alone, so equal calls give
+ * equal bits.  Outputs must not overlap inputs, but for state.
  * Every wait inside LA_PATH_TC has a limit: LA_ERR_TIMEOUT from la_last_device_status.
  * Returns LA_OK, LA_ERR_NULL, LA_ERR_SHAPE, LA_ERR_UNSUPPORTED, LA_ERR_ARG (strides, alignment, scale),
  * LA_ERR_WORKSPACE or LA_ERR_CUDA.  Asynchronous on `stream`.
@@ -732,7 +737,9 @@ size_t la_gated_workspace_bytes(int B, int H, int L, int dk, int dv, int dtype);
  * row), the gradient of S_t:
  *     dq_t = scale S_t dout_t,    dk_t = D_t v_t,    dv_t = D_t^T k_t,
  *     dlog_decay_t = <D_t, a_t S_{t-1}>,    dstate0 = a_0 D_0.
- * The states are formed again from k, v and log_decay; nothing of the forward pass is kept.
+ * The states are formed again from k, v and log_decay; nothing of the forward pass is kept.  What is not finite
+ * reaches dq as it does out, and from its row back dk, dv and dstate0: up to the last -inf in an earlier
+ * chunk, before whose row they are those of finite inputs; dlog_decay both ways.
  *   dout          [B, H, L, dv], dtype `dtype`
  *   dstate        device fp32 [B, H, dk, dv], the gradient of the state behind the last row, or NULL for zero
  *   dq, dk, dv    as q, k, v, fully overwritten, 0 behind a sequence's end; dk and dv of a shared key
@@ -741,8 +748,10 @@ size_t la_gated_workspace_bytes(int B, int H, int L, int dk, int dv, int dtype);
  *   dlog_decay_head  device fp32 [H]: its sums over sequences and rows, the gradient of a constant for
  *                 each head; or NULL.  Without both the decays' gradient is not formed.  It is summed
  *                 back over up to 1024 rows from products of states, so it is off by a few fp32
- *                 roundings of the largest values (and of <dstate, state>) among those rows.  It is 0 itself
- *                 where the decay is, and for a first row without state0.
+ *                 roundings of the largest values (and of <dstate, state>) among those rows, back to the last
+ *                 row whose decay is 0, where the sum begins again.  It is 0 itself there, and for a first
+ *                 row without state0.  Asking for it lets LA_PATH_TC read the state in three bf16 parts, so
+ *                 dq and dk are nearer to fp32's than without.
  *   dstate0       device fp32 [B, H, dk, dv] or NULL; may be dstate.  Otherwise outputs must not overlap
  *                 inputs.
  *   workspace     la_gated_bwd_workspace_bytes(...) bytes, 16-byte aligned
